@@ -552,6 +552,101 @@ vsd_status vsd_advance_lengths(int B, int gamma, const int32_t* accepted, int ma
                                int n_copies, int32_t* prefix_copies, void* stream);
 
 /* ------------------------------------------------------------------------------
+ * 8-bit KV cache.  The pages of the caches above hold 8-bit codes and every (page, KV
+ * head) has one scale, K and V apart:
+ *   k_cache, v_cache  e4m3 codes [num_blocks][Hkv][page_size][head_dim] (one byte each)
+ *   k_scale, v_scale  fp32 [num_blocks][Hkv]
+ *   value             K[b, j, g, :] = code * scale, with the code's row and the scale's
+ *                     page found through the block table as in a bf16 cache
+ * Half the bytes of a bf16 cache, for storing and for attending.
+ *
+ * vsd_append_kv_quant: vsd_append_kv into such a cache: the rows
+ *   k_new[b][t], v_new[b][t] (bf16), t < n_valid[b], at p = pos_base[b] + pos_offset + t
+ *   n_valid   int32 [B] (device) or NULL (n_new rows of every sequence); a padded
+ *             batch passes its lengths, nothing behind them is read or written
+ * The rows of one call that fall into one page are quantised together (for each KV head,
+ * K and V apart).  With a = their largest finite magnitude and s = the smallest power of
+ * two (at least 2^-126) with a <= 448 s:
+ *   - a page whose slot 0 is written by the call takes the scale s;
+ *   - otherwise the slots before the first written one hold earlier rows: the page keeps
+ *     its scale if a <= 448 scale, else it takes s and those rows' codes become
+ *     e4m3(code * (scale / s)) (exact but for codes that fall below 2^-6);
+ *   - the new codes are e4m3(x / scale), rounded to nearest even; NaN and infinities
+ *     become NaN.
+ * Slots behind the last written one keep their codes: like rows behind a sequence's end
+ * they mean nothing (a scale may have changed above them).  The rows of one sequence are
+ * therefore appended in order; a call that starts at an earlier position drops what lay
+ * behind.  A page is written for one sequence at a time: two sequences of a call must
+ * not write into one physical block.
+ * A sequence whose rows [pos, pos + n_valid) leave [0, max_blocks_per_seq * page_size),
+ * or with n_valid outside [0, n_new], is skipped and flagged VSD_DEV_BAD_LENGTH; a page
+ * whose block-table entry is outside [0, num_blocks) is skipped and flagged
+ * VSD_DEV_BAD_BLOCK.
+ *
+ * vsd_read_kv_quant: the rows at the same positions as bf16,
+ *   k_out[b][t], v_out[b][t] = bf16(code * scale)   [B][n][Hkv][head_dim], t < n_valid[b]
+ * Rows that are skipped (as above) or lie behind n_valid are left as they were.
+ *
+ * Both are programmatic dependents of the preceding kernel on the stream.  Pointers
+ * 16-byte aligned (scales and int32 arrays 4-byte); head_dim 64 or 128.
+ * ------------------------------------------------------------------------------ */
+vsd_status vsd_append_kv_quant(const vsd_geom* geom, int n_new, const void* k_new,
+                               const void* v_new, const int32_t* block_table,
+                               const int32_t* pos_base, int pos_offset, const int32_t* n_valid,
+                               void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                               void* stream);
+
+vsd_status vsd_read_kv_quant(const vsd_geom* geom, int n, const void* k_cache,
+                             const void* v_cache, const float* k_scale, const float* v_scale,
+                             const int32_t* block_table, const int32_t* pos_base,
+                             int pos_offset, const int32_t* n_valid, void* k_out, void* v_out,
+                             void* stream);
+
+/* ------------------------------------------------------------------------------
+ * Verification attention with Collect-2-Query over the 8-bit cache (with R = 1: the
+ * attention of single tokens).  vsd_verify_attn_collect with K and V as above:
+ *   z[b,t,h,j] = scale * k_scale[page(j), g] * <q[b,t,h,:], k_code[b,j,g,:]>
+ *   out[b,t,h,:] = sum_j softmax_j(z[b,t,h,:]) * v_scale[page(j), g] * v_code[b,j,g,:]
+ * logits, partial_scores, the collected rows, prefix_len and every rule as there; scales
+ * are finite and not negative (what vsd_append_kv_quant writes, or a caller's own).
+ *   score, score_hist  both or neither: as vsd_verify_attn_collect_scored (partial_scores
+ *                      is then required), for vsd_select_topk_scored with n_sink, n_recent
+ *   workspace  >= vsd_verify_quant_workspace_size(...) bytes, 256-byte aligned; contents
+ *              ignored on entry
+ * Supported: as vsd_verify_attn_collect.
+ * ------------------------------------------------------------------------------ */
+vsd_status vsd_verify_quant_workspace_size(const vsd_geom* geom, int R, int P_max,
+                                           size_t* bytes);
+
+vsd_status vsd_verify_attn_collect_quant(const vsd_geom* geom, int R, const void* q,
+                                         const void* k_cache, const void* v_cache,
+                                         const float* k_scale, const float* v_scale,
+                                         const int32_t* block_table, const int32_t* prefix_len,
+                                         int collect_row0, int collect_row1, int P_max,
+                                         float scale, float* logits, float* partial_scores,
+                                         float* score, uint32_t* score_hist, int n_sink,
+                                         int n_recent, void* out, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * Sparse draft-step attention over the 8-bit cache: vsd_sparse_decode_attn with K and V
+ * as above.  idx, n_sel, tail_start, seq_len, max_tail and every rule as there.
+ *   workspace  >= vsd_sparse_quant_workspace_size(...) bytes, 256-byte aligned (0 bytes:
+ *              may be NULL); contents ignored on entry (no counters to keep zero)
+ * ------------------------------------------------------------------------------ */
+vsd_status vsd_sparse_quant_workspace_size(const vsd_geom* geom, int k_max, int max_tail,
+                                           size_t* bytes);
+
+vsd_status vsd_sparse_decode_attn_quant(const vsd_geom* geom, const void* q,
+                                        const void* k_cache, const void* v_cache,
+                                        const float* k_scale, const float* v_scale,
+                                        const int32_t* block_table, const int32_t* idx,
+                                        const int32_t* n_sel, int k_max,
+                                        const int32_t* tail_start, const int32_t* seq_len,
+                                        int max_tail, float scale, void* out, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------
  * vsd_copy: dst <- src as a kernel on `stream` (a programmatic dependent of the
  * preceding kernel).  Either pointer may be pinned host memory, which the device
  * addresses directly; a decode loop moves its inputs in and its results out this way.

@@ -21,6 +21,9 @@ from ._lib import (DEV_BAD_BLOCK, DEV_BAD_INDEX, DEV_BAD_LENGTH, DEV_TIMEOUT, Ge
                    vsd_verify_attn_collect_noalloc, vsd_verify_workspace_size,
                    page_blocks, vsd_page_key_means, vsd_block_topk,
                    vsd_verify_attn_collect_scored, vsd_select_topk_scored, HIST_BINS,
-                   vsd_copy, vsd_append_kv, vsd_advance_lengths, vsd_sparse_decode_attn_step)
+                   vsd_copy, vsd_append_kv, vsd_advance_lengths, vsd_sparse_decode_attn_step,
+                   vsd_append_kv_quant, vsd_read_kv_quant, vsd_verify_attn_collect_quant,
+                   vsd_verify_attn_collect_scored_quant, vsd_verify_quant_workspace_size,
+                   vsd_sparse_decode_attn_quant, vsd_sparse_quant_workspace_size)
 from .decode_loop import DecodeLoop  # noqa: F401
 from .iteration import IterationGraph  # noqa: F401

@@ -6,7 +6,9 @@ missing the calls raise immediately; there is no fallback implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional, Tuple
@@ -93,6 +95,14 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         lib.vsd_sparse_decode_attn_step.argtypes = [GP, P, P, P, P, P, P, P, P, I, P, P, I, P,
                                                     ctypes.c_uint, F, P, P, SZ, P]
         lib.vsd_advance_lengths.argtypes = [I, I, P, I, P, P, P, I, P, P]
+        lib.vsd_append_kv_quant.argtypes = [GP, I, P, P, P, P, I, P, P, P, P, P, P]
+        lib.vsd_read_kv_quant.argtypes = [GP, I, P, P, P, P, P, P, I, P, P, P, P]
+        lib.vsd_verify_quant_workspace_size.argtypes = [GP, I, I, ctypes.POINTER(SZ)]
+        lib.vsd_verify_attn_collect_quant.argtypes = [GP, I, P, P, P, P, P, P, P, I, I, I, F, P,
+                                                      P, P, P, I, I, P, P, SZ, P]
+        lib.vsd_sparse_quant_workspace_size.argtypes = [GP, I, I, ctypes.POINTER(SZ)]
+        lib.vsd_sparse_decode_attn_quant.argtypes = [GP, P, P, P, P, P, P, P, P, I, P, P, I, F, P,
+                                                     P, SZ, P]
         lib.vsd_block_topk.argtypes = [GP, I, P, P, P, I, I, F, P, P, P]
         lib.vsd_read_device_status.argtypes = [P, ctypes.POINTER(ctypes.c_uint)]
         lib.vsd_get_error_string.argtypes = [I]
@@ -107,6 +117,9 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                      "vsd_select_workspace_size", "vsd_select_topk", "vsd_sparse_workspace_size",
                      "vsd_sparse_decode_attn", "vsd_page_key_means", "vsd_block_topk",
                      "vsd_verify_attn_collect_scored", "vsd_select_topk_scored", "vsd_copy",
+                     "vsd_append_kv_quant", "vsd_read_kv_quant", "vsd_verify_quant_workspace_size",
+                     "vsd_verify_attn_collect_quant", "vsd_sparse_quant_workspace_size",
+                     "vsd_sparse_decode_attn_quant",
                      "vsd_append_kv", "vsd_advance_lengths", "vsd_sparse_decode_attn_step",
                      "vsd_read_device_status", "vsd_last_cuda_error"):
             getattr(lib, name).restype = ctypes.c_int
@@ -631,4 +644,239 @@ def vsd_sparse_decode_attn_step(q, k_cache, v_cache, block_table, idx, n_sel, ta
                                          int(flags), float(scale), _ptr(out), _ptr(workspace),
                                          ws_bytes, _stream(stream))
     _check(rc, "vsd_sparse_decode_attn_step")
+    return out
+
+
+# ------------------------------------------------------------------ 8-bit cache
+def _need_quant_cache(k_cache, v_cache, k_scale, v_scale, like) -> None:
+    """The caches of the 8-bit calls: float8_e4m3fn [num_blocks, Hkv, 16, d] and float32
+    scales [num_blocks, Hkv], on the device of `like`."""
+    for name, c, s in (("k", k_cache, k_scale), ("v", v_cache, v_scale)):
+        _need(c, torch.float8_e4m3fn, name + "_cache")
+        _need(s, torch.float32, name + "_scale")
+        if c.dim() != 4 or c.shape != k_cache.shape or s.shape != c.shape[:2]:
+            raise ValueError("%s_cache must be [num_blocks, Hkv, page, d] and %s_scale "
+                             "[num_blocks, Hkv]" % (name, name))
+        _same_device(c, like, name + "_cache")
+        _same_device(s, like, name + "_scale")
+
+
+def _same_device(t, like, name: str) -> None:
+    if t.get_device() != like.get_device():
+        raise ValueError("%s is on another device" % name)
+
+
+def _need_like(t, dtype, shape, like, name: str) -> None:
+    """A tensor of the given type and shape on the device of `like`."""
+    _need(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    _same_device(t, like, name)
+
+
+def _on_device(fn):
+    """Run a call with the device of its first tensor current (the library launches on
+    the current device)."""
+    @functools.wraps(fn)
+    def call(first, *args, **kw):
+        dev = first.get_device()
+        if dev < 0 or dev == torch.cuda.current_device():
+            return fn(first, *args, **kw)
+        with torch.cuda.device(dev):
+            return fn(first, *args, **kw)
+    return call
+
+
+def _stream_context(stream):
+    """What a call allocates (outputs, its scratch) comes from torch's allocator tied to
+    the stream that the call runs on: calls on other streams, and captured graphs, get
+    memory of their own, and it goes back in stream order."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _quant_rows(k_rows, v_rows, names, k_cache, v_cache, k_scale, v_scale, block_table, pos_base,
+                n_valid) -> Geom:
+    if k_rows.dim() != 4:
+        raise ValueError("%s must be [B, n, Hkv, d]" % names[0])
+    B = int(k_rows.shape[0])
+    _need(k_rows, torch.bfloat16, names[0])
+    _need_like(v_rows, torch.bfloat16, k_rows.shape, k_rows, names[1])
+    _need_quant_cache(k_cache, v_cache, k_scale, v_scale, k_rows)
+    if k_rows.shape[2:] != (k_cache.shape[1], k_cache.shape[3]):
+        raise ValueError("%s do not fit the cache's heads" % " and ".join(names))
+    _need_like(block_table, torch.int32, (B, block_table.shape[-1]), k_rows, "block_table")
+    _need_like(pos_base, torch.int32, (B,), k_rows, "pos_base")
+    if n_valid is not None:
+        _need_like(n_valid, torch.int32, (B,), k_rows, "n_valid")
+    return geom_for(B, int(k_cache.shape[1]), k_cache, block_table)
+
+
+@_on_device
+def vsd_append_kv_quant(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, pos_base, *,
+                        pos_offset: int = 0, n_valid=None, stream=None) -> None:
+    """Quantise and store K/V rows k_new, v_new (bf16 [B, n_new, Hkv, d]) at positions
+    pos_base[b] + pos_offset + t, t < n_valid[b] (None: all), of an 8-bit cache
+    (float8_e4m3fn [num_blocks, Hkv, 16, d], scales float32 [num_blocks, Hkv]).  Rows are
+    appended in order: a page whose slot 0 is written starts afresh, otherwise its earlier
+    rows are kept (requantised when its scale has to grow)."""
+    geom = _quant_rows(k_new, v_new, ("k_new", "v_new"), k_cache, v_cache, k_scale, v_scale,
+                       block_table, pos_base, n_valid)
+    _check(load().vsd_append_kv_quant(
+        ctypes.byref(geom), int(k_new.shape[1]), _ptr(k_new), _ptr(v_new), _ptr(block_table),
+        _ptr(pos_base), int(pos_offset), _ptr(n_valid), _ptr(k_cache), _ptr(v_cache),
+        _ptr(k_scale), _ptr(v_scale), _stream(stream)), "vsd_append_kv_quant")
+
+
+@_on_device
+def vsd_read_kv_quant(k_cache, v_cache, k_scale, v_scale, block_table, pos_base, *, n: int,
+                      pos_offset: int = 0, n_valid=None, k_out=None, v_out=None, stream=None):
+    """The rows at positions pos_base[b] + pos_offset + t, t < n_valid[b] (None: n), of an
+    8-bit cache as bf16 [B, n, Hkv, d].  Rows behind n_valid are left as they were in
+    k_out, v_out (zeros when allocated here).  Returns (k_out, v_out)."""
+    shape = (int(pos_base.shape[0]), int(n), int(k_cache.shape[1]), int(k_cache.shape[3]))
+    make = torch.empty if n_valid is None else torch.zeros
+    with _stream_context(stream):
+        if k_out is None:
+            k_out = make(shape, dtype=torch.bfloat16, device=k_cache.device)
+        if v_out is None:
+            v_out = make(shape, dtype=torch.bfloat16, device=k_cache.device)
+    geom = _quant_rows(k_out, v_out, ("k_out", "v_out"), k_cache, v_cache, k_scale, v_scale,
+                       block_table, pos_base, n_valid)
+    if k_out.shape != shape:
+        raise ValueError("k_out and v_out must be [B, n, Hkv, d]")
+    _check(load().vsd_read_kv_quant(
+        ctypes.byref(geom), int(n), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+        _ptr(block_table), _ptr(pos_base), int(pos_offset), _ptr(n_valid), _ptr(k_out),
+        _ptr(v_out), _stream(stream)), "vsd_read_kv_quant")
+    return k_out, v_out
+
+
+def vsd_verify_quant_workspace_size(geom: Geom, R: int, P_max: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().vsd_verify_quant_workspace_size(ctypes.byref(geom), int(R), int(P_max),
+                                                  ctypes.byref(out)),
+           "vsd_verify_quant_workspace_size")
+    return int(out.value)
+
+
+def _verify_quant(q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, P_max, scale,
+                  row0, row1, logits, partial, score, score_hist, n_sink, n_recent, out,
+                  workspace, stream, collect, scored):
+    if q.dim() != 4:
+        raise ValueError("q must be [B, R, Hq, d]")
+    B, R, Hq, d = q.shape
+    P_max = int(P_max)
+    _need(q, torch.bfloat16, "q")
+    _need_quant_cache(k_cache, v_cache, k_scale, v_scale, q)
+    if d != k_cache.shape[3]:
+        raise ValueError("q and the caches have different head dimensions")
+    _need_like(block_table, torch.int32, (B, block_table.shape[-1]), q, "block_table")
+    _need_like(prefix_len, torch.int32, (B,), q, "prefix_len")
+    geom = geom_for(B, Hq, k_cache, block_table)
+    given = (("out", out, torch.bfloat16, (B, R, Hq, d)),
+             ("logits", logits, torch.float32, (B, 2, Hq, P_max)),
+             ("partial", partial, torch.float32, (B, geom.Hkv, P_max)),
+             ("score", score, torch.float32, (B, P_max)),
+             ("score_hist", score_hist, torch.int32, (B, HIST_BINS)))
+    for name, t, dtype, shape in given:
+        if t is not None:
+            _need_like(t, dtype, shape, q, name)
+    dev = q.device
+    with _stream_context(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if collect and logits is None:
+            logits = torch.empty((B, 2, Hq, P_max), dtype=torch.float32, device=dev)
+        if (collect or scored) and partial is None:
+            partial = torch.empty((B, geom.Hkv, P_max), dtype=torch.float32, device=dev)
+        if scored and score is None:
+            score = torch.empty((B, P_max), dtype=torch.float32, device=dev)
+        if scored and score_hist is None:
+            score_hist = torch.empty((B, HIST_BINS), dtype=torch.int32, device=dev)
+        if workspace is None:
+            nb = vsd_verify_quant_workspace_size(geom, R, P_max)
+            workspace = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().vsd_verify_attn_collect_quant(
+        ctypes.byref(geom), R, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+        _ptr(v_scale), _ptr(block_table), _ptr(prefix_len), int(row0),
+        R - 1 if row1 is None else int(row1), P_max, float(scale), _ptr(logits), _ptr(partial),
+        _ptr(score), _ptr(score_hist), int(n_sink), int(n_recent), _ptr(out), _ptr(workspace),
+        ws_bytes, _stream(stream)), "vsd_verify_attn_collect_quant")
+    return out, logits, partial, score, score_hist
+
+
+@_on_device
+def vsd_verify_attn_collect_quant(q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len,
+                                  *, P_max: int, scale: float, row0: int = 0,
+                                  row1: Optional[int] = None, logits=None, partial=None, out=None,
+                                  collect: bool = True, workspace=None, stream=None):
+    """Verification attention + Collect-2-Query over an 8-bit cache (float8_e4m3fn
+    [num_blocks, Hkv, 16, d] with scales float32 [num_blocks, Hkv]); with R = 1 the
+    attention of single tokens.  Returns (out, logits, partial)."""
+    return _verify_quant(q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, P_max,
+                         scale, row0, row1, logits, partial, None, None, 0, 0, out, workspace,
+                         stream, collect, False)[:3]
+
+
+@_on_device
+def vsd_verify_attn_collect_scored_quant(q, k_cache, v_cache, k_scale, v_scale, block_table,
+                                         prefix_len, *, P_max: int, scale: float, row0: int = 0,
+                                         row1: Optional[int] = None, logits=None, partial=None,
+                                         score=None, score_hist=None, n_sink: int = 0,
+                                         n_recent: int = 0, out=None, workspace=None, stream=None):
+    """vsd_verify_attn_collect_quant that also writes the aggregated score and its
+    histogram for vsd_select_topk_scored (logits are written when given).  Returns (out,
+    logits, partial, score, score_hist)."""
+    return _verify_quant(q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, P_max,
+                         scale, row0, row1, logits, partial, score, score_hist, n_sink, n_recent,
+                         out, workspace, stream, False, True)
+
+
+def vsd_sparse_quant_workspace_size(geom: Geom, k_max: int, max_tail: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().vsd_sparse_quant_workspace_size(ctypes.byref(geom), int(k_max), int(max_tail),
+                                                  ctypes.byref(out)),
+           "vsd_sparse_quant_workspace_size")
+    return int(out.value)
+
+
+@_on_device
+def vsd_sparse_decode_attn_quant(q, k_cache, v_cache, k_scale, v_scale, block_table, idx, n_sel,
+                                 tail_start, seq_len, *, scale: float, max_tail: int, out=None,
+                                 workspace=None, stream=None):
+    """Sparse draft-step attention over an 8-bit cache.  q: bf16 [B, Hq, d]; idx: int32
+    [B, k_max] and n_sel: int32 [B], or both None.  Returns out."""
+    if q.dim() != 3:
+        raise ValueError("q must be [B, Hq, d]")
+    B, Hq, d = q.shape
+    _need(q, torch.bfloat16, "q")
+    _need_quant_cache(k_cache, v_cache, k_scale, v_scale, q)
+    if d != k_cache.shape[3]:
+        raise ValueError("q and the caches have different head dimensions")
+    _need_like(block_table, torch.int32, (B, block_table.shape[-1]), q, "block_table")
+    _need_like(tail_start, torch.int32, (B,), q, "tail_start")
+    _need_like(seq_len, torch.int32, (B,), q, "seq_len")
+    k_max = 0
+    if (idx is None) != (n_sel is None):
+        raise ValueError("idx and n_sel go together")
+    if idx is not None:
+        k_max = int(idx.shape[-1])
+        _need_like(idx, torch.int32, (B, k_max), q, "idx")
+        _need_like(n_sel, torch.int32, (B,), q, "n_sel")
+    if out is not None:
+        _need_like(out, torch.bfloat16, (B, Hq, d), q, "out")
+    geom = geom_for(B, Hq, k_cache, block_table)
+    with _stream_context(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            nb = vsd_sparse_quant_workspace_size(geom, k_max, max_tail)
+            workspace = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().vsd_sparse_decode_attn_quant(
+        ctypes.byref(geom), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+        _ptr(block_table), _ptr(idx), _ptr(n_sel), k_max, _ptr(tail_start), _ptr(seq_len),
+        int(max_tail), float(scale), _ptr(out), _ptr(workspace), ws_bytes, _stream(stream)),
+        "vsd_sparse_decode_attn_quant")
     return out

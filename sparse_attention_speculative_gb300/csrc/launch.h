@@ -211,4 +211,39 @@ cudaError_t launch_page_means(const BlockTopkArgs& a, cudaStream_t stream);
 cudaError_t launch_block_topk(const CUtensorMap& kbar_map, const BlockTopkArgs& a,
                               cudaStream_t stream);
 
+// ---------------------------------------------------------------- 8-bit cache
+// Caches of e4m3 codes [num_blocks][Hkv][16][d] with fp32 scales [num_blocks][Hkv].
+struct QuantRowsArgs {
+  const void* k_new = nullptr;  // append: bf16 [B][n][Hkv][d]
+  const void* v_new = nullptr;
+  void* k_out = nullptr;        // read: bf16 [B][n][Hkv][d]
+  void* v_out = nullptr;
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* block_table;
+  const int32_t* pos_base;
+  const int32_t* n_valid;       // [B] rows of each sequence, or null (all n)
+  unsigned* status;
+  int B, n, Hkv, d, max_blocks, num_blocks, pos_offset;
+};
+
+cudaError_t launch_append_kv_quant(const QuantRowsArgs& a, cudaStream_t stream);
+cudaError_t launch_read_kv_quant(const QuantRowsArgs& a, cudaStream_t stream);
+
+// Attention over such caches.  VerifyArgs / SparseArgs as for the bf16 calls (k_new and
+// the step options unused), with the scales beside them.
+struct QuantScales {
+  const float* k;
+  const float* v;
+};
+
+size_t verify_quant_workspace_bytes(const VerifyPlan& plan, int head_dim);
+cudaError_t launch_verify_quant(const VerifyArgs& a, const QuantScales& s, const void* k_cache,
+                                const void* v_cache, const VerifyPlan& plan,
+                                cudaStream_t stream);
+size_t sparse_quant_workspace_bytes(int B, int Hkv, int G, int head_dim, int k_max, int max_tail);
+cudaError_t launch_sparse_quant(const SparseArgs& a, const QuantScales& s, cudaStream_t stream);
+
 }  // namespace vsd

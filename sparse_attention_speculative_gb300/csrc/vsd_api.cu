@@ -925,4 +925,245 @@ vsd_status vsd_block_topk(const vsd_geom* geom, int R, const void* q, const floa
   return VSD_OK;
 }
 
+// ---------------------------------------------------------------- 8-bit cache
+namespace {
+
+constexpr int kMaxPositions = 1 << 30;  // positions of one sequence: sums stay below 2^31
+
+bool quant_cache_ok(const void* k_cache, const void* v_cache, const float* k_scale,
+                    const float* v_scale) {
+  return k_cache && v_cache && k_scale && v_scale && aligned(k_cache, 16) &&
+         aligned(v_cache, 16) && aligned(k_scale, 4) && aligned(v_scale, 4);
+}
+
+// The checks and arguments that storing and reading rows share.  *run is false where
+// there is nothing to do.
+vsd_status quant_rows(const vsd_geom* geom, int n, const void* k_rows, const void* v_rows,
+                      const int32_t* block_table, const int32_t* pos_base, int pos_offset,
+                      const int32_t* n_valid, const void* k_cache, const void* v_cache,
+                      const float* k_scale, const float* v_scale, vsd::QuantRowsArgs* a,
+                      bool* run) {
+  *run = false;
+  vsd_status st = check_geom(geom);
+  if (st != VSD_OK) return st;
+  if (n < 0) return VSD_ERR_INVALID_ARG;
+  if (geom->B == 0 || n == 0) return VSD_OK;
+  if (!k_rows || !v_rows || !block_table || !pos_base ||
+      !quant_cache_ok(k_cache, v_cache, k_scale, v_scale))
+    return VSD_ERR_INVALID_ARG;
+  if (!aligned(k_rows, 16) || !aligned(v_rows, 16) || !aligned(block_table, 4) ||
+      !aligned(pos_base, 4) || !aligned(n_valid, 4))
+    return VSD_ERR_INVALID_ARG;
+  unsigned* status = nullptr;
+  st = device_info(&status, nullptr);
+  if (st != VSD_OK) return st;
+  a->k_cache = const_cast<void*>(k_cache);  // written by the append only
+  a->v_cache = const_cast<void*>(v_cache);
+  a->k_scale = const_cast<float*>(k_scale);
+  a->v_scale = const_cast<float*>(v_scale);
+  a->block_table = block_table;
+  a->pos_base = pos_base;
+  a->n_valid = n_valid;
+  a->status = status;
+  a->B = geom->B;
+  a->n = n;
+  a->Hkv = geom->Hkv;
+  a->d = geom->head_dim;
+  a->max_blocks = geom->max_blocks_per_seq;
+  a->num_blocks = geom->num_blocks;
+  a->pos_offset = pos_offset;
+  *run = true;
+  return VSD_OK;
+}
+
+}  // namespace
+
+vsd_status vsd_append_kv_quant(const vsd_geom* geom, int n_new, const void* k_new,
+                               const void* v_new, const int32_t* block_table,
+                               const int32_t* pos_base, int pos_offset, const int32_t* n_valid,
+                               void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                               void* stream) {
+  vsd::QuantRowsArgs a;
+  bool run = false;
+  vsd_status st = quant_rows(geom, n_new, k_new, v_new, block_table, pos_base, pos_offset,
+                             n_valid, k_cache, v_cache, k_scale, v_scale, &a, &run);
+  if (st != VSD_OK || !run) return st;
+  a.k_new = k_new;
+  a.v_new = v_new;
+  cudaError_t e = vsd::launch_append_kv_quant(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VSD_OK : cuda_fail(e);
+}
+
+vsd_status vsd_read_kv_quant(const vsd_geom* geom, int n, const void* k_cache,
+                             const void* v_cache, const float* k_scale, const float* v_scale,
+                             const int32_t* block_table, const int32_t* pos_base,
+                             int pos_offset, const int32_t* n_valid, void* k_out, void* v_out,
+                             void* stream) {
+  vsd::QuantRowsArgs a;
+  bool run = false;
+  vsd_status st = quant_rows(geom, n, k_out, v_out, block_table, pos_base, pos_offset, n_valid,
+                             k_cache, v_cache, k_scale, v_scale, &a, &run);
+  if (st != VSD_OK || !run) return st;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  cudaError_t e = vsd::launch_read_kv_quant(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VSD_OK : cuda_fail(e);
+}
+
+vsd_status vsd_verify_quant_workspace_size(const vsd_geom* geom, int R, int P_max,
+                                           size_t* bytes) {
+  if (bytes == nullptr) return VSD_ERR_INVALID_ARG;
+  vsd_status st = verify_checks(geom, R, P_max);
+  if (st != VSD_OK) return st;
+  if (P_max > kMaxPositions) return VSD_ERR_UNSUPPORTED;
+  int sms = 0;
+  st = device_info(nullptr, &sms);
+  if (st != VSD_OK) return st;
+  const vsd::VerifyPlan plan =
+      vsd::plan_verify(geom->B, geom->Hkv, R, geom->Hq / geom->Hkv, P_max, sms);
+  *bytes = vsd::verify_quant_workspace_bytes(plan, geom->head_dim);
+  return VSD_OK;
+}
+
+vsd_status vsd_verify_attn_collect_quant(const vsd_geom* geom, int R, const void* q,
+                                         const void* k_cache, const void* v_cache,
+                                         const float* k_scale, const float* v_scale,
+                                         const int32_t* block_table, const int32_t* prefix_len,
+                                         int collect_row0, int collect_row1, int P_max,
+                                         float scale, float* logits, float* partial_scores,
+                                         float* score, uint32_t* score_hist, int n_sink,
+                                         int n_recent, void* out, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+  vsd_status st = verify_checks(geom, R, P_max);
+  if (st != VSD_OK) return st;
+  if ((score == nullptr) != (score_hist == nullptr) || n_sink < 0 || n_recent < 0)
+    return VSD_ERR_INVALID_ARG;
+  if (P_max > kMaxPositions) return VSD_ERR_UNSUPPORTED;
+  if (geom->B == 0) return VSD_OK;
+  if (score != nullptr && partial_scores == nullptr) return VSD_ERR_INVALID_ARG;
+  if (score != nullptr) return VSD_ERR_UNSUPPORTED;  // the plain kernel does not aggregate
+  if (!q || !block_table || !prefix_len || !out ||
+      !quant_cache_ok(k_cache, v_cache, k_scale, v_scale))
+    return VSD_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(logits, 16) ||
+      !aligned(partial_scores, 16) || !aligned(block_table, 4) || !aligned(prefix_len, 4) ||
+      !aligned(score, 4) || !aligned(score_hist, 4))
+    return VSD_ERR_INVALID_ARG;
+  if ((logits || partial_scores) &&
+      (collect_row0 < 0 || collect_row0 >= R || collect_row1 < 0 || collect_row1 >= R))
+    return VSD_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return VSD_ERR_INVALID_ARG;
+  unsigned* status = nullptr;
+  int sms = 0;
+  st = device_info(&status, &sms);
+  if (st != VSD_OK) return st;
+  const int G = geom->Hq / geom->Hkv;
+  const vsd::VerifyPlan plan = vsd::plan_verify(geom->B, geom->Hkv, R, G, P_max, sms);
+  const size_t need = vsd::verify_quant_workspace_bytes(plan, geom->head_dim);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256)))
+    return VSD_ERR_WORKSPACE;
+  vsd::VerifyArgs va;
+  va.q = q;
+  va.block_table = block_table;
+  va.prefix_len = prefix_len;
+  va.logits = logits;
+  va.partial = partial_scores;
+  va.out = out;
+  va.ws = static_cast<float*>(workspace);
+  va.status = status;
+  va.B = geom->B;
+  va.Hq = geom->Hq;
+  va.Hkv = geom->Hkv;
+  va.G = G;
+  va.R = R;
+  va.d = geom->head_dim;
+  va.max_blocks = geom->max_blocks_per_seq;
+  va.num_blocks = geom->num_blocks;
+  va.P_max = P_max;
+  va.row0 = collect_row0;
+  va.row1 = collect_row1;
+  va.collect_all = 0;
+  va.score = score;
+  va.hist = score_hist;
+  va.hist_sink = n_sink;
+  va.hist_recent = n_recent;
+  va.scale = scale;
+  const vsd::QuantScales qs{k_scale, v_scale};
+  cudaError_t e = vsd::launch_verify_quant(va, qs, k_cache, v_cache, plan,
+                                           static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VSD_OK : cuda_fail(e);
+}
+
+vsd_status vsd_sparse_quant_workspace_size(const vsd_geom* geom, int k_max, int max_tail,
+                                           size_t* bytes) {
+  if (bytes == nullptr || k_max < 0 || max_tail < 0) return VSD_ERR_INVALID_ARG;
+  vsd_status st = check_geom(geom);
+  if (st != VSD_OK) return st;
+  if (geom->Hq / geom->Hkv > 16 || static_cast<long long>(k_max) + max_tail > kMaxPositions)
+    return VSD_ERR_UNSUPPORTED;
+  *bytes = vsd::sparse_quant_workspace_bytes(geom->B, geom->Hkv, geom->Hq / geom->Hkv,
+                                             geom->head_dim, k_max, max_tail);
+  return VSD_OK;
+}
+
+vsd_status vsd_sparse_decode_attn_quant(const vsd_geom* geom, const void* q,
+                                        const void* k_cache, const void* v_cache,
+                                        const float* k_scale, const float* v_scale,
+                                        const int32_t* block_table, const int32_t* idx,
+                                        const int32_t* n_sel, int k_max,
+                                        const int32_t* tail_start, const int32_t* seq_len,
+                                        int max_tail, float scale, void* out, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  vsd_status st = check_geom(geom);
+  if (st != VSD_OK) return st;
+  if (geom->Hq / geom->Hkv > 16 || geom->B > 65535) return VSD_ERR_UNSUPPORTED;
+  // cache rows are 32-bit: block * Hkv * page_size + offset
+  if (static_cast<long long>(geom->num_blocks) * geom->Hkv * geom->page_size > 0x7FFFFFFFll)
+    return VSD_ERR_UNSUPPORTED;
+  if (k_max < 0 || max_tail < 0) return VSD_ERR_INVALID_ARG;
+  if (static_cast<long long>(k_max) + max_tail > kMaxPositions) return VSD_ERR_UNSUPPORTED;
+  if (geom->B == 0) return VSD_OK;
+  const size_t need = vsd::sparse_quant_workspace_bytes(
+      geom->B, geom->Hkv, geom->Hq / geom->Hkv, geom->head_dim, k_max, max_tail);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256)))
+    return VSD_ERR_WORKSPACE;
+  if (!q || !block_table || !tail_start || !seq_len || !out ||
+      !quant_cache_ok(k_cache, v_cache, k_scale, v_scale))
+    return VSD_ERR_INVALID_ARG;
+  if (k_max > 0 && (!idx || !n_sel)) return VSD_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(idx, 4) || !aligned(n_sel, 4) ||
+      !aligned(block_table, 4) || !aligned(tail_start, 4) || !aligned(seq_len, 4))
+    return VSD_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return VSD_ERR_INVALID_ARG;
+  unsigned* status = nullptr;
+  st = device_info(&status, nullptr);
+  if (st != VSD_OK) return st;
+  vsd::SparseArgs sa;
+  sa.q = q;
+  sa.k_cache = k_cache;
+  sa.v_cache = v_cache;
+  sa.block_table = block_table;
+  sa.idx = k_max > 0 ? idx : nullptr;
+  sa.n_sel = k_max > 0 ? n_sel : nullptr;
+  sa.tail_start = tail_start;
+  sa.seq_len = seq_len;
+  sa.out = out;
+  sa.counters = nullptr;
+  sa.ws = static_cast<float*>(workspace);
+  sa.status = status;
+  sa.B = geom->B;
+  sa.Hq = geom->Hq;
+  sa.Hkv = geom->Hkv;
+  sa.G = geom->Hq / geom->Hkv;
+  sa.d = geom->head_dim;
+  sa.max_blocks = geom->max_blocks_per_seq;
+  sa.num_blocks = geom->num_blocks;
+  sa.k_max = k_max;
+  sa.max_tail = max_tail;
+  sa.scale = scale;
+  const vsd::QuantScales qs{k_scale, v_scale};
+  cudaError_t e = vsd::launch_sparse_quant(sa, qs, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VSD_OK : cuda_fail(e);
+}
+
 }  // extern "C"
