@@ -167,36 +167,6 @@ cudaError_t launch_plain(const PlainParams& p, int d, cudaStream_t stream) {
 
 }  // namespace
 
-size_t verify_quant_workspace_bytes(const VerifyPlan&, int) { return 0; }
-
-cudaError_t launch_verify_quant(const VerifyArgs& a, const QuantScales& s, const void* k_cache,
-                                const void* v_cache, const VerifyPlan&, cudaStream_t stream) {
-  PlainParams p = {};
-  p.q = static_cast<const uint16_t*>(a.q);
-  p.k_cache = static_cast<const uint8_t*>(k_cache);
-  p.v_cache = static_cast<const uint8_t*>(v_cache);
-  p.k_scale = s.k;
-  p.v_scale = s.v;
-  p.block_table = a.block_table;
-  p.prefix_len = a.prefix_len;
-  p.logits = a.logits;
-  p.partial = a.partial;
-  p.out = static_cast<uint16_t*>(a.out);
-  p.status = a.status;
-  p.B = a.B;
-  p.Hq = a.Hq;
-  p.Hkv = a.Hkv;
-  p.G = a.G;
-  p.R = a.R;
-  p.max_blocks = a.max_blocks;
-  p.num_blocks = a.num_blocks;
-  p.P_max = a.P_max;
-  p.row0 = a.row0;
-  p.row1 = a.row1;
-  p.scale = a.scale;
-  return launch_plain(p, a.d, stream);
-}
-
 size_t sparse_quant_workspace_bytes(int, int, int, int, int, int) { return 0; }
 
 cudaError_t launch_sparse_quant(const SparseArgs& a, const QuantScales& s, cudaStream_t stream) {

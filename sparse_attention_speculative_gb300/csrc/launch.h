@@ -240,8 +240,7 @@ struct QuantScales {
 };
 
 size_t verify_quant_workspace_bytes(const VerifyPlan& plan, int head_dim);
-cudaError_t launch_verify_quant(const VerifyArgs& a, const QuantScales& s, const void* k_cache,
-                                const void* v_cache, const VerifyPlan& plan,
+cudaError_t launch_verify_quant(const VerifyArgs& a, const QuantScales& s, const VerifyPlan& plan,
                                 cudaStream_t stream);
 size_t sparse_quant_workspace_bytes(int B, int Hkv, int G, int head_dim, int k_max, int max_tail);
 cudaError_t launch_sparse_quant(const SparseArgs& a, const QuantScales& s, cudaStream_t stream);

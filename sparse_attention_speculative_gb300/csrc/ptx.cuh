@@ -262,6 +262,18 @@ __device__ __forceinline__ void umma_tf32(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
+// D[tmem] (+)= A[smem] * B[smem], 8-bit floating inputs (e4m3 with the descriptor below),
+// fp32 accumulate; 32 elements along K.
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Arrive once on `bar` when all previously issued tcgen05.mma of this thread complete.
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
   asm volatile(
@@ -386,6 +398,13 @@ __host__ __device__ constexpr uint32_t idesc_tf32_f32(uint32_t M, uint32_t N, ui
          ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
+// Instruction descriptor, kind::f8f6f4: e4m3 A and B (format 0), fp32 accumulator; the
+// other fields as for kind::f16.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N, uint32_t a_mn_major,
+                                                      uint32_t b_mn_major) {
+  return (1u << 4) | (a_mn_major << 15) | (b_mn_major << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
 // Shared-memory matrix descriptor with the 128-byte swizzle.
 //   bits 0-13 start >> 4, 16-29 leading byte offset >> 4, 32-45 stride byte offset >> 4,
 //   bits 46-47 version (1), 61-63 layout (2 = 128-byte swizzle).
@@ -401,6 +420,24 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t smem_addr, uint32_t lbo
   d |= 1ull << 46;
   d |= 2ull << 61;
   return d;
+}
+
+// The same for rows of kRowBytes = 128 or 64 bytes (the swizzle spans one row; layout 2 =
+// 128-byte, 4 = 64-byte swizzle).  8-bit elements: a row holds kRowBytes of them, along K
+// (K-major) or along MN (MN-major), 8-row atoms of 8 * kRowBytes bytes at SBO.
+template <int kRowBytes>
+__device__ __forceinline__ uint64_t sdesc_rows(uint32_t smem_addr, uint32_t lbo_bytes,
+                                               uint32_t sbo_bytes) {
+  static_assert(kRowBytes == 128 || kRowBytes == 64, "swizzle span");
+  const uint64_t d = sdesc_sw128(smem_addr, lbo_bytes, sbo_bytes);
+  return kRowBytes == 128 ? d : (d & ~(7ull << 61)) | (4ull << 61);
+}
+
+// Byte offset of 16-byte chunk `ch` of row `r` under that swizzle (rows kRowBytes apart
+// from a 1024-byte boundary).
+template <int kRowBytes>
+__device__ __forceinline__ uint32_t swizzled_chunk(uint32_t r, uint32_t ch) {
+  return kRowBytes == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
 }
 
 }  // namespace ptx

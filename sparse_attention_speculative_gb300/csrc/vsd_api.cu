@@ -930,6 +930,29 @@ namespace {
 
 constexpr int kMaxPositions = 1 << 30;  // positions of one sequence: sums stay below 2^31
 
+// 4-D tiled map over 8-bit codes [num_blocks][Hkv][page][d]: box = one page and head, the
+// swizzle spanning a row.
+vsd_status make_code_map(CUtensorMap* map, const void* cache, const vsd_geom* g) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+  vsd_status st = encoder(&enc);
+  if (st != VSD_OK) return st;
+  const cuuint64_t d = static_cast<cuuint64_t>(g->head_dim);
+  cuuint64_t dims[4] = {d, 16, static_cast<cuuint64_t>(g->Hkv),
+                        static_cast<cuuint64_t>(g->num_blocks)};
+  cuuint64_t strides[3] = {d, 16 * d, static_cast<cuuint64_t>(g->Hkv) * 16 * d};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(d), 16, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(cache), dims, strides,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    t_last_cuda_error = static_cast<int>(r);
+    return VSD_ERR_CUDA;
+  }
+  return VSD_OK;
+}
+
 bool quant_cache_ok(const void* k_cache, const void* v_cache, const float* k_scale,
                     const float* v_scale) {
   return k_cache && v_cache && k_scale && v_scale && aligned(k_cache, 16) &&
@@ -1041,7 +1064,6 @@ vsd_status vsd_verify_attn_collect_quant(const vsd_geom* geom, int R, const void
   if (P_max > kMaxPositions) return VSD_ERR_UNSUPPORTED;
   if (geom->B == 0) return VSD_OK;
   if (score != nullptr && partial_scores == nullptr) return VSD_ERR_INVALID_ARG;
-  if (score != nullptr) return VSD_ERR_UNSUPPORTED;  // the plain kernel does not aggregate
   if (!q || !block_table || !prefix_len || !out ||
       !quant_cache_ok(k_cache, v_cache, k_scale, v_scale))
     return VSD_ERR_INVALID_ARG;
@@ -1063,6 +1085,10 @@ vsd_status vsd_verify_attn_collect_quant(const vsd_geom* geom, int R, const void
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256)))
     return VSD_ERR_WORKSPACE;
   vsd::VerifyArgs va;
+  st = make_code_map(&va.kmap, k_cache, geom);
+  if (st != VSD_OK) return st;
+  st = make_code_map(&va.vmap, v_cache, geom);
+  if (st != VSD_OK) return st;
   va.q = q;
   va.block_table = block_table;
   va.prefix_len = prefix_len;
@@ -1089,8 +1115,7 @@ vsd_status vsd_verify_attn_collect_quant(const vsd_geom* geom, int R, const void
   va.hist_recent = n_recent;
   va.scale = scale;
   const vsd::QuantScales qs{k_scale, v_scale};
-  cudaError_t e = vsd::launch_verify_quant(va, qs, k_cache, v_cache, plan,
-                                           static_cast<cudaStream_t>(stream));
+  cudaError_t e = vsd::launch_verify_quant(va, qs, plan, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? VSD_OK : cuda_fail(e);
 }
 
