@@ -31,17 +31,14 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t codes) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// ---------------------------------------------------------------- operands in parts
-// The attention kernels multiply the cache's codes as they are, so the other operand has
-// to be e4m3 too.  A value is held as a sum of parts, each the nearest e4m3 number of what
-// the parts before it leave over, at scales 2^5 or more apart, whose products go to
-// accumulator columns of their own.
-//
-// Queries: two parts, hi + lo / 32.  A row is first scaled by a power of two so that its
-// largest magnitude lies in [128, 256).  bf16 has 8 significant bits; hi takes 4 of them
-// (nearest) and what it leaves is a multiple of bf16's step of at most half of hi's, 4
-// bits again: the sum is exact for every value above 2^-14 of the row's largest and within
-// 2^-22 of that below.
+// ---------------------------------------------------------------- queries in two parts
+// The attention kernels multiply the cache's key codes as they are (kind::f8f6f4), so the
+// queries have to be e4m3 too: hi + lo / 32, the products of the two in accumulator
+// columns of their own.  A row is first scaled by a power of two so that its largest
+// magnitude lies in [128, 256).  bf16 has 8 significant bits; hi takes 4 of them (nearest)
+// and what it leaves is a multiple of bf16's step of at most half of hi's, 4 bits again:
+// the sum is exact for every value above 2^-14 of the row's largest and within 2^-22 of
+// that below.
 constexpr float kQLo = 1.f / 32.f;
 
 struct QScale {
@@ -68,36 +65,81 @@ __device__ __forceinline__ void query_parts(float a, float b, float f, uint32_t&
   lo = pack_e4m3x2((a - h.x) * 32.f, (b - h.y) * 32.f);
 }
 
-// Probabilities: x = 16 p w (p at most 16 above the running maximum's reference, w <= 1 the
-// page's value scale over the largest so far), three parts x0 + x1 / 2^5 + x2 / 2^13 of
-// the half nearest to x.  Up to x = 32 they hold it to its 11 bits or to 2^-23 (2^-27 of a
-// probability of 1, which keeps the sums of long tails); above that the third part
-// saturates and two parts hold 9 bits.
+// ---------------------------------------------------------------- probabilities
+// P is an f16 operand: x = 16 p w with p at most 2^8 above the running maximum's reference
+// and w = (the page's value scale) / (the reference of the value scales), at most 8: x stays
+// below 2^15.  11 bits of every p w above 2^-18, 2^-29 absolute below (what sums of a
+// hundred thousand small ones need).
 constexpr float kPScale = 16.f;
-constexpr float kPTau = 4.f;  // log2 of the largest p
-constexpr float kPMid = 1.f / 32.f;
-constexpr float kPLow = 1.f / 8192.f;
+constexpr float kPTau = 8.f;    // log2 of the largest p
+constexpr float kPSlack = 8.f;  // the largest w
 
-__device__ __forceinline__ uint32_t pack_e4m3x2_h(uint32_t h2) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Packed pairs of fp32 (two roundings of one instruction).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
+        "l"(reinterpret_cast<const uint64_t&>(c)));
+  return d;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return d;
+}
+
+// Maximum over a warp (NaN ignored).
+__device__ __forceinline__ float warp_max_f32(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
 }
 
-// Parts of two values, each as two codes in the low 16 bits.
-__device__ __forceinline__ void prob_parts(float a, float b, uint32_t& p0, uint32_t& p1,
-                                           uint32_t& p2) {
-  const __half2 x = __floats2half2_rn(a, b);
-  p0 = pack_e4m3x2_h(*reinterpret_cast<const uint32_t*>(&x));
-  const uint32_t h0 = e4m3x2_to_f16x2(p0);
-  // differences and products by powers of two: exact in halves
-  const __half2 k32 = __float2half2_rn(32.f);
-  const __half2 r1 = __hmul2(__hsub2(x, *reinterpret_cast<const __half2*>(&h0)), k32);
-  p1 = pack_e4m3x2_h(*reinterpret_cast<const uint32_t*>(&r1));
-  const uint32_t h1 = e4m3x2_to_f16x2(p1);
-  const __half2 r2 = __hmul2(__hsub2(r1, *reinterpret_cast<const __half2*>(&h1)),
-                             __float2half2_rn(256.f));
-  p2 = pack_e4m3x2_h(*reinterpret_cast<const uint32_t*>(&r2));
+// Sums of N columns over the warp's lanes, every column at once (N = 8, 16 or 32): full
+// exchanges at the lane distances of N and above, then steps that halve the columns a lane
+// keeps.  Afterwards lane L holds column L % N.
+template <int N>
+__device__ __forceinline__ float warp_sum_columns(float* v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int off = 16; off >= N; off >>= 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+  }
+#pragma unroll
+  for (int m = N / 2; m >= 1; m >>= 1) {
+    const bool upper = (lane & m) != 0;
+#pragma unroll
+    for (int i = 0; i < m; ++i) {
+      const float send = upper ? v[i] : v[i + m];
+      const float keep = upper ? v[i + m] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+    }
+  }
+  return v[0];
 }
 
 }  // namespace vsd

@@ -4,22 +4,26 @@
 //   z[j] = scale * ks[page(j)] * <q, kc[j]>,   out = sum_j softmax(z)[j] * vs[page(j)] * vc[j]
 // with e4m3 codes kc, vc.  A page's scales are constant for its 16 keys, and with the
 // key on the accumulator's lanes both are one factor per thread: ks multiplies the
-// finished dot product, vs the probability.  So the codes go from HBM to the tensor
-// cores as they are (kind::f8f6f4, no conversion of K or V anywhere), and the small
-// operands are what is converted: the queries into two e4m3 parts (exact for bf16), the
-// probabilities into three (see quant.cuh).  The parts are extra columns of N, which
-// these products have to spare: M = 128 keys (or dimensions), N = 2 NQ and 3 NQ.
+// finished dot product, vs the probability.  So the key codes go from HBM to the
+// tensor cores as they are (kind::f8f6f4), and the small
+// operand of the first product is what is converted: the queries into two e4m3 parts
+// (exact for bf16, see quant.cuh), extra columns of N, which this product has to spare.
+// The second product's small operand are the probabilities; three e4m3 parts of them took
+// more instructions than widening the V tile once (10 for each two probabilities against
+// 1.5 for each two codes; 71 us a call on the 32K layer), so V is widened to f16 in shared
+// memory and P is f16.
 //
 // How: the persistent split-K plan, rings and warp roles of the bf16 kernel (see
-// verify_attn.cuh), with 16 KB tiles:
-//   S^T[128 keys x 2 NQ] = K[128 x d] * [Qhi; Qlo]^T        (K-major A and B)
-//   O^T[d x 3 NQ]       += V^T[d x 128 keys] * [P0 P1 P2]^T  (MN-major A and B)
+// verify_attn.cuh), with 16 KB tiles and four more warps:
+//   S^T[128 keys x 2 NQ] = K[128 x d] * [Qhi; Qlo]^T   (e4m3, K-major A and B)
+//   O^T[d x NQ]         += V^T[d x 128 keys] * P^T     (f16, MN-major A and B)
 // Rows of d bytes are one swizzle span (128-byte for d = 128, 64-byte for d = 64), so a
-// page and head is one TMA box of 16 rows.
+// page and head is one TMA box of 16 rows.  Warps 11-14 widen the V tile to f16 (exact),
+// one key per thread, into two buffers; they also clear what no row may see.
 //
 // The running maximum of a column is raised (one vote per tile) when a logit exceeds it by
-// more than 2^4; the same vote raises the reference vref of the value scales, so that p *
-// vs / vref stays below 16 and fits e4m3.
+// more than 2^8; the same vote raises the reference of the value scales when a page's is
+// more than 8 times it, so that p * vs / vref fits f16.
 #pragma once
 
 #include "quant.cuh"
@@ -34,7 +38,6 @@ using verify_detail::kHistBins;
 using verify_detail::kPage;
 using verify_detail::kPagesPerTile;
 using verify_detail::kSoftmaxThreads;
-using verify_detail::kThreads;
 using verify_detail::kTile;
 using verify_detail::kVWarp;
 using verify_detail::Seg;
@@ -42,11 +45,12 @@ using verify_detail::segment_at;
 using verify_detail::softmax_sync;
 using verify_detail::softmax_vote;
 using verify_detail::VParams;
-using verify_detail::warp_max;
-using verify_detail::warp_sum;
 
 constexpr float kNoMax = -3e38f;     // a running maximum before the first key (finite: no NaN arises)
 constexpr float kMinRef = 0x1p-120f;  // smallest reference of the value scales
+constexpr int kWidenWarp = 11;        // warps 11-14 widen V
+constexpr int kWidenThreads = 128;
+constexpr int kQThreads = 32 * kWidenWarp + kWidenThreads;
 
 struct QVParams {
   VParams v;
@@ -57,63 +61,32 @@ struct QVParams {
 
 template <int D, int NQ>
 struct QCfg {
-  static constexpr int kTileBytes = kTile * D;               // K (or V) codes of one tile
-  static constexpr int kPBlocks = (3 * NQ + 127) / 128;      // 128-byte blocks of a P^T row
-  static constexpr int kPBuf = kPBlocks * kTile * 128;
-  static constexpr int kStages = D == 64 ? 8 : (NQ <= 32 ? 5 : 4);
+  static constexpr int kTileBytes = kTile * D;        // K (or V) codes of one tile
+  static constexpr int kWideBytes = 2 * kTileBytes;   // V of one tile in f16
+  static constexpr int kHalfBytes = kTile * 128;      // 64 dimensions of it
+  static constexpr bool kSplitP = NQ <= 32;           // both P buffers in one 128-byte row
+  static constexpr int kPBytes = (kSplitP ? 1 : 2) * kTile * 128;
+  static constexpr int kStages = D == 64 ? 8 : (NQ <= 32 ? 4 : 3);
   static constexpr int kQBytes = 2 * NQ * D;
   static constexpr int kOffV = kStages * kTileBytes;
-  static constexpr int kOffQ = 2 * kOffV;
+  static constexpr int kOffWide = 2 * kOffV;
+  static constexpr int kOffQ = kOffWide + 2 * kWideBytes;
   static constexpr int kOffP = kOffQ + kQBytes;
-  static constexpr int kOffMisc = kOffP + 2 * kPBuf;
+  static constexpr int kOffMisc = kOffP + kPBytes;
   static constexpr int kMiscBytes = 4096;
-  static constexpr int kSmemBytes = kOffMisc + kMiscBytes + 1024;
-  static constexpr int kTmemS = 2 * NQ;                       // columns of one S^T buffer
-  static constexpr int kTmemO = 2 * kTmemS;                   // first column of O^T
-  static constexpr int kTmemCols = 7 * NQ <= 128 ? 128 : (7 * NQ <= 256 ? 256 : 512);
+  // d = 64: the PV product reads 16 KB past a widened tile (rows of the accumulator that
+  // are never used); the Q, P and misc areas behind the last one cover that
+  static constexpr int kSmemBytes =
+      (kOffMisc + kMiscBytes > kOffQ + kHalfBytes ? kOffMisc + kMiscBytes : kOffQ + kHalfBytes) + 1024;
+  static constexpr int kTmemS = 2 * NQ;               // columns of one S^T buffer
+  static constexpr int kTmemO = 2 * kTmemS;           // first column of O^T
+  static constexpr int kTmemCols = 5 * NQ <= 128 ? 128 : (5 * NQ <= 256 ? 256 : 512);
   static_assert(kQBytes % 1024 == 0 && kOffQ % 1024 == 0, "swizzle atoms need 1 KB alignment");
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
-// Store the three parts of NC consecutive columns (col0 .. ) of row `key` of P^T: part s
-// of column c is byte s * NQ + c of the row.  x[] holds 16 p w.
-template <int NQ, int NC>
-__device__ __forceinline__ void store_prob_parts(uint8_t* p_buf, int key, int col0,
-                                                 const float (&x)[NC]) {
-  uint32_t w[3][NC / 4];
-#pragma unroll
-  for (int i = 0; i < NC / 4; ++i) {
-    uint32_t a0, a1, a2, b0, b1, b2;
-    prob_parts(x[4 * i], x[4 * i + 1], a0, a1, a2);
-    prob_parts(x[4 * i + 2], x[4 * i + 3], b0, b1, b2);
-    w[0][i] = a0 | b0 << 16;
-    w[1][i] = a1 | b1 << 16;
-    w[2][i] = a2 | b2 << 16;
-  }
-#pragma unroll
-  for (int s = 0; s < 3; ++s) {
-    if constexpr (NC % 16 == 0) {
-#pragma unroll
-      for (int k = 0; k < NC / 16; ++k) {
-        const int off = s * NQ + col0 + 16 * k;
-        *reinterpret_cast<uint4*>(p_buf + (off >> 7) * (kTile * 128) +
-                                  swizzled_chunk<128>(key, (off & 127) >> 4)) =
-            make_uint4(w[s][4 * k], w[s][4 * k + 1], w[s][4 * k + 2], w[s][4 * k + 3]);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < NC / 8; ++k) {
-        const int off = s * NQ + col0 + 8 * k;
-        *reinterpret_cast<uint2*>(p_buf + (off >> 7) * (kTile * 128) +
-                                  swizzled_chunk<128>(key, (off & 127) >> 4) + (off & 8)) =
-            make_uint2(w[s][2 * k], w[s][2 * k + 1]);
-      }
-    }
-  }
-}
-
 template <int D, int NQ>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kQThreads, 1)
     verify_quant_kernel(const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap, const QVParams qa) {
   using Cfg = QCfg<D, NQ>;
@@ -125,6 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* k_ring = base;
   uint8_t* v_ring = base + Cfg::kOffV;
+  uint8_t* wide = base + Cfg::kOffWide;
   uint8_t* q_smem = base + Cfg::kOffQ;
   uint8_t* p_smem = base + Cfg::kOffP;
   uint8_t* misc = base + Cfg::kOffMisc;
@@ -136,7 +110,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* s_empty = s_full + 2;   // [2]
   uint64_t* p_full = s_empty + 2;   // [2]
   uint64_t* pv_done = p_full + 2;   // [2]
-  uint64_t* q_ready = pv_done + 2;
+  uint64_t* w_full = pv_done + 2;   // [2] widened V tile ready
+  uint64_t* q_ready = w_full + 2;
   uint64_t* mma_fin = q_ready + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 384);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 388);
@@ -159,13 +134,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
       mbar_init(&v_full[s], 1);
-      mbar_init(&v_empty[s], 1);
+      mbar_init(&v_empty[s], kWidenThreads);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], kSoftmaxThreads);
       mbar_init(&p_full[i], kSoftmaxThreads);
       mbar_init(&pv_done[i], 1);
+      mbar_init(&w_full[i], kWidenThreads);
     }
     mbar_init(q_ready, kSoftmaxThreads);
     mbar_init(mma_fin, 1);
@@ -183,8 +159,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait_primary();
   pdl_launch_dependents();
   if (a.hist != nullptr) {
-    for (int i = blockIdx.x * kThreads + threadIdx.x; i < a.B * kHistBins;
-         i += gridDim.x * kThreads)
+    for (int i = blockIdx.x * kQThreads + threadIdx.x; i < a.B * kHistBins;
+         i += gridDim.x * kQThreads)
       a.hist[i] = 0u;
   }
   const uint32_t tmem_o = tmem + Cfg::kTmemO;
@@ -268,11 +244,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       constexpr uint32_t idesc_qk = idesc_e4m3_f32(128, 2 * NQ, 0, 0);
-      constexpr uint32_t idesc_pv = idesc_e4m3_f32(128, 3 * NQ, 1, 1);
+      constexpr uint32_t idesc_pv = idesc_f16_f32(128, NQ, 1, 1);
       const uint32_t q_addr = smem_u32(q_smem);
       const uint32_t p_addr = smem_u32(p_smem);
       const uint32_t k_addr0 = smem_u32(k_ring);
-      const uint32_t v_addr0 = smem_u32(v_ring);
+      const uint32_t w_addr0 = smem_u32(wide);
       uint32_t total = 0;
       for (long long v = v0; v < v1;) {
         const Seg s = segment_at(v, v1, a);
@@ -290,21 +266,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (pi < total) {
         bool progressed = false;
         if (pi < qi && mbar_test(&p_full[pi & 1], (pi >> 1) & 1) &&
-            mbar_test(&v_full[pi % ST], (pi / ST) & 1)) {
+            mbar_test(&w_full[pi & 1], (pi >> 1) & 1)) {
           tc_fence_after();
-          const int stage = static_cast<int>(pi % ST);
           const bool first = (first_bits >> (pi & 31)) & 1u;
-          const uint32_t va = v_addr0 + stage * Cfg::kTileBytes;
-          const uint32_t pa = p_addr + (pi & 1) * Cfg::kPBuf;
+          const uint32_t wa = w_addr0 + (pi & 1) * Cfg::kWideBytes;
+          const uint32_t pa = p_addr + (pi & 1) * (Cfg::kSplitP ? 64u : static_cast<uint32_t>(kTile * 128));
 #pragma unroll
-          for (int kk = 0; kk < kTile / 32; ++kk) {
-            // d = 64: the accumulator's rows 64 .. 127 come from the 8 KB behind the tile
-            // (this CTA's shared memory) and are never read
-            const uint64_t ad = sdesc_rows<D>(va + kk * 32 * D, kTile * D, 8 * D);
-            const uint64_t bd = sdesc_rows<128>(pa + kk * 4096, kTile * 128, 1024);
-            umma_f8(tmem_o, ad, bd, idesc_pv, (kk > 0 || !first) ? 1u : 0u);
-          }
-          umma_commit(&v_empty[stage]);
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            umma_bf16(tmem_o, sdesc_sw128(wa + kk * 2048, Cfg::kHalfBytes, 1024),
+                      sdesc_sw128(pa + kk * 2048, Cfg::kHalfBytes, 1024), idesc_pv,
+                      (kk > 0 || !first) ? 1u : 0u);
           umma_commit(&pv_done[pi & 1]);
           ++pi;
           progressed = true;
@@ -357,6 +328,68 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_drain(mma_fin, 0);
     }
     __syncwarp();
+  } else if (warp >= kWidenWarp) {
+    // ------------------------------------------------------------ V codes to f16
+    const int row = threadIdx.x - 32 * kWidenWarp;  // key in tile
+    uint32_t it = 0, nseg = 0;
+    for (long long v = v0; v < v1;) {
+      const Seg s = segment_at(v, v1, a);
+      v = s.next_v;
+      if (s.t_begin >= s.t_end) continue;
+      const uint32_t seg_parity = nseg++ & 1;
+      for (int tile = s.t_begin; tile < s.t_end; ++tile, ++it) {
+        const int stage = it % ST;
+        if (!mbar_wait(&v_full[stage], (it / ST) & 1, abort_flag)) set_abort();
+        const uint8_t* src = v_ring + stage * Cfg::kTileBytes;
+        uint4 x[D / 16];
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+          x[c] = *reinterpret_cast<const uint4*>(src + swizzled_chunk<D>(row, c));
+        mbar_arrive(&v_empty[stage]);
+        const int j = tile * kTile + row;
+        if (j >= s.P) {
+          // Rows past the end hold whatever the cache holds: zeros in their place.  In the
+          // verify block's rows a NaN would reach the rows that do not see it (0 * NaN): it
+          // is cleared here, and put back into the rows that do in the epilogue.
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (j >= s.L) w[i] = 0u;
+              // bytes whose low seven bits are all ones
+              if (__vcmpeq4(w[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0u) {
+                // the softmax threads have reset nan_rows for this segment
+                if (!mbar_wait(q_ready, seg_parity, abort_flag)) set_abort();
+#pragma unroll 1
+                for (int y = 0; y < 4; ++y) {
+                  if (((w[i] >> (8 * y)) & 0x7Fu) == 0x7Fu) {
+                    atomicOr(&nan_rows[c * 16 + i * 4 + y], 1u << (j - s.P));
+                    w[i] &= ~(0xFFu << (8 * y));
+                  }
+                }
+              }
+            }
+            x[c] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        // the PV product that last read this buffer must be done
+        if (it >= 2 && !mbar_wait(&pv_done[it & 1], ((it - 2) >> 1) & 1, abort_flag)) set_abort();
+        uint8_t* dst = wide + (it & 1) * Cfg::kWideBytes;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+          uint8_t* half = dst + (c >> 2) * Cfg::kHalfBytes;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<uint4*>(half + swizzled_chunk<128>(row, (c & 3) * 2 + i)) =
+                make_uint4(e4m3x2_to_f16x2(w[2 * i] & 0xFFFFu), e4m3x2_to_f16x2(w[2 * i] >> 16),
+                           e4m3x2_to_f16x2(w[2 * i + 1] & 0xFFFFu), e4m3x2_to_f16x2(w[2 * i + 1] >> 16));
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&w_full[it & 1]);
+      }
+    }
   } else {
     // ------------------------------------------------------------ softmax / epilogue
     const int sw = warp - 2;
@@ -368,15 +401,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const int G = 1 << qa.gshift;
     const bool collect = a.logits != nullptr || a.partial != nullptr;
-    // this thread's columns of the two collected rows
-    uint32_t cm0 = 0, cm1 = 0;
-    if (collect) {
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        if (col0 + c < a.NV && (col0 + c) >> qa.gshift == a.row0) cm0 |= 1u << c;
-        if (col0 + c < a.NV && (col0 + c) >> qa.gshift == a.row1) cm1 |= 1u << c;
-      }
-    }
+    // the lower half collects row0, the upper half row1
+    const int crow = half == 0 ? a.row0 : a.row1;
     uint32_t it = 0;
     for (long long v = v0; v < v1;) {
       const Seg s = segment_at(v, v1, a);
@@ -400,13 +426,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int ent0 = entry_of(s.t_begin), ent1 = entry_of(s.t_begin + 1);
       float ks_n = scale_of(qa.k_scale, ent0), vs_n = scale_of(qa.v_scale, ent0);
 
-      float lacc[NC], m2[NC];
+      float2 lacc[NC / 2];
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        lacc[c] = 0.f;
-        // padded columns: p = exp2(-inf) = 0, and they never raise the maximum
-        m2[c] = (col0 + c < a.NV) ? kNoMax : INFINITY;
-      }
+      for (int c = 0; c < NC / 2; ++c) lacc[c] = make_float2(0.f, 0.f);
       float vref = kMinRef;
 
       if (has_tiles) {
@@ -442,6 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
           }
         }
+        // padded columns: p = exp2(-inf) = 0, and they never raise the maximum
         if (ts < 64) m2s[ts] = (ts < a.NV) ? kNoMax : INFINITY;
         if (ts < D) nan_rows[ts] = 0u;
         if (ts == 0) *vref_s = kMinRef;
@@ -451,7 +474,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 
       for (int tile = s.t_begin; tile < s.t_end; ++tile, ++it) {
-        const int stage = it % ST;
         const int buf = it & 1;
         const float ks = ks_n, vs = vs_n;
         const int entry = ent0;
@@ -463,74 +485,94 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  : mbar_wait(&s_full[buf], (it >> 1) & 1, abort_flag)))
           set_abort();
         const int j = tile * kTile + row;
-        tc_fence_after();
-        const uint32_t s_addr = tmem + buf * Cfg::kTmemS + lane_addr + col0;
-        float sv[NC];
-        {
-          float lo[NC];
-          tmem_ld_cols<NC>(s_addr, reinterpret_cast<uint32_t*>(sv));
-          tmem_ld_cols<NC>(s_addr + NQ, reinterpret_cast<uint32_t*>(lo));
-          tmem_wait_ld();
-          tc_fence_before();
-          mbar_arrive(&s_empty[buf]);
-#pragma unroll
-          for (int c = 0; c < NC; ++c) sv[c] = fmaf(lo[c], kQLo, sv[c]) * qinv[col0 + c];
-        }
-
         const bool bad = entry < 0 || entry >= a.num_blocks;  // past the end too
         const float zs = ks * a.scale;
+        tc_fence_after();
+        const uint32_t s_base = tmem + buf * Cfg::kTmemS + lane_addr;
 
-        // Collect-2-Query: logits of rows row0 / row1 and their group sum, j < P_b (a key
-        // of an invalid page has zero logits)
+        // Collect-2-Query: this half's row, four (or one) heads at a time, for j < P_b (a
+        // key of an invalid page has zero logits); the two rows' group sums meet in xsum
         float csum = 0.f;
-        if (collect && j < s.P) {
-          float* l0 = a.logits == nullptr
+        if (collect) {
+          float* lg = a.logits == nullptr
                           ? nullptr
-                          : a.logits + (static_cast<size_t>(s.b) * 2 * a.Hq + s.g * G) * a.P_max + j;
+                          : a.logits + ((static_cast<size_t>(s.b) * 2 + half) * a.Hq + s.g * G) * a.P_max + j;
+          const auto heads = [&](auto width) {
+            constexpr int kH = decltype(width)::value;
+            for (int h = 0; h < G; h += kH) {
+              const int col = crow * G + h;
+              uint32_t hi[kH], lo[kH];
+              tmem_ld<kH>(s_base + col, hi);
+              tmem_ld<kH>(s_base + NQ + col, lo);
+              tmem_wait_ld();
+              if (j < s.P) {
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            if (((cm0 | cm1) >> c) & 1u) {
-              const float z = bad ? 0.f : sv[c] * zs;
-              const size_t hl = static_cast<size_t>((col0 + c) & (G - 1)) * a.P_max;
-              if ((cm0 >> c) & 1u) {
-                if (l0 != nullptr) __stcs(l0 + hl, z);
-                csum += z;
-              }
-              if ((cm1 >> c) & 1u) {
-                if (l0 != nullptr) __stcs(l0 + static_cast<size_t>(a.Hq) * a.P_max + hl, z);
-                csum += z;
+                for (int i = 0; i < kH; ++i) {
+                  const float z = bad ? 0.f
+                                      : fmaf(__uint_as_float(lo[i]), kQLo, __uint_as_float(hi[i])) *
+                                            qinv[col + i] * zs;
+                  if (lg != nullptr) __stcs(lg + static_cast<size_t>(h + i) * a.P_max, z);
+                  csum += z;
+                }
               }
             }
-          }
+          };
+          if (qa.gshift >= 2)
+            heads(std::integral_constant<int, 4>{});
+          else
+            heads(std::integral_constant<int, 1>{});
           if (half == 1) xsum[buf * kTile + row] = csum;
         }
 
-        // log2 units; masks only where a key can be hidden
-        const float zl = zs * kLog2e;
-        const bool masked = j >= s.P || bad;
-        int c_lo = 0;  // first visible column of this key
-        if (masked) c_lo = (j < s.L && !bad) ? (j - s.P) << qa.gshift : NQ;
-        if (masked && j < s.P) c_lo = NQ;
+        float2 y[NC / 2];  // logits in log2 units
+        {
+          const float2 zl = make_float2(zs * kLog2e, zs * kLog2e);
+          const float2 klo = make_float2(kQLo, kQLo);
+          constexpr int kC = NC % 16 == 0 ? 16 : 8;
+#pragma unroll
+          for (int c0 = 0; c0 < NC; c0 += kC) {
+            float2 hi[kC / 2], lo[kC / 2];
+            tmem_ld<kC>(s_base + col0 + c0, reinterpret_cast<uint32_t*>(hi));
+            tmem_ld<kC>(s_base + NQ + col0 + c0, reinterpret_cast<uint32_t*>(lo));
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < kC / 2; ++c) {
+              const float2 qi = *reinterpret_cast<const float2*>(qinv + col0 + c0 + 2 * c);
+              // rounded here: against a maximum formed from the same numbers the
+              // difference of the largest is 0 however large they are
+              y[c0 / 2 + c] = mul2(mul2(fma2(lo[c], klo, hi[c]), qi), zl);
+            }
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&s_empty[buf]);
+        if (j >= s.P || bad) {
+          // first visible column of this key
+          const int c_lo = j >= s.P && j < s.L && !bad ? (j - s.P) << qa.gshift : NQ;
+#pragma unroll
+          for (int c = 0; c < NC / 2; ++c) {
+            if (col0 + 2 * c < c_lo) y[c].x = -INFINITY;
+            if (col0 + 2 * c + 1 < c_lo) y[c].y = -INFINITY;
+          }
+        }
         float dmax = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          // rounded here once: against a maximum formed from the same numbers the
-          // difference of the largest is 0 however large they are
-          sv[c] = __fmul_rn(sv[c], zl);
-          if (!masked || col0 + c >= c_lo) dmax = fmaxf(dmax, sv[c] - m2[c]);
+        for (int c = 0; c < NC / 2; ++c) {
+          const float2 m = *reinterpret_cast<const float2*>(m2s + col0 + 2 * c);
+          const float2 dd = add2(y[c], make_float2(-m.x, -m.y));
+          dmax = fmaxf(dmax, fmaxf(dd.x, dd.y));
         }
-        const bool raise = softmax_vote(dmax > kPTau || (!bad && vs > vref));
+        const bool raise = softmax_vote(dmax > kPTau || vs > kPSlack * vref);
         if (collect && half == 0 && j < s.P && a.partial != nullptr)
           a.partial[(static_cast<size_t>(s.b) * a.Hkv + s.g) * a.P_max + j] =
               csum + xsum[buf * kTile + row];
         if (raise) {
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const bool vis = !masked || col0 + c >= c_lo;
-            const float x = warp_max(vis ? sv[c] : kNoMax);
-            if (lane == 0) red[quarter * 64 + col0 + c] = x;
+          for (int c = 0; c < NC / 2; ++c) {
+            const float mx = warp_max_f32(fmaxf(y[c].x, kNoMax)), my = warp_max_f32(fmaxf(y[c].y, kNoMax));
+            if (lane == 0) *reinterpret_cast<float2*>(red + quarter * 64 + col0 + 2 * c) = make_float2(mx, my);
           }
-          const float vm = warp_max(bad ? 0.f : vs);
+          const float vm = warp_max_f32(vs);
           if (lane == 0) vred[sw] = vm;
           softmax_sync();
           if (ts < NQ) {
@@ -551,69 +593,46 @@ __global__ void __launch_bounds__(kThreads, 1)
           softmax_sync();
           const float vratio = *vratio_s;
           vref = *vref_s;
-#pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            lacc[c] *= alphas[col0 + c];
-            m2[c] = m2s[col0 + c];
-          }
+          const float2 vr2 = make_float2(vratio, vratio);
           if (tile != s.t_begin) {
             // O^T holds earlier tiles: rescale its columns once the last PV is done
             if (!mbar_wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, abort_flag)) set_abort();
             tc_fence_after();
+            const uint32_t oa = tmem_o + lane_addr + col0;
+            float2 r[NC / 2];
+            tmem_ld_cols<NC>(oa, reinterpret_cast<uint32_t*>(r));
+            tmem_wait_ld();
 #pragma unroll
-            for (int part = 0; part < 3; ++part) {
-              const uint32_t oa = tmem_o + lane_addr + part * NQ + col0;
-              uint32_t r[NC];
-              tmem_ld_cols<NC>(oa, r);
-              tmem_wait_ld();
-#pragma unroll
-              for (int c = 0; c < NC; ++c)
-                r[c] = __float_as_uint(__uint_as_float(r[c]) * (alphas[col0 + c] * vratio));
-              tmem_st_cols<NC>(oa, r);
+            for (int c = 0; c < NC / 2; ++c) {
+              const float2 al = *reinterpret_cast<const float2*>(alphas + col0 + 2 * c);
+              lacc[c] = mul2(lacc[c], al);
+              r[c] = mul2(r[c], mul2(al, vr2));
             }
+            tmem_st_cols<NC>(oa, reinterpret_cast<uint32_t*>(r));
             tmem_wait_st();
           }
         }
-        const float w = kPScale * (vs / vref);
+        const float w = vs * (kPScale / vref);
+        const float2 w2 = make_float2(w, w);
+        uint32_t pk[NC / 2];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const bool vis = !masked || col0 + c >= c_lo;
-          const float pc = vis ? exp2f(sv[c] - m2[c]) : 0.f;
-          lacc[c] += pc;
-          sv[c] = vis ? pc * w : 0.f;
+        for (int c = 0; c < NC / 2; ++c) {
+          const float2 m = *reinterpret_cast<const float2*>(m2s + col0 + 2 * c);
+          const float2 dd = add2(y[c], make_float2(-m.x, -m.y));
+          const float2 pc = make_float2(ex2(dd.x), ex2(dd.y));
+          lacc[c] = add2(lacc[c], pc);
+          const float2 x = mul2(pc, w2);
+          pk[c] = pack_f16x2(x.x, x.y);
         }
         // P^T buffer: the PV that last read it must be done
         if (it >= 2 && !mbar_wait(&pv_done[buf], ((it - 2) >> 1) & 1, abort_flag)) set_abort();
-        if (j >= s.P) {
-          // Rows past the end hold whatever the cache holds: zero them once the tile has
-          // landed.  In the verify block's rows a NaN code would reach the rows that do
-          // not see it (0 * NaN): it is zeroed here and put back into the rows that do in
-          // the epilogue.
-          if (!mbar_wait(&v_full[stage], (it / ST) & 1, abort_flag)) set_abort();
-          uint8_t* tilep = v_ring + stage * Cfg::kTileBytes;
-          const uint32_t bit = j < s.L ? 1u << (j - s.P) : 0u;
-#pragma unroll 1
-          for (int ch = half * (D / 32); ch < (half + 1) * (D / 32); ++ch) {
-            uint32_t* at = reinterpret_cast<uint32_t*>(tilep + swizzled_chunk<D>(row, ch));
-#pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-              if (bit == 0u) {
-                at[i] = 0u;
-                continue;
-              }
-              uint32_t x = at[i];
-#pragma unroll 1
-              for (int y = 0; y < 4; ++y) {
-                if (((x >> (8 * y)) & 0x7Fu) == 0x7Fu) {
-                  atomicOr(&nan_rows[ch * 16 + i * 4 + y], bit);
-                  x &= ~(0xFFu << (8 * y));
-                  at[i] = x;
-                }
-              }
-            }
-          }
+        uint8_t* prow = p_smem + (Cfg::kSplitP ? 0 : buf * kTile * 128);
+#pragma unroll
+        for (int k = 0; k < NC / 8; ++k) {
+          const int ch = (Cfg::kSplitP ? buf * 4 : 0) + col0 / 8 + k;
+          *reinterpret_cast<uint4*>(prow + swizzled_chunk<128>(row, ch)) =
+              make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
         }
-        store_prob_parts<NQ, NC>(p_smem + buf * Cfg::kPBuf, row, col0, sv);
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(&p_full[buf]);
@@ -622,29 +641,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- pair epilogue
       const size_t slot_base = static_cast<size_t>(slot) * NQ * (D + 2);
       if (has_tiles) {
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const float x = warp_sum(lacc[c]);
-          if (lane == 0) red[quarter * 64 + col0 + c] = x;
+        {
+          float* lv = reinterpret_cast<float*>(lacc);
+          if constexpr (NC == 24) {
+            const float x = warp_sum_columns<16>(lv), x8 = warp_sum_columns<8>(lv + 16);
+            if (lane < 16) red[quarter * 64 + col0 + lane] = x;
+            if (lane < 8) red[quarter * 64 + col0 + 16 + lane] = x8;
+          } else {
+            const float x = warp_sum_columns<NC>(lv);
+            if (lane < NC) red[quarter * 64 + col0 + lane] = x;
+          }
         }
         softmax_sync();
         if (!mbar_wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, abort_flag)) set_abort();
         tc_fence_after();
         float o[NC];
-        {
-          float part[NC];
-          const uint32_t oa = tmem_o + lane_addr + col0;
-          tmem_ld_cols<NC>(oa + 2 * NQ, reinterpret_cast<uint32_t*>(o));
-          tmem_ld_cols<NC>(oa + NQ, reinterpret_cast<uint32_t*>(part));
-          tmem_wait_ld();
+        tmem_ld_cols<NC>(tmem_o + lane_addr + col0, reinterpret_cast<uint32_t*>(o));
+        tmem_wait_ld();
+        const float back = vref / kPScale;
 #pragma unroll
-          for (int c = 0; c < NC; ++c) o[c] = fmaf(o[c], kPLow, part[c] * kPMid);
-          tmem_ld_cols<NC>(oa, reinterpret_cast<uint32_t*>(part));
-          tmem_wait_ld();
-          const float back = vref / kPScale;
-#pragma unroll
-          for (int c = 0; c < NC; ++c) o[c] = (part[c] + o[c]) * back;
-        }
+        for (int c = 0; c < NC; ++c) o[c] *= back;
         tc_fence_before();
         if (row < D) {
           const int dim = row;
@@ -771,7 +787,7 @@ cudaError_t launch_quant(const VerifyArgs& va, const VerifyPlan& plan, const QVP
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(plan.ctas, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(kQThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
