@@ -239,6 +239,7 @@ struct QuantScales {
   const float* v;
 };
 
+size_t verify_quant_span_bytes(const VerifyPlan& plan);
 size_t verify_quant_workspace_bytes(const VerifyPlan& plan, int head_dim);
 cudaError_t launch_verify_quant(const VerifyArgs& a, const QuantScales& s, const VerifyPlan& plan,
                                 cudaStream_t stream);

@@ -13,13 +13,22 @@
 // 1.5 for each two codes; 71 us a call on the 32K layer), so V is widened to f16 in shared
 // memory and P is f16.
 //
-// How: the persistent split-K plan, rings and warp roles of the bf16 kernel (see
-// verify_attn.cuh), with 16 KB tiles and four more warps:
+// How: the rings and warp roles of the bf16 kernel (see verify_attn.cuh), with 16 KB tiles
+// and five more warps:
 //   S^T[128 keys x 2 NQ] = K[128 x d] * [Qhi; Qlo]^T   (e4m3, K-major A and B)
 //   O^T[d x NQ]         += V^T[d x 128 keys] * P^T     (f16, MN-major A and B)
 // Rows of d bytes are one swizzle span (128-byte for d = 128, 64-byte for d = 64), so a
 // page and head is one TMA box of 16 rows.  Warps 11-14 widen the V tile to f16 (exact),
-// one key per thread, into two buffers; they also clear what no row may see.
+// one key per thread, into two buffers; they also clear what no row may see.  Warp 15
+// runs ahead through the block table and brings the pages' scales into shared memory, 32
+// pages (4 tiles) a round, up to 4 rounds ahead: loaded by the softmax threads one tile
+// ahead, a tile took the latency of a load from HBM (1.6 us against 0.8 us for its bytes).
+//
+// The work is the list of all (sequence, KV head, 128-key tile) in order, cut into equal
+// ranges, one for each SM's CTA, by the sequences' real lengths (up to 256 sequences, whose
+// first tiles every CTA sums up for itself; beyond that as if every sequence were as long
+// as the longest admissible).  Along the list either the pair or the CTA changes from one
+// partial result to the next, so slot (pair + CTA) holds it: pairs + CTAs slots in all.
 //
 // The running maximum of a column is raised (one vote per tile) when a logit exceeds it by
 // more than 2^8; the same vote raises the reference of the value scales when a page's is
@@ -40,8 +49,6 @@ using verify_detail::kPagesPerTile;
 using verify_detail::kSoftmaxThreads;
 using verify_detail::kTile;
 using verify_detail::kVWarp;
-using verify_detail::Seg;
-using verify_detail::segment_at;
 using verify_detail::softmax_sync;
 using verify_detail::softmax_vote;
 using verify_detail::VParams;
@@ -50,13 +57,111 @@ constexpr float kNoMax = -3e38f;     // a running maximum before the first key (
 constexpr float kMinRef = 0x1p-120f;  // smallest reference of the value scales
 constexpr int kWidenWarp = 11;        // warps 11-14 widen V
 constexpr int kWidenThreads = 128;
-constexpr int kQThreads = 32 * kWidenWarp + kWidenThreads;
+constexpr int kScaleWarp = 15;        // warp 15 fetches the pages' scales
+constexpr int kQThreads = 512;
+constexpr int kRounds = 4;            // rounds of 4 tiles of scales in shared memory
+constexpr int kTableSeqs = 256;       // sequences whose lengths every CTA holds
 
 struct QVParams {
   VParams v;
   const float* k_scale;
   const float* v_scale;
   int gshift;  // log2 of the group size
+  int2* spans;  // [pairs] first and last CTA of each pair (null: one CTA has them all)
+};
+
+// The positions of one sequence (a length outside the declared bounds: none).
+struct SeqLen {
+  int P, L, tiles;
+  bool bad;
+};
+
+__device__ __forceinline__ SeqLen seq_len(const VParams& a, int P) {
+  SeqLen s;
+  s.bad = !(P >= 0 && P <= a.P_max &&
+            static_cast<long long>(P) + a.R <= static_cast<long long>(a.max_blocks) * kPage);
+  s.P = s.bad ? 0 : P;
+  s.L = s.bad ? 0 : P + a.R;
+  s.tiles = s.bad ? 1 : (s.L + kTile - 1) / kTile;  // (one empty tile: its output is written)
+  return s;
+}
+
+// One CTA's part of a pair, and the walk over its range of the list.
+struct Seg {
+  int p, b, g, P, L;
+  int t_begin, t_end;   // tiles of the pair (none for a bad length)
+  int c_first, c_last;  // CTAs that share the pair
+  bool bad_len;
+};
+
+struct Walk {
+  const VParams& a;
+  const int* plen;  // prefix lengths in shared memory, or null (uniform plan)
+  long long v, v1, W, base;
+  int b, g, C;
+
+  __device__ __forceinline__ Walk(const VParams& a_, const int* plen_, const long long* cum, long long W_)
+      : a(a_), plen(plen_), W(W_) {
+    // no more CTAs than tiles: the CTAs that share a pair are consecutive, each with a part
+    C = W < static_cast<int>(gridDim.x) ? static_cast<int>(W) : static_cast<int>(gridDim.x);
+    const int c = static_cast<int>(blockIdx.x) < C ? static_cast<int>(blockIdx.x) : C;
+    v = c * W / C;
+    v1 = c < C ? (c + 1) * W / C : v;
+    b = g = 0;
+    base = 0;
+    if (done()) return;
+    if (plen != nullptr) {
+      // the last sequence whose first tile (times the heads) is not behind v
+      int lo = 0, hi = a.B - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cum[mid] * a.Hkv <= v)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      b = lo;
+      const int T = seq_len(a, plen[b]).tiles;
+      g = static_cast<int>((v - cum[b] * a.Hkv) / T);
+      base = cum[b] * a.Hkv + static_cast<long long>(g) * T;
+    } else {
+      const long long p = v / a.t_max;
+      b = static_cast<int>(p / a.Hkv);
+      g = static_cast<int>(p % a.Hkv);
+      base = p * a.t_max;
+    }
+  }
+
+  __device__ __forceinline__ bool done() const { return v >= v1; }
+
+  __device__ __forceinline__ Seg next() {
+    const SeqLen n = seq_len(a, plen != nullptr ? plen[b] : __ldcg(a.prefix_len + b));
+    const int T = plen != nullptr ? n.tiles : a.t_max;  // tiles of the pair in the list
+    Seg s;
+    s.p = b * a.Hkv + g;
+    s.b = b;
+    s.g = g;
+    s.P = n.P;
+    s.L = n.L;
+    s.bad_len = n.bad;
+    const long long end = base + T;
+    const long long e = v1 < end ? v1 : end;
+    const int real = n.bad ? 0 : n.tiles;
+    s.t_begin = static_cast<int>(v - base);
+    s.t_end = static_cast<int>(e - base) < real ? static_cast<int>(e - base) : real;
+    if (s.t_end < s.t_begin) s.t_end = s.t_begin;
+    s.c_first = cta_of(base, W, C);
+    s.c_last = cta_of(end - 1, W, C);
+    v = e;
+    if (e == end) {
+      base = end;
+      if (++g == a.Hkv) {
+        g = 0;
+        ++b;
+      }
+    }
+    return s;
+  }
 };
 
 template <int D, int NQ>
@@ -73,7 +178,7 @@ struct QCfg {
   static constexpr int kOffQ = kOffWide + 2 * kWideBytes;
   static constexpr int kOffP = kOffQ + kQBytes;
   static constexpr int kOffMisc = kOffP + kPBytes;
-  static constexpr int kMiscBytes = 4096;
+  static constexpr int kMiscBytes = 8192;
   // d = 64: the PV product reads 16 KB past a widened tile (rows of the accumulator that
   // are never used); the Q, P and misc areas behind the last one cover that
   static constexpr int kSmemBytes =
@@ -107,15 +212,16 @@ __global__ void __launch_bounds__(kQThreads, 1)
   uint64_t* v_full = k_empty + ST;
   uint64_t* v_empty = v_full + ST;
   uint64_t* s_full = v_empty + ST;  // [2]
-  uint64_t* s_empty = s_full + 2;   // [2]
-  uint64_t* p_full = s_empty + 2;   // [2]
+  uint64_t* p_full = s_full + 2;    // [2] P^T stored and V widened
   uint64_t* pv_done = p_full + 2;   // [2]
-  uint64_t* w_full = pv_done + 2;   // [2] widened V tile ready
-  uint64_t* q_ready = w_full + 2;
+  uint64_t* sc_full = pv_done + 2;  // [kRounds] scales of a round ready
+  uint64_t* sc_empty = sc_full + kRounds;
+  uint64_t* q_ready = sc_empty + kRounds;
   uint64_t* mma_fin = q_ready + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 384);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 388);
-  float* vref_s = reinterpret_cast<float*>(misc + 392);        // reference of the value scales
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 448);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 452);
+  static_assert((4 * ST + 6 + 2 * kRounds + 2) * 8 <= 448, "barriers");
+  float* vref_s = reinterpret_cast<float*>(misc + 456);        // reference of the value scales
   float* vratio_s = vref_s + 1;                                // its last change (old / new)
   float* m2s = reinterpret_cast<float*>(misc + 512);           // [64] running maxima
   float* alphas = m2s + 64;                                    // [64] rescale factors
@@ -124,7 +230,13 @@ __global__ void __launch_bounds__(kQThreads, 1)
   float* xsum = red + 256;                                     // [2][kTile] group sums
   float* vred = xsum + 256;                                    // [8] largest value scale per warp
   uint32_t* nan_rows = reinterpret_cast<uint32_t*>(vred + 8);  // [D] verify-block rows with a NaN
-  static_assert(512 + (64 * 3 + 256 + 256 + 8 + 128) * 4 <= Cfg::kMiscBytes, "misc area");
+  // [kRounds][2][32] scales of K and V (a key scale below 0: no such page)
+  float* sc_s = reinterpret_cast<float*>(nan_rows + 128);
+  long long* cum_s = reinterpret_cast<long long*>(sc_s + kRounds * 64);  // first tile of each sequence
+  int* plen_s = reinterpret_cast<int*>(cum_s + kTableSeqs + 1);
+  static_assert(512 + (64 * 3 + 256 + 256 + 8 + 128 + kRounds * 64) * 4 + (kTableSeqs + 1) * 8 +
+                        kTableSeqs * 4 <= Cfg::kMiscBytes,
+                "misc area");
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -138,10 +250,12 @@ __global__ void __launch_bounds__(kQThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], kSoftmaxThreads);
-      mbar_init(&p_full[i], kSoftmaxThreads);
+      mbar_init(&p_full[i], kSoftmaxThreads + kWidenThreads);
       mbar_init(&pv_done[i], 1);
-      mbar_init(&w_full[i], kWidenThreads);
+    }
+    for (int i = 0; i < kRounds; ++i) {
+      mbar_init(&sc_full[i], 1);
+      mbar_init(&sc_empty[i], kSoftmaxThreads);
     }
     mbar_init(q_ready, kSoftmaxThreads);
     mbar_init(mma_fin, 1);
@@ -163,12 +277,33 @@ __global__ void __launch_bounds__(kQThreads, 1)
          i += gridDim.x * kQThreads)
       a.hist[i] = 0u;
   }
+  // lengths and first tiles of the sequences
+  const bool table = a.B <= kTableSeqs;
+  if (table && warp == 0) {
+    long long sum = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      const int b = b0 + lane;
+      const int P = b < a.B ? __ldcg(a.prefix_len + b) : 0;
+      const int T = b < a.B ? seq_len(a, P).tiles : 0;
+      long long x = T;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (b < a.B) {
+        plen_s[b] = P;
+        cum_s[b] = sum + x - T;
+      }
+      sum += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) cum_s[a.B] = sum;
+  }
+  __syncthreads();
+  const int* plen = table ? plen_s : nullptr;
+  const long long W = table ? cum_s[a.B] * a.Hkv : static_cast<long long>(a.pairs) * a.t_max;
+  const auto walk_of = [&] { return Walk(a, plen, cum_s, W); };
   const uint32_t tmem_o = tmem + Cfg::kTmemO;
-
-  const long long W = static_cast<long long>(a.pairs) * a.t_max;
-  const int C = gridDim.x;
-  const long long v0 = static_cast<long long>(blockIdx.x) * W / C;
-  const long long v1 = static_cast<long long>(blockIdx.x + 1) * W / C;
 
   auto set_abort = [&]() {
     if (!*abort_flag) {
@@ -187,20 +322,16 @@ __global__ void __launch_bounds__(kQThreads, 1)
     const uint64_t pol = l2_policy_evict_first();
     if (lane == 0) tma_prefetch_desc(map);
     uint32_t it = 0, issued = 0;
-    for (long long v = v0; v < v1;) {
+    for (Walk w = walk_of(); !w.done();) {
       // block-table entries: 4 tiles (32 pages, one per lane) per load round, two rounds ahead
-      const int p0 = static_cast<int>(v / a.t_max);
-      const int b0 = p0 / a.Hkv;
-      const int tb0 = static_cast<int>(v - static_cast<long long>(p0) * a.t_max);
-      const int32_t* bt_row = a.block_table + static_cast<size_t>(b0) * a.max_blocks;
+      const Seg s = w.next();
+      const int32_t* bt_row = a.block_table + static_cast<size_t>(s.b) * a.max_blocks;
       auto raw_entry = [&](int tile_base) {
         const int lp = (tile_base + (lane >> 3)) * kPagesPerTile + (lane & 7);
         return lp < a.max_blocks ? __ldcg(bt_row + lp) : a.num_blocks;
       };
-      int ent_cur = raw_entry(tb0);
-      int ent_nxt = raw_entry(tb0 + 4);
-      const Seg s = segment_at(v, v1, a);
-      v = s.next_v;
+      int ent_cur = raw_entry(s.t_begin);
+      int ent_nxt = raw_entry(s.t_begin + 4);
       if (is_k && s.bad_len && lane == 0) flag_status(a.status, VSD_DEV_BAD_LENGTH);
       for (int tile = s.t_begin; tile < s.t_end; ++tile, ++it) {
         const int k4 = (tile - s.t_begin) & 3;
@@ -242,99 +373,127 @@ __global__ void __launch_bounds__(kQThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_qk = idesc_e4m3_f32(128, 2 * NQ, 0, 0);
-      constexpr uint32_t idesc_pv = idesc_f16_f32(128, NQ, 1, 1);
-      const uint32_t q_addr = smem_u32(q_smem);
-      const uint32_t p_addr = smem_u32(p_smem);
-      const uint32_t k_addr0 = smem_u32(k_ring);
-      const uint32_t w_addr0 = smem_u32(wide);
-      uint32_t total = 0;
-      for (long long v = v0; v < v1;) {
-        const Seg s = segment_at(v, v1, a);
-        v = s.next_v;
-        total += static_cast<uint32_t>(s.t_end - s.t_begin);
-      }
-      long long qv = v0;
-      Seg qs = segment_at(qv, v1, a);
-      int q_tile = qs.t_begin;
-      uint32_t nseg = 0;
-      uint32_t first_bits = 0;  // bit (i & 31): tile i is the first tile of its segment
-      uint32_t qi = 0, pi = 0;
-      const uint64_t t_start = global_timer_ns();
-      uint32_t spins = 0;
-      while (pi < total) {
-        bool progressed = false;
-        if (pi < qi && mbar_test(&p_full[pi & 1], (pi >> 1) & 1) &&
-            mbar_test(&w_full[pi & 1], (pi >> 1) & 1)) {
-          tc_fence_after();
-          const bool first = (first_bits >> (pi & 31)) & 1u;
-          const uint32_t wa = w_addr0 + (pi & 1) * Cfg::kWideBytes;
-          const uint32_t pa = p_addr + (pi & 1) * (Cfg::kSplitP ? 64u : static_cast<uint32_t>(kTile * 128));
-#pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            umma_bf16(tmem_o, sdesc_sw128(wa + kk * 2048, Cfg::kHalfBytes, 1024),
-                      sdesc_sw128(pa + kk * 2048, Cfg::kHalfBytes, 1024), idesc_pv,
-                      (kk > 0 || !first) ? 1u : 0u);
-          umma_commit(&pv_done[pi & 1]);
-          ++pi;
-          progressed = true;
-        }
-        if (qi < total && qi < pi + 2) {
-          while (q_tile >= qs.t_end) {
-            qv = qs.next_v;
-            qs = segment_at(qv, v1, a);
-            q_tile = qs.t_begin;
-          }
-          const bool first = q_tile == qs.t_begin;
-          const int stage = static_cast<int>(qi % ST);
-          const int buf = qi & 1;
-          const bool ready = (!first || mbar_test(q_ready, nseg & 1)) &&
-                             mbar_test(&k_full[stage], (qi / ST) & 1) &&
-                             (qi < 2 || mbar_test(&s_empty[buf], ((qi >> 1) - 1) & 1));
-          if (ready) {
-            tc_fence_after();
-            const uint32_t ka = k_addr0 + stage * Cfg::kTileBytes;
-#pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk)
-              umma_f8(tmem + buf * Cfg::kTmemS, sdesc_rows<D>(ka + kk * 32, 16, 8 * D),
-                      sdesc_rows<D>(q_addr + kk * 32, 16, 8 * D), idesc_qk, kk > 0 ? 1u : 0u);
-            umma_commit(&k_empty[stage]);
-            umma_commit(&s_full[buf]);
-            if (first) {
-              first_bits |= 1u << (qi & 31);
-              ++nseg;
-            } else {
-              first_bits &= ~(1u << (qi & 31));
-            }
-            ++q_tile;
-            ++qi;
-            progressed = true;
-          }
-        }
-        if (progressed) {
-          spins = 0;
-        } else {
-          __nanosleep(32);
-          if ((++spins & 63u) == 0 &&
-              (*abort_flag || global_timer_ns() - t_start > VSD_WAIT_LIMIT_NS)) {
-            set_abort();
-            break;
-          }
-        }
-      }
-      // never leave an MMA in flight (see verify_attn.cuh)
-      umma_commit(mma_fin);
-      mbar_wait_drain(mma_fin, 0);
+    // The whole warp runs the loop in uniform control flow and one elected lane issues:
+    // with a single lane in the loop every product's descriptors were moved to uniform
+    // registers one by one (75 cycles a product against 22).  The order is fixed: the QK
+    // product of tile i + 1 before the PV product of tile i, except across a segment's
+    // border, where the queries are rewritten only after the last PV product.  It spares
+    // waits of a hundred cycles each: P of tile i - 2 stored means that its S^T has been
+    // read, and S^T of tile i complete that PV of tile i - 2 is (a commit covers every
+    // product issued before it).
+    constexpr uint32_t idesc_qk = idesc_e4m3_f32(128, 2 * NQ, 0, 0);
+    constexpr uint32_t idesc_pv = idesc_f16_f32(128, NQ, 1, 1);
+    const uint64_t q_desc = sdesc_rows<D>(smem_u32(q_smem), 16, 8 * D);
+    const uint64_t k_desc = sdesc_rows<D>(smem_u32(k_ring), 16, 8 * D);
+    const uint64_t p_desc = sdesc_sw128(smem_u32(p_smem), Cfg::kHalfBytes, 1024);
+    const uint64_t w_desc = sdesc_sw128(smem_u32(wide), Cfg::kHalfBytes, 1024);
+    const uint32_t leader = elect_one();
+    uint32_t total = 0;
+    for (Walk w = walk_of(); !w.done();) {
+      const Seg s = w.next();
+      total += static_cast<uint32_t>(s.t_end - s.t_begin);
     }
+    Walk qw = walk_of();
+    int q_begin = 0, q_end = 0, q_tile = 0;  // the segment of the next QK product
+    uint32_t nseg = 0, first_bits = 0;       // bit (i & 31): tile i is its segment's first
+    uint32_t qi = 0, pi = 0;
+    bool ok = true;
+    while (pi < total && ok) {
+      if (qi < total && q_tile >= q_end) {
+        do {
+          const Seg s = qw.next();
+          q_tile = q_begin = s.t_begin;
+          q_end = s.t_end;
+        } while (q_tile >= q_end);
+      }
+      const bool first = q_tile == q_begin;
+      if (qi < total && (first ? pi == qi : qi < pi + 2)) {
+        const uint32_t stage = qi % ST, buf = qi & 1;
+        if (first) ok = mbar_wait(q_ready, nseg & 1, abort_flag);
+        ok = ok && mbar_wait(&k_full[stage], (qi / ST) & 1, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t ad = k_desc + stage * (Cfg::kTileBytes >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk)
+          umma_f8_if(leader, tmem + buf * Cfg::kTmemS, ad + kk * 2, q_desc + kk * 2, idesc_qk,
+                     kk > 0 ? 1u : 0u);
+        umma_commit_if(leader, &k_empty[stage]);
+        umma_commit_if(leader, &s_full[buf]);
+        if (first) {
+          first_bits |= 1u << (qi & 31);
+          ++nseg;
+        } else {
+          first_bits &= ~(1u << (qi & 31));
+        }
+        ++q_tile;
+        ++qi;
+      } else {
+        const uint32_t buf = pi & 1;
+        ok = mbar_wait(&p_full[buf], (pi >> 1) & 1, abort_flag);  // P^T and the widened V
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t keep = ((first_bits >> (pi & 31)) & 1u) ^ 1u;  // accumulate the first step too
+        const uint64_t ad = w_desc + buf * (Cfg::kWideBytes >> 4);
+        const uint64_t bd = p_desc + buf * ((Cfg::kSplitP ? 64 : kTile * 128) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          umma_f16_if(leader, tmem_o, ad + kk * 128, bd + kk * 128, idesc_pv, kk > 0 ? 1u : keep);
+        umma_commit_if(leader, &pv_done[buf]);
+        ++pi;
+      }
+    }
+    if (!ok && lane == 0) set_abort();
+    // never leave an MMA in flight: one more commit arrives once every product the elected
+    // lane issued is done; wait for it with the drain limit before the TMEM columns go back
     __syncwarp();
+    umma_commit_if(leader, mma_fin);
+    mbar_wait_drain(mma_fin, 0);
+    __syncwarp();
+  } else if (warp == kScaleWarp) {
+    // ------------------------------------------------------------ scales of the pages
+    uint32_t round = 0;
+    for (Walk w = walk_of(); !w.done();) {
+      const Seg s = w.next();
+      if (s.t_begin >= s.t_end) continue;
+      const int32_t* bt_row = a.block_table + static_cast<size_t>(s.b) * a.max_blocks;
+      // this lane's page of a round: its table entry (-1: past the sequence), its scales
+      const auto entry_at = [&](int tile) {
+        const int lp = tile * kPagesPerTile + lane;
+        return tile < s.t_end && lp < (s.L + kPage - 1) / kPage ? __ldcg(bt_row + lp) : -1;
+      };
+      const auto scales_at = [&](int e) {
+        if (e < 0 || e >= a.num_blocks) return make_float2(-1.f, 0.f);
+        const size_t at = static_cast<size_t>(e) * a.Hkv + s.g;
+        return make_float2(__ldcg(qa.k_scale + at), __ldcg(qa.v_scale + at));
+      };
+      // in flight: the next round's scales and the table entries of the one after it
+      float2 sc = scales_at(entry_at(s.t_begin));
+      int ent = entry_at(s.t_begin + 4);
+      for (int tile = s.t_begin; tile < s.t_end; tile += 4, ++round) {
+        const float2 now = sc;
+        sc = scales_at(ent);
+        ent = entry_at(tile + 8);
+        const int slot = round % kRounds;
+        int ok = 1;
+        if (lane == 0 && round >= kRounds)
+          ok = mbar_wait(&sc_empty[slot], (round / kRounds - 1) & 1, abort_flag);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok && lane == 0) set_abort();
+        sc_s[slot * 64 + lane] = now.x;
+        sc_s[slot * 64 + 32 + lane] = now.y;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sc_full[slot]);
+      }
+    }
   } else if (warp >= kWidenWarp) {
     // ------------------------------------------------------------ V codes to f16
     const int row = threadIdx.x - 32 * kWidenWarp;  // key in tile
     uint32_t it = 0, nseg = 0;
-    for (long long v = v0; v < v1;) {
-      const Seg s = segment_at(v, v1, a);
-      v = s.next_v;
+    for (Walk walk = walk_of(); !walk.done();) {
+      const Seg s = walk.next();
       if (s.t_begin >= s.t_end) continue;
       const uint32_t seg_parity = nseg++ & 1;
       for (int tile = s.t_begin; tile < s.t_end; ++tile, ++it) {
@@ -387,7 +546,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
                            e4m3x2_to_f16x2(w[2 * i + 1] & 0xFFFFu), e4m3x2_to_f16x2(w[2 * i + 1] >> 16));
         }
         fence_proxy_async_smem();
-        mbar_arrive(&w_full[it & 1]);
+        mbar_arrive(&p_full[it & 1]);
       }
     }
   } else {
@@ -403,29 +562,19 @@ __global__ void __launch_bounds__(kQThreads, 1)
     const bool collect = a.logits != nullptr || a.partial != nullptr;
     // the lower half collects row0, the upper half row1
     const int crow = half == 0 ? a.row0 : a.row1;
-    uint32_t it = 0;
-    for (long long v = v0; v < v1;) {
-      const Seg s = segment_at(v, v1, a);
-      v = s.next_v;
-      const long long first_v = static_cast<long long>(s.p) * a.t_max;
-      const int c_first = cta_of(first_v, W, C);
-      const int c_last = cta_of(first_v + a.t_max - 1, W, C);
-      const bool direct = c_first == c_last;
-      const int slot = s.p * a.max_chunks + (static_cast<int>(blockIdx.x) - c_first);
+    uint32_t it = 0, round = 0;
+    for (Walk walk = walk_of(); !walk.done();) {
+      const Seg s = walk.next();
+      const bool direct = s.c_first == s.c_last;
+      const size_t slot = static_cast<size_t>(s.p) + blockIdx.x;
       const bool has_tiles = s.t_begin < s.t_end;
-      const int32_t* bt_row = a.block_table + static_cast<size_t>(s.b) * a.max_blocks;
-      // block-table entry of this thread's key in a tile (-1: past the sequence)
-      auto entry_of = [&](int tile) {
-        const int jj = tile * kTile + row;
-        return (tile < s.t_end && jj < s.L) ? __ldcg(bt_row + jj / kPage) : -1;
-      };
-      auto scale_of = [&](const float* sc, int e) {
-        return (e >= 0 && e < a.num_blocks) ? __ldcg(sc + static_cast<size_t>(e) * a.Hkv + s.g) : 0.f;
-      };
-      // the key's scales are loaded one tile ahead, its table entry two
-      int ent0 = entry_of(s.t_begin), ent1 = entry_of(s.t_begin + 1);
-      float ks_n = scale_of(qa.k_scale, ent0), vs_n = scale_of(qa.v_scale, ent0);
+      if (ts == 0 && qa.spans != nullptr && s.c_first == static_cast<int>(blockIdx.x))
+        qa.spans[s.p] = make_int2(s.c_first, s.c_last);
 
+      // the collected row's logits of this thread's key (key 0 of the pair, head 0)
+      float* lg = a.logits == nullptr
+                      ? nullptr
+                      : a.logits + ((static_cast<size_t>(s.b) * 2 + half) * a.Hq + s.g * G) * a.P_max + row;
       float2 lacc[NC / 2];
 #pragma unroll
       for (int c = 0; c < NC / 2; ++c) lacc[c] = make_float2(0.f, 0.f);
@@ -475,56 +624,38 @@ __global__ void __launch_bounds__(kQThreads, 1)
 
       for (int tile = s.t_begin; tile < s.t_end; ++tile, ++it) {
         const int buf = it & 1;
-        const float ks = ks_n, vs = vs_n;
-        const int entry = ent0;
-        ent0 = ent1;
-        ent1 = entry_of(tile + 2);
-        ks_n = scale_of(qa.k_scale, ent0);
-        vs_n = scale_of(qa.v_scale, ent0);
+        const int k4 = (tile - s.t_begin) & 3;
+        if (k4 == 0 && !mbar_wait(&sc_full[round % kRounds], (round / kRounds) & 1, abort_flag)) set_abort();
+        const float* sc = sc_s + (round % kRounds) * 64 + k4 * kPagesPerTile + row / kPage;
+        const float ks = sc[0];
+        const float vs = sc[32];
+        if (k4 == 3 || tile + 1 == s.t_end) mbar_arrive(&sc_empty[round++ % kRounds]);
         if (!(VSD_STALL(it == 0) ? mbar_wait(mma_fin, 0, abort_flag)
                                  : mbar_wait(&s_full[buf], (it >> 1) & 1, abort_flag)))
           set_abort();
         const int j = tile * kTile + row;
-        const bool bad = entry < 0 || entry >= a.num_blocks;  // past the end too
+        const bool bad = ks < 0.f;  // no such page (past the end too)
         const float zs = ks * a.scale;
         tc_fence_after();
         const uint32_t s_base = tmem + buf * Cfg::kTmemS + lane_addr;
 
-        // Collect-2-Query: this half's row, four (or one) heads at a time, for j < P_b (a
-        // key of an invalid page has zero logits); the two rows' group sums meet in xsum
-        float csum = 0.f;
-        if (collect) {
-          float* lg = a.logits == nullptr
-                          ? nullptr
-                          : a.logits + ((static_cast<size_t>(s.b) * 2 + half) * a.Hq + s.g * G) * a.P_max + j;
-          const auto heads = [&](auto width) {
-            constexpr int kH = decltype(width)::value;
-            for (int h = 0; h < G; h += kH) {
-              const int col = crow * G + h;
-              uint32_t hi[kH], lo[kH];
-              tmem_ld<kH>(s_base + col, hi);
-              tmem_ld<kH>(s_base + NQ + col, lo);
-              tmem_wait_ld();
-              if (j < s.P) {
-#pragma unroll
-                for (int i = 0; i < kH; ++i) {
-                  const float z = bad ? 0.f
-                                      : fmaf(__uint_as_float(lo[i]), kQLo, __uint_as_float(hi[i])) *
-                                            qinv[col + i] * zs;
-                  if (lg != nullptr) __stcs(lg + static_cast<size_t>(h + i) * a.P_max, z);
-                  csum += z;
-                }
-              }
-            }
-          };
-          if (qa.gshift >= 2)
-            heads(std::integral_constant<int, 4>{});
-          else
-            heads(std::integral_constant<int, 1>{});
-          if (half == 1) xsum[buf * kTile + row] = csum;
+        // the logits, and with up to four heads in the group the collected row's, in one
+        // round of TMEM loads
+        float2 y[NC / 2];  // log2 units
+        float ch[4], cl[4];
+        const bool collect4 = collect && G <= 4;
+        if (collect4) {
+          if (G == 4) {
+            tmem_ld<4>(s_base + crow * 4, reinterpret_cast<uint32_t*>(ch));
+            tmem_ld<4>(s_base + NQ + crow * 4, reinterpret_cast<uint32_t*>(cl));
+          } else if (G == 2) {
+            tmem_ld<2>(s_base + crow * 2, reinterpret_cast<uint32_t*>(ch));
+            tmem_ld<2>(s_base + NQ + crow * 2, reinterpret_cast<uint32_t*>(cl));
+          } else {
+            tmem_ld<1>(s_base + crow, reinterpret_cast<uint32_t*>(ch));
+            tmem_ld<1>(s_base + NQ + crow, reinterpret_cast<uint32_t*>(cl));
+          }
         }
-
-        float2 y[NC / 2];  // logits in log2 units
         {
           const float2 zl = make_float2(zs * kLog2e, zs * kLog2e);
           const float2 klo = make_float2(kQLo, kQLo);
@@ -536,16 +667,50 @@ __global__ void __launch_bounds__(kQThreads, 1)
             tmem_ld<kC>(s_base + NQ + col0 + c0, reinterpret_cast<uint32_t*>(lo));
             tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < kC / 2; ++c) {
-              const float2 qi = *reinterpret_cast<const float2*>(qinv + col0 + c0 + 2 * c);
+            for (int c = 0; c < kC / 4; ++c) {
+              const float4 qi = *reinterpret_cast<const float4*>(qinv + col0 + c0 + 4 * c);
               // rounded here: against a maximum formed from the same numbers the
               // difference of the largest is 0 however large they are
-              y[c0 / 2 + c] = mul2(mul2(fma2(lo[c], klo, hi[c]), qi), zl);
+              y[c0 / 2 + 2 * c] = mul2(mul2(fma2(lo[2 * c], klo, hi[2 * c]), make_float2(qi.x, qi.y)), zl);
+              y[c0 / 2 + 2 * c + 1] =
+                  mul2(mul2(fma2(lo[2 * c + 1], klo, hi[2 * c + 1]), make_float2(qi.z, qi.w)), zl);
             }
           }
         }
+        // Collect-2-Query: this half's row for j < P_b (a key of an invalid page has zero
+        // logits); the two rows' group sums meet in xsum
+        float csum = 0.f;
+        if (collect) {
+          const auto put = [&](int h, float hi, float lo) {
+            const float z = bad ? 0.f : fmaf(lo, kQLo, hi) * qinv[crow * G + h] * zs;
+            if (lg != nullptr) __stcs(lg + static_cast<size_t>(h) * a.P_max + tile * kTile, z);
+            csum += z;
+          };
+          if (collect4) {
+            if (j < s.P) {
+              put(0, ch[0], cl[0]);
+              if (G >= 2) put(1, ch[1], cl[1]);
+              if (G == 4) {
+                put(2, ch[2], cl[2]);
+                put(3, ch[3], cl[3]);
+              }
+            }
+          } else {
+#pragma unroll 1
+            for (int h = 0; h < G; h += 8) {
+              uint32_t hi[8], lo[8];
+              tmem_ld<8>(s_base + crow * G + h, hi);
+              tmem_ld<8>(s_base + NQ + crow * G + h, lo);
+              tmem_wait_ld();
+              if (j < s.P) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) put(h + i, __uint_as_float(hi[i]), __uint_as_float(lo[i]));
+              }
+            }
+          }
+          if (half == 1) xsum[buf * kTile + row] = csum;
+        }
         tc_fence_before();
-        mbar_arrive(&s_empty[buf]);
         if (j >= s.P || bad) {
           // first visible column of this key
           const int c_lo = j >= s.P && j < s.L && !bad ? (j - s.P) << qa.gshift : NQ;
@@ -557,10 +722,11 @@ __global__ void __launch_bounds__(kQThreads, 1)
         }
         float dmax = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < NC / 2; ++c) {
-          const float2 m = *reinterpret_cast<const float2*>(m2s + col0 + 2 * c);
-          const float2 dd = add2(y[c], make_float2(-m.x, -m.y));
-          dmax = fmaxf(dmax, fmaxf(dd.x, dd.y));
+        for (int c = 0; c < NC / 4; ++c) {
+          const float4 m = *reinterpret_cast<const float4*>(m2s + col0 + 4 * c);
+          const float2 d0 = add2(y[2 * c], make_float2(-m.x, -m.y));
+          const float2 d1 = add2(y[2 * c + 1], make_float2(-m.z, -m.w));
+          dmax = fmaxf(dmax, fmaxf(fmaxf(d0.x, d0.y), fmaxf(d1.x, d1.y)));
         }
         const bool raise = softmax_vote(dmax > kPTau || vs > kPSlack * vref);
         if (collect && half == 0 && j < s.P && a.partial != nullptr)
@@ -616,16 +782,18 @@ __global__ void __launch_bounds__(kQThreads, 1)
         const float2 w2 = make_float2(w, w);
         uint32_t pk[NC / 2];
 #pragma unroll
-        for (int c = 0; c < NC / 2; ++c) {
-          const float2 m = *reinterpret_cast<const float2*>(m2s + col0 + 2 * c);
-          const float2 dd = add2(y[c], make_float2(-m.x, -m.y));
-          const float2 pc = make_float2(ex2(dd.x), ex2(dd.y));
-          lacc[c] = add2(lacc[c], pc);
-          const float2 x = mul2(pc, w2);
-          pk[c] = pack_f16x2(x.x, x.y);
+        for (int c = 0; c < NC / 4; ++c) {
+          const float4 m = *reinterpret_cast<const float4*>(m2s + col0 + 4 * c);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float2 dd = add2(y[2 * c + i], i == 0 ? make_float2(-m.x, -m.y) : make_float2(-m.z, -m.w));
+            const float2 pc = make_float2(ex2(dd.x), ex2(dd.y));
+            lacc[2 * c + i] = add2(lacc[2 * c + i], pc);
+            const float2 x = mul2(pc, w2);
+            pk[2 * c + i] = pack_f16x2(x.x, x.y);
+          }
         }
-        // P^T buffer: the PV that last read it must be done
-        if (it >= 2 && !mbar_wait(&pv_done[buf], ((it - 2) >> 1) & 1, abort_flag)) set_abort();
+        // (the PV product that last read this P^T buffer is done: see the issuer)
         uint8_t* prow = p_smem + (Cfg::kSplitP ? 0 : buf * kTile * 128);
 #pragma unroll
         for (int k = 0; k < NC / 8; ++k) {
@@ -639,7 +807,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
       }
 
       // ---------------------------------------------------------- pair epilogue
-      const size_t slot_base = static_cast<size_t>(slot) * NQ * (D + 2);
+      const size_t slot_base = slot * NQ * (D + 2);
       if (has_tiles) {
         {
           float* lv = reinterpret_cast<float*>(lacc);
@@ -718,7 +886,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
 // thread = dimension, kU partials loaded per round; the blocks past them aggregate the
 // scores (see verify_attn.cuh, whose merge this follows; a NaN sum stays NaN here).
 template <int D, bool kAgg, int kU>
-__global__ void __launch_bounds__(D) verify_quant_merge_kernel(const QVParams qa, int NQ, int ctas,
+__global__ void __launch_bounds__(D) verify_quant_merge_kernel(const QVParams qa, int NQ,
                                                                int merge_pairs) {
   const VParams& a = qa.v;
   const int x = blockIdx.x;
@@ -731,14 +899,11 @@ __global__ void __launch_bounds__(D) verify_quant_merge_kernel(const QVParams qa
   }
   const int p = x / a.NV;
   const int c = x - p * a.NV;
-  const long long W = static_cast<long long>(a.pairs) * a.t_max;
-  const long long first_v = static_cast<long long>(p) * a.t_max;
-  const int c_first = cta_of(first_v, W, ctas);
-  const int c_last = cta_of(first_v + a.t_max - 1, W, ctas);
-  if (c_first == c_last) return;
-  const int n = c_last - c_first + 1;
+  const int2 span = __ldcg(qa.spans + p);
+  if (span.x == span.y) return;
+  const int n = span.y - span.x + 1;
   const size_t stride = static_cast<size_t>(NQ) * (D + 2);
-  const float* base = a.ws + static_cast<size_t>(p) * a.max_chunks * stride;
+  const float* base = a.ws + (static_cast<size_t>(p) + span.x) * stride;
   float M = kNoMax, L = 0.f, O = 0.f;
   for (int k0 = 0; k0 < n; k0 += kU) {
     float mk[kU], lk[kU], ok[kU];
@@ -793,7 +958,7 @@ cudaError_t launch_quant(const VerifyArgs& va, const VerifyPlan& plan, const QVP
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, va.kmap, va.vmap, p);
-  const int merge_pairs = plan.max_chunks > 1 ? plan.pairs : 0;
+  const int merge_pairs = p.spans != nullptr ? plan.pairs : 0;
   const int agg = p.v.score != nullptr ? p.v.B * ((p.v.P_max + 4 * D - 1) / (4 * D)) : 0;
   if (e != cudaSuccess || merge_pairs + agg == 0) return e;
   cfg.gridDim = dim3(merge_pairs * p.v.NV + agg, 1, 1);
@@ -801,10 +966,10 @@ cudaError_t launch_quant(const VerifyArgs& va, const VerifyPlan& plan, const QVP
   cfg.dynamicSmemBytes = 0;
   const bool few = plan.max_chunks <= 8;  // partials per pair: one round of 8 loads
   if (agg > 0)
-    return few ? cudaLaunchKernelEx(&cfg, verify_quant_merge_kernel<D, true, 8>, p, NQ, plan.ctas, merge_pairs)
-               : cudaLaunchKernelEx(&cfg, verify_quant_merge_kernel<D, true, 32>, p, NQ, plan.ctas, merge_pairs);
-  return few ? cudaLaunchKernelEx(&cfg, verify_quant_merge_kernel<D, false, 8>, p, NQ, plan.ctas, merge_pairs)
-             : cudaLaunchKernelEx(&cfg, verify_quant_merge_kernel<D, false, 32>, p, NQ, plan.ctas, merge_pairs);
+    return few ? cudaLaunchKernelEx(&cfg, verify_quant_merge_kernel<D, true, 8>, p, NQ, merge_pairs)
+               : cudaLaunchKernelEx(&cfg, verify_quant_merge_kernel<D, true, 32>, p, NQ, merge_pairs);
+  return few ? cudaLaunchKernelEx(&cfg, verify_quant_merge_kernel<D, false, 8>, p, NQ, merge_pairs)
+             : cudaLaunchKernelEx(&cfg, verify_quant_merge_kernel<D, false, 32>, p, NQ, merge_pairs);
 }
 
 template <int D>
@@ -814,6 +979,11 @@ cudaError_t launch_quant_d(const VerifyArgs& va, const QuantScales& sc, const Ve
   p.v = verify_detail::make_params(va, plan);
   p.k_scale = sc.k;
   p.v_scale = sc.v;
+  p.spans = nullptr;
+  if (plan.ctas > 1) {  // workspace: the pairs' spans, then the partial results
+    p.spans = reinterpret_cast<int2*>(va.ws);
+    p.v.ws = va.ws + verify_quant_span_bytes(plan) / sizeof(float);
+  }
   p.gshift = 0;
   while ((1 << p.gshift) < va.G) ++p.gshift;
   switch (plan.nq) {

@@ -221,6 +221,19 @@ def test_verify_many_sequences_share_sms(vsd):
     check_verify(vsd, cache, prefix, 8, 64, 2, P_max=400, rows=(1, 1))
 
 
+def test_verify_more_sequences_than_a_cta_holds_lengths_of(vsd):
+    g = torch.Generator().manual_seed(2)
+    prefix = torch.randint(0, 150, (300,), generator=g).tolist()
+    cache = ref.Cache([p + 1 for p in prefix], 1, 64, seed=18)
+    check_verify(vsd, cache, prefix, 1, 64, 1, P_max=150)
+
+
+def test_verify_one_long_sequence_among_short_ones(vsd):
+    prefix = [3, 0, 9000, 40, 1, 700]
+    cache = ref.Cache([p + 2 for p in prefix], 2, 128, seed=19)
+    check_verify(vsd, cache, prefix, 4, 128, 2, P_max=9100)
+
+
 def test_verify_peaked_rows_and_rising_maxima(vsd):
     """Logits up to a few hundred whose maximum keeps rising along the sequence, and pages
     whose value scales differ by 2^12: running maxima and value references move."""
