@@ -45,7 +45,8 @@ struct QScale {
   float f, inv;  // powers of two, f * inv = 1
 };
 
-// `amax_bits`: the largest bit pattern of the row's |bf16| values.
+// `amax_bits`: the largest bit pattern of the row's |bf16| values.  A row that holds a NaN or
+// an infinity becomes NaN.
 __device__ __forceinline__ QScale query_scale(uint32_t amax_bits) {
   // exponent field e (value 2^(e - 127)); f = 2^(134 - e), kept at most 2^120
   const int e = static_cast<int>(amax_bits >> 7);
@@ -53,13 +54,14 @@ __device__ __forceinline__ QScale query_scale(uint32_t amax_bits) {
   QScale s;
   s.f = __uint_as_float(static_cast<uint32_t>(127 + x) << 23);
   s.inv = __uint_as_float(static_cast<uint32_t>(127 - x) << 23);
+  if (e == 255) s.f = NAN;
   return s;
 }
 
-// The two parts of two scaled query values; what is not finite becomes NaN.
+// The two parts of two query values scaled by f.
 __device__ __forceinline__ void query_parts(float a, float b, float f, uint32_t& hi, uint32_t& lo) {
-  a = isfinite(a) ? a * f : NAN;
-  b = isfinite(b) ? b * f : NAN;
+  a *= f;
+  b *= f;
   hi = pack_e4m3x2(a, b);
   const float2 h = e4m3x2_to_float2(hi);
   lo = pack_e4m3x2((a - h.x) * 32.f, (b - h.y) * 32.f);

@@ -42,7 +42,6 @@ namespace vsd {
 namespace verify_quant_detail {
 
 using namespace ptx;
-using verify_detail::cta_of;
 using verify_detail::kHistBins;
 using verify_detail::kPage;
 using verify_detail::kPagesPerTile;
@@ -86,48 +85,68 @@ __device__ __forceinline__ SeqLen seq_len(const VParams& a, int P) {
   return s;
 }
 
+// The list of W tiles in C nearly equal ranges: the first `more` CTAs have per + 1 tiles, the
+// others per.  (No more CTAs than tiles, so that the CTAs that share a pair are consecutive
+// and each holds a part of it.)  The host keeps W below 2^31.
+struct Ranges {
+  int W, C, per, more;
+
+  __device__ __forceinline__ int first(int c) const { return c * per + (c < more ? c : more); }
+  __device__ __forceinline__ int cta_of(int v) const {
+    const int big = more * (per + 1);
+    return v < big ? v / (per + 1) : more + (v - big) / per;
+  }
+};
+
+__device__ __forceinline__ Ranges make_ranges(int W) {
+  Ranges r;
+  r.W = W;
+  r.C = W < static_cast<int>(gridDim.x) ? W : static_cast<int>(gridDim.x);
+  r.per = W / r.C;
+  r.more = W - r.per * r.C;
+  return r;
+}
+
 // One CTA's part of a pair, and the walk over its range of the list.
 struct Seg {
   int p, b, g, P, L;
-  int t_begin, t_end;   // tiles of the pair (none for a bad length)
-  int c_first, c_last;  // CTAs that share the pair
+  int t_begin, t_end;  // tiles of the pair (none for a bad length)
+  bool first, last;    // the pair begins / ends in this CTA
+  int end;             // the pair's end in the list
   bool bad_len;
 };
 
 struct Walk {
   const VParams& a;
   const int* plen;  // prefix lengths in shared memory, or null (uniform plan)
-  long long v, v1, W, base;
-  int b, g, C;
+  int v, v1, base, b, g;
 
-  __device__ __forceinline__ Walk(const VParams& a_, const int* plen_, const long long* cum, long long W_)
-      : a(a_), plen(plen_), W(W_) {
-    // no more CTAs than tiles: the CTAs that share a pair are consecutive, each with a part
-    C = W < static_cast<int>(gridDim.x) ? static_cast<int>(W) : static_cast<int>(gridDim.x);
-    const int c = static_cast<int>(blockIdx.x) < C ? static_cast<int>(blockIdx.x) : C;
-    v = c * W / C;
-    v1 = c < C ? (c + 1) * W / C : v;
-    b = g = 0;
-    base = 0;
+  __device__ __forceinline__ Walk(const VParams& a_, const int* plen_, const int* cum, const Ranges& r)
+      : a(a_), plen(plen_) {
+    const int c = static_cast<int>(blockIdx.x) < r.C ? static_cast<int>(blockIdx.x) : r.C;
+    v = r.first(c);
+    v1 = c < r.C ? r.first(c + 1) : v;
+    b = g = base = 0;
     if (done()) return;
     if (plen != nullptr) {
       // the last sequence whose first tile (times the heads) is not behind v
       int lo = 0, hi = a.B - 1;
+#pragma unroll 1
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (cum[mid] * a.Hkv <= v)
+        if (cum[mid] <= v)
           lo = mid;
         else
           hi = mid - 1;
       }
       b = lo;
       const int T = seq_len(a, plen[b]).tiles;
-      g = static_cast<int>((v - cum[b] * a.Hkv) / T);
-      base = cum[b] * a.Hkv + static_cast<long long>(g) * T;
+      g = (v - cum[b]) / T;
+      base = cum[b] + g * T;
     } else {
-      const long long p = v / a.t_max;
-      b = static_cast<int>(p / a.Hkv);
-      g = static_cast<int>(p % a.Hkv);
+      const int p = v / a.t_max;
+      b = p / a.Hkv;
+      g = p - b * a.Hkv;
       base = p * a.t_max;
     }
   }
@@ -144,17 +163,17 @@ struct Walk {
     s.P = n.P;
     s.L = n.L;
     s.bad_len = n.bad;
-    const long long end = base + T;
-    const long long e = v1 < end ? v1 : end;
+    s.end = base + T;
+    const int e = v1 < s.end ? v1 : s.end;
     const int real = n.bad ? 0 : n.tiles;
-    s.t_begin = static_cast<int>(v - base);
-    s.t_end = static_cast<int>(e - base) < real ? static_cast<int>(e - base) : real;
+    s.t_begin = v - base;
+    s.t_end = e - base < real ? e - base : real;
     if (s.t_end < s.t_begin) s.t_end = s.t_begin;
-    s.c_first = cta_of(base, W, C);
-    s.c_last = cta_of(end - 1, W, C);
+    s.first = s.t_begin == 0;
+    s.last = e == s.end;
     v = e;
-    if (e == end) {
-      base = end;
+    if (s.last) {
+      base = s.end;
       if (++g == a.Hkv) {
         g = 0;
         ++b;
@@ -227,20 +246,20 @@ __global__ void __launch_bounds__(kQThreads, 1)
   float* alphas = m2s + 64;                                    // [64] rescale factors
   float* qinv = alphas + 64;                                   // [64] 1 / query scale
   float* red = qinv + 64;                                      // [4][64] reductions
-  float* xsum = red + 256;                                     // [2][kTile] group sums
-  float* vred = xsum + 256;                                    // [8] largest value scale per warp
+  float* vred = red + 256;                                     // [8] largest value scale per warp
   uint32_t* nan_rows = reinterpret_cast<uint32_t*>(vred + 8);  // [D] verify-block rows with a NaN
   // [kRounds][2][32] scales of K and V (a key scale below 0: no such page)
   float* sc_s = reinterpret_cast<float*>(nan_rows + 128);
-  long long* cum_s = reinterpret_cast<long long*>(sc_s + kRounds * 64);  // first tile of each sequence
+  int* cum_s = reinterpret_cast<int*>(sc_s + kRounds * 64);  // first tile of each sequence
   int* plen_s = reinterpret_cast<int*>(cum_s + kTableSeqs + 1);
-  static_assert(512 + (64 * 3 + 256 + 256 + 8 + 128 + kRounds * 64) * 4 + (kTableSeqs + 1) * 8 +
-                        kTableSeqs * 4 <= Cfg::kMiscBytes,
+  static_assert(512 + (64 * 3 + 256 + 8 + 128 + kRounds * 64 + 2 * kTableSeqs + 1) * 4 <=
+                    Cfg::kMiscBytes,
                 "misc area");
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
+  const bool collect_any = a.logits != nullptr || a.partial != nullptr;
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) {
       mbar_init(&k_full[s], 1);
@@ -255,7 +274,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
     }
     for (int i = 0; i < kRounds; ++i) {
       mbar_init(&sc_full[i], 1);
-      mbar_init(&sc_empty[i], kSoftmaxThreads);
+      mbar_init(&sc_empty[i], kSoftmaxThreads + (collect_any ? kWidenThreads : 0));
     }
     mbar_init(q_ready, kSoftmaxThreads);
     mbar_init(mma_fin, 1);
@@ -277,18 +296,18 @@ __global__ void __launch_bounds__(kQThreads, 1)
          i += gridDim.x * kQThreads)
       a.hist[i] = 0u;
   }
-  // lengths and first tiles of the sequences
+  // lengths and first tiles (in the list: times the heads) of the sequences
   const bool table = a.B <= kTableSeqs;
   if (table && warp == 0) {
-    long long sum = 0;
+    int sum = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       const int b = b0 + lane;
       const int P = b < a.B ? __ldcg(a.prefix_len + b) : 0;
-      const int T = b < a.B ? seq_len(a, P).tiles : 0;
-      long long x = T;
+      const int T = b < a.B ? seq_len(a, P).tiles * a.Hkv : 0;
+      int x = T;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
       }
       if (b < a.B) {
@@ -301,8 +320,8 @@ __global__ void __launch_bounds__(kQThreads, 1)
   }
   __syncthreads();
   const int* plen = table ? plen_s : nullptr;
-  const long long W = table ? cum_s[a.B] * a.Hkv : static_cast<long long>(a.pairs) * a.t_max;
-  const auto walk_of = [&] { return Walk(a, plen, cum_s, W); };
+  const Ranges ranges = make_ranges(table ? cum_s[a.B] : a.pairs * a.t_max);
+  const auto walk_of = [&] { return Walk(a, plen, cum_s, ranges); };
   const uint32_t tmem_o = tmem + Cfg::kTmemO;
 
   auto set_abort = [&]() {
@@ -489,9 +508,11 @@ __global__ void __launch_bounds__(kQThreads, 1)
       }
     }
   } else if (warp >= kWidenWarp) {
-    // ------------------------------------------------------------ V codes to f16
-    const int row = threadIdx.x - 32 * kWidenWarp;  // key in tile
-    uint32_t it = 0, nseg = 0;
+    // ------------------------------------------------------------ V codes to f16, logits out
+    const int row = (warp & 3) * 32 + lane;  // key in tile (and TMEM lane)
+    const bool collect = collect_any;
+    const int G = 1 << qa.gshift;
+    uint32_t it = 0, nseg = 0, round = 0;
     for (Walk walk = walk_of(); !walk.done();) {
       const Seg s = walk.next();
       if (s.t_begin >= s.t_end) continue;
@@ -546,6 +567,53 @@ __global__ void __launch_bounds__(kQThreads, 1)
                            e4m3x2_to_f16x2(w[2 * i + 1] & 0xFFFFu), e4m3x2_to_f16x2(w[2 * i + 1] >> 16));
         }
         fence_proxy_async_smem();
+        if (collect) {
+          // Collect-2-Query: the two rows' logits of this thread's key and their group sum
+          // (a key of an invalid page has zero logits)
+          const int k4 = (tile - s.t_begin) & 3;
+          if (k4 == 0 && !mbar_wait(&sc_full[round % kRounds], (round / kRounds) & 1, abort_flag)) set_abort();
+          const float ks = sc_s[(round % kRounds) * 64 + k4 * kPagesPerTile + row / kPage];
+          if (k4 == 3 || tile + 1 == s.t_end) mbar_arrive(&sc_empty[round++ % kRounds]);
+          if (!mbar_wait(&s_full[it & 1], (it >> 1) & 1, abort_flag)) set_abort();
+          tc_fence_after();
+          const float zs = ks < 0.f ? 0.f : ks * a.scale;
+          const uint32_t s_base = tmem + (it & 1) * Cfg::kTmemS + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+          float csum = 0.f;
+          const auto group = [&](auto width) {  // kH heads at a time
+            constexpr int kH = decltype(width)::value;
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+              const int col = (c == 0 ? a.row0 : a.row1) << qa.gshift;
+              float* lg = a.logits + ((static_cast<size_t>(s.b) * 2 + c) * a.Hq + (s.g << qa.gshift)) * a.P_max + j;
+#pragma unroll 1
+              for (int h = 0; h < G; h += kH) {
+                uint32_t hi[kH], lo[kH];
+                tmem_ld<kH>(s_base + col + h, hi);
+                tmem_ld<kH>(s_base + NQ + col + h, lo);
+                tmem_wait_ld();
+                if (j < s.P) {
+#pragma unroll
+                  for (int i = 0; i < kH; ++i) {
+                    const float t = fmaf(__uint_as_float(lo[i]), kQLo, __uint_as_float(hi[i])) * qinv[col + h + i];
+                    const float z = ks < 0.f ? 0.f : t * zs;
+                    if (a.logits != nullptr) __stcs(lg, z);
+                    lg += a.P_max;
+                    csum += z;
+                  }
+                }
+              }
+            }
+          };
+          if (qa.gshift >= 3)
+            group(std::integral_constant<int, 8>{});
+          else if (qa.gshift == 2)
+            group(std::integral_constant<int, 4>{});
+          else
+            group(std::integral_constant<int, 1>{});
+          if (j < s.P && a.partial != nullptr)
+            a.partial[(static_cast<size_t>(s.b) * a.Hkv + s.g) * a.P_max + j] = csum;
+          tc_fence_before();
+        }
         mbar_arrive(&p_full[it & 1]);
       }
     }
@@ -559,31 +627,24 @@ __global__ void __launch_bounds__(kQThreads, 1)
     const int col0 = half * NC;
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const int G = 1 << qa.gshift;
-    const bool collect = a.logits != nullptr || a.partial != nullptr;
-    // the lower half collects row0, the upper half row1
-    const int crow = half == 0 ? a.row0 : a.row1;
     uint32_t it = 0, round = 0;
     for (Walk walk = walk_of(); !walk.done();) {
       const Seg s = walk.next();
-      const bool direct = s.c_first == s.c_last;
+      const bool direct = s.first && s.last;  // the whole pair is in this CTA
       const size_t slot = static_cast<size_t>(s.p) + blockIdx.x;
       const bool has_tiles = s.t_begin < s.t_end;
-      if (ts == 0 && qa.spans != nullptr && s.c_first == static_cast<int>(blockIdx.x))
-        qa.spans[s.p] = make_int2(s.c_first, s.c_last);
+      if (ts == 0 && qa.spans != nullptr && s.first)
+        qa.spans[s.p] = make_int2(blockIdx.x, direct ? blockIdx.x : ranges.cta_of(s.end - 1));
 
-      // the collected row's logits of this thread's key (key 0 of the pair, head 0)
-      float* lg = a.logits == nullptr
-                      ? nullptr
-                      : a.logits + ((static_cast<size_t>(s.b) * 2 + half) * a.Hq + s.g * G) * a.P_max + row;
       float2 lacc[NC / 2];
 #pragma unroll
       for (int c = 0; c < NC / 2; ++c) lacc[c] = make_float2(0.f, 0.f);
-      float vref = kMinRef;
+      float vref = kMinRef, vscale = kPScale / kMinRef;  // (reference of the value scales)
 
       if (has_tiles) {
         // queries of this (sequence, KV group): row r = t * G + hl, in two parts
         constexpr int kCh = D / 8;
-#pragma unroll
+#pragma unroll 1
         for (int u = 0; u < (NQ * kCh + kSoftmaxThreads - 1) / kSoftmaxThreads; ++u) {
           const int idx = ts + u * kSoftmaxThreads;
           if (idx < NQ * kCh) {  // uniform per warp
@@ -639,25 +700,14 @@ __global__ void __launch_bounds__(kQThreads, 1)
         tc_fence_after();
         const uint32_t s_base = tmem + buf * Cfg::kTmemS + lane_addr;
 
-        // the logits, and with up to four heads in the group the collected row's, in one
-        // round of TMEM loads
-        float2 y[NC / 2];  // log2 units
-        float ch[4], cl[4];
-        const bool collect4 = collect && G <= 4;
-        if (collect4) {
-          if (G == 4) {
-            tmem_ld<4>(s_base + crow * 4, reinterpret_cast<uint32_t*>(ch));
-            tmem_ld<4>(s_base + NQ + crow * 4, reinterpret_cast<uint32_t*>(cl));
-          } else if (G == 2) {
-            tmem_ld<2>(s_base + crow * 2, reinterpret_cast<uint32_t*>(ch));
-            tmem_ld<2>(s_base + NQ + crow * 2, reinterpret_cast<uint32_t*>(cl));
-          } else {
-            tmem_ld<1>(s_base + crow, reinterpret_cast<uint32_t*>(ch));
-            tmem_ld<1>(s_base + NQ + crow, reinterpret_cast<uint32_t*>(cl));
-          }
-        }
-        {
-          const float2 zl = make_float2(zs * kLog2e, zs * kLog2e);
+        float2 y[NC / 2];  // logits in log2 units, then their distance to the running maxima
+        const float2 zl = make_float2(zs * kLog2e, zs * kLog2e);
+        // first visible column of this key
+        const int c_lo = j < s.P && !bad ? 0 : (j < s.L && !bad ? (j - s.P) << qa.gshift : NQ);
+        // y = the logits of this thread's columns from TMEM, hidden ones at -inf.  Rounded
+        // before the maximum is taken off: against a maximum formed from the same numbers
+        // the difference of the largest is 0 however large they are.
+        const auto load_logits = [&] {
           const float2 klo = make_float2(kQLo, kQLo);
           constexpr int kC = NC % 16 == 0 ? 16 : 8;
 #pragma unroll
@@ -669,70 +719,35 @@ __global__ void __launch_bounds__(kQThreads, 1)
 #pragma unroll
             for (int c = 0; c < kC / 4; ++c) {
               const float4 qi = *reinterpret_cast<const float4*>(qinv + col0 + c0 + 4 * c);
-              // rounded here: against a maximum formed from the same numbers the
-              // difference of the largest is 0 however large they are
               y[c0 / 2 + 2 * c] = mul2(mul2(fma2(lo[2 * c], klo, hi[2 * c]), make_float2(qi.x, qi.y)), zl);
               y[c0 / 2 + 2 * c + 1] =
                   mul2(mul2(fma2(lo[2 * c + 1], klo, hi[2 * c + 1]), make_float2(qi.z, qi.w)), zl);
             }
           }
-        }
-        // Collect-2-Query: this half's row for j < P_b (a key of an invalid page has zero
-        // logits); the two rows' group sums meet in xsum
-        float csum = 0.f;
-        if (collect) {
-          const auto put = [&](int h, float hi, float lo) {
-            const float z = bad ? 0.f : fmaf(lo, kQLo, hi) * qinv[crow * G + h] * zs;
-            if (lg != nullptr) __stcs(lg + static_cast<size_t>(h) * a.P_max + tile * kTile, z);
-            csum += z;
-          };
-          if (collect4) {
-            if (j < s.P) {
-              put(0, ch[0], cl[0]);
-              if (G >= 2) put(1, ch[1], cl[1]);
-              if (G == 4) {
-                put(2, ch[2], cl[2]);
-                put(3, ch[3], cl[3]);
-              }
-            }
-          } else {
-#pragma unroll 1
-            for (int h = 0; h < G; h += 8) {
-              uint32_t hi[8], lo[8];
-              tmem_ld<8>(s_base + crow * G + h, hi);
-              tmem_ld<8>(s_base + NQ + crow * G + h, lo);
-              tmem_wait_ld();
-              if (j < s.P) {
+          if (c_lo > 0) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) put(h + i, __uint_as_float(hi[i]), __uint_as_float(lo[i]));
-              }
+            for (int c = 0; c < NC / 2; ++c) {
+              if (col0 + 2 * c < c_lo) y[c].x = -INFINITY;
+              if (col0 + 2 * c + 1 < c_lo) y[c].y = -INFINITY;
             }
           }
-          if (half == 1) xsum[buf * kTile + row] = csum;
-        }
-        tc_fence_before();
-        if (j >= s.P || bad) {
-          // first visible column of this key
-          const int c_lo = j >= s.P && j < s.L && !bad ? (j - s.P) << qa.gshift : NQ;
+        };
+        const auto take_maxima_off = [&] {
+          float dmax = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < NC / 2; ++c) {
-            if (col0 + 2 * c < c_lo) y[c].x = -INFINITY;
-            if (col0 + 2 * c + 1 < c_lo) y[c].y = -INFINITY;
+          for (int c = 0; c < NC / 4; ++c) {
+            const float4 m = *reinterpret_cast<const float4*>(m2s + col0 + 4 * c);
+            y[2 * c] = add2(y[2 * c], make_float2(-m.x, -m.y));
+            y[2 * c + 1] = add2(y[2 * c + 1], make_float2(-m.z, -m.w));
+            dmax = fmaxf(dmax, fmaxf(fmaxf(y[2 * c].x, y[2 * c].y), fmaxf(y[2 * c + 1].x, y[2 * c + 1].y)));
           }
-        }
-        float dmax = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < NC / 4; ++c) {
-          const float4 m = *reinterpret_cast<const float4*>(m2s + col0 + 4 * c);
-          const float2 d0 = add2(y[2 * c], make_float2(-m.x, -m.y));
-          const float2 d1 = add2(y[2 * c + 1], make_float2(-m.z, -m.w));
-          dmax = fmaxf(dmax, fmaxf(fmaxf(d0.x, d0.y), fmaxf(d1.x, d1.y)));
-        }
+          return dmax;
+        };
+        load_logits();
+        const float dmax = take_maxima_off();
         const bool raise = softmax_vote(dmax > kPTau || vs > kPSlack * vref);
-        if (collect && half == 0 && j < s.P && a.partial != nullptr)
-          a.partial[(static_cast<size_t>(s.b) * a.Hkv + s.g) * a.P_max + j] =
-              csum + xsum[buf * kTile + row];
         if (raise) {
+          load_logits();  // (S^T stays until this tile's P^T is stored)
 #pragma unroll
           for (int c = 0; c < NC / 2; ++c) {
             const float mx = warp_max_f32(fmaxf(y[c].x, kNoMax)), my = warp_max_f32(fmaxf(y[c].y, kNoMax));
@@ -746,7 +761,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
             const float mx = fmaxf(fmaxf(red[c], red[64 + c]), fmaxf(red[128 + c], red[192 + c]));
             const float mo = m2s[c];
             const float mn = fmaxf(mo, mx);
-            alphas[c] = (mo == INFINITY) ? 1.f : exp2f(mo - mn);
+            alphas[c] = (mo == INFINITY) ? 1.f : ex2(mo - mn);
             m2s[c] = mn;
           }
           if (ts == 255) {
@@ -759,39 +774,41 @@ __global__ void __launch_bounds__(kQThreads, 1)
           softmax_sync();
           const float vratio = *vratio_s;
           vref = *vref_s;
+          vscale = kPScale / vref;
           const float2 vr2 = make_float2(vratio, vratio);
           if (tile != s.t_begin) {
             // O^T holds earlier tiles: rescale its columns once the last PV is done
             if (!mbar_wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, abort_flag)) set_abort();
             tc_fence_after();
             const uint32_t oa = tmem_o + lane_addr + col0;
-            float2 r[NC / 2];
-            tmem_ld_cols<NC>(oa, reinterpret_cast<uint32_t*>(r));
-            tmem_wait_ld();
+            constexpr int kC = NC % 16 == 0 ? 16 : 8;
 #pragma unroll
-            for (int c = 0; c < NC / 2; ++c) {
-              const float2 al = *reinterpret_cast<const float2*>(alphas + col0 + 2 * c);
-              lacc[c] = mul2(lacc[c], al);
-              r[c] = mul2(r[c], mul2(al, vr2));
+            for (int c0 = 0; c0 < NC; c0 += kC) {
+              float2 r[kC / 2];
+              tmem_ld<kC>(oa + c0, reinterpret_cast<uint32_t*>(r));
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < kC / 2; ++c) {
+                const float2 al = *reinterpret_cast<const float2*>(alphas + col0 + c0 + 2 * c);
+                lacc[c0 / 2 + c] = mul2(lacc[c0 / 2 + c], al);
+                r[c] = mul2(r[c], mul2(al, vr2));
+              }
+              tmem_st_cols<kC>(oa + c0, reinterpret_cast<uint32_t*>(r));
             }
-            tmem_st_cols<NC>(oa, reinterpret_cast<uint32_t*>(r));
             tmem_wait_st();
           }
+          take_maxima_off();
         }
-        const float w = vs * (kPScale / vref);
+        tc_fence_before();
+        const float w = vs * vscale;
         const float2 w2 = make_float2(w, w);
         uint32_t pk[NC / 2];
 #pragma unroll
-        for (int c = 0; c < NC / 4; ++c) {
-          const float4 m = *reinterpret_cast<const float4*>(m2s + col0 + 4 * c);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float2 dd = add2(y[2 * c + i], i == 0 ? make_float2(-m.x, -m.y) : make_float2(-m.z, -m.w));
-            const float2 pc = make_float2(ex2(dd.x), ex2(dd.y));
-            lacc[2 * c + i] = add2(lacc[2 * c + i], pc);
-            const float2 x = mul2(pc, w2);
-            pk[2 * c + i] = pack_f16x2(x.x, x.y);
-          }
+        for (int c = 0; c < NC / 2; ++c) {
+          const float2 pc = make_float2(ex2(y[c].x), ex2(y[c].y));
+          lacc[c] = add2(lacc[c], pc);
+          const float2 x = mul2(pc, w2);
+          pk[c] = pack_f16x2(x.x, x.y);
         }
         // (the PV product that last read this P^T buffer is done: see the issuer)
         uint8_t* prow = p_smem + (Cfg::kSplitP ? 0 : buf * kTile * 128);
@@ -833,21 +850,27 @@ __global__ void __launch_bounds__(kQThreads, 1)
         if (row < D) {
           const int dim = row;
           const uint32_t nans = nan_rows[dim];
+          if (nans != 0u) {
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const int cc = col0 + c;
-            if (cc < a.NV) {
-              const int t = cc >> qa.gshift, hl = cc & (G - 1);
-              if (nans & ((2u << t) - 1u)) o[c] = NAN;
-              if (direct) {
+            for (int c = 0; c < NC; ++c)
+              if (nans & ((2u << ((col0 + c) >> qa.gshift)) - 1u)) o[c] = NAN;
+          }
+          if (direct) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              const int cc = col0 + c;
+              if (cc < a.NV) {
                 const float l = red[cc] + red[64 + cc] + red[128 + cc] + red[192 + cc];
                 const __nv_bfloat16 bv = __float2bfloat16_rn(l == 0.f ? 0.f : o[c] / l);
-                a.out[((static_cast<size_t>(s.b) * a.R + t) * a.Hq + s.g * G + hl) * D + dim] =
-                    *reinterpret_cast<const uint16_t*>(&bv);
-              } else {
-                a.ws[slot_base + 2 * NQ + static_cast<size_t>(cc) * D + dim] = o[c];
+                a.out[((static_cast<size_t>(s.b) * a.R + (cc >> qa.gshift)) * a.Hq + s.g * G +
+                       (cc & (G - 1))) * D + dim] = *reinterpret_cast<const uint16_t*>(&bv);
               }
             }
+          } else {
+            float* to = a.ws + slot_base + 2 * NQ + static_cast<size_t>(col0) * D + dim;
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+              if (col0 + c < a.NV) to[c * D] = o[c];
           }
         }
         if (!direct && ts < NQ) {
