@@ -101,6 +101,29 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
   }
 }
 
+// The same wait in few instructions, for kernels with many waits in their inner loops: each
+// try suspends the thread for up to 20 us, the time and the abort flag are looked at only
+// between tries.
+__device__ __forceinline__ bool mbar_wait_compact(uint64_t* bar, uint32_t parity,
+                                                  const volatile int* abort) {
+  const uint32_t addr = smem_u32(bar);
+  uint64_t t0 = 0;
+  for (;;) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(addr), "r"(parity)
+        : "memory");
+    if (done) return true;
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if (*abort || now - t0 > VSD_WAIT_LIMIT_NS) return false;
+  }
+}
+
 // The same wait with the drain limit and no abort flag.
 __device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return true;

@@ -68,13 +68,18 @@ __device__ __forceinline__ void query_parts(float a, float b, float f, uint32_t&
 }
 
 // ---------------------------------------------------------------- probabilities
-// P is an f16 operand: x = 16 p w with p at most 2^8 above the running maximum's reference
-// and w = (the page's value scale) / (the reference of the value scales), at most 8: x stays
-// below 2^15.  11 bits of every p w above 2^-18, 2^-29 absolute below (what sums of a
-// hundred thousand small ones need).
-constexpr float kPScale = 16.f;
-constexpr float kPTau = 8.f;    // log2 of the largest p
-constexpr float kPSlack = 8.f;  // the largest w
+// What multiplies a value code is x = p vs (the probability times the value scale of the
+// key's page), so the two meet in the exponent: x = 2^(z log2 e + log2 vs - r) with one
+// reference r per column, and the sum of the probabilities takes x / vs.  No scale needs a
+// reference of its own, and no column more than one exponential.
+//
+// x is an f16 operand.  When some x would exceed 2^15, r is set so that the largest so far
+// becomes 2^2: it may grow by 2^13 before the next change, x holds 11 bits down to 2^-14
+// and is within 2^-25 below that, 2^-27 of the largest: what sums of a hundred thousand
+// small ones need.
+constexpr float kTopX = 15.f;    // log2 of the largest x
+constexpr float kRaisedX = 2.f;  // log2 of the largest x after a change of r
+constexpr float kMinVScale = 0x1p-100f;  // value scales below count as this
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -87,30 +92,10 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Packed pairs of fp32 (two roundings of one instruction).
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
-        "l"(reinterpret_cast<const uint64_t&>(c)));
-  return d;
-}
-
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
-  return d;
-}
-
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
-  return d;
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // Maximum over a warp (NaN ignored).

@@ -13,16 +13,24 @@
 // 1.5 for each two codes; 71 us a call on the 32K layer), so V is widened to f16 in shared
 // memory and P is f16.
 //
-// How: the rings and warp roles of the bf16 kernel (see verify_attn.cuh), with 16 KB tiles
-// and five more warps:
+// How: one persistent CTA per SM with the rings of the bf16 kernel (see verify_attn.cuh),
+// 16 KB tiles and 24 warps:
 //   S^T[128 keys x 2 NQ] = K[128 x d] * [Qhi; Qlo]^T   (e4m3, K-major A and B)
 //   O^T[d x NQ]         += V^T[d x 128 keys] * P^T     (f16, MN-major A and B)
 // Rows of d bytes are one swizzle span (128-byte for d = 128, 64-byte for d = 64), so a
-// page and head is one TMA box of 16 rows.  Warps 11-14 widen the V tile to f16 (exact),
-// one key per thread, into two buffers; they also clear what no row may see.  Warp 15
-// runs ahead through the block table and brings the pages' scales into shared memory, 32
-// pages (4 tiles) a round, up to 4 rounds ahead: loaded by the softmax threads one tile
-// ahead, a tile took the latency of a load from HBM (1.6 us against 0.8 us for its bytes).
+// page and head is one TMA box of 16 rows.
+//   * warps 0 and 2 copy the K and V tiles; warp 1 issues the products; warp 3 runs ahead
+//     through the block table and brings the pages' scales into shared memory, 32 pages
+//     (4 tiles) a round, up to 4 rounds ahead (loaded by the softmax threads one tile
+//     ahead, a tile took the latency of a load from HBM).
+//   * warps 4-7 widen the V tile to f16 (exact), one key per thread, into two buffers, and
+//     clear what no row may see; they also write the collected logits (in the softmax
+//     warps these took 700 of 2600 cycles a tile, in a chain that nothing overlapped).
+//   * warps 8-15 and 16-23 are two softmax groups on alternate tiles, each with its own
+//     references, P^T buffer and accumulator O^T; they meet at the end of a pair.  A tile is a chain of some 2000 cycles (wait, TMEM load,
+//     vote, exponentials, store) against 1400 for its bytes from HBM: one group of eight
+//     warps was bound by that chain (368 us for the batch of 16 x 32K, 72B geometry),
+//     two overlap it.
 //
 // The work is the list of all (sequence, KV head, 128-key tile) in order, cut into equal
 // ranges, one for each SM's CTA, by the sequences' real lengths (up to 256 sequences, whose
@@ -30,9 +38,13 @@
 // as the longest admissible).  Along the list either the pair or the CTA changes from one
 // partial result to the next, so slot (pair + CTA) holds it: pairs + CTAs slots in all.
 //
-// The running maximum of a column is raised (one vote per tile) when a logit exceeds it by
-// more than 2^8; the same vote raises the reference of the value scales when a page's is
-// more than 8 times it, so that p * vs / vref fits f16.
+// Every column has a reference r (see quant.cuh) that one vote per tile raises when it has
+// to; a raise costs 1500 cycles, so it leaves room of 2^13 (with 2^8 and 48 columns that
+// grow at different times, every fourth tile of a part of 54 tiles had one).
+//
+// Of the warps that wait for the same thing one polls the mbarrier and the others wait at a
+// hardware barrier: with every warp polling, 500 tries a tile and their loops were half of
+// all instructions issued.
 #pragma once
 
 #include "quant.cuh"
@@ -45,21 +57,37 @@ using namespace ptx;
 using verify_detail::kHistBins;
 using verify_detail::kPage;
 using verify_detail::kPagesPerTile;
-using verify_detail::kSoftmaxThreads;
 using verify_detail::kTile;
-using verify_detail::kVWarp;
-using verify_detail::softmax_sync;
-using verify_detail::softmax_vote;
 using verify_detail::VParams;
 
-constexpr float kNoMax = -3e38f;     // a running maximum before the first key (finite: no NaN arises)
-constexpr float kMinRef = 0x1p-120f;  // smallest reference of the value scales
-constexpr int kWidenWarp = 11;        // warps 11-14 widen V
+constexpr float kNoMax = -3e38f;      // a reference before the first key (finite: no NaN arises)
+constexpr int kVProdWarp = 2;         // warp 0: K tiles, 1: products, 2: V tiles, 3: scales
+constexpr int kScaleWarp = 3;
+constexpr int kWidenWarp = 4;         // warps 4-7
+constexpr int kSoftWarp = 8;          // warps 8-15 and 16-23
 constexpr int kWidenThreads = 128;
-constexpr int kScaleWarp = 15;        // warp 15 fetches the pages' scales
-constexpr int kQThreads = 512;
+constexpr int kGroupThreads = 256;    // one softmax group
+constexpr int kSoftThreads = 512;
+constexpr int kQThreads = 768;
 constexpr int kRounds = 4;            // rounds of 4 tiles of scales in shared memory
 constexpr int kTableSeqs = 256;       // sequences whose lengths every CTA holds
+
+__device__ __forceinline__ bool group_vote(int group, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(pred)), "r"(1 + group), "n"(kGroupThreads)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ void group_sync(int group) { named_barrier_sync(1 + group, kGroupThreads); }
+__device__ __forceinline__ void soft_sync() { named_barrier_sync(3, kSoftThreads); }
+__device__ __forceinline__ void widen_sync() { named_barrier_sync(4, kWidenThreads); }
 
 struct QVParams {
   VParams v;
@@ -197,14 +225,14 @@ struct QCfg {
   static constexpr int kOffQ = kOffWide + 2 * kWideBytes;
   static constexpr int kOffP = kOffQ + kQBytes;
   static constexpr int kOffMisc = kOffP + kPBytes;
-  static constexpr int kMiscBytes = 8192;
+  static constexpr int kMiscBytes = 9216;
   // d = 64: the PV product reads 16 KB past a widened tile (rows of the accumulator that
   // are never used); the Q, P and misc areas behind the last one cover that
   static constexpr int kSmemBytes =
-      (kOffMisc + kMiscBytes > kOffQ + kHalfBytes ? kOffMisc + kMiscBytes : kOffQ + kHalfBytes) + 1024;
+      (kOffMisc + kMiscBytes > kOffQ + kHalfBytes ? kOffMisc + kMiscBytes : kOffQ + kHalfBytes);
   static constexpr int kTmemS = 2 * NQ;               // columns of one S^T buffer
-  static constexpr int kTmemO = 2 * kTmemS;           // first column of O^T
-  static constexpr int kTmemCols = 5 * NQ <= 128 ? 128 : (5 * NQ <= 256 ? 256 : 512);
+  static constexpr int kTmemO = 2 * kTmemS;           // O^T of the two groups
+  static constexpr int kTmemCols = 6 * NQ <= 128 ? 128 : (6 * NQ <= 256 ? 256 : 512);
   static_assert(kQBytes % 1024 == 0 && kOffQ % 1024 == 0, "swizzle atoms need 1 KB alignment");
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
@@ -217,9 +245,8 @@ __global__ void __launch_bounds__(kQThreads, 1)
   constexpr int ST = Cfg::kStages;
   constexpr int NC = NQ / 2;  // columns per softmax thread
   const VParams& a = qa.v;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t verify_quant_smem[];
+  uint8_t* const base = verify_quant_smem;
   uint8_t* k_ring = base;
   uint8_t* v_ring = base + Cfg::kOffV;
   uint8_t* wide = base + Cfg::kOffWide;
@@ -240,19 +267,19 @@ __global__ void __launch_bounds__(kQThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 448);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 452);
   static_assert((4 * ST + 6 + 2 * kRounds + 2) * 8 <= 448, "barriers");
-  float* vref_s = reinterpret_cast<float*>(misc + 456);        // reference of the value scales
-  float* vratio_s = vref_s + 1;                                // its last change (old / new)
-  float* m2s = reinterpret_cast<float*>(misc + 512);           // [64] running maxima
-  float* alphas = m2s + 64;                                    // [64] rescale factors
-  float* qinv = alphas + 64;                                   // [64] 1 / query scale
-  float* red = qinv + 64;                                      // [4][64] reductions
-  float* vred = red + 256;                                     // [8] largest value scale per warp
-  uint32_t* nan_rows = reinterpret_cast<uint32_t*>(vred + 8);  // [D] verify-block rows with a NaN
-  // [kRounds][2][32] scales of K and V (a key scale below 0: no such page)
+  float* quni_s = reinterpret_cast<float*>(misc + 456);        // 1 / query scale of all rows, or 0
+  float* m2s = reinterpret_cast<float*>(misc + 512);           // [2][64] references
+  float* alphas = m2s + 128;                                   // [2][64] rescale factors
+  float* qinv = alphas + 128;                                  // [64] 1 / query scale of a row
+  float* red = qinv + 64;                                      // [2][4][64] reductions
+  uint32_t* qmax = reinterpret_cast<uint32_t*>(red + 512);     // [64] largest |q| of a row, as bf16 bits
+  uint32_t* nan_rows = qmax + 64;                              // [D] verify-block rows with a NaN
+  // [kRounds][3][32] per page: key scale (below 0: no such page), log2 and inverse of the
+  // value scale
   float* sc_s = reinterpret_cast<float*>(nan_rows + 128);
-  int* cum_s = reinterpret_cast<int*>(sc_s + kRounds * 64);  // first tile of each sequence
-  int* plen_s = reinterpret_cast<int*>(cum_s + kTableSeqs + 1);
-  static_assert(512 + (64 * 3 + 256 + 8 + 128 + kRounds * 64 + 2 * kTableSeqs + 1) * 4 <=
+  int* cum_s = reinterpret_cast<int*>(sc_s + kRounds * 96);    // first tile of each sequence
+  int* plen_s = cum_s + kTableSeqs + 1;
+  static_assert(512 + (128 * 2 + 64 + 512 + 64 + 128 + kRounds * 96 + 2 * kTableSeqs + 1) * 4 <=
                     Cfg::kMiscBytes,
                 "misc area");
 
@@ -269,14 +296,14 @@ __global__ void __launch_bounds__(kQThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], kSoftmaxThreads + kWidenThreads);
+      mbar_init(&p_full[i], kGroupThreads + kWidenThreads);
       mbar_init(&pv_done[i], 1);
     }
     for (int i = 0; i < kRounds; ++i) {
       mbar_init(&sc_full[i], 1);
-      mbar_init(&sc_empty[i], kSoftmaxThreads + (collect_any ? kWidenThreads : 0));
+      mbar_init(&sc_empty[i], kSoftThreads + (collect_any ? kWidenThreads : 0));
     }
-    mbar_init(q_ready, kSoftmaxThreads);
+    mbar_init(q_ready, kSoftThreads);
     mbar_init(mma_fin, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
@@ -331,7 +358,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
     }
   };
 
-  if (warp == 0 || warp == kVWarp) {
+  if (warp == 0 || warp == kVProdWarp) {
     // ------------------------------------------------------------ TMA producers
     const bool is_k = warp == 0;
     const CUtensorMap* map = is_k ? &kmap : &vmap;
@@ -368,7 +395,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
         const int stage = it % ST;
         const uint32_t use = it / ST;
         int ok = 1;
-        if (lane == 0 && use > 0) ok = mbar_wait(&empty[stage], (use - 1) & 1, abort_flag);
+        if (lane == 0 && use > 0) ok = mbar_wait_compact(&empty[stage], (use - 1) & 1, abort_flag);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok && lane == 0) set_abort();
         if (*abort_flag) continue;
@@ -414,7 +441,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
     }
     Walk qw = walk_of();
     int q_begin = 0, q_end = 0, q_tile = 0;  // the segment of the next QK product
-    uint32_t nseg = 0, first_bits = 0;       // bit (i & 31): tile i is its segment's first
+    uint32_t nseg = 0, first_bits = 0;       // bit (i & 31): tile i is its group's first in the segment
     uint32_t qi = 0, pi = 0;
     bool ok = true;
     while (pi < total && ok) {
@@ -428,8 +455,8 @@ __global__ void __launch_bounds__(kQThreads, 1)
       const bool first = q_tile == q_begin;
       if (qi < total && (first ? pi == qi : qi < pi + 2)) {
         const uint32_t stage = qi % ST, buf = qi & 1;
-        if (first) ok = mbar_wait(q_ready, nseg & 1, abort_flag);
-        ok = ok && mbar_wait(&k_full[stage], (qi / ST) & 1, abort_flag);
+        if (first) ok = mbar_wait_compact(q_ready, nseg & 1, abort_flag);
+        ok = ok && mbar_wait_compact(&k_full[stage], (qi / ST) & 1, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -440,17 +467,16 @@ __global__ void __launch_bounds__(kQThreads, 1)
                      kk > 0 ? 1u : 0u);
         umma_commit_if(leader, &k_empty[stage]);
         umma_commit_if(leader, &s_full[buf]);
-        if (first) {
+        if (q_tile < q_begin + 2)
           first_bits |= 1u << (qi & 31);
-          ++nseg;
-        } else {
+        else
           first_bits &= ~(1u << (qi & 31));
-        }
+        if (first) ++nseg;
         ++q_tile;
         ++qi;
       } else {
         const uint32_t buf = pi & 1;
-        ok = mbar_wait(&p_full[buf], (pi >> 1) & 1, abort_flag);  // P^T and the widened V
+        ok = mbar_wait_compact(&p_full[buf], (pi >> 1) & 1, abort_flag);  // P^T and the widened V
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -459,7 +485,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
         const uint64_t bd = p_desc + buf * ((Cfg::kSplitP ? 64 : kTile * 128) >> 4);
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
-          umma_f16_if(leader, tmem_o, ad + kk * 128, bd + kk * 128, idesc_pv, kk > 0 ? 1u : keep);
+          umma_f16_if(leader, tmem_o + buf * NQ, ad + kk * 128, bd + kk * 128, idesc_pv, kk > 0 ? 1u : keep);
         umma_commit_if(leader, &pv_done[buf]);
         ++pi;
       }
@@ -484,7 +510,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
         return tile < s.t_end && lp < (s.L + kPage - 1) / kPage ? __ldcg(bt_row + lp) : -1;
       };
       const auto scales_at = [&](int e) {
-        if (e < 0 || e >= a.num_blocks) return make_float2(-1.f, 0.f);
+        if (e < 0 || e >= a.num_blocks) return make_float2(-1.f, 1.f);
         const size_t at = static_cast<size_t>(e) * a.Hkv + s.g;
         return make_float2(__ldcg(qa.k_scale + at), __ldcg(qa.v_scale + at));
       };
@@ -498,16 +524,18 @@ __global__ void __launch_bounds__(kQThreads, 1)
         const int slot = round % kRounds;
         int ok = 1;
         if (lane == 0 && round >= kRounds)
-          ok = mbar_wait(&sc_empty[slot], (round / kRounds - 1) & 1, abort_flag);
+          ok = mbar_wait_compact(&sc_empty[slot], (round / kRounds - 1) & 1, abort_flag);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok && lane == 0) set_abort();
-        sc_s[slot * 64 + lane] = now.x;
-        sc_s[slot * 64 + 32 + lane] = now.y;
+        const float vs = fmaxf(now.y, kMinVScale);
+        sc_s[slot * 96 + lane] = now.x;
+        sc_s[slot * 96 + 32 + lane] = lg2(vs);
+        sc_s[slot * 96 + 64 + lane] = 1.f / vs;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sc_full[slot]);
       }
     }
-  } else if (warp >= kWidenWarp) {
+  } else if (warp < kSoftWarp) {
     // ------------------------------------------------------------ V codes to f16, logits out
     const int row = (warp & 3) * 32 + lane;  // key in tile (and TMEM lane)
     const bool collect = collect_any;
@@ -519,42 +547,49 @@ __global__ void __launch_bounds__(kQThreads, 1)
       const uint32_t seg_parity = nseg++ & 1;
       for (int tile = s.t_begin; tile < s.t_end; ++tile, ++it) {
         const int stage = it % ST;
-        if (!mbar_wait(&v_full[stage], (it / ST) & 1, abort_flag)) set_abort();
-        const uint8_t* src = v_ring + stage * Cfg::kTileBytes;
+        if (warp == kWidenWarp &&
+            !(mbar_wait_compact(&v_full[stage], (it / ST) & 1, abort_flag) &&
+              // the PV product that last read this buffer must be done
+              (it < 2 || mbar_wait_compact(&pv_done[it & 1], ((it - 2) >> 1) & 1, abort_flag))))
+          set_abort();
+        widen_sync();
+        uint8_t* src = v_ring + stage * Cfg::kTileBytes;
+        const int j = tile * kTile + row;
         uint4 x[D / 16];
 #pragma unroll
         for (int c = 0; c < D / 16; ++c)
           x[c] = *reinterpret_cast<const uint4*>(src + swizzled_chunk<D>(row, c));
-        mbar_arrive(&v_empty[stage]);
-        const int j = tile * kTile + row;
         if (j >= s.P) {
           // Rows past the end hold whatever the cache holds: zeros in their place.  In the
           // verify block's rows a NaN would reach the rows that do not see it (0 * NaN): it
           // is cleared here, and put back into the rows that do in the epilogue.
+          const uint32_t keep = j < s.L ? 0xFFFFFFFFu : 0u;
+          uint32_t nan = 0;  // a byte whose low seven bits are all ones carries into bit 7
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
-            uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (j >= s.L) w[i] = 0u;
-              // bytes whose low seven bits are all ones
-              if (__vcmpeq4(w[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0u) {
-                // the softmax threads have reset nan_rows for this segment
-                if (!mbar_wait(q_ready, seg_parity, abort_flag)) set_abort();
+            x[c].x &= keep, x[c].y &= keep, x[c].z &= keep, x[c].w &= keep;
+            nan |= ((x[c].x & 0x7F7F7F7Fu) + 0x01010101u) | ((x[c].y & 0x7F7F7F7Fu) + 0x01010101u) |
+                   ((x[c].z & 0x7F7F7F7Fu) + 0x01010101u) | ((x[c].w & 0x7F7F7F7Fu) + 0x01010101u);
+          }
+          if (nan & 0x80808080u) {
+            // rare: clean the row in shared memory, once the softmax threads have reset
+            // nan_rows for this segment
+            if (!mbar_wait_compact(q_ready, seg_parity, abort_flag)) set_abort();
 #pragma unroll 1
-                for (int y = 0; y < 4; ++y) {
-                  if (((w[i] >> (8 * y)) & 0x7Fu) == 0x7Fu) {
-                    atomicOr(&nan_rows[c * 16 + i * 4 + y], 1u << (j - s.P));
-                    w[i] &= ~(0xFFu << (8 * y));
-                  }
-                }
+            for (int c = 0; c < D; ++c) {
+              uint8_t* at = src + swizzled_chunk<D>(row, c >> 4) + (c & 15);
+              if ((*at & 0x7Fu) == 0x7Fu) {
+                atomicOr(&nan_rows[c], 1u << (j - s.P));
+                *at = 0;
               }
             }
-            x[c] = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+              x[c] = *reinterpret_cast<const uint4*>(src + swizzled_chunk<D>(row, c));
+            fence_proxy_async_smem();  // (the next copy into this stage comes after these writes)
           }
         }
-        // the PV product that last read this buffer must be done
-        if (it >= 2 && !mbar_wait(&pv_done[it & 1], ((it - 2) >> 1) & 1, abort_flag)) set_abort();
+        mbar_arrive(&v_empty[stage]);
         uint8_t* dst = wide + (it & 1) * Cfg::kWideBytes;
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
@@ -571,12 +606,16 @@ __global__ void __launch_bounds__(kQThreads, 1)
           // Collect-2-Query: the two rows' logits of this thread's key and their group sum
           // (a key of an invalid page has zero logits)
           const int k4 = (tile - s.t_begin) & 3;
-          if (k4 == 0 && !mbar_wait(&sc_full[round % kRounds], (round / kRounds) & 1, abort_flag)) set_abort();
-          const float ks = sc_s[(round % kRounds) * 64 + k4 * kPagesPerTile + row / kPage];
+          if (warp == kWidenWarp &&
+              !((k4 != 0 || mbar_wait_compact(&sc_full[round % kRounds], (round / kRounds) & 1, abort_flag)) &&
+                mbar_wait_compact(&s_full[it & 1], (it >> 1) & 1, abort_flag)))
+            set_abort();
+          widen_sync();
+          const float ks = sc_s[(round % kRounds) * 96 + k4 * kPagesPerTile + row / kPage];
           if (k4 == 3 || tile + 1 == s.t_end) mbar_arrive(&sc_empty[round++ % kRounds]);
-          if (!mbar_wait(&s_full[it & 1], (it >> 1) & 1, abort_flag)) set_abort();
           tc_fence_after();
-          const float zs = ks < 0.f ? 0.f : ks * a.scale;
+          const float quni = *quni_s;  // 0: every row has its own scale
+          const float zs = ks < 0.f ? 0.f : ks * a.scale * (quni == 0.f ? 1.f : quni);
           const uint32_t s_base = tmem + (it & 1) * Cfg::kTmemS + (static_cast<uint32_t>((warp & 3) * 32) << 16);
           float csum = 0.f;
           const auto group = [&](auto width) {  // kH heads at a time
@@ -594,8 +633,9 @@ __global__ void __launch_bounds__(kQThreads, 1)
                 if (j < s.P) {
 #pragma unroll
                   for (int i = 0; i < kH; ++i) {
-                    const float t = fmaf(__uint_as_float(lo[i]), kQLo, __uint_as_float(hi[i])) * qinv[col + h + i];
-                    const float z = ks < 0.f ? 0.f : t * zs;
+                    // (the keys of an invalid page were filled with zeros)
+                    float z = fmaf(__uint_as_float(lo[i]), kQLo, __uint_as_float(hi[i])) * zs;
+                    if (quni == 0.f) z *= qinv[col + h + i];
                     if (a.logits != nullptr) __stcs(lg, z);
                     lg += a.P_max;
                     csum += z;
@@ -619,50 +659,80 @@ __global__ void __launch_bounds__(kQThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax / epilogue
-    const int sw = warp - 2;
-    const int quarter = warp & 3;              // TMEM lane quarter
-    const int half = sw >> 2;                  // which NC columns
-    const int row = quarter * 32 + lane;       // key in tile (S^T) / dimension (O^T)
-    const int ts = threadIdx.x - 64;           // 0..255
+    const int ts = threadIdx.x - 32 * kSoftWarp;  // 0..511
+    const int grp = ts >> 8;                      // this group's tiles: it & 1 == grp
+    const int tg = ts & (kGroupThreads - 1);
+    const int sw = tg >> 5;
+    const int quarter = warp & 3;                 // TMEM lane quarter
+    const int half = sw >> 2;                     // which NC columns
+    const int row = quarter * 32 + lane;          // key in tile (S^T) / dimension (O^T)
     const int col0 = half * NC;
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const int G = 1 << qa.gshift;
+    float* m2 = m2s + grp * 64;
+    float* alpha = alphas + grp * 64;
+    float* redg = red + grp * 256;
+    const uint32_t s_base = tmem + grp * Cfg::kTmemS + lane_addr;
+    const uint32_t o_base = tmem_o + grp * NQ + lane_addr + col0;
+    uint8_t* const prow = p_smem + (Cfg::kSplitP ? 0 : grp * kTile * 128);
     uint32_t it = 0, round = 0;
     for (Walk walk = walk_of(); !walk.done();) {
       const Seg s = walk.next();
       const bool direct = s.first && s.last;  // the whole pair is in this CTA
-      const size_t slot = static_cast<size_t>(s.p) + blockIdx.x;
       const bool has_tiles = s.t_begin < s.t_end;
       if (ts == 0 && qa.spans != nullptr && s.first)
         qa.spans[s.p] = make_int2(blockIdx.x, direct ? blockIdx.x : ranges.cta_of(s.end - 1));
 
-      float2 lacc[NC / 2];
+      float lacc[NC];
 #pragma unroll
-      for (int c = 0; c < NC / 2; ++c) lacc[c] = make_float2(0.f, 0.f);
-      float vref = kMinRef, vscale = kPScale / kMinRef;  // (reference of the value scales)
+      for (int c = 0; c < NC; ++c) lacc[c] = 0.f;
+      bool started = false;  // this group's O^T holds tiles of the segment
+      const uint32_t it0 = it;
+      float quni = 0.f;      // 1 / query scale of all rows, or 0
 
       if (has_tiles) {
         // queries of this (sequence, KV group): row r = t * G + hl, in two parts
         constexpr int kCh = D / 8;
-#pragma unroll 1
-        for (int u = 0; u < (NQ * kCh + kSoftmaxThreads - 1) / kSoftmaxThreads; ++u) {
-          const int idx = ts + u * kSoftmaxThreads;
-          if (idx < NQ * kCh) {  // uniform per warp
-            const int r = idx / kCh, ch = idx % kCh;
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (r < a.NV)
-              x = ldg_stream16(a.q + ((static_cast<size_t>(s.b) * a.R + (r >> qa.gshift)) * a.Hq +
-                                      s.g * G + (r & (G - 1))) * D + ch * 8);
-            uint32_t mx = 0;
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        constexpr int kQL = (NQ * kCh + kSoftThreads - 1) / kSoftThreads;
+        uint4 qv[kQL];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              mx = max(mx, w[i] & 0x7FFFu);
-              mx = max(mx, (w[i] >> 16) & 0x7FFFu);
-            }
+        for (int u = 0; u < kQL; ++u) {
+          const int idx = ts + u * kSoftThreads;
+          const int r = idx / kCh, ch = idx % kCh;
+          qv[u] = make_uint4(0, 0, 0, 0);
+          if (r < a.NV)
+            qv[u] = ldg_stream16(a.q + ((static_cast<size_t>(s.b) * a.R + (r >> qa.gshift)) * a.Hq +
+                                        s.g * G + (r & (G - 1))) * D + ch * 8);
+        }
+#pragma unroll
+        for (int u = 0; u < kQL; ++u) {
+          const int idx = ts + u * kSoftThreads;
+          if (idx < NQ * kCh) {  // uniform per warp
+            uint32_t mx = 0;
+            const uint32_t w[4] = {qv[u].x, qv[u].y, qv[u].z, qv[u].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mx = max(mx, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
 #pragma unroll
             for (int o = kCh / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const QScale qs = query_scale(mx);
+            if (idx % kCh == 0) qmax[idx / kCh] = mx;
+          }
+        }
+        soft_sync();
+        // one scale for rows whose largest magnitudes lie within 2^4 of each other (rows of
+        // zeros fit any): the logits then need no factor per column
+        const uint32_t r0 = lane < NQ ? qmax[lane] : 0u, r1 = lane + 32 < NQ ? qmax[lane + 32] : 0u;
+        const uint32_t top = __reduce_max_sync(0xffffffffu, max(r0, r1));
+        const uint32_t low = __reduce_min_sync(0xffffffffu, min(r0 ? r0 : 0xFFFFu, r1 ? r1 : 0xFFFFu));
+        const bool uniform = top == 0u || (top >> 7) - (low >> 7) <= 4u;
+        const QScale qu = query_scale(top);
+        quni = uniform ? qu.inv : 0.f;
+#pragma unroll
+        for (int u = 0; u < kQL; ++u) {
+          const int idx = ts + u * kSoftThreads;
+          if (idx < NQ * kCh) {
+            const int r = idx / kCh, ch = idx % kCh;
+            const uint32_t w[4] = {qv[u].x, qv[u].y, qv[u].z, qv[u].w};
+            const QScale qs = uniform ? qu : query_scale(qmax[r]);
             if (ch == 0) qinv[r] = qs.inv;
             uint32_t hi[4], lo[4];
 #pragma unroll
@@ -675,213 +745,199 @@ __global__ void __launch_bounds__(kQThreads, 1)
           }
         }
         // padded columns: p = exp2(-inf) = 0, and they never raise the maximum
-        if (ts < 64) m2s[ts] = (ts < a.NV) ? kNoMax : INFINITY;
+        if (ts < 128) m2s[ts] = ((ts & 63) < a.NV) ? kNoMax : INFINITY;
         if (ts < D) nan_rows[ts] = 0u;
-        if (ts == 0) *vref_s = kMinRef;
+        if (ts == 0) *quni_s = quni;
         fence_proxy_async_smem();
         mbar_arrive(q_ready);
-        softmax_sync();  // qinv, m2s
+        soft_sync();  // qinv, m2s
       }
 
+      const float zq = a.scale * kLog2e * (quni == 0.f ? 1.f : quni);
       for (int tile = s.t_begin; tile < s.t_end; ++tile, ++it) {
-        const int buf = it & 1;
         const int k4 = (tile - s.t_begin) & 3;
-        if (k4 == 0 && !mbar_wait(&sc_full[round % kRounds], (round / kRounds) & 1, abort_flag)) set_abort();
-        const float* sc = sc_s + (round % kRounds) * 64 + k4 * kPagesPerTile + row / kPage;
-        const float ks = sc[0];
-        const float vs = sc[32];
+        const bool mine = static_cast<int>(it & 1) == grp;  // else the other group's tile
+        if (mine) {
+          // (a test build waits for a barrier that nothing completes yet)
+          if (sw == 0 &&
+              !(mbar_wait_compact(&sc_full[round % kRounds], (round / kRounds) & 1, abort_flag) &&
+                (VSD_STALL(it == 0) ? mbar_wait_compact(mma_fin, 0, abort_flag)
+                                    : mbar_wait_compact(&s_full[grp], (it >> 1) & 1, abort_flag))))
+            set_abort();
+          group_sync(grp);
+        }
+        const float* sc = sc_s + (round % kRounds) * 96 + k4 * kPagesPerTile + row / kPage;
+        const float ks = sc[0], lvs = sc[32], ivs = sc[64];
         if (k4 == 3 || tile + 1 == s.t_end) mbar_arrive(&sc_empty[round++ % kRounds]);
-        if (!(VSD_STALL(it == 0) ? mbar_wait(mma_fin, 0, abort_flag)
-                                 : mbar_wait(&s_full[buf], (it >> 1) & 1, abort_flag)))
-          set_abort();
+        if (!mine) continue;
         const int j = tile * kTile + row;
         const bool bad = ks < 0.f;  // no such page (past the end too)
-        const float zs = ks * a.scale;
+        const float zl = ks * zq;
         tc_fence_after();
-        const uint32_t s_base = tmem + buf * Cfg::kTmemS + lane_addr;
-
-        float2 y[NC / 2];  // logits in log2 units, then their distance to the running maxima
-        const float2 zl = make_float2(zs * kLog2e, zs * kLog2e);
         // first visible column of this key
         const int c_lo = j < s.P && !bad ? 0 : (j < s.L && !bad ? (j - s.P) << qa.gshift : NQ);
-        // y = the logits of this thread's columns from TMEM, hidden ones at -inf.  Rounded
-        // before the maximum is taken off: against a maximum formed from the same numbers
-        // the difference of the largest is 0 however large they are.
+        float y[NC];  // z log2 e + log2 vs, then its distance to the references
+        // From the two parts' logits of this thread's columns in TMEM; hidden ones are -inf.
+        // Rounded before the reference is taken off: a reference formed from the same
+        // numbers stays at its distance from the largest however large they are.
         const auto load_logits = [&] {
-          const float2 klo = make_float2(kQLo, kQLo);
-          constexpr int kC = NC % 16 == 0 ? 16 : 8;
 #pragma unroll
-          for (int c0 = 0; c0 < NC; c0 += kC) {
-            float2 hi[kC / 2], lo[kC / 2];
-            tmem_ld<kC>(s_base + col0 + c0, reinterpret_cast<uint32_t*>(hi));
-            tmem_ld<kC>(s_base + NQ + col0 + c0, reinterpret_cast<uint32_t*>(lo));
+          for (int c0 = 0; c0 < NC; c0 += 8) {
+            float hi[8], lo[8];
+            tmem_ld<8>(s_base + col0 + c0, reinterpret_cast<uint32_t*>(hi));
+            tmem_ld<8>(s_base + NQ + col0 + c0, reinterpret_cast<uint32_t*>(lo));
             tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < kC / 4; ++c) {
-              const float4 qi = *reinterpret_cast<const float4*>(qinv + col0 + c0 + 4 * c);
-              y[c0 / 2 + 2 * c] = mul2(mul2(fma2(lo[2 * c], klo, hi[2 * c]), make_float2(qi.x, qi.y)), zl);
-              y[c0 / 2 + 2 * c + 1] =
-                  mul2(mul2(fma2(lo[2 * c + 1], klo, hi[2 * c + 1]), make_float2(qi.z, qi.w)), zl);
+            for (int i = 0; i < 8; ++i) y[c0 + i] = fmaf(lo[i], kQLo, hi[i]);
+            if (quni == 0.f) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) y[c0 + i] *= qinv[col0 + c0 + i];
             }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[c0 + i] = __fmaf_rn(y[c0 + i], zl, lvs);
           }
           if (c_lo > 0) {
 #pragma unroll
-            for (int c = 0; c < NC / 2; ++c) {
-              if (col0 + 2 * c < c_lo) y[c].x = -INFINITY;
-              if (col0 + 2 * c + 1 < c_lo) y[c].y = -INFINITY;
-            }
+            for (int c = 0; c < NC; ++c)
+              if (col0 + c < c_lo) y[c] = -INFINITY;
           }
         };
-        const auto take_maxima_off = [&] {
+        const auto take_references_off = [&] {
           float dmax = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < NC / 4; ++c) {
-            const float4 m = *reinterpret_cast<const float4*>(m2s + col0 + 4 * c);
-            y[2 * c] = add2(y[2 * c], make_float2(-m.x, -m.y));
-            y[2 * c + 1] = add2(y[2 * c + 1], make_float2(-m.z, -m.w));
-            dmax = fmaxf(dmax, fmaxf(fmaxf(y[2 * c].x, y[2 * c].y), fmaxf(y[2 * c + 1].x, y[2 * c + 1].y)));
+          for (int c = 0; c < NC; c += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(m2 + col0 + c);
+            y[c] -= m.x;
+            y[c + 1] -= m.y;
+            y[c + 2] -= m.z;
+            y[c + 3] -= m.w;
+            dmax = fmaxf(dmax, fmaxf(fmaxf(y[c], y[c + 1]), fmaxf(y[c + 2], y[c + 3])));
           }
           return dmax;
         };
         load_logits();
-        const float dmax = take_maxima_off();
-        const bool raise = softmax_vote(dmax > kPTau || vs > kPSlack * vref);
-        if (raise) {
+        const float dmax = take_references_off();
+        if (group_vote(grp, dmax > kTopX)) {
           load_logits();  // (S^T stays until this tile's P^T is stored)
 #pragma unroll
-          for (int c = 0; c < NC / 2; ++c) {
-            const float mx = warp_max_f32(fmaxf(y[c].x, kNoMax)), my = warp_max_f32(fmaxf(y[c].y, kNoMax));
-            if (lane == 0) *reinterpret_cast<float2*>(red + quarter * 64 + col0 + 2 * c) = make_float2(mx, my);
+          for (int c = 0; c < NC; c += 2) {
+            const float mx = warp_max_f32(fmaxf(y[c], kNoMax)), my = warp_max_f32(fmaxf(y[c + 1], kNoMax));
+            if (lane == 0) *reinterpret_cast<float2*>(redg + quarter * 64 + col0 + c) = make_float2(mx, my);
           }
-          const float vm = warp_max_f32(vs);
-          if (lane == 0) vred[sw] = vm;
-          softmax_sync();
-          if (ts < NQ) {
-            const int c = ts;
-            const float mx = fmaxf(fmaxf(red[c], red[64 + c]), fmaxf(red[128 + c], red[192 + c]));
-            const float mo = m2s[c];
-            const float mn = fmaxf(mo, mx);
-            alphas[c] = (mo == INFINITY) ? 1.f : ex2(mo - mn);
-            m2s[c] = mn;
+          group_sync(grp);
+          if (tg < NQ) {
+            const float mx = fmaxf(fmaxf(redg[tg], redg[64 + tg]), fmaxf(redg[128 + tg], redg[192 + tg]));
+            const float mo = m2[tg];
+            const float mn = fmaxf(mo, mx - kRaisedX);
+            alpha[tg] = mo == mn ? 1.f : ex2(mo - mn);
+            m2[tg] = mn;
           }
-          if (ts == 255) {
-            float vm8 = vref;
+          group_sync(grp);
+          if (started) {
+            // O^T holds earlier tiles (their products are done: see the issuer)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) vm8 = fmaxf(vm8, vred[i]);
-            *vratio_s = vref / vm8;
-            *vref_s = vm8;
-          }
-          softmax_sync();
-          const float vratio = *vratio_s;
-          vref = *vref_s;
-          vscale = kPScale / vref;
-          const float2 vr2 = make_float2(vratio, vratio);
-          if (tile != s.t_begin) {
-            // O^T holds earlier tiles: rescale its columns once the last PV is done
-            if (!mbar_wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, abort_flag)) set_abort();
-            tc_fence_after();
-            const uint32_t oa = tmem_o + lane_addr + col0;
-            constexpr int kC = NC % 16 == 0 ? 16 : 8;
-#pragma unroll
-            for (int c0 = 0; c0 < NC; c0 += kC) {
-              float2 r[kC / 2];
-              tmem_ld<kC>(oa + c0, reinterpret_cast<uint32_t*>(r));
+            for (int c0 = 0; c0 < NC; c0 += 8) {
+              float r[8];
+              tmem_ld<8>(o_base + c0, reinterpret_cast<uint32_t*>(r));
               tmem_wait_ld();
 #pragma unroll
-              for (int c = 0; c < kC / 2; ++c) {
-                const float2 al = *reinterpret_cast<const float2*>(alphas + col0 + c0 + 2 * c);
-                lacc[c0 / 2 + c] = mul2(lacc[c0 / 2 + c], al);
-                r[c] = mul2(r[c], mul2(al, vr2));
+              for (int c = 0; c < 8; ++c) {
+                const float al = alpha[col0 + c0 + c];
+                lacc[c0 + c] *= al;
+                r[c] *= al;
               }
-              tmem_st_cols<kC>(oa + c0, reinterpret_cast<uint32_t*>(r));
+              tmem_st8(o_base + c0, reinterpret_cast<uint32_t*>(r));
             }
             tmem_wait_st();
           }
-          take_maxima_off();
+          take_references_off();
         }
+        started = true;
         tc_fence_before();
-        const float w = vs * vscale;
-        const float2 w2 = make_float2(w, w);
-        uint32_t pk[NC / 2];
-#pragma unroll
-        for (int c = 0; c < NC / 2; ++c) {
-          const float2 pc = make_float2(ex2(y[c].x), ex2(y[c].y));
-          lacc[c] = add2(lacc[c], pc);
-          const float2 x = mul2(pc, w2);
-          pk[c] = pack_f16x2(x.x, x.y);
-        }
         // (the PV product that last read this P^T buffer is done: see the issuer)
-        uint8_t* prow = p_smem + (Cfg::kSplitP ? 0 : buf * kTile * 128);
 #pragma unroll
         for (int k = 0; k < NC / 8; ++k) {
-          const int ch = (Cfg::kSplitP ? buf * 4 : 0) + col0 / 8 + k;
-          *reinterpret_cast<uint4*>(prow + swizzled_chunk<128>(row, ch)) =
-              make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+          uint32_t pk[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float pa = ex2(y[8 * k + 2 * i]), pb = ex2(y[8 * k + 2 * i + 1]);
+            lacc[8 * k + 2 * i] = fmaf(pa, ivs, lacc[8 * k + 2 * i]);
+            lacc[8 * k + 2 * i + 1] = fmaf(pb, ivs, lacc[8 * k + 2 * i + 1]);
+            pk[i] = pack_f16x2(pa, pb);
+          }
+          const int ch = (Cfg::kSplitP ? grp * 4 : 0) + col0 / 8 + k;
+          *reinterpret_cast<uint4*>(prow + swizzled_chunk<128>(row, ch)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
         fence_proxy_async_smem();
-        tc_fence_before();
-        mbar_arrive(&p_full[buf]);
+        mbar_arrive(&p_full[grp]);
       }
 
       // ---------------------------------------------------------- pair epilogue
-      const size_t slot_base = slot * NQ * (D + 2);
+      const size_t slot_base = (static_cast<size_t>(s.p) + blockIdx.x) * NQ * (D + 2);
       if (has_tiles) {
         {
-          float* lv = reinterpret_cast<float*>(lacc);
+          float* lv = lacc;
           if constexpr (NC == 24) {
             const float x = warp_sum_columns<16>(lv), x8 = warp_sum_columns<8>(lv + 16);
-            if (lane < 16) red[quarter * 64 + col0 + lane] = x;
-            if (lane < 8) red[quarter * 64 + col0 + 16 + lane] = x8;
+            if (lane < 16) redg[quarter * 64 + col0 + lane] = x;
+            if (lane < 8) redg[quarter * 64 + col0 + 16 + lane] = x8;
           } else {
             const float x = warp_sum_columns<NC>(lv);
-            if (lane < NC) red[quarter * 64 + col0 + lane] = x;
+            if (lane < NC) redg[quarter * 64 + col0 + lane] = x;
           }
         }
-        softmax_sync();
-        if (!mbar_wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, abort_flag)) set_abort();
+        soft_sync();
+        // the groups' accumulators in one unit: column c of group g counts 2^(m_g - m); a
+        // group without a tile has none
+        if (!mbar_wait_compact(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, abort_flag)) set_abort();
         tc_fence_after();
-        float o[NC];
-        tmem_ld_cols<NC>(tmem_o + lane_addr + col0, reinterpret_cast<uint32_t*>(o));
-        tmem_wait_ld();
-        const float back = vref / kPScale;
+        const bool one = it - it0 == 1;
+        const bool has0 = !one || (it0 & 1) == 0, has1 = !one || (it0 & 1) == 1;
+        const int part = ts >> 7;         // 16 warps: four quarters of NE columns each
+        constexpr int NE = NQ / 4;
+        const uint32_t oa = tmem_o + lane_addr + part * NE;
+        const uint32_t nans = row < D ? nan_rows[row] : 0u;
+        // (rolled: run once a segment, its code should not push the tile loop's out of the
+        // instruction caches)
+#pragma unroll 1
+        for (int c0 = 0; c0 < NE; c0 += 4) {
+          uint32_t ra[4], rb[4];
+          tmem_ld<4>(oa + c0, ra);
+          tmem_ld<4>(oa + NQ + c0, rb);
+          tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < NC; ++c) o[c] *= back;
-        tc_fence_before();
-        if (row < D) {
-          const int dim = row;
-          const uint32_t nans = nan_rows[dim];
-          if (nans != 0u) {
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-              if (nans & ((2u << ((col0 + c) >> qa.gshift)) - 1u)) o[c] = NAN;
-          }
-          if (direct) {
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              const int cc = col0 + c;
-              if (cc < a.NV) {
-                const float l = red[cc] + red[64 + cc] + red[128 + cc] + red[192 + cc];
-                const __nv_bfloat16 bv = __float2bfloat16_rn(l == 0.f ? 0.f : o[c] / l);
+          for (int c = 0; c < 4; ++c) {
+            const int cc = part * NE + c0 + c;
+            const float ma = m2s[cc], mb = m2s[64 + cc], m = fmaxf(ma, mb);
+            const float fa = ex2(ma - m), fb = ex2(mb - m);
+            float o = (has0 ? __uint_as_float(ra[c]) * fa : 0.f) +
+                      (has1 ? __uint_as_float(rb[c]) * fb : 0.f);
+            if (nans & ((2u << (cc >> qa.gshift)) - 1u)) o = NAN;
+            if (cc < a.NV && row < D) {
+              if (direct) {
+                const float l = (red[cc] + red[64 + cc] + red[128 + cc] + red[192 + cc]) * fa +
+                                (red[256 + cc] + red[320 + cc] + red[384 + cc] + red[448 + cc]) * fb;
+                const __nv_bfloat16 bv = __float2bfloat16_rn(l == 0.f ? 0.f : __fdividef(o, l));
                 a.out[((static_cast<size_t>(s.b) * a.R + (cc >> qa.gshift)) * a.Hq + s.g * G +
-                       (cc & (G - 1))) * D + dim] = *reinterpret_cast<const uint16_t*>(&bv);
+                       (cc & (G - 1))) * D + row] = *reinterpret_cast<const uint16_t*>(&bv);
+              } else {
+                a.ws[slot_base + 2 * NQ + static_cast<size_t>(cc) * D + row] = o;
               }
             }
-          } else {
-            float* to = a.ws + slot_base + 2 * NQ + static_cast<size_t>(col0) * D + dim;
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-              if (col0 + c < a.NV) to[c * D] = o[c];
           }
         }
+        tc_fence_before();
         if (!direct && ts < NQ) {
-          a.ws[slot_base + ts] = m2s[ts];
-          a.ws[slot_base + NQ + ts] = red[ts] + red[64 + ts] + red[128 + ts] + red[192 + ts];
+          const float ma = m2s[ts], mb = m2s[64 + ts], m = fmaxf(ma, mb);
+          a.ws[slot_base + ts] = m;
+          a.ws[slot_base + NQ + ts] = (red[ts] + red[64 + ts] + red[128 + ts] + red[192 + ts]) * ex2(ma - m) +
+                                      (red[256 + ts] + red[320 + ts] + red[384 + ts] + red[448 + ts]) * ex2(mb - m);
         }
-        softmax_sync();
+        soft_sync();
       } else {
         // no key of this pair in this CTA: an empty partial (or zeros when alone)
         if (direct) {
-          for (int idx = ts; idx < a.NV * D; idx += kSoftmaxThreads) {
+          for (int idx = ts; idx < a.NV * D; idx += kSoftThreads) {
             const int c = idx / D, dim = idx % D;
             const int t = c >> qa.gshift, hl = c & (G - 1);
             a.out[((static_cast<size_t>(s.b) * a.R + t) * a.Hq + s.g * G + hl) * D + dim] = 0;
@@ -891,7 +947,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
             a.ws[slot_base + ts] = kNoMax;
             a.ws[slot_base + NQ + ts] = 0.f;
           }
-          for (int idx = ts; idx < NQ * D; idx += kSoftmaxThreads) a.ws[slot_base + 2 * NQ + idx] = 0.f;
+          for (int idx = ts; idx < NQ * D; idx += kSoftThreads) a.ws[slot_base + 2 * NQ + idx] = 0.f;
         }
       }
     }
@@ -909,7 +965,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
 // thread = dimension, kU partials loaded per round; the blocks past them aggregate the
 // scores (see verify_attn.cuh, whose merge this follows; a NaN sum stays NaN here).
 template <int D, bool kAgg, int kU>
-__global__ void __launch_bounds__(D) verify_quant_merge_kernel(const QVParams qa, int NQ,
+__global__ void __launch_bounds__(D) verify_quant_merge_kernel(const QVParams qa, int NQ, int ctas,
                                                                int merge_pairs) {
   const VParams& a = qa.v;
   const int x = blockIdx.x;
@@ -923,7 +979,7 @@ __global__ void __launch_bounds__(D) verify_quant_merge_kernel(const QVParams qa
   const int p = x / a.NV;
   const int c = x - p * a.NV;
   const int2 span = __ldcg(qa.spans + p);
-  if (span.x == span.y) return;
+  if (span.x < 0 || span.y >= ctas || span.x >= span.y) return;  // one CTA wrote the output
   const int n = span.y - span.x + 1;
   const size_t stride = static_cast<size_t>(NQ) * (D + 2);
   const float* base = a.ws + (static_cast<size_t>(p) + span.x) * stride;
@@ -989,10 +1045,10 @@ cudaError_t launch_quant(const VerifyArgs& va, const VerifyPlan& plan, const QVP
   cfg.dynamicSmemBytes = 0;
   const bool few = plan.max_chunks <= 8;  // partials per pair: one round of 8 loads
   if (agg > 0)
-    return few ? cudaLaunchKernelEx(&cfg, verify_quant_merge_kernel<D, true, 8>, p, NQ, merge_pairs)
-               : cudaLaunchKernelEx(&cfg, verify_quant_merge_kernel<D, true, 32>, p, NQ, merge_pairs);
-  return few ? cudaLaunchKernelEx(&cfg, verify_quant_merge_kernel<D, false, 8>, p, NQ, merge_pairs)
-             : cudaLaunchKernelEx(&cfg, verify_quant_merge_kernel<D, false, 32>, p, NQ, merge_pairs);
+    return few ? cudaLaunchKernelEx(&cfg, verify_quant_merge_kernel<D, true, 8>, p, NQ, plan.ctas, merge_pairs)
+               : cudaLaunchKernelEx(&cfg, verify_quant_merge_kernel<D, true, 32>, p, NQ, plan.ctas, merge_pairs);
+  return few ? cudaLaunchKernelEx(&cfg, verify_quant_merge_kernel<D, false, 8>, p, NQ, plan.ctas, merge_pairs)
+             : cudaLaunchKernelEx(&cfg, verify_quant_merge_kernel<D, false, 32>, p, NQ, plan.ctas, merge_pairs);
 }
 
 template <int D>
