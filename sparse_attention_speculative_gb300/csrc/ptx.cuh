@@ -106,6 +106,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
 // between tries.
 __device__ __forceinline__ bool mbar_wait_compact(uint64_t* bar, uint32_t parity,
                                                   const volatile int* abort) {
+  if (mbar_test(bar, parity)) return true;
   const uint32_t addr = smem_u32(bar);
   uint64_t t0 = 0;
   for (;;) {

@@ -19,15 +19,15 @@
 //   O^T[d x NQ]         += V^T[d x 128 keys] * P^T     (f16, MN-major A and B)
 // Rows of d bytes are one swizzle span (128-byte for d = 128, 64-byte for d = 64), so a
 // page and head is one TMA box of 16 rows.
-//   * warps 0 and 2 copy the K and V tiles; warp 1 issues the products; warp 3 runs ahead
-//     through the block table and brings the pages' scales into shared memory, 32 pages
+//   * warp 0 copies the K and V tiles; warps 1 and 2 issue the products; warp 3 runs
+//     ahead through the block table and brings the pages' scales into shared memory, 32 pages
 //     (4 tiles) a round, up to 4 rounds ahead (loaded by the softmax threads one tile
 //     ahead, a tile took the latency of a load from HBM).
 //   * warps 4-7 widen the V tile to f16 (exact), one key per thread, into two buffers, and
-//     clear what no row may see; they also write the collected logits (in the softmax
-//     warps these took 700 of 2600 cycles a tile, in a chain that nothing overlapped).
+//     clear what no row may see.
 //   * warps 8-15 and 16-23 are two softmax groups on alternate tiles, each with its own
-//     references, P^T buffer and accumulator O^T; they meet at the end of a pair.  A tile is a chain of some 2000 cycles (wait, TMEM load,
+//     references, P^T buffer and accumulator O^T; they meet at the end of a pair.  They
+//     also write the collected logits, each half of a group's threads one row.  A tile is a chain of some 2000 cycles (wait, TMEM load,
 //     vote, exponentials, store) against 1400 for its bytes from HBM: one group of eight
 //     warps was bound by that chain (368 us for the batch of 16 x 32K, 72B geometry),
 //     two overlap it.
@@ -61,7 +61,7 @@ using verify_detail::kTile;
 using verify_detail::VParams;
 
 constexpr float kNoMax = -3e38f;      // a reference before the first key (finite: no NaN arises)
-constexpr int kVProdWarp = 2;         // warp 0: K tiles, 1: products, 2: V tiles, 3: scales
+constexpr int kPvWarp = 2;            // warp 0: K and V tiles, 1: QK products, 2: PV products, 3: scales
 constexpr int kScaleWarp = 3;
 constexpr int kWidenWarp = 4;         // warps 4-7
 constexpr int kSoftWarp = 8;          // warps 8-15 and 16-23
@@ -225,7 +225,7 @@ struct QCfg {
   static constexpr int kOffQ = kOffWide + 2 * kWideBytes;
   static constexpr int kOffP = kOffQ + kQBytes;
   static constexpr int kOffMisc = kOffP + kPBytes;
-  static constexpr int kMiscBytes = 9216;
+  static constexpr int kMiscBytes = 10240;
   // d = 64: the PV product reads 16 KB past a widened tile (rows of the accumulator that
   // are never used); the Q, P and misc areas behind the last one cover that
   static constexpr int kSmemBytes =
@@ -263,10 +263,11 @@ __global__ void __launch_bounds__(kQThreads, 1)
   uint64_t* sc_full = pv_done + 2;  // [kRounds] scales of a round ready
   uint64_t* sc_empty = sc_full + kRounds;
   uint64_t* q_ready = sc_empty + kRounds;
-  uint64_t* mma_fin = q_ready + 1;
+  uint64_t* mma_fin = q_ready + 1;    // every QK product complete
+  uint64_t* pv_fin = mma_fin + 1;     // every PV product complete
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 448);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 452);
-  static_assert((4 * ST + 6 + 2 * kRounds + 2) * 8 <= 448, "barriers");
+  static_assert((4 * ST + 6 + 2 * kRounds + 3) * 8 <= 448, "barriers");
   float* quni_s = reinterpret_cast<float*>(misc + 456);        // 1 / query scale of all rows, or 0
   float* m2s = reinterpret_cast<float*>(misc + 512);           // [2][64] references
   float* alphas = m2s + 128;                                   // [2][64] rescale factors
@@ -274,19 +275,18 @@ __global__ void __launch_bounds__(kQThreads, 1)
   float* red = qinv + 64;                                      // [2][4][64] reductions
   uint32_t* qmax = reinterpret_cast<uint32_t*>(red + 512);     // [64] largest |q| of a row, as bf16 bits
   uint32_t* nan_rows = qmax + 64;                              // [D] verify-block rows with a NaN
-  // [kRounds][3][32] per page: key scale (below 0: no such page), log2 and inverse of the
-  // value scale
-  float* sc_s = reinterpret_cast<float*>(nan_rows + 128);
+  // [kRounds][3][32] per page: key scale, log2 and inverse of the value scale
+  float* xsum = reinterpret_cast<float*>(nan_rows + 128);      // [2][kTile] a row's group sums
+  float* sc_s = xsum + 2 * kTile;
   int* cum_s = reinterpret_cast<int*>(sc_s + kRounds * 96);    // first tile of each sequence
   int* plen_s = cum_s + kTableSeqs + 1;
-  static_assert(512 + (128 * 2 + 64 + 512 + 64 + 128 + kRounds * 96 + 2 * kTableSeqs + 1) * 4 <=
+  static_assert(512 + (128 * 2 + 64 + 512 + 64 + 128 + 2 * kTile + kRounds * 96 + 2 * kTableSeqs + 1) * 4 <=
                     Cfg::kMiscBytes,
                 "misc area");
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  const bool collect_any = a.logits != nullptr || a.partial != nullptr;
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) {
       mbar_init(&k_full[s], 1);
@@ -301,10 +301,11 @@ __global__ void __launch_bounds__(kQThreads, 1)
     }
     for (int i = 0; i < kRounds; ++i) {
       mbar_init(&sc_full[i], 1);
-      mbar_init(&sc_empty[i], kSoftThreads + (collect_any ? kWidenThreads : 0));
+      mbar_init(&sc_empty[i], 2);  // one thread of each softmax group
     }
     mbar_init(q_ready, kSoftThreads);
     mbar_init(mma_fin, 1);
+    mbar_init(pv_fin, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -358,105 +359,83 @@ __global__ void __launch_bounds__(kQThreads, 1)
     }
   };
 
-  if (warp == 0 || warp == kVProdWarp) {
-    // ------------------------------------------------------------ TMA producers
-    const bool is_k = warp == 0;
-    const CUtensorMap* map = is_k ? &kmap : &vmap;
-    uint8_t* ring = is_k ? k_ring : v_ring;
-    uint64_t* full = is_k ? k_full : v_full;
-    uint64_t* empty = is_k ? k_empty : v_empty;
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    // lanes 0-7 copy the pages of a K tile, lanes 8-15 those of the V tile
+    const bool is_v = lane >= kPagesPerTile;
+    const CUtensorMap* map = is_v ? &vmap : &kmap;
+    uint8_t* const dst = (is_v ? v_ring : k_ring) + (lane & 7) * (kPage * D);
+    uint64_t* const full = is_v ? v_full : k_full;
+    uint64_t* const empty = is_v ? v_empty : k_empty;
+    const bool leads = (lane & 7) == 0 && lane < 16;  // one lane of each ring waits and counts
     const uint64_t pol = l2_policy_evict_first();
-    if (lane == 0) tma_prefetch_desc(map);
-    uint32_t it = 0, issued = 0;
+    if (leads) tma_prefetch_desc(map);
+    uint32_t it = 0;
     for (Walk w = walk_of(); !w.done();) {
       // block-table entries: 4 tiles (32 pages, one per lane) per load round, two rounds ahead
       const Seg s = w.next();
       const int32_t* bt_row = a.block_table + static_cast<size_t>(s.b) * a.max_blocks;
       auto raw_entry = [&](int tile_base) {
-        const int lp = (tile_base + (lane >> 3)) * kPagesPerTile + (lane & 7);
+        const int lp = tile_base * kPagesPerTile + lane;
         return lp < a.max_blocks ? __ldcg(bt_row + lp) : a.num_blocks;
       };
       int ent_cur = raw_entry(s.t_begin);
       int ent_nxt = raw_entry(s.t_begin + 4);
-      if (is_k && s.bad_len && lane == 0) flag_status(a.status, VSD_DEV_BAD_LENGTH);
+      if (s.bad_len && lane == 0) flag_status(a.status, VSD_DEV_BAD_LENGTH);
       for (int tile = s.t_begin; tile < s.t_end; ++tile, ++it) {
         const int k4 = (tile - s.t_begin) & 3;
         if (k4 == 0 && tile != s.t_begin) {
           ent_cur = ent_nxt;
           ent_nxt = raw_entry(tile + 4);
         }
-        // block of page `lane` (lanes 0-7) of this tile; outside the sequence or invalid:
-        // an out-of-range block, which the copy fills with zeros
+        // block of page (lane & 7) of this tile; outside the sequence or invalid: an
+        // out-of-range block, which the copy fills with zeros
         const int e = __shfl_sync(0xffffffffu, ent_cur, k4 * 8 + (lane & 7));
-        const int lp = tile * kPagesPerTile + (lane & 7);
-        const bool inside = lane < kPagesPerTile && lp * kPage < s.L;
+        const bool inside = (tile * kPagesPerTile + (lane & 7)) * kPage < s.L;
         const bool bad = inside && (e < 0 || e >= a.num_blocks);
         const int blk = (inside && !bad) ? e : a.num_blocks;
         const int stage = it % ST;
-        const uint32_t use = it / ST;
-        int ok = 1;
-        if (lane == 0 && use > 0) ok = mbar_wait_compact(&empty[stage], (use - 1) & 1, abort_flag);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok && lane == 0) set_abort();
-        if (*abort_flag) continue;
-        const unsigned badbits = __ballot_sync(0xffffffffu, bad);
-        if (lane == 0) {
-          if (is_k && badbits) flag_status(a.status, VSD_DEV_BAD_BLOCK);
-          mbar_arrive_expect_tx(&full[stage], Cfg::kTileBytes);
-        }
+        bool ok = true;
+        if (leads && it >= ST) ok = mbar_wait_compact(&empty[stage], (it / ST - 1) & 1, abort_flag);
+        if (!ok) set_abort();
+        ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+        if (!ok) break;
+        if (bad && lane < kPagesPerTile) flag_status(a.status, VSD_DEV_BAD_BLOCK);
+        if (leads) mbar_arrive_expect_tx(&full[stage], Cfg::kTileBytes);
         __syncwarp();
-        if (lane < kPagesPerTile)
-          tma_load_4d(ring + stage * Cfg::kTileBytes + lane * (kPage * D), map, &full[stage], 0, 0,
-                      s.g, blk, pol);
-        issued = it + 1;
+        if (lane < 2 * kPagesPerTile)
+          tma_load_4d(dst + stage * Cfg::kTileBytes, map, &full[stage], 0, 0, s.g, blk, pol);
       }
+      if (*abort_flag) break;
     }
     // never leave a copy in flight: wait (with the drain limit) for the last stages
-    if (lane == 0) {
-      const uint32_t first = issued > static_cast<uint32_t>(ST) ? issued - ST : 0;
-      for (uint32_t i = first; i < issued; ++i) mbar_wait_drain(&full[i % ST], (i / ST) & 1);
+    if (leads) {
+      const uint32_t first = it > static_cast<uint32_t>(ST) ? it - ST : 0;
+      for (uint32_t i = first; i < it; ++i) mbar_wait_drain(&full[i % ST], (i / ST) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    // The whole warp runs the loop in uniform control flow and one elected lane issues:
-    // with a single lane in the loop every product's descriptors were moved to uniform
-    // registers one by one (75 cycles a product against 22).  The order is fixed: the QK
-    // product of tile i + 1 before the PV product of tile i, except across a segment's
-    // border, where the queries are rewritten only after the last PV product.  It spares
-    // waits of a hundred cycles each: P of tile i - 2 stored means that its S^T has been
-    // read, and S^T of tile i complete that PV of tile i - 2 is (a commit covers every
-    // product issued before it).
+    // ------------------------------------------------------------ QK products
+    // A whole warp runs the loop in uniform control flow and one elected lane issues: with a
+    // single lane in the loop every product's descriptors were moved to uniform registers
+    // one by one (75 cycles a product against 22).  QK and PV products have a warp each: one
+    // warp's waits and products for both took 1700 cycles a tile.
     constexpr uint32_t idesc_qk = idesc_e4m3_f32(128, 2 * NQ, 0, 0);
-    constexpr uint32_t idesc_pv = idesc_f16_f32(128, NQ, 1, 1);
     const uint64_t q_desc = sdesc_rows<D>(smem_u32(q_smem), 16, 8 * D);
     const uint64_t k_desc = sdesc_rows<D>(smem_u32(k_ring), 16, 8 * D);
-    const uint64_t p_desc = sdesc_sw128(smem_u32(p_smem), Cfg::kHalfBytes, 1024);
-    const uint64_t w_desc = sdesc_sw128(smem_u32(wide), Cfg::kHalfBytes, 1024);
     const uint32_t leader = elect_one();
-    uint32_t total = 0;
-    for (Walk w = walk_of(); !w.done();) {
-      const Seg s = w.next();
-      total += static_cast<uint32_t>(s.t_end - s.t_begin);
-    }
-    Walk qw = walk_of();
-    int q_begin = 0, q_end = 0, q_tile = 0;  // the segment of the next QK product
-    uint32_t nseg = 0, first_bits = 0;       // bit (i & 31): tile i is its group's first in the segment
-    uint32_t qi = 0, pi = 0;
+    uint32_t i = 0, nseg = 0;
     bool ok = true;
-    while (pi < total && ok) {
-      if (qi < total && q_tile >= q_end) {
-        do {
-          const Seg s = qw.next();
-          q_tile = q_begin = s.t_begin;
-          q_end = s.t_end;
-        } while (q_tile >= q_end);
-      }
-      const bool first = q_tile == q_begin;
-      if (qi < total && (first ? pi == qi : qi < pi + 2)) {
-        const uint32_t stage = qi % ST, buf = qi & 1;
-        if (first) ok = mbar_wait_compact(q_ready, nseg & 1, abort_flag);
-        ok = ok && mbar_wait_compact(&k_full[stage], (qi / ST) & 1, abort_flag);
+    for (Walk w = walk_of(); !w.done() && ok;) {
+      const Seg s = w.next();
+      if (s.t_begin >= s.t_end) continue;
+      ok = mbar_wait_compact(q_ready, nseg & 1, abort_flag);  // (the last segment's products are done)
+      ++nseg;
+      for (int tile = s.t_begin; tile < s.t_end; ++tile, ++i) {
+        const uint32_t stage = i % ST, buf = i & 1;
+        ok = ok && mbar_wait_compact(&k_full[stage], (i / ST) & 1, abort_flag);
+        // S^T of tile i - 2 has been read: its P^T is stored
+        if (i >= 2) ok = ok && mbar_wait_compact(&p_full[buf], ((i - 2) >> 1) & 1, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -467,27 +446,6 @@ __global__ void __launch_bounds__(kQThreads, 1)
                      kk > 0 ? 1u : 0u);
         umma_commit_if(leader, &k_empty[stage]);
         umma_commit_if(leader, &s_full[buf]);
-        if (q_tile < q_begin + 2)
-          first_bits |= 1u << (qi & 31);
-        else
-          first_bits &= ~(1u << (qi & 31));
-        if (first) ++nseg;
-        ++q_tile;
-        ++qi;
-      } else {
-        const uint32_t buf = pi & 1;
-        ok = mbar_wait_compact(&p_full[buf], (pi >> 1) & 1, abort_flag);  // P^T and the widened V
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t keep = ((first_bits >> (pi & 31)) & 1u) ^ 1u;  // accumulate the first step too
-        const uint64_t ad = w_desc + buf * (Cfg::kWideBytes >> 4);
-        const uint64_t bd = p_desc + buf * ((Cfg::kSplitP ? 64 : kTile * 128) >> 4);
-#pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          umma_f16_if(leader, tmem_o + buf * NQ, ad + kk * 128, bd + kk * 128, idesc_pv, kk > 0 ? 1u : keep);
-        umma_commit_if(leader, &pv_done[buf]);
-        ++pi;
       }
     }
     if (!ok && lane == 0) set_abort();
@@ -496,6 +454,36 @@ __global__ void __launch_bounds__(kQThreads, 1)
     __syncwarp();
     umma_commit_if(leader, mma_fin);
     mbar_wait_drain(mma_fin, 0);
+    __syncwarp();
+  } else if (warp == kPvWarp) {
+    // ------------------------------------------------------------ PV products
+    constexpr uint32_t idesc_pv = idesc_f16_f32(128, NQ, 1, 1);
+    const uint64_t p_desc = sdesc_sw128(smem_u32(p_smem), Cfg::kHalfBytes, 1024);
+    const uint64_t w_desc = sdesc_sw128(smem_u32(wide), Cfg::kHalfBytes, 1024);
+    const uint32_t leader = elect_one();
+    uint32_t i = 0;
+    bool ok = true;
+    for (Walk w = walk_of(); !w.done() && ok;) {
+      const Seg s = w.next();
+      for (int tile = s.t_begin; tile < s.t_end; ++tile, ++i) {
+        const uint32_t buf = i & 1;
+        ok = mbar_wait_compact(&p_full[buf], (i >> 1) & 1, abort_flag);  // P^T and the widened V
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t keep = tile >= s.t_begin + 2 ? 1u : 0u;  // the group's first tile starts O^T
+        const uint64_t ad = w_desc + buf * (Cfg::kWideBytes >> 4);
+        const uint64_t bd = p_desc + buf * ((Cfg::kSplitP ? 64 : kTile * 128) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          umma_f16_if(leader, tmem_o + buf * NQ, ad + kk * 128, bd + kk * 128, idesc_pv, kk > 0 ? 1u : keep);
+        umma_commit_if(leader, &pv_done[buf]);
+      }
+    }
+    if (!ok && lane == 0) set_abort();
+    __syncwarp();
+    umma_commit_if(leader, pv_fin);
+    mbar_wait_drain(pv_fin, 0);
     __syncwarp();
   } else if (warp == kScaleWarp) {
     // ------------------------------------------------------------ scales of the pages
@@ -510,7 +498,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
         return tile < s.t_end && lp < (s.L + kPage - 1) / kPage ? __ldcg(bt_row + lp) : -1;
       };
       const auto scales_at = [&](int e) {
-        if (e < 0 || e >= a.num_blocks) return make_float2(-1.f, 1.f);
+        if (e < 0 || e >= a.num_blocks) return make_float2(0.f, -1.f);
         const size_t at = static_cast<size_t>(e) * a.Hkv + s.g;
         return make_float2(__ldcg(qa.k_scale + at), __ldcg(qa.v_scale + at));
       };
@@ -527,20 +515,19 @@ __global__ void __launch_bounds__(kQThreads, 1)
           ok = mbar_wait_compact(&sc_empty[slot], (round / kRounds - 1) & 1, abort_flag);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok && lane == 0) set_abort();
+        // (no such page: its keys, copied as zeros, get zero logits and x = 2^-inf)
         const float vs = fmaxf(now.y, kMinVScale);
         sc_s[slot * 96 + lane] = now.x;
-        sc_s[slot * 96 + 32 + lane] = lg2(vs);
+        sc_s[slot * 96 + 32 + lane] = now.y < 0.f ? -INFINITY : lg2(vs);
         sc_s[slot * 96 + 64 + lane] = 1.f / vs;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sc_full[slot]);
       }
     }
   } else if (warp < kSoftWarp) {
-    // ------------------------------------------------------------ V codes to f16, logits out
-    const int row = (warp & 3) * 32 + lane;  // key in tile (and TMEM lane)
-    const bool collect = collect_any;
-    const int G = 1 << qa.gshift;
-    uint32_t it = 0, nseg = 0, round = 0;
+    // ------------------------------------------------------------ V codes to f16
+    const int row = (warp & 3) * 32 + lane;  // key in tile
+    uint32_t it = 0, nseg = 0;
     for (Walk walk = walk_of(); !walk.done();) {
       const Seg s = walk.next();
       if (s.t_begin >= s.t_end) continue;
@@ -602,58 +589,6 @@ __global__ void __launch_bounds__(kQThreads, 1)
                            e4m3x2_to_f16x2(w[2 * i + 1] & 0xFFFFu), e4m3x2_to_f16x2(w[2 * i + 1] >> 16));
         }
         fence_proxy_async_smem();
-        if (collect) {
-          // Collect-2-Query: the two rows' logits of this thread's key and their group sum
-          // (a key of an invalid page has zero logits)
-          const int k4 = (tile - s.t_begin) & 3;
-          if (warp == kWidenWarp &&
-              !((k4 != 0 || mbar_wait_compact(&sc_full[round % kRounds], (round / kRounds) & 1, abort_flag)) &&
-                mbar_wait_compact(&s_full[it & 1], (it >> 1) & 1, abort_flag)))
-            set_abort();
-          widen_sync();
-          const float ks = sc_s[(round % kRounds) * 96 + k4 * kPagesPerTile + row / kPage];
-          if (k4 == 3 || tile + 1 == s.t_end) mbar_arrive(&sc_empty[round++ % kRounds]);
-          tc_fence_after();
-          const float quni = *quni_s;  // 0: every row has its own scale
-          const float zs = ks < 0.f ? 0.f : ks * a.scale * (quni == 0.f ? 1.f : quni);
-          const uint32_t s_base = tmem + (it & 1) * Cfg::kTmemS + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-          float csum = 0.f;
-          const auto group = [&](auto width) {  // kH heads at a time
-            constexpr int kH = decltype(width)::value;
-#pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
-              const int col = (c == 0 ? a.row0 : a.row1) << qa.gshift;
-              float* lg = a.logits + ((static_cast<size_t>(s.b) * 2 + c) * a.Hq + (s.g << qa.gshift)) * a.P_max + j;
-#pragma unroll 1
-              for (int h = 0; h < G; h += kH) {
-                uint32_t hi[kH], lo[kH];
-                tmem_ld<kH>(s_base + col + h, hi);
-                tmem_ld<kH>(s_base + NQ + col + h, lo);
-                tmem_wait_ld();
-                if (j < s.P) {
-#pragma unroll
-                  for (int i = 0; i < kH; ++i) {
-                    // (the keys of an invalid page were filled with zeros)
-                    float z = fmaf(__uint_as_float(lo[i]), kQLo, __uint_as_float(hi[i])) * zs;
-                    if (quni == 0.f) z *= qinv[col + h + i];
-                    if (a.logits != nullptr) __stcs(lg, z);
-                    lg += a.P_max;
-                    csum += z;
-                  }
-                }
-              }
-            }
-          };
-          if (qa.gshift >= 3)
-            group(std::integral_constant<int, 8>{});
-          else if (qa.gshift == 2)
-            group(std::integral_constant<int, 4>{});
-          else
-            group(std::integral_constant<int, 1>{});
-          if (j < s.P && a.partial != nullptr)
-            a.partial[(static_cast<size_t>(s.b) * a.Hkv + s.g) * a.P_max + j] = csum;
-          tc_fence_before();
-        }
         mbar_arrive(&p_full[it & 1]);
       }
     }
@@ -674,6 +609,8 @@ __global__ void __launch_bounds__(kQThreads, 1)
     float* redg = red + grp * 256;
     const uint32_t s_base = tmem + grp * Cfg::kTmemS + lane_addr;
     const uint32_t o_base = tmem_o + grp * NQ + lane_addr + col0;
+    const bool collect = a.logits != nullptr || a.partial != nullptr;
+    const int ccol = (half == 0 ? a.row0 : a.row1) << qa.gshift;  // the half's collected row
     uint8_t* const prow = p_smem + (Cfg::kSplitP ? 0 : grp * kTile * 128);
     uint32_t it = 0, round = 0;
     for (Walk walk = walk_of(); !walk.done();) {
@@ -753,29 +690,31 @@ __global__ void __launch_bounds__(kQThreads, 1)
         soft_sync();  // qinv, m2s
       }
 
+      // where this thread's key 0 of the pair has its logits (head 0) and partial sum
+      const size_t lg_off = ((static_cast<size_t>(s.b) * 2 + half) * a.Hq + s.g * G) * a.P_max + row;
+      const size_t part_off = (static_cast<size_t>(s.b) * a.Hkv + s.g) * a.P_max + row;
       const float zq = a.scale * kLog2e * (quni == 0.f ? 1.f : quni);
-      for (int tile = s.t_begin; tile < s.t_end; ++tile, ++it) {
-        const int k4 = (tile - s.t_begin) & 3;
-        const bool mine = static_cast<int>(it & 1) == grp;  // else the other group's tile
-        if (mine) {
-          // (a test build waits for a barrier that nothing completes yet)
-          if (sw == 0 &&
-              !(mbar_wait_compact(&sc_full[round % kRounds], (round / kRounds) & 1, abort_flag) &&
-                (VSD_STALL(it == 0) ? mbar_wait_compact(mma_fin, 0, abort_flag)
-                                    : mbar_wait_compact(&s_full[grp], (it >> 1) & 1, abort_flag))))
-            set_abort();
-          group_sync(grp);
-        }
-        const float* sc = sc_s + (round % kRounds) * 96 + k4 * kPagesPerTile + row / kPage;
-        const float ks = sc[0], lvs = sc[32], ivs = sc[64];
-        if (k4 == 3 || tile + 1 == s.t_end) mbar_arrive(&sc_empty[round++ % kRounds]);
-        if (!mine) continue;
-        const int j = tile * kTile + row;
-        const bool bad = ks < 0.f;  // no such page (past the end too)
-        const float zl = ks * zq;
+      const int n = s.t_end - s.t_begin;
+      const int k0 = (it0 & 1) == static_cast<uint32_t>(grp) ? 0 : 1;  // this group's first tile
+      for (int k = k0; k < n; k += 2) {
+        const int tile = s.t_begin + k;
+        const uint32_t ik = it0 + k;
+        const uint32_t slot = (round + (k >> 2)) % kRounds;
+        // a warp each for the scales, S^T and the PV product that last read the P^T buffer
+        // (a test build waits for a barrier that nothing completes yet)
+        bool ok = true;
+        if (sw == 0)
+          ok = VSD_STALL(ik == 0) ? mbar_wait_compact(mma_fin, 0, abort_flag)
+                                  : mbar_wait_compact(&s_full[grp], (ik >> 1) & 1, abort_flag);
+        else if (sw == 1)
+          ok = mbar_wait_compact(&sc_full[slot], ((round + (k >> 2)) / kRounds) & 1, abort_flag);
+        else if (sw == 2 && ik >= 2)
+          ok = mbar_wait_compact(&pv_done[grp], ((ik - 2) >> 1) & 1, abort_flag);
+        if (!ok) set_abort();
+        group_sync(grp);
+        const float* sc = sc_s + slot * 96 + (k & 3) * kPagesPerTile + row / kPage;
+        const float zl = sc[0] * zq, lvs = sc[32], ivs = sc[64];
         tc_fence_after();
-        // first visible column of this key
-        const int c_lo = j < s.P && !bad ? 0 : (j < s.L && !bad ? (j - s.P) << qa.gshift : NQ);
         float y[NC];  // z log2 e + log2 vs, then its distance to the references
         // From the two parts' logits of this thread's columns in TMEM; hidden ones are -inf.
         // Rounded before the reference is taken off: a reference formed from the same
@@ -796,7 +735,9 @@ __global__ void __launch_bounds__(kQThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[c0 + i] = __fmaf_rn(y[c0 + i], zl, lvs);
           }
-          if (c_lo > 0) {
+          if ((tile + 1) * kTile > s.P) {  // keys of the verify block, or past the end
+            const int j = tile * kTile + row;
+            const int c_lo = j < s.L ? (j - s.P) << qa.gshift : NQ;  // first column that sees it
 #pragma unroll
             for (int c = 0; c < NC; ++c)
               if (col0 + c < c_lo) y[c] = -INFINITY;
@@ -816,8 +757,48 @@ __global__ void __launch_bounds__(kQThreads, 1)
           return dmax;
         };
         load_logits();
+        // Collect-2-Query: the lower half of the group writes row0's logits of its keys, the
+        // upper half row1's; their sums over the group's heads meet in xsum across the vote
+        float csum = 0.f;
+        const bool counted = collect && tile * kTile + row < s.P;
+        if (collect) {
+          const float zs = sc[0] * a.scale * (quni == 0.f ? 1.f : quni);
+          float* lg = a.logits + lg_off + tile * kTile;
+          const auto heads = [&](auto width) {  // kH heads at a time
+            constexpr int kH = decltype(width)::value;
+#pragma unroll 1
+            for (int h = 0; h < G; h += kH) {
+              float hi[kH], lo[kH];
+              tmem_ld<kH>(s_base + ccol + h, reinterpret_cast<uint32_t*>(hi));
+              tmem_ld<kH>(s_base + NQ + ccol + h, reinterpret_cast<uint32_t*>(lo));
+              tmem_wait_ld();
+              if (counted) {
+#pragma unroll
+                for (int i = 0; i < kH; ++i) {
+                  float z = fmaf(lo[i], kQLo, hi[i]) * zs;
+                  if (quni == 0.f) z *= qinv[ccol + h + i];
+                  if (a.logits != nullptr) __stcs(lg, z);
+                  lg += a.P_max;
+                  csum += z;
+                }
+              }
+            }
+          };
+          if (qa.gshift >= 3)
+            heads(std::integral_constant<int, 8>{});
+          else if (qa.gshift == 2)
+            heads(std::integral_constant<int, 4>{});
+          else
+            heads(std::integral_constant<int, 1>{});
+          if (half == 1) xsum[grp * kTile + row] = csum;
+        }
         const float dmax = take_references_off();
-        if (group_vote(grp, dmax > kTopX)) {
+        const bool raise = group_vote(grp, dmax > kTopX);
+        if (counted && half == 0 && a.partial != nullptr)
+          a.partial[part_off + tile * kTile] = csum + xsum[grp * kTile + row];
+        // every thread has read its scales: the round's last tile of this group gives them back
+        if (tg == 0 && (((k + 2) >> 2) != (k >> 2) || k + 2 >= n)) mbar_arrive(&sc_empty[slot]);
+        if (raise) {
           load_logits();  // (S^T stays until this tile's P^T is stored)
 #pragma unroll
           for (int c = 0; c < NC; c += 2) {
@@ -834,7 +815,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
           }
           group_sync(grp);
           if (started) {
-            // O^T holds earlier tiles (their products are done: see the issuer)
+            // O^T holds earlier tiles (their products are done)
 #pragma unroll
             for (int c0 = 0; c0 < NC; c0 += 8) {
               float r[8];
@@ -854,7 +835,6 @@ __global__ void __launch_bounds__(kQThreads, 1)
         }
         started = true;
         tc_fence_before();
-        // (the PV product that last read this P^T buffer is done: see the issuer)
 #pragma unroll
         for (int k = 0; k < NC / 8; ++k) {
           uint32_t pk[4];
@@ -871,6 +851,10 @@ __global__ void __launch_bounds__(kQThreads, 1)
         fence_proxy_async_smem();
         mbar_arrive(&p_full[grp]);
       }
+      // (a last round of one tile, the other group's)
+      if (tg == 0 && (n & 3) == 1 && ((n - 1 - k0) & 1)) mbar_arrive(&sc_empty[(round + (n >> 2)) % kRounds]);
+      it = it0 + n;
+      round += (n + 3) >> 2;
 
       // ---------------------------------------------------------- pair epilogue
       const size_t slot_base = (static_cast<size_t>(s.p) + blockIdx.x) * NQ * (D + 2);
