@@ -113,8 +113,14 @@ __device__ __forceinline__ SeqLen seq_len(const VParams& a, int P) {
   return s;
 }
 
-// The list of W tiles in C nearly equal ranges: the first `more` CTAs have per + 1 tiles, the
-// others per.  (No more CTAs than tiles, so that the CTAs that share a pair are consecutive
+// Every pair stands in the list with kStartTiles units before its tiles: what a CTA spends on
+// its start and end (queries, first references, the partial result) in tiles, so that a
+// range with many short pairs has fewer tiles (a batch of unequal sequences: the slowest
+// CTA took 31 us where the mean was 19.5).
+constexpr int kStartTiles = 3;
+
+// The list of W units in C nearly equal ranges: the first `more` CTAs have per + 1 tiles, the
+// others per.  (No more CTAs than units, so that the CTAs that share a pair are consecutive
 // and each holds a part of it.)  The host keeps W below 2^31.
 struct Ranges {
   int W, C, per, more;
@@ -139,7 +145,7 @@ __device__ __forceinline__ Ranges make_ranges(int W) {
 struct Seg {
   int p, b, g, P, L;
   int t_begin, t_end;  // tiles of the pair (none for a bad length)
-  bool first, last;    // the pair begins / ends in this CTA
+  bool first, last;    // the pair's tiles begin / end in this CTA
   int end;             // the pair's end in the list
   bool bad_len;
 };
@@ -155,9 +161,9 @@ struct Walk {
     v = r.first(c);
     v1 = c < r.C ? r.first(c + 1) : v;
     b = g = base = 0;
-    if (done()) return;
+    if (v >= v1) return;
     if (plen != nullptr) {
-      // the last sequence whose first tile (times the heads) is not behind v
+      // the last sequence whose first unit (times the heads) is not behind v
       int lo = 0, hi = a.B - 1;
 #pragma unroll 1
       while (lo < hi) {
@@ -168,46 +174,50 @@ struct Walk {
           hi = mid - 1;
       }
       b = lo;
-      const int T = seq_len(a, plen[b]).tiles;
+      const int T = seq_len(a, plen[b]).tiles + kStartTiles;
       g = (v - cum[b]) / T;
       base = cum[b] + g * T;
     } else {
-      const int p = v / a.t_max;
+      const int T = a.t_max + kStartTiles;
+      const int p = v / T;
       b = p / a.Hkv;
       g = p - b * a.Hkv;
-      base = p * a.t_max;
+      base = p * T;
     }
   }
 
-  __device__ __forceinline__ bool done() const { return v >= v1; }
-
-  __device__ __forceinline__ Seg next() {
-    const SeqLen n = seq_len(a, plen != nullptr ? plen[b] : __ldcg(a.prefix_len + b));
-    const int T = plen != nullptr ? n.tiles : a.t_max;  // tiles of the pair in the list
-    Seg s;
-    s.p = b * a.Hkv + g;
-    s.b = b;
-    s.g = g;
-    s.P = n.P;
-    s.L = n.L;
-    s.bad_len = n.bad;
-    s.end = base + T;
-    const int e = v1 < s.end ? v1 : s.end;
-    const int real = n.bad ? 0 : n.tiles;
-    s.t_begin = v - base;
-    s.t_end = e - base < real ? e - base : real;
-    if (s.t_end < s.t_begin) s.t_end = s.t_begin;
-    s.first = s.t_begin == 0;
-    s.last = e == s.end;
-    v = e;
-    if (s.last) {
-      base = s.end;
-      if (++g == a.Hkv) {
-        g = 0;
-        ++b;
+  // The next part that holds tiles of a pair; false at the end of the range.
+  __device__ __forceinline__ bool next(Seg& s) {
+    while (v < v1) {
+      const SeqLen n = seq_len(a, plen != nullptr ? plen[b] : __ldcg(a.prefix_len + b));
+      const int T = plen != nullptr ? n.tiles : a.t_max;  // tiles of the pair in the list
+      const int start = base + kStartTiles;
+      s.p = b * a.Hkv + g;
+      s.b = b;
+      s.g = g;
+      s.P = n.P;
+      s.L = n.L;
+      s.bad_len = n.bad;
+      s.end = start + T;
+      const int from = v > start ? v : start;
+      const int to = v1 < s.end ? v1 : s.end;
+      const int real = n.bad ? 0 : n.tiles;
+      s.t_begin = from - start;
+      s.t_end = to - start < real ? to - start : real;
+      if (s.t_end < s.t_begin) s.t_end = s.t_begin;
+      s.first = s.t_begin == 0;
+      s.last = to == s.end;
+      v = to > v ? to : v1;  // (a range that ends in the units before the tiles)
+      if (s.last) {
+        base = s.end;
+        if (++g == a.Hkv) {
+          g = 0;
+          ++b;
+        }
       }
+      if (to > from) return true;
     }
-    return s;
+    return false;
   }
 };
 
@@ -331,7 +341,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       const int b = b0 + lane;
       const int P = b < a.B ? __ldcg(a.prefix_len + b) : 0;
-      const int T = b < a.B ? seq_len(a, P).tiles * a.Hkv : 0;
+      const int T = b < a.B ? (seq_len(a, P).tiles + kStartTiles) * a.Hkv : 0;
       int x = T;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -348,7 +358,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
   }
   __syncthreads();
   const int* plen = table ? plen_s : nullptr;
-  const Ranges ranges = make_ranges(table ? cum_s[a.B] : a.pairs * a.t_max);
+  const Ranges ranges = make_ranges(table ? cum_s[a.B] : a.pairs * (a.t_max + kStartTiles));
   const auto walk_of = [&] { return Walk(a, plen, cum_s, ranges); };
   const uint32_t tmem_o = tmem + Cfg::kTmemO;
 
@@ -371,9 +381,9 @@ __global__ void __launch_bounds__(kQThreads, 1)
     const uint64_t pol = l2_policy_evict_first();
     if (leads) tma_prefetch_desc(map);
     uint32_t it = 0;
-    for (Walk w = walk_of(); !w.done();) {
+    Seg s;
+    for (Walk w = walk_of(); w.next(s);) {
       // block-table entries: 4 tiles (32 pages, one per lane) per load round, two rounds ahead
-      const Seg s = w.next();
       const int32_t* bt_row = a.block_table + static_cast<size_t>(s.b) * a.max_blocks;
       auto raw_entry = [&](int tile_base) {
         const int lp = tile_base * kPagesPerTile + lane;
@@ -426,8 +436,8 @@ __global__ void __launch_bounds__(kQThreads, 1)
     const uint32_t leader = elect_one();
     uint32_t i = 0, nseg = 0;
     bool ok = true;
-    for (Walk w = walk_of(); !w.done() && ok;) {
-      const Seg s = w.next();
+    Seg s;
+    for (Walk w = walk_of(); ok && w.next(s);) {
       if (s.t_begin >= s.t_end) continue;
       ok = mbar_wait_compact(q_ready, nseg & 1, abort_flag);  // (the last segment's products are done)
       ++nseg;
@@ -463,8 +473,8 @@ __global__ void __launch_bounds__(kQThreads, 1)
     const uint32_t leader = elect_one();
     uint32_t i = 0;
     bool ok = true;
-    for (Walk w = walk_of(); !w.done() && ok;) {
-      const Seg s = w.next();
+    Seg s;
+    for (Walk w = walk_of(); ok && w.next(s);) {
       for (int tile = s.t_begin; tile < s.t_end; ++tile, ++i) {
         const uint32_t buf = i & 1;
         ok = mbar_wait_compact(&p_full[buf], (i >> 1) & 1, abort_flag);  // P^T and the widened V
@@ -488,8 +498,8 @@ __global__ void __launch_bounds__(kQThreads, 1)
   } else if (warp == kScaleWarp) {
     // ------------------------------------------------------------ scales of the pages
     uint32_t round = 0;
-    for (Walk w = walk_of(); !w.done();) {
-      const Seg s = w.next();
+    Seg s;
+    for (Walk w = walk_of(); w.next(s);) {
       if (s.t_begin >= s.t_end) continue;
       const int32_t* bt_row = a.block_table + static_cast<size_t>(s.b) * a.max_blocks;
       // this lane's page of a round: its table entry (-1: past the sequence), its scales
@@ -528,8 +538,8 @@ __global__ void __launch_bounds__(kQThreads, 1)
     // ------------------------------------------------------------ V codes to f16
     const int row = (warp & 3) * 32 + lane;  // key in tile
     uint32_t it = 0, nseg = 0;
-    for (Walk walk = walk_of(); !walk.done();) {
-      const Seg s = walk.next();
+    Seg s;
+    for (Walk walk = walk_of(); walk.next(s);) {
       if (s.t_begin >= s.t_end) continue;
       const uint32_t seg_parity = nseg++ & 1;
       for (int tile = s.t_begin; tile < s.t_end; ++tile, ++it) {
@@ -613,8 +623,27 @@ __global__ void __launch_bounds__(kQThreads, 1)
     const int ccol = (half == 0 ? a.row0 : a.row1) << qa.gshift;  // the half's collected row
     uint8_t* const prow = p_smem + (Cfg::kSplitP ? 0 : grp * kTile * 128);
     uint32_t it = 0, round = 0;
-    for (Walk walk = walk_of(); !walk.done();) {
-      const Seg s = walk.next();
+    // queries of a (sequence, KV group): row r = t * G + hl, 8 dimensions of a row a thread;
+    // those of the next part are in flight during the end of the last one
+    constexpr int kCh = D / 8;
+    constexpr int kQL = (NQ * kCh + kSoftThreads - 1) / kSoftThreads;
+    uint4 qv[kQL];
+    const auto load_queries = [&](const Seg& s) {
+#pragma unroll
+      for (int u = 0; u < kQL; ++u) {
+        const int idx = ts + u * kSoftThreads;
+        const int r = idx / kCh, ch = idx % kCh;
+        qv[u] = make_uint4(0, 0, 0, 0);
+        if (r < a.NV)
+          qv[u] = ldg_stream16(a.q + ((static_cast<size_t>(s.b) * a.R + (r >> qa.gshift)) * a.Hq +
+                                      s.g * G + (r & (G - 1))) * D + ch * 8);
+      }
+    };
+    Walk walk = walk_of();
+    Seg s;
+    bool more = walk.next(s);
+    if (more) load_queries(s);
+    while (more) {
       const bool direct = s.first && s.last;  // the whole pair is in this CTA
       const bool has_tiles = s.t_begin < s.t_end;
       if (ts == 0 && qa.spans != nullptr && s.first)
@@ -628,19 +657,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
       float quni = 0.f;      // 1 / query scale of all rows, or 0
 
       if (has_tiles) {
-        // queries of this (sequence, KV group): row r = t * G + hl, in two parts
-        constexpr int kCh = D / 8;
-        constexpr int kQL = (NQ * kCh + kSoftThreads - 1) / kSoftThreads;
-        uint4 qv[kQL];
-#pragma unroll
-        for (int u = 0; u < kQL; ++u) {
-          const int idx = ts + u * kSoftThreads;
-          const int r = idx / kCh, ch = idx % kCh;
-          qv[u] = make_uint4(0, 0, 0, 0);
-          if (r < a.NV)
-            qv[u] = ldg_stream16(a.q + ((static_cast<size_t>(s.b) * a.R + (r >> qa.gshift)) * a.Hq +
-                                        s.g * G + (r & (G - 1))) * D + ch * 8);
-        }
+        // the queries in two parts
 #pragma unroll
         for (int u = 0; u < kQL; ++u) {
           const int idx = ts + u * kSoftThreads;
@@ -857,6 +874,9 @@ __global__ void __launch_bounds__(kQThreads, 1)
       round += (n + 3) >> 2;
 
       // ---------------------------------------------------------- pair epilogue
+      Seg after;
+      more = walk.next(after);
+      if (more) load_queries(after);
       const size_t slot_base = (static_cast<size_t>(s.p) + blockIdx.x) * NQ * (D + 2);
       if (has_tiles) {
         {
@@ -934,6 +954,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
           for (int idx = ts; idx < NQ * D; idx += kSoftThreads) a.ws[slot_base + 2 * NQ + idx] = 0.f;
         }
       }
+      s = after;
     }
   }
 

@@ -1081,7 +1081,9 @@ vsd_status vsd_verify_attn_collect_quant(const vsd_geom* geom, int R, const void
   if (st != VSD_OK) return st;
   const int G = geom->Hq / geom->Hkv;
   const vsd::VerifyPlan plan = vsd::plan_verify(geom->B, geom->Hkv, R, G, P_max, sms);
-  if (static_cast<long long>(plan.pairs) * plan.t_max > 0x7FFFFFFFll) return VSD_ERR_UNSUPPORTED;
+  // (the kernel counts the tiles of the call, and a few more of each pair, in 32 bits)
+  if (static_cast<long long>(plan.pairs) * (plan.t_max + 8ll) > 0x7FFFFFFFll)
+    return VSD_ERR_UNSUPPORTED;
   const size_t need = vsd::verify_quant_workspace_bytes(plan, geom->head_dim);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256)))
     return VSD_ERR_WORKSPACE;
