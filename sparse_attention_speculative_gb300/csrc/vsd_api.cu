@@ -1144,7 +1144,9 @@ vsd_status vsd_sparse_decode_attn_quant(const vsd_geom* geom, const void* q,
                                         size_t workspace_bytes, void* stream) {
   vsd_status st = check_geom(geom);
   if (st != VSD_OK) return st;
-  if (geom->Hq / geom->Hkv > 16 || geom->B > 65535) return VSD_ERR_UNSUPPORTED;
+  if (geom->Hq / geom->Hkv > 16 || geom->B > 65535 || geom->Hkv > 65535 ||
+      static_cast<long long>(geom->B) * geom->Hq > 0x7FFFFFFFll)
+    return VSD_ERR_UNSUPPORTED;
   // cache rows are 32-bit: block * Hkv * page_size + offset
   if (static_cast<long long>(geom->num_blocks) * geom->Hkv * geom->page_size > 0x7FFFFFFFll)
     return VSD_ERR_UNSUPPORTED;
