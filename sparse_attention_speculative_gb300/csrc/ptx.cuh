@@ -488,22 +488,24 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t smem_addr, uint32_t lbo
   return d;
 }
 
-// The same for rows of kRowBytes = 128 or 64 bytes (the swizzle spans one row; layout 2 =
-// 128-byte, 4 = 64-byte swizzle).  8-bit elements: a row holds kRowBytes of them, along K
-// (K-major) or along MN (MN-major), 8-row atoms of 8 * kRowBytes bytes at SBO.
+// The same for rows of kRowBytes = 128, 64 or 32 bytes (the swizzle spans one row; layout 2 =
+// 128-byte, 4 = 64-byte, 6 = 32-byte swizzle).  A row holds its elements along K (K-major) or
+// along MN (MN-major); 8-row atoms of 8 * kRowBytes bytes at SBO.
 template <int kRowBytes>
 __device__ __forceinline__ uint64_t sdesc_rows(uint32_t smem_addr, uint32_t lbo_bytes,
                                                uint32_t sbo_bytes) {
-  static_assert(kRowBytes == 128 || kRowBytes == 64, "swizzle span");
-  const uint64_t d = sdesc_sw128(smem_addr, lbo_bytes, sbo_bytes);
-  return kRowBytes == 128 ? d : (d & ~(7ull << 61)) | (4ull << 61);
+  static_assert(kRowBytes == 128 || kRowBytes == 64 || kRowBytes == 32, "swizzle span");
+  constexpr uint64_t layout = kRowBytes == 128 ? 2 : (kRowBytes == 64 ? 4 : 6);
+  return (sdesc_sw128(smem_addr, lbo_bytes, sbo_bytes) & ~(7ull << 61)) | (layout << 61);
 }
 
 // Byte offset of 16-byte chunk `ch` of row `r` under that swizzle (rows kRowBytes apart
 // from a 1024-byte boundary).
 template <int kRowBytes>
 __device__ __forceinline__ uint32_t swizzled_chunk(uint32_t r, uint32_t ch) {
-  return kRowBytes == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
+  return kRowBytes == 128  ? r * 128 + ((ch ^ (r & 7)) << 4)
+         : kRowBytes == 64 ? r * 64 + ((ch ^ ((r >> 1) & 3)) << 4)
+                           : r * 32 + ((ch ^ ((r >> 2) & 1)) << 4);
 }
 
 }  // namespace ptx

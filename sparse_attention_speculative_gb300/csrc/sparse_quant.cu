@@ -12,8 +12,9 @@
 //   * thread t resolves position t (index or tail -> block table -> page and row) and loads
 //     its page's two scales; the warps copy the rows (d bytes, 16 bytes a lane, whole rows
 //     per instruction) into the swizzled layouts with asynchronous copies, keys first;
-//   * one warp issues S^T[128 keys x 32] = K * [Qhi; Qlo]^T while every thread widens its
-//     value row; thread t then owns key t (TMEM lane t), the heads' maxima and sums meet in
+//   * one warp issues S^T[128 keys x 32] = K * [Qhi; Qlo]^T while every thread takes its
+//     value row into registers, to widen it into the place of the codes once the keys have
+//     been read; thread t then owns key t (TMEM lane t), the heads' maxima and sums meet in
 //     shared memory, and one warp issues O^T[d x 16] = V^T * P^T;
 //   * thread d writes dimension d of the heads' outputs, or of the split's (m, l, o), which
 //     a second kernel (a programmatic dependent, one block per output row) merges.
@@ -23,7 +24,7 @@
 //
 // A split is a chain of dependent latencies (lengths and indices, block table, rows, two
 // products, softmax: about 5 us at one sequence), so what counts is that all loads of a
-// step are in flight together and that three CTAs share an SM.
+// step are in flight together and that five CTAs share an SM (41 KB of shared memory each).
 #include <cfloat>
 
 #include "launch.h"
@@ -85,19 +86,21 @@ struct SqSlot {
 template <int D>
 struct SqSmem {
   static constexpr int kTileBytes = kKeys * D;
-  // d = 64: the PV product reads 16 KB past the widened tile (rows of the accumulator that
-  // are never used), which the tiles behind it cover
-  static constexpr int kOffWide = 0;
-  static constexpr int kOffP = kOffWide + 2 * kTileBytes;  // 128-byte rows
-  static constexpr int kOffK = kOffP;                      // P^T takes the key tile's place
-  static constexpr int kOffV = kOffK + (kTileBytes < kKeys * 128 ? kKeys * 128 : kTileBytes);
-  static constexpr int kOffQ = kOffV + kTileBytes;
+  // the widened values take the place of the key and value codes: every thread holds its
+  // value row in registers by then, and the keys have been read
+  static constexpr int kOffK = 0;
+  static constexpr int kOffV = kTileBytes;
+  static constexpr int kOffWide = 0;                       // d / 64 halves of 128-byte rows
+  static constexpr int kOffP = 2 * kTileBytes;             // 32-byte rows
+  static constexpr int kOffQ = kOffP + kKeys * 32;
   static constexpr int kOffRed = kOffQ + 2 * kSqNQ * D;    // [2][4][kSqNQ] floats
   static constexpr int kOffQinv = kOffRed + 2 * 4 * kSqNQ * 4;
   static constexpr int kOffBar = kOffQinv + kSqNQ * 4;
-  static constexpr int kBytes = kOffBar + 64;
+  static constexpr int kUsed = kOffBar + 64;
+  // d = 64: the PV product reads 16 KB past the widened tile (rows of the accumulator that
+  // are never used), inside this allocation
+  static constexpr int kBytes = kUsed > 2 * kKeys * 128 ? kUsed : 2 * kKeys * 128;
   static_assert(kOffQ % 1024 == 0 && 2 * kSqNQ * D % 1024 == 0, "swizzle atoms need 1 KB alignment");
-  static_assert(kBytes >= kOffWide + kKeys * 128 * 2, "the second half of M = 128 stays inside");
 };
 
 // Sums of G values over a warp; lane L gets column L % G (G a power of two up to 16).
@@ -125,7 +128,7 @@ __device__ __forceinline__ float sq_warp_sums(float (&v)[G]) {
 }
 
 template <int D, int G>
-__global__ void __launch_bounds__(kSqThreads) sparse_quant_kernel(const SqParams a) {
+__global__ void __launch_bounds__(kSqThreads, G == 16 ? 3 : 5) sparse_quant_kernel(const SqParams a) {
   using Sm = SqSmem<D>;
   constexpr int LPR = D / 16;       // 16-byte chunks of a row of codes
   constexpr int RPI = 32 / LPR;     // rows per warp instruction
@@ -279,13 +282,22 @@ __global__ void __launch_bounds__(kSqThreads) sparse_quant_kernel(const SqParams
           ptx::umma_f8_if(leader, tmem, ad + kk * 2, bd + kk * 2, idesc, kk > 0 ? 1u : 0u);
         ptx::umma_commit_if(leader, bar_s);
       }
-      // ---- meanwhile every thread widens its value row (absent rows are zeros)
+      // ---- meanwhile every thread takes its value row into registers (absent: zeros)
       ptx::cp_async_wait_all();
       __syncthreads();
+      uint4 vr[D / 16];
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+        vr[c] = *reinterpret_cast<const uint4*>(v_s + ptx::swizzled_chunk<D>(t, c));
+      // (d = 128: a thread widens into its own value row and the key tile; d = 64: into others')
+      if constexpr (D == 64) __syncthreads();
+      // (a test build waits on the end-of-kernel barrier here, which nothing completes yet)
+      const bool ok_s = ptx::mbar_wait(VSD_STALL(true) ? bar_fin : bar_s, products & 1);
+      ptx::tc_fence_after();
+      // ---- the value row as f16 in the place of the codes
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
-        const uint4 x = *reinterpret_cast<const uint4*>(v_s + ptx::swizzled_chunk<D>(t, c));
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        const uint32_t w[4] = {vr[c].x, vr[c].y, vr[c].z, vr[c].w};
         uint8_t* half = wide + (c >> 2) * (kKeys * 128);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -293,9 +305,6 @@ __global__ void __launch_bounds__(kSqThreads) sparse_quant_kernel(const SqParams
               make_uint4(e4m3x2_to_f16x2(w[2 * i] & 0xFFFFu), e4m3x2_to_f16x2(w[2 * i] >> 16),
                          e4m3x2_to_f16x2(w[2 * i + 1] & 0xFFFFu), e4m3x2_to_f16x2(w[2 * i + 1] >> 16));
       }
-      // (a test build waits on the end-of-kernel barrier here, which nothing completes yet)
-      const bool ok_s = ptx::mbar_wait(VSD_STALL(true) ? bar_fin : bar_s, products & 1);
-      ptx::tc_fence_after();
       // ---- softmax over the batch, per head: y = z log2 e + log2 vs
       float y[G];
       {
@@ -326,10 +335,10 @@ __global__ void __launch_bounds__(kSqThreads) sparse_quant_kernel(const SqParams
         m[h] = mn;
         x[h] = ex2(y[h] - mn);
       }
-      // row t of P^T (the key tile has been read: every thread waited for the product)
+      // row t of P^T: 16 halves, one 32-byte swizzle span
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        *reinterpret_cast<uint4*>(p_s + ptx::swizzled_chunk<128>(t, k)) =
+        *reinterpret_cast<uint4*>(p_s + ptx::swizzled_chunk<32>(t, k)) =
             make_uint4(pack_f16x2(x[8 * k], x[8 * k + 1]), pack_f16x2(x[8 * k + 2], x[8 * k + 3]),
                        pack_f16x2(x[8 * k + 4], x[8 * k + 5]), pack_f16x2(x[8 * k + 6], x[8 * k + 7]));
       ptx::fence_proxy_async_smem();
@@ -342,11 +351,11 @@ __global__ void __launch_bounds__(kSqThreads) sparse_quant_kernel(const SqParams
         ptx::tc_fence_after();
         constexpr uint32_t idesc = ptx::idesc_f16_f32(128, kSqNQ, 1, 1);
         const uint64_t ad = ptx::sdesc_sw128(ptx::smem_u32(wide), kKeys * 128, 1024);
-        const uint64_t bd = ptx::sdesc_sw128(ptx::smem_u32(p_s), kKeys * 128, 1024);
+        const uint64_t bd = ptx::sdesc_rows<32>(ptx::smem_u32(p_s), kKeys * 32, 256);
         const uint32_t leader = ptx::elect_one();
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
-          ptx::umma_f16_if(leader, tmem + 2 * kSqNQ, ad + kk * 128, bd + kk * 128, idesc, kk > 0 ? 1u : 0u);
+          ptx::umma_f16_if(leader, tmem + 2 * kSqNQ, ad + kk * 128, bd + kk * 32, idesc, kk > 0 ? 1u : 0u);
         ptx::umma_commit_if(leader, bar_o);
       }
       // ---- the heads' sums while the product runs
