@@ -6,7 +6,6 @@ missing the calls raise immediately; there is no fallback implementation.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import os
@@ -95,13 +94,13 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         lib.vsd_sparse_decode_attn_step.argtypes = [GP, P, P, P, P, P, P, P, P, I, P, P, I, P,
                                                     ctypes.c_uint, F, P, P, SZ, P]
         lib.vsd_advance_lengths.argtypes = [I, I, P, I, P, P, P, I, P, P]
-        lib.vsd_append_kv_quant.argtypes = [GP, I, P, P, P, P, I, P, P, P, P, P, P]
-        lib.vsd_read_kv_quant.argtypes = [GP, I, P, P, P, P, P, P, I, P, P, P, P]
-        lib.vsd_verify_quant_workspace_size.argtypes = [GP, I, I, ctypes.POINTER(SZ)]
-        lib.vsd_verify_attn_collect_quant.argtypes = [GP, I, P, P, P, P, P, P, P, I, I, I, F, P,
+        lib.vsd_append_kv_quant.argtypes = [P, I, P, P, P, P, I, P, P, P, P, P, P]
+        lib.vsd_read_kv_quant.argtypes = [P, I, P, P, P, P, P, P, I, P, P, P, P]
+        lib.vsd_verify_quant_workspace_size.argtypes = [P, I, I, ctypes.POINTER(SZ)]
+        lib.vsd_verify_attn_collect_quant.argtypes = [P, I, P, P, P, P, P, P, P, I, I, I, F, P,
                                                       P, P, P, I, I, P, P, SZ, P]
-        lib.vsd_sparse_quant_workspace_size.argtypes = [GP, I, I, ctypes.POINTER(SZ)]
-        lib.vsd_sparse_decode_attn_quant.argtypes = [GP, P, P, P, P, P, P, P, P, I, P, P, I, F, P,
+        lib.vsd_sparse_quant_workspace_size.argtypes = [P, I, I, ctypes.POINTER(SZ)]
+        lib.vsd_sparse_decode_attn_quant.argtypes = [P, P, P, P, P, P, P, P, P, I, P, P, I, F, P,
                                                      P, SZ, P]
         lib.vsd_block_topk.argtypes = [GP, I, P, P, P, I, I, F, P, P, P]
         lib.vsd_read_device_status.argtypes = [P, ctypes.POINTER(ctypes.c_uint)]
@@ -648,30 +647,42 @@ def vsd_sparse_decode_attn_step(q, k_cache, v_cache, block_table, idx, n_sel, ta
 
 
 # ------------------------------------------------------------------ 8-bit cache
-def _need_quant_cache(k_cache, v_cache, k_scale, v_scale, like) -> None:
-    """The caches of the 8-bit calls: float8_e4m3fn [num_blocks, Hkv, 16, d] and float32
-    scales [num_blocks, Hkv], on the device of `like`."""
-    for name, c, s in (("k", k_cache, k_scale), ("v", v_cache, v_scale)):
-        _need(c, torch.float8_e4m3fn, name + "_cache")
-        _need(s, torch.float32, name + "_scale")
-        if c.dim() != 4 or c.shape != k_cache.shape or s.shape != c.shape[:2]:
-            raise ValueError("%s_cache must be [num_blocks, Hkv, page, d] and %s_scale "
-                             "[num_blocks, Hkv]" % (name, name))
-        _same_device(c, like, name + "_cache")
-        _same_device(s, like, name + "_scale")
-
-
-def _same_device(t, like, name: str) -> None:
-    if t.get_device() != like.get_device():
-        raise ValueError("%s is on another device" % name)
-
-
-def _need_like(t, dtype, shape, like, name: str) -> None:
-    """A tensor of the given type and shape on the device of `like`."""
+def _refuse(t, dtype, shape, dev, name: str) -> None:
+    """Say what is wrong with a tensor that _take refused."""
     _need(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    _same_device(t, like, name)
+    raise ValueError("%s is on another device" % name)
+
+
+def _take(t, dtype, shape, dev, name: str) -> int:
+    """The address of a contiguous tensor of the given type and shape (None: any) on CUDA
+    device `dev`; one pass of cheap comparisons, these calls are made once per layer and
+    step."""
+    if t.dtype is not dtype or (shape is not None and t.shape != shape) or \
+            t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, dtype, shape, dev, name)
+    return t.data_ptr()
+
+
+def _take_quant_cache(k_cache, v_cache, k_scale, v_scale, dev):
+    """The caches of the 8-bit calls: float8_e4m3fn [num_blocks, Hkv, 16, d] and float32
+    scales [num_blocks, Hkv], on device `dev`.  Returns their shape and addresses."""
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [num_blocks, Hkv, 16, d]")
+    shape = k_cache.shape
+    return shape, _take(k_cache, torch.float8_e4m3fn, None, dev, "k_cache"), \
+        _take(v_cache, torch.float8_e4m3fn, shape, dev, "v_cache"), \
+        _take(k_scale, torch.float32, shape[:2], dev, "k_scale"), \
+        _take(v_scale, torch.float32, shape[:2], dev, "v_scale")
+
+
+def _cuda_index(t, dtype, name: str) -> int:
+    """The device of a call's first tensor."""
+    dev = t.get_device()
+    if dev < 0:
+        _need(t, dtype, name)
+    return dev
 
 
 def _on_device(fn):
@@ -687,28 +698,65 @@ def _on_device(fn):
     return call
 
 
-def _stream_context(stream):
+def _empty(stream, shape, dtype, dev, make=torch.empty):
     """What a call allocates (outputs, its scratch) comes from torch's allocator tied to
     the stream that the call runs on: calls on other streams, and captured graphs, get
     memory of their own, and it goes back in stream order."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    if stream is None:
+        return make(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=dev)
+
+
+def _raw_stream(stream, dev: int) -> int:
+    """The cudaStream_t of a call (torch's own accessor: a Stream object costs 3 us)."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+@functools.lru_cache(maxsize=256)
+def _quant_geom(B: int, Hq: int, Hkv: int, d: int, page: int, max_blocks: int, num_blocks: int):
+    """A geometry, kept for the next call of the same shape."""
+    return Geom(B, Hq, Hkv, d, page, max_blocks, num_blocks)
+
+
+@functools.lru_cache(maxsize=256)
+def _quant_workspace_bytes(dev: int, call: str, shape, x: int, y: int) -> int:
+    """Workspace of a call over a geometry (a number of its shape and the device's SMs)."""
+    out = ctypes.c_size_t(0)
+    _check(getattr(load(), call)(ctypes.addressof(_quant_geom(*shape)), x, y, ctypes.byref(out)),
+           call)
+    return int(out.value)
+
+
+def _workspace_of(workspace, nbytes: int, stream, dev: int):
+    """(the tensor that keeps it alive, address, bytes) of a call's scratch."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, None, 0
+        workspace = _empty(stream, nbytes, torch.uint8, dev)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the call's device")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _quant_rows(k_rows, v_rows, names, k_cache, v_cache, k_scale, v_scale, block_table, pos_base,
-                n_valid) -> Geom:
-    if k_rows.dim() != 4:
-        raise ValueError("%s must be [B, n, Hkv, d]" % names[0])
-    B = int(k_rows.shape[0])
-    _need(k_rows, torch.bfloat16, names[0])
-    _need_like(v_rows, torch.bfloat16, k_rows.shape, k_rows, names[1])
-    _need_quant_cache(k_cache, v_cache, k_scale, v_scale, k_rows)
-    if k_rows.shape[2:] != (k_cache.shape[1], k_cache.shape[3]):
-        raise ValueError("%s do not fit the cache's heads" % " and ".join(names))
-    _need_like(block_table, torch.int32, (B, block_table.shape[-1]), k_rows, "block_table")
-    _need_like(pos_base, torch.int32, (B,), k_rows, "pos_base")
-    if n_valid is not None:
-        _need_like(n_valid, torch.int32, (B,), k_rows, "n_valid")
-    return geom_for(B, int(k_cache.shape[1]), k_cache, block_table)
+                n_valid):
+    """Checks and addresses that storing and reading rows share."""
+    dev = _cuda_index(k_rows, torch.bfloat16, names[0])
+    shape, kc, vc, ks, vs = _take_quant_cache(k_cache, v_cache, k_scale, v_scale, dev)
+    rows = k_rows.shape
+    if len(rows) != 4 or rows[2] != shape[1] or rows[3] != shape[3]:
+        raise ValueError("%s must be [B, n, %d, %d]" % (names[0], shape[1], shape[3]))
+    B = rows[0]
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    width = block_table.shape[1]
+    geom = _quant_geom(B, shape[1], shape[1], shape[3], shape[2], width, shape[0])
+    return geom, _take(k_rows, torch.bfloat16, None, dev, names[0]), \
+        _take(v_rows, torch.bfloat16, rows, dev, names[1]), kc, vc, ks, vs, \
+        _take(block_table, torch.int32, (B, width), dev, "block_table"), \
+        _take(pos_base, torch.int32, (B,), dev, "pos_base"), \
+        None if n_valid is None else _take(n_valid, torch.int32, (B,), dev, "n_valid")
 
 
 @_on_device
@@ -719,12 +767,12 @@ def vsd_append_kv_quant(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_
     (float8_e4m3fn [num_blocks, Hkv, 16, d], scales float32 [num_blocks, Hkv]).  Rows are
     appended in order: a page whose slot 0 is written starts afresh, otherwise its earlier
     rows are kept (requantised when its scale has to grow)."""
-    geom = _quant_rows(k_new, v_new, ("k_new", "v_new"), k_cache, v_cache, k_scale, v_scale,
-                       block_table, pos_base, n_valid)
-    _check(load().vsd_append_kv_quant(
-        ctypes.byref(geom), int(k_new.shape[1]), _ptr(k_new), _ptr(v_new), _ptr(block_table),
-        _ptr(pos_base), int(pos_offset), _ptr(n_valid), _ptr(k_cache), _ptr(v_cache),
-        _ptr(k_scale), _ptr(v_scale), _stream(stream)), "vsd_append_kv_quant")
+    geom, kn, vn, kc, vc, ks, vs, bt, pos, nv = _quant_rows(
+        k_new, v_new, ("k_new", "v_new"), k_cache, v_cache, k_scale, v_scale, block_table, pos_base,
+        n_valid)
+    _check((_lib or load()).vsd_append_kv_quant(
+        ctypes.addressof(geom), k_new.shape[1], kn, vn, bt, pos, pos_offset, nv, kc, vc, ks, vs,
+        _raw_stream(stream, k_new.get_device())), "vsd_append_kv_quant")
 
 
 @_on_device
@@ -733,27 +781,26 @@ def vsd_read_kv_quant(k_cache, v_cache, k_scale, v_scale, block_table, pos_base,
     """The rows at positions pos_base[b] + pos_offset + t, t < n_valid[b] (None: n), of an
     8-bit cache as bf16 [B, n, Hkv, d].  Rows behind n_valid are left as they were in
     k_out, v_out (zeros when allocated here).  Returns (k_out, v_out)."""
-    shape = (int(pos_base.shape[0]), int(n), int(k_cache.shape[1]), int(k_cache.shape[3]))
-    make = torch.empty if n_valid is None else torch.zeros
-    with _stream_context(stream):
-        if k_out is None:
-            k_out = make(shape, dtype=torch.bfloat16, device=k_cache.device)
-        if v_out is None:
-            v_out = make(shape, dtype=torch.bfloat16, device=k_cache.device)
-    geom = _quant_rows(k_out, v_out, ("k_out", "v_out"), k_cache, v_cache, k_scale, v_scale,
-                       block_table, pos_base, n_valid)
+    shape = (pos_base.shape[0], int(n), k_cache.shape[1], k_cache.shape[-1])
+    if k_out is None or v_out is None:
+        make = torch.empty if n_valid is None else torch.zeros
+        dev = _cuda_index(k_cache, torch.float8_e4m3fn, "k_cache")
+        k_out = _empty(stream, shape, torch.bfloat16, dev, make) if k_out is None else k_out
+        v_out = _empty(stream, shape, torch.bfloat16, dev, make) if v_out is None else v_out
+    geom, ko, vo, kc, vc, ks, vs, bt, pos, nv = _quant_rows(
+        k_out, v_out, ("k_out", "v_out"), k_cache, v_cache, k_scale, v_scale, block_table, pos_base,
+        n_valid)
     if k_out.shape != shape:
         raise ValueError("k_out and v_out must be [B, n, Hkv, d]")
-    _check(load().vsd_read_kv_quant(
-        ctypes.byref(geom), int(n), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-        _ptr(block_table), _ptr(pos_base), int(pos_offset), _ptr(n_valid), _ptr(k_out),
-        _ptr(v_out), _stream(stream)), "vsd_read_kv_quant")
+    _check((_lib or load()).vsd_read_kv_quant(
+        ctypes.addressof(geom), shape[1], kc, vc, ks, vs, bt, pos, pos_offset, nv, ko, vo,
+        _raw_stream(stream, k_out.get_device())), "vsd_read_kv_quant")
     return k_out, v_out
 
 
 def vsd_verify_quant_workspace_size(geom: Geom, R: int, P_max: int) -> int:
     out = ctypes.c_size_t(0)
-    _check(load().vsd_verify_quant_workspace_size(ctypes.byref(geom), int(R), int(P_max),
+    _check(load().vsd_verify_quant_workspace_size(ctypes.addressof(geom), int(R), int(P_max),
                                                   ctypes.byref(out)),
            "vsd_verify_quant_workspace_size")
     return int(out.value)
@@ -762,47 +809,44 @@ def vsd_verify_quant_workspace_size(geom: Geom, R: int, P_max: int) -> int:
 def _verify_quant(q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, P_max, scale,
                   row0, row1, logits, partial, score, score_hist, n_sink, n_recent, out,
                   workspace, stream, collect, scored):
-    if q.dim() != 4:
-        raise ValueError("q must be [B, R, Hq, d]")
+    dev = _cuda_index(q, torch.bfloat16, "q")
+    shape, kc, vc, ks, vs = _take_quant_cache(k_cache, v_cache, k_scale, v_scale, dev)
+    if q.dim() != 4 or q.shape[3] != shape[3]:
+        raise ValueError("q must be [B, R, Hq, %d]" % shape[3])
     B, R, Hq, d = q.shape
-    P_max = int(P_max)
-    _need(q, torch.bfloat16, "q")
-    _need_quant_cache(k_cache, v_cache, k_scale, v_scale, q)
-    if d != k_cache.shape[3]:
-        raise ValueError("q and the caches have different head dimensions")
-    _need_like(block_table, torch.int32, (B, block_table.shape[-1]), q, "block_table")
-    _need_like(prefix_len, torch.int32, (B,), q, "prefix_len")
-    geom = geom_for(B, Hq, k_cache, block_table)
-    given = (("out", out, torch.bfloat16, (B, R, Hq, d)),
-             ("logits", logits, torch.float32, (B, 2, Hq, P_max)),
-             ("partial", partial, torch.float32, (B, geom.Hkv, P_max)),
-             ("score", score, torch.float32, (B, P_max)),
-             ("score_hist", score_hist, torch.int32, (B, HIST_BINS)))
-    for name, t, dtype, shape in given:
-        if t is not None:
-            _need_like(t, dtype, shape, q, name)
-    dev = q.device
-    with _stream_context(stream):
-        if out is None:
-            out = torch.empty_like(q)
-        if collect and logits is None:
-            logits = torch.empty((B, 2, Hq, P_max), dtype=torch.float32, device=dev)
-        if (collect or scored) and partial is None:
-            partial = torch.empty((B, geom.Hkv, P_max), dtype=torch.float32, device=dev)
-        if scored and score is None:
-            score = torch.empty((B, P_max), dtype=torch.float32, device=dev)
-        if scored and score_hist is None:
-            score_hist = torch.empty((B, HIST_BINS), dtype=torch.int32, device=dev)
-        if workspace is None:
-            nb = vsd_verify_quant_workspace_size(geom, R, P_max)
-            workspace = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(load().vsd_verify_attn_collect_quant(
-        ctypes.byref(geom), R, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-        _ptr(v_scale), _ptr(block_table), _ptr(prefix_len), int(row0),
-        R - 1 if row1 is None else int(row1), P_max, float(scale), _ptr(logits), _ptr(partial),
-        _ptr(score), _ptr(score_hist), int(n_sink), int(n_recent), _ptr(out), _ptr(workspace),
-        ws_bytes, _stream(stream)), "vsd_verify_attn_collect_quant")
+    Hkv, P_max = shape[1], int(P_max)
+    qp = _take(q, torch.bfloat16, None, dev, "q")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    width = block_table.shape[1]
+    bt = _take(block_table, torch.int32, (B, width), dev, "block_table")
+    pl = _take(prefix_len, torch.int32, (B,), dev, "prefix_len")
+    f32 = torch.float32
+    if out is None:
+        out = _empty(stream, q.shape, torch.bfloat16, dev)
+    if collect and logits is None:
+        logits = _empty(stream, (B, 2, Hq, P_max), f32, dev)
+    if (collect or scored) and partial is None:
+        partial = _empty(stream, (B, Hkv, P_max), f32, dev)
+    if scored and score is None:
+        score = _empty(stream, (B, P_max), f32, dev)
+    if scored and score_hist is None:
+        score_hist = _empty(stream, (B, HIST_BINS), torch.int32, dev)
+    op = _take(out, torch.bfloat16, q.shape, dev, "out")
+    lp = None if logits is None else _take(logits, f32, (B, 2, Hq, P_max), dev, "logits")
+    pp = None if partial is None else _take(partial, f32, (B, Hkv, P_max), dev, "partial")
+    sp = None if score is None else _take(score, f32, (B, P_max), dev, "score")
+    hp = None if score_hist is None else \
+        _take(score_hist, torch.int32, (B, HIST_BINS), dev, "score_hist")
+    key = (B, Hq, Hkv, d, shape[2], width, shape[0])
+    geom = _quant_geom(*key)
+    keep, wp, wb = _workspace_of(
+        workspace, _quant_workspace_bytes(dev, "vsd_verify_quant_workspace_size", key, R, P_max),
+        stream, dev)
+    _check((_lib or load()).vsd_verify_attn_collect_quant(
+        ctypes.addressof(geom), R, qp, kc, vc, ks, vs, bt, pl, row0, R - 1 if row1 is None else row1, P_max, scale,
+        lp, pp, sp, hp, n_sink, n_recent, op, wp, wb, _raw_stream(stream, dev)),
+        "vsd_verify_attn_collect_quant")
     return out, logits, partial, score, score_hist
 
 
@@ -835,8 +879,8 @@ def vsd_verify_attn_collect_scored_quant(q, k_cache, v_cache, k_scale, v_scale, 
 
 def vsd_sparse_quant_workspace_size(geom: Geom, k_max: int, max_tail: int) -> int:
     out = ctypes.c_size_t(0)
-    _check(load().vsd_sparse_quant_workspace_size(ctypes.byref(geom), int(k_max), int(max_tail),
-                                                  ctypes.byref(out)),
+    _check(load().vsd_sparse_quant_workspace_size(ctypes.addressof(geom), int(k_max),
+                                                  int(max_tail), ctypes.byref(out)),
            "vsd_sparse_quant_workspace_size")
     return int(out.value)
 
@@ -847,36 +891,36 @@ def vsd_sparse_decode_attn_quant(q, k_cache, v_cache, k_scale, v_scale, block_ta
                                  workspace=None, stream=None):
     """Sparse draft-step attention over an 8-bit cache.  q: bf16 [B, Hq, d]; idx: int32
     [B, k_max] and n_sel: int32 [B], or both None.  Returns out."""
-    if q.dim() != 3:
-        raise ValueError("q must be [B, Hq, d]")
+    dev = _cuda_index(q, torch.bfloat16, "q")
+    shape, kc, vc, ks, vs = _take_quant_cache(k_cache, v_cache, k_scale, v_scale, dev)
+    if q.dim() != 3 or q.shape[2] != shape[3]:
+        raise ValueError("q must be [B, Hq, %d]" % shape[3])
     B, Hq, d = q.shape
-    _need(q, torch.bfloat16, "q")
-    _need_quant_cache(k_cache, v_cache, k_scale, v_scale, q)
-    if d != k_cache.shape[3]:
-        raise ValueError("q and the caches have different head dimensions")
-    _need_like(block_table, torch.int32, (B, block_table.shape[-1]), q, "block_table")
-    _need_like(tail_start, torch.int32, (B,), q, "tail_start")
-    _need_like(seq_len, torch.int32, (B,), q, "seq_len")
-    k_max = 0
+    qp = _take(q, torch.bfloat16, None, dev, "q")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    width = block_table.shape[1]
+    bt = _take(block_table, torch.int32, (B, width), dev, "block_table")
+    t0 = _take(tail_start, torch.int32, (B,), dev, "tail_start")
+    t1 = _take(seq_len, torch.int32, (B,), dev, "seq_len")
     if (idx is None) != (n_sel is None):
         raise ValueError("idx and n_sel go together")
+    k_max, ip, np_ = 0, None, None
     if idx is not None:
-        k_max = int(idx.shape[-1])
-        _need_like(idx, torch.int32, (B, k_max), q, "idx")
-        _need_like(n_sel, torch.int32, (B,), q, "n_sel")
-    if out is not None:
-        _need_like(out, torch.bfloat16, (B, Hq, d), q, "out")
-    geom = geom_for(B, Hq, k_cache, block_table)
-    with _stream_context(stream):
-        if out is None:
-            out = torch.empty_like(q)
-        if workspace is None:
-            nb = vsd_sparse_quant_workspace_size(geom, k_max, max_tail)
-            workspace = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(load().vsd_sparse_decode_attn_quant(
-        ctypes.byref(geom), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-        _ptr(block_table), _ptr(idx), _ptr(n_sel), k_max, _ptr(tail_start), _ptr(seq_len),
-        int(max_tail), float(scale), _ptr(out), _ptr(workspace), ws_bytes, _stream(stream)),
-        "vsd_sparse_decode_attn_quant")
+        if idx.dim() != 2:
+            raise ValueError("idx must be [B, k_max]")
+        k_max = idx.shape[1]
+        ip = _take(idx, torch.int32, (B, k_max), dev, "idx")
+        np_ = _take(n_sel, torch.int32, (B,), dev, "n_sel")
+    if out is None:
+        out = _empty(stream, q.shape, torch.bfloat16, dev)
+    op = _take(out, torch.bfloat16, q.shape, dev, "out")
+    key = (B, Hq, shape[1], d, shape[2], width, shape[0])
+    geom = _quant_geom(*key)
+    keep, wp, wb = _workspace_of(
+        workspace, _quant_workspace_bytes(dev, "vsd_sparse_quant_workspace_size", key, k_max,
+                                          int(max_tail)), stream, dev)
+    _check((_lib or load()).vsd_sparse_decode_attn_quant(
+        ctypes.addressof(geom), qp, kc, vc, ks, vs, bt, ip, np_, k_max, t0, t1, max_tail, scale, op, wp, wb,
+        _raw_stream(stream, dev)), "vsd_sparse_decode_attn_quant")
     return out

@@ -11,7 +11,11 @@
 //
 // How: one warp owns one (sequence, page, KV head) of K or of V: at most 16 rows x 256
 // bytes, which its lanes hold in registers between the maximum and the conversion, so
-// the rows are read once.  No two warps touch the same page and head.
+// the rows are read once.  No two warps touch the same page and head.  Both kernels are
+// bound by HBM (2 bytes read and 1 written for each value stored, the reverse when read
+// back), so every load of a page is in flight at once and the arithmetic is kept small: the
+// maximum is taken on the packed bit patterns, and a division by a power of two is a
+// multiplication.
 #include <cmath>
 
 #include "launch.h"
@@ -21,8 +25,8 @@
 namespace vsd {
 namespace {
 
-constexpr int kQThreads = 128;
-constexpr int kQWarps = kQThreads / 32;
+constexpr int kRowThreads = 128;
+constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kPageQ = 16;
 
 struct RowsParams {
@@ -36,6 +40,7 @@ struct RowsParams {
   unsigned* status;
   int B, n, Hkv, max_blocks, num_blocks, pos_offset;
   int pages;  // pages that n rows of one sequence can meet
+  unsigned units;  // warps' parts: 2 * B * pages * Hkv
 };
 
 // The rows [p0, p0 + count) of sequence b (count 0 and a flag where they do not fit).
@@ -66,8 +71,45 @@ __device__ __forceinline__ float page_scale(float amax) {
   return ldexpf(1.f, s);
 }
 
+// The part of a call that one warp does: unit = ((b * pages + page) * 2 + kv) * Hkv + g.
+struct PageUnit {
+  int b, kv;
+  long long lo;  // position of the page's slot 0
+  int s0, s1;    // slots [s0, s1) belong to the call (none: s1 <= s0)
+  size_t ph;     // (physical page, head)
+  RowRange rr;
+};
+
+__device__ __forceinline__ PageUnit page_unit(const RowsParams& a, unsigned u, int lane) {
+  PageUnit p;
+  const unsigned r1 = u / a.Hkv;
+  const int g = static_cast<int>(u - r1 * a.Hkv);
+  p.kv = static_cast<int>(r1 & 1u);
+  const unsigned r2 = r1 >> 1;
+  p.b = static_cast<int>(r2 / a.pages);
+  const int pg = static_cast<int>(r2 - static_cast<unsigned>(p.b) * a.pages);
+  p.rr = row_range(a, p.b, lane == 0 && p.kv == 0 && g == 0 && pg == 0);
+  const long long lp = p.rr.p0 / kPageQ + pg;
+  p.lo = lp * kPageQ;
+  p.s0 = static_cast<int>(p.rr.p0 > p.lo ? p.rr.p0 - p.lo : 0);
+  const long long left = p.rr.p0 + p.rr.count - p.lo;
+  p.s1 = left < kPageQ ? static_cast<int>(left) : kPageQ;
+  if (p.rr.count <= 0) p.s1 = 0;
+  p.ph = 0;
+  if (p.s1 > p.s0) {
+    const int blk = __ldcg(a.block_table + static_cast<size_t>(p.b) * a.max_blocks + lp);
+    if (blk < 0 || blk >= a.num_blocks) {
+      if (lane == 0) flag_status(a.status, VSD_DEV_BAD_BLOCK);
+      p.s1 = p.s0;
+    } else {
+      p.ph = static_cast<size_t>(blk) * a.Hkv + g;
+    }
+  }
+  return p;
+}
+
 template <int D>
-__global__ void __launch_bounds__(kQThreads) append_kv_quant_kernel(const RowsParams a) {
+__global__ void __launch_bounds__(kRowThreads) append_kv_quant_kernel(const RowsParams a) {
   constexpr int LPR = D / 8;           // lanes of a row: 8 values each
   constexpr int RPI = 32 / LPR;        // rows per warp instruction
   constexpr int NI = kPageQ / RPI;     // instructions of a page
@@ -75,123 +117,129 @@ __global__ void __launch_bounds__(kQThreads) append_kv_quant_kernel(const RowsPa
   ptx::pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int sub = lane / LPR, lr = lane % LPR;
-  const long long units = 2ll * a.B * a.pages * a.Hkv;
-  for (long long u = static_cast<long long>(blockIdx.x) * kQWarps + (threadIdx.x >> 5); u < units;
-       u += static_cast<long long>(gridDim.x) * kQWarps) {
-    // u = ((b * pages + page) * 2 + kv) * Hkv + g
-    const int g = static_cast<int>(u % a.Hkv);
-    const long long r1 = u / a.Hkv;
-    const int kv = static_cast<int>(r1 & 1);
-    const long long r2 = r1 >> 1;
-    const int pg = static_cast<int>(r2 % a.pages);
-    const int b = static_cast<int>(r2 / a.pages);
-    const RowRange rr = row_range(a, b, lane == 0 && kv == 0 && g == 0 && pg == 0);
-    const long long lp = rr.p0 / kPageQ + pg;  // logical page
-    // written slots [s0, s1) of the page
-    const long long lo = lp * kPageQ;
-    const int s0 = static_cast<int>(rr.p0 > lo ? rr.p0 - lo : 0);
-    const long long left = rr.p0 + rr.count - lo;
-    const int s1 = left < kPageQ ? static_cast<int>(left) : kPageQ;
-    if (rr.count <= 0 || s1 <= s0) continue;
-    const int blk = __ldcg(a.block_table + static_cast<size_t>(b) * a.max_blocks + lp);
-    if (blk < 0 || blk >= a.num_blocks) {
-      if (lane == 0) flag_status(a.status, VSD_DEV_BAD_BLOCK);
-      continue;
-    }
-    const size_t ph = static_cast<size_t>(blk) * a.Hkv + g;  // (page, head)
-    const uint16_t* src = a.src[kv];
-    uint8_t* page = a.cache[kv] + ph * (kPageQ * D);
-    const float was = s0 > 0 ? __ldcg(a.scale[kv] + ph) : 0.f;
-    uint4 x[NI];
-    float amax = 0.f;
+  const unsigned u = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  if (u >= a.units) return;
+  const PageUnit pu = page_unit(a, u, lane);
+  const int s0 = pu.s0, s1 = pu.s1;
+  if (s1 <= s0) return;
+  const int g = static_cast<int>(u % a.Hkv);
+  const uint16_t* src = a.src[pu.kv] +
+                        ((static_cast<size_t>(pu.b) * a.n) * a.Hkv + g) * D + lr * 8;
+  uint8_t* page = a.cache[pu.kv] + pu.ph * (kPageQ * D) + lr * 8;
+  uint4 x[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int slot = i * RPI + sub;
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (slot >= s0 && slot < s1)
+      x[i] = ldg_stream16(src + static_cast<size_t>(pu.lo + slot - pu.rr.p0) * a.Hkv * D);
+  }
+  const float was = s0 > 0 ? __ldcg(a.scale[pu.kv] + pu.ph) : 0.f;
+  // the largest magnitude, on the bit patterns of two values at a time (they order alike)
+  uint32_t top2 = 0u;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const uint32_t p = __vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu);
+    const uint32_t q = __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu);
+    top2 = __vmaxu2(top2, __vmaxu2(p, q));
+  }
+  uint32_t top = __reduce_max_sync(0xffffffffu, max(top2 & 0xFFFFu, top2 >> 16));
+  if (top >= 0x7F80u) {
+    // rare: a NaN or an infinity somewhere.  They do not set the scale and become NaN.
+    top = 0u;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int slot = i * RPI + sub;
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (slot >= s0 && slot < s1) {
-        const size_t row = (static_cast<size_t>(b) * a.n + static_cast<size_t>(lo + slot - rr.p0)) *
-                               a.Hkv + g;
-        x[i] = ldg_stream16(src + row * D + lr * 8);
-      }
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float f0 = fabsf(bf16_lo(w[k])), f1 = fabsf(bf16_hi(w[k]));
-        if (f0 < INFINITY) amax = fmaxf(amax, f0);
-        if (f1 < INFINITY) amax = fmaxf(amax, f1);
+        const uint32_t l = w[k] & 0x7FFFu, h = (w[k] >> 16) & 0x7FFFu;
+        if (l < 0x7F80u) top = max(top, l);
+        else w[k] |= 0x7FFFu;
+        if (h < 0x7F80u) top = max(top, h);
+        else w[k] |= 0x7FFF0000u;
       }
+      x[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    top = __reduce_max_sync(0xffffffffu, top);
+  }
+  const float amax = __uint_as_float(top << 16);
+  float now = page_scale(amax);
+  if (s0 > 0 && amax <= was * kE4M3Max) now = was;
+  // codes = x / now; by a power of two (any scale stored here; not every caller's own) the
+  // product with its reciprocal is the same number
+  const bool pow2 = (__float_as_uint(now) & 0x007FFFFFu) == 0u && now >= 0x1p-126f;
+  const float inv = pow2 ? 1.f / now : 0.f;
+  const auto two = [&](uint32_t w) {
+    const float lo = bf16_lo(w), hi = bf16_hi(w);
+    return pow2 ? pack_e4m3x2(lo * inv, hi * inv) : pack_e4m3x2(__fdiv_rn(lo, now), __fdiv_rn(hi, now));
+  };
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    float now = page_scale(amax);
-    if (s0 > 0 && amax <= was * kE4M3Max) now = was;
-    const auto code = [now](float v) {
-      return isfinite(v) ? __fdiv_rn(v, now) : NAN;
+  for (int i = 0; i < NI; ++i) {
+    const int slot = i * RPI + sub;
+    if (slot >= s0 && slot < s1)
+      *reinterpret_cast<uint2*>(page + slot * D) =
+          make_uint2(two(x[i].x) | two(x[i].y) << 16, two(x[i].z) | two(x[i].w) << 16);
+  }
+  if (s0 > 0 && now != was) {
+    // earlier rows of a page whose scale grows
+    const float ratio = __fdiv_rn(was, now);
+    const auto again = [ratio](uint32_t w) {
+      const float2 p = e4m3x2_to_float2(w & 0xFFFFu), q = e4m3x2_to_float2(w >> 16);
+      return pack_e4m3x2(__fmul_rn(p.x, ratio), __fmul_rn(p.y, ratio)) |
+             pack_e4m3x2(__fmul_rn(q.x, ratio), __fmul_rn(q.y, ratio)) << 16;
     };
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int slot = i * RPI + sub;
-      if (slot >= s0 && slot < s1) {
-        uint2 c;
-        c.x = pack_e4m3x2(code(bf16_lo(x[i].x)), code(bf16_hi(x[i].x))) |
-              pack_e4m3x2(code(bf16_lo(x[i].y)), code(bf16_hi(x[i].y))) << 16;
-        c.y = pack_e4m3x2(code(bf16_lo(x[i].z)), code(bf16_hi(x[i].z))) |
-              pack_e4m3x2(code(bf16_lo(x[i].w)), code(bf16_hi(x[i].w))) << 16;
-        *reinterpret_cast<uint2*>(page + slot * D + lr * 8) = c;
-      } else if (slot < s0 && now != was) {
-        // an earlier row of a page whose scale grows
-        const float ratio = __fdiv_rn(was, now);
-        uint2* at = reinterpret_cast<uint2*>(page + slot * D + lr * 8);
+      if (slot < s0) {
+        uint2* at = reinterpret_cast<uint2*>(page + slot * D);
         const uint2 old = *at;
-        const auto again = [ratio](uint32_t w) {
-          const float2 p = e4m3x2_to_float2(w & 0xFFFFu), q = e4m3x2_to_float2(w >> 16);
-          return pack_e4m3x2(__fmul_rn(p.x, ratio), __fmul_rn(p.y, ratio)) |
-                 pack_e4m3x2(__fmul_rn(q.x, ratio), __fmul_rn(q.y, ratio)) << 16;
-        };
         *at = make_uint2(again(old.x), again(old.y));
       }
     }
-    __syncwarp();
-    if (lane == 0 && (s0 == 0 || now != was)) a.scale[kv][ph] = now;
   }
+  if (lane == 0 && (s0 == 0 || now != was)) a.scale[pu.kv][pu.ph] = now;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kQThreads) read_kv_quant_kernel(const RowsParams a) {
-  constexpr int LPR = D / 8;
+__global__ void __launch_bounds__(kRowThreads) read_kv_quant_kernel(const RowsParams a) {
+  constexpr int LPR = D / 16;          // lanes of a row: 16 codes each
+  constexpr int RPI = 32 / LPR;
+  constexpr int NI = kPageQ / RPI;
   ptx::pdl_wait_primary();
   ptx::pdl_launch_dependents();
-  const long long total = 2ll * a.B * a.n * a.Hkv * LPR;
-  for (long long i = static_cast<long long>(blockIdx.x) * kQThreads + threadIdx.x; i < total;
-       i += static_cast<long long>(gridDim.x) * kQThreads) {
-    // i = (((kv * B + b) * n + t) * Hkv + g) * LPR + chunk
-    const int c = static_cast<int>(i % LPR);
-    const long long row = i / LPR;
-    const int g = static_cast<int>(row % a.Hkv);
-    const long long r1 = row / a.Hkv;
-    const int t = static_cast<int>(r1 % a.n);
-    const long long r2 = r1 / a.n;
-    const int b = static_cast<int>(r2 % a.B);
-    const int kv = static_cast<int>(r2 / a.B);
-    const RowRange rr = row_range(a, b, c == 0 && g == 0 && kv == 0 && t == 0);
-    if (t >= rr.count) continue;
-    const long long p = rr.p0 + t;
-    const int blk = __ldcg(a.block_table + static_cast<size_t>(b) * a.max_blocks + p / kPageQ);
-    if (blk < 0 || blk >= a.num_blocks) {
-      if (c == 0) flag_status(a.status, VSD_DEV_BAD_BLOCK);
-      continue;
+  const int lane = threadIdx.x & 31;
+  const int sub = lane / LPR, lr = lane % LPR;
+  const unsigned u = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  if (u >= a.units) return;
+  const PageUnit pu = page_unit(a, u, lane);
+  if (pu.s1 <= pu.s0) return;
+  const uint8_t* page = a.cache[pu.kv] + pu.ph * (kPageQ * D) + lr * 16;
+  uint4 x[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int slot = i * RPI + sub;
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (slot >= pu.s0 && slot < pu.s1) x[i] = ldg_stream16(page + slot * D);
+  }
+  const float s = __ldcg(a.scale[pu.kv] + pu.ph);
+  const int g = static_cast<int>(u % a.Hkv);
+  uint16_t* dst = a.dst[pu.kv] + ((static_cast<size_t>(pu.b) * a.n) * a.Hkv + g) * D + lr * 16;
+  const auto two = [s](uint32_t codes) {
+    const float2 v = e4m3x2_to_float2(codes);
+    return pack_bf16x2(__fmul_rn(v.x, s), __fmul_rn(v.y, s));
+  };
+  const auto four = [&](uint32_t a0, uint32_t b0) {
+    return make_uint4(two(a0 & 0xFFFFu), two(a0 >> 16), two(b0 & 0xFFFFu), two(b0 >> 16));
+  };
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int slot = i * RPI + sub;
+    if (slot >= pu.s0 && slot < pu.s1) {
+      uint4* to = reinterpret_cast<uint4*>(dst + static_cast<size_t>(pu.lo + slot - pu.rr.p0) * a.Hkv * D);
+      __stcs(to, four(x[i].x, x[i].y));
+      __stcs(to + 1, four(x[i].z, x[i].w));
     }
-    const size_t ph = static_cast<size_t>(blk) * a.Hkv + g;
-    const float s = __ldcg(a.scale[kv] + ph);
-    const uint2 w = ldg_stream8(a.cache[kv] + (ph * kPageQ + static_cast<size_t>(p % kPageQ)) * D +
-                                c * 8);
-    const auto two = [s](uint32_t codes) {
-      const float2 v = e4m3x2_to_float2(codes);
-      return pack_bf16x2(__fmul_rn(v.x, s), __fmul_rn(v.y, s));
-    };
-    const uint4 o = make_uint4(two(w.x & 0xFFFFu), two(w.x >> 16), two(w.y & 0xFFFFu), two(w.y >> 16));
-    const size_t out = (static_cast<size_t>(b) * a.n + t) * a.Hkv + g;
-    *reinterpret_cast<uint4*>(a.dst[kv] + out * D + c * 8) = o;
   }
 }
 
@@ -215,19 +263,19 @@ RowsParams rows_params(const QuantRowsArgs& x) {
   p.max_blocks = x.max_blocks;
   p.num_blocks = x.num_blocks;
   p.pos_offset = x.pos_offset;
-  p.pages = static_cast<int>((static_cast<long long>(x.n) + kPageQ - 2) / kPageQ + 1);
+  p.pages = quant_pages(x.n);
+  p.units = 2u * p.B * p.pages * p.Hkv;
   return p;
 }
 
 template <typename Kernel>
-cudaError_t launch_rows(Kernel kern, long long blocks, const RowsParams& p, cudaStream_t stream) {
-  if (blocks > 4096) blocks = 4096;
+cudaError_t launch_rows(Kernel kern, const RowsParams& p, cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
-  cfg.blockDim = dim3(kQThreads, 1, 1);
+  cfg.gridDim = dim3((p.units + kRowWarps - 1) / kRowWarps, 1, 1);
+  cfg.blockDim = dim3(kRowThreads, 1, 1);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -238,18 +286,14 @@ cudaError_t launch_rows(Kernel kern, long long blocks, const RowsParams& p, cuda
 
 cudaError_t launch_append_kv_quant(const QuantRowsArgs& x, cudaStream_t stream) {
   const RowsParams p = rows_params(x);
-  const long long units = 2ll * p.B * p.pages * p.Hkv;
-  const long long blocks = (units + kQWarps - 1) / kQWarps;
-  return x.d == 128 ? launch_rows(append_kv_quant_kernel<128>, blocks, p, stream)
-                    : launch_rows(append_kv_quant_kernel<64>, blocks, p, stream);
+  return x.d == 128 ? launch_rows(append_kv_quant_kernel<128>, p, stream)
+                    : launch_rows(append_kv_quant_kernel<64>, p, stream);
 }
 
 cudaError_t launch_read_kv_quant(const QuantRowsArgs& x, cudaStream_t stream) {
   const RowsParams p = rows_params(x);
-  const long long total = 2ll * p.B * p.n * p.Hkv * (x.d / 8);
-  const long long blocks = (total + kQThreads - 1) / kQThreads;
-  return x.d == 128 ? launch_rows(read_kv_quant_kernel<128>, blocks, p, stream)
-                    : launch_rows(read_kv_quant_kernel<64>, blocks, p, stream);
+  return x.d == 128 ? launch_rows(read_kv_quant_kernel<128>, p, stream)
+                    : launch_rows(read_kv_quant_kernel<64>, p, stream);
 }
 
 }  // namespace vsd

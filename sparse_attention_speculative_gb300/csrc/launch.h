@@ -229,6 +229,11 @@ struct QuantRowsArgs {
   int B, n, Hkv, d, max_blocks, num_blocks, pos_offset;
 };
 
+// Pages that n >= 1 rows of one sequence can meet.  The kernels number 2 * B * pages * Hkv
+// parts in 32 bits.
+inline int quant_pages(int n) {
+  return static_cast<int>((static_cast<long long>(n) + 14) / 16 + 1);
+}
 cudaError_t launch_append_kv_quant(const QuantRowsArgs& a, cudaStream_t stream);
 cudaError_t launch_read_kv_quant(const QuantRowsArgs& a, cudaStream_t stream);
 

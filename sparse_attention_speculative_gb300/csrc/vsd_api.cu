@@ -971,6 +971,7 @@ vsd_status quant_rows(const vsd_geom* geom, int n, const void* k_rows, const voi
   if (st != VSD_OK) return st;
   if (n < 0) return VSD_ERR_INVALID_ARG;
   if (geom->B == 0 || n == 0) return VSD_OK;
+  if (2.0 * geom->B * vsd::quant_pages(n) * geom->Hkv > 2147483647.0) return VSD_ERR_UNSUPPORTED;
   if (!k_rows || !v_rows || !block_table || !pos_base ||
       !quant_cache_ok(k_cache, v_cache, k_scale, v_scale))
     return VSD_ERR_INVALID_ARG;

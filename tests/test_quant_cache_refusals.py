@@ -83,6 +83,7 @@ def test_row_calls(lib, p, call):
     for name in ("bt", "pos", "nv", "ks", "vs"):
         assert call(lib, geom(), p, **{name: off(p, 2)}) == -1
     assert call(lib, geom(), p, n=-1) == -1
+    assert call(lib, geom(B=2 ** 20), p, n=2 ** 20) == -2   # more parts than 32 bits count
     assert call(lib, geom(), p, n=0, k=None) == 0        # nothing to do: no device needed
     assert call(lib, geom(B=0), p, k=None) == 0
 
