@@ -71,6 +71,13 @@ __device__ __forceinline__ float page_scale(float amax) {
   return ldexpf(1.f, s);
 }
 
+// The larger magnitudes of two pairs of bf16 values (with some sign; NaN if either is).
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // The part of a call that one warp does: unit = ((b * pages + page) * 2 + kv) * Hkv + g.
 struct PageUnit {
   int b, kv;
@@ -135,14 +142,12 @@ __global__ void __launch_bounds__(kRowThreads) append_kv_quant_kernel(const Rows
       x[i] = ldg_stream16(src + static_cast<size_t>(pu.lo + slot - pu.rr.p0) * a.Hkv * D);
   }
   const float was = s0 > 0 ? __ldcg(a.scale[pu.kv] + pu.ph) : 0.f;
-  // the largest magnitude, on the bit patterns of two values at a time (they order alike)
+  // the largest magnitude, two values at a time (a NaN wins, signs mean nothing)
   uint32_t top2 = 0u;
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const uint32_t p = __vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu);
-    const uint32_t q = __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu);
-    top2 = __vmaxu2(top2, __vmaxu2(p, q));
-  }
+  for (int i = 0; i < NI; ++i)
+    top2 = max_abs2(top2, max_abs2(max_abs2(x[i].x, x[i].y), max_abs2(x[i].z, x[i].w)));
+  top2 &= 0x7FFF7FFFu;
   uint32_t top = __reduce_max_sync(0xffffffffu, max(top2 & 0xFFFFu, top2 >> 16));
   if (top >= 0x7F80u) {
     // rare: a NaN or an infinity somewhere.  They do not set the scale and become NaN.
