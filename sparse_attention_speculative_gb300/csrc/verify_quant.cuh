@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
         if (lane < 2 * kPagesPerTile)
           tma_load_4d(dst + stage * Cfg::kTileBytes, map, &full[stage], 0, 0, s.g, blk, pol);
       }
-      if (*abort_flag) break;
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
     }
     // never leave a copy in flight: wait (with the drain limit) for the last stages
     if (leads) {
@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
         // (a test build waits for a barrier that nothing completes yet)
         bool ok = true;
         if (sw == 0)
-          ok = VSD_STALL(ik == 0) ? mbar_wait_compact(mma_fin, 0, abort_flag)
+          ok = VSD_STALL(ik == 0) ? mbar_wait_compact(pv_fin, 0, abort_flag)
                                   : mbar_wait_compact(&s_full[grp], (ik >> 1) & 1, abort_flag);
         else if (sw == 1)
           ok = mbar_wait_compact(&sc_full[slot], ((round + (k >> 2)) / kRounds) & 1, abort_flag);
