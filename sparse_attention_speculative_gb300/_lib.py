@@ -647,34 +647,23 @@ def vsd_sparse_decode_attn_step(q, k_cache, v_cache, block_table, idx, n_sel, ta
 
 
 # ------------------------------------------------------------------ 8-bit cache
-def _refuse(t, dtype, shape, dev, name: str) -> None:
-    """Say what is wrong with a tensor that _take refused."""
-    _need(t, dtype, name)
-    if shape is not None and t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    raise ValueError("%s is on another device" % name)
+# These calls are made once per layer and step, so their checks are one comparison per
+# property and tensor on the way through; _refuse says afterwards what was wrong.
+_F8, _BF16, _F32, _I32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32
 
 
-def _take(t, dtype, shape, dev, name: str) -> int:
-    """The address of a contiguous tensor of the given type and shape (None: any) on CUDA
-    device `dev`; one pass of cheap comparisons, these calls are made once per layer and
-    step."""
-    if t.dtype is not dtype or (shape is not None and t.shape != shape) or \
-            t.get_device() != dev or not t.is_contiguous():
-        _refuse(t, dtype, shape, dev, name)
-    return t.data_ptr()
-
-
-def _take_quant_cache(k_cache, v_cache, k_scale, v_scale, dev):
-    """The caches of the 8-bit calls: float8_e4m3fn [num_blocks, Hkv, 16, d] and float32
-    scales [num_blocks, Hkv], on device `dev`.  Returns their shape and addresses."""
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache must be [num_blocks, Hkv, 16, d]")
-    shape = k_cache.shape
-    return shape, _take(k_cache, torch.float8_e4m3fn, None, dev, "k_cache"), \
-        _take(v_cache, torch.float8_e4m3fn, shape, dev, "v_cache"), \
-        _take(k_scale, torch.float32, shape[:2], dev, "k_scale"), \
-        _take(v_scale, torch.float32, shape[:2], dev, "v_scale")
+def _refuse(*wanted) -> None:
+    """Raise what is wrong with the first of (tensor, dtype, shape, device, name) that is
+    not as wanted."""
+    for t, dtype, shape, dev, name in wanted:
+        if t is None:
+            continue
+        _need(t, dtype, name)
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+        if t.get_device() != dev:
+            raise ValueError("%s is on another device" % name)
+    raise ValueError("tensors do not fit together")
 
 
 def _cuda_index(t, dtype, name: str) -> int:
@@ -685,17 +674,32 @@ def _cuda_index(t, dtype, name: str) -> int:
     return dev
 
 
-def _on_device(fn):
-    """Run a call with the device of its first tensor current (the library launches on
-    the current device)."""
-    @functools.wraps(fn)
-    def call(first, *args, **kw):
-        dev = first.get_device()
-        if dev < 0 or dev == torch.cuda.current_device():
-            return fn(first, *args, **kw)
-        with torch.cuda.device(dev):
-            return fn(first, *args, **kw)
-    return call
+def _is(t, dtype, numel: int, dim: int, dev: int) -> bool:
+    return t.dtype is dtype and t.numel() == numel and t.dim() == dim and \
+        t.get_device() == dev and t.is_contiguous()
+
+
+def _cache_shape(k_cache, v_cache, k_scale, v_scale, dev):
+    """The shape (num_blocks, Hkv, 16, d) of an 8-bit cache: float8_e4m3fn codes and
+    float32 scales [num_blocks, Hkv] on device `dev`."""
+    shape = k_cache.shape
+    if len(shape) == 4:
+        n = shape[0] * shape[1]
+        if k_cache.dtype is _F8 and v_cache.dtype is _F8 and v_cache.shape == shape and \
+                k_cache.is_contiguous() and v_cache.is_contiguous() and \
+                k_cache.get_device() == dev and v_cache.get_device() == dev and \
+                k_scale.shape == v_scale.shape == shape[:2] and \
+                _is(k_scale, _F32, n, 2, dev) and _is(v_scale, _F32, n, 2, dev):
+            return shape
+    _refuse((k_cache, _F8, shape if len(shape) == 4 else ("num_blocks", "Hkv", 16, "d"), dev, "k_cache"),
+            (v_cache, _F8, shape, dev, "v_cache"), (k_scale, _F32, shape[:2], dev, "k_scale"),
+            (v_scale, _F32, shape[:2], dev, "v_scale"))
+
+
+def _elsewhere(dev: int) -> bool:
+    """Whether a call's tensors are on another device than the current one (the library
+    launches on the current device)."""
+    return dev >= 0 and dev != torch._C._cuda_getDevice()
 
 
 def _empty(stream, shape, dtype, dev, make=torch.empty):
@@ -713,19 +717,16 @@ def _raw_stream(stream, dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-@functools.lru_cache(maxsize=256)
-def _quant_geom(B: int, Hq: int, Hkv: int, d: int, page: int, max_blocks: int, num_blocks: int):
-    """A geometry, kept for the next call of the same shape."""
-    return Geom(B, Hq, Hkv, d, page, max_blocks, num_blocks)
-
-
-@functools.lru_cache(maxsize=256)
-def _quant_workspace_bytes(dev: int, call: str, shape, x: int, y: int) -> int:
-    """Workspace of a call over a geometry (a number of its shape and the device's SMs)."""
-    out = ctypes.c_size_t(0)
-    _check(getattr(load(), call)(ctypes.addressof(_quant_geom(*shape)), x, y, ctypes.byref(out)),
-           call)
-    return int(out.value)
+@functools.lru_cache(maxsize=512)
+def _quant_plan(call: str, dev: int, x: int, y: int, B: int, Hq: int, Hkv: int, d: int, page: int,
+                max_blocks: int, num_blocks: int):
+    """(geometry, its address, workspace bytes) of a call, kept for the next one of the same
+    shape.  `call` names the size query, "" for calls without a workspace."""
+    geom = Geom(B, Hq, Hkv, d, page, max_blocks, num_blocks)
+    nbytes = ctypes.c_size_t(0)
+    if call:
+        _check(getattr(load(), call)(ctypes.addressof(geom), x, y, ctypes.byref(nbytes)), call)
+    return geom, ctypes.addressof(geom), int(nbytes.value)
 
 
 def _workspace_of(workspace, nbytes: int, stream, dev: int):
@@ -739,27 +740,23 @@ def _workspace_of(workspace, nbytes: int, stream, dev: int):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _quant_rows(k_rows, v_rows, names, k_cache, v_cache, k_scale, v_scale, block_table, pos_base,
-                n_valid):
-    """Checks and addresses that storing and reading rows share."""
-    dev = _cuda_index(k_rows, torch.bfloat16, names[0])
-    shape, kc, vc, ks, vs = _take_quant_cache(k_cache, v_cache, k_scale, v_scale, dev)
+def _rows_plan(k_rows, v_rows, names, k_cache, v_cache, k_scale, v_scale, block_table, pos_base,
+               n_valid, dev):
+    """The checks that storing and reading rows share, and the geometry."""
+    NB, Hkv, page, d = _cache_shape(k_cache, v_cache, k_scale, v_scale, dev)
     rows = k_rows.shape
-    if len(rows) != 4 or rows[2] != shape[1] or rows[3] != shape[3]:
-        raise ValueError("%s must be [B, n, %d, %d]" % (names[0], shape[1], shape[3]))
-    B = rows[0]
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_blocks]")
-    width = block_table.shape[1]
-    geom = _quant_geom(B, shape[1], shape[1], shape[3], shape[2], width, shape[0])
-    return geom, _take(k_rows, torch.bfloat16, None, dev, names[0]), \
-        _take(v_rows, torch.bfloat16, rows, dev, names[1]), kc, vc, ks, vs, \
-        _take(block_table, torch.int32, (B, width), dev, "block_table"), \
-        _take(pos_base, torch.int32, (B,), dev, "pos_base"), \
-        None if n_valid is None else _take(n_valid, torch.int32, (B,), dev, "n_valid")
+    B, width = rows[0], block_table.shape[-1]
+    if not (len(rows) == 4 and rows[2] == Hkv and rows[3] == d and
+            _is(k_rows, _BF16, k_rows.numel(), 4, dev) and _is(v_rows, _BF16, k_rows.numel(), 4, dev) and
+            v_rows.shape == rows and _is(block_table, _I32, B * width, 2, dev) and
+            _is(pos_base, _I32, B, 1, dev) and (n_valid is None or _is(n_valid, _I32, B, 1, dev))):
+        want = (B, rows[1] if len(rows) == 4 else "n", Hkv, d)
+        _refuse((k_rows, _BF16, want, dev, names[0]), (v_rows, _BF16, want, dev, names[1]),
+                (block_table, _I32, (B, width), dev, "block_table"), (pos_base, _I32, (B,), dev, "pos_base"),
+                (n_valid, _I32, (B,), dev, "n_valid"))
+    return _quant_plan("", dev, 0, 0, B, Hkv, Hkv, d, page, width, NB)
 
 
-@_on_device
 def vsd_append_kv_quant(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, pos_base, *,
                         pos_offset: int = 0, n_valid=None, stream=None) -> None:
     """Quantise and store K/V rows k_new, v_new (bf16 [B, n_new, Hkv, d]) at positions
@@ -767,34 +764,45 @@ def vsd_append_kv_quant(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_
     (float8_e4m3fn [num_blocks, Hkv, 16, d], scales float32 [num_blocks, Hkv]).  Rows are
     appended in order: a page whose slot 0 is written starts afresh, otherwise its earlier
     rows are kept (requantised when its scale has to grow)."""
-    geom, kn, vn, kc, vc, ks, vs, bt, pos, nv = _quant_rows(
-        k_new, v_new, ("k_new", "v_new"), k_cache, v_cache, k_scale, v_scale, block_table, pos_base,
-        n_valid)
+    dev = _cuda_index(k_new, _BF16, "k_new")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return vsd_append_kv_quant(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table,
+                                       pos_base, pos_offset=pos_offset, n_valid=n_valid, stream=stream)
+    geom = _rows_plan(k_new, v_new, ("k_new", "v_new"), k_cache, v_cache, k_scale, v_scale, block_table,
+                      pos_base, n_valid, dev)
     _check((_lib or load()).vsd_append_kv_quant(
-        ctypes.addressof(geom), k_new.shape[1], kn, vn, bt, pos, pos_offset, nv, kc, vc, ks, vs,
-        _raw_stream(stream, k_new.get_device())), "vsd_append_kv_quant")
+        geom[1], k_new.shape[1], k_new.data_ptr(), v_new.data_ptr(), block_table.data_ptr(),
+        pos_base.data_ptr(), pos_offset, None if n_valid is None else n_valid.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        _raw_stream(stream, dev)), "vsd_append_kv_quant")
 
 
-@_on_device
 def vsd_read_kv_quant(k_cache, v_cache, k_scale, v_scale, block_table, pos_base, *, n: int,
                       pos_offset: int = 0, n_valid=None, k_out=None, v_out=None, stream=None):
     """The rows at positions pos_base[b] + pos_offset + t, t < n_valid[b] (None: n), of an
     8-bit cache as bf16 [B, n, Hkv, d].  Rows behind n_valid are left as they were in
     k_out, v_out (zeros when allocated here).  Returns (k_out, v_out)."""
-    shape = (pos_base.shape[0], int(n), k_cache.shape[1], k_cache.shape[-1])
+    dev = _cuda_index(k_cache, _F8, "k_cache")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return vsd_read_kv_quant(k_cache, v_cache, k_scale, v_scale, block_table, pos_base, n=n,
+                                     pos_offset=pos_offset, n_valid=n_valid, k_out=k_out, v_out=v_out,
+                                     stream=stream)
     if k_out is None or v_out is None:
+        shape = (pos_base.shape[0], n, k_cache.shape[1], k_cache.shape[-1])
         make = torch.empty if n_valid is None else torch.zeros
-        dev = _cuda_index(k_cache, torch.float8_e4m3fn, "k_cache")
-        k_out = _empty(stream, shape, torch.bfloat16, dev, make) if k_out is None else k_out
-        v_out = _empty(stream, shape, torch.bfloat16, dev, make) if v_out is None else v_out
-    geom, ko, vo, kc, vc, ks, vs, bt, pos, nv = _quant_rows(
-        k_out, v_out, ("k_out", "v_out"), k_cache, v_cache, k_scale, v_scale, block_table, pos_base,
-        n_valid)
-    if k_out.shape != shape:
+        k_out = _empty(stream, shape, _BF16, dev, make) if k_out is None else k_out
+        v_out = _empty(stream, shape, _BF16, dev, make) if v_out is None else v_out
+    geom = _rows_plan(k_out, v_out, ("k_out", "v_out"), k_cache, v_cache, k_scale, v_scale, block_table,
+                      pos_base, n_valid, dev)
+    if k_out.shape[1] != n:
         raise ValueError("k_out and v_out must be [B, n, Hkv, d]")
     _check((_lib or load()).vsd_read_kv_quant(
-        ctypes.addressof(geom), shape[1], kc, vc, ks, vs, bt, pos, pos_offset, nv, ko, vo,
-        _raw_stream(stream, k_out.get_device())), "vsd_read_kv_quant")
+        geom[1], n, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        block_table.data_ptr(), pos_base.data_ptr(), pos_offset,
+        None if n_valid is None else n_valid.data_ptr(), k_out.data_ptr(), v_out.data_ptr(),
+        _raw_stream(stream, dev)), "vsd_read_kv_quant")
     return k_out, v_out
 
 
@@ -806,51 +814,57 @@ def vsd_verify_quant_workspace_size(geom: Geom, R: int, P_max: int) -> int:
     return int(out.value)
 
 
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
 def _verify_quant(q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, P_max, scale,
                   row0, row1, logits, partial, score, score_hist, n_sink, n_recent, out,
                   workspace, stream, collect, scored):
-    dev = _cuda_index(q, torch.bfloat16, "q")
-    shape, kc, vc, ks, vs = _take_quant_cache(k_cache, v_cache, k_scale, v_scale, dev)
-    if q.dim() != 4 or q.shape[3] != shape[3]:
-        raise ValueError("q must be [B, R, Hq, %d]" % shape[3])
-    B, R, Hq, d = q.shape
-    Hkv, P_max = shape[1], int(P_max)
-    qp = _take(q, torch.bfloat16, None, dev, "q")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_blocks]")
-    width = block_table.shape[1]
-    bt = _take(block_table, torch.int32, (B, width), dev, "block_table")
-    pl = _take(prefix_len, torch.int32, (B,), dev, "prefix_len")
-    f32 = torch.float32
+    dev = _cuda_index(q, _BF16, "q")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return _verify_quant(q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, P_max,
+                                 scale, row0, row1, logits, partial, score, score_hist, n_sink,
+                                 n_recent, out, workspace, stream, collect, scored)
+    NB, Hkv, page, d = _cache_shape(k_cache, v_cache, k_scale, v_scale, dev)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, R, Hq, d]")
+    B, R, Hq, dq = q.shape
+    width = block_table.shape[-1]
     if out is None:
-        out = _empty(stream, q.shape, torch.bfloat16, dev)
+        out = _empty(stream, q.shape, _BF16, dev)
     if collect and logits is None:
-        logits = _empty(stream, (B, 2, Hq, P_max), f32, dev)
+        logits = _empty(stream, (B, 2, Hq, P_max), _F32, dev)
     if (collect or scored) and partial is None:
-        partial = _empty(stream, (B, Hkv, P_max), f32, dev)
+        partial = _empty(stream, (B, Hkv, P_max), _F32, dev)
     if scored and score is None:
-        score = _empty(stream, (B, P_max), f32, dev)
+        score = _empty(stream, (B, P_max), _F32, dev)
     if scored and score_hist is None:
-        score_hist = _empty(stream, (B, HIST_BINS), torch.int32, dev)
-    op = _take(out, torch.bfloat16, q.shape, dev, "out")
-    lp = None if logits is None else _take(logits, f32, (B, 2, Hq, P_max), dev, "logits")
-    pp = None if partial is None else _take(partial, f32, (B, Hkv, P_max), dev, "partial")
-    sp = None if score is None else _take(score, f32, (B, P_max), dev, "score")
-    hp = None if score_hist is None else \
-        _take(score_hist, torch.int32, (B, HIST_BINS), dev, "score_hist")
-    key = (B, Hq, Hkv, d, shape[2], width, shape[0])
-    geom = _quant_geom(*key)
-    keep, wp, wb = _workspace_of(
-        workspace, _quant_workspace_bytes(dev, "vsd_verify_quant_workspace_size", key, R, P_max),
-        stream, dev)
+        score_hist = _empty(stream, (B, HIST_BINS), _I32, dev)
+    if not (dq == d and _is(q, _BF16, q.numel(), 4, dev) and _is(out, _BF16, q.numel(), 4, dev) and
+            out.shape == q.shape and _is(block_table, _I32, B * width, 2, dev) and
+            _is(prefix_len, _I32, B, 1, dev) and
+            (logits is None or logits.shape == (B, 2, Hq, P_max) and _is(logits, _F32, logits.numel(), 4, dev)) and
+            (partial is None or partial.shape == (B, Hkv, P_max) and _is(partial, _F32, partial.numel(), 3, dev)) and
+            (score is None or score.shape == (B, P_max) and _is(score, _F32, score.numel(), 2, dev)) and
+            (score_hist is None or score_hist.shape == (B, HIST_BINS) and _is(score_hist, _I32, B * HIST_BINS, 2, dev))):
+        _refuse((q, _BF16, (B, R, Hq, d), dev, "q"), (out, _BF16, (B, R, Hq, d), dev, "out"),
+                (block_table, _I32, (B, width), dev, "block_table"),
+                (prefix_len, _I32, (B,), dev, "prefix_len"), (logits, _F32, (B, 2, Hq, P_max), dev, "logits"),
+                (partial, _F32, (B, Hkv, P_max), dev, "partial"), (score, _F32, (B, P_max), dev, "score"),
+                (score_hist, _I32, (B, HIST_BINS), dev, "score_hist"))
+    plan = _quant_plan("vsd_verify_quant_workspace_size", dev, R, P_max, B, Hq, Hkv, d, page, width, NB)
+    keep, wp, wb = _workspace_of(workspace, plan[2], stream, dev)
     _check((_lib or load()).vsd_verify_attn_collect_quant(
-        ctypes.addressof(geom), R, qp, kc, vc, ks, vs, bt, pl, row0, R - 1 if row1 is None else row1, P_max, scale,
-        lp, pp, sp, hp, n_sink, n_recent, op, wp, wb, _raw_stream(stream, dev)),
-        "vsd_verify_attn_collect_quant")
+        plan[1], R, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+        v_scale.data_ptr(), block_table.data_ptr(), prefix_len.data_ptr(), row0,
+        R - 1 if row1 is None else row1, P_max, scale, _address(logits), _address(partial),
+        _address(score), _address(score_hist), n_sink, n_recent, out.data_ptr(), wp, wb,
+        _raw_stream(stream, dev)), "vsd_verify_attn_collect_quant")
     return out, logits, partial, score, score_hist
 
 
-@_on_device
 def vsd_verify_attn_collect_quant(q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len,
                                   *, P_max: int, scale: float, row0: int = 0,
                                   row1: Optional[int] = None, logits=None, partial=None, out=None,
@@ -863,7 +877,6 @@ def vsd_verify_attn_collect_quant(q, k_cache, v_cache, k_scale, v_scale, block_t
                          stream, collect, False)[:3]
 
 
-@_on_device
 def vsd_verify_attn_collect_scored_quant(q, k_cache, v_cache, k_scale, v_scale, block_table,
                                          prefix_len, *, P_max: int, scale: float, row0: int = 0,
                                          row1: Optional[int] = None, logits=None, partial=None,
@@ -885,42 +898,42 @@ def vsd_sparse_quant_workspace_size(geom: Geom, k_max: int, max_tail: int) -> in
     return int(out.value)
 
 
-@_on_device
 def vsd_sparse_decode_attn_quant(q, k_cache, v_cache, k_scale, v_scale, block_table, idx, n_sel,
                                  tail_start, seq_len, *, scale: float, max_tail: int, out=None,
                                  workspace=None, stream=None):
     """Sparse draft-step attention over an 8-bit cache.  q: bf16 [B, Hq, d]; idx: int32
     [B, k_max] and n_sel: int32 [B], or both None.  Returns out."""
-    dev = _cuda_index(q, torch.bfloat16, "q")
-    shape, kc, vc, ks, vs = _take_quant_cache(k_cache, v_cache, k_scale, v_scale, dev)
-    if q.dim() != 3 or q.shape[2] != shape[3]:
-        raise ValueError("q must be [B, Hq, %d]" % shape[3])
-    B, Hq, d = q.shape
-    qp = _take(q, torch.bfloat16, None, dev, "q")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_blocks]")
-    width = block_table.shape[1]
-    bt = _take(block_table, torch.int32, (B, width), dev, "block_table")
-    t0 = _take(tail_start, torch.int32, (B,), dev, "tail_start")
-    t1 = _take(seq_len, torch.int32, (B,), dev, "seq_len")
+    dev = _cuda_index(q, _BF16, "q")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return vsd_sparse_decode_attn_quant(q, k_cache, v_cache, k_scale, v_scale, block_table, idx,
+                                                n_sel, tail_start, seq_len, scale=scale,
+                                                max_tail=max_tail, out=out, workspace=workspace,
+                                                stream=stream)
+    NB, Hkv, page, d = _cache_shape(k_cache, v_cache, k_scale, v_scale, dev)
+    if q.dim() != 3:
+        raise ValueError("q must be [B, Hq, d]")
+    B, Hq, dq = q.shape
+    width = block_table.shape[-1]
     if (idx is None) != (n_sel is None):
         raise ValueError("idx and n_sel go together")
-    k_max, ip, np_ = 0, None, None
-    if idx is not None:
-        if idx.dim() != 2:
-            raise ValueError("idx must be [B, k_max]")
-        k_max = idx.shape[1]
-        ip = _take(idx, torch.int32, (B, k_max), dev, "idx")
-        np_ = _take(n_sel, torch.int32, (B,), dev, "n_sel")
+    k_max = 0 if idx is None else idx.shape[-1]
     if out is None:
-        out = _empty(stream, q.shape, torch.bfloat16, dev)
-    op = _take(out, torch.bfloat16, q.shape, dev, "out")
-    key = (B, Hq, shape[1], d, shape[2], width, shape[0])
-    geom = _quant_geom(*key)
-    keep, wp, wb = _workspace_of(
-        workspace, _quant_workspace_bytes(dev, "vsd_sparse_quant_workspace_size", key, k_max,
-                                          int(max_tail)), stream, dev)
+        out = _empty(stream, q.shape, _BF16, dev)
+    if not (dq == d and _is(q, _BF16, q.numel(), 3, dev) and _is(out, _BF16, q.numel(), 3, dev) and
+            out.shape == q.shape and _is(block_table, _I32, B * width, 2, dev) and
+            _is(tail_start, _I32, B, 1, dev) and _is(seq_len, _I32, B, 1, dev) and
+            (idx is None or _is(idx, _I32, B * k_max, 2, dev) and _is(n_sel, _I32, B, 1, dev))):
+        _refuse((q, _BF16, (B, Hq, d), dev, "q"), (out, _BF16, (B, Hq, d), dev, "out"),
+                (block_table, _I32, (B, width), dev, "block_table"),
+                (tail_start, _I32, (B,), dev, "tail_start"), (seq_len, _I32, (B,), dev, "seq_len"),
+                (idx, _I32, (B, k_max), dev, "idx"), (n_sel, _I32, (B,), dev, "n_sel"))
+    plan = _quant_plan("vsd_sparse_quant_workspace_size", dev, k_max, max_tail, B, Hq, Hkv, d, page,
+                       width, NB)
+    keep, wp, wb = _workspace_of(workspace, plan[2], stream, dev)
     _check((_lib or load()).vsd_sparse_decode_attn_quant(
-        ctypes.addressof(geom), qp, kc, vc, ks, vs, bt, ip, np_, k_max, t0, t1, max_tail, scale, op, wp, wb,
+        plan[1], q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+        v_scale.data_ptr(), block_table.data_ptr(), _address(idx), _address(n_sel), k_max,
+        tail_start.data_ptr(), seq_len.data_ptr(), max_tail, scale, out.data_ptr(), wp, wb,
         _raw_stream(stream, dev)), "vsd_sparse_decode_attn_quant")
     return out

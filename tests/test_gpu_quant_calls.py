@@ -181,6 +181,8 @@ def test_binding_refuses_mismatched_tensors(vsd):
         ((q, kc, vc, ks, vs.cpu(), bt, pl), ok),
         ((q, kc, vc, ks[:-1], vs, bt, pl), ok),
         ((q, kc, vc[:-1], ks, vs, bt, pl), ok),
+        ((q, kc, vc, ks.t().contiguous(), vs, bt, pl), ok),
+        ((q, kc, vc, ks, vs.t(), bt, pl), ok),
         ((q, kc.view(torch.uint8), vc, ks, vs, bt, pl), ok),
         ((q.transpose(1, 2), kc, vc, ks, vs, bt, pl), ok),
         ((q, kc, vc, ks, vs, bt, pl.long()), ok),
