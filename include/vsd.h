@@ -569,8 +569,8 @@ vsd_status vsd_advance_lengths(int B, int gamma, const int32_t* accepted, int ma
  * two (at least 2^-126) with a <= 448 s:
  *   - a page whose slot 0 is written by the call takes the scale s;
  *   - otherwise the slots before the first written one hold earlier rows: the page keeps
- *     its scale if a <= 448 scale, else it takes s and those rows' codes become
- *     e4m3(code * (scale / s)) (exact but for codes that fall below 2^-6);
+ *     its scale if that is not 0 and a <= 448 scale, else it takes s and those rows' codes
+ *     become e4m3(code * (scale / s)) (exact but for codes that fall below 2^-6);
  *   - the new codes are e4m3(x / scale), rounded to nearest even; NaN and infinities
  *     become NaN.
  * Slots behind the last written one keep their codes: like rows behind a sequence's end

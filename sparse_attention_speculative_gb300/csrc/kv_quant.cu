@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kRowThreads) append_kv_quant_kernel(const Rows
   }
   const float amax = __uint_as_float(top << 16);
   float now = page_scale(amax);
-  if (s0 > 0 && amax <= was * kE4M3Max) now = was;
+  if (s0 > 0 && was != 0.f && amax <= was * kE4M3Max) now = was;
   // codes = x / now; by a power of two (any scale stored here; not every caller's own) the
   // product with its reciprocal is the same number
   const bool pow2 = (__float_as_uint(now) & 0x007FFFFFu) == 0u && now >= 0x1p-126f;

@@ -74,7 +74,7 @@ def append(codes, scales, rows, table, pos, valid):
                     was = float(scales[blk, g])
                     if s0 > 0:
                         # the comparison is in fp32, as the scale is
-                        keep = torch.tensor(amax, dtype=torch.float32) <= \
+                        keep = was != 0 and torch.tensor(amax, dtype=torch.float32) <= \
                             scales[blk, g] * torch.tensor(448.0)
                         if bool(keep):
                             s = was

@@ -68,6 +68,20 @@ def test_append_over_scales_that_are_no_powers_of_two(vsd):
         _check_append(vsd, cache, rows, [50, 61], [5, 5], 5, pos_offset=-1, pass_valid=False)
 
 
+@pytest.mark.parametrize("mag", [0.0, 0.3])
+def test_append_into_a_page_of_scale_zero(vsd, mag):
+    """Earlier rows with scale 0 (a caller's own page of zeros): a scale of 0 cannot hold
+    the new rows, zeros among them; the earlier rows stay zeros."""
+    cache = ref.Cache([40, 40], 2, 64, seed=12)
+    for b in range(2):
+        blk = int(cache.table[b, 1])
+        cache.scales[0][blk] = 0.0
+        cache.scales[1][blk] = 0.0
+    g = torch.Generator().manual_seed(7)
+    rows = [(torch.randn((2, 3, 2, 64), generator=g) * mag).bfloat16() for _ in range(2)]
+    _check_append(vsd, cache, rows, [20, 31], [3, 1], 3)
+
+
 def test_append_extreme_values(vsd):
     """Zero rows, subnormal and largest bf16 values, values at the border of a scale,
     NaN and infinities (which do not set the scale)."""
