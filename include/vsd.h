@@ -607,13 +607,16 @@ vsd_status vsd_read_kv_quant(const vsd_geom* geom, int n, const void* k_cache,
  * attention of single tokens).  vsd_verify_attn_collect with K and V as above:
  *   z[b,t,h,j] = scale * k_scale[page(j), g] * <q[b,t,h,:], k_code[b,j,g,:]>
  *   out[b,t,h,:] = sum_j softmax_j(z[b,t,h,:]) * v_scale[page(j), g] * v_code[b,j,g,:]
- * logits, partial_scores, the collected rows, prefix_len and every rule as there; scales
- * are finite and not negative (what vsd_append_kv_quant writes, or a caller's own).
+ * logits, partial_scores, the collected rows, prefix_len and every rule as there.  Scales
+ * are finite and not negative (what vsd_append_kv_quant writes, or a caller's own); value
+ * scales below 2^-80 count as 2^-80, and those that one row attends to lie within 2^120
+ * of each other then.  A query row that holds a NaN or an infinity gives NaN.
  *   score, score_hist  both or neither: as vsd_verify_attn_collect_scored (partial_scores
  *                      is then required), for vsd_select_topk_scored with n_sink, n_recent
  *   workspace  >= vsd_verify_quant_workspace_size(...) bytes, 256-byte aligned; contents
  *              ignored on entry
- * Supported: as vsd_verify_attn_collect.
+ * Supported: as vsd_verify_attn_collect, with P_max up to 2^30 and
+ *            B * Hkv * (P_max / 128 + 10) below 2^31.
  * ------------------------------------------------------------------------------ */
 vsd_status vsd_verify_quant_workspace_size(const vsd_geom* geom, int R, int P_max,
                                            size_t* bytes);
@@ -630,7 +633,10 @@ vsd_status vsd_verify_attn_collect_quant(const vsd_geom* geom, int R, const void
 
 /* ------------------------------------------------------------------------------
  * Sparse draft-step attention over the 8-bit cache: vsd_sparse_decode_attn with K and V
- * as above.  idx, n_sel, tail_start, seq_len, max_tail and every rule as there.
+ * as above.  idx, n_sel, tail_start, seq_len, max_tail and every rule as there; a list
+ * longer than k_max + max_tail is flagged VSD_DEV_BAD_LENGTH (output zeros).  Supported:
+ * Hq/Hkv up to 16, B and Hkv up to 65535, k_max + max_tail up to 2^30 and fewer than 2^31
+ * rows (num_blocks * Hkv * page_size) in the cache.
  *   workspace  >= vsd_sparse_quant_workspace_size(...) bytes, 256-byte aligned (0 bytes:
  *              may be NULL); contents ignored on entry (no counters to keep zero)
  * ------------------------------------------------------------------------------ */

@@ -79,7 +79,10 @@ __device__ __forceinline__ void query_parts(float a, float b, float f, uint32_t&
 // small ones need.
 constexpr float kTopX = 15.f;    // log2 of the largest x
 constexpr float kRaisedX = 2.f;  // log2 of the largest x after a change of r
-constexpr float kMinVScale = 0x1p-100f;  // value scales below count as this
+//
+// Value scales below 2^-80 count as 2^-80 (a page of zeros has 2^-126): x / vs stays at most
+// 2^95, and a sum over 2^30 keys below the 2^126 where fp32 quotients end.
+constexpr float kMinVScale = 0x1p-80f;
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);

@@ -284,6 +284,31 @@ def test_verify_one_loud_key_over_many_quiet_ones(vsd):
         check_verify(vsd, cache, [P], 1, d, 1, P_max=P, q=q, scale=1.0)
 
 
+def test_verify_zero_values_with_tiny_scales_before_ordinary_ones(vsd):
+    """3.2 million keys whose values are zeros with the smallest scale that storing rows
+    writes, their logits 9 above the first ones', then a thousand ordinary keys: the sums
+    of the former's probabilities stay finite in every part of the sequence."""
+    d, P, tail = 64, 3200000, 1000
+    one = ref.encode(torch.tensor([1.0], dtype=torch.float64))[0]
+    codes = torch.zeros((2, 3, 1, 16, d), dtype=torch.uint8)  # K and V of three pages
+    codes[0, 1:, 0, :, 0] = one
+    codes[1, 2] = one
+    scales = torch.tensor([[1.0, 1.0, 1.0], [2.0 ** -126, 2.0 ** -126, 1.0]])[..., None].contiguous()
+    table = torch.ones((1, P // 16 + 1), dtype=torch.int32)
+    table[0, :8] = 0
+    table[0, (P - tail) // 16:] = 2
+    n = P + 1 - (P - tail) // 16 * 16  # keys of the last page
+    q = torch.zeros((1, 1, 1, d)).bfloat16()
+    q[..., 0] = 9.0
+    kc, vc = (codes[i].cuda().view(torch.float8_e4m3fn) for i in range(2))
+    out = vsd.vsd_verify_attn_collect_quant(
+        q.cuda(), kc, vc, scales[0].cuda(), scales[1].cuda(), table.cuda(),
+        torch.tensor([P], dtype=torch.int32, device="cuda"), P_max=P, scale=1.0, collect=False)[0]
+    assert vsd.vsd_read_device_status() == 0
+    want = torch.tensor(n / (P + 1 - 128 + 128 * math.exp(-9.0)), dtype=torch.float64)
+    assert torch.all((out.cpu().double() - want).abs() <= ref.out_bound(want, want))
+
+
 def test_verify_query_ranges(vsd):
     """Queries whose dimensions differ by 2^14, zero queries and the largest bf16 values'
     binade: the two parts a query is split into hold it."""
