@@ -729,11 +729,28 @@ def _quant_plan(call: str, dev: int, x: int, y: int, B: int, Hq: int, Hkv: int, 
     return geom, ctypes.addressof(geom), int(nbytes.value)
 
 
+# Scratch of the current streams' eager calls, by (device, stream): (tensor, address, bytes).
+# The calls of one stream run one after the other and ignore what it holds, so one buffer
+# serves them all (an allocation between two launches takes 6 us).
+_stream_scratch = {}
+_PER_THREAD_STREAM = 2  # cudaStreamPerThread: one handle for a stream of every host thread
+
+
 def _workspace_of(workspace, nbytes: int, stream, dev: int):
-    """(the tensor that keeps it alive, address, bytes) of a call's scratch."""
+    """(the tensor that keeps it alive, address, bytes) of a call's scratch.  A captured call,
+    and one that names its stream, gets memory of its own."""
     if workspace is None:
         if nbytes == 0:
             return None, None, 0
+        if stream is None:
+            raw = torch._C._cuda_getCurrentRawStream(dev)
+            if raw != _PER_THREAD_STREAM and not torch._C._cuda_isCurrentStreamCapturing():
+                kept = _stream_scratch.get((dev, raw))
+                if kept is None or kept[2] < nbytes:
+                    # (the smaller one goes back to the allocator in stream order)
+                    new = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+                    kept = _stream_scratch[(dev, raw)] = (new, new.data_ptr(), nbytes)
+                return kept
         workspace = _empty(stream, nbytes, torch.uint8, dev)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on the call's device")

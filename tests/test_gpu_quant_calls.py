@@ -99,6 +99,41 @@ def test_calls_on_two_streams_at_once(vsd):
     assert vsd.vsd_read_device_status() == 0
 
 
+def test_calls_of_growing_and_shrinking_sizes_on_two_streams(vsd):
+    """Calls without a workspace of their own, small and large in turn and on two streams,
+    give the bits of calls with one."""
+    def sizes():
+        for B, P in ((1, 300), (3, 2000), (1, 300), (2, 5000), (3, 2000)):
+            cache = ref.Cache([P + 4] * B, 2, 64, seed=B * 31 + P)
+            q = torch.randn((B, 4, 8, 64), generator=cache.gen).bfloat16().cuda()
+            yield cache.cuda(), q, i32([P] * B), P
+
+    own = [torch.empty(1 << 25, dtype=torch.uint8, device="cuda")]
+    calls = list(sizes())
+
+    def run(x, **kw):
+        (kc, vc, ks, vs, bt), q, pl, P = x
+        idx = torch.arange(0, P, 3, dtype=torch.int32, device="cuda").repeat(q.shape[0], 1)
+        n = i32([idx.shape[1]] * q.shape[0])
+        return (vsd.vsd_verify_attn_collect_quant(q, kc, vc, ks, vs, bt, pl, P_max=P, scale=0.125, **kw) +
+                (vsd.vsd_sparse_decode_attn_quant(q[:, 0].contiguous(), kc, vc, ks, vs, bt, idx, n, pl, pl + 1,
+                                                  scale=0.125, max_tail=1, **kw),))
+
+    want = [run(x, workspace=own[0]) for x in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for x in calls + calls[::-1]:
+        for s, g in zip(streams, got):
+            with torch.cuda.stream(s):
+                g.append(run(x))
+    torch.cuda.synchronize()
+    assert vsd.vsd_read_device_status() == 0
+    for g in got:
+        for a, b in zip(g, want + want[::-1]):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 def test_captured_graphs_replayed_together(vsd):
     alone = [[x.clone() for x in _calls(vsd, s)()] for s in (54, 55)]
     graphs, outs = [], []
