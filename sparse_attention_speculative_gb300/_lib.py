@@ -7,7 +7,6 @@ missing the calls raise immediately; there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import threading
 from typing import Optional, Tuple
@@ -647,131 +646,31 @@ def vsd_sparse_decode_attn_step(q, k_cache, v_cache, block_table, idx, n_sel, ta
 
 
 # ------------------------------------------------------------------ 8-bit cache
-# These calls are made once per layer and step, so their checks are one comparison per
-# property and tensor on the way through; _refuse says afterwards what was wrong.
-_F8, _BF16, _F32, _I32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32
+# The checks, outputs and scratch of these calls are in csrc/binding.cpp: they are made once
+# per layer and step, and their small ones run for a few microseconds on the GPU.
+_binding = None
 
 
-def _refuse(*wanted) -> None:
-    """Raise what is wrong with the first of (tensor, dtype, shape, device, name) that is
-    not as wanted."""
-    for t, dtype, shape, dev, name in wanted:
-        if t is None:
-            continue
-        _need(t, dtype, name)
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-        if t.get_device() != dev:
-            raise ValueError("%s is on another device" % name)
-    raise ValueError("tensors do not fit together")
+def _bound():
+    """The extension module of the calls below, with the library's addresses."""
+    global _binding
+    lib = load()
+    try:
+        from . import _binding as module
+    except ImportError as e:
+        raise RuntimeError("_binding.so is not built or does not fit this torch; run "
+                           "`python -m sparse_attention_speculative_gb300.build`") from e
+    module.attach(VsdError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.vsd_append_kv_quant, lib.vsd_read_kv_quant, lib.vsd_verify_quant_workspace_size,
+        lib.vsd_verify_attn_collect_quant, lib.vsd_sparse_quant_workspace_size,
+        lib.vsd_sparse_decode_attn_quant)))
+    _binding = module
+    return module
 
 
-def _cuda_index(t, dtype, name: str) -> int:
-    """The device of a call's first tensor."""
-    dev = t.get_device()
-    if dev < 0:
-        _need(t, dtype, name)
-    return dev
-
-
-def _is(t, dtype, numel: int, dim: int, dev: int) -> bool:
-    return t.dtype is dtype and t.numel() == numel and t.dim() == dim and \
-        t.get_device() == dev and t.is_contiguous()
-
-
-def _cache_shape(k_cache, v_cache, k_scale, v_scale, dev):
-    """The shape (num_blocks, Hkv, 16, d) of an 8-bit cache: float8_e4m3fn codes and
-    float32 scales [num_blocks, Hkv] on device `dev`."""
-    shape = k_cache.shape
-    if len(shape) == 4:
-        n = shape[0] * shape[1]
-        if k_cache.dtype is _F8 and v_cache.dtype is _F8 and v_cache.shape == shape and \
-                k_cache.is_contiguous() and v_cache.is_contiguous() and \
-                k_cache.get_device() == dev and v_cache.get_device() == dev and \
-                k_scale.shape == v_scale.shape == shape[:2] and \
-                _is(k_scale, _F32, n, 2, dev) and _is(v_scale, _F32, n, 2, dev):
-            return shape
-    _refuse((k_cache, _F8, shape if len(shape) == 4 else ("num_blocks", "Hkv", 16, "d"), dev, "k_cache"),
-            (v_cache, _F8, shape, dev, "v_cache"), (k_scale, _F32, shape[:2], dev, "k_scale"),
-            (v_scale, _F32, shape[:2], dev, "v_scale"))
-
-
-def _elsewhere(dev: int) -> bool:
-    """Whether a call's tensors are on another device than the current one (the library
-    launches on the current device)."""
-    return dev >= 0 and dev != torch._C._cuda_getDevice()
-
-
-def _empty(stream, shape, dtype, dev, make=torch.empty):
-    """What a call allocates (outputs, its scratch) comes from torch's allocator tied to
-    the stream that the call runs on: calls on other streams, and captured graphs, get
-    memory of their own, and it goes back in stream order."""
-    if stream is None:
-        return make(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(stream):
-        return make(shape, dtype=dtype, device=dev)
-
-
-def _raw_stream(stream, dev: int) -> int:
-    """The cudaStream_t of a call (torch's own accessor: a Stream object costs 3 us)."""
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-@functools.lru_cache(maxsize=512)
-def _quant_plan(call: str, dev: int, x: int, y: int, B: int, Hq: int, Hkv: int, d: int, page: int,
-                max_blocks: int, num_blocks: int):
-    """(geometry, its address, workspace bytes) of a call, kept for the next one of the same
-    shape.  `call` names the size query, "" for calls without a workspace."""
-    geom = Geom(B, Hq, Hkv, d, page, max_blocks, num_blocks)
-    nbytes = ctypes.c_size_t(0)
-    if call:
-        _check(getattr(load(), call)(ctypes.addressof(geom), x, y, ctypes.byref(nbytes)), call)
-    return geom, ctypes.addressof(geom), int(nbytes.value)
-
-
-# Scratch of the current streams' eager calls, by (device, stream): (tensor, address, bytes).
-# The calls of one stream run one after the other and ignore what it holds, so one buffer
-# serves them all (an allocation between two launches takes 6 us).
-_stream_scratch = {}
-_PER_THREAD_STREAM = 2  # cudaStreamPerThread: one handle for a stream of every host thread
-
-
-def _workspace_of(workspace, nbytes: int, stream, dev: int):
-    """(the tensor that keeps it alive, address, bytes) of a call's scratch.  A captured call,
-    and one that names its stream, gets memory of its own."""
-    if workspace is None:
-        if nbytes == 0:
-            return None, None, 0
-        if stream is None:
-            raw = torch._C._cuda_getCurrentRawStream(dev)
-            if raw != _PER_THREAD_STREAM and not torch._C._cuda_isCurrentStreamCapturing():
-                kept = _stream_scratch.get((dev, raw))
-                if kept is None or kept[2] < nbytes:
-                    # (the smaller one goes back to the allocator in stream order)
-                    new = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-                    kept = _stream_scratch[(dev, raw)] = (new, new.data_ptr(), nbytes)
-                return kept
-        workspace = _empty(stream, nbytes, torch.uint8, dev)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous and on the call's device")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
-def _rows_plan(k_rows, v_rows, names, k_cache, v_cache, k_scale, v_scale, block_table, pos_base,
-               n_valid, dev):
-    """The checks that storing and reading rows share, and the geometry."""
-    NB, Hkv, page, d = _cache_shape(k_cache, v_cache, k_scale, v_scale, dev)
-    rows = k_rows.shape
-    B, width = rows[0], block_table.shape[-1]
-    if not (len(rows) == 4 and rows[2] == Hkv and rows[3] == d and
-            _is(k_rows, _BF16, k_rows.numel(), 4, dev) and _is(v_rows, _BF16, k_rows.numel(), 4, dev) and
-            v_rows.shape == rows and _is(block_table, _I32, B * width, 2, dev) and
-            _is(pos_base, _I32, B, 1, dev) and (n_valid is None or _is(n_valid, _I32, B, 1, dev))):
-        want = (B, rows[1] if len(rows) == 4 else "n", Hkv, d)
-        _refuse((k_rows, _BF16, want, dev, names[0]), (v_rows, _BF16, want, dev, names[1]),
-                (block_table, _I32, (B, width), dev, "block_table"), (pos_base, _I32, (B,), dev, "pos_base"),
-                (n_valid, _I32, (B,), dev, "n_valid"))
-    return _quant_plan("", dev, 0, 0, B, Hkv, Hkv, d, page, width, NB)
+def _handle(stream):
+    """The cudaStream_t of a stream, None for the current one."""
+    return None if stream is None else stream.cuda_stream
 
 
 def vsd_append_kv_quant(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, pos_base, *,
@@ -781,18 +680,8 @@ def vsd_append_kv_quant(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_
     (float8_e4m3fn [num_blocks, Hkv, 16, d], scales float32 [num_blocks, Hkv]).  Rows are
     appended in order: a page whose slot 0 is written starts afresh, otherwise its earlier
     rows are kept (requantised when its scale has to grow)."""
-    dev = _cuda_index(k_new, _BF16, "k_new")
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return vsd_append_kv_quant(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table,
-                                       pos_base, pos_offset=pos_offset, n_valid=n_valid, stream=stream)
-    geom = _rows_plan(k_new, v_new, ("k_new", "v_new"), k_cache, v_cache, k_scale, v_scale, block_table,
-                      pos_base, n_valid, dev)
-    _check((_lib or load()).vsd_append_kv_quant(
-        geom[1], k_new.shape[1], k_new.data_ptr(), v_new.data_ptr(), block_table.data_ptr(),
-        pos_base.data_ptr(), pos_offset, None if n_valid is None else n_valid.data_ptr(),
-        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-        _raw_stream(stream, dev)), "vsd_append_kv_quant")
+    (_binding or _bound()).append(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table,
+                                  pos_base, pos_offset, n_valid, _handle(stream))
 
 
 def vsd_read_kv_quant(k_cache, v_cache, k_scale, v_scale, block_table, pos_base, *, n: int,
@@ -800,27 +689,8 @@ def vsd_read_kv_quant(k_cache, v_cache, k_scale, v_scale, block_table, pos_base,
     """The rows at positions pos_base[b] + pos_offset + t, t < n_valid[b] (None: n), of an
     8-bit cache as bf16 [B, n, Hkv, d].  Rows behind n_valid are left as they were in
     k_out, v_out (zeros when allocated here).  Returns (k_out, v_out)."""
-    dev = _cuda_index(k_cache, _F8, "k_cache")
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return vsd_read_kv_quant(k_cache, v_cache, k_scale, v_scale, block_table, pos_base, n=n,
-                                     pos_offset=pos_offset, n_valid=n_valid, k_out=k_out, v_out=v_out,
-                                     stream=stream)
-    if k_out is None or v_out is None:
-        shape = (pos_base.shape[0], n, k_cache.shape[1], k_cache.shape[-1])
-        make = torch.empty if n_valid is None else torch.zeros
-        k_out = _empty(stream, shape, _BF16, dev, make) if k_out is None else k_out
-        v_out = _empty(stream, shape, _BF16, dev, make) if v_out is None else v_out
-    geom = _rows_plan(k_out, v_out, ("k_out", "v_out"), k_cache, v_cache, k_scale, v_scale, block_table,
-                      pos_base, n_valid, dev)
-    if k_out.shape[1] != n:
-        raise ValueError("k_out and v_out must be [B, n, Hkv, d]")
-    _check((_lib or load()).vsd_read_kv_quant(
-        geom[1], n, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-        block_table.data_ptr(), pos_base.data_ptr(), pos_offset,
-        None if n_valid is None else n_valid.data_ptr(), k_out.data_ptr(), v_out.data_ptr(),
-        _raw_stream(stream, dev)), "vsd_read_kv_quant")
-    return k_out, v_out
+    return (_binding or _bound()).read(k_cache, v_cache, k_scale, v_scale, block_table, pos_base,
+                                       n, pos_offset, n_valid, k_out, v_out, _handle(stream))
 
 
 def vsd_verify_quant_workspace_size(geom: Geom, R: int, P_max: int) -> int:
@@ -831,57 +701,6 @@ def vsd_verify_quant_workspace_size(geom: Geom, R: int, P_max: int) -> int:
     return int(out.value)
 
 
-def _address(t):
-    return None if t is None else t.data_ptr()
-
-
-def _verify_quant(q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, P_max, scale,
-                  row0, row1, logits, partial, score, score_hist, n_sink, n_recent, out,
-                  workspace, stream, collect, scored):
-    dev = _cuda_index(q, _BF16, "q")
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return _verify_quant(q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, P_max,
-                                 scale, row0, row1, logits, partial, score, score_hist, n_sink,
-                                 n_recent, out, workspace, stream, collect, scored)
-    NB, Hkv, page, d = _cache_shape(k_cache, v_cache, k_scale, v_scale, dev)
-    if q.dim() != 4:
-        raise ValueError("q must be [B, R, Hq, d]")
-    B, R, Hq, dq = q.shape
-    width = block_table.shape[-1]
-    if out is None:
-        out = _empty(stream, q.shape, _BF16, dev)
-    if collect and logits is None:
-        logits = _empty(stream, (B, 2, Hq, P_max), _F32, dev)
-    if (collect or scored) and partial is None:
-        partial = _empty(stream, (B, Hkv, P_max), _F32, dev)
-    if scored and score is None:
-        score = _empty(stream, (B, P_max), _F32, dev)
-    if scored and score_hist is None:
-        score_hist = _empty(stream, (B, HIST_BINS), _I32, dev)
-    if not (dq == d and _is(q, _BF16, q.numel(), 4, dev) and _is(out, _BF16, q.numel(), 4, dev) and
-            out.shape == q.shape and _is(block_table, _I32, B * width, 2, dev) and
-            _is(prefix_len, _I32, B, 1, dev) and
-            (logits is None or logits.shape == (B, 2, Hq, P_max) and _is(logits, _F32, logits.numel(), 4, dev)) and
-            (partial is None or partial.shape == (B, Hkv, P_max) and _is(partial, _F32, partial.numel(), 3, dev)) and
-            (score is None or score.shape == (B, P_max) and _is(score, _F32, score.numel(), 2, dev)) and
-            (score_hist is None or score_hist.shape == (B, HIST_BINS) and _is(score_hist, _I32, B * HIST_BINS, 2, dev))):
-        _refuse((q, _BF16, (B, R, Hq, d), dev, "q"), (out, _BF16, (B, R, Hq, d), dev, "out"),
-                (block_table, _I32, (B, width), dev, "block_table"),
-                (prefix_len, _I32, (B,), dev, "prefix_len"), (logits, _F32, (B, 2, Hq, P_max), dev, "logits"),
-                (partial, _F32, (B, Hkv, P_max), dev, "partial"), (score, _F32, (B, P_max), dev, "score"),
-                (score_hist, _I32, (B, HIST_BINS), dev, "score_hist"))
-    plan = _quant_plan("vsd_verify_quant_workspace_size", dev, R, P_max, B, Hq, Hkv, d, page, width, NB)
-    keep, wp, wb = _workspace_of(workspace, plan[2], stream, dev)
-    _check((_lib or load()).vsd_verify_attn_collect_quant(
-        plan[1], R, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-        v_scale.data_ptr(), block_table.data_ptr(), prefix_len.data_ptr(), row0,
-        R - 1 if row1 is None else row1, P_max, scale, _address(logits), _address(partial),
-        _address(score), _address(score_hist), n_sink, n_recent, out.data_ptr(), wp, wb,
-        _raw_stream(stream, dev)), "vsd_verify_attn_collect_quant")
-    return out, logits, partial, score, score_hist
-
-
 def vsd_verify_attn_collect_quant(q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len,
                                   *, P_max: int, scale: float, row0: int = 0,
                                   row1: Optional[int] = None, logits=None, partial=None, out=None,
@@ -889,9 +708,10 @@ def vsd_verify_attn_collect_quant(q, k_cache, v_cache, k_scale, v_scale, block_t
     """Verification attention + Collect-2-Query over an 8-bit cache (float8_e4m3fn
     [num_blocks, Hkv, 16, d] with scales float32 [num_blocks, Hkv]); with R = 1 the
     attention of single tokens.  Returns (out, logits, partial)."""
-    return _verify_quant(q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, P_max,
-                         scale, row0, row1, logits, partial, None, None, 0, 0, out, workspace,
-                         stream, collect, False)[:3]
+    return (_binding or _bound()).verify(q, k_cache, v_cache, k_scale, v_scale, block_table,
+                                         prefix_len, P_max, scale, row0, row1, logits, partial,
+                                         None, None, 0, 0, out, workspace, _handle(stream),
+                                         collect, False)[:3]
 
 
 def vsd_verify_attn_collect_scored_quant(q, k_cache, v_cache, k_scale, v_scale, block_table,
@@ -902,9 +722,10 @@ def vsd_verify_attn_collect_scored_quant(q, k_cache, v_cache, k_scale, v_scale, 
     """vsd_verify_attn_collect_quant that also writes the aggregated score and its
     histogram for vsd_select_topk_scored (logits are written when given).  Returns (out,
     logits, partial, score, score_hist)."""
-    return _verify_quant(q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, P_max,
-                         scale, row0, row1, logits, partial, score, score_hist, n_sink, n_recent,
-                         out, workspace, stream, False, True)
+    return (_binding or _bound()).verify(q, k_cache, v_cache, k_scale, v_scale, block_table,
+                                         prefix_len, P_max, scale, row0, row1, logits, partial,
+                                         score, score_hist, n_sink, n_recent, out, workspace,
+                                         _handle(stream), False, True)
 
 
 def vsd_sparse_quant_workspace_size(geom: Geom, k_max: int, max_tail: int) -> int:
@@ -920,37 +741,6 @@ def vsd_sparse_decode_attn_quant(q, k_cache, v_cache, k_scale, v_scale, block_ta
                                  workspace=None, stream=None):
     """Sparse draft-step attention over an 8-bit cache.  q: bf16 [B, Hq, d]; idx: int32
     [B, k_max] and n_sel: int32 [B], or both None.  Returns out."""
-    dev = _cuda_index(q, _BF16, "q")
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return vsd_sparse_decode_attn_quant(q, k_cache, v_cache, k_scale, v_scale, block_table, idx,
-                                                n_sel, tail_start, seq_len, scale=scale,
-                                                max_tail=max_tail, out=out, workspace=workspace,
-                                                stream=stream)
-    NB, Hkv, page, d = _cache_shape(k_cache, v_cache, k_scale, v_scale, dev)
-    if q.dim() != 3:
-        raise ValueError("q must be [B, Hq, d]")
-    B, Hq, dq = q.shape
-    width = block_table.shape[-1]
-    if (idx is None) != (n_sel is None):
-        raise ValueError("idx and n_sel go together")
-    k_max = 0 if idx is None else idx.shape[-1]
-    if out is None:
-        out = _empty(stream, q.shape, _BF16, dev)
-    if not (dq == d and _is(q, _BF16, q.numel(), 3, dev) and _is(out, _BF16, q.numel(), 3, dev) and
-            out.shape == q.shape and _is(block_table, _I32, B * width, 2, dev) and
-            _is(tail_start, _I32, B, 1, dev) and _is(seq_len, _I32, B, 1, dev) and
-            (idx is None or _is(idx, _I32, B * k_max, 2, dev) and _is(n_sel, _I32, B, 1, dev))):
-        _refuse((q, _BF16, (B, Hq, d), dev, "q"), (out, _BF16, (B, Hq, d), dev, "out"),
-                (block_table, _I32, (B, width), dev, "block_table"),
-                (tail_start, _I32, (B,), dev, "tail_start"), (seq_len, _I32, (B,), dev, "seq_len"),
-                (idx, _I32, (B, k_max), dev, "idx"), (n_sel, _I32, (B,), dev, "n_sel"))
-    plan = _quant_plan("vsd_sparse_quant_workspace_size", dev, k_max, max_tail, B, Hq, Hkv, d, page,
-                       width, NB)
-    keep, wp, wb = _workspace_of(workspace, plan[2], stream, dev)
-    _check((_lib or load()).vsd_sparse_decode_attn_quant(
-        plan[1], q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-        v_scale.data_ptr(), block_table.data_ptr(), _address(idx), _address(n_sel), k_max,
-        tail_start.data_ptr(), seq_len.data_ptr(), max_tail, scale, out.data_ptr(), wp, wb,
-        _raw_stream(stream, dev)), "vsd_sparse_decode_attn_quant")
-    return out
+    return (_binding or _bound()).sparse(q, k_cache, v_cache, k_scale, v_scale, block_table, idx,
+                                         n_sel, tail_start, seq_len, scale, max_tail, out,
+                                         workspace, _handle(stream))

@@ -2,6 +2,8 @@
 
 Each translation unit under ``csrc/`` is compiled in parallel with nvcc, then linked
 into ``libvsd.so`` next to this file.  Objects go to ``_build/`` (not committed).
+``csrc/binding.cpp``, the Python calls of the 8-bit cache, becomes the extension module
+``_binding.so`` beside it.
 """
 from __future__ import annotations
 
@@ -10,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +20,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libvsd.so")
+BINDING = os.path.join(PKG, "_binding.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 HEADER = os.path.join(ROOT, "include", "vsd.h")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -40,20 +45,44 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        glob.glob(os.path.join(CSRC, "*.h")) + [HEADER, os.path.abspath(__file__)]
+        glob.glob(os.path.join(CSRC, "*.h")) + [BINDING_SRC, HEADER, os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def build_binding() -> str:
+    """Compile csrc/binding.cpp against the installed torch; returns the module's path."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    include = [os.path.join(root, "include"),
+               os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"],
+               os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    tmp = BINDING + ".%d.tmp" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI]
+    for p in include:
+        cmd += ["-isystem", p]
+    cmd += [BINDING_SRC, "-o", tmp, "-L" + os.path.join(root, "lib"), "-ltorch_python",
+            "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            "-L" + os.path.join(os.path.dirname(os.path.dirname(nvcc())), "lib64"), "-lcudart"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), out: str = None,
           objdir: str = None) -> str:
-    """Compile and link libvsd.so; returns its path.  `out` / `objdir` build a separate
-    copy (e.g. with other -D settings in `extra_flags`) without touching the main one."""
+    """Compile and link libvsd.so, and the binding beside it; returns the library's path.
+    `out` / `objdir` build a separate copy of the library (e.g. with other -D settings in
+    `extra_flags`) without touching the main one."""
     if out is None and not force and up_to_date():
         return LIB
     lib_path = out or LIB
@@ -73,7 +102,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), out: str =
 
     srcs = _sources()
     with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+        binding = ex.submit(build_binding) if out is None else None
         objs = list(ex.map(compile_one, srcs))
+        if binding is not None:
+            binding.result()
     tmp = lib_path + ".%d.tmp" % os.getpid()
     cmd = [cc] + ARCH + ["-shared", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
