@@ -2,7 +2,8 @@
 
 The hot path is three C-ABI calls of ``libvsd.so`` (see ``include/vsd.h``):
 verification attention with Collect-2-Query, protected top-k selection over the
-aggregated logits, and the sparse draft-step attention.  This package holds the
+aggregated logits, and the sparse draft-step attention; the ``_quant`` calls do the same
+over an 8-bit cache.  This package holds the
 CUDA sources (``csrc/``), the in-tree build (``build.py``), the ctypes binding
 (``_lib.py``), one decode iteration as a CUDA graph (``iteration.py``), decode
 iterations over a multi-layer stack with the cache appends and prefix growth on the

@@ -27,10 +27,16 @@
 //     clear what no row may see.
 //   * warps 8-15 and 16-23 are two softmax groups on alternate tiles, each with its own
 //     references, P^T buffer and accumulator O^T; they meet at the end of a pair.  They
-//     also write the collected logits, each half of a group's threads one row.  A tile is a chain of some 2000 cycles (wait, TMEM load,
-//     vote, exponentials, store) against 1400 for its bytes from HBM: one group of eight
-//     warps was bound by that chain (368 us for the batch of 16 x 32K, 72B geometry),
-//     two overlap it.
+//     also write the collected logits, each half of a group's threads one row.  A tile is a
+//     chain (wait, TMEM load, vote, exponentials, store) longer than its bytes take from
+//     HBM: one group of eight warps was bound by it (368 us for 16 sequences of 32K and 48
+//     columns; two groups 345), and writing the logits by the widening warps was slower.
+//
+// Measured: 28 us for the 32K layer (32 columns, 77 MB: 11.5 at the copy rate; 13 tiles a
+// CTA, of which its start, the segments and the merge take a third), 344 us for 16 sequences
+// of 32K (48 columns; 204 at the copy rate).  There a tile is 6300 warp instructions at half
+// of the issue slots, 3000 cycles against 1800 for its bytes; a quarter of them collect
+// logits (without: 267 us), and time follows their number.
 //
 // The work is the list of all (sequence, KV head, 128-key tile) in order, cut into equal
 // ranges, one for each SM's CTA, by the sequences' real lengths (up to 256 sequences, whose
