@@ -101,6 +101,31 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
+// The same x as an e4m3 operand (the draft step, whose products have columns to spare): three
+// parts x0 + x1 / 2^5 + x2 / 2^13 of the half nearest to x, each in accumulator columns of
+// its own.  Up to x = 32 they hold the half's 11 bits, or are within 2^-23.
+constexpr float kPMid = 1.f / 32.f;
+constexpr float kPLow = 1.f / 8192.f;
+
+__device__ __forceinline__ uint32_t pack_e4m3x2_h(__half2 h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&h)));
+  return r;
+}
+
+// Parts of two values, each as two codes in the low 16 bits (differences and products by
+// powers of two are exact in halves).
+__device__ __forceinline__ void prob_parts(float a, float b, uint32_t (&part)[3]) {
+  __half2 x = __floats2half2_rn(a, b);
+  part[0] = pack_e4m3x2_h(x);
+  uint32_t h = e4m3x2_to_f16x2(part[0]);
+  x = __hmul2(__hsub2(x, *reinterpret_cast<const __half2*>(&h)), __float2half2_rn(32.f));
+  part[1] = pack_e4m3x2_h(x);
+  h = e4m3x2_to_f16x2(part[1]);
+  x = __hmul2(__hsub2(x, *reinterpret_cast<const __half2*>(&h)), __float2half2_rn(256.f));
+  part[2] = pack_e4m3x2_h(x);
+}
+
 // Maximum over a warp (NaN ignored).
 __device__ __forceinline__ float warp_max_f32(float x) {
   float r;

@@ -4,18 +4,21 @@
 // idx[0 .. n_sel) followed by [tail_start, seq_len)
 //   z_j = scale * ks[page(j)] * <q, kc[j]>,  out = sum_j softmax(z)_j * vs[page(j)] * vc[j]
 // As in the verification (see verify_quant.cuh and quant.cuh) the key codes feed the
-// tensor cores as they are, against queries in two e4m3 parts; the value codes are widened
-// to f16 in shared memory; the probability and the value scale meet in the exponent.
+// tensor cores as they are, against queries in two e4m3 parts, and the probability and the
+// value scale meet in the exponent.  The value codes feed them as they are too, against the
+// probabilities in three e4m3 parts: a group has few heads, so the parts are columns that
+// the products have to spare, and splitting a thread's few probabilities takes a third of
+// the instructions that widening its row of values does (widened to f16: 12.2 us for 16
+// sequences against 10.6, 14.5 for four of 64K against 11.5).
 //
 // How: the list of a (sequence, KV head) pair is cut into splits of 128 positions (longer
 // ones, walked batch by batch, beyond 1024 splits), a CTA of four warps each:
 //   * thread t resolves position t (index or tail -> block table -> page and row) and loads
 //     its page's two scales; the warps copy the rows (d bytes, 16 bytes a lane, whole rows
 //     per instruction) into the swizzled layouts with asynchronous copies, keys first;
-//   * one warp issues S^T[128 keys x 32] = K * [Qhi; Qlo]^T while every thread takes its
-//     value row into registers, to widen it into the place of the codes once the keys have
-//     been read; thread t then owns key t (TMEM lane t), the heads' maxima and sums meet in
-//     shared memory, and one warp issues O^T[d x 16] = V^T * P^T;
+//   * one warp issues S^T[128 keys x 2 G] = K * [Qhi; Qlo]^T; thread t then owns key t (TMEM
+//     lane t), the heads' maxima and sums meet in shared memory, P^T takes the place of the
+//     keys, and one warp issues O^T[d x 3 G] = V^T * [P0; P1; P2]^T (G padded to 8 or 16);
 //   * thread d writes dimension d of the heads' outputs, or of the split's (m, l, o), which
 //     a second kernel (a programmatic dependent, one block per output row) merges.
 // The second kernel instead of a last arrival's merge keeps the workspace free of counters
@@ -23,8 +26,10 @@
 // can take theirs from an allocator.
 //
 // A split is a chain of dependent latencies (lengths and indices, block table, rows, two
-// products, softmax: about 5 us at one sequence), so what counts is that all loads of a
-// step are in flight together and that five CTAs share an SM (41 KB of shared memory each).
+// products, softmax: 3 of the 5.2 us that one sequence of 4000 positions takes, the merge the
+// rest), so what counts is that all loads of a step are in flight together and that six
+// CTAs share an SM (36 KB of shared memory each).  Two batches a split were slower (6.6 and
+// 11.8 us) but where the splits fill more than a wave (10.1).
 #include <cfloat>
 
 #include "launch.h"
@@ -38,8 +43,7 @@ constexpr int kKeys = 128;      // positions of one batch (the products' M)
 constexpr int kSqThreads = 128;
 constexpr int kSqPage = 16;
 constexpr int kSqMaxSplits = 1024;
-constexpr int kSqNQ = 16;       // query heads of a group, padded
-constexpr float kSqTop = 14.f;  // log2 of the largest x of a batch
+constexpr float kSqTop = 5.f;   // log2 of the largest x of a batch
 constexpr float kSqNoMax = -3e38f;
 
 struct SqParams {
@@ -83,24 +87,26 @@ struct SqSlot {
   static constexpr int kFloats = kO + G * D;
 };
 
-template <int D>
+template <int D, int G>
 struct SqSmem {
+  static constexpr int kCols = G <= 8 ? 8 : 16;            // columns of one part of P or Q
+  static constexpr int kPRow = kCols == 8 ? 32 : 64;       // bytes of a key's row of P
+  static constexpr int kNS = 2 * kCols;                    // N of the two products
+  static constexpr int kNO = kCols == 8 ? 32 : 48;
+  static constexpr int kTmemCols = kNS + kNO <= 64 ? 64 : 128;
   static constexpr int kTileBytes = kKeys * D;
-  // the widened values take the place of the key and value codes: every thread holds its
-  // value row in registers by then, and the keys have been read
   static constexpr int kOffK = 0;
   static constexpr int kOffV = kTileBytes;
-  static constexpr int kOffWide = 0;                       // d / 64 halves of 128-byte rows
-  static constexpr int kOffP = 2 * kTileBytes;             // 32-byte rows
-  static constexpr int kOffQ = kOffP + kKeys * 32;
-  static constexpr int kOffRed = kOffQ + 2 * kSqNQ * D;    // [2][4][kSqNQ] floats
-  static constexpr int kOffQinv = kOffRed + 2 * 4 * kSqNQ * 4;
-  static constexpr int kOffBar = kOffQinv + kSqNQ * 4;
+  static constexpr int kOffP = 0;  // in the place of the keys, which have been read by then
+  static constexpr int kOffQ = 2 * kTileBytes;
+  static constexpr int kOffRed = kOffQ + 2 * kCols * D;    // [2][4][kCols] floats
+  static constexpr int kOffQinv = kOffRed + 2 * 4 * kCols * 4;
+  static constexpr int kOffBar = kOffQinv + kCols * 4;
   static constexpr int kUsed = kOffBar + 64;
-  // d = 64: the PV product reads 16 KB past the widened tile (rows of the accumulator that
-  // are never used), inside this allocation
-  static constexpr int kBytes = kUsed > 2 * kKeys * 128 ? kUsed : 2 * kKeys * 128;
-  static_assert(kOffQ % 1024 == 0 && 2 * kSqNQ * D % 1024 == 0, "swizzle atoms need 1 KB alignment");
+  // d = 64: the PV product reads 8 KB past the value tile (rows of the accumulator that are
+  // never used), inside this allocation
+  static constexpr int kBytes = kUsed > kOffV + 128 * kKeys ? kUsed : kOffV + 128 * kKeys;
+  static_assert(kOffQ % 1024 == 0, "swizzle atoms need 1 KB alignment");
 };
 
 // Sums of G values over a warp; lane L gets column L % G (G a power of two up to 16).
@@ -128,12 +134,12 @@ __device__ __forceinline__ float sq_warp_sums(float (&v)[G]) {
 }
 
 template <int D, int G>
-__global__ void __launch_bounds__(kSqThreads, G == 16 ? 3 : 5) sparse_quant_kernel(const SqParams a) {
-  using Sm = SqSmem<D>;
+__global__ void __launch_bounds__(kSqThreads, G == 16 ? 3 : 6) sparse_quant_kernel(const SqParams a) {
+  using Sm = SqSmem<D, G>;
+  constexpr int GP = Sm::kCols;
   constexpr int LPR = D / 16;       // 16-byte chunks of a row of codes
   constexpr int RPI = 32 / LPR;     // rows per warp instruction
   extern __shared__ __align__(1024) uint8_t sparse_quant_smem[];
-  uint8_t* const wide = sparse_quant_smem + Sm::kOffWide;
   uint8_t* const p_s = sparse_quant_smem + Sm::kOffP;
   uint8_t* const k_s = sparse_quant_smem + Sm::kOffK;
   uint8_t* const v_s = sparse_quant_smem + Sm::kOffV;
@@ -154,13 +160,13 @@ __global__ void __launch_bounds__(kSqThreads, G == 16 ? 3 : 5) sparse_quant_kern
     ptx::fence_mbarrier_init();
   }
   if (warp == 0) {
-    ptx::tmem_alloc(tmem_slot, 64);
+    ptx::tmem_alloc(tmem_slot, Sm::kTmemCols);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;  // S^T: columns [0, 32); O^T: [32, 48)
+  const uint32_t tmem = *tmem_slot;  // S^T: kNS columns, O^T: kNO
   const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
   ptx::pdl_wait_primary();
   ptx::pdl_launch_dependents();
@@ -175,7 +181,7 @@ __global__ void __launch_bounds__(kSqThreads, G == 16 ? 3 : 5) sparse_quant_kern
   const int t0_raw = __ldcg(a.tail_start + b);
   const int t1_raw = __ldcg(a.seq_len + b);
   constexpr int kCh = D / 8;
-  constexpr int kQL = kSqNQ * kCh / kSqThreads;  // 8-dimension pieces of the queries a thread
+  constexpr int kQL = (G * kCh + kSqThreads - 1) / kSqThreads;  // 8-dimension pieces a thread
   uint4 qv[kQL];
 #pragma unroll
   for (int u = 0; u < kQL; ++u) {
@@ -229,27 +235,28 @@ __global__ void __launch_bounds__(kSqThreads, G == 16 ? 3 : 5) sparse_quant_kern
       }
       // ---- gather: warp w copies rows 32 w .. 32 w + 31, the keys as the first group
       const int ch = lane % LPR;
+      int cr[32 / RPI];
 #pragma unroll
       for (int u = 0; u < 32 / RPI; ++u) {
         const int rl = u * RPI + lane / LPR;
-        const int cr = __shfl_sync(0xffffffffu, row, rl);
-        const size_t src = cr >= 0 ? static_cast<size_t>(cr) * D + ch * 16 : 0;
-        ptx::cp_async16(k_s + ptx::swizzled_chunk<D>(warp * 32 + rl, ch), a.k_cache + src, cr >= 0 ? 16u : 0u);
+        cr[u] = __shfl_sync(0xffffffffu, row, rl);
+        const size_t src = static_cast<size_t>(cr[u] >= 0 ? cr[u] : 0) * D + ch * 16;
+        ptx::cp_async16(k_s + ptx::swizzled_chunk<D>(warp * 32 + rl, ch), a.k_cache + src, cr[u] >= 0 ? 16u : 0u);
       }
       ptx::cp_async_commit();
 #pragma unroll
       for (int u = 0; u < 32 / RPI; ++u) {
         const int rl = u * RPI + lane / LPR;
-        const int cr = __shfl_sync(0xffffffffu, row, rl);
-        const size_t src = cr >= 0 ? static_cast<size_t>(cr) * D + ch * 16 : 0;
-        ptx::cp_async16(v_s + ptx::swizzled_chunk<D>(warp * 32 + rl, ch), a.v_cache + src, cr >= 0 ? 16u : 0u);
+        const size_t src = static_cast<size_t>(cr[u] >= 0 ? cr[u] : 0) * D + ch * 16;
+        ptx::cp_async16(v_s + ptx::swizzled_chunk<D>(warp * 32 + rl, ch), a.v_cache + src, cr[u] >= 0 ? 16u : 0u);
       }
       ptx::cp_async_commit();
       if (at == lo) {
-        // ---- the queries in two parts (rows past the group are zeros)
+        // ---- the queries in two parts (columns past the group are never read)
 #pragma unroll
         for (int u = 0; u < kQL; ++u) {
           const int i = t + u * kSqThreads, r = i / kCh, c = i % kCh;
+          if (G * kCh % kSqThreads != 0 && (i & ~31) >= G * kCh) break;  // (uniform per warp)
           const uint32_t w[4] = {qv[u].x, qv[u].y, qv[u].z, qv[u].w};
           uint32_t mx = 0;
 #pragma unroll
@@ -257,13 +264,14 @@ __global__ void __launch_bounds__(kSqThreads, G == 16 ? 3 : 5) sparse_quant_kern
 #pragma unroll
           for (int o = kCh / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
           const QScale qs = query_scale(mx);
+          if (G * kCh % 32 != 0 && r >= G) break;
           if (c == 0) qinv[r] = qs.inv;
           uint32_t qh[4], ql[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) query_parts(bf16_lo(w[k]), bf16_hi(w[k]), qs.f, qh[k], ql[k]);
           const uint32_t o = ptx::swizzled_chunk<D>(r, c >> 1) + (c & 1) * 8;
           *reinterpret_cast<uint2*>(q_s + o) = make_uint2(qh[0] | qh[1] << 16, qh[2] | qh[3] << 16);
-          *reinterpret_cast<uint2*>(q_s + kSqNQ * D + o) = make_uint2(ql[0] | ql[1] << 16, ql[2] | ql[3] << 16);
+          *reinterpret_cast<uint2*>(q_s + GP * D + o) = make_uint2(ql[0] | ql[1] << 16, ql[2] | ql[3] << 16);
         }
       }
       asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -273,7 +281,7 @@ __global__ void __launch_bounds__(kSqThreads, G == 16 ? 3 : 5) sparse_quant_kern
       // ---- S^T = K [Qhi; Qlo]^T by the first warp
       if (warp == 0) {
         ptx::tc_fence_after();
-        constexpr uint32_t idesc = ptx::idesc_e4m3_f32(128, 2 * kSqNQ, 0, 0);
+        constexpr uint32_t idesc = ptx::idesc_e4m3_f32(128, Sm::kNS, 0, 0);
         const uint64_t ad = ptx::sdesc_rows<D>(ptx::smem_u32(k_s), 16, 8 * D);
         const uint64_t bd = ptx::sdesc_rows<D>(ptx::smem_u32(q_s), 16, 8 * D);
         const uint32_t leader = ptx::elect_one();
@@ -282,35 +290,15 @@ __global__ void __launch_bounds__(kSqThreads, G == 16 ? 3 : 5) sparse_quant_kern
           ptx::umma_f8_if(leader, tmem, ad + kk * 2, bd + kk * 2, idesc, kk > 0 ? 1u : 0u);
         ptx::umma_commit_if(leader, bar_s);
       }
-      // ---- meanwhile every thread takes its value row into registers (absent: zeros)
-      ptx::cp_async_wait_all();
-      __syncthreads();
-      uint4 vr[D / 16];
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c)
-        vr[c] = *reinterpret_cast<const uint4*>(v_s + ptx::swizzled_chunk<D>(t, c));
-      // (d = 128: a thread widens into its own value row and the key tile; d = 64: into others')
-      if constexpr (D == 64) __syncthreads();
       // (a test build waits on the end-of-kernel barrier here, which nothing completes yet)
       const bool ok_s = ptx::mbar_wait(VSD_STALL(true) ? bar_fin : bar_s, products & 1);
       ptx::tc_fence_after();
-      // ---- the value row as f16 in the place of the codes
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        const uint32_t w[4] = {vr[c].x, vr[c].y, vr[c].z, vr[c].w};
-        uint8_t* half = wide + (c >> 2) * (kKeys * 128);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          *reinterpret_cast<uint4*>(half + ptx::swizzled_chunk<128>(t, (c & 3) * 2 + i)) =
-              make_uint4(e4m3x2_to_f16x2(w[2 * i] & 0xFFFFu), e4m3x2_to_f16x2(w[2 * i] >> 16),
-                         e4m3x2_to_f16x2(w[2 * i + 1] & 0xFFFFu), e4m3x2_to_f16x2(w[2 * i + 1] >> 16));
-      }
       // ---- softmax over the batch, per head: y = z log2 e + log2 vs
       float y[G];
       {
         float sh[G], sl[G];
         ptx::tmem_ld<G>(tmem + lane_addr, reinterpret_cast<uint32_t*>(sh));
-        ptx::tmem_ld<G>(tmem + lane_addr + kSqNQ, reinterpret_cast<uint32_t*>(sl));
+        ptx::tmem_ld<G>(tmem + lane_addr + GP, reinterpret_cast<uint32_t*>(sl));
         ptx::tmem_wait_ld();
         const float vsf = fmaxf(vs, kMinVScale);
         const float zl = ks * a.scale * kLog2e, lvs = lg2(vsf);
@@ -318,29 +306,42 @@ __global__ void __launch_bounds__(kSqThreads, G == 16 ? 3 : 5) sparse_quant_kern
         for (int h = 0; h < G; ++h) {
           y[h] = row >= 0 ? __fmaf_rn(fmaf(sl[h], kQLo, sh[h]) * qinv[h], zl, lvs) : -INFINITY;
           const float wm = warp_max_f32(fmaxf(y[h], kSqNoMax));
-          if (lane == 0) red[warp * kSqNQ + h] = wm;
+          if (lane == 0) red[warp * GP + h] = wm;
         }
       }
       __syncthreads();
       const float ivs = 1.f / fmaxf(vs, kMinVScale);
-      float x[kSqNQ];
+      float x[GP];
 #pragma unroll
-      for (int h = 0; h < kSqNQ; ++h) x[h] = 0.f;
+      for (int h = 0; h < GP; ++h) x[h] = 0.f;
       float alpha[G];
 #pragma unroll
       for (int h = 0; h < G; ++h) {
-        const float top = fmaxf(fmaxf(red[h], red[kSqNQ + h]), fmaxf(red[2 * kSqNQ + h], red[3 * kSqNQ + h]));
+        const float top = fmaxf(fmaxf(red[h], red[GP + h]), fmaxf(red[2 * GP + h], red[3 * GP + h]));
         const float mn = fmaxf(m[h], top - kSqTop);
         alpha[h] = ex2(m[h] - mn);
         m[h] = mn;
         x[h] = ex2(y[h] - mn);
       }
-      // row t of P^T: 16 halves, one 32-byte swizzle span
+      // row t of P^T: the heads' first parts, second, third (columns of one swizzle span)
+      uint32_t w[3][GP / 4];
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        *reinterpret_cast<uint4*>(p_s + ptx::swizzled_chunk<32>(t, k)) =
-            make_uint4(pack_f16x2(x[8 * k], x[8 * k + 1]), pack_f16x2(x[8 * k + 2], x[8 * k + 3]),
-                       pack_f16x2(x[8 * k + 4], x[8 * k + 5]), pack_f16x2(x[8 * k + 6], x[8 * k + 7]));
+      for (int h = 0; h < GP; h += 4) {
+        uint32_t lo2[3], hi2[3];
+        prob_parts(x[h], x[h + 1], lo2);
+        prob_parts(x[h + 2], x[h + 3], hi2);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) w[k][h / 4] = lo2[k] | hi2[k] << 16;
+      }
+      if constexpr (GP == 8) {
+        *reinterpret_cast<uint4*>(p_s + ptx::swizzled_chunk<32>(t, 0)) = make_uint4(w[0][0], w[0][1], w[1][0], w[1][1]);
+        *reinterpret_cast<uint2*>(p_s + ptx::swizzled_chunk<32>(t, 1)) = make_uint2(w[2][0], w[2][1]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          *reinterpret_cast<uint4*>(p_s + ptx::swizzled_chunk<64>(t, k)) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+      }
+      ptx::cp_async_wait_all();  // (the value rows)
       ptx::fence_proxy_async_smem();
       ptx::tc_fence_before();
       // (every thread learns whether some wait gave up: a product may still be running)
@@ -349,13 +350,14 @@ __global__ void __launch_bounds__(kSqThreads, G == 16 ? 3 : 5) sparse_quant_kern
       // ---- O^T = V^T P^T
       if (warp == 0) {
         ptx::tc_fence_after();
-        constexpr uint32_t idesc = ptx::idesc_f16_f32(128, kSqNQ, 1, 1);
-        const uint64_t ad = ptx::sdesc_sw128(ptx::smem_u32(wide), kKeys * 128, 1024);
-        const uint64_t bd = ptx::sdesc_rows<32>(ptx::smem_u32(p_s), kKeys * 32, 256);
+        constexpr uint32_t idesc = ptx::idesc_e4m3_f32(128, Sm::kNO, 1, 1);
+        const uint64_t ad = ptx::sdesc_rows<D>(ptx::smem_u32(v_s), kKeys * D, 8 * D);
+        const uint64_t bd = ptx::sdesc_rows<Sm::kPRow>(ptx::smem_u32(p_s), kKeys * Sm::kPRow, 8 * Sm::kPRow);
         const uint32_t leader = ptx::elect_one();
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          ptx::umma_f16_if(leader, tmem + 2 * kSqNQ, ad + kk * 128, bd + kk * 32, idesc, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < kKeys / 32; ++kk)
+          ptx::umma_f8_if(leader, tmem + Sm::kNS, ad + kk * (32 * D >> 4), bd + kk * (32 * Sm::kPRow >> 4), idesc,
+                          kk > 0 ? 1u : 0u);
         ptx::umma_commit_if(leader, bar_o);
       }
       // ---- the heads' sums while the product runs
@@ -363,20 +365,22 @@ __global__ void __launch_bounds__(kSqThreads, G == 16 ? 3 : 5) sparse_quant_kern
 #pragma unroll
       for (int h = 0; h < G; ++h) ls[h] = x[h] * ivs;
       const float wsum = sq_warp_sums<G>(ls);
-      if (lane < G) red[4 * kSqNQ + warp * kSqNQ + lane] = wsum;
+      if (lane < G) red[4 * GP + warp * GP + lane] = wsum;
       const bool ok_o = ptx::mbar_wait(bar_o, products & 1);
       ++products;
       ptx::tc_fence_after();
-      float o[G];
-      ptx::tmem_ld<G>(tmem + lane_addr + 2 * kSqNQ, reinterpret_cast<uint32_t*>(o));
+      float o[G], o1[G], o2[G];
+      const uint32_t o_at = tmem + lane_addr + Sm::kNS;
+      ptx::tmem_ld<G>(o_at, reinterpret_cast<uint32_t*>(o));
+      ptx::tmem_ld<G>(o_at + GP, reinterpret_cast<uint32_t*>(o1));
+      ptx::tmem_ld<G>(o_at + 2 * GP, reinterpret_cast<uint32_t*>(o2));
       ptx::tmem_wait_ld();
       ptx::tc_fence_before();
       timed_out = __syncthreads_or(!ok_o);
 #pragma unroll
       for (int h = 0; h < G; ++h) {
-        lsum[h] = lsum[h] * alpha[h] + (red[4 * kSqNQ + h] + red[5 * kSqNQ + h] + red[6 * kSqNQ + h] +
-                                        red[7 * kSqNQ + h]);
-        acc[h] = acc[h] * alpha[h] + o[h];
+        lsum[h] = lsum[h] * alpha[h] + (red[4 * GP + h] + red[5 * GP + h] + red[6 * GP + h] + red[7 * GP + h]);
+        acc[h] = acc[h] * alpha[h] + (fmaf(o2[h], kPLow, o1[h] * kPMid) + o[h]);
       }
     }
     if (t < D) {
@@ -411,7 +415,7 @@ __global__ void __launch_bounds__(kSqThreads, G == 16 ? 3 : 5) sparse_quant_kern
   __syncthreads();
   if (warp == 0) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 64);
+    ptx::tmem_dealloc(tmem, Sm::kTmemCols);
   }
 }
 
@@ -487,7 +491,8 @@ SqPlan sq_plan(int k_max, int max_tail) {
 template <int D, int G>
 cudaError_t launch_sq(const SqParams& p, int B, cudaStream_t stream) {
   auto kern = sparse_quant_kernel<D, G>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SqSmem<D>::kBytes);
+  constexpr int smem = SqSmem<D, G>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -495,7 +500,7 @@ cudaError_t launch_sq(const SqParams& p, int B, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.max_splits, p.Hkv, B);
   cfg.blockDim = dim3(kSqThreads, 1, 1);
-  cfg.dynamicSmemBytes = SqSmem<D>::kBytes;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
