@@ -11,8 +11,9 @@
 // the instructions that widening its row of values does (widened to f16: 12.2 us for 16
 // sequences against 10.6, 14.5 for four of 64K against 11.5).
 //
-// How: the list of a (sequence, KV head) pair is cut into splits of 128 positions (longer
-// ones, walked batch by batch, beyond 1024 splits), a CTA of four warps each:
+// How: the list of a (sequence, KV head) pair is cut into splits of 128 positions (a few times
+// as many, walked batch by batch, where the splits fill more than a wave), a CTA of four
+// warps each:
 //   * thread t resolves position t (index or tail -> block table -> page and row) and loads
 //     its page's two scales; the warps copy the rows (d bytes, 16 bytes a lane, whole rows
 //     per instruction) into the swizzled layouts with asynchronous copies, keys first;
@@ -28,8 +29,7 @@
 // A split is a chain of dependent latencies (lengths and indices, block table, rows, two
 // products, softmax: 3 of the 5.2 us that one sequence of 4000 positions takes, the merge the
 // rest), so what counts is that all loads of a step are in flight together and that six
-// CTAs share an SM (36 KB of shared memory each).  Two batches a split were slower (6.6 and
-// 11.8 us) but where the splits fill more than a wave (10.1).
+// CTAs share an SM (36 KB of shared memory each).
 #include <cfloat>
 
 #include "launch.h"
@@ -43,6 +43,7 @@ constexpr int kKeys = 128;      // positions of one batch (the products' M)
 constexpr int kSqThreads = 128;
 constexpr int kSqPage = 16;
 constexpr int kSqMaxSplits = 1024;
+constexpr int kSqWave = 152 * 6;  // CTAs that run at once
 constexpr float kSqTop = 5.f;   // log2 of the largest x of a batch
 constexpr float kSqNoMax = -3e38f;
 
@@ -174,9 +175,10 @@ __global__ void __launch_bounds__(kSqThreads, G == 16 ? 3 : 6) sparse_quant_kern
   // in flight together: the first batch's indices (used where they turn out to be selected
   // positions), the lengths and the queries
   const int lo = split * a.split_len;
-  int spec = (a.idx != nullptr && lo + t < a.k_max)
-                 ? __ldcg(a.idx + static_cast<size_t>(b) * a.k_max + lo + t)
-                 : 0;
+  const auto raw_index = [&](int pos) {
+    return a.idx != nullptr && pos < a.k_max ? __ldcg(a.idx + static_cast<size_t>(b) * a.k_max + pos) : 0;
+  };
+  int raw = raw_index(lo + t);
   const int ns_raw = a.n_sel != nullptr ? __ldcg(a.n_sel + b) : 0;
   const int t0_raw = __ldcg(a.tail_start + b);
   const int t1_raw = __ldcg(a.seq_len + b);
@@ -205,32 +207,36 @@ __global__ void __launch_bounds__(kSqThreads, G == 16 ? 3 : 6) sparse_quant_kern
   }
 
   if (work) {
+    // This thread's position in the batch at `at`: its index in the sequence (-1: absent) from
+    // the raw list entry, then its entry of the block table.  Both are loaded ahead, the
+    // list two batches and the table one, so that only the first batch waits for them.
+    const auto index_of = [&](int at, int listed) {
+      const int pos = at + t;
+      if (pos >= hi_pos) return -1;
+      if (pos >= L.ns) return L.t0 + (pos - L.ns);
+      const bool ok = listed >= 0 && listed < L.t1;
+      if (!ok) flag_status(a.status, VSD_DEV_BAD_INDEX);
+      return ok ? listed : -1;
+    };
+    const auto entry_of = [&](int j) {
+      return j >= 0 ? __ldcg(a.block_table + static_cast<size_t>(b) * a.max_blocks + j / kSqPage) : 0;
+    };
+    int j = index_of(lo, raw);
+    int entry = entry_of(j);
+    raw = a.split_len > kKeys ? raw_index(lo + kKeys + t) : 0;
 #pragma unroll 1
     for (int at = lo; at < hi_pos && !timed_out; at += kKeys) {
-      // ---- this thread's position: page and row (-1: absent), and the page's scales
-      const int pos = at + t;
+      // ---- this thread's row (-1: absent) and its page's scales
       int row = -1;
       float ks = 0.f, vs = -1.f;
-      if (pos < hi_pos) {
-        int j;
-        bool ok = true;
-        if (pos < L.ns) {
-          j = at == lo ? spec : __ldcg(a.idx + static_cast<size_t>(b) * a.k_max + pos);
-          ok = j >= 0 && j < L.t1;
-          if (!ok) flag_status(a.status, VSD_DEV_BAD_INDEX);
+      if (j >= 0) {
+        if (entry < 0 || entry >= a.num_blocks) {
+          flag_status(a.status, VSD_DEV_BAD_BLOCK);
         } else {
-          j = L.t0 + (pos - L.ns);
-        }
-        if (ok) {
-          const int blk = __ldcg(a.block_table + static_cast<size_t>(b) * a.max_blocks + j / kSqPage);
-          if (blk < 0 || blk >= a.num_blocks) {
-            flag_status(a.status, VSD_DEV_BAD_BLOCK);
-          } else {
-            const int ph = blk * a.Hkv + g;
-            row = ph * kSqPage + j % kSqPage;
-            ks = __ldcg(a.k_scale + ph);
-            vs = __ldcg(a.v_scale + ph);
-          }
+          const int ph = entry * a.Hkv + g;
+          row = ph * kSqPage + j % kSqPage;
+          ks = __ldcg(a.k_scale + ph);
+          vs = __ldcg(a.v_scale + ph);
         }
       }
       // ---- gather: warp w copies rows 32 w .. 32 w + 31, the keys as the first group
@@ -251,6 +257,11 @@ __global__ void __launch_bounds__(kSqThreads, G == 16 ? 3 : 6) sparse_quant_kern
         ptx::cp_async16(v_s + ptx::swizzled_chunk<D>(warp * 32 + rl, ch), a.v_cache + src, cr[u] >= 0 ? 16u : 0u);
       }
       ptx::cp_async_commit();
+      if (at + kKeys < hi_pos) {
+        j = index_of(at + kKeys, raw);
+        entry = entry_of(j);
+        raw = raw_index(at + 2 * kKeys + t);
+      }
       if (at == lo) {
         // ---- the queries in two parts (columns past the group are never read)
 #pragma unroll
@@ -481,10 +492,18 @@ struct SqPlan {
   int split_len, splits;
 };
 
-SqPlan sq_plan(int k_max, int max_tail) {
+// One batch a split while the CTAs fill one wave, then two, and four beyond four waves: fewer
+// partial results, and only a CTA's first batch waits for the list and the table.  (One
+// sequence of 4000 positions: 5.3 us with one batch, 6.4 with two; four of them with 8 heads
+// 11.5 and 9.8; 32 of them 65 with one, 56 with two, 54 with four, 53 with six.)
+SqPlan sq_plan(long long pairs, int k_max, int max_tail) {
   const int n = k_max + max_tail;  // (below 2^31: checked by the caller)
   const int batches = n > 0 ? (n + kKeys - 1) / kKeys : 1;
-  const int per = (batches + kSqMaxSplits - 1) / kSqMaxSplits;
+  const long long ctas = pairs * batches;
+  int per = ctas <= kSqWave ? 1 : (ctas <= 4 * kSqWave ? 2 : 4);
+  if (per > batches) per = batches;
+  const int least = (batches + kSqMaxSplits - 1) / kSqMaxSplits;
+  if (per < least) per = least;
   return SqPlan{per * kKeys, (batches + per - 1) / per};
 }
 
@@ -527,14 +546,14 @@ cudaError_t launch_sq_d(const SqParams& p, int B, int G, cudaStream_t stream) {
 }  // namespace
 
 size_t sparse_quant_workspace_bytes(int B, int Hkv, int G, int head_dim, int k_max, int max_tail) {
-  const SqPlan plan = sq_plan(k_max, max_tail);
+  const SqPlan plan = sq_plan(static_cast<long long>(B) * Hkv, k_max, max_tail);
   if (plan.splits <= 1) return 0;
   const size_t slot = (2 * G + 3) / 4 * 4 + static_cast<size_t>(G) * head_dim;
   return static_cast<size_t>(B) * Hkv * plan.splits * slot * sizeof(float);
 }
 
 cudaError_t launch_sparse_quant(const SparseArgs& a, const QuantScales& s, cudaStream_t stream) {
-  const SqPlan plan = sq_plan(a.k_max, a.max_tail);
+  const SqPlan plan = sq_plan(static_cast<long long>(a.B) * a.Hkv, a.k_max, a.max_tail);
   SqParams p;
   p.q = static_cast<const uint16_t*>(a.q);
   p.k_cache = static_cast<const uint8_t*>(a.k_cache);
