@@ -68,6 +68,21 @@ def test_append_over_scales_that_are_no_powers_of_two(vsd):
         _check_append(vsd, cache, rows, [50, 61], [5, 5], 5, pos_offset=-1, pass_valid=False)
 
 
+@pytest.mark.parametrize("scale", [2.0 ** 127, 1.37, 2.0 ** -126, 2.0 ** -130])
+def test_append_keeps_a_callers_scale(vsd, scale):
+    """Scales at the ends of the range and between powers of two, rows that they hold (some
+    values below the smallest code), NaN and infinities among them."""
+    cache = ref.Cache([40], 3, 128, seed=13)
+    blk = int(cache.table[0, 1])
+    for kv in range(2):
+        cache.scales[kv][blk] = scale
+    g = torch.Generator().manual_seed(8)
+    rows = [(torch.randn((1, 7, 3, 128), generator=g) * 50.0 * min(scale, 2.0 ** 118)).bfloat16() for _ in range(2)]
+    for x in rows:
+        x[0, 1, 0, 5], x[0, 2, 1, 127], x[0, 6, 2, 0] = math.nan, math.inf, -math.inf
+    _check_append(vsd, cache, rows, [21], [7], 7)
+
+
 @pytest.mark.parametrize("mag", [0.0, 0.3])
 def test_append_into_a_page_of_scale_zero(vsd, mag):
     """Earlier rows with scale 0 (a caller's own page of zeros): a scale of 0 cannot hold
