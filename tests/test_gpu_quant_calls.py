@@ -2,6 +2,7 @@
 captured graphs, caches past 2^31 bytes, waits that run out."""
 import ctypes
 import math
+import threading
 import time
 
 import pytest
@@ -132,6 +133,34 @@ def test_calls_of_growing_and_shrinking_sizes_on_two_streams(vsd):
     for g in got:
         for a, b in zip(g, want + want[::-1]):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_calls_from_several_threads(vsd):
+    """Four host threads, two of them on one stream, call without workspaces of their own."""
+    runs = [_calls(vsd, 90 + i) for i in range(4)]
+    want = [[x.clone() for x in run()] for run in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    streams.append(streams[0])
+    bad = []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(streams[i]):
+                for _ in range(25):
+                    got = [x.clone() for x in runs[i]()]
+                    streams[i].synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                        bad.append(i)
+        except Exception as e:  # noqa: BLE001 (reported below)
+            bad.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not bad
+    assert vsd.vsd_read_device_status() == 0
 
 
 def test_captured_graphs_replayed_together(vsd):
