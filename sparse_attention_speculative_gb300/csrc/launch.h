@@ -244,6 +244,7 @@ struct QuantScales {
   const float* v;
 };
 
+bool verify_quant_whole(const VerifyPlan& plan);
 size_t verify_quant_span_bytes(const VerifyPlan& plan);
 size_t verify_quant_workspace_bytes(const VerifyPlan& plan, int head_dim);
 cudaError_t launch_verify_quant(const VerifyArgs& a, const QuantScales& s, const VerifyPlan& plan,

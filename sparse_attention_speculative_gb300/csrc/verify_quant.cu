@@ -16,6 +16,21 @@ size_t verify_quant_span_bytes(const VerifyPlan& plan) {
   return (static_cast<size_t>(plan.pairs) * 8 + 255) / 256 * 256;
 }
 
+// Whether every pair has a CTA of its own.  That takes up to t_max tiles one after the other
+// instead of W / ctas, but no partial results, no kernel that merges them (together about
+// 3 tiles' time), and, where many pairs share CTAs, no second part in a CTA (up to 5 more).
+// With 12 tiles at most, since ranges follow the real lengths and this the longest.  Split and
+// whole, us: one pair, 3 tiles 8.9 / 8.3, 5 tiles 8.9 / 10.1; 8 pairs, 2 tiles 11.4 / 9.1,
+// 4 tiles 10.8 / 10.9, 6 tiles 11.0 / 13.0; 64 pairs of ragged single tokens, 6 tiles
+// 15.1 / 10.7, 8 tiles 15.2 / 12.7; 128 pairs of 48 columns, 4 tiles 31.7 / 18.4, 8 tiles
+// 41.0 / 25.8.
+bool verify_quant_whole(const VerifyPlan& plan) {
+  if (plan.pairs == 0 || plan.pairs > plan.ctas || plan.t_max > 12) return false;
+  const int shared = plan.pairs * plan.t_max / plan.ctas;
+  const int room = plan.pairs < 64 ? plan.pairs * 5 / 64 : 5;
+  return plan.t_max - shared <= 3 + room;
+}
+
 size_t verify_quant_workspace_bytes(const VerifyPlan& plan, int head_dim) {
   if (plan.ctas <= 1 || plan.pairs == 0) return 0;
   return verify_quant_span_bytes(plan) +

@@ -42,7 +42,8 @@
 // ranges, one for each SM's CTA, by the sequences' real lengths (up to 256 sequences, whose
 // first tiles every CTA sums up for itself; beyond that as if every sequence were as long
 // as the longest admissible).  Along the list either the pair or the CTA changes from one
-// partial result to the next, so slot (pair + CTA) holds it: pairs + CTAs slots in all.
+// partial result to the next, so slot (pair + CTA) holds it: pairs + CTAs slots in all.  A few
+// short pairs take one CTA each instead, without partial results and their merge.
 //
 // Every column has a reference r (see quant.cuh) that one vote per tile raises when it has
 // to; a raise costs 1500 cycles, so it leaves room of 2^13 (with 2^8 and 48 columns that
@@ -100,7 +101,8 @@ struct QVParams {
   const float* k_scale;
   const float* v_scale;
   int gshift;  // log2 of the group size
-  int2* spans;  // [pairs] first and last CTA of each pair (null: one CTA has them all)
+  int2* spans;  // [pairs] first and last CTA of each pair (null: every pair has one CTA)
+  int whole;    // CTA p has pair p
 };
 
 // The positions of one sequence (a length outside the declared bounds: none).
@@ -161,8 +163,17 @@ struct Walk {
   const int* plen;  // prefix lengths in shared memory, or null (uniform plan)
   int v, v1, base, b, g;
 
-  __device__ __forceinline__ Walk(const VParams& a_, const int* plen_, const int* cum, const Ranges& r)
+  __device__ __forceinline__ Walk(const VParams& a_, const int* plen_, const int* cum, const Ranges& r, bool whole)
       : a(a_), plen(plen_) {
+    if (whole) {
+      const int p = blockIdx.x;
+      b = p / a.Hkv;
+      g = p - b * a.Hkv;
+      const int T = (plen != nullptr ? seq_len(a, plen[b]).tiles : a.t_max) + kStartTiles;
+      v = base = plen != nullptr ? cum[b] + g * T : p * T;
+      v1 = base + T;
+      return;
+    }
     const int c = static_cast<int>(blockIdx.x) < r.C ? static_cast<int>(blockIdx.x) : r.C;
     v = r.first(c);
     v1 = c < r.C ? r.first(c + 1) : v;
@@ -365,7 +376,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
   __syncthreads();
   const int* plen = table ? plen_s : nullptr;
   const Ranges ranges = make_ranges(table ? cum_s[a.B] : a.pairs * (a.t_max + kStartTiles));
-  const auto walk_of = [&] { return Walk(a, plen, cum_s, ranges); };
+  const auto walk_of = [&] { return Walk(a, plen, cum_s, ranges, qa.whole != 0); };
   const uint32_t tmem_o = tmem + Cfg::kTmemO;
 
   auto set_abort = [&]() {
@@ -1041,7 +1052,7 @@ cudaError_t launch_quant(const VerifyArgs& va, const VerifyPlan& plan, const QVP
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(plan.ctas, 1, 1);
+  cfg.gridDim = dim3(p.whole ? plan.pairs : plan.ctas, 1, 1);
   cfg.blockDim = dim3(kQThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -1070,7 +1081,8 @@ cudaError_t launch_quant_d(const VerifyArgs& va, const QuantScales& sc, const Ve
   p.k_scale = sc.k;
   p.v_scale = sc.v;
   p.spans = nullptr;
-  if (plan.ctas > 1) {  // workspace: the pairs' spans, then the partial results
+  p.whole = verify_quant_whole(plan);
+  if (plan.ctas > 1 && !p.whole) {  // workspace: the pairs' spans, then the partial results
     p.spans = reinterpret_cast<int2*>(va.ws);
     p.v.ws = va.ws + verify_quant_span_bytes(plan) / sizeof(float);
   }

@@ -250,6 +250,17 @@ def test_verify_many_sequences_share_sms(vsd):
     check_verify(vsd, cache, prefix, 8, 64, 2, P_max=400, rows=(1, 1))
 
 
+@pytest.mark.parametrize("B,P", [(1, 380), (1, 381), (1, 508), (1, 509), (19, 600), (19, 1300), (40, 1500), (76, 200)])
+def test_verify_short_sequences(vsd, B, P):
+    """Pairs that take one CTA each and pairs that share them, lengths from none to the longest."""
+    g = torch.Generator().manual_seed(B * 7 + P)
+    prefix = [P] + torch.randint(0, P + 1, (B - 1,), generator=g).tolist()
+    if B > 2:
+        prefix[1] = 0
+    cache = ref.Cache([p + 4 for p in prefix], 2, 64, seed=B + P)
+    check_verify(vsd, cache, prefix, 4, 64, 4, P_max=P)
+
+
 def test_verify_more_sequences_than_a_cta_holds_lengths_of(vsd):
     g = torch.Generator().manual_seed(2)
     prefix = torch.randint(0, 150, (300,), generator=g).tolist()
