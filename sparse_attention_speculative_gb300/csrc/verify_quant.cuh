@@ -102,7 +102,6 @@ struct QVParams {
   const float* v_scale;
   int gshift;  // log2 of the group size
   int2* spans;  // [pairs] first and last CTA of each pair (null: every pair has one CTA)
-  int whole;    // CTA p has pair p
 };
 
 // The positions of one sequence (a length outside the declared bounds: none).
@@ -158,48 +157,50 @@ struct Seg {
   bool bad_len;
 };
 
+// kWhole: CTA p has pair p.
+template <bool kWhole>
 struct Walk {
   const VParams& a;
   const int* plen;  // prefix lengths in shared memory, or null (uniform plan)
   int v, v1, base, b, g;
 
-  __device__ __forceinline__ Walk(const VParams& a_, const int* plen_, const int* cum, const Ranges& r, bool whole)
+  __device__ __forceinline__ Walk(const VParams& a_, const int* plen_, const int* cum, const Ranges& r)
       : a(a_), plen(plen_) {
-    if (whole) {
+    if constexpr (kWhole) {
       const int p = blockIdx.x;
       b = p / a.Hkv;
       g = p - b * a.Hkv;
       const int T = (plen != nullptr ? seq_len(a, plen[b]).tiles : a.t_max) + kStartTiles;
       v = base = plen != nullptr ? cum[b] + g * T : p * T;
       v1 = base + T;
-      return;
-    }
-    const int c = static_cast<int>(blockIdx.x) < r.C ? static_cast<int>(blockIdx.x) : r.C;
-    v = r.first(c);
-    v1 = c < r.C ? r.first(c + 1) : v;
-    b = g = base = 0;
-    if (v >= v1) return;
-    if (plen != nullptr) {
-      // the last sequence whose first unit (times the heads) is not behind v
-      int lo = 0, hi = a.B - 1;
-#pragma unroll 1
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (cum[mid] <= v)
-          lo = mid;
-        else
-          hi = mid - 1;
-      }
-      b = lo;
-      const int T = seq_len(a, plen[b]).tiles + kStartTiles;
-      g = (v - cum[b]) / T;
-      base = cum[b] + g * T;
     } else {
-      const int T = a.t_max + kStartTiles;
-      const int p = v / T;
-      b = p / a.Hkv;
-      g = p - b * a.Hkv;
-      base = p * T;
+      const int c = static_cast<int>(blockIdx.x) < r.C ? static_cast<int>(blockIdx.x) : r.C;
+      v = r.first(c);
+      v1 = c < r.C ? r.first(c + 1) : v;
+      b = g = base = 0;
+      if (v >= v1) return;
+      if (plen != nullptr) {
+        // the last sequence whose first unit (times the heads) is not behind v
+        int lo = 0, hi = a.B - 1;
+#pragma unroll 1
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (cum[mid] <= v)
+            lo = mid;
+          else
+            hi = mid - 1;
+        }
+        b = lo;
+        const int T = seq_len(a, plen[b]).tiles + kStartTiles;
+        g = (v - cum[b]) / T;
+        base = cum[b] + g * T;
+      } else {
+        const int T = a.t_max + kStartTiles;
+        const int p = v / T;
+        b = p / a.Hkv;
+        g = p - b * a.Hkv;
+        base = p * T;
+      }
     }
   }
 
@@ -264,7 +265,8 @@ struct QCfg {
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
-template <int D, int NQ>
+// (kWhole is a parameter of the kernel: chosen at run time it cost the others 2 %)
+template <int D, int NQ, bool kWhole>
 __global__ void __launch_bounds__(kQThreads, 1)
     verify_quant_kernel(const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap, const QVParams qa) {
@@ -376,7 +378,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
   __syncthreads();
   const int* plen = table ? plen_s : nullptr;
   const Ranges ranges = make_ranges(table ? cum_s[a.B] : a.pairs * (a.t_max + kStartTiles));
-  const auto walk_of = [&] { return Walk(a, plen, cum_s, ranges, qa.whole != 0); };
+  const auto walk_of = [&] { return Walk<kWhole>(a, plen, cum_s, ranges); };
   const uint32_t tmem_o = tmem + Cfg::kTmemO;
 
   auto set_abort = [&]() {
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
     if (leads) tma_prefetch_desc(map);
     uint32_t it = 0;
     Seg s;
-    for (Walk w = walk_of(); w.next(s);) {
+    for (auto w = walk_of(); w.next(s);) {
       // block-table entries: 4 tiles (32 pages, one per lane) per load round, two rounds ahead
       const int32_t* bt_row = a.block_table + static_cast<size_t>(s.b) * a.max_blocks;
       auto raw_entry = [&](int tile_base) {
@@ -454,7 +456,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
     uint32_t i = 0, nseg = 0;
     bool ok = true;
     Seg s;
-    for (Walk w = walk_of(); ok && w.next(s);) {
+    for (auto w = walk_of(); ok && w.next(s);) {
       if (s.t_begin >= s.t_end) continue;
       ok = mbar_wait_compact(q_ready, nseg & 1, abort_flag);  // (the last segment's products are done)
       ++nseg;
@@ -491,7 +493,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
     uint32_t i = 0;
     bool ok = true;
     Seg s;
-    for (Walk w = walk_of(); ok && w.next(s);) {
+    for (auto w = walk_of(); ok && w.next(s);) {
       for (int tile = s.t_begin; tile < s.t_end; ++tile, ++i) {
         const uint32_t buf = i & 1;
         ok = mbar_wait_compact(&p_full[buf], (i >> 1) & 1, abort_flag);  // P^T and the widened V
@@ -516,7 +518,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
     // ------------------------------------------------------------ scales of the pages
     uint32_t round = 0;
     Seg s;
-    for (Walk w = walk_of(); w.next(s);) {
+    for (auto w = walk_of(); w.next(s);) {
       if (s.t_begin >= s.t_end) continue;
       const int32_t* bt_row = a.block_table + static_cast<size_t>(s.b) * a.max_blocks;
       // this lane's page of a round: its table entry (-1: past the sequence), its scales
@@ -556,7 +558,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
     const int row = (warp & 3) * 32 + lane;  // key in tile
     uint32_t it = 0, nseg = 0;
     Seg s;
-    for (Walk walk = walk_of(); walk.next(s);) {
+    for (auto walk = walk_of(); walk.next(s);) {
       if (s.t_begin >= s.t_end) continue;
       const uint32_t seg_parity = nseg++ & 1;
       for (int tile = s.t_begin; tile < s.t_end; ++tile, ++it) {
@@ -656,7 +658,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
                                       s.g * G + (r & (G - 1))) * D + ch * 8);
       }
     };
-    Walk walk = walk_of();
+    auto walk = walk_of();
     Seg s;
     bool more = walk.next(s);
     if (more) load_queries(s);
@@ -1044,7 +1046,8 @@ __global__ void __launch_bounds__(D) verify_quant_merge_kernel(const QVParams qa
 template <int D, int NQ>
 cudaError_t launch_quant(const VerifyArgs& va, const VerifyPlan& plan, const QVParams& p,
                          cudaStream_t stream) {
-  auto kern = verify_quant_kernel<D, NQ>;
+  const bool whole = verify_quant_whole(plan);
+  auto kern = whole ? verify_quant_kernel<D, NQ, true> : verify_quant_kernel<D, NQ, false>;
   constexpr int smem = QCfg<D, NQ>::kSmemBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -1052,7 +1055,7 @@ cudaError_t launch_quant(const VerifyArgs& va, const VerifyPlan& plan, const QVP
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.whole ? plan.pairs : plan.ctas, 1, 1);
+  cfg.gridDim = dim3(whole ? plan.pairs : plan.ctas, 1, 1);
   cfg.blockDim = dim3(kQThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -1081,8 +1084,7 @@ cudaError_t launch_quant_d(const VerifyArgs& va, const QuantScales& sc, const Ve
   p.k_scale = sc.k;
   p.v_scale = sc.v;
   p.spans = nullptr;
-  p.whole = verify_quant_whole(plan);
-  if (plan.ctas > 1 && !p.whole) {  // workspace: the pairs' spans, then the partial results
+  if (plan.ctas > 1 && !verify_quant_whole(plan)) {  // workspace: the pairs' spans, then the partial results
     p.spans = reinterpret_cast<int2*>(va.ws);
     p.v.ws = va.ws + verify_quant_span_bytes(plan) / sizeof(float);
   }
