@@ -67,6 +67,19 @@ vsd_status encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
   return VSD_OK;
 }
 
+// Encoding a descriptor is a call of the driver, which wants the device's context current on
+// the host thread.  The runtime makes it so at the thread's first call that needs it, and an
+// encoding may well come before that.
+template <typename Encode>
+CUresult with_context(Encode&& encode) {
+  CUresult r = encode();
+  int dev = 0;
+  if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess &&
+      cudaSetDevice(dev) == cudaSuccess)
+    r = encode();
+  return r;
+}
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
@@ -93,9 +106,11 @@ vsd_status make_cache_map(CUtensorMap* map, const void* cache, const vsd_geom* g
   cuuint64_t strides[3] = {d * 2, 16 * d * 2, static_cast<cuuint64_t>(g->Hkv) * 16 * d * 2};
   cuuint32_t box[4] = {64, 16, 1, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(cache), dims,
-                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = with_context([&] {
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(cache), dims,
+               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
   if (r != CUDA_SUCCESS) {
     t_last_cuda_error = static_cast<int>(r);
     return VSD_ERR_CUDA;
@@ -112,9 +127,11 @@ vsd_status make_means_map(CUtensorMap* map, const float* means, int d, long long
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(d) * 4};
   cuuint32_t box[2] = {32, 128};
   cuuint32_t estr[2] = {1, 1};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float*>(means), dims,
-                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = with_context([&] {
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float*>(means), dims,
+               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
   if (r != CUDA_SUCCESS) {
     t_last_cuda_error = static_cast<int>(r);
     return VSD_ERR_CUDA;
@@ -942,10 +959,12 @@ vsd_status make_code_map(CUtensorMap* map, const void* cache, const vsd_geom* g)
   cuuint64_t strides[3] = {d, 16 * d, static_cast<cuuint64_t>(g->Hkv) * 16 * d};
   cuuint32_t box[4] = {static_cast<cuuint32_t>(d), 16, 1, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(cache), dims, strides,
-                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = with_context([&] {
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(cache), dims, strides,
+               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
   if (r != CUDA_SUCCESS) {
     t_last_cuda_error = static_cast<int>(r);
     return VSD_ERR_CUDA;
