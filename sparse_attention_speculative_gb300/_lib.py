@@ -647,7 +647,9 @@ def vsd_sparse_decode_attn_step(q, k_cache, v_cache, block_table, idx, n_sel, ta
 
 # ------------------------------------------------------------------ 8-bit cache
 # The checks, outputs and scratch of these calls are in csrc/binding.cpp: they are made once
-# per layer and step, and their small ones run for a few microseconds on the GPU.
+# per layer and step, and their small ones run for a few microseconds on the GPU.  Scratch
+# that is not given is allocated for the call (in a capture by torch.cuda.graph, from the
+# graph's pool; a capture by other means takes a workspace of its caller's).
 _binding = None
 
 

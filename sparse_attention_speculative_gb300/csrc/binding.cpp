@@ -3,14 +3,12 @@
 //
 // The calls are made once per layer and step, and the smallest ones run for 2 to 6 us on the
 // GPU: reading some forty properties of ten tensors from Python, and passing twenty arguments
-// through ctypes, took longer than that (draft step 14.0 us a call on the host, 5.4 here; one token
-// stored 9.0, 3.1; a short verification 14.6, 5.9).
+// through ctypes, took longer than that (draft step 18.8 us a call on the host, 6.3 here; one token
+// stored 8.5, 2.9; a short verification 20.4, 7.1).
 #include <climits>
 #include <string>
-#include <unordered_map>
 
 #include <ATen/ATen.h>
-#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -157,11 +155,9 @@ struct Place {
   c10::cuda::CUDAGuard device;
   c10::cuda::OptionalCUDAStreamGuard on;
   cudaStream_t stream;
-  bool given;
 
   Place(const at::Tensor& first, PyObject* raw) : dev(first.get_device()), device(static_cast<c10::DeviceIndex>(dev)) {
-    given = raw != Py_None;
-    if (given) {
+    if (raw != Py_None) {
       stream = static_cast<cudaStream_t>(PyLong_AsVoidPtr(raw));
       if (PyErr_Occurred()) throw PythonError{};
       on.reset_stream(c10::cuda::getStreamFromExternal(stream, static_cast<c10::DeviceIndex>(dev)));
@@ -175,9 +171,13 @@ struct Place {
   }
 };
 
-// Scratch: the caller's, or, for an eager call on a current stream, one buffer of that
-// stream (its calls run one after the other and ignore what the buffer holds; an
-// allocation between two launches takes 6 us), else memory of the call's own.
+// Scratch: the caller's, or memory of the call's own.  A call is up to two launches that
+// hand partial results on through it, made with the interpreter's lock released: memory that
+// calls share would let a second thread's launch come between them (both threads on one
+// stream).  Memory of its own belongs to the call until both launches are made, and goes back
+// to its stream then; a captured call takes it from the graph's pool.  (One buffer kept for
+// each stream, with a lock over a call's launches, would save 1.2 us of host time; it would
+// keep the largest call's memory for good.)
 struct Scratch {
   void* at = nullptr;
   size_t bytes = 0;
@@ -191,18 +191,7 @@ struct Scratch {
     } else if (need_bytes == 0) {
       return;
     } else {
-      // (cudaStreamPerThread is one handle for a stream of every host thread)
-      const bool shared = !p.given && p.stream != reinterpret_cast<cudaStream_t>(2) &&
-                          c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None;
-      if (shared) {
-        static auto* buffers = new std::unordered_map<int, std::unordered_map<cudaStream_t, at::Tensor>>;
-        at::Tensor& mine = (*buffers)[p.dev][p.stream];
-        if (!mine.defined() || static_cast<size_t>(mine.numel()) < need_bytes)
-          mine = p.empty({static_cast<int64_t>(need_bytes)}, at::kByte);
-        keep = mine;
-      } else {
-        keep = p.empty({static_cast<int64_t>(need_bytes)}, at::kByte);
-      }
+      keep = p.empty({static_cast<int64_t>(need_bytes)}, at::kByte);
     }
     at = pointer(keep);
     bytes = keep.nbytes();
