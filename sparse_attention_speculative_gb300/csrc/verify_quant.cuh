@@ -291,12 +291,12 @@ __global__ void __launch_bounds__(kQThreads, 1)
   uint64_t* pv_done = p_full + 2;   // [2]
   uint64_t* sc_full = pv_done + 2;  // [kRounds] scales of a round ready
   uint64_t* sc_empty = sc_full + kRounds;
-  uint64_t* q_ready = sc_empty + kRounds;
-  uint64_t* mma_fin = q_ready + 1;    // every QK product complete
+  uint64_t* q_ready = sc_empty + kRounds;  // [2] a segment's queries stored, nan_rows reset: in turn
+  uint64_t* mma_fin = q_ready + 2;    // every QK product complete
   uint64_t* pv_fin = mma_fin + 1;     // every PV product complete
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 448);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 452);
-  static_assert((4 * ST + 6 + 2 * kRounds + 3) * 8 <= 448, "barriers");
+  static_assert((4 * ST + 6 + 2 * kRounds + 4) * 8 <= 448, "barriers");
   float* quni_s = reinterpret_cast<float*>(misc + 456);        // 1 / query scale of all rows, or 0
   float* m2s = reinterpret_cast<float*>(misc + 512);           // [2][64] references
   float* alphas = m2s + 128;                                   // [2][64] rescale factors
@@ -327,12 +327,12 @@ __global__ void __launch_bounds__(kQThreads, 1)
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], kGroupThreads + kWidenThreads);
       mbar_init(&pv_done[i], 1);
+      mbar_init(&q_ready[i], kSoftThreads);
     }
     for (int i = 0; i < kRounds; ++i) {
       mbar_init(&sc_full[i], 1);
       mbar_init(&sc_empty[i], 2);  // one thread of each softmax group
     }
-    mbar_init(q_ready, kSoftThreads);
     mbar_init(mma_fin, 1);
     mbar_init(pv_fin, 1);
     *abort_flag = 0;
@@ -458,7 +458,8 @@ __global__ void __launch_bounds__(kQThreads, 1)
     Seg s;
     for (auto w = walk_of(); ok && w.next(s);) {
       if (s.t_begin >= s.t_end) continue;
-      ok = mbar_wait_compact(q_ready, nseg & 1, abort_flag);  // (the last segment's products are done)
+      // (the last segment's products are done)
+      ok = mbar_wait_compact(&q_ready[nseg & 1], (nseg >> 1) & 1, abort_flag);
       ++nseg;
       for (int tile = s.t_begin; tile < s.t_end; ++tile, ++i) {
         const uint32_t stage = i % ST, buf = i & 1;
@@ -560,7 +561,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
     Seg s;
     for (auto walk = walk_of(); walk.next(s);) {
       if (s.t_begin >= s.t_end) continue;
-      const uint32_t seg_parity = nseg++ & 1;
+      const uint32_t seg = nseg++;
       for (int tile = s.t_begin; tile < s.t_end; ++tile, ++it) {
         const int stage = it % ST;
         if (warp == kWidenWarp &&
@@ -589,8 +590,11 @@ __global__ void __launch_bounds__(kQThreads, 1)
           }
           if (nan & 0x80808080u) {
             // rare: clean the row in shared memory, once the softmax threads have reset
-            // nan_rows for this segment
-            if (!mbar_wait_compact(q_ready, seg_parity, abort_flag)) set_abort();
+            // nan_rows for this segment.  They may be two segments behind (the PV product of
+            // the last tile but one is done, its segment's end may be pending), so two
+            // barriers take turns: on a single one the segment before the last has this one's
+            // parity, and the wait would be over at once.
+            if (!mbar_wait_compact(&q_ready[seg & 1], (seg >> 1) & 1, abort_flag)) set_abort();
 #pragma unroll 1
             for (int c = 0; c < D; ++c) {
               uint8_t* at = src + swizzled_chunk<D>(row, c >> 4) + (c & 15);
@@ -641,7 +645,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
     const bool collect = a.logits != nullptr || a.partial != nullptr;
     const int ccol = (half == 0 ? a.row0 : a.row1) << qa.gshift;  // the half's collected row
     uint8_t* const prow = p_smem + (Cfg::kSplitP ? 0 : grp * kTile * 128);
-    uint32_t it = 0, round = 0;
+    uint32_t it = 0, round = 0, nseg = 0;
     // queries of a (sequence, KV group): row r = t * G + hl, 8 dimensions of a row a thread;
     // those of the next part are in flight during the end of the last one
     constexpr int kCh = D / 8;
@@ -722,7 +726,8 @@ __global__ void __launch_bounds__(kQThreads, 1)
         if (ts < D) nan_rows[ts] = 0u;
         if (ts == 0) *quni_s = quni;
         fence_proxy_async_smem();
-        mbar_arrive(q_ready);
+        mbar_arrive(&q_ready[nseg & 1]);
+        ++nseg;
         soft_sync();  // qinv, m2s
       }
 

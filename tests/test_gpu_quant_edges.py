@@ -149,3 +149,60 @@ def test_calls_keep_no_memory(vsd):
     stream.synchronize()
     assert torch.cuda.memory_allocated() == before
     assert vsd.vsd_read_device_status() == 0
+
+
+# ------------------------------------------------------------------ NaN and infinities
+def attend(cache, prefix, q, Hkv, scale):
+    """The verification's outputs in 64 bits: [B, R, Hq, d].  Nothing of a key that a row does
+    not see enters it; a NaN in what it sees does."""
+    B, R, Hq, d = q.shape
+    out = torch.zeros((B, R, Hq, d), dtype=torch.float64)
+    mag = torch.zeros_like(out)
+    for b in range(B):
+        k, v = cache.kv(b, torch.arange(prefix[b] + R))
+        for h in range(Hq):
+            g = h // (Hq // Hkv)
+            for t in range(R):
+                n = prefix[b] + t + 1
+                out[b, t, h], mag[b, t, h] = ref.softmax_av(scale * (k[:n, g] @ q[b, t, h].double()), v[:n, g])
+    return out, mag
+
+
+def assert_outputs(got, want, mag):
+    """NaN exactly where the definition has it, the others within the bound."""
+    got = got.cpu().double()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    fin = ~torch.isnan(want)
+    assert torch.all((got - want).abs()[fin] <= ref.out_bound(want, mag)[fin])
+
+
+@pytest.mark.parametrize("B,Hkv,d,longest", [(64, 8, 64, 120), (64, 8, 128, 120), (70, 8, 64, 300), (300, 2, 64, 100),
+                                             (3, 2, 64, 500)])
+def test_verify_nan_values_reach_the_rows_that_see_them(vsd, B, Hkv, d, longest):
+    """NaN codes in the values of every third pair's verify block, in another row and
+    dimension each, and of a few pairs' prefixes: the outputs are NaN in the rows and
+    dimensions that see one, and nowhere else.  Most sequences are one or two tiles, so that a
+    CTA walks several pairs."""
+    R, G = 3, 2
+    g = torch.Generator().manual_seed(B + d)
+    prefix = torch.randint(0, longest - R, (B,), generator=g).tolist()
+    cache = ref.Cache([p + R for p in prefix], Hkv, d, seed=B * 3 + d)
+    for pair in range(0, B * Hkv, 3):
+        b, h = pair // Hkv, pair % Hkv
+        j = prefix[b] + pair % R
+        cache.codes[1][int(cache.table[b, j // 16]), h, j % 16, (pair * 7) % d] = ref.NAN_CODE + 128 * (pair & 1)
+    for pair in range(1, B * Hkv, 50):
+        b, h = pair // Hkv, pair % Hkv
+        if prefix[b]:
+            j = (pair * 5) % prefix[b]
+            cache.codes[1][int(cache.table[b, j // 16]), h, j % 16, pair % d] = ref.NAN_CODE
+    q = torch.randn((B, R, Hkv * G, d), generator=g).bfloat16()
+    args, pl, qc = cache.cuda(), i32(prefix), q.cuda()
+    out = [vsd.vsd_verify_attn_collect_quant(qc, *args, pl, P_max=longest, scale=0.125, collect=False)[0]
+           for _ in range(20)]
+    assert vsd.vsd_read_device_status() == 0
+    want, mag = attend(cache, prefix, q, Hkv, 0.125)
+    assert torch.isnan(want).any() and not torch.isnan(want).all()
+    assert_outputs(out[0], want, mag)
+    for o in out[1:]:
+        assert torch.equal(o.view(torch.int16), out[0].view(torch.int16))
