@@ -101,8 +101,8 @@ struct SqSmem {
   static constexpr int kOffP = 0;  // in the place of the keys, which have been read by then
   static constexpr int kOffQ = 2 * kTileBytes;
   static constexpr int kOffRed = kOffQ + 2 * kCols * D;    // [2][4][kCols] floats
-  static constexpr int kOffQinv = kOffRed + 2 * 4 * kCols * 4;
-  static constexpr int kOffBar = kOffQinv + kCols * 4;
+  static constexpr int kOffQlog = kOffRed + 2 * 4 * kCols * 4;
+  static constexpr int kOffBar = kOffQlog + kCols * 4;
   static constexpr int kUsed = kOffBar + 64;
   // d = 64: the PV product reads 8 KB past the value tile (rows of the accumulator that are
   // never used), inside this allocation
@@ -146,7 +146,8 @@ __global__ void __launch_bounds__(kSqThreads, G == 16 ? 3 : 6) sparse_quant_kern
   uint8_t* const v_s = sparse_quant_smem + Sm::kOffV;
   uint8_t* const q_s = sparse_quant_smem + Sm::kOffQ;
   float* const red = reinterpret_cast<float*>(sparse_quant_smem + Sm::kOffRed);
-  float* const qinv = reinterpret_cast<float*>(sparse_quant_smem + Sm::kOffQinv);
+  // scale log2 e / query scale of a row
+  float* const qlog = reinterpret_cast<float*>(sparse_quant_smem + Sm::kOffQlog);
   uint64_t* const bar_s = reinterpret_cast<uint64_t*>(sparse_quant_smem + Sm::kOffBar);
   uint64_t* const bar_o = bar_s + 1;
   uint64_t* const bar_fin = bar_s + 2;  // every product of this CTA complete
@@ -276,7 +277,7 @@ __global__ void __launch_bounds__(kSqThreads, G == 16 ? 3 : 6) sparse_quant_kern
           for (int o = kCh / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
           const QScale qs = query_scale(mx);
           if (G * kCh % 32 != 0 && r >= G) break;
-          if (c == 0) qinv[r] = qs.inv;
+          if (c == 0) qlog[r] = a.scale * kLog2e * qs.inv;
           uint32_t qh[4], ql[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) query_parts(bf16_lo(w[k]), bf16_hi(w[k]), qs.f, qh[k], ql[k]);
@@ -312,10 +313,11 @@ __global__ void __launch_bounds__(kSqThreads, G == 16 ? 3 : 6) sparse_quant_kern
         ptx::tmem_ld<G>(tmem + lane_addr + GP, reinterpret_cast<uint32_t*>(sl));
         ptx::tmem_wait_ld();
         const float vsf = fmaxf(vs, kMinVScale);
-        const float zl = ks * a.scale * kLog2e, lvs = lg2(vsf);
+        const float lvs = lg2(vsf);
 #pragma unroll
         for (int h = 0; h < G; ++h) {
-          y[h] = row >= 0 ? __fmaf_rn(fmaf(sl[h], kQLo, sh[h]) * qinv[h], zl, lvs) : -INFINITY;
+          // (the scales meet first: a large query's product alone may leave fp32's range)
+          y[h] = row >= 0 ? __fmaf_rn(fmaf(sl[h], kQLo, sh[h]), ks * qlog[h], lvs) : -INFINITY;
           const float wm = warp_max_f32(fmaxf(y[h], kSqNoMax));
           if (lane == 0) red[warp * GP + h] = wm;
         }

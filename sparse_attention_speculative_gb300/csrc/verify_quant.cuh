@@ -300,8 +300,9 @@ __global__ void __launch_bounds__(kQThreads, 1)
   float* quni_s = reinterpret_cast<float*>(misc + 456);        // 1 / query scale of all rows, or 0
   float* m2s = reinterpret_cast<float*>(misc + 512);           // [2][64] references
   float* alphas = m2s + 128;                                   // [2][64] rescale factors
-  float* qinv = alphas + 128;                                  // [64] 1 / query scale of a row
-  float* red = qinv + 64;                                      // [2][4][64] reductions
+  float* qinv = alphas + 128;                                  // [64] scale / query scale of a row
+  float* qlog = qinv + 64;                                     // [64] the same times log2 e
+  float* red = qlog + 64;                                      // [2][4][64] reductions
   uint32_t* qmax = reinterpret_cast<uint32_t*>(red + 512);     // [64] largest |q| of a row, as bf16 bits
   uint32_t* nan_rows = qmax + 64;                              // [D] verify-block rows with a NaN
   // [kRounds][3][32] per page: key scale, log2 and inverse of the value scale
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
   float* sc_s = xsum + 2 * kTile;
   int* cum_s = reinterpret_cast<int*>(sc_s + kRounds * 96);    // first tile of each sequence
   int* plen_s = cum_s + kTableSeqs + 1;
-  static_assert(512 + (128 * 2 + 64 + 512 + 64 + 128 + 2 * kTile + kRounds * 96 + 2 * kTableSeqs + 1) * 4 <=
+  static_assert(512 + (128 * 2 + 128 + 512 + 64 + 128 + 2 * kTile + kRounds * 96 + 2 * kTableSeqs + 1) * 4 <=
                     Cfg::kMiscBytes,
                 "misc area");
 
@@ -710,7 +711,10 @@ __global__ void __launch_bounds__(kQThreads, 1)
             const int r = idx / kCh, ch = idx % kCh;
             const uint32_t w[4] = {qv[u].x, qv[u].y, qv[u].z, qv[u].w};
             const QScale qs = uniform ? qu : query_scale(qmax[r]);
-            if (ch == 0) qinv[r] = qs.inv;
+            if (ch == 0) {
+              qinv[r] = a.scale * qs.inv;
+              qlog[r] = a.scale * kLog2e * qs.inv;
+            }
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -734,7 +738,9 @@ __global__ void __launch_bounds__(kQThreads, 1)
       // where this thread's key 0 of the pair has its logits (head 0) and partial sum
       const size_t lg_off = ((static_cast<size_t>(s.b) * 2 + half) * a.Hq + s.g * G) * a.P_max + row;
       const size_t part_off = (static_cast<size_t>(s.b) * a.Hkv + s.g) * a.P_max + row;
-      const float zq = a.scale * kLog2e * (quni == 0.f ? 1.f : quni);
+      // the logits' factors but for the page's: the scales meet before the products, which
+      // would leave fp32's range where a large query meets small key scales
+      const float zq = a.scale * kLog2e * quni, zqs = a.scale * quni;
       const int n = s.t_end - s.t_begin;
       const int k0 = (it0 & 1) == static_cast<uint32_t>(grp) ? 0 : 1;  // this group's first tile
       for (int k = k0; k < n; k += 2) {
@@ -754,7 +760,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
         if (!ok) set_abort();
         group_sync(grp);
         const float* sc = sc_s + slot * 96 + (k & 3) * kPagesPerTile + row / kPage;
-        const float zl = sc[0] * zq, lvs = sc[32], ivs = sc[64];
+        const float ks = sc[0], zl = ks * zq, lvs = sc[32], ivs = sc[64];
         tc_fence_after();
         float y[NC];  // z log2 e + log2 vs, then its distance to the references
         // From the two parts' logits of this thread's columns in TMEM; hidden ones are -inf.
@@ -771,10 +777,11 @@ __global__ void __launch_bounds__(kQThreads, 1)
             for (int i = 0; i < 8; ++i) y[c0 + i] = fmaf(lo[i], kQLo, hi[i]);
             if (quni == 0.f) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) y[c0 + i] *= qinv[col0 + c0 + i];
-            }
+              for (int i = 0; i < 8; ++i) y[c0 + i] = __fmaf_rn(y[c0 + i], ks * qlog[col0 + c0 + i], lvs);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[c0 + i] = __fmaf_rn(y[c0 + i], zl, lvs);
+              for (int i = 0; i < 8; ++i) y[c0 + i] = __fmaf_rn(y[c0 + i], zl, lvs);
+            }
           }
           if ((tile + 1) * kTile > s.P) {  // keys of the verify block, or past the end
             const int j = tile * kTile + row;
@@ -803,7 +810,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
         float csum = 0.f;
         const bool counted = collect && tile * kTile + row < s.P;
         if (collect) {
-          const float zs = sc[0] * a.scale * (quni == 0.f ? 1.f : quni);
+          const float zs = ks * zqs;
           float* lg = a.logits + lg_off + tile * kTile;
           const auto heads = [&](auto width) {  // kH heads at a time
             constexpr int kH = decltype(width)::value;
@@ -816,8 +823,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
               if (counted) {
 #pragma unroll
                 for (int i = 0; i < kH; ++i) {
-                  float z = fmaf(lo[i], kQLo, hi[i]) * zs;
-                  if (quni == 0.f) z *= qinv[ccol + h + i];
+                  const float z = fmaf(lo[i], kQLo, hi[i]) * (quni == 0.f ? ks * qinv[ccol + h + i] : zs);
                   if (a.logits != nullptr) __stcs(lg, z);
                   lg += a.P_max;
                   csum += z;

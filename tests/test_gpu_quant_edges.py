@@ -206,3 +206,36 @@ def test_verify_nan_values_reach_the_rows_that_see_them(vsd, B, Hkv, d, longest)
     assert_outputs(out[0], want, mag)
     for o in out[1:]:
         assert torch.equal(o.view(torch.int16), out[0].view(torch.int16))
+
+
+# ------------------------------------------------------------------ ends of the ranges
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_queries_meet_small_key_scales(vsd, d):
+    """Query rows from 2^-60 to bf16's last binade in one group, key scales near 2^-125: the
+    logits are of order one, and no factor of theirs overflows on the way."""
+    R, Hq, Hkv, P = 3, 4, 2, 300
+    cache = ref.Cache([P + R], Hkv, d, seed=d + 5)
+    for s in cache.scales[0]:
+        s *= 2.0 ** -118
+    q = torch.randn((1, R, Hq, d), generator=cache.gen)
+    q = q.sign() * 2.0 ** 127
+    q[0, 1, 1] *= 2.0 ** -127
+    q[0, 2] *= 2.0 ** -100
+    q[0, 0, 3] *= 2.0 ** -187
+    q = q.bfloat16()
+    for rows in (q, q[:, :, ::3].repeat_interleave(2, dim=2), q[:, :1].expand(1, R, Hq, d).contiguous()):
+        logits = torch.zeros((1, 2, Hq, P), device="cuda")
+        out = vsd.vsd_verify_attn_collect_quant(rows.cuda(), *cache.cuda(), i32([P]), P_max=P, scale=2.0 ** -12,
+                                                logits=logits)[0]
+        drafts = vsd.vsd_sparse_decode_attn_quant(rows[:, R - 1].contiguous().cuda(), *cache.cuda(), None, None,
+                                                  i32([0]), i32([P + R]), scale=2.0 ** -12, max_tail=P + R)
+        assert vsd.vsd_read_device_status() == 0
+        want, mag = attend(cache, [P], rows, Hkv, 2.0 ** -12)
+        assert_outputs(out, want, mag)
+        assert_outputs(drafts, want[:, R - 1], mag[:, R - 1])
+        k = cache.kv(0, torch.arange(P))[0]
+        for c, t in ((0, 0), (1, R - 1)):
+            for h in range(Hq):
+                x = rows[0, t, h].double()
+                err = (logits[0, c, h].cpu().double() - 2.0 ** -12 * (k[:, h // 2] @ x)).abs()
+                assert torch.all(err <= ref.logit_bound(x, k[:, h // 2], 2.0 ** -12))
