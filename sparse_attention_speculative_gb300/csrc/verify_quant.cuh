@@ -697,11 +697,12 @@ __global__ void __launch_bounds__(kQThreads, 1)
         }
         soft_sync();
         // one scale for rows whose largest magnitudes lie within 2^4 of each other (rows of
-        // zeros fit any): the logits then need no factor per column
+        // zeros fit any): the logits then need no factor per column.  A NaN or an infinity
+        // makes its own row NaN: it never sets the others' scale.
         const uint32_t r0 = lane < NQ ? qmax[lane] : 0u, r1 = lane + 32 < NQ ? qmax[lane + 32] : 0u;
         const uint32_t top = __reduce_max_sync(0xffffffffu, max(r0, r1));
         const uint32_t low = __reduce_min_sync(0xffffffffu, min(r0 ? r0 : 0xFFFFu, r1 ? r1 : 0xFFFFu));
-        const bool uniform = top == 0u || (top >> 7) - (low >> 7) <= 4u;
+        const bool uniform = top == 0u || (top < 0x7F80u && (top >> 7) - (low >> 7) <= 4u);
         const QScale qu = query_scale(top);
         quni = uniform ? qu.inv : 0.f;
 #pragma unroll

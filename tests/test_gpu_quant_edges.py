@@ -208,6 +208,41 @@ def test_verify_nan_values_reach_the_rows_that_see_them(vsd, B, Hkv, d, longest)
         assert torch.equal(o.view(torch.int16), out[0].view(torch.int16))
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("others", ["zeros", "ordinary", "largest"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_nan_or_an_infinity_in_a_query_row_stays_in_it(vsd, bad, others, d):
+    """The row that holds it becomes NaN, outputs and logits; the rows beside it do not, be they
+    zeros (they average the values), ordinary or within a few binades of the largest."""
+    R, Hq, Hkv, P = 3, 4, 2, 150
+    cache = ref.Cache([P + R], Hkv, d, seed=d)
+    q = torch.zeros((1, R, Hq, d))
+    if others != "zeros":
+        q = torch.randn((1, R, Hq, d), generator=cache.gen)
+        if others == "largest":
+            q = q.sign() * 2.0 ** 127
+            for s in cache.scales[0]:
+                s *= 2.0 ** -118
+    q = q.bfloat16()
+    q[0, 1, 2, 17] = bad
+    logits = torch.zeros((1, 2, Hq, P), device="cuda")
+    out, lg, _ = vsd.vsd_verify_attn_collect_quant(q.cuda(), *cache.cuda(), i32([P]), P_max=P, scale=2.0 ** -12,
+                                                   row0=0, row1=1, logits=logits)
+    drafts = vsd.vsd_sparse_decode_attn_quant(q[:, 1].contiguous().cuda(), *cache.cuda(), None, None, i32([0]),
+                                              i32([P + 2]), scale=2.0 ** -12, max_tail=P + 2)
+    assert vsd.vsd_read_device_status() == 0
+    mine = torch.zeros((1, R, Hq), dtype=torch.bool)
+    mine[0, 1, 2] = True
+    want, mag = attend(cache, [P], torch.where(mine[..., None], torch.zeros_like(q), q), Hkv, 2.0 ** -12)
+    want[mine] = float("nan")
+    assert_outputs(out, want, mag)
+    assert_outputs(drafts, want[:, 1], mag[:, 1])
+    nan = torch.isnan(lg.cpu())
+    assert nan[0, 1, 2].all() and nan.sum() == P
+    if others == "zeros":
+        assert torch.all(lg.cpu()[~nan] == 0)
+
+
 # ------------------------------------------------------------------ ends of the ranges
 @pytest.mark.parametrize("d", [64, 128])
 def test_large_queries_meet_small_key_scales(vsd, d):
