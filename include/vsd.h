@@ -586,8 +586,10 @@ vsd_status vsd_advance_lengths(int B, int gamma, const int32_t* accepted, int ma
  * vsd_read_kv_quant: the rows at the same positions as bf16,
  *   k_out[b][t], v_out[b][t] = bf16(code * scale)   [B][n][Hkv][head_dim], t < n_valid[b]
  * Rows that are skipped (as above) or lie behind n_valid are left as they were.
+ * vsd_read_kv_quant_zeroed: the same, and of the outputs that `zeroed` names (VSD_READ_ZEROED_K,
+ * VSD_READ_ZEROED_V) those rows become zeros: for memory whose contents must not show.
  *
- * Both are programmatic dependents of the preceding kernel on the stream.  Pointers
+ * All are programmatic dependents of the preceding kernel on the stream.  Pointers
  * 16-byte aligned (scales and int32 arrays 4-byte); head_dim 64 or 128.
  * ------------------------------------------------------------------------------ */
 vsd_status vsd_append_kv_quant(const vsd_geom* geom, int n_new, const void* k_new,
@@ -601,6 +603,15 @@ vsd_status vsd_read_kv_quant(const vsd_geom* geom, int n, const void* k_cache,
                              const int32_t* block_table, const int32_t* pos_base,
                              int pos_offset, const int32_t* n_valid, void* k_out, void* v_out,
                              void* stream);
+
+#define VSD_READ_ZEROED_K 0x1u
+#define VSD_READ_ZEROED_V 0x2u
+vsd_status vsd_read_kv_quant_zeroed(const vsd_geom* geom, int n, const void* k_cache,
+                                    const void* v_cache, const float* k_scale,
+                                    const float* v_scale, const int32_t* block_table,
+                                    const int32_t* pos_base, int pos_offset,
+                                    const int32_t* n_valid, void* k_out, void* v_out,
+                                    unsigned zeroed, void* stream);
 
 /* ------------------------------------------------------------------------------
  * Verification attention with Collect-2-Query over the 8-bit cache (with R = 1: the

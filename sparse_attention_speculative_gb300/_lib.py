@@ -95,6 +95,8 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         lib.vsd_advance_lengths.argtypes = [I, I, P, I, P, P, P, I, P, P]
         lib.vsd_append_kv_quant.argtypes = [P, I, P, P, P, P, I, P, P, P, P, P, P]
         lib.vsd_read_kv_quant.argtypes = [P, I, P, P, P, P, P, P, I, P, P, P, P]
+        lib.vsd_read_kv_quant_zeroed.argtypes = [P, I, P, P, P, P, P, P, I, P, P, P,
+                                                 ctypes.c_uint, P]
         lib.vsd_verify_quant_workspace_size.argtypes = [P, I, I, ctypes.POINTER(SZ)]
         lib.vsd_verify_attn_collect_quant.argtypes = [P, I, P, P, P, P, P, P, P, I, I, I, F, P,
                                                       P, P, P, I, I, P, P, SZ, P]
@@ -115,7 +117,8 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                      "vsd_select_workspace_size", "vsd_select_topk", "vsd_sparse_workspace_size",
                      "vsd_sparse_decode_attn", "vsd_page_key_means", "vsd_block_topk",
                      "vsd_verify_attn_collect_scored", "vsd_select_topk_scored", "vsd_copy",
-                     "vsd_append_kv_quant", "vsd_read_kv_quant", "vsd_verify_quant_workspace_size",
+                     "vsd_append_kv_quant", "vsd_read_kv_quant", "vsd_read_kv_quant_zeroed",
+                     "vsd_verify_quant_workspace_size",
                      "vsd_verify_attn_collect_quant", "vsd_sparse_quant_workspace_size",
                      "vsd_sparse_decode_attn_quant",
                      "vsd_append_kv", "vsd_advance_lengths", "vsd_sparse_decode_attn_step",
@@ -663,8 +666,9 @@ def _bound():
         raise RuntimeError("_binding.so is not built or does not fit this torch; run "
                            "`python -m sparse_attention_speculative_gb300.build`") from e
     module.attach(VsdError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
-        lib.vsd_append_kv_quant, lib.vsd_read_kv_quant, lib.vsd_verify_quant_workspace_size,
-        lib.vsd_verify_attn_collect_quant, lib.vsd_sparse_quant_workspace_size,
+        lib.vsd_append_kv_quant, lib.vsd_read_kv_quant_zeroed,
+        lib.vsd_verify_quant_workspace_size, lib.vsd_verify_attn_collect_quant,
+        lib.vsd_sparse_quant_workspace_size,
         lib.vsd_sparse_decode_attn_quant)))
     _binding = module
     return module
@@ -689,8 +693,9 @@ def vsd_append_kv_quant(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_
 def vsd_read_kv_quant(k_cache, v_cache, k_scale, v_scale, block_table, pos_base, *, n: int,
                       pos_offset: int = 0, n_valid=None, k_out=None, v_out=None, stream=None):
     """The rows at positions pos_base[b] + pos_offset + t, t < n_valid[b] (None: n), of an
-    8-bit cache as bf16 [B, n, Hkv, d].  Rows behind n_valid are left as they were in
-    k_out, v_out (zeros when allocated here).  Returns (k_out, v_out)."""
+    8-bit cache as bf16 [B, n, Hkv, d].  Rows behind n_valid, and those that are skipped
+    because their range or block is bad, are left as they were in k_out, v_out, and zeros
+    in outputs that are allocated here.  Returns (k_out, v_out)."""
     return (_binding or _bound()).read(k_cache, v_cache, k_scale, v_scale, block_table, pos_base,
                                        n, pos_offset, n_valid, k_out, v_out, _handle(stream))
 

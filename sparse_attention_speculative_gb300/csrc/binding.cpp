@@ -23,7 +23,7 @@ constexpr int64_t kHistBins = 4096;  // of a scored verification's histogram
 // ---------------------------------------------------------------- the library's calls
 struct Calls {
   decltype(&vsd_append_kv_quant) append = nullptr;
-  decltype(&vsd_read_kv_quant) read = nullptr;
+  decltype(&vsd_read_kv_quant_zeroed) read = nullptr;
   decltype(&vsd_verify_quant_workspace_size) verify_size = nullptr;
   decltype(&vsd_verify_attn_collect_quant) verify = nullptr;
   decltype(&vsd_sparse_quant_workspace_size) sparse_size = nullptr;
@@ -204,8 +204,7 @@ struct Output {
   at::Tensor made;
   void* at = nullptr;
 
-  void take(PyObject* given, const Place& p, at::ScalarType type, at::IntArrayRef shape, const char* name,
-            bool zeros = false) {
+  void take(PyObject* given, const Place& p, at::ScalarType type, at::IntArrayRef shape, const char* name) {
     if (given != Py_None) {
       object = given;
       const at::Tensor& t = as_tensor(given, name);
@@ -213,7 +212,6 @@ struct Output {
       at = pointer(t);
     } else {
       made = p.empty(shape, type);
-      if (zeros) made.zero_();
       at = pointer(made);
     }
   }
@@ -298,10 +296,13 @@ PyObject* py_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g.B = dim_of(B, "B");
     g.Hq = g.Hkv;
     Output ko, vo;
-    ko.take(a[9], p, at::kBFloat16, {B, rows, g.Hkv, g.head_dim}, "k_out", nv != nullptr);
-    vo.take(a[10], p, at::kBFloat16, {B, rows, g.Hkv, g.head_dim}, "v_out", nv != nullptr);
+    ko.take(a[9], p, at::kBFloat16, {B, rows, g.Hkv, g.head_dim}, "k_out");
+    vo.take(a[10], p, at::kBFloat16, {B, rows, g.Hkv, g.head_dim}, "v_out");
+    // (what a new output's memory held before must not show in the rows that are skipped)
+    const unsigned zeroed = (ko.made.defined() ? VSD_READ_ZEROED_K : 0u) | (vo.made.defined() ? VSD_READ_ZEROED_V : 0u);
     check(without_gil([&] {
-            return g_calls.read(&g, rows, c.k, c.v, c.ks, c.vs, bt, pos, offset, nv, ko.at, vo.at, p.stream);
+            return g_calls.read(&g, rows, c.k, c.v, c.ks, c.vs, bt, pos, offset, nv, ko.at, vo.at, zeroed,
+                                p.stream);
           }),
           "vsd_read_kv_quant");
     return Py_BuildValue("(NN)", ko.result(), vo.result());

@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kRowThreads = 128;
 constexpr int kRowWarps = kRowThreads / 32;
-constexpr int kPageQ = 16;
+constexpr int kPageQ = 16;  // (2^4)
 
 struct RowsParams {
   const uint16_t* src[2];  // append: bf16 rows of K, V
@@ -99,6 +99,9 @@ struct PageUnit {
   RowRange rr;
 };
 
+// kBelow: pages are counted down from a position below 0 too (its range is skipped, but the
+// n rows of the output are to be numbered).
+template <bool kBelow = false>
 __device__ __forceinline__ PageUnit page_unit(const RowsParams& a, unsigned u, int lane) {
   PageUnit p;
   const unsigned r1 = u / a.Hkv;
@@ -108,7 +111,7 @@ __device__ __forceinline__ PageUnit page_unit(const RowsParams& a, unsigned u, i
   p.b = static_cast<int>(r2 / a.pages);
   const int pg = static_cast<int>(r2 - static_cast<unsigned>(p.b) * a.pages);
   p.rr = row_range(a, p.b, lane == 0 && p.kv == 0 && g == 0 && pg == 0);
-  const long long lp = p.rr.p0 / kPageQ + pg;
+  const long long lp = (kBelow ? p.rr.p0 >> 4 : p.rr.p0 / kPageQ) + pg;
   p.lo = lp * kPageQ;
   p.s0 = static_cast<int>(p.rr.p0 > p.lo ? p.rr.p0 - p.lo : 0);
   const long long left = p.rr.p0 + p.rr.count - p.lo;
@@ -225,7 +228,10 @@ __global__ void __launch_bounds__(kRowThreads, 8) append_kv_quant_kernel(const R
   if (lane == 0 && (s0 == 0 || now != was)) of(a.scale, pu.kv)[pu.ph] = now;
 }
 
-template <int D>
+// kZeroed: the outputs (1: K, 2: V) in which rows that are not read become zeros.  (A parameter
+// of the kernel: as a choice at run time it cost the others 2.5 %, 65.7 -> 67.4 us for the
+// size above.)
+template <int D, unsigned kZeroed>
 __global__ void __launch_bounds__(kRowThreads) read_kv_quant_kernel(const RowsParams a) {
   constexpr int LPR = D / 16;          // lanes of a row: 16 codes each
   constexpr int RPI = 32 / LPR;
@@ -236,8 +242,9 @@ __global__ void __launch_bounds__(kRowThreads) read_kv_quant_kernel(const RowsPa
   const int sub = lane / LPR, lr = lane % LPR;
   const unsigned u = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
   if (u >= a.units) return;
-  const PageUnit pu = page_unit(a, u, lane);
-  if (pu.s1 <= pu.s0) return;
+  const PageUnit pu = page_unit<kZeroed != 0u>(a, u, lane);
+  const bool zeroed = (kZeroed >> pu.kv & 1u) != 0u;
+  if (pu.s1 <= pu.s0 && !zeroed) return;
   const uint8_t* page = of(a.cache, pu.kv) + pu.ph * (kPageQ * D) + lr * 16;
   uint4 x[NI];
 #pragma unroll
@@ -246,7 +253,7 @@ __global__ void __launch_bounds__(kRowThreads) read_kv_quant_kernel(const RowsPa
     x[i] = make_uint4(0, 0, 0, 0);
     if (slot >= pu.s0 && slot < pu.s1) x[i] = ldg_stream16(page + slot * D);
   }
-  const float s = __ldcg(of(a.scale, pu.kv) + pu.ph);
+  const float s = __ldcg(of(a.scale, pu.kv) + pu.ph);  // (page 0's where there are no rows: not used)
   const int g = static_cast<int>(u % a.Hkv);
   uint16_t* dst = of(a.dst, pu.kv) + ((static_cast<size_t>(pu.b) * a.n) * a.Hkv + g) * D + lr * 16;
   const auto two = [s](uint32_t codes) {
@@ -263,6 +270,16 @@ __global__ void __launch_bounds__(kRowThreads) read_kv_quant_kernel(const RowsPa
       uint4* to = reinterpret_cast<uint4*>(dst + static_cast<size_t>(pu.lo + slot - pu.rr.p0) * a.Hkv * D);
       __stcs(to, four(x[i].x, x[i].y));
       __stcs(to + 1, four(x[i].z, x[i].w));
+    }
+  }
+  if (!zeroed) return;
+#pragma unroll 1
+  for (int slot = sub; slot < kPageQ; slot += RPI) {
+    const long long t = pu.lo + slot - pu.rr.p0;  // row of the output
+    if ((slot < pu.s0 || slot >= pu.s1) && t >= 0 && t < a.n) {
+      uint4* to = reinterpret_cast<uint4*>(dst + static_cast<size_t>(t) * a.Hkv * D);
+      __stcs(to, make_uint4(0, 0, 0, 0));
+      __stcs(to + 1, make_uint4(0, 0, 0, 0));
     }
   }
 }
@@ -306,6 +323,12 @@ cudaError_t launch_rows(Kernel kern, const RowsParams& p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+template <unsigned kZeroed>
+cudaError_t launch_read(const RowsParams& p, int d, cudaStream_t stream) {
+  return d == 128 ? launch_rows(read_kv_quant_kernel<128, kZeroed>, p, stream)
+                  : launch_rows(read_kv_quant_kernel<64, kZeroed>, p, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_append_kv_quant(const QuantRowsArgs& x, cudaStream_t stream) {
@@ -316,8 +339,13 @@ cudaError_t launch_append_kv_quant(const QuantRowsArgs& x, cudaStream_t stream) 
 
 cudaError_t launch_read_kv_quant(const QuantRowsArgs& x, cudaStream_t stream) {
   const RowsParams p = rows_params(x);
-  return x.d == 128 ? launch_rows(read_kv_quant_kernel<128>, p, stream)
-                    : launch_rows(read_kv_quant_kernel<64>, p, stream);
+  switch (x.zeroed) {
+    case 0u: return launch_read<0u>(p, x.d, stream);
+    case 1u: return launch_read<1u>(p, x.d, stream);
+    case 2u: return launch_read<2u>(p, x.d, stream);
+    case 3u: return launch_read<3u>(p, x.d, stream);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace vsd

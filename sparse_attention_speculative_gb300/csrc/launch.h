@@ -227,6 +227,7 @@ struct QuantRowsArgs {
   const int32_t* n_valid;       // [B] rows of each sequence, or null (all n)
   unsigned* status;
   int B, n, Hkv, d, max_blocks, num_blocks, pos_offset;
+  unsigned zeroed = 0;          // read: outputs whose skipped rows become zeros (1: K, 2: V)
 };
 
 // Pages that n >= 1 rows of one sequence can meet.  The kernels number 2 * B * pages * Hkv

@@ -1037,20 +1037,33 @@ vsd_status vsd_append_kv_quant(const vsd_geom* geom, int n_new, const void* k_ne
   return e == cudaSuccess ? VSD_OK : cuda_fail(e);
 }
 
+vsd_status vsd_read_kv_quant_zeroed(const vsd_geom* geom, int n, const void* k_cache,
+                                    const void* v_cache, const float* k_scale,
+                                    const float* v_scale, const int32_t* block_table,
+                                    const int32_t* pos_base, int pos_offset,
+                                    const int32_t* n_valid, void* k_out, void* v_out,
+                                    unsigned zeroed, void* stream) {
+  vsd::QuantRowsArgs a;
+  bool run = false;
+  vsd_status st = quant_rows(geom, n, k_out, v_out, block_table, pos_base, pos_offset, n_valid,
+                             k_cache, v_cache, k_scale, v_scale, &a, &run);
+  if (st != VSD_OK) return st;
+  if ((zeroed & ~(VSD_READ_ZEROED_K | VSD_READ_ZEROED_V)) != 0u) return VSD_ERR_INVALID_ARG;
+  if (!run) return VSD_OK;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.zeroed = zeroed;
+  cudaError_t e = vsd::launch_read_kv_quant(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VSD_OK : cuda_fail(e);
+}
+
 vsd_status vsd_read_kv_quant(const vsd_geom* geom, int n, const void* k_cache,
                              const void* v_cache, const float* k_scale, const float* v_scale,
                              const int32_t* block_table, const int32_t* pos_base,
                              int pos_offset, const int32_t* n_valid, void* k_out, void* v_out,
                              void* stream) {
-  vsd::QuantRowsArgs a;
-  bool run = false;
-  vsd_status st = quant_rows(geom, n, k_out, v_out, block_table, pos_base, pos_offset, n_valid,
-                             k_cache, v_cache, k_scale, v_scale, &a, &run);
-  if (st != VSD_OK || !run) return st;
-  a.k_out = k_out;
-  a.v_out = v_out;
-  cudaError_t e = vsd::launch_read_kv_quant(a, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? VSD_OK : cuda_fail(e);
+  return vsd_read_kv_quant_zeroed(geom, n, k_cache, v_cache, k_scale, v_scale, block_table,
+                                  pos_base, pos_offset, n_valid, k_out, v_out, 0u, stream);
 }
 
 vsd_status vsd_verify_quant_workspace_size(const vsd_geom* geom, int R, int P_max,

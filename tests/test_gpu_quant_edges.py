@@ -95,7 +95,7 @@ def recorded(vsd):
     sparse = SPARSE(lambda *a: body(a[15], a[16]))
     addr = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
     module = _lib._bound()
-    module.attach(vsd.VsdError, addr(lib.vsd_append_kv_quant), addr(lib.vsd_read_kv_quant),
+    module.attach(vsd.VsdError, addr(lib.vsd_append_kv_quant), addr(lib.vsd_read_kv_quant_zeroed),
                   addr(lib.vsd_verify_quant_workspace_size), addr(verify),
                   addr(lib.vsd_sparse_quant_workspace_size), addr(sparse))
     yield seen, shared
@@ -274,3 +274,59 @@ def test_large_queries_meet_small_key_scales(vsd, d):
                 x = rows[0, t, h].double()
                 err = (logits[0, c, h].cpu().double() - 2.0 ** -12 * (k[:, h // 2] @ x)).abs()
                 assert torch.all(err <= ref.logit_bound(x, k[:, h // 2], 2.0 ** -12))
+
+
+# ------------------------------------------------------------------ rows that are skipped
+@pytest.mark.parametrize("given", [None, "k", "v"])
+@pytest.mark.parametrize("with_valid", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_read_returns_zeros_for_rows_it_skips(vsd, with_valid, given, d):
+    """Outputs that the call allocates hold nothing of what their memory held before, neither
+    for a page whose block is bad nor for a sequence whose range leaves the table at either
+    end; an output that is given keeps those rows."""
+    B, n, Hkv = 5, 40, 2
+    cache = ref.Cache([64] * B, Hkv, d, seed=9)
+    cache.table[0, 1] = 9999
+    width = cache.table.shape[1] * 16
+    args, pos = cache.cuda(), i32([10, 5000, 8, -7, width - n + 1])
+    nv = i32([n, n, n - 7, n, n]) if with_valid else None
+    torch.cuda.synchronize()
+    old = [torch.full((B, n, Hkv, d), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(8)]
+    mine = torch.full((B, n, Hkv, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    del old
+    got = vsd.vsd_read_kv_quant(*args, pos, n=n, n_valid=nv, **({} if given is None else {given + "_out": mine}))
+    assert vsd.vsd_read_device_status() == vsd.DEV_BAD_BLOCK | vsd.DEV_BAD_LENGTH
+    for kv, name in enumerate("kv"):
+        want = torch.full((B, n, Hkv, d), 7.0 if given == name else 0.0, dtype=torch.bfloat16)
+        for b, t0, t1 in ((0, 0, 6), (0, 22, n), (2, 0, n - 7 if with_valid else n)):
+            j = int(pos[b]) + torch.arange(t0, t1)
+            want[b, t0:t1] = cache.kv(b, j)[kv].float().bfloat16()
+        assert torch.equal(got[kv].cpu(), want)
+
+
+@pytest.mark.parametrize("n", [1, 15, 16, 17, 18, 31, 33, 50])
+def test_read_zeros_every_skipped_row_and_no_other_memory(vsd, n):
+    """Ranges that begin at every slot of a page, below 0 and past the table, all of them
+    skipped: n rows of zeros each, and what lies around the outputs stays."""
+    Hkv, d, B = 1, 64, 40
+    starts = list(range(-20, 0)) + list(range(5000, 5000 + B - 20))
+    cache = ref.Cache([64] * B, Hkv, d, seed=10)
+    kc, vc, ks, vs, bt = cache.cuda()
+    from sparse_attention_speculative_gb300._lib import Geom, load
+    geom = Geom(B, Hkv, Hkv, d, 16, bt.shape[1], kc.shape[0])
+    size, pad = B * n * Hkv * d, 1024
+    outs = [torch.full((size + 2 * pad,), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    pos = i32(starts)
+    p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    for zeroed in (0, 1, 2, 3):
+        for o in outs:
+            o.fill_(7.0)
+        torch.cuda.synchronize()
+        assert load().vsd_read_kv_quant_zeroed(ctypes.addressof(geom), n, p(kc), p(vc), p(ks), p(vs), p(bt), p(pos), 0,
+                                               None, p(outs[0][pad:]), p(outs[1][pad:]), zeroed, None) == 0
+        torch.cuda.synchronize()
+        assert vsd.vsd_read_device_status() == vsd.DEV_BAD_LENGTH
+        for i, o in enumerate(outs):
+            assert torch.all(o[:pad] == 7.0) and torch.all(o[pad + size:] == 7.0)
+            assert torch.all(o[pad:pad + size] == (0.0 if zeroed >> i & 1 else 7.0))
