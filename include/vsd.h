@@ -622,6 +622,11 @@ vsd_status vsd_read_kv_quant_zeroed(const vsd_geom* geom, int n, const void* k_c
  * are finite and not negative (what vsd_append_kv_quant writes, or a caller's own); value
  * scales below 2^-80 count as 2^-80, and those that one row attends to lie within 2^120
  * of each other then.  A query row that holds a NaN or an infinity gives NaN.
+ * The products x = softmax * v_scale that multiply the codes are held to 2^-11 of their
+ * value or 2^-27 of the row's largest x, whichever is more: a key adds an error of up to
+ * 2^-27 * (largest x) * |code| to a dimension.  That shows only where value scales differ
+ * by thousands and the pages of large scales hold (nearly) nothing in a dimension: keys
+ * whose x lies 2^-27 below the largest do not count there.
  *   score, score_hist  both or neither: as vsd_verify_attn_collect_scored (partial_scores
  *                      is then required), for vsd_select_topk_scored with n_sink, n_recent
  *   workspace  >= vsd_verify_quant_workspace_size(...) bytes, 256-byte aligned; contents
@@ -645,7 +650,8 @@ vsd_status vsd_verify_attn_collect_quant(const vsd_geom* geom, int R, const void
 /* ------------------------------------------------------------------------------
  * Sparse draft-step attention over the 8-bit cache: vsd_sparse_decode_attn with K and V
  * as above.  idx, n_sel, tail_start, seq_len, max_tail and every rule as there; a list
- * longer than k_max + max_tail is flagged VSD_DEV_BAD_LENGTH (output zeros).  Supported:
+ * longer than k_max + max_tail is flagged VSD_DEV_BAD_LENGTH (output zeros).  Scales as in
+ * vsd_verify_attn_collect_quant, x to 2^-28 of the row's largest.  Supported:
  * Hq/Hkv up to 16, B and Hkv up to 65535, k_max + max_tail up to 2^30 and fewer than 2^31
  * rows (num_blocks * Hkv * page_size) in the cache.
  *   workspace  >= vsd_sparse_quant_workspace_size(...) bytes, 256-byte aligned (0 bytes:

@@ -76,7 +76,9 @@ __device__ __forceinline__ void query_parts(float a, float b, float f, uint32_t&
 // x is an f16 operand.  When some x would exceed 2^15, r is set so that the largest so far
 // becomes 2^2: it may grow by 2^13 before the next change, x holds 11 bits down to 2^-14
 // and is within 2^-25 below that, 2^-27 of the largest: what sums of a hundred thousand
-// small ones need.
+// small ones need.  The largest is one of p vs, over pages of all scales: where a loud page
+// holds zeros in a dimension, the quiet pages' codes there meet x that have lost bits (from
+// 2^-16 of the largest on) or vanished (2^-27).
 constexpr float kTopX = 15.f;    // log2 of the largest x
 constexpr float kRaisedX = 2.f;  // log2 of the largest x after a change of r
 //
@@ -103,7 +105,8 @@ __device__ __forceinline__ float lg2(float x) {
 
 // The same x as an e4m3 operand (the draft step, whose products have columns to spare): three
 // parts x0 + x1 / 2^5 + x2 / 2^13 of the half nearest to x, each in accumulator columns of
-// its own.  Up to x = 32 they hold the half's 11 bits, or are within 2^-23.
+// its own.  Up to x = 32 they hold the half's 11 bits, or are within 2^-23 (2^-28 of a
+// batch's largest, which is put at 2^5).
 constexpr float kPMid = 1.f / 32.f;
 constexpr float kPLow = 1.f / 8192.f;
 

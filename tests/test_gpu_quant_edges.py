@@ -330,3 +330,49 @@ def test_read_zeros_every_skipped_row_and_no_other_memory(vsd, n):
         for i, o in enumerate(outs):
             assert torch.all(o[:pad] == 7.0) and torch.all(o[pad + size:] == 7.0)
             assert torch.all(o[pad:pad + size] == (0.0 if zeroed >> i & 1 else 7.0))
+
+
+# ------------------------------------------------------------------ value scales far apart
+@pytest.mark.parametrize("gap", [0, 4, 10, 14, 20])
+@pytest.mark.parametrize("at", ["first", "middle", "last"])
+@pytest.mark.parametrize("call", ["verify", "draft"])
+def test_value_scales_far_apart(vsd, call, at, gap):
+    """One page of loud values with half of the probability, its codes zero in every other
+    dimension, among 8192 equal keys of value scales 2^gap smaller: every dimension is within
+    the bound of products x = p vs that are held to 2^-27 (draft step: 2^-28) of the largest.
+    Where the scales are within 2^4 of each other that adds nothing that counts."""
+    d, P = 64, 8192
+    cache = ref.Cache([P + 1], 1, d, seed=gap + 77)
+    loud = {"first": 0, "middle": P // 32, "last": P // 16 - 1}[at]
+    one = ref.encode(torch.tensor([1.0], dtype=torch.float64))[0]
+    for lp in range(P // 16 + 1):
+        blk = int(cache.table[0, lp])
+        n = min(16, P + 1 - lp * 16)
+        cache.codes[0][blk, :, :n] = 0
+        cache.scales[0][blk] = 1.0
+        cache.scales[1][blk] = 2.0 ** -gap
+    blk = int(cache.table[0, loud])
+    cache.codes[0][blk, 0, :, 0] = one
+    cache.scales[1][blk] = 1.0
+    cache.codes[1][blk, 0, :, ::2] = 0
+    q = torch.zeros((1, 1, 1, d)).bfloat16()
+    q[..., 0] = 6.25                                    # 16 e^6.25 = 8288
+    args = cache.cuda()
+    if call == "verify":
+        out = vsd.vsd_verify_attn_collect_quant(q.cuda(), *args, i32([P]), P_max=P, scale=1.0, collect=False)[0]
+    else:
+        idx = torch.arange(P, dtype=torch.int32, device="cuda")[None]
+        out = vsd.vsd_sparse_decode_attn_quant(q[:, 0].cuda(), *args, idx, i32([P]), i32([P]), i32([P + 1]),
+                                               scale=1.0, max_tail=1)
+    assert vsd.vsd_read_device_status() == 0
+    j = torch.arange(P + 1)
+    k, v = (x[:, 0] for x in cache.kv(0, j))
+    z = k @ q[0, 0, 0].double()
+    want, mag = ref.softmax_av(z, v)
+    vs = cache.scales[1][cache.table[0].long()[j // 16], 0].double()
+    top = float((torch.softmax(z, 0) * vs).max())
+    floor = 2.0 ** (-27 if call == "verify" else -28) * top * (v / vs[:, None]).abs().sum(0)
+    bound = ref.out_bound(want, mag)
+    assert torch.all((out.cpu().double().reshape(d) - want).abs() <= bound + floor)
+    if gap <= 4:
+        assert torch.all(floor <= bound / 8)
