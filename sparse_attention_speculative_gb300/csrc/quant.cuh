@@ -38,7 +38,9 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t codes) {
 // magnitude lies in [128, 256).  bf16 has 8 significant bits; hi takes 4 of them (nearest)
 // and what it leaves is a multiple of bf16's step of at most half of hi's, 4 bits again:
 // the sum is exact for every value above 2^-14 of the row's largest and within 2^-22 of
-// that below.
+// that below.  Where rows share the factor of the largest among them (the verification, rows
+// within 2^4 of it by their exponents) that holds for the largest: a row at the far end is
+// exact above 2^-10 of its own largest magnitude, and within 2^-18 of it below.
 constexpr float kQLo = 1.f / 32.f;
 
 struct QScale {

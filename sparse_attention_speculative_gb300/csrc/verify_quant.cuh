@@ -697,7 +697,8 @@ __global__ void __launch_bounds__(kQThreads, 1)
         }
         soft_sync();
         // one scale for rows whose largest magnitudes lie within 2^4 of each other (rows of
-        // zeros fit any): the logits then need no factor per column.  A NaN or an infinity
+        // zeros fit any): the logits then need no factor per column, for the bound that quant.cuh
+        // states.  A NaN or an infinity
         // makes its own row NaN: it never sets the others' scale.
         const uint32_t r0 = lane < NQ ? qmax[lane] : 0u, r1 = lane + 32 < NQ ? qmax[lane + 32] : 0u;
         const uint32_t top = __reduce_max_sync(0xffffffffu, max(r0, r1));

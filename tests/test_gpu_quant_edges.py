@@ -376,3 +376,35 @@ def test_value_scales_far_apart(vsd, call, at, gap):
     assert torch.all((out.cpu().double().reshape(d) - want).abs() <= bound + floor)
     if gap <= 4:
         assert torch.all(floor <= bound / 8)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("down", [0, 1, 2, 4, 5])
+def test_logits_of_rows_that_share_a_factor(vsd, d, down):
+    """Rows whose largest magnitudes lie 2^down apart, their other dimensions far below and all
+    of one sign against keys of one sign, so that what the queries' parts cannot hold adds up:
+    each logit is within the stated 2^-18 of its row's largest (2^-22 where the rows have
+    factors of their own, or the same one) times the keys' magnitudes, and fp32's sums."""
+    R, Hq, P = 2, 4, 40
+    cache = ref.Cache([P + R], 1, d, seed=d + down)
+    for blk in cache.table[0, :3].tolist():
+        for code in cache.codes[0][blk:blk + 1]:
+            code &= 0x7F
+            code[code == 0x7F] = 0x7E
+    n = torch.arange(d)
+    # 1.9921875 * 2^-k, every significant bit set, k from 8 to 23
+    low = (2.0 - 2.0 ** -7) * 2.0 ** -(8.0 + n % 16)
+    q = low.expand(1, R, Hq, d).clone()
+    q[..., 0] = 1.5
+    q[0, 1] *= 2.0 ** -down
+    q = q.bfloat16()
+    logits = torch.zeros((1, 2, Hq, P), device="cuda")
+    vsd.vsd_verify_attn_collect_quant(q.cuda(), *cache.cuda(), i32([P]), P_max=P, scale=1.0, logits=logits)
+    assert vsd.vsd_read_device_status() == 0
+    k = cache.kv(0, torch.arange(P))[0][:, 0]
+    for t in range(R):
+        x = q[0, t, 0].double()
+        held = 2.0 ** -22 if t == 0 or down in (0, 5) else 2.0 ** (-22 + down)
+        bound = 2.0 ** -16 * (k.abs() @ x.abs()) + held * x.abs().max() * k.abs().sum(-1)
+        err = (logits[0, t].cpu().double() - k @ x).abs()
+        assert torch.all(err <= bound)
