@@ -25,6 +25,7 @@ size_t verify_quant_span_bytes(const VerifyPlan& plan) {
 // 15.1 / 10.7, 8 tiles 15.2 / 12.7; 128 pairs of 48 columns, 4 tiles 31.7 / 18.4, 8 tiles
 // 41.0 / 25.8.
 bool verify_quant_whole(const VerifyPlan& plan) {
+  // (at most as many pairs as CTAs, of which a plan has no more than a CTA holds lengths)
   if (plan.pairs == 0 || plan.pairs > plan.ctas || plan.t_max > 12) return false;
   const int shared = plan.pairs * plan.t_max / plan.ctas;
   const int room = plan.pairs < 64 ? plan.pairs * 5 / 64 : 5;

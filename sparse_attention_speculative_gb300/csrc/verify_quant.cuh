@@ -157,7 +157,7 @@ struct Seg {
   bool bad_len;
 };
 
-// kWhole: CTA p has pair p.
+// kWhole: CTA p has pair p (no more pairs than CTAs, so every CTA holds the lengths).
 template <bool kWhole>
 struct Walk {
   const VParams& a;
@@ -170,9 +170,8 @@ struct Walk {
       const int p = blockIdx.x;
       b = p / a.Hkv;
       g = p - b * a.Hkv;
-      const int T = (plen != nullptr ? seq_len(a, plen[b]).tiles : a.t_max) + kStartTiles;
-      v = base = plen != nullptr ? cum[b] + g * T : p * T;
-      v1 = base + T;
+      v = base = 0;
+      v1 = seq_len(a, plen[b]).tiles + kStartTiles;
     } else {
       const int c = static_cast<int>(blockIdx.x) < r.C ? static_cast<int>(blockIdx.x) : r.C;
       v = r.first(c);
@@ -297,7 +296,6 @@ __global__ void __launch_bounds__(kQThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 448);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 452);
   static_assert((4 * ST + 6 + 2 * kRounds + 4) * 8 <= 448, "barriers");
-  float* quni_s = reinterpret_cast<float*>(misc + 456);        // 1 / query scale of all rows, or 0
   float* m2s = reinterpret_cast<float*>(misc + 512);           // [2][64] references
   float* alphas = m2s + 128;                                   // [2][64] rescale factors
   float* qinv = alphas + 128;                                  // [64] scale / query scale of a row
@@ -355,7 +353,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
       a.hist[i] = 0u;
   }
   // lengths and first tiles (in the list: times the heads) of the sequences
-  const bool table = a.B <= kTableSeqs;
+  const bool table = kWhole || a.B <= kTableSeqs;
   if (table && warp == 0) {
     int sum = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
@@ -730,7 +728,6 @@ __global__ void __launch_bounds__(kQThreads, 1)
         // padded columns: p = exp2(-inf) = 0, and they never raise the maximum
         if (ts < 128) m2s[ts] = ((ts & 63) < a.NV) ? kNoMax : INFINITY;
         if (ts < D) nan_rows[ts] = 0u;
-        if (ts == 0) *quni_s = quni;
         fence_proxy_async_smem();
         mbar_arrive(&q_ready[nseg & 1]);
         ++nseg;
