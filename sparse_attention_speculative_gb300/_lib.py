@@ -660,11 +660,16 @@ def _bound():
     """The extension module of the calls below, with the library's addresses."""
     global _binding
     lib = load()
+    from . import build
     try:
         from . import _binding as module
+        built_for = getattr(module, "built_for", "other sources")
     except ImportError as e:
         raise RuntimeError("_binding.so is not built or does not fit this torch; run "
                            "`python -m sparse_attention_speculative_gb300.build`") from e
+    if built_for != build._installed():
+        raise RuntimeError("_binding.so was built for %s, this is %s; run `python -m "
+                           "sparse_attention_speculative_gb300.build`" % (built_for, build._installed()))
     module.attach(VsdError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.vsd_append_kv_quant, lib.vsd_read_kv_quant_zeroed,
         lib.vsd_verify_quant_workspace_size, lib.vsd_verify_attn_collect_quant,

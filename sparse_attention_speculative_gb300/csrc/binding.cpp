@@ -427,4 +427,12 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&g_module); }
+// (built_for: the versions whose headers this was compiled with)
+PyMODINIT_FUNC PyInit__binding() {
+  PyObject* m = PyModule_Create(&g_module);
+  if (m != nullptr && PyModule_AddStringConstant(m, "built_for", VSD_BUILT_FOR) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
