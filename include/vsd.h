@@ -262,6 +262,7 @@ vsd_status vsd_select_topk(int n_rows, int Hkv, const float* partial_scores,
  * uint32 [B][4096] are caller-owned (4-byte aligned; the rows of several calls may
  * share one buffer); score_hist is overwritten (no zeroing needed).  The selection
  * reads a score buffer with 16-byte loads: its base must be 16-byte aligned.
+ * Supported: as vsd_verify_attn_collect, with B below 524288 (4096 * B bins).
  *
  * vsd_select_topk_scored: vsd_select_topk on n_rows = B rows of such a score
  * (Hkv = 1) and its histogram (of the candidates for the same n_sink and n_recent, or
@@ -631,7 +632,8 @@ vsd_status vsd_read_kv_quant_zeroed(const vsd_geom* geom, int n, const void* k_c
  *                      is then required), for vsd_select_topk_scored with n_sink, n_recent
  *   workspace  >= vsd_verify_quant_workspace_size(...) bytes, 256-byte aligned; contents
  *              ignored on entry
- * Supported: as vsd_verify_attn_collect, with P_max up to 2^30 and
+ * Supported: as vsd_verify_attn_collect, with P_max up to 2^30, B below 524288 with a
+ *            score (4096 * B bins) and
  *            B * Hkv * (P_max / 128 + 10) below 2^31.
  * ------------------------------------------------------------------------------ */
 vsd_status vsd_verify_quant_workspace_size(const vsd_geom* geom, int R, int P_max,

@@ -80,6 +80,10 @@ CUresult with_context(Encode&& encode) {
   return r;
 }
 
+// Sequences of a scored verification: its kernels number their histograms' bins (4096 each) in
+// 32 bits.
+constexpr int kMaxHistRows = 1 << 19;
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
@@ -312,6 +316,7 @@ vsd_status vsd_verify_attn_collect_scored(const vsd_geom* geom, int R, const voi
     return VSD_ERR_INVALID_ARG;
   if (partial_scores == nullptr || score == nullptr || score_hist == nullptr)
     return geom != nullptr && geom->B == 0 ? VSD_OK : VSD_ERR_INVALID_ARG;
+  if (geom != nullptr && geom->B >= kMaxHistRows) return VSD_ERR_UNSUPPORTED;
   // the aggregation writes the score one float at a time: 4-byte alignment suffices
   if (!aligned(score, 4) || !aligned(score_hist, 4)) return VSD_ERR_INVALID_ARG;
   return verify_call(geom, R, q, k_cache, v_cache, block_table, prefix_len, false,
@@ -972,6 +977,17 @@ vsd_status make_code_map(CUtensorMap* map, const void* cache, const vsd_geom* g)
   return VSD_OK;
 }
 
+// The shape of a verification over the 8-bit cache.  Its kernel counts the tiles of the call,
+// and a few more of each pair, in 32 bits; what follows plans with such numbers.
+vsd_status verify_quant_checks(const vsd_geom* geom, int R, int P_max) {
+  vsd_status st = verify_checks(geom, R, P_max);
+  if (st != VSD_OK) return st;
+  const double tiles = P_max / 128 + 10.0;
+  if (P_max > kMaxPositions || static_cast<double>(geom->B) * geom->Hkv * tiles > 2147483647.0)
+    return VSD_ERR_UNSUPPORTED;
+  return VSD_OK;
+}
+
 bool quant_cache_ok(const void* k_cache, const void* v_cache, const float* k_scale,
                     const float* v_scale) {
   return k_cache && v_cache && k_scale && v_scale && aligned(k_cache, 16) &&
@@ -1069,9 +1085,8 @@ vsd_status vsd_read_kv_quant(const vsd_geom* geom, int n, const void* k_cache,
 vsd_status vsd_verify_quant_workspace_size(const vsd_geom* geom, int R, int P_max,
                                            size_t* bytes) {
   if (bytes == nullptr) return VSD_ERR_INVALID_ARG;
-  vsd_status st = verify_checks(geom, R, P_max);
+  vsd_status st = verify_quant_checks(geom, R, P_max);
   if (st != VSD_OK) return st;
-  if (P_max > kMaxPositions) return VSD_ERR_UNSUPPORTED;
   int sms = 0;
   st = device_info(nullptr, &sms);
   if (st != VSD_OK) return st;
@@ -1090,11 +1105,11 @@ vsd_status vsd_verify_attn_collect_quant(const vsd_geom* geom, int R, const void
                                          float* score, uint32_t* score_hist, int n_sink,
                                          int n_recent, void* out, void* workspace,
                                          size_t workspace_bytes, void* stream) {
-  vsd_status st = verify_checks(geom, R, P_max);
+  vsd_status st = verify_quant_checks(geom, R, P_max);
   if (st != VSD_OK) return st;
   if ((score == nullptr) != (score_hist == nullptr) || n_sink < 0 || n_recent < 0)
     return VSD_ERR_INVALID_ARG;
-  if (P_max > kMaxPositions) return VSD_ERR_UNSUPPORTED;
+  if (score_hist != nullptr && geom->B >= kMaxHistRows) return VSD_ERR_UNSUPPORTED;
   if (geom->B == 0) return VSD_OK;
   if (score != nullptr && partial_scores == nullptr) return VSD_ERR_INVALID_ARG;
   if (!q || !block_table || !prefix_len || !out ||
@@ -1114,9 +1129,6 @@ vsd_status vsd_verify_attn_collect_quant(const vsd_geom* geom, int R, const void
   if (st != VSD_OK) return st;
   const int G = geom->Hq / geom->Hkv;
   const vsd::VerifyPlan plan = vsd::plan_verify(geom->B, geom->Hkv, R, G, P_max, sms);
-  // (the kernel counts the tiles of the call, and a few more of each pair, in 32 bits)
-  if (static_cast<long long>(plan.pairs) * (plan.t_max + 8ll) > 0x7FFFFFFFll)
-    return VSD_ERR_UNSUPPORTED;
   const size_t need = vsd::verify_quant_workspace_bytes(plan, geom->head_dim);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256)))
     return VSD_ERR_WORKSPACE;

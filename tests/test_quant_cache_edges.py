@@ -1,11 +1,13 @@
 """What the 8-bit cache's calls refuse on the host, beside test_quant_cache_refusals.py, and
 how their extension module is built."""
+import ctypes
 import os
 import types
 
 import pytest
 
-from tests.test_quant_cache_refusals import geom, lib, off, p  # noqa: F401
+from sparse_attention_speculative_gb300._lib import Geom
+from tests.test_quant_cache_refusals import geom, lib, off, p, verify  # noqa: F401
 
 
 def test_zeroed_read_call(lib, p):  # noqa: F811
@@ -20,6 +22,27 @@ def test_zeroed_read_call(lib, p):  # noqa: F811
     for name in ("k", "v", "kc", "vc"):
         assert call(geom(), **{name: None}) == -1
         assert call(geom(), **{name: off(p, 8)}) == -1
+
+
+@pytest.mark.parametrize("kw,P_max,code", [
+    (dict(B=2 ** 16, Hkv=2 ** 16, Hq=2 ** 16), 0, -2),      # 2^32 pairs: none in 32 bits
+    (dict(B=2 ** 20, Hkv=2 ** 12, Hq=2 ** 12), 1000, -2),
+    (dict(B=2 ** 15, Hkv=2 ** 14, Hq=2 ** 14), 16, -2),     # 2^29 pairs of 10 tiles and more
+    (dict(B=1, Hkv=8, Hq=32), 2 ** 30 + 1, -2),
+    (dict(B=256, Hkv=1, Hq=1), 2 ** 30, -2),
+])
+def test_verifications_that_32_bits_do_not_count(lib, p, kw, P_max, code):  # noqa: F811
+    size = ctypes.c_size_t(0)
+    assert lib.vsd_verify_quant_workspace_size(geom(**kw), 1, P_max, ctypes.byref(size)) == code
+    assert verify(lib, geom(**kw), p, R=1, P_max=P_max, row1=0) == code
+
+
+def test_scored_verifications_of_too_many_sequences(lib, p):  # noqa: F811
+    """4096 bins for each of 2^19 sequences are more than the kernels number."""
+    many = dict(B=2 ** 19, Hkv=1, Hq=1)
+    assert verify(lib, geom(**many), p, P_max=16, sc=p, hist=p) == -2
+    assert lib.vsd_verify_attn_collect_scored(ctypes.cast(geom(**many), ctypes.POINTER(Geom)), 1, p, p, p, p, p, 0, 0,
+                                              16, 0.1, None, p, p, p, 0, 0, 0, None, None, p, None, 0, None) == -2
 
 
 # ------------------------------------------------------------------ the extension module
