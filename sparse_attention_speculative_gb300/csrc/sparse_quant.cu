@@ -27,9 +27,9 @@
 // can take theirs from an allocator.
 //
 // A split is a chain of dependent latencies (lengths and indices, block table, rows, two
-// products, softmax: 3 of the 5.2 us that one sequence of 4000 positions takes, the merge the
+// products, softmax: 3 of the 5.2 us that one sequence of 2048 positions takes, the merge the
 // rest), so what counts is that all loads of a step are in flight together and that six
-// CTAs share an SM (36 KB of shared memory each).
+// CTAs share an SM (36 KB of shared memory each; three with 16 heads a group, by registers).
 #include <cfloat>
 
 #include "launch.h"
@@ -43,7 +43,8 @@ constexpr int kKeys = 128;      // positions of one batch (the products' M)
 constexpr int kSqThreads = 128;
 constexpr int kSqPage = 16;
 constexpr int kSqMaxSplits = 1024;
-constexpr int kSqWave = 152 * 6;  // CTAs that run at once
+// CTAs that share an SM (16 heads a group hold twice as many sums and columns in registers)
+constexpr int sq_ctas_per_sm(int G) { return G == 16 ? 3 : 6; }
 constexpr float kSqTop = 5.f;   // log2 of the largest x of a batch
 constexpr float kSqNoMax = -3e38f;
 
@@ -135,7 +136,7 @@ __device__ __forceinline__ float sq_warp_sums(float (&v)[G]) {
 }
 
 template <int D, int G>
-__global__ void __launch_bounds__(kSqThreads, G == 16 ? 3 : 6) sparse_quant_kernel(const SqParams a) {
+__global__ void __launch_bounds__(kSqThreads, sq_ctas_per_sm(G)) sparse_quant_kernel(const SqParams a) {
   using Sm = SqSmem<D, G>;
   constexpr int GP = Sm::kCols;
   constexpr int LPR = D / 16;       // 16-byte chunks of a row of codes
@@ -436,7 +437,11 @@ __global__ void __launch_bounds__(kSqThreads, G == 16 ? 3 : 6) sparse_quant_kern
 // partials' loads in flight per round, combined in split order.
 template <int D, int G>
 __global__ void __launch_bounds__(D) sparse_quant_merge_kernel(const SqParams a) {
-  constexpr int kU = 18;  // 2048 selected positions and their tail: one round
+  // (Lists of 200 to 16000 positions in 8 to 128 pairs, kU = 8, 12, 16, 18, 24, 32: 18 is the best or
+  // within 3 % of it everywhere but at 16000 positions of one sequence.  17 splits 6.0, 5.7, 5.8,
+  // 5.3, 5.5, 5.5 us; 128 pairs of 3 splits 11.8, 11.4, 10.9, 10.5, 11.5, 12.1; 126 splits
+  // 11.9, 11.7, 11.9, 12.0, 12.2, 11.0.)
+  constexpr int kU = 18;
   const int h = blockIdx.x % G, pair = blockIdx.x / G;
   const int b = pair / a.Hkv, g = pair - b * a.Hkv;
   const int t = threadIdx.x;
@@ -494,15 +499,17 @@ struct SqPlan {
   int split_len, splits;
 };
 
-// One batch a split while the CTAs fill one wave, then two, and four beyond four waves: fewer
+// One batch a split while the CTAs fill one wave, then two, and four beyond 24 CTAs an SM: fewer
 // partial results, and only a CTA's first batch waits for the list and the table.  (One
-// sequence of 4000 positions: 5.3 us with one batch, 6.4 with two; four of them with 8 heads
-// 11.5 and 9.8; 32 of them 65 with one, 56 with two, 54 with four, 53 with six.)
-SqPlan sq_plan(long long pairs, int k_max, int max_tail) {
+// sequence of 2048 positions: 5.3 us with one batch, 6.4 with two; four of 4096
+// 11.5 and 9.8; 32 of them 65 with one, 56 with two, 54 with four, 53 with six.  With 16 heads a
+// group, whose wave is half as large: 32 pairs of 2000 positions 11.9 with one, 11.0 with
+// two, of 3500 16.2 and 12.2; 64 pairs of 4500 31.3 with two, 32.6 with four.)
+SqPlan sq_plan(long long pairs, int G, int k_max, int max_tail) {
   const int n = k_max + max_tail;  // (below 2^31: checked by the caller)
   const int batches = n > 0 ? (n + kKeys - 1) / kKeys : 1;
   const long long ctas = pairs * batches;
-  int per = ctas <= kSqWave ? 1 : (ctas <= 4 * kSqWave ? 2 : 4);
+  int per = ctas <= 152ll * sq_ctas_per_sm(G) ? 1 : (ctas <= 152ll * 24 ? 2 : 4);
   if (per > batches) per = batches;
   const int least = (batches + kSqMaxSplits - 1) / kSqMaxSplits;
   if (per < least) per = least;
@@ -548,14 +555,14 @@ cudaError_t launch_sq_d(const SqParams& p, int B, int G, cudaStream_t stream) {
 }  // namespace
 
 size_t sparse_quant_workspace_bytes(int B, int Hkv, int G, int head_dim, int k_max, int max_tail) {
-  const SqPlan plan = sq_plan(static_cast<long long>(B) * Hkv, k_max, max_tail);
+  const SqPlan plan = sq_plan(static_cast<long long>(B) * Hkv, G, k_max, max_tail);
   if (plan.splits <= 1) return 0;
   const size_t slot = (2 * G + 3) / 4 * 4 + static_cast<size_t>(G) * head_dim;
   return static_cast<size_t>(B) * Hkv * plan.splits * slot * sizeof(float);
 }
 
 cudaError_t launch_sparse_quant(const SparseArgs& a, const QuantScales& s, cudaStream_t stream) {
-  const SqPlan plan = sq_plan(static_cast<long long>(a.B) * a.Hkv, a.k_max, a.max_tail);
+  const SqPlan plan = sq_plan(static_cast<long long>(a.B) * a.Hkv, a.G, a.k_max, a.max_tail);
   SqParams p;
   p.q = static_cast<const uint16_t*>(a.q);
   p.k_cache = static_cast<const uint8_t*>(a.k_cache);

@@ -408,3 +408,28 @@ def test_logits_of_rows_that_share_a_factor(vsd, d, down):
         bound = 2.0 ** -16 * (k.abs() @ x.abs()) + held * x.abs().max() * k.abs().sum(-1)
         err = (logits[0, t].cpu().double() - k @ x).abs()
         assert torch.all(err <= bound)
+
+
+# ------------------------------------------------------------------ splits of 16 heads a group
+@pytest.mark.parametrize("B,k", [(4, 1781), (4, 1800), (8, 7000), (8, 7300)])
+def test_draft_of_sixteen_heads_around_its_waves(vsd, B, k):
+    """Lists on both sides of the borders where a split takes one, two and four batches with 16
+    heads a group (456 and 3648 CTAs)."""
+    Hkv, d, G = 8, 64, 16
+    tail = 5
+    cache = ref.Cache([k + 50] * B, Hkv, d, seed=k)
+    g = torch.Generator().manual_seed(k)
+    n = [k] + [int(x) for x in torch.randint(0, k, (B - 1,), generator=g)]
+    idx = torch.full((B, k), -1, dtype=torch.int32)
+    for b in range(B):
+        idx[b, :n[b]] = torch.randperm(k + 40, generator=g)[:n[b]].sort().values.to(torch.int32)
+    q = torch.randn((B, Hkv * G, d), generator=g).bfloat16()
+    out = vsd.vsd_sparse_decode_attn_quant(q.cuda(), *cache.cuda(), idx.cuda(), i32(n), i32([k + 40] * B),
+                                           i32([k + 40 + tail] * B), scale=0.125, max_tail=tail).cpu().double()
+    assert vsd.vsd_read_device_status() == 0
+    for b in range(B):
+        j = torch.cat([idx[b, :n[b]].long(), torch.arange(k + 40, k + 40 + tail)])
+        kk, vv = cache.kv(b, j)
+        for h in range(0, Hkv * G, 5):
+            want, mag = ref.softmax_av(0.125 * (kk[:, h // G] @ q[b, h].double()), vv[:, h // G])
+            assert torch.all((out[b, h] - want).abs() <= ref.out_bound(want, mag))
