@@ -1825,7 +1825,11 @@ __global__ void __launch_bounds__(kWsThreads, 1)
         set_abort();
       const bool stop = *abort_flag != 0;
       if (!work) {
-        if (ct == 0) ptx::mbar_arrive(&empty[s]);  // nothing of this stage is read
+        // Nothing of this stage is read, but every thread has to have seen it filled before it
+        // goes back: a thread that comes later, when it has been filled once more, would
+        // take its own wait's phase for one that is still to come.
+        csync();
+        if (ct == 0) ptx::mbar_arrive(&empty[s]);
         continue;
       }
       const bool valid = (meta[s * 16 + cw] >> (ct & 31)) & 1u;
