@@ -33,7 +33,7 @@
 //     columns; two groups 345), and writing the logits by the widening warps was slower.
 //
 // Measured: 28 us for the 32K layer (32 columns, 77 MB: 11.5 at the copy rate; 13 tiles a
-// CTA, of which its start, the segments and the merge take a third), 344 us for 16 sequences
+// CTA, of which its start, the segments and the merge take a third), 339 us for 16 sequences
 // of 32K (48 columns; 204 at the copy rate).  There a tile is 6300 warp instructions at half
 // of the issue slots, 3000 cycles against 1800 for its bytes; a quarter of them collect
 // logits (without: 267 us), and time follows their number.
