@@ -67,7 +67,7 @@ vsd_status encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
   return VSD_OK;
 }
 
-// Encoding a descriptor is a call of the driver, which wants the device's context current on
+// Encoding a descriptor is a call of CUDA's lower API, which wants the device's context current on
 // the host thread.  The runtime makes it so at the thread's first call that needs it, and an
 // encoding may well come before that.
 template <typename Encode>
