@@ -672,6 +672,163 @@ vsd_status vsd_sparse_decode_attn_quant(const vsd_geom* geom, const void* q,
                                         size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------------
+ * Rows before they are stored or attend: the norm of each head and the rotation by the
+ * position, in one pass over a layer's projections (which may be views of one product).
+ *
+ * For sequence b, row t < n_valid[b] and a head's row x of q or k:
+ *   y = x * w / sqrt(mean(x^2) + eps)       (w: q_weight or k_weight; y = x where it is NULL)
+ *   pairs i < rot_dim / 2 of y's dimensions turned by the angle a = p * f_i:
+ *     (y0, y1) <- amplitude * (y0 cos a - y1 sin a, y1 cos a + y0 sin a)
+ *     of dimensions (i, i + rot_dim / 2), or (2 i, 2 i + 1) with `interleaved`
+ *   dimensions from rot_dim on stay y.
+ * p = the row's position, rope_base[b] + pos_offset + t (pos_base where rope_base is NULL:
+ * after an eviction a sequence holds fewer rows than it has positions).  All in fp32, rounded
+ * once to what is written; a row whose sum of squares leaves fp32's range becomes zeros.
+ *   turns   int64 [rot_dim / 2] (device): f_i / (2 pi) in units of 2^-64, modulo 1.  The
+ *           product with p wraps at whole turns, so that every position's angle is exact to
+ *           2^-24 of half a turn
+ *   vsd_rows  bf16 rows: the row of (b, t, head) begins at data + b * batch_stride + t *
+ *           row_stride + head * head_stride (elements; multiples of 8), its head_dim elements
+ *           one after the other.  data 16-byte aligned
+ *   n_valid int32 [B] or NULL (n rows of every sequence); a count outside [0, n] is flagged
+ *           VSD_DEV_BAD_LENGTH and counts as 0.  Rows behind it are not read; those of q_out
+ *           (k_out) are left as they were, or become zeros with VSD_ROPE_ZEROED_Q (_K)
+ *   q_out, k_out  bf16 [B][n][Hq or Hkv][head_dim].  q_out may be q's own memory where q is
+ *           contiguous (k_out k's)
+ *
+ * vsd_norm_rope: q and, unless it is NULL, k.  geom's page_size, max_blocks_per_seq and
+ *   num_blocks are not used.
+ * vsd_norm_rope_append_kv: q to q_out; k, and v as it is, into the cache at positions
+ *   pos_base[b] + pos_offset + t with the rules of vsd_append_kv.
+ * vsd_norm_rope_append_kv_quant: the same into an 8-bit cache with the rules of
+ *   vsd_append_kv_quant; a page's scale is that of the turned rows (fp32, not rounded to bf16
+ *   in between).  A sequence whose range is refused stores nothing; its q_out is written.
+ *
+ * Supported: head_dim 64 or 128, rot_dim a multiple of 8 up to head_dim (0: no rotation, turns
+ * may be NULL), B * n * ceil((Hq + 2 Hkv) / 2) below 2^31.  All are programmatic dependents of
+ * the preceding kernel on the stream.
+ * ------------------------------------------------------------------------------ */
+typedef struct vsd_rows {
+  const void* data;
+  int64_t batch_stride, row_stride, head_stride;
+} vsd_rows;
+
+typedef struct vsd_rope {
+  const int64_t* turns;
+  int rot_dim;
+  int interleaved;
+  float amplitude; /* 1 for a plain rotation */
+  const void* q_weight; /* bf16 [head_dim] or NULL */
+  const void* k_weight;
+  float eps;
+} vsd_rope;
+
+#define VSD_ROPE_ZEROED_Q 0x1u
+#define VSD_ROPE_ZEROED_K 0x2u
+
+vsd_status vsd_norm_rope(const vsd_geom* geom, int n, const vsd_rows* q, const vsd_rows* k,
+                         const vsd_rope* rope, const int32_t* pos_base, int pos_offset,
+                         const int32_t* n_valid, void* q_out, void* k_out, unsigned zeroed,
+                         void* stream);
+
+vsd_status vsd_norm_rope_append_kv(const vsd_geom* geom, int n, const vsd_rows* q,
+                                   const vsd_rows* k, const vsd_rows* v, const vsd_rope* rope,
+                                   const int32_t* block_table, const int32_t* pos_base,
+                                   int pos_offset, const int32_t* rope_base,
+                                   const int32_t* n_valid, void* q_out, unsigned zeroed,
+                                   void* k_cache, void* v_cache, void* stream);
+
+vsd_status vsd_norm_rope_append_kv_quant(const vsd_geom* geom, int n, const vsd_rows* q,
+                                         const vsd_rows* k, const vsd_rows* v,
+                                         const vsd_rope* rope, const int32_t* block_table,
+                                         const int32_t* pos_base, int pos_offset,
+                                         const int32_t* rope_base, const int32_t* n_valid,
+                                         void* q_out, unsigned zeroed, void* k_cache,
+                                         void* v_cache, float* k_scale, float* v_scale,
+                                         void* stream);
+
+/* ------------------------------------------------------------------------------
+ * Attention weight accumulated by position, from the logits that a verification collected.
+ *
+ * Slot c < C of `logits` holds the logits of verify row r_c = rows[c] (of vsd_verify_attn_
+ * collect: C = 2, its two collected rows; of vsd_verify_attn_collect_all: C = R, all of them).
+ * With P = prefix_len[b] and the row's logits against the verify block itself,
+ *   z'[u] = scale * <q[b,r_c,h,:], K[b, P + u, h/G, :]>      u <= r_c,
+ *   L     = log(sum_{j < P} e^{logits[b,c,h,j]} + sum_{u <= r_c} e^{z'[u]})
+ *   weights[b,g,j] += sum_c sum_{h in group g} e^{logits[b,c,h,j] - L[b,c,h]}      j < P
+ * so that each row and head adds the part of its attention that falls on the prefix.  Later
+ * entries of weights are neither read nor written: those of new positions start at what the
+ * caller put there (zeros).
+ *   logits     fp32 [B][C][Hq][P_max]
+ *   rows       C host integers in [-1, R): -1 leaves a slot out (with R = 1 a collecting
+ *              verification writes its one row twice: rows = {0, -1} counts it once)
+ *   q          bf16 [B][R][Hq][head_dim], scale: the verification's
+ *   weights    fp32 [B][Hkv][weights_stride], weights_stride >= P_max
+ * The keys are those of the cache; with an 8-bit cache its key codes and their scales.  A key
+ * of the verify block whose block-table entry is outside the cache is left out and flagged
+ * VSD_DEV_BAD_BLOCK; a prefix outside [0, P_max], or whose verify block leaves the table, is
+ * flagged VSD_DEV_BAD_LENGTH and that sequence's weights stay.  A row with a NaN or an
+ * infinite logit adds NaN, one whose logits are all minus infinity adds nothing.  Sums are
+ * formed in a fixed order (two runs are bit-identical).
+ * Supported: as vsd_verify_attn_collect with C <= 16, C * G <= 64, P_max up to 2^30 and B * Hkv
+ * below 2^26.
+ * ------------------------------------------------------------------------------ */
+vsd_status vsd_accumulate_weights(const vsd_geom* geom, int R, int C, const int* rows,
+                                  const float* logits, const void* q, const void* k_cache,
+                                  const int32_t* block_table, const int32_t* prefix_len,
+                                  int P_max, float scale, float* weights, int weights_stride,
+                                  void* stream);
+
+vsd_status vsd_accumulate_weights_quant(const vsd_geom* geom, int R, int C, const int* rows,
+                                        const float* logits, const void* q, const void* k_cache,
+                                        const float* k_scale, const int32_t* block_table,
+                                        const int32_t* prefix_len, int P_max, float scale,
+                                        float* weights, int weights_stride, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * Eviction: the rows that a selection kept, moved together.
+ *
+ * For sequence b, KV head g and i < n = n_sel[b][s] (s = g with idx_heads = Hkv, 0 with
+ * idx_heads = 1), with j = idx[b][s][i]:
+ *   row i of dst_table's sequence <- row j of block_table's        (K and V, the same caches)
+ *   weights_out[b][g][i] <- weights[b][g][j];  weights_out[b][g][n ..] <- 0
+ * idx is ascending, as vsd_select_topk gives it from the accumulated weights (one set for all
+ * heads with its partial_scores = weights; one for each head with n_rows = B * Hkv rows of one
+ * group), and n_sel is the new length.  Keys keep the rotation of their old positions, and new
+ * rows follow at n with rope_base still counting every position (vsd_norm_rope_append_kv).
+ *   dst_table  int32 [B][dst_blocks].  The page that the rows 16 i .. 16 i + 15 go to is either
+ *              block_table's page i of that sequence (moved in place: dst_table may be
+ *              block_table itself) or a page that no sequence of the call reads; no page is
+ *              written for two sequences.  Rows at n and beyond stay as they were
+ *   weights, weights_out  fp32 [B][Hkv][stride] each, both or neither NULL; weights_out may be
+ *              weights (with one stride); weights_out_stride >= k_max
+ *   8-bit cache  a destination page takes the largest scale of the rows that come into it, and
+ *              codes of a smaller one become e4m3(code * (scale / largest)) (exact down to
+ *              e4m3's subnormals where scales are powers of two)
+ * An index outside [i, prefix_len[b]) is flagged VSD_DEV_BAD_INDEX and its row is not written;
+ * a count outside [0, k_max] or beyond dst_table's pages, or a bad prefix length, is flagged
+ * VSD_DEV_BAD_LENGTH and that list moves nothing (its weights_out stays too); a source or
+ * destination entry outside the cache is flagged VSD_DEV_BAD_BLOCK and its rows are not
+ * written.  weights_out of a row whose index or source is refused becomes 0.
+ * Supported: head_dim 64 or 128, B * Hkv below 2^26.  Programmatic dependents of the preceding
+ * kernel.
+ * ------------------------------------------------------------------------------ */
+vsd_status vsd_compact_kv(const vsd_geom* geom, const int32_t* block_table,
+                          const int32_t* dst_table, int dst_blocks, const int32_t* prefix_len,
+                          const int32_t* idx, const int32_t* n_sel, int idx_heads, int k_max,
+                          void* k_cache, void* v_cache, const float* weights,
+                          int weights_stride, float* weights_out, int weights_out_stride,
+                          void* stream);
+
+vsd_status vsd_compact_kv_quant(const vsd_geom* geom, const int32_t* block_table,
+                                const int32_t* dst_table, int dst_blocks,
+                                const int32_t* prefix_len, const int32_t* idx,
+                                const int32_t* n_sel, int idx_heads, int k_max, void* k_cache,
+                                void* v_cache, float* k_scale, float* v_scale,
+                                const float* weights, int weights_stride, float* weights_out,
+                                int weights_out_stride, void* stream);
+
+/* ------------------------------------------------------------------------------
  * vsd_copy: dst <- src as a kernel on `stream` (a programmatic dependent of the
  * preceding kernel).  Either pointer may be pinned host memory, which the device
  * addresses directly; a decode loop moves its inputs in and its results out this way.

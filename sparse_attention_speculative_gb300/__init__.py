@@ -25,6 +25,9 @@ from ._lib import (DEV_BAD_BLOCK, DEV_BAD_INDEX, DEV_BAD_LENGTH, DEV_TIMEOUT, Ge
                    vsd_copy, vsd_append_kv, vsd_advance_lengths, vsd_sparse_decode_attn_step,
                    vsd_append_kv_quant, vsd_read_kv_quant, vsd_verify_attn_collect_quant,
                    vsd_verify_attn_collect_scored_quant, vsd_verify_quant_workspace_size,
-                   vsd_sparse_decode_attn_quant, vsd_sparse_quant_workspace_size)
+                   vsd_sparse_decode_attn_quant, vsd_sparse_quant_workspace_size,
+                   vsd_rope_turns, vsd_norm_rope, vsd_norm_rope_append_kv,
+                   vsd_norm_rope_append_kv_quant, vsd_accumulate_weights,
+                   vsd_accumulate_weights_quant, vsd_compact_kv, vsd_compact_kv_quant)
 from .decode_loop import DecodeLoop  # noqa: F401
 from .iteration import IterationGraph  # noqa: F401

@@ -7,6 +7,7 @@ missing the calls raise immediately; there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 from typing import Optional, Tuple
@@ -104,6 +105,15 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         lib.vsd_sparse_decode_attn_quant.argtypes = [P, P, P, P, P, P, P, P, P, I, P, P, I, F, P,
                                                      P, SZ, P]
         lib.vsd_block_topk.argtypes = [GP, I, P, P, P, I, I, F, P, P, P]
+        lib.vsd_norm_rope.argtypes = [P, I, P, P, P, P, I, P, P, P, ctypes.c_uint, P]
+        lib.vsd_norm_rope_append_kv.argtypes = [P, I, P, P, P, P, P, P, I, P, P, P, ctypes.c_uint,
+                                                P, P, P]
+        lib.vsd_norm_rope_append_kv_quant.argtypes = [P, I, P, P, P, P, P, P, I, P, P, P,
+                                                      ctypes.c_uint, P, P, P, P, P]
+        lib.vsd_accumulate_weights.argtypes = [P, I, I, P, P, P, P, P, P, I, F, P, I, P]
+        lib.vsd_accumulate_weights_quant.argtypes = [P, I, I, P, P, P, P, P, P, P, I, F, P, I, P]
+        lib.vsd_compact_kv.argtypes = [P, P, P, I, P, P, P, I, I, P, P, P, I, P, I, P]
+        lib.vsd_compact_kv_quant.argtypes = [P, P, P, I, P, P, P, I, I, P, P, P, P, P, I, P, I, P]
         lib.vsd_read_device_status.argtypes = [P, ctypes.POINTER(ctypes.c_uint)]
         lib.vsd_get_error_string.argtypes = [I]
         lib.vsd_get_error_string.restype = ctypes.c_char_p
@@ -120,7 +130,9 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                      "vsd_append_kv_quant", "vsd_read_kv_quant", "vsd_read_kv_quant_zeroed",
                      "vsd_verify_quant_workspace_size",
                      "vsd_verify_attn_collect_quant", "vsd_sparse_quant_workspace_size",
-                     "vsd_sparse_decode_attn_quant",
+                     "vsd_sparse_decode_attn_quant", "vsd_norm_rope", "vsd_norm_rope_append_kv",
+                     "vsd_norm_rope_append_kv_quant", "vsd_accumulate_weights",
+                     "vsd_accumulate_weights_quant", "vsd_compact_kv", "vsd_compact_kv_quant",
                      "vsd_append_kv", "vsd_advance_lengths", "vsd_sparse_decode_attn_step",
                      "vsd_read_device_status", "vsd_last_cuda_error"):
             getattr(lib, name).restype = ctypes.c_int
@@ -649,8 +661,9 @@ def vsd_sparse_decode_attn_step(q, k_cache, v_cache, block_table, idx, n_sel, ta
 
 
 # ------------------------------------------------------------------ 8-bit cache
-# The checks, outputs and scratch of these calls are in csrc/binding.cpp: they are made once
-# per layer and step, and their small ones run for a few microseconds on the GPU.  Scratch
+# The checks, outputs and scratch of these calls and those below are in csrc/binding.cpp: they
+# are made once per layer and step, and their small ones run for a few microseconds on the
+# GPU.  Scratch
 # that is not given is allocated for the call (in a capture by torch.cuda.graph, from the
 # graph's pool; a capture by other means takes a workspace of its caller's).
 _binding = None
@@ -675,6 +688,10 @@ def _bound():
         lib.vsd_verify_quant_workspace_size, lib.vsd_verify_attn_collect_quant,
         lib.vsd_sparse_quant_workspace_size,
         lib.vsd_sparse_decode_attn_quant)))
+    module.attach_more(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.vsd_norm_rope, lib.vsd_norm_rope_append_kv, lib.vsd_norm_rope_append_kv_quant,
+        lib.vsd_accumulate_weights, lib.vsd_accumulate_weights_quant, lib.vsd_compact_kv,
+        lib.vsd_compact_kv_quant)))
     _binding = module
     return module
 
@@ -756,3 +773,106 @@ def vsd_sparse_decode_attn_quant(q, k_cache, v_cache, k_scale, v_scale, block_ta
     return (_binding or _bound()).sparse(q, k_cache, v_cache, k_scale, v_scale, block_table, idx,
                                          n_sel, tail_start, seq_len, scale, max_tail, out,
                                          workspace, _handle(stream))
+
+
+# ------------------------------------------------------------------ normed and rotated rows
+def vsd_rope_turns(inv_freq, device=None):
+    """The rotation's table for the calls below, made once for a model: int64 [rot_dim / 2],
+    each inv_freq / (2 pi) in units of 2^-64, modulo 1.  inv_freq: radians per position, a
+    tensor or sequence (taken in 64 bits)."""
+    f = torch.as_tensor(inv_freq, dtype=torch.float64)
+    if device is None:
+        device = f.device if f.is_cuda else "cuda"
+    t = f.to(device) / (2.0 * math.pi)
+    t = (t - torch.floor(t)) * 2.0 ** 32
+    high = torch.floor(t)
+    low = torch.floor((t - high) * 2.0 ** 32)
+    # (the upper half as a signed number: 2^64 does not fit)
+    return ((high - 2.0 ** 32 * (high >= 2.0 ** 31)).long() << 32) | low.long()
+
+
+def vsd_norm_rope(q, k, turns, pos_base, *, pos_offset: int = 0, n_valid=None, q_weight=None,
+                  k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+                  amplitude: float = 1.0, q_out=None, k_out=None, stream=None):
+    """Rows q (bf16 [B, n, Hq, d], any strides that are multiples of 8) and k ([B, n, Hkv, d] or
+    None) normed per head (where its weight, bf16 [d], is given) and rotated by their positions
+    pos_base[b] + pos_offset + t: pairs (i, i + rot_dim / 2) of the first rot_dim = 2 *
+    len(turns) dimensions, or (2 i, 2 i + 1) with interleaved.  Rows t >= n_valid[b] are left as
+    they were in q_out, k_out, and zeros in outputs that are allocated here.  Returns (q_out,
+    k_out)."""
+    return (_binding or _bound()).rope(q, k, None, None, None, None, None, None, pos_base, turns,
+                                       pos_offset, None, n_valid, q_weight, k_weight, eps,
+                                       interleaved, amplitude, q_out, k_out, _handle(stream))
+
+
+def vsd_norm_rope_append_kv(q, k_new, v_new, k_cache, v_cache, block_table, pos_base, turns, *,
+                            pos_offset: int = 0, rope_base=None, n_valid=None, q_weight=None,
+                            k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+                            amplitude: float = 1.0, q_out=None, stream=None):
+    """vsd_norm_rope whose keys, and values v_new as they are, are stored at positions
+    pos_base[b] + pos_offset + t of a bf16 cache.  The rotation counts from rope_base[b] (None:
+    pos_base) + pos_offset: after an eviction a sequence holds fewer rows than it has
+    positions.  Returns q_out."""
+    return (_binding or _bound()).rope(q, k_new, v_new, k_cache, v_cache, None, None, block_table,
+                                       pos_base, turns, pos_offset, rope_base, n_valid, q_weight,
+                                       k_weight, eps, interleaved, amplitude, q_out, None,
+                                       _handle(stream))
+
+
+def vsd_norm_rope_append_kv_quant(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table,
+                                  pos_base, turns, *, pos_offset: int = 0, rope_base=None,
+                                  n_valid=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                                  interleaved: bool = False, amplitude: float = 1.0, q_out=None,
+                                  stream=None):
+    """vsd_norm_rope_append_kv into an 8-bit cache (as vsd_append_kv_quant; the turned keys are
+    quantised without a rounding to bf16 in between).  Returns q_out."""
+    if k_scale is None or v_scale is None:
+        raise TypeError("k_scale and v_scale must be tensors")
+    return (_binding or _bound()).rope(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale,
+                                       block_table, pos_base, turns, pos_offset, rope_base, n_valid,
+                                       q_weight, k_weight, eps, interleaved, amplitude, q_out, None,
+                                       _handle(stream))
+
+
+# ------------------------------------------------------------------ accumulated weights, eviction
+def vsd_accumulate_weights(logits, q, k_cache, block_table, prefix_len, weights, *, scale: float,
+                           rows=None, stream=None):
+    """Adds the attention weight of a verification's collected logits (fp32 [B, C, Hq, P_max])
+    to weights (fp32 [B, Hkv, at least P_max]), for each prefix position and KV head.  q, the
+    cache and scale are the verification's.  rows: the verify row of each of the C slots, -1 to
+    leave one out; None: all of them where C = R, else the two collected rows 0 and R - 1 (one,
+    for R = 1).  Returns weights."""
+    return (_binding or _bound()).weights(logits, q, k_cache, None, block_table, prefix_len,
+                                          weights, scale, rows, _handle(stream))
+
+
+def vsd_accumulate_weights_quant(logits, q, k_cache, k_scale, block_table, prefix_len, weights, *,
+                                 scale: float, rows=None, stream=None):
+    """vsd_accumulate_weights beside an 8-bit cache."""
+    if k_scale is None:
+        raise TypeError("k_scale must be a tensor")
+    return (_binding or _bound()).weights(logits, q, k_cache, k_scale, block_table, prefix_len,
+                                          weights, scale, rows, _handle(stream))
+
+
+def vsd_compact_kv(k_cache, v_cache, block_table, dst_table, prefix_len, idx, n_sel, *,
+                   weights=None, weights_out=None, stream=None):
+    """Eviction from a bf16 cache: the rows idx (int32 [B, k], or [B, Hkv, k] with a list for
+    each KV head; ascending, as vsd_select_topk gives them) of each sequence move to rows 0 ..
+    n_sel - 1 of dst_table's pages (int32 [B, pages]: block_table itself, its leading columns'
+    copy, or pages that nothing else uses), and so do their weights (fp32 [B, Hkv, .]), with
+    zeros behind them.  n_sel is the new length.  Returns weights_out."""
+    return (_binding or _bound()).compact(k_cache, v_cache, None, None, block_table, dst_table,
+                                          prefix_len, idx, n_sel, weights, weights_out,
+                                          _handle(stream))
+
+
+def vsd_compact_kv_quant(k_cache, v_cache, k_scale, v_scale, block_table, dst_table, prefix_len,
+                         idx, n_sel, *, weights=None, weights_out=None, stream=None):
+    """vsd_compact_kv on an 8-bit cache: a page takes the largest scale of the rows that come
+    into it."""
+    if k_scale is None or v_scale is None:
+        raise TypeError("k_scale and v_scale must be tensors")
+    return (_binding or _bound()).compact(k_cache, v_cache, k_scale, v_scale, block_table, dst_table,
+                                          prefix_len, idx, n_sel, weights, weights_out,
+                                          _handle(stream))

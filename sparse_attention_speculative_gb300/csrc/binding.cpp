@@ -1,5 +1,6 @@
-// binding.cpp -- the Python calls of the 8-bit cache: the checks of their tensors, outputs
-// and scratch from torch's allocator, and one call of the C ABI each.
+// binding.cpp -- the Python calls of the 8-bit cache, and of normed and rotated rows, accumulated
+// weights and eviction (of either cache): the checks of their tensors, outputs and scratch from
+// torch's allocator, and one call of the C ABI each.
 //
 // The calls are made once per layer and step, and the smallest ones run for 2 to 6 us on the
 // GPU: reading some forty properties of ten tensors from Python, and passing twenty arguments
@@ -28,6 +29,13 @@ struct Calls {
   decltype(&vsd_verify_attn_collect_quant) verify = nullptr;
   decltype(&vsd_sparse_quant_workspace_size) sparse_size = nullptr;
   decltype(&vsd_sparse_decode_attn_quant) sparse = nullptr;
+  decltype(&vsd_norm_rope) rope = nullptr;
+  decltype(&vsd_norm_rope_append_kv) rope_append = nullptr;
+  decltype(&vsd_norm_rope_append_kv_quant) rope_append_quant = nullptr;
+  decltype(&vsd_accumulate_weights) weights = nullptr;
+  decltype(&vsd_accumulate_weights_quant) weights_quant = nullptr;
+  decltype(&vsd_compact_kv) compact = nullptr;
+  decltype(&vsd_compact_kv_quant) compact_quant = nullptr;
   PyObject* error = nullptr;  // VsdError(status, name)
 };
 Calls g_calls;
@@ -395,6 +403,251 @@ PyObject* py_sparse(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A cache of either type: bf16 rows (no scales), or codes and their scales.
+Cache any_cache(PyObject* const* a, int dev, vsd_geom* geom) {
+  if (a[2] != Py_None || a[3] != Py_None) return cache_of(a, dev, geom);
+  const at::Tensor &k = as_tensor(a[0], "k_cache"), &v = as_tensor(a[1], "v_cache");
+  need(k, at::kBFloat16, 4, "k_cache");
+  if (k.get_device() != dev) refuse(PyExc_ValueError, "k_cache is on another device");
+  need(v, at::kBFloat16, k.sizes(), dev, "v_cache");
+  geom->num_blocks = dim_of(k.size(0), "num_blocks");
+  geom->Hkv = dim_of(k.size(1), "Hkv");
+  geom->page_size = dim_of(k.size(2), "page_size");
+  geom->head_dim = dim_of(k.size(3), "head_dim");
+  return Cache{pointer(k), pointer(v), nullptr, nullptr};
+}
+
+// bf16 rows [B][n][heads][d], each contiguous, by their strides.
+vsd_rows strided(const at::Tensor& t, at::IntArrayRef shape, int dev, const char* name) {
+  if (t.scalar_type() != at::kBFloat16)
+    refuse(PyExc_TypeError, std::string(name) + " must be BFloat16, got " + c10::toString(t.scalar_type()));
+  if (!t.is_cuda()) refuse(PyExc_ValueError, std::string(name) + " must be a CUDA tensor");
+  if (t.sizes() != shape)
+    refuse(PyExc_ValueError, std::string(name) + " must have shape " + text(shape) + ", got " + text(t.sizes()));
+  if (t.get_device() != dev) refuse(PyExc_ValueError, std::string(name) + " is on another device");
+  if (t.stride(3) != 1) refuse(PyExc_ValueError, std::string(name) + "'s rows must be contiguous");
+  int64_t s[3];
+  for (int i = 0; i < 3; ++i) {
+    s[i] = t.size(i) > 1 ? t.stride(i) : 0;  // (a dimension of one element has no stride)
+    if (s[i] % 8 != 0)
+      refuse(PyExc_ValueError, std::string(name) + "'s strides must be multiples of 8 elements");
+  }
+  return vsd_rows{pointer(t), s[0], s[1], s[2]};
+}
+
+// rope(q, k, v, k_cache, v_cache, k_scale, v_scale, block_table, pos_base, turns, pos_offset,
+//      rope_base, n_valid, q_weight, k_weight, eps, interleaved, amplitude, q_out, k_out, stream)
+//   -> q_out with a cache; (q_out, k_out) where v and the cache are None
+PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 21, [&]() -> PyObject* {
+    const at::Tensor& q = as_tensor(a[0], "q");
+    if (!q.is_cuda()) refuse(PyExc_ValueError, "q must be a CUDA tensor");
+    if (q.dim() != 4) refuse(PyExc_ValueError, "q must have 4 dimensions, got shape " + text(q.sizes()));
+    const Place p(q, a[20]);
+    const int64_t B = q.size(0), rows = q.size(1), d = q.size(3);
+    const bool cached = a[3] != Py_None, with_k = cached || a[1] != Py_None;
+    vsd_geom g;
+    g.B = dim_of(B, "B");
+    g.Hq = dim_of(q.size(2), "Hq");
+    g.head_dim = dim_of(d, "head_dim");
+    g.Hkv = g.Hq;
+    Cache c{};
+    const int32_t* bt = nullptr;
+    if (cached) {
+      c = any_cache(a + 3, p.dev, &g);
+      bt = table_of(as_tensor(a[7], "block_table"), B, p.dev, &g);
+    } else if (with_k) {
+      const at::Tensor& k = as_tensor(a[1], "k");
+      if (k.dim() != 4) refuse(PyExc_ValueError, "k must have 4 dimensions, got shape " + text(k.sizes()));
+      g.Hkv = dim_of(k.size(2), "Hkv");
+    }
+    const vsd_rows qr = strided(q, {B, rows, g.Hq, g.head_dim}, p.dev, "q");
+    vsd_rows kr{}, vr{};
+    if (with_k) kr = strided(as_tensor(a[1], "k"), {B, rows, g.Hkv, g.head_dim}, p.dev, "k");
+    if (cached) vr = strided(as_tensor(a[2], "v"), {B, rows, g.Hkv, g.head_dim}, p.dev, "v");
+    const int32_t* pos = lengths(as_tensor(a[8], "pos_base"), B, p.dev, "pos_base");
+    const int32_t* from = a[11] == Py_None ? nullptr : lengths(as_tensor(a[11], "rope_base"), B, p.dev, "rope_base");
+    const int32_t* nv = a[12] == Py_None ? nullptr : lengths(as_tensor(a[12], "n_valid"), B, p.dev, "n_valid");
+    vsd_rope r{};
+    if (a[9] != Py_None) {
+      const at::Tensor& t = as_tensor(a[9], "turns");
+      need(t, at::kLong, 1, "turns");
+      if (t.get_device() != p.dev) refuse(PyExc_ValueError, "turns is on another device");
+      if (t.size(0) > INT_MAX / 2) refuse(PyExc_ValueError, "turns is too large");
+      r.turns = static_cast<const int64_t*>(pointer(t));
+      r.rot_dim = static_cast<int>(2 * t.size(0));
+    }
+    const auto weight = [&](PyObject* o, const char* name) -> const void* {
+      if (o == Py_None) return nullptr;
+      const at::Tensor& w = as_tensor(o, name);
+      need(w, at::kBFloat16, {d}, p.dev, name);
+      return pointer(w);
+    };
+    r.q_weight = weight(a[13], "q_weight");
+    r.k_weight = weight(a[14], "k_weight");
+    r.eps = as_float(a[15]);
+    r.interleaved = as_bool(a[16]) ? 1 : 0;
+    r.amplitude = as_float(a[17]);
+    const int nrows = dim_of(rows, "q"), offset = as_int(a[10], "pos_offset");
+    Output qo, ko;
+    qo.take(a[18], p, at::kBFloat16, {B, rows, g.Hq, g.head_dim}, "q_out");
+    if (with_k && !cached) ko.take(a[19], p, at::kBFloat16, {B, rows, g.Hkv, g.head_dim}, "k_out");
+    // (what a new output's memory held before must not show in the rows behind n_valid)
+    const unsigned zeroed = (qo.made.defined() ? VSD_ROPE_ZEROED_Q : 0u) | (ko.made.defined() ? VSD_ROPE_ZEROED_K : 0u);
+    const char* name = !cached ? "vsd_norm_rope" : c.ks ? "vsd_norm_rope_append_kv_quant" : "vsd_norm_rope_append_kv";
+    check(without_gil([&] {
+            if (!cached)
+              return g_calls.rope(&g, nrows, &qr, with_k ? &kr : nullptr, &r, pos, offset, nv, qo.at, ko.at, zeroed,
+                                  p.stream);
+            if (c.ks == nullptr)
+              return g_calls.rope_append(&g, nrows, &qr, &kr, &vr, &r, bt, pos, offset, from, nv, qo.at, zeroed, c.k,
+                                         c.v, p.stream);
+            return g_calls.rope_append_quant(&g, nrows, &qr, &kr, &vr, &r, bt, pos, offset, from, nv, qo.at, zeroed,
+                                             c.k, c.v, c.ks, c.vs, p.stream);
+          }),
+          name);
+    if (cached) return qo.result();
+    return Py_BuildValue("(NN)", qo.result(), ko.result());
+  });
+}
+
+// weights(logits, q, k_cache, k_scale, block_table, prefix_len, weights, scale, rows, stream)
+PyObject* py_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 10, [&]() -> PyObject* {
+    const at::Tensor &q = as_tensor(a[1], "q"), &lg = as_tensor(a[0], "logits");
+    need(q, at::kBFloat16, 4, "q");
+    const Place p(q, a[9]);
+    const at::Tensor& kc = as_tensor(a[2], "k_cache");
+    const bool quant = a[3] != Py_None;
+    need(kc, quant ? at::kFloat8_e4m3fn : at::kBFloat16, 4, "k_cache");
+    if (kc.get_device() != p.dev) refuse(PyExc_ValueError, "k_cache is on another device");
+    vsd_geom g;
+    const int64_t B = q.size(0);
+    const int R = dim_of(q.size(1), "R");
+    g.B = dim_of(B, "B");
+    g.Hq = dim_of(q.size(2), "Hq");
+    g.num_blocks = dim_of(kc.size(0), "num_blocks");
+    g.Hkv = dim_of(kc.size(1), "Hkv");
+    g.page_size = dim_of(kc.size(2), "page_size");
+    g.head_dim = dim_of(kc.size(3), "head_dim");
+    need(q, at::kBFloat16, {B, R, g.Hq, g.head_dim}, p.dev, "q");
+    const float* ks = nullptr;
+    if (quant) {
+      const at::Tensor& s = as_tensor(a[3], "k_scale");
+      need(s, at::kFloat, {g.num_blocks, g.Hkv}, p.dev, "k_scale");
+      ks = static_cast<const float*>(pointer(s));
+    }
+    const int32_t* bt = table_of(as_tensor(a[4], "block_table"), B, p.dev, &g);
+    const int32_t* pl = lengths(as_tensor(a[5], "prefix_len"), B, p.dev, "prefix_len");
+    need(lg, at::kFloat, 4, "logits");
+    const int C = dim_of(lg.size(1), "logits"), P_max = dim_of(lg.size(3), "P_max");
+    need(lg, at::kFloat, {B, C, g.Hq, P_max}, p.dev, "logits");
+    const at::Tensor& w = as_tensor(a[6], "weights");
+    need(w, at::kFloat, 3, "weights");
+    need(w, at::kFloat, {B, g.Hkv, w.size(2)}, p.dev, "weights");
+    const int stride = dim_of(w.size(2), "weights");
+    if (stride < P_max) refuse(PyExc_ValueError, "weights must have room for every position of logits");
+    const float scale = as_float(a[7]);
+    int rows[16];
+    if (C > 16) refuse(PyExc_ValueError, "logits has more than 16 rows");
+    if (a[8] == Py_None) {  // all rows, or a verification's two collected ones (one of them, written twice)
+      if (C != R && C != 2) refuse(PyExc_ValueError, "rows are needed for these logits");
+      for (int c = 0; c < C; ++c) rows[c] = C == R ? c : c == 0 ? 0 : R == 1 ? -1 : R - 1;
+    } else {
+      PyObject* seq = PySequence_Fast(a[8], "rows must be a sequence of integers");
+      if (seq == nullptr) throw PythonError{};
+      const Py_ssize_t count = PySequence_Fast_GET_SIZE(seq);
+      bool bad = count != C;
+      for (int c = 0; c < C && !bad; ++c) {
+        const long v = PyLong_AsLong(PySequence_Fast_GET_ITEM(seq, c));
+        bad = v < -1 || v >= R || PyErr_Occurred();
+        rows[c] = static_cast<int>(v);
+      }
+      Py_DECREF(seq);
+      if (PyErr_Occurred()) throw PythonError{};
+      if (bad) refuse(PyExc_ValueError, "rows must name a verify row (or -1) for each row of logits");
+    }
+    check(without_gil([&] {
+            const float* at = static_cast<const float*>(pointer(lg));
+            float* to = static_cast<float*>(pointer(w));
+            if (quant)
+              return g_calls.weights_quant(&g, R, C, rows, at, pointer(q), pointer(kc), ks, bt, pl, P_max, scale, to,
+                                           stride, p.stream);
+            return g_calls.weights(&g, R, C, rows, at, pointer(q), pointer(kc), bt, pl, P_max, scale, to, stride,
+                                   p.stream);
+          }),
+          quant ? "vsd_accumulate_weights_quant" : "vsd_accumulate_weights");
+    Py_INCREF(a[6]);
+    return a[6];
+  });
+}
+
+// compact(k_cache, v_cache, k_scale, v_scale, block_table, dst_table, prefix_len, idx, n_sel,
+//         weights, weights_out, stream) -> weights_out
+PyObject* py_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 12, [&]() -> PyObject* {
+    const at::Tensor& kc = as_tensor(a[0], "k_cache");
+    if (!kc.is_cuda()) refuse(PyExc_ValueError, "k_cache must be a CUDA tensor");
+    const Place p(kc, a[11]);
+    vsd_geom g, other;
+    const Cache c = any_cache(a, p.dev, &g);
+    const at::Tensor& pt = as_tensor(a[6], "prefix_len");
+    need(pt, at::kInt, 1, "prefix_len");
+    const int64_t B = pt.size(0);
+    const int32_t* pl = lengths(pt, B, p.dev, "prefix_len");
+    const int32_t* bt = table_of(as_tensor(a[4], "block_table"), B, p.dev, &g);
+    const int32_t* dt = table_of(as_tensor(a[5], "dst_table"), B, p.dev, &other);
+    g.B = dim_of(B, "B");
+    g.Hq = g.Hkv;
+    const at::Tensor &it = as_tensor(a[7], "idx"), &nt = as_tensor(a[8], "n_sel");
+    const bool heads = it.dim() == 3;
+    need(it, at::kInt, heads ? 3 : 2, "idx");
+    const int k = dim_of(it.size(heads ? 2 : 1), "idx");
+    if (heads) {
+      need(it, at::kInt, {B, g.Hkv, k}, p.dev, "idx");
+      need(nt, at::kInt, {B, g.Hkv}, p.dev, "n_sel");
+    } else {
+      need(it, at::kInt, {B, k}, p.dev, "idx");
+      need(nt, at::kInt, {B}, p.dev, "n_sel");
+    }
+    const float* w = nullptr;
+    int ws = 0, wos = 0;
+    Output wo;
+    if (a[9] != Py_None) {
+      const at::Tensor& wt = as_tensor(a[9], "weights");
+      need(wt, at::kFloat, 3, "weights");
+      need(wt, at::kFloat, {B, g.Hkv, wt.size(2)}, p.dev, "weights");
+      w = static_cast<const float*>(pointer(wt));
+      ws = dim_of(wt.size(2), "weights");
+      if (a[10] != Py_None) {
+        const at::Tensor& ot = as_tensor(a[10], "weights_out");
+        need(ot, at::kFloat, 3, "weights_out");
+        wos = dim_of(ot.size(2), "weights_out");
+        if (wos < k) refuse(PyExc_ValueError, "weights_out must have room for every index");
+        wo.take(a[10], p, at::kFloat, {B, g.Hkv, wos}, "weights_out");
+      } else {
+        wos = k;
+        wo.take(Py_None, p, at::kFloat, {B, g.Hkv, wos}, "weights_out");
+        wo.made.zero_();  // (a list that is refused leaves its row)
+      }
+    } else if (a[10] != Py_None) {
+      refuse(PyExc_ValueError, "weights_out needs weights");
+    }
+    check(without_gil([&] {
+            const int32_t* idx = static_cast<const int32_t*>(pointer(it));
+            const int32_t* ns = static_cast<const int32_t*>(pointer(nt));
+            float* to = static_cast<float*>(wo.at);
+            const int lists = heads ? g.Hkv : 1, dst = other.max_blocks_per_seq;
+            if (c.ks != nullptr)
+              return g_calls.compact_quant(&g, bt, dt, dst, pl, idx, ns, lists, k, c.k, c.v, c.ks, c.vs, w, ws, to,
+                                           wos, p.stream);
+            return g_calls.compact(&g, bt, dt, dst, pl, idx, ns, lists, k, c.k, c.v, w, ws, to, wos, p.stream);
+          }),
+          c.ks ? "vsd_compact_kv_quant" : "vsd_compact_kv");
+    return wo.result();
+  });
+}
+
 // attach(error class, addresses of the six library calls)
 PyObject* py_attach(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 7) {
@@ -417,11 +670,34 @@ PyObject* py_attach(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+// attach_more(addresses of the seven library calls of rows, weights and eviction)
+PyObject* py_attach_more(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 7) {
+    PyErr_SetString(PyExc_TypeError, "attach_more takes seven addresses");
+    return nullptr;
+  }
+  void* at[7];
+  for (int i = 0; i < 7; ++i) {
+    at[i] = PyLong_AsVoidPtr(a[i]);
+    if (PyErr_Occurred()) return nullptr;
+  }
+  g_calls.rope = reinterpret_cast<decltype(g_calls.rope)>(at[0]);
+  g_calls.rope_append = reinterpret_cast<decltype(g_calls.rope_append)>(at[1]);
+  g_calls.rope_append_quant = reinterpret_cast<decltype(g_calls.rope_append_quant)>(at[2]);
+  g_calls.weights = reinterpret_cast<decltype(g_calls.weights)>(at[3]);
+  g_calls.weights_quant = reinterpret_cast<decltype(g_calls.weights_quant)>(at[4]);
+  g_calls.compact = reinterpret_cast<decltype(g_calls.compact)>(at[5]);
+  g_calls.compact_quant = reinterpret_cast<decltype(g_calls.compact_quant)>(at[6]);
+  Py_RETURN_NONE;
+}
+
 #define VSD_METHOD(name, fn) \
   {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(fn)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {VSD_METHOD("attach", py_attach), VSD_METHOD("append", py_append),
                            VSD_METHOD("read", py_read),     VSD_METHOD("verify", py_verify),
-                           VSD_METHOD("sparse", py_sparse), {nullptr, nullptr, 0, nullptr}};
+                           VSD_METHOD("sparse", py_sparse), VSD_METHOD("attach_more", py_attach_more),
+                           VSD_METHOD("rope", py_rope),     VSD_METHOD("weights", py_weights),
+                           VSD_METHOD("compact", py_compact), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};
 

@@ -253,4 +253,78 @@ cudaError_t launch_verify_quant(const VerifyArgs& a, const QuantScales& s, const
 size_t sparse_quant_workspace_bytes(int B, int Hkv, int G, int head_dim, int k_max, int max_tail);
 cudaError_t launch_sparse_quant(const SparseArgs& a, const QuantScales& s, cudaStream_t stream);
 
+// ---------------------------------------------------------------- normed and rotated rows
+// bf16 rows by strides (elements): row (b, t, head) at data + b * batch + t * row + head * head.
+struct StridedRows {
+  const void* data;
+  long long batch, row, head;
+};
+
+struct RopeArgs {
+  StridedRows q, k, v;        // k.data null: queries alone
+  const int64_t* turns;
+  const void* q_weight;
+  const void* k_weight;
+  float eps, amplitude;
+  int rot_dim, interleaved;
+  const int32_t* rope_base;   // positions of the rotation (may be pos_base)
+  const int32_t* pos_base;    // positions in the cache
+  const int32_t* n_valid;
+  const int32_t* block_table; // null: k goes to k_out
+  void* q_out;
+  void* k_out;
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;             // not null: an 8-bit cache
+  float* v_scale;
+  unsigned* status;
+  int B, n, Hq, Hkv, d, max_blocks, num_blocks, pos_offset;
+  unsigned zeroed;
+  int num_sms;
+};
+
+cudaError_t launch_norm_rope(const RopeArgs& a, cudaStream_t stream);
+cudaError_t launch_norm_rope_quant(const RopeArgs& a, cudaStream_t stream);
+
+// ---------------------------------------------------------------- accumulated weights
+constexpr int kMaxWeightSlots = 16;
+constexpr int kMaxWeightCols = 64;  // slots times heads of a group
+
+struct WeightsArgs {
+  const float* logits;
+  const void* q;
+  const void* k_cache;
+  const float* k_scale;  // not null: an 8-bit cache
+  const int32_t* block_table;
+  const int32_t* prefix_len;
+  float* weights;
+  unsigned* status;
+  int B, Hq, Hkv, G, R, C, d, max_blocks, num_blocks, P_max, weights_stride;
+  float scale;
+  int used;                       // slots that count
+  int8_t slot[kMaxWeightSlots];   // ... their places
+  int8_t row[kMaxWeightSlots];    // ... and verify rows
+  int num_sms;
+};
+
+cudaError_t launch_accumulate_weights(const WeightsArgs& a, cudaStream_t stream);
+
+// ---------------------------------------------------------------- eviction
+struct CompactArgs {
+  void* cache[2];
+  float* scale[2];  // not null: an 8-bit cache
+  const int32_t* block_table;
+  const int32_t* dst_table;
+  const int32_t* prefix_len;
+  const int32_t* idx;
+  const int32_t* n_sel;
+  const float* weights;
+  float* weights_out;
+  unsigned* status;
+  int B, Hkv, d, max_blocks, num_blocks, dst_blocks, idx_heads, k_max, w_stride, w_out_stride;
+  int num_sms;
+};
+
+cudaError_t launch_compact(const CompactArgs& a, cudaStream_t stream);
+
 }  // namespace vsd

@@ -1241,4 +1241,305 @@ vsd_status vsd_sparse_decode_attn_quant(const vsd_geom* geom, const void* q,
   return e == cudaSuccess ? VSD_OK : cuda_fail(e);
 }
 
+// ---------------------------------------------------------------- normed and rotated rows
+namespace {
+
+bool rows_ok(const vsd_rows* r) {
+  return r != nullptr && r->data != nullptr && aligned(r->data, 16) && r->batch_stride % 8 == 0 &&
+         r->row_stride % 8 == 0 && r->head_stride % 8 == 0;
+}
+
+vsd::StridedRows rows_of(const vsd_rows* r) {
+  return vsd::StridedRows{r->data, r->batch_stride, r->row_stride, r->head_stride};
+}
+
+// The checks that the calls share.  *run is false where there is nothing to do.
+vsd_status rope_checks(const vsd_geom* geom, int n, const vsd_rows* q, const vsd_rows* k,
+                       const vsd_rope* rope, const int32_t* pos_base, const int32_t* rope_base,
+                       const int32_t* n_valid, const void* q_out, unsigned zeroed, bool* run) {
+  *run = false;
+  vsd_status st = check_geom(geom);
+  if (st != VSD_OK) return st;
+  if (n < 0 || rope == nullptr || (zeroed & ~(VSD_ROPE_ZEROED_Q | VSD_ROPE_ZEROED_K)) != 0u)
+    return VSD_ERR_INVALID_ARG;
+  if (rope->rot_dim < 0 || rope->rot_dim > geom->head_dim) return VSD_ERR_INVALID_ARG;
+  if (rope->rot_dim % 8 != 0) return VSD_ERR_UNSUPPORTED;
+  if (!std::isfinite(rope->amplitude) || !std::isfinite(rope->eps) || rope->eps < 0.f)
+    return VSD_ERR_INVALID_ARG;
+  if (geom->B == 0 || n == 0) return VSD_OK;
+  const double heads = geom->Hq + 2.0 * geom->Hkv;
+  if (static_cast<double>(geom->B) * n * (heads / 2 + 1) > 2147483647.0) return VSD_ERR_UNSUPPORTED;
+  if (!rows_ok(q) || !pos_base || !q_out || (k != nullptr && !rows_ok(k)))
+    return VSD_ERR_INVALID_ARG;
+  if (!aligned(q_out, 16) || !aligned(pos_base, 4) || !aligned(rope_base, 4) ||
+      !aligned(n_valid, 4) || !aligned(rope->q_weight, 16) || !aligned(rope->k_weight, 16))
+    return VSD_ERR_INVALID_ARG;
+  if (rope->rot_dim > 0 && (!rope->turns || !aligned(rope->turns, 8))) return VSD_ERR_INVALID_ARG;
+  *run = true;
+  return VSD_OK;
+}
+
+// Their arguments, checked.
+vsd_status rope_args(const vsd_geom* geom, int n, const vsd_rows* q, const vsd_rows* k,
+                     const vsd_rope* rope, const int32_t* pos_base, int pos_offset,
+                     const int32_t* rope_base, const int32_t* n_valid, void* q_out,
+                     unsigned zeroed, vsd::RopeArgs* a) {
+  *a = vsd::RopeArgs{};
+  vsd_status st = device_info(&a->status, &a->num_sms);
+  if (st != VSD_OK) return st;
+  a->q = rows_of(q);
+  if (k != nullptr) a->k = rows_of(k);
+  a->turns = rope->turns;
+  a->q_weight = rope->q_weight;
+  a->k_weight = rope->k_weight;
+  a->eps = rope->eps;
+  a->amplitude = rope->amplitude;
+  a->rot_dim = rope->rot_dim;
+  a->interleaved = rope->interleaved != 0;
+  a->rope_base = rope_base != nullptr ? rope_base : pos_base;
+  a->pos_base = pos_base;
+  a->n_valid = n_valid;
+  a->q_out = q_out;
+  a->B = geom->B;
+  a->n = n;
+  a->Hq = geom->Hq;
+  a->Hkv = geom->Hkv;
+  a->d = geom->head_dim;
+  a->max_blocks = geom->max_blocks_per_seq;
+  a->num_blocks = geom->num_blocks;
+  a->pos_offset = pos_offset;
+  a->zeroed = zeroed;
+  return VSD_OK;
+}
+
+}  // namespace
+
+vsd_status vsd_norm_rope(const vsd_geom* geom, int n, const vsd_rows* q, const vsd_rows* k,
+                         const vsd_rope* rope, const int32_t* pos_base, int pos_offset,
+                         const int32_t* n_valid, void* q_out, void* k_out, unsigned zeroed,
+                         void* stream) {
+  if (geom == nullptr) return VSD_ERR_INVALID_ARG;
+  vsd_geom g = *geom;  // (no cache)
+  g.page_size = 16;
+  g.max_blocks_per_seq = g.num_blocks = 1;
+  bool run = false;
+  vsd_status st = rope_checks(&g, n, q, k, rope, pos_base, nullptr, n_valid, q_out, zeroed, &run);
+  if (st != VSD_OK || !run) return st;
+  if (k != nullptr && (!k_out || !aligned(k_out, 16))) return VSD_ERR_INVALID_ARG;
+  vsd::RopeArgs a;
+  st = rope_args(&g, n, q, k, rope, pos_base, pos_offset, nullptr, n_valid, q_out, zeroed, &a);
+  if (st != VSD_OK) return st;
+  a.k_out = k_out;
+  cudaError_t e = vsd::launch_norm_rope(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VSD_OK : cuda_fail(e);
+}
+
+vsd_status vsd_norm_rope_append_kv(const vsd_geom* geom, int n, const vsd_rows* q,
+                                   const vsd_rows* k, const vsd_rows* v, const vsd_rope* rope,
+                                   const int32_t* block_table, const int32_t* pos_base,
+                                   int pos_offset, const int32_t* rope_base,
+                                   const int32_t* n_valid, void* q_out, unsigned zeroed,
+                                   void* k_cache, void* v_cache, void* stream) {
+  bool run = false;
+  vsd_status st = rope_checks(geom, n, q, k, rope, pos_base, rope_base, n_valid, q_out, zeroed,
+                              &run);
+  if (st != VSD_OK || !run) return st;
+  if (!k || !rows_ok(v) || !block_table || !k_cache || !v_cache || !aligned(block_table, 4) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16))
+    return VSD_ERR_INVALID_ARG;
+  vsd::RopeArgs a;
+  st = rope_args(geom, n, q, k, rope, pos_base, pos_offset, rope_base, n_valid, q_out, zeroed, &a);
+  if (st != VSD_OK) return st;
+  a.v = rows_of(v);
+  a.block_table = block_table;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  cudaError_t e = vsd::launch_norm_rope(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VSD_OK : cuda_fail(e);
+}
+
+vsd_status vsd_norm_rope_append_kv_quant(const vsd_geom* geom, int n, const vsd_rows* q,
+                                         const vsd_rows* k, const vsd_rows* v,
+                                         const vsd_rope* rope, const int32_t* block_table,
+                                         const int32_t* pos_base, int pos_offset,
+                                         const int32_t* rope_base, const int32_t* n_valid,
+                                         void* q_out, unsigned zeroed, void* k_cache,
+                                         void* v_cache, float* k_scale, float* v_scale,
+                                         void* stream) {
+  bool run = false;
+  vsd_status st = rope_checks(geom, n, q, k, rope, pos_base, rope_base, n_valid, q_out, zeroed,
+                              &run);
+  if (st != VSD_OK || !run) return st;
+  if (2.0 * geom->B * vsd::quant_pages(n) * geom->Hkv > 2147483647.0) return VSD_ERR_UNSUPPORTED;
+  if (!k || !rows_ok(v) || !block_table || !aligned(block_table, 4) ||
+      !quant_cache_ok(k_cache, v_cache, k_scale, v_scale))
+    return VSD_ERR_INVALID_ARG;
+  vsd::RopeArgs a;
+  st = rope_args(geom, n, q, k, rope, pos_base, pos_offset, rope_base, n_valid, q_out, zeroed, &a);
+  if (st != VSD_OK) return st;
+  a.v = rows_of(v);
+  a.block_table = block_table;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  cudaError_t e = vsd::launch_norm_rope_quant(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VSD_OK : cuda_fail(e);
+}
+
+// ---------------------------------------------------------------- accumulated weights
+namespace {
+
+constexpr long long kMaxPairs = 1ll << 26;  // (sequence, KV head) pairs: times a cluster's CTAs below 2^31
+
+vsd_status weights_call(const vsd_geom* geom, int R, int C, const int* rows, const float* logits,
+                        const void* q, const void* k_cache, const float* k_scale,
+                        const int32_t* block_table, const int32_t* prefix_len, int P_max,
+                        float scale, float* weights, int weights_stride, void* stream) {
+  vsd_status st = verify_checks(geom, R, P_max);
+  if (st != VSD_OK) return st;
+  if (C < 0 || weights_stride < P_max) return VSD_ERR_INVALID_ARG;
+  const int G = geom->Hq / geom->Hkv;
+  if (C > vsd::kMaxWeightSlots || C * G > vsd::kMaxWeightCols || P_max > kMaxPositions ||
+      static_cast<long long>(geom->B) * geom->Hkv >= kMaxPairs)
+    return VSD_ERR_UNSUPPORTED;
+  if (C > 0 && rows == nullptr) return VSD_ERR_INVALID_ARG;
+  vsd::WeightsArgs a = {};
+  for (int c = 0; c < C; ++c) {
+    if (rows[c] < -1 || rows[c] >= R) return VSD_ERR_INVALID_ARG;
+    if (rows[c] < 0) continue;
+    a.slot[a.used] = static_cast<int8_t>(c);
+    a.row[a.used++] = static_cast<int8_t>(rows[c]);
+  }
+  if (!std::isfinite(scale)) return VSD_ERR_INVALID_ARG;
+  if (geom->B == 0 || P_max == 0 || a.used == 0) return VSD_OK;
+  if (!logits || !q || !k_cache || !block_table || !prefix_len || !weights)
+    return VSD_ERR_INVALID_ARG;
+  if (!aligned(logits, 4) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(k_scale, 4) ||
+      !aligned(block_table, 4) || !aligned(prefix_len, 4) || !aligned(weights, 4))
+    return VSD_ERR_INVALID_ARG;
+  st = device_info(&a.status, &a.num_sms);
+  if (st != VSD_OK) return st;
+  a.logits = logits;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.k_scale = k_scale;
+  a.block_table = block_table;
+  a.prefix_len = prefix_len;
+  a.weights = weights;
+  a.B = geom->B;
+  a.Hq = geom->Hq;
+  a.Hkv = geom->Hkv;
+  a.G = G;
+  a.R = R;
+  a.C = C;
+  a.d = geom->head_dim;
+  a.max_blocks = geom->max_blocks_per_seq;
+  a.num_blocks = geom->num_blocks;
+  a.P_max = P_max;
+  a.weights_stride = weights_stride;
+  a.scale = scale;
+  cudaError_t e = vsd::launch_accumulate_weights(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VSD_OK : cuda_fail(e);
+}
+
+vsd_status compact_call(const vsd_geom* geom, const int32_t* block_table,
+                        const int32_t* dst_table, int dst_blocks, const int32_t* prefix_len,
+                        const int32_t* idx, const int32_t* n_sel, int idx_heads, int k_max,
+                        void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                        const float* weights, int weights_stride, float* weights_out,
+                        int weights_out_stride, void* stream) {
+  vsd_status st = check_geom(geom);
+  if (st != VSD_OK) return st;
+  if (dst_blocks < 0 || k_max < 0 || (idx_heads != 1 && idx_heads != geom->Hkv))
+    return VSD_ERR_INVALID_ARG;
+  if ((weights == nullptr) != (weights_out == nullptr) ||
+      (weights != nullptr && (weights_stride < 0 || weights_out_stride < k_max)) ||
+      (weights != nullptr && weights == weights_out && weights_stride != weights_out_stride))
+    return VSD_ERR_INVALID_ARG;
+  if (static_cast<long long>(geom->B) * geom->Hkv >= kMaxPairs || k_max > kMaxPositions)
+    return VSD_ERR_UNSUPPORTED;
+  if (geom->B == 0) return VSD_OK;
+  if (!block_table || !dst_table || !prefix_len || !n_sel || !k_cache || !v_cache ||
+      (k_max > 0 && !idx))
+    return VSD_ERR_INVALID_ARG;
+  if (!aligned(block_table, 4) || !aligned(dst_table, 4) || !aligned(prefix_len, 4) ||
+      !aligned(idx, 4) || !aligned(n_sel, 4) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(weights, 4) ||
+      !aligned(weights_out, 4))
+    return VSD_ERR_INVALID_ARG;
+  vsd::CompactArgs a = {};
+  st = device_info(&a.status, &a.num_sms);
+  if (st != VSD_OK) return st;
+  a.cache[0] = k_cache;
+  a.cache[1] = v_cache;
+  a.scale[0] = k_scale;
+  a.scale[1] = v_scale;
+  a.block_table = block_table;
+  a.dst_table = dst_table;
+  a.prefix_len = prefix_len;
+  a.idx = idx;
+  a.n_sel = n_sel;
+  a.weights = weights;
+  a.weights_out = weights_out;
+  a.B = geom->B;
+  a.Hkv = geom->Hkv;
+  a.d = geom->head_dim;
+  a.max_blocks = geom->max_blocks_per_seq;
+  a.num_blocks = geom->num_blocks;
+  a.dst_blocks = dst_blocks;
+  a.idx_heads = idx_heads;
+  a.k_max = k_max;
+  a.w_stride = weights_stride;
+  a.w_out_stride = weights_out_stride;
+  cudaError_t e = vsd::launch_compact(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VSD_OK : cuda_fail(e);
+}
+
+}  // namespace
+
+vsd_status vsd_accumulate_weights(const vsd_geom* geom, int R, int C, const int* rows,
+                                  const float* logits, const void* q, const void* k_cache,
+                                  const int32_t* block_table, const int32_t* prefix_len,
+                                  int P_max, float scale, float* weights, int weights_stride,
+                                  void* stream) {
+  return weights_call(geom, R, C, rows, logits, q, k_cache, nullptr, block_table, prefix_len,
+                      P_max, scale, weights, weights_stride, stream);
+}
+
+vsd_status vsd_accumulate_weights_quant(const vsd_geom* geom, int R, int C, const int* rows,
+                                        const float* logits, const void* q, const void* k_cache,
+                                        const float* k_scale, const int32_t* block_table,
+                                        const int32_t* prefix_len, int P_max, float scale,
+                                        float* weights, int weights_stride, void* stream) {
+  if (k_scale == nullptr && geom != nullptr && geom->B != 0) return VSD_ERR_INVALID_ARG;
+  return weights_call(geom, R, C, rows, logits, q, k_cache, k_scale, block_table, prefix_len,
+                      P_max, scale, weights, weights_stride, stream);
+}
+
+vsd_status vsd_compact_kv(const vsd_geom* geom, const int32_t* block_table,
+                          const int32_t* dst_table, int dst_blocks, const int32_t* prefix_len,
+                          const int32_t* idx, const int32_t* n_sel, int idx_heads, int k_max,
+                          void* k_cache, void* v_cache, const float* weights,
+                          int weights_stride, float* weights_out, int weights_out_stride,
+                          void* stream) {
+  return compact_call(geom, block_table, dst_table, dst_blocks, prefix_len, idx, n_sel, idx_heads,
+                      k_max, k_cache, v_cache, nullptr, nullptr, weights, weights_stride,
+                      weights_out, weights_out_stride, stream);
+}
+
+vsd_status vsd_compact_kv_quant(const vsd_geom* geom, const int32_t* block_table,
+                                const int32_t* dst_table, int dst_blocks,
+                                const int32_t* prefix_len, const int32_t* idx,
+                                const int32_t* n_sel, int idx_heads, int k_max, void* k_cache,
+                                void* v_cache, float* k_scale, float* v_scale,
+                                const float* weights, int weights_stride, float* weights_out,
+                                int weights_out_stride, void* stream) {
+  if ((k_scale == nullptr || v_scale == nullptr) && geom != nullptr && geom->B != 0)
+    return VSD_ERR_INVALID_ARG;
+  return compact_call(geom, block_table, dst_table, dst_blocks, prefix_len, idx, n_sel, idx_heads,
+                      k_max, k_cache, v_cache, k_scale, v_scale, weights, weights_stride,
+                      weights_out, weights_out_stride, stream);
+}
+
 }  // extern "C"
