@@ -7,11 +7,14 @@
 // keys a row) are products of the queries and the cache's rows here.
 //
 // How: one cluster for each (sequence, KV head), each CTA with a slice of the positions and all
-// columns (counted rows times heads of the group).  A CTA keeps, for each column, the maximum
-// and the sum of exponentials of its slice; the cluster's CTAs exchange those once through
-// distributed shared memory, and each then adds e^(z - m) / l over the columns to its
-// positions.  A thread owns four positions of each 2048, so the sums of a position are formed in
-// one thread, in column order.
+// columns (counted rows times heads of the group).  A CTA forms, for each column, the maximum
+// and the sum of exponentials of its slice and writes them into every CTA of the cluster; after
+// one cluster barrier each adds the columns' weights to its positions.  A thread owns four
+// positions of a step, so the sums of a position are formed in one thread, in column order.
+// The operands of the few products of the verify block come while the logits are on their way.
+//   Where a slice is one step of at most 16 columns and the clusters fit the GPU at once, the
+// exponentials stay in registers between the passes (one exponential for each logit, one read).
+// Otherwise the slices are read again, from L2, by smaller CTAs of which several share an SM.
 #include <cooperative_groups.h>
 
 #include "launch.h"
@@ -23,9 +26,6 @@ namespace cg = cooperative_groups;
 namespace vsd {
 namespace {
 
-constexpr int kWThreads = 512;
-constexpr int kWWarps = kWThreads / 32;
-constexpr int kWTile = kWThreads * 4;  // positions of a CTA's step
 constexpr int kWMaxCluster = 16;
 constexpr int kWGroup = 8;             // columns at a time
 constexpr int kPageW = 16;
@@ -51,24 +51,42 @@ struct Stat {
 
 __device__ __forceinline__ float exp_of(float x) { return ex2(x * kLog2e); }
 
-// Two parts of a sum.  (Minus infinity: nothing yet; NaN stays.)
-__device__ __forceinline__ Stat join(Stat a, Stat b) {
-  const float m = a.m > b.m || isnan(a.m) ? a.m : b.m;
-  if (m == -INFINITY) return Stat{m, a.l + b.l};
-  return Stat{m, a.l * exp_of(a.m - m) + b.l * exp_of(b.m - m)};
+// What exponents are taken against: the maximum, or 0 where there is nothing yet.
+__device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.f : m; }
+
+// The sum of kLanes neighbouring lanes' parts (in all of them).  A maximum ignores NaN; the sum
+// keeps it.
+template <int kLanes>
+__device__ __forceinline__ Stat join_lanes(Stat s) {
+  float m = s.m;
+#pragma unroll
+  for (int x = kLanes / 2; x >= 1; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+  float l = s.l * exp_of(s.m - reference(m));
+#pragma unroll
+  for (int x = kLanes / 2; x >= 1; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+  return Stat{m, l};
 }
 
-// Position of a thread's value j of a step: next to each other (vectors) or kWThreads apart.
-template <bool kVec>
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// Position of a thread's value j of a step of kThreads * 4: next to each other (vectors) or
+// kThreads apart.
+template <bool kVec, int kThreads>
 __device__ __forceinline__ int place(int base, int j) {
-  return kVec ? base + 4 * static_cast<int>(threadIdx.x) + j : base + j * kWThreads + static_cast<int>(threadIdx.x);
+  return kVec ? base + 4 * static_cast<int>(threadIdx.x) + j : base + j * kThreads + static_cast<int>(threadIdx.x);
 }
 
 // A thread's four values of a step (those at `end` and beyond: `fill`).
-template <bool kVec>
+template <bool kVec, int kThreads>
 __device__ __forceinline__ void load4(const float* p, int base, int end, float fill, float (&z)[4]) {
-  if (kVec && place<kVec>(base, 3) < end) {
-    const uint4 v = ldg_stream16(p + place<kVec>(base, 0));
+  if (kVec && place<kVec, kThreads>(base, 3) < end) {
+    const uint4 v = ldg_stream16(p + place<kVec, kThreads>(base, 0));
     z[0] = __uint_as_float(v.x);
     z[1] = __uint_as_float(v.y);
     z[2] = __uint_as_float(v.z);
@@ -77,59 +95,111 @@ __device__ __forceinline__ void load4(const float* p, int base, int end, float f
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int at = place<kVec>(base, j);
+    const int at = place<kVec, kThreads>(base, j);
     z[j] = at < end ? __ldcg(p + at) : fill;
   }
 }
 
-// The logits of verify row r, head h against the verify block, as a sum's part (one warp).
-__device__ __forceinline__ Stat block_part(const WeightsParams& a, int b, int g, int h, int r, int P, bool flag) {
-  const int lane = threadIdx.x & 31;
-  const int n = a.d / 32;  // values of a lane: 2 or 4
-  const uint16_t* q = a.q + ((static_cast<size_t>(b) * a.R + r) * a.Hq + h) * a.d + lane * n;
-  float x[4];
-  for (int i = 0; i < n; ++i) x[i] = __uint_as_float(static_cast<uint32_t>(__ldcg(q + i)) << 16);
-  Stat s{-INFINITY, 0.f};
-  for (int u = 0; u <= r; ++u) {
+// The verify block's part: a CTA has column `rank` of each CS.  Their queries and the block's keys
+// are copied to shared memory (as bf16, which e4m3 codes are values of) while the logits arrive;
+// then a thread forms one product.
+constexpr int kRowBytes = 272;  // 128 values and 16 bytes: rows next to each other in other banks
+
+struct Block {
+  uint4 q[kMaxWeightCols][kRowBytes / 16];
+  uint4 k[kMaxWeightSlots][kRowBytes / 16];
+  float factor[kMaxWeightSlots];           // scale, times the key's; NaN: no such key
+  float z[kMaxWeightCols][kMaxWeightSlots];  // logits; minus infinity: not seen
+};
+
+template <int kThreads>
+__device__ __forceinline__ void copy_block(const WeightsParams& a, int b, int g, int P, int rank, int CS, Block& s) {
+  const int pieces = a.d / 8;
+  for (int i = threadIdx.x; i < a.R * pieces; i += kThreads) {
+    const int u = i / pieces, c = i - u * pieces;
     const int pos = P + u;
     const int blk = __ldcg(a.block_table + static_cast<size_t>(b) * a.max_blocks + pos / kPageW);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    float f = a.scale;
     if (blk < 0 || blk >= a.num_blocks) {
-      if (flag && lane == 0) flag_status(a.status, VSD_DEV_BAD_BLOCK);
-      continue;
+      if (g == 0 && rank == 0 && c == 0) flag_status(a.status, VSD_DEV_BAD_BLOCK);
+      f = NAN;
+    } else {
+      const size_t ph = static_cast<size_t>(blk) * a.Hkv + g;
+      const size_t at = (ph * kPageW + pos % kPageW) * a.d + c * 8;
+      if (a.k_scale == nullptr) {
+        v = ldg_stream16(static_cast<const uint16_t*>(a.k_cache) + at);
+      } else {
+        const uint2 x = ldg_stream8(static_cast<const uint8_t*>(a.k_cache) + at);
+        const auto two = [](uint32_t codes) {
+          const float2 y = e4m3x2_to_float2(codes);
+          return pack_bf16x2(y.x, y.y);
+        };
+        v = make_uint4(two(x.x & 0xFFFFu), two(x.x >> 16), two(x.y & 0xFFFFu), two(x.y >> 16));
+        if (c == 0) f *= __ldcg(a.k_scale + ph);
+      }
     }
-    const size_t ph = static_cast<size_t>(blk) * a.Hkv + g;
-    const size_t at = (ph * kPageW + pos % kPageW) * a.d + lane * n;
-    float dot = 0.f;
-    for (int i = 0; i < n; ++i) {
-      float k;
-      if (a.k_scale != nullptr)
-        k = e4m3x2_to_float2(__ldcg(static_cast<const unsigned char*>(a.k_cache) + at + i)).x;
-      else
-        k = __uint_as_float(static_cast<uint32_t>(__ldcg(static_cast<const uint16_t*>(a.k_cache) + at + i)) << 16);
-      dot = fmaf(x[i], k, dot);
-    }
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
-    float z = dot * a.scale;
-    if (a.k_scale != nullptr) z = dot * (a.scale * __ldcg(a.k_scale + ph));
-    s = join(s, Stat{z, 1.f});
+    s.k[u][c] = v;
+    if (c == 0) s.factor[u] = f;
   }
-  return s;
+  const int mine = (a.cols - rank + CS - 1) / CS;  // columns of this CTA
+  for (int i = threadIdx.x; i < mine * pieces; i += kThreads) {
+    const int at = i / pieces, c = i - at * pieces, col = rank + at * CS;
+    const int slot = col / a.G;
+    s.q[at][c] = ldg_stream16(
+        a.q + ((static_cast<size_t>(b) * a.R + a.row[slot]) * a.Hq + g * a.G + (col - slot * a.G)) * a.d + c * 8);
+  }
 }
 
-// kHold: columns whose values stay in registers between the two passes (the slice is one step
-// and the columns are at most kHold); 0: they are read again.
-template <bool kVec, int kHold>
-__global__ void __launch_bounds__(kWThreads) accumulate_weights_kernel(const WeightsParams a) {
-  __shared__ Stat part[kWWarps + 1][kMaxWeightCols];  // of each warp; the last: of the verify block
-  __shared__ Stat mine[kMaxWeightCols];               // of the CTA
+template <int kThreads>
+__device__ __forceinline__ void block_logits(const WeightsParams& a, int rank, int CS, Block& s) {
+  const int mine = (a.cols - rank + CS - 1) / CS;
+  for (int i = threadIdx.x; i < mine * kMaxWeightSlots; i += kThreads) {
+    const int at = i / kMaxWeightSlots, u = i % kMaxWeightSlots;
+    float z = -INFINITY;
+    if (u <= a.row[(rank + at * CS) / a.G] && !isnan(s.factor[u])) {
+      float dot[2] = {0.f, 0.f};
+      for (int c = 0; c < a.d / 8; ++c) {
+        const uint4 x = s.q[at][c], y = s.k[u][c];
+        dot[0] = fmaf(bf16_lo(x.x), bf16_lo(y.x), dot[0]);
+        dot[1] = fmaf(bf16_hi(x.x), bf16_hi(y.x), dot[1]);
+        dot[0] = fmaf(bf16_lo(x.y), bf16_lo(y.y), dot[0]);
+        dot[1] = fmaf(bf16_hi(x.y), bf16_hi(y.y), dot[1]);
+        dot[0] = fmaf(bf16_lo(x.z), bf16_lo(y.z), dot[0]);
+        dot[1] = fmaf(bf16_hi(x.z), bf16_hi(y.z), dot[1]);
+        dot[0] = fmaf(bf16_lo(x.w), bf16_lo(y.w), dot[0]);
+        dot[1] = fmaf(bf16_hi(x.w), bf16_hi(y.w), dot[1]);
+      }
+      z = (dot[0] + dot[1]) * s.factor[u];
+    }
+    s.z[at][u] = z;
+  }
+}
+
+// kHold: columns whose exponentials stay in registers between the passes (the slice is one step then); 0: the slice
+// is read again.
+template <bool kVec, int kHold, int kThreads, int kBlocks>
+__global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(const WeightsParams a) {
+  constexpr int kWarps = kThreads / 32;
+  constexpr int kStep = kThreads * 4;
+  __shared__ const float* column[kMaxWeightCols];
+  __shared__ Stat part[kWarps][kMaxWeightCols];       // of each warp
+  __shared__ Stat slices[kWMaxCluster][kMaxWeightCols];  // of each CTA of the cluster
   __shared__ Stat whole[kMaxWeightCols];              // of the row: maximum and 1 / sum
+  __shared__ float factor[kHold > 0 ? kWarps : 1][kHold > 0 ? kHold : 1];
+  __shared__ Block block;
   cg::cluster_group cluster = cg::this_cluster();
   const int CS = static_cast<int>(cluster.num_blocks());
   const int rank = static_cast<int>(cluster.block_rank());
   const int pair = static_cast<int>(blockIdx.x) / CS;
   const int b = pair / a.Hkv, g = pair - b * a.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (static_cast<int>(threadIdx.x) < a.cols) {
+    const int s = static_cast<int>(threadIdx.x) / a.G;
+    column[threadIdx.x] = a.logits + ((static_cast<size_t>(b) * a.C + a.slot[s]) * a.Hq + g * a.G +
+                                      (static_cast<int>(threadIdx.x) - s * a.G)) * static_cast<size_t>(a.P_max);
+  }
+  __syncthreads();
   ptx::pdl_wait_primary();
   ptx::pdl_launch_dependents();
   const int P = __ldcg(a.prefix_len + b);
@@ -138,112 +208,154 @@ __global__ void __launch_bounds__(kWThreads) accumulate_weights_kernel(const Wei
     return;
   }
   if (P == 0) return;  // (the cluster together, as above)
+  cluster_arrive();
   // slices of whole 128-byte lines
   const int len = static_cast<int>(((static_cast<long long>(P) + CS - 1) / CS + 31) / 32 * 32);
   const long long first = static_cast<long long>(rank) * len;
   const int lo = static_cast<int>(first < P ? first : P);
   const int hi = P - lo < len ? P : lo + len;
-  const auto logits_of = [&](int col) {
-    const int s = col / a.G;
-    return a.logits + ((static_cast<size_t>(b) * a.C + a.slot[s]) * a.Hq + g * a.G + (col - s * a.G)) *
-                          static_cast<size_t>(a.P_max);
-  };
+  float* out = a.weights + (static_cast<size_t>(b) * a.Hkv + g) * static_cast<size_t>(a.weights_stride);
   constexpr int kKeep = kHold > 0 ? kHold : 1;
   float keep[kKeep][4];
+  float w[4] = {0.f, 0.f, 0.f, 0.f};
 
   // ---- pass 1: maximum and sum of every column over the slice
-  for (int c0 = 0; c0 < a.cols; c0 += kWGroup) {
-    const int nc = min(kWGroup, a.cols - c0);
-    float m[kWGroup], l[kWGroup];
+  if (kHold == 0) copy_block<kThreads>(a, b, g, P, rank, CS, block);
+  if (kHold > 0) {
 #pragma unroll
-    for (int c = 0; c < kWGroup; ++c) {
-      m[c] = -INFINITY;
-      l[c] = 0.f;
+    for (int c = 0; c < kHold; ++c) {
+      if (c < a.cols) {
+        load4<kVec, kThreads>(column[c], lo, hi, -INFINITY, keep[c]);
+      } else {
+        keep[c][0] = keep[c][1] = keep[c][2] = keep[c][3] = -INFINITY;
+      }
     }
-    for (int base = lo; base < hi; base += kWTile) {
-      float z[kWGroup][4];
+    load4<kVec, kThreads>(out, lo, hi, 0.f, w);
+    copy_block<kThreads>(a, b, g, P, rank, CS, block);
+#pragma unroll
+    for (int c0 = 0; c0 < kHold; c0 += kWGroup) {
+      float m[kWGroup], l[kWGroup];
 #pragma unroll
       for (int c = 0; c < kWGroup; ++c) {
-        if (c < nc) {
-          load4<kVec>(logits_of(c0 + c), base, hi, -INFINITY, z[c]);
-        } else {
-          z[c][0] = z[c][1] = z[c][2] = z[c][3] = -INFINITY;
+        float(&z)[4] = keep[c0 + c];
+        m[c] = warp_max_f32(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])));
+        const float ref = reference(m[c]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[j] = exp_of(z[j] - ref);
+        l[c] = (z[0] + z[1]) + (z[2] + z[3]);
+      }
+      const float sum = warp_sum_columns<kWGroup>(l);
+#pragma unroll
+      for (int c = 0; c < kWGroup; ++c)
+        if (lane == c) part[warp][c0 + c] = Stat{m[c], sum};
+    }
+  } else {
+    for (int c0 = 0; c0 < a.cols; c0 += kWGroup) {
+      const int nc = min(kWGroup, a.cols - c0);
+      float m[kWGroup], l[kWGroup];
+#pragma unroll
+      for (int c = 0; c < kWGroup; ++c) {
+        m[c] = -INFINITY;
+        l[c] = 0.f;
+      }
+      for (int base = lo; base < hi; base += kStep) {
+        float z[kWGroup][4];
+#pragma unroll
+        for (int c = 0; c < kWGroup; ++c) {
+          if (c < nc) {
+            load4<kVec, kThreads>(column[c0 + c], base, hi, -INFINITY, z[c]);
+          } else {
+            z[c][0] = z[c][1] = z[c][2] = z[c][3] = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < kWGroup; ++c) {
+          const float now = fmaxf(m[c], fmaxf(fmaxf(z[c][0], z[c][1]), fmaxf(z[c][2], z[c][3])));
+          const float ref = reference(now);
+          l[c] *= exp_of(m[c] - ref);
+          l[c] += (exp_of(z[c][0] - ref) + exp_of(z[c][1] - ref)) + (exp_of(z[c][2] - ref) + exp_of(z[c][3] - ref));
+          m[c] = now;
         }
       }
 #pragma unroll
       for (int c = 0; c < kWGroup; ++c) {
-        const float top = fmaxf(fmaxf(z[c][0], z[c][1]), fmaxf(z[c][2], z[c][3]));
-        const float now = fmaxf(m[c], top);
-        const float ref = now == -INFINITY ? 0.f : now;
-        l[c] *= exp_of(m[c] - ref);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) l[c] += exp_of(z[c][j] - ref);
-        m[c] = now;
-        if (kHold > 0) {
-#pragma unroll
-          for (int q = 0; q < kHold / kWGroup; ++q)
-            if (c0 == q * kWGroup) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) keep[q * kWGroup + c][j] = z[c][j];
-            }
-        }
+        const float wm = warp_max_f32(m[c]);
+        l[c] *= exp_of(m[c] - reference(wm));
+        m[c] = wm;
       }
-    }
+      const float sum = warp_sum_columns<kWGroup>(l);
 #pragma unroll
-    for (int c = 0; c < kWGroup; ++c) {
-      const float wm = warp_max_f32(m[c]);
-      l[c] *= exp_of(m[c] - (wm == -INFINITY ? 0.f : wm));
-      m[c] = wm;
+      for (int c = 0; c < kWGroup; ++c)
+        if (lane == c && c < nc) part[warp][c0 + c] = Stat{m[c], sum};
     }
-    const float sum = warp_sum_columns<kWGroup>(l);
-#pragma unroll
-    for (int c = 0; c < kWGroup; ++c)
-      if (lane == c && c < nc) part[warp][c0 + c] = Stat{m[c], sum};
-  }
-  // the verify block's keys: a column for each warp of the cluster
-  for (int col = warp * CS + rank; col < a.cols; col += kWWarps * CS) {
-    const int s = col / a.G;
-    const Stat t = block_part(a, b, g, g * a.G + (col - s * a.G), a.row[s], P, g == 0 && col % a.G == 0);
-    if (lane == 0) part[kWWarps][col] = t;
   }
   __syncthreads();
-  for (int col = threadIdx.x; col < a.cols; col += kWThreads) {
-    Stat s = part[0][col];
-    for (int w = 1; w < kWWarps; ++w) s = join(s, part[w][col]);
-    if (col % CS == rank) s = join(s, part[kWWarps][col]);
-    mine[col] = s;
+  block_logits<kThreads>(a, rank, CS, block);
+  cluster_wait();  // every CTA of the cluster runs
+  __syncthreads();
+  // the CTA's part of each column (16 lanes a column, each with a warp's and a key of the verify
+  // block), to every CTA of the cluster
+  const int l16 = lane & 15;
+  for (int c0 = 2 * warp; c0 < a.cols; c0 += 2 * kWarps) {  // (the warp together)
+    const int col = c0 + (lane >> 4);
+    Stat s{-INFINITY, 0.f};
+    if (col < a.cols) {
+      if (l16 < kWarps) s = part[l16][col];
+      if (col % CS == rank) {
+        const float z = block.z[col / CS][l16], m = fmaxf(s.m, z);
+        s = Stat{m, s.l * exp_of(s.m - reference(m)) + exp_of(z - reference(m))};
+      }
+    }
+    s = join_lanes<16>(s);
+    if (col < a.cols && l16 < CS) *cluster.map_shared_rank(&slices[rank][col], l16) = s;
   }
   cluster.sync();
-  for (int col = threadIdx.x; col < a.cols; col += kWThreads) {
+  for (int c0 = 2 * warp; c0 < a.cols; c0 += 2 * kWarps) {
+    const int col = c0 + (lane >> 4);
     Stat s{-INFINITY, 0.f};
-    for (int r = 0; r < CS; ++r) s = join(s, *cluster.map_shared_rank(&mine[col], r));
-    const bool none = s.m == -INFINITY;  // (l is 0 then, or NaN)
-    whole[col] = Stat{none ? 0.f : s.m, none ? s.l : 1.f / s.l};
+    if (col < a.cols && l16 < CS) s = slices[l16][col];
+    s = join_lanes<16>(s);
+    // (nothing in sight: l is 0, or NaN)
+    if (col < a.cols && l16 == 0) whole[col] = Stat{reference(s.m), s.m == -INFINITY ? s.l : 1.f / s.l};
   }
   __syncthreads();
 
   // ---- pass 2: the weight of every position
-  float* out = a.weights + (static_cast<size_t>(b) * a.Hkv + g) * static_cast<size_t>(a.weights_stride);
-  for (int base = lo; base < hi; base += kWTile) {
-    float w[4];
-    load4<kVec>(out, base, hi, 0.f, w);
-    float p[4] = {0.f, 0.f, 0.f, 0.f};
-    if (kHold > 0) {
-#pragma unroll
-      for (int c = 0; c < kKeep; ++c) {
-        if (c < a.cols) {
-          const Stat s = whole[c];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) p[j] = fmaf(exp_of(keep[c][j] - s.m), s.l, p[j]);
-        }
-      }
+  const auto add = [&](int base, const float (&p)[4]) {
+    if (kVec && place<kVec, kThreads>(base, 3) < hi) {
+      *reinterpret_cast<float4*>(out + place<kVec, kThreads>(base, 0)) =
+          make_float4(w[0] + p[0], w[1] + p[1], w[2] + p[2], w[3] + p[3]);
     } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (place<kVec, kThreads>(base, j) < hi) out[place<kVec, kThreads>(base, j)] = w[j] + p[j];
+    }
+  };
+  if (kHold > 0) {
+    // e^(z - M) / L = e^(z - m) (e^(m - M) / L), m the warp's maximum
+    if (lane < kHold) {
+      const Stat s = whole[lane < a.cols ? lane : 0];
+      factor[warp][lane] = lane < a.cols ? exp_of(part[warp][lane].m - s.m) * s.l : 0.f;
+    }
+    __syncwarp();
+    float p[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < kKeep; ++c) {
+      const float f = factor[warp][c];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[j] = fmaf(keep[c][j], f, p[j]);
+    }
+    add(lo, p);
+  } else {
+    for (int base = lo; base < hi; base += kStep) {
+      load4<kVec, kThreads>(out, base, hi, 0.f, w);
+      float p[4] = {0.f, 0.f, 0.f, 0.f};
       for (int c0 = 0; c0 < a.cols; c0 += kWGroup) {
         const int nc = min(kWGroup, a.cols - c0);
         float z[kWGroup][4];
 #pragma unroll
         for (int c = 0; c < kWGroup; ++c)
-          if (c < nc) load4<kVec>(logits_of(c0 + c), base, hi, -INFINITY, z[c]);
+          if (c < nc) load4<kVec, kThreads>(column[c0 + c], base, hi, -INFINITY, z[c]);
 #pragma unroll
         for (int c = 0; c < kWGroup; ++c) {
           if (c < nc) {
@@ -253,22 +365,14 @@ __global__ void __launch_bounds__(kWThreads) accumulate_weights_kernel(const Wei
           }
         }
       }
-    }
-    if (kVec && place<kVec>(base, 3) < hi) {
-      *reinterpret_cast<float4*>(out + place<kVec>(base, 0)) =
-          make_float4(w[0] + p[0], w[1] + p[1], w[2] + p[2], w[3] + p[3]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (place<kVec>(base, j) < hi) out[place<kVec>(base, j)] = w[j] + p[j];
+      add(base, p);
     }
   }
-  cluster.sync();  // (no CTA leaves while another reads its sums)
 }
 
-template <bool kVec, int kHold>
+template <bool kVec, int kHold, int kThreads, int kBlocks>
 cudaError_t launch(const WeightsParams& p, int CS, cudaStream_t stream) {
-  auto* kern = accumulate_weights_kernel<kVec, kHold>;
+  auto* kern = accumulate_weights_kernel<kVec, kHold, kThreads, kBlocks>;
   if (CS > 8) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
@@ -282,7 +386,7 @@ cudaError_t launch(const WeightsParams& p, int CS, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.Hkv * CS), 1, 1);
-  cfg.blockDim = dim3(kWThreads, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
@@ -290,11 +394,17 @@ cudaError_t launch(const WeightsParams& p, int CS, cudaStream_t stream) {
 }
 
 template <bool kVec>
-cudaError_t launch_hold(const WeightsParams& p, int CS, cudaStream_t stream) {
-  const bool one = (p.P_max + CS - 1) / CS <= kWTile;  // a slice is one step
-  if (one && p.cols <= 8) return launch<kVec, 8>(p, CS, stream);
-  if (one && p.cols <= 16) return launch<kVec, 16>(p, CS, stream);
-  return launch<kVec, 0>(p, CS, stream);
+cudaError_t launch_vec(const WeightsParams& p, int num_sms, cudaStream_t stream) {
+  const long long pairs = static_cast<long long>(p.B) * p.Hkv;
+  // held: slices of 2048 positions, one CTA for each SM
+  int CS = 1;
+  while (CS < kWMaxCluster && CS * 2048 < p.P_max) CS *= 2;
+  if (CS * 2048 >= p.P_max && p.cols <= 16 && pairs * CS <= num_sms)
+    return p.cols <= 8 ? launch<kVec, 8, 512, 1>(p, CS, stream) : launch<kVec, 16, 512, 1>(p, CS, stream);
+  // read again: slices of at least a step of 1024 positions, for up to three CTAs each SM
+  CS = 1;
+  while (CS < kWMaxCluster && CS * 1024 < p.P_max && pairs * CS < 3ll * num_sms) CS *= 2;
+  return launch<kVec, 0, 256, 3>(p, CS, stream);
 }
 
 }  // namespace
@@ -326,11 +436,9 @@ cudaError_t launch_accumulate_weights(const WeightsArgs& x, cudaStream_t stream)
     p.slot[i] = x.slot[i];
     p.row[i] = x.row[i];
   }
-  int CS = 1;
-  while (CS < kWMaxCluster && CS * kWTile < x.P_max) CS *= 2;
   const auto aligned = [](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; };
   const bool vec = x.P_max % 4 == 0 && x.weights_stride % 4 == 0 && aligned(x.logits) && aligned(x.weights);
-  return vec ? launch_hold<true>(p, CS, stream) : launch_hold<false>(p, CS, stream);
+  return vec ? launch_vec<true>(p, x.num_sms, stream) : launch_vec<false>(p, x.num_sms, stream);
 }
 
 }  // namespace vsd
