@@ -112,54 +112,77 @@ struct Block {
   float z[kMaxWeightCols][kMaxWeightSlots];  // logits; minus infinity: not seen
 };
 
-template <int kThreads>
-__device__ __forceinline__ void copy_block(const WeightsParams& a, int b, int g, int P, int rank, int CS, Block& s) {
+// Piece i of those operands: 8 values of a key (the block's first), or of a column's query.
+struct Piece {
+  uint4 v;
+  float f;
+};
+
+__device__ __forceinline__ int block_pieces(const WeightsParams& a, int rank, int CS) {
+  return (a.R + (a.cols - rank + CS - 1) / CS) * (a.d / 8);
+}
+
+__device__ __forceinline__ Piece fetch_piece(const WeightsParams& a, int b, int g, int P, int rank, int CS, int i) {
   const int pieces = a.d / 8;
-  for (int i = threadIdx.x; i < a.R * pieces; i += kThreads) {
-    const int u = i / pieces, c = i - u * pieces;
-    const int pos = P + u;
-    const int blk = __ldcg(a.block_table + static_cast<size_t>(b) * a.max_blocks + pos / kPageW);
-    uint4 v = make_uint4(0, 0, 0, 0);
-    float f = a.scale;
-    if (blk < 0 || blk >= a.num_blocks) {
-      if (g == 0 && rank == 0 && c == 0) flag_status(a.status, VSD_DEV_BAD_BLOCK);
-      f = NAN;
-    } else {
-      const size_t ph = static_cast<size_t>(blk) * a.Hkv + g;
-      const size_t at = (ph * kPageW + pos % kPageW) * a.d + c * 8;
-      if (a.k_scale == nullptr) {
-        v = ldg_stream16(static_cast<const uint16_t*>(a.k_cache) + at);
-      } else {
-        const uint2 x = ldg_stream8(static_cast<const uint8_t*>(a.k_cache) + at);
-        const auto two = [](uint32_t codes) {
-          const float2 y = e4m3x2_to_float2(codes);
-          return pack_bf16x2(y.x, y.y);
-        };
-        v = make_uint4(two(x.x & 0xFFFFu), two(x.x >> 16), two(x.y & 0xFFFFu), two(x.y >> 16));
-        if (c == 0) f *= __ldcg(a.k_scale + ph);
-      }
-    }
-    s.k[u][c] = v;
-    if (c == 0) s.factor[u] = f;
-  }
-  const int mine = (a.cols - rank + CS - 1) / CS;  // columns of this CTA
-  for (int i = threadIdx.x; i < mine * pieces; i += kThreads) {
-    const int at = i / pieces, c = i - at * pieces, col = rank + at * CS;
-    const int slot = col / a.G;
-    s.q[at][c] = ldg_stream16(
+  const int u = i / pieces, c = i - u * pieces;
+  Piece r{make_uint4(0, 0, 0, 0), a.scale};
+  if (u >= a.R) {
+    const int col = rank + (u - a.R) * CS, slot = col / a.G;
+    r.v = ldg_stream16(
         a.q + ((static_cast<size_t>(b) * a.R + a.row[slot]) * a.Hq + g * a.G + (col - slot * a.G)) * a.d + c * 8);
+    return r;
+  }
+  const int pos = P + u;
+  const int blk = __ldcg(a.block_table + static_cast<size_t>(b) * a.max_blocks + pos / kPageW);
+  if (blk < 0 || blk >= a.num_blocks) {
+    if (g == 0 && rank == 0 && c == 0) flag_status(a.status, VSD_DEV_BAD_BLOCK);
+    r.f = NAN;
+    return r;
+  }
+  const size_t ph = static_cast<size_t>(blk) * a.Hkv + g;
+  const size_t at = (ph * kPageW + pos % kPageW) * a.d + c * 8;
+  if (a.k_scale == nullptr) {
+    r.v = ldg_stream16(static_cast<const uint16_t*>(a.k_cache) + at);
+  } else {
+    const uint2 x = ldg_stream8(static_cast<const uint8_t*>(a.k_cache) + at);
+    r.v.x = x.x;
+    r.v.y = x.y;
+    if (c == 0) r.f *= __ldcg(a.k_scale + ph);
+  }
+  return r;
+}
+
+__device__ __forceinline__ void put_piece(const WeightsParams& a, int i, const Piece& r, Block& s) {
+  const int pieces = a.d / 8;
+  const int u = i / pieces, c = i - u * pieces;
+  if (u >= a.R) {
+    s.q[u - a.R][c] = r.v;
+    return;
+  }
+  if (c == 0) s.factor[u] = r.f;
+  if (a.k_scale == nullptr) {
+    s.k[u][c] = r.v;
+  } else {
+    const auto two = [](uint32_t codes) {
+      const float2 y = e4m3x2_to_float2(codes);
+      return pack_bf16x2(y.x, y.y);
+    };
+    s.k[u][c] = make_uint4(two(r.v.x & 0xFFFFu), two(r.v.x >> 16), two(r.v.y & 0xFFFFu), two(r.v.y >> 16));
   }
 }
 
+// Eight lanes form one product.
 template <int kThreads>
 __device__ __forceinline__ void block_logits(const WeightsParams& a, int rank, int CS, Block& s) {
-  const int mine = (a.cols - rank + CS - 1) / CS;
-  for (int i = threadIdx.x; i < mine * kMaxWeightSlots; i += kThreads) {
-    const int at = i / kMaxWeightSlots, u = i % kMaxWeightSlots;
-    float z = -INFINITY;
-    if (u <= a.row[(rank + at * CS) / a.G] && !isnan(s.factor[u])) {
-      float dot[2] = {0.f, 0.f};
-      for (int c = 0; c < a.d / 8; ++c) {
+  const int mine = (a.cols - rank + CS - 1) / CS;  // columns of this CTA
+  const int l8 = threadIdx.x & 7;
+  for (int i0 = static_cast<int>(threadIdx.x >> 5) * 4; i0 < mine * a.R; i0 += kThreads / 8) {  // (the warp together)
+    const int i = i0 + static_cast<int>((threadIdx.x >> 3) & 3u);
+    const int at = i / a.R, u = i - at * a.R;
+    const bool real = at < mine;
+    float dot[2] = {0.f, 0.f};
+    if (real) {
+      for (int c = l8; c < a.d / 8; c += 8) {
         const uint4 x = s.q[at][c], y = s.k[u][c];
         dot[0] = fmaf(bf16_lo(x.x), bf16_lo(y.x), dot[0]);
         dot[1] = fmaf(bf16_hi(x.x), bf16_hi(y.x), dot[1]);
@@ -170,10 +193,22 @@ __device__ __forceinline__ void block_logits(const WeightsParams& a, int rank, i
         dot[0] = fmaf(bf16_lo(x.w), bf16_lo(y.w), dot[0]);
         dot[1] = fmaf(bf16_hi(x.w), bf16_hi(y.w), dot[1]);
       }
-      z = (dot[0] + dot[1]) * s.factor[u];
     }
-    s.z[at][u] = z;
+    float z = dot[0] + dot[1];
+#pragma unroll
+    for (int m = 4; m >= 1; m >>= 1) z += __shfl_xor_sync(0xffffffffu, z, m);
+    if (real && l8 == 0) {
+      const bool seen = u <= a.row[(rank + at * CS) / a.G] && !isnan(s.factor[u]);
+      s.z[at][u] = seen ? z * s.factor[u] : -INFINITY;
+    }
   }
+}
+
+// A CTA's slice: whole 128-byte lines of the prefix.  (With values in registers, of the longest
+// prefix: their loads need not wait for the length.)
+template <int kHold>
+__device__ __forceinline__ int slice_of(const WeightsParams& a, int P, int CS) {
+  return (((kHold > 0 ? a.P_max : P) + CS - 1) / CS + 31) / 32 * 32;
 }
 
 // kHold: columns whose exponentials stay in registers between the passes (the slice is one step then); 0: the slice
@@ -202,6 +237,19 @@ __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(c
   __syncthreads();
   ptx::pdl_wait_primary();
   ptx::pdl_launch_dependents();
+  constexpr int kKeep = kHold > 0 ? kHold : 1;
+  float keep[kKeep][4];
+  if (kHold > 0) {  // on their way before the length is known (what lies behind it is not used)
+    const int len = slice_of<kHold>(a, 0, CS), end = min((rank + 1) * len, a.P_max);
+#pragma unroll
+    for (int c = 0; c < kHold; ++c) {
+      if (c < a.cols) {
+        load4<kVec, kThreads>(column[c], rank * len, end, -INFINITY, keep[c]);
+      } else {
+        keep[c][0] = keep[c][1] = keep[c][2] = keep[c][3] = -INFINITY;
+      }
+    }
+  }
   const int P = __ldcg(a.prefix_len + b);
   if (P < 0 || P > a.P_max || static_cast<long long>(P) + a.R > static_cast<long long>(a.max_blocks) * kPageW) {
     if (g == 0 && rank == 0 && threadIdx.x == 0) flag_status(a.status, VSD_DEV_BAD_LENGTH);
@@ -209,29 +257,23 @@ __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(c
   }
   if (P == 0) return;  // (the cluster together, as above)
   cluster_arrive();
-  // slices of whole 128-byte lines
-  const int len = static_cast<int>(((static_cast<long long>(P) + CS - 1) / CS + 31) / 32 * 32);
-  const long long first = static_cast<long long>(rank) * len;
-  const int lo = static_cast<int>(first < P ? first : P);
-  const int hi = P - lo < len ? P : lo + len;
+  const int len = slice_of<kHold>(a, P, CS);
+  const int lo = min(rank * len, P), hi = min(lo + len, P);
   float* out = a.weights + (static_cast<size_t>(b) * a.Hkv + g) * static_cast<size_t>(a.weights_stride);
-  constexpr int kKeep = kHold > 0 ? kHold : 1;
-  float keep[kKeep][4];
   float w[4] = {0.f, 0.f, 0.f, 0.f};
 
   // ---- pass 1: maximum and sum of every column over the slice
-  if (kHold == 0) copy_block<kThreads>(a, b, g, P, rank, CS, block);
+  const int pieces = block_pieces(a, rank, CS);
+  Piece piece;
+  if (static_cast<int>(threadIdx.x) < pieces) piece = fetch_piece(a, b, g, P, rank, CS, threadIdx.x);
   if (kHold > 0) {
+    load4<kVec, kThreads>(out, lo, hi, 0.f, w);
 #pragma unroll
     for (int c = 0; c < kHold; ++c) {
-      if (c < a.cols) {
-        load4<kVec, kThreads>(column[c], lo, hi, -INFINITY, keep[c]);
-      } else {
-        keep[c][0] = keep[c][1] = keep[c][2] = keep[c][3] = -INFINITY;
-      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (place<kVec, kThreads>(lo, j) >= hi) keep[c][j] = -INFINITY;
     }
-    load4<kVec, kThreads>(out, lo, hi, 0.f, w);
-    copy_block<kThreads>(a, b, g, P, rank, CS, block);
 #pragma unroll
     for (int c0 = 0; c0 < kHold; c0 += kWGroup) {
       float m[kWGroup], l[kWGroup];
@@ -289,6 +331,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(c
         if (lane == c && c < nc) part[warp][c0 + c] = Stat{m[c], sum};
     }
   }
+  for (int i = threadIdx.x; i < pieces; i += kThreads) {
+    if (i >= kThreads) piece = fetch_piece(a, b, g, P, rank, CS, i);
+    put_piece(a, i, piece, block);
+  }
   __syncthreads();
   block_logits<kThreads>(a, rank, CS, block);
   cluster_wait();  // every CTA of the cluster runs
@@ -302,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(c
     if (col < a.cols) {
       if (l16 < kWarps) s = part[l16][col];
       if (col % CS == rank) {
-        const float z = block.z[col / CS][l16], m = fmaxf(s.m, z);
+        const float z = l16 < a.R ? block.z[col / CS][l16] : -INFINITY, m = fmaxf(s.m, z);
         s = Stat{m, s.l * exp_of(s.m - reference(m)) + exp_of(z - reference(m))};
       }
     }
@@ -397,13 +443,12 @@ template <bool kVec>
 cudaError_t launch_vec(const WeightsParams& p, int num_sms, cudaStream_t stream) {
   const long long pairs = static_cast<long long>(p.B) * p.Hkv;
   // held: slices of 2048 positions, one CTA for each SM
-  int CS = 1;
-  while (CS < kWMaxCluster && CS * 2048 < p.P_max) CS *= 2;
-  if (CS * 2048 >= p.P_max && p.cols <= 16 && pairs * CS <= num_sms)
-    return p.cols <= 8 ? launch<kVec, 8, 512, 1>(p, CS, stream) : launch<kVec, 16, 512, 1>(p, CS, stream);
-  // read again: slices of at least a step of 1024 positions, for up to three CTAs each SM
-  CS = 1;
-  while (CS < kWMaxCluster && CS * 1024 < p.P_max && pairs * CS < 3ll * num_sms) CS *= 2;
+  int CS = (p.P_max + 2047) / 2048;
+  if (CS <= kWMaxCluster && p.cols <= 16 && pairs * CS <= num_sms)
+    return p.cols <= 8 ? launch<kVec, 8, 512, 2>(p, CS, stream) : launch<kVec, 16, 512, 1>(p, CS, stream);
+  // read again: slices of at least a step of 1024 positions
+  CS = (p.P_max + 1023) / 1024;
+  if (CS > kWMaxCluster) CS = kWMaxCluster;
   return launch<kVec, 0, 256, 3>(p, CS, stream);
 }
 
