@@ -82,22 +82,42 @@ __device__ __forceinline__ int place(int base, int j) {
   return kVec ? base + 4 * static_cast<int>(threadIdx.x) + j : base + j * kThreads + static_cast<int>(threadIdx.x);
 }
 
-// A thread's four values of a step (those at `end` and beyond: `fill`).
+// A load that is left out where `there` is false (z keeps its values), without a branch: many of
+// them are to be in flight.
+__device__ __forceinline__ void load_if(const float* p, bool there, float (&z)[4]) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "@p ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "+f"(z[0]), "+f"(z[1]), "+f"(z[2]), "+f"(z[3])
+      : "l"(p), "r"(static_cast<uint32_t>(there))
+      : "memory");
+}
+
+__device__ __forceinline__ void load_if(const float* p, bool there, float& z) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p ld.global.cg.f32 %0, [%1];\n\t}"
+               : "+f"(z)
+               : "l"(p), "r"(static_cast<uint32_t>(there))
+               : "memory");
+}
+
+// A thread's four values of a step (those at `end` and beyond: minus infinity; a vector that
+// begins before it is read whole, row strides being multiples of four then, and masked).
 template <bool kVec, int kThreads>
-__device__ __forceinline__ void load4(const float* p, int base, int end, float fill, float (&z)[4]) {
-  if (kVec && place<kVec, kThreads>(base, 3) < end) {
-    const uint4 v = ldg_stream16(p + place<kVec, kThreads>(base, 0));
-    z[0] = __uint_as_float(v.x);
-    z[1] = __uint_as_float(v.y);
-    z[2] = __uint_as_float(v.z);
-    z[3] = __uint_as_float(v.w);
-    return;
-  }
+__device__ __forceinline__ void load4(const float* p, int base, int end, float (&z)[4]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int at = place<kVec, kThreads>(base, j);
-    z[j] = at < end ? __ldcg(p + at) : fill;
+  for (int j = 0; j < 4; ++j) z[j] = -INFINITY;
+  if (kVec) {
+    load_if(p + place<kVec, kThreads>(base, 0), place<kVec, kThreads>(base, 0) < end, z);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load_if(p + place<kVec, kThreads>(base, j), place<kVec, kThreads>(base, j) < end, z[j]);
   }
+}
+
+template <bool kVec, int kThreads>
+__device__ __forceinline__ void mask4(int base, int end, float (&z)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) z[j] = place<kVec, kThreads>(base, j) < end ? z[j] : -INFINITY;
 }
 
 // The verify block's part: a CTA has column `rank` of each CS.  Their queries and the block's keys
@@ -122,7 +142,14 @@ __device__ __forceinline__ int block_pieces(const WeightsParams& a, int rank, in
   return (a.R + (a.cols - rank + CS - 1) / CS) * (a.d / 8);
 }
 
-__device__ __forceinline__ Piece fetch_piece(const WeightsParams& a, int b, int g, int P, int rank, int CS, int i) {
+// The block-table entry of a key's piece (-1: none, or a query's).
+__device__ __forceinline__ int piece_page(const WeightsParams& a, int b, int P, int i) {
+  const int u = i / (a.d / 8);
+  return u < a.R ? __ldcg(a.block_table + static_cast<size_t>(b) * a.max_blocks + (P + u) / kPageW) : -1;
+}
+
+__device__ __forceinline__ Piece fetch_piece(const WeightsParams& a, int b, int g, int P, int rank, int CS, int i,
+                                             int blk) {
   const int pieces = a.d / 8;
   const int u = i / pieces, c = i - u * pieces;
   Piece r{make_uint4(0, 0, 0, 0), a.scale};
@@ -132,15 +159,13 @@ __device__ __forceinline__ Piece fetch_piece(const WeightsParams& a, int b, int 
         a.q + ((static_cast<size_t>(b) * a.R + a.row[slot]) * a.Hq + g * a.G + (col - slot * a.G)) * a.d + c * 8);
     return r;
   }
-  const int pos = P + u;
-  const int blk = __ldcg(a.block_table + static_cast<size_t>(b) * a.max_blocks + pos / kPageW);
   if (blk < 0 || blk >= a.num_blocks) {
     if (g == 0 && rank == 0 && c == 0) flag_status(a.status, VSD_DEV_BAD_BLOCK);
     r.f = NAN;
     return r;
   }
   const size_t ph = static_cast<size_t>(blk) * a.Hkv + g;
-  const size_t at = (ph * kPageW + pos % kPageW) * a.d + c * 8;
+  const size_t at = (ph * kPageW + (P + u) % kPageW) * a.d + c * 8;
   if (a.k_scale == nullptr) {
     r.v = ldg_stream16(static_cast<const uint16_t*>(a.k_cache) + at);
   } else {
@@ -204,6 +229,47 @@ __device__ __forceinline__ void block_logits(const WeightsParams& a, int rank, i
   }
 }
 
+// From each warp's part of every column, and the verify block's operands, to every column's
+// maximum and 1 / sum in every CTA of the cluster.
+template <int kThreads>
+__device__ __forceinline__ void share_sums(const WeightsParams& a, int rank, int CS,
+                                           const Stat (*part)[kMaxWeightCols], Block& block,
+                                           Stat (*slices)[kMaxWeightCols], Stat* whole, bool first) {
+  constexpr int kWarps = kThreads / 32;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __syncthreads();
+  block_logits<kThreads>(a, rank, CS, block);
+  if (first) cluster_wait();  // every CTA of the cluster runs
+  __syncthreads();
+  // the CTA's part of each column (16 lanes a column, each with a warp's and a key of the verify
+  // block), to every CTA of the cluster
+  const int l16 = lane & 15;
+  for (int c0 = 2 * warp; c0 < a.cols; c0 += 2 * kWarps) {  // (the warp together)
+    const int col = c0 + (lane >> 4);
+    Stat s{-INFINITY, 0.f};
+    if (col < a.cols) {
+      if (l16 < kWarps) s = part[l16][col];
+      if (col % CS == rank) {
+        const float z = l16 < a.R ? block.z[col / CS][l16] : -INFINITY, m = fmaxf(s.m, z);
+        s = Stat{m, s.l * exp_of(s.m - reference(m)) + exp_of(z - reference(m))};
+      }
+    }
+    s = join_lanes<16>(s);
+    if (col < a.cols && l16 < CS) *cluster.map_shared_rank(&slices[rank][col], l16) = s;
+  }
+  cluster.sync();
+  for (int c0 = 2 * warp; c0 < a.cols; c0 += 2 * kWarps) {
+    const int col = c0 + (lane >> 4);
+    Stat s{-INFINITY, 0.f};
+    if (col < a.cols && l16 < CS) s = slices[l16][col];
+    s = join_lanes<16>(s);
+    // (nothing in sight: l is 0, or NaN)
+    if (col < a.cols && l16 == 0) whole[col] = Stat{reference(s.m), s.m == -INFINITY ? s.l : 1.f / s.l};
+  }
+  __syncthreads();
+}
+
 // A CTA's slice: whole 128-byte lines of the prefix.  (With values in registers, of the longest
 // prefix: their loads need not wait for the length.)
 template <int kHold>
@@ -244,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(c
 #pragma unroll
     for (int c = 0; c < kHold; ++c) {
       if (c < a.cols) {
-        load4<kVec, kThreads>(column[c], rank * len, end, -INFINITY, keep[c]);
+        load4<kVec, kThreads>(column[c], rank * len, end, keep[c]);
       } else {
         keep[c][0] = keep[c][1] = keep[c][2] = keep[c][3] = -INFINITY;
       }
@@ -265,15 +331,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(c
   // ---- pass 1: maximum and sum of every column over the slice
   const int pieces = block_pieces(a, rank, CS);
   Piece piece;
-  if (static_cast<int>(threadIdx.x) < pieces) piece = fetch_piece(a, b, g, P, rank, CS, threadIdx.x);
+  if (static_cast<int>(threadIdx.x) < pieces)
+    piece = fetch_piece(a, b, g, P, rank, CS, threadIdx.x, piece_page(a, b, P, threadIdx.x));
   if (kHold > 0) {
-    load4<kVec, kThreads>(out, lo, hi, 0.f, w);
+    load4<kVec, kThreads>(out, lo, hi, w);
 #pragma unroll
-    for (int c = 0; c < kHold; ++c) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (place<kVec, kThreads>(lo, j) >= hi) keep[c][j] = -INFINITY;
-    }
+    for (int c = 0; c < kHold; ++c) mask4<kVec, kThreads>(lo, hi, keep[c]);
 #pragma unroll
     for (int c0 = 0; c0 < kHold; c0 += kWGroup) {
       float m[kWGroup], l[kWGroup];
@@ -305,10 +368,14 @@ __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(c
 #pragma unroll
         for (int c = 0; c < kWGroup; ++c) {
           if (c < nc) {
-            load4<kVec, kThreads>(column[c0 + c], base, hi, -INFINITY, z[c]);
+            load4<kVec, kThreads>(column[c0 + c], base, hi, z[c]);
           } else {
             z[c][0] = z[c][1] = z[c][2] = z[c][3] = -INFINITY;
           }
+        }
+        if (base + kStep > hi) {
+#pragma unroll
+          for (int c = 0; c < kWGroup; ++c) mask4<kVec, kThreads>(base, hi, z[c]);
         }
 #pragma unroll
         for (int c = 0; c < kWGroup; ++c) {
@@ -332,39 +399,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(c
     }
   }
   for (int i = threadIdx.x; i < pieces; i += kThreads) {
-    if (i >= kThreads) piece = fetch_piece(a, b, g, P, rank, CS, i);
+    if (i >= kThreads) piece = fetch_piece(a, b, g, P, rank, CS, i, piece_page(a, b, P, i));
     put_piece(a, i, piece, block);
   }
-  __syncthreads();
-  block_logits<kThreads>(a, rank, CS, block);
-  cluster_wait();  // every CTA of the cluster runs
-  __syncthreads();
-  // the CTA's part of each column (16 lanes a column, each with a warp's and a key of the verify
-  // block), to every CTA of the cluster
-  const int l16 = lane & 15;
-  for (int c0 = 2 * warp; c0 < a.cols; c0 += 2 * kWarps) {  // (the warp together)
-    const int col = c0 + (lane >> 4);
-    Stat s{-INFINITY, 0.f};
-    if (col < a.cols) {
-      if (l16 < kWarps) s = part[l16][col];
-      if (col % CS == rank) {
-        const float z = l16 < a.R ? block.z[col / CS][l16] : -INFINITY, m = fmaxf(s.m, z);
-        s = Stat{m, s.l * exp_of(s.m - reference(m)) + exp_of(z - reference(m))};
-      }
-    }
-    s = join_lanes<16>(s);
-    if (col < a.cols && l16 < CS) *cluster.map_shared_rank(&slices[rank][col], l16) = s;
-  }
-  cluster.sync();
-  for (int c0 = 2 * warp; c0 < a.cols; c0 += 2 * kWarps) {
-    const int col = c0 + (lane >> 4);
-    Stat s{-INFINITY, 0.f};
-    if (col < a.cols && l16 < CS) s = slices[l16][col];
-    s = join_lanes<16>(s);
-    // (nothing in sight: l is 0, or NaN)
-    if (col < a.cols && l16 == 0) whole[col] = Stat{reference(s.m), s.m == -INFINITY ? s.l : 1.f / s.l};
-  }
-  __syncthreads();
+  share_sums<kThreads>(a, rank, CS, part, block, slices, whole, true);
 
   // ---- pass 2: the weight of every position
   const auto add = [&](int base, const float (&p)[4]) {
@@ -394,14 +432,14 @@ __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(c
     add(lo, p);
   } else {
     for (int base = lo; base < hi; base += kStep) {
-      load4<kVec, kThreads>(out, base, hi, 0.f, w);
+      load4<kVec, kThreads>(out, base, hi, w);
       float p[4] = {0.f, 0.f, 0.f, 0.f};
       for (int c0 = 0; c0 < a.cols; c0 += kWGroup) {
         const int nc = min(kWGroup, a.cols - c0);
         float z[kWGroup][4];
 #pragma unroll
         for (int c = 0; c < kWGroup; ++c)
-          if (c < nc) load4<kVec, kThreads>(column[c0 + c], base, hi, -INFINITY, z[c]);
+          if (c < nc) load4<kVec, kThreads>(column[c0 + c], base, hi, z[c]);
 #pragma unroll
         for (int c = 0; c < kWGroup; ++c) {
           if (c < nc) {
@@ -446,9 +484,12 @@ cudaError_t launch_vec(const WeightsParams& p, int num_sms, cudaStream_t stream)
   int CS = (p.P_max + 2047) / 2048;
   if (CS <= kWMaxCluster && p.cols <= 16 && pairs * CS <= num_sms)
     return p.cols <= 8 ? launch<kVec, 8, 512, 2>(p, CS, stream) : launch<kVec, 16, 512, 1>(p, CS, stream);
-  // read again: slices of at least a step of 1024 positions
+  // read again: slices of at least a step of 1024 positions.  Where clusters of 8 fill the GPU
+  // (three CTAs an SM), wider ones wait for one another more than they win: 16 x 32K with 8
+  // heads of 8 queries 93 us with 8 CTAs, 111 with 16, 99 with 6.
   CS = (p.P_max + 1023) / 1024;
-  if (CS > kWMaxCluster) CS = kWMaxCluster;
+  const int widest = pairs * 8 >= 3ll * num_sms ? 8 : kWMaxCluster;
+  if (CS > widest) CS = widest;
   return launch<kVec, 0, 256, 3>(p, CS, stream);
 }
 
