@@ -52,10 +52,52 @@ struct RopeParams {
   int chunk, chunks;  // heads of a warp, and warps of a token
   unsigned tasks;     // B * n * chunks
   int pages;          // 8-bit cache: pages that n rows of one sequence can meet
-  unsigned units;     // ... and warps' parts, 2 * B * pages * Hkv
+  int head_groups;    // ... heads of a page in blocks of kRopeWarps
+  unsigned page_blocks;  // ... and blocks of pages, 2 * B * pages * head_groups
 };
 
-// Where a lane's eight values lie in a row, and the first of its four pairs.
+// ---------------------------------------------------------------- pairs of floats
+// (one instruction for two; the row arithmetic is what bounds these kernels beside the reading)
+using F2 = unsigned long long;
+
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+
+__device__ __forceinline__ float2 parts(F2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+__device__ __forceinline__ F2 widen2(uint32_t w) { return f2(bf16_lo(w), bf16_hi(w)); }
+
+__device__ __forceinline__ uint32_t narrow2(F2 x) {
+  const float2 v = parts(x);
+  return pack_bf16x2(v.x, v.y);
+}
+
+__device__ __forceinline__ F2 swapped(F2 x) {
+  const float2 v = parts(x);
+  return f2(v.y, v.x);
+}
+
+// ---------------------------------------------------------------- a lane's part of a row
+// Eight values at two places (four each), and the first of their four pairs.
 template <int D, bool kPairs>
 struct Lanes {
   int a, b, pair;
@@ -73,272 +115,361 @@ struct Lanes {
   }
 };
 
-struct Angles {
-  float c[4], s[4];
+struct Row {
+  F2 x[4];  // the first place's values, then the second's
 };
 
-__device__ __forceinline__ Angles angles_of(const RopeParams& a, long long p, int pair) {
-  Angles r;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint64_t phase = static_cast<uint64_t>(p) * static_cast<uint64_t>(__ldcg(a.turns + pair + j));
-    sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 0x1p-31f, &r.s[j], &r.c[j]);
-    r.s[j] *= a.amplitude;
-    r.c[j] *= a.amplitude;
-  }
-  return r;
+__device__ __forceinline__ Row widen_row(uint2 a, uint2 b) {
+  return Row{{widen2(a.x), widen2(a.y), widen2(b.x), widen2(b.y)}};
 }
 
-__device__ __forceinline__ void widen(uint2 x, float* f) {
-  f[0] = bf16_lo(x.x);
-  f[1] = bf16_hi(x.x);
-  f[2] = bf16_lo(x.y);
-  f[3] = bf16_hi(x.y);
-}
+// What turns a row: x' = x c + (its partner) s.
+struct Turn {
+  F2 c[4], s[4];
+};
 
-// f[0..3], f[4..7]: the lane's values at its two places.  (Lanes beyond rot_dim keep theirs: by
-// an angle of 0 an infinity would make its partner NaN.)
+// Of the cosines and sines of four pairs, in the row's order (s of the pair's first value is
+// negative), times a weight for each value.
 template <bool kPairs>
-__device__ __forceinline__ void turn(float (&f)[8], const Angles& r) {
+__device__ __forceinline__ Turn turn_of(const float (&c)[4], const float (&s)[4], const Row& w) {
+  Turn t;
+  if (kPairs) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int i0 = kPairs ? 2 * j : j, i1 = kPairs ? 2 * j + 1 : j + 4;
-    const float y0 = f[i0], y1 = f[i1];
-    f[i0] = y0 * r.c[j] - y1 * r.s[j];
-    f[i1] = y1 * r.c[j] + y0 * r.s[j];
-  }
-}
-
-// 1 / sqrt(mean of squares + eps) of the rows that the warp's lanes hold, LPR lanes each.
-template <int D>
-__device__ __forceinline__ float norm_factor(const float (&f)[8], float eps) {
-  float ss = 0.f;
+    for (int p = 0; p < 4; ++p) {
+      t.c[p] = mul2(f2(c[p], c[p]), w.x[p]);
+      t.s[p] = mul2(f2(-s[p], s[p]), swapped(w.x[p]));
+    }
+  } else {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
-#pragma unroll
-  for (int m = D / 16; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-  return rsqrtf(fmaf(ss, 1.f / D, eps));
-}
-
-__device__ __forceinline__ uint2 narrow(const float* f) {
-  return make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
-}
-
-__device__ __forceinline__ uint2 weight_of(const uint16_t* w, int at) {
-  return w != nullptr ? ldg_stream8(w + at) : make_uint2(0x3F803F80u, 0x3F803F80u);  // ones
-}
-
-// One warp's rows: a range of the heads of one token.  kCache: k and v go to the bf16 cache.
-template <int D, bool kPairs, bool kCache>
-__device__ __forceinline__ void token_rows(const RopeParams& a, unsigned task) {
-  constexpr int LPR = D / 8;    // lanes of a row
-  constexpr int RPI = 32 / LPR; // rows of a warp instruction
-  constexpr int U = 4;          // instructions in flight
-  const int lane = threadIdx.x & 31;
-  const int sub = lane / LPR;
-  const Lanes<D, kPairs> at(lane % LPR, a.rot_dim);
-  const unsigned bt = task / a.chunks;
-  const int h0 = static_cast<int>(task - bt * a.chunks) * a.chunk;
-  const int h1 = min(h0 + a.chunk, a.heads);
-  const int b = static_cast<int>(bt / a.n);
-  const int t = static_cast<int>(bt - static_cast<unsigned>(b) * a.n);
-  int count = a.n_valid != nullptr ? __ldcg(a.n_valid + b) : a.n;
-  if (count < 0 || count > a.n) {
-    if (lane == 0) flag_status(a.status, VSD_DEV_BAD_LENGTH);
-    count = 0;
-  }
-  const bool there = t < count;
-  if (!there && a.zeroed == 0u) return;
-  // the token's row of the cache
-  long long slot = -1;  // ((block * Hkv) * 16 + row), -1: not stored
-  if (kCache && there && h1 > a.Hq) {
-    const long long pos = static_cast<long long>(__ldcg(a.pos_base + b)) + a.pos_offset + t;
-    if (pos < 0 || pos >= static_cast<long long>(a.max_blocks) * kPageQ) {
-      if (lane == 0) flag_status(a.status, VSD_DEV_BAD_LENGTH);
-    } else {
-      const int blk = __ldcg(a.block_table + static_cast<size_t>(b) * a.max_blocks + pos / kPageQ);
-      if (blk < 0 || blk >= a.num_blocks) {
-        if (lane == 0) flag_status(a.status, VSD_DEV_BAD_BLOCK);
-      } else {
-        slot = static_cast<long long>(blk) * a.Hkv * kPageQ + pos % kPageQ;
-      }
+    for (int p = 0; p < 2; ++p) {
+      const F2 cc = f2(c[2 * p], c[2 * p + 1]);
+      t.c[p] = mul2(cc, w.x[p]);
+      t.c[p + 2] = mul2(cc, w.x[p + 2]);
+      t.s[p] = mul2(f2(-s[2 * p], -s[2 * p + 1]), w.x[p + 2]);
+      t.s[p + 2] = mul2(f2(s[2 * p], s[2 * p + 1]), w.x[p]);
     }
   }
-  const uint16_t* src_q = a.q.data + b * a.q.batch + t * a.q.row;
-  const uint16_t* src_k = a.k.data + b * a.k.batch + t * a.k.row;
-  const uint16_t* src_v = a.v.data + b * a.v.batch + t * a.v.row;
-  const auto load = [&](int h, uint2& x, uint2& y) {
-    x = y = make_uint2(0, 0);
-    if (!there || h >= h1) return;
-    const uint16_t* p = h < a.Hq ? src_q + h * a.q.head
-                        : !kCache || h < a.Hq + a.Hkv ? src_k + (h - a.Hq) * a.k.head
-                                                      : src_v + (h - a.Hq - a.Hkv) * a.v.head;
-    x = ldg_stream8(p + at.a);
-    y = ldg_stream8(p + at.b);
-  };
-  uint2 x[U], y[U];
+  return t;
+}
+
+// (A lane beyond rot_dim has s = 0, and no partner: an infinity times 0 would be NaN.)
+template <bool kPairs, bool kFull>
+__device__ __forceinline__ Row turn_row(const Row& r, const Turn& t, bool turned) {
+  Row y;
 #pragma unroll
-  for (int i = 0; i < U; ++i) load(h0 + i * RPI + sub, x[i], y[i]);
-  float wq[8], wk[8];
-  widen(weight_of(a.q_weight, at.a), wq);
-  widen(weight_of(a.q_weight, at.b), wq + 4);
-  widen(weight_of(a.k_weight, at.a), wk);
-  widen(weight_of(a.k_weight, at.b), wk + 4);
-  Angles r;
-  if (at.turned)
-    r = angles_of(a, static_cast<long long>(__ldcg(a.rope_base + b)) + a.pos_offset + t, at.pair);
+  for (int p = 0; p < 4; ++p) {
+    F2 other = kPairs ? swapped(r.x[p]) : r.x[p ^ 2];
+    if (!kFull && !turned) other = 0ull;
+    y.x[p] = fma2(other, t.s[p], mul2(r.x[p], t.c[p]));
+  }
+  return y;
+}
+
+// The rows that the warp's lanes hold, d / 8 lanes each, times 1 / sqrt(mean of squares + eps).
+template <int D>
+__device__ __forceinline__ void norm_row(Row& r, float eps) {
+  F2 sum = mul2(r.x[0], r.x[0]);
+#pragma unroll
+  for (int p = 1; p < 4; ++p) sum = fma2(r.x[p], r.x[p], sum);
+  const float2 v = parts(sum);
+  float ss = v.x + v.y;
+#pragma unroll
+  for (int m = D / 16; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+  const float f = rsqrtf(fmaf(ss, 1.f / D, eps));
+#pragma unroll
+  for (int p = 0; p < 4; ++p) r.x[p] = mul2(r.x[p], f2(f, f));
+}
+
+// A weight's values at a lane's places (ones without a weight).
+template <int D, bool kPairs>
+__device__ __forceinline__ Row weight_row(const uint16_t* w, const Lanes<D, kPairs>& at) {
+  const uint2 ones = make_uint2(0x3F803F80u, 0x3F803F80u);
+  return w != nullptr ? widen_row(ldg_stream8(w + at.a), ldg_stream8(w + at.b)) : widen_row(ones, ones);
+}
+
+__device__ __forceinline__ void cos_sin(uint64_t phase, float amplitude, float* c, float* s) {
+  sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 0x1p-31f, s, c);
+  *s *= amplitude;
+  *c *= amplitude;
+}
+
+// ---------------------------------------------------------------- tokens
+// Rows of one kind: heads [h0, h1) of a token, from src + head * from to dst + head * to.
+template <int D, bool kPairs, bool kFull>
+__device__ __forceinline__ void turn_heads(const RopeParams& a, const Lanes<D, kPairs>& at, const float (&c)[4],
+                                           const float (&s)[4], const uint16_t* weight, int h0, int h1,
+                                           const uint16_t* src, long long from, uint16_t* dst, int to) {
+  constexpr int RPI = 32 / (D / 8);  // rows of a warp instruction
+  constexpr int U = 4;               // instructions in flight
+  const int sub = (threadIdx.x & 31) / (D / 8);
+  const bool normed = weight != nullptr;
+  Turn t;
+  bool have = false;
   for (int h = h0; h < h1; h += U * RPI) {
-    if (h != h0) {
+    uint2 x[U], y[U];
 #pragma unroll
-      for (int i = 0; i < U; ++i) load(h + i * RPI + sub, x[i], y[i]);
+    for (int i = 0; i < U; ++i) {
+      const int hh = h + i * RPI + sub;
+      const uint16_t* p = src + (hh < h1 ? hh : h0) * from;
+      x[i] = ldg_stream8(p + at.a);
+      y[i] = ldg_stream8(p + at.b);
+    }
+    if (!have) {  // (while the first rows are on their way)
+      t = turn_of<kPairs>(c, s, weight_row(weight, at));
+      have = true;
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       if (h + i * RPI >= h1) break;  // (the warp together)
       const int hh = h + i * RPI + sub;
-      const bool is_q = hh < a.Hq, is_v = kCache && hh >= a.Hq + a.Hkv;
-      float f[8];
-      widen(x[i], f);
-      widen(y[i], f + 4);
-      if (a.q_weight != nullptr || a.k_weight != nullptr) {
-        const bool normed = is_q ? a.q_weight != nullptr : a.k_weight != nullptr;
-        const float s = norm_factor<D>(f, a.eps);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = normed ? f[j] * s * (is_q ? wq[j] : wk[j]) : f[j];
+      Row r = widen_row(x[i], y[i]);
+      if (normed) norm_row<D>(r, a.eps);
+      r = turn_row<kPairs, kFull>(r, t, at.turned);
+      if (hh < h1) {
+        uint16_t* p = dst + hh * to;
+        *reinterpret_cast<uint2*>(p + at.a) = make_uint2(narrow2(r.x[0]), narrow2(r.x[1]));
+        *reinterpret_cast<uint2*>(p + at.b) = make_uint2(narrow2(r.x[2]), narrow2(r.x[3]));
       }
-      if (at.turned) turn<kPairs>(f, r);
-      if (hh >= h1) continue;
-      uint16_t* to;
-      if (is_q) {
-        if (!there && (a.zeroed & VSD_ROPE_ZEROED_Q) == 0u) continue;
-        to = a.q_out + (static_cast<size_t>(bt) * a.Hq + hh) * D;
-      } else if (!kCache) {
-        if (!there && (a.zeroed & VSD_ROPE_ZEROED_K) == 0u) continue;
-        to = a.k_out + (static_cast<size_t>(bt) * a.Hkv + (hh - a.Hq)) * D;
-      } else {
-        if (slot < 0) continue;
-        const int g = is_v ? hh - a.Hq - a.Hkv : hh - a.Hq;
-        to = (is_v ? a.v_cache : a.k_cache) + (slot + static_cast<long long>(g) * kPageQ) * D;
-      }
-      // (v's bits as they are; rows that are not there are zeros)
-      *reinterpret_cast<uint2*>(to + at.a) = is_v || !there ? x[i] : narrow(f);
-      *reinterpret_cast<uint2*>(to + at.b) = is_v || !there ? y[i] : narrow(f + 4);
     }
   }
 }
 
-template <int D, bool kPairs, bool kCache>
+// Heads [h0, h1) copied as they are (src null: zeros).
+template <int D>
+__device__ __forceinline__ void copy_heads(int h0, int h1, const uint16_t* src, long long from, uint16_t* dst, int to) {
+  constexpr int RPI = 32 / (D / 8);
+  constexpr int U = 4;
+  const int sub = (threadIdx.x & 31) / (D / 8), at = (threadIdx.x & 31) % (D / 8) * 8;
+  for (int h = h0 + sub; h < h1; h += U * RPI) {
+    uint4 x[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (src != nullptr && h + i * RPI < h1) x[i] = ldg_stream16(src + (h + i * RPI) * from + at);
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (h + i * RPI < h1) *reinterpret_cast<uint4*>(dst + (h + i * RPI) * to + at) = x[i];
+  }
+}
+
+// One warp's rows: a range of the heads of one token.  kCache: k and v go to the bf16 cache.
+template <int D, bool kPairs, bool kFull, bool kCache>
+__device__ __forceinline__ void token_rows(const RopeParams& a, unsigned task) {
+  const int lane = threadIdx.x & 31;
+  const unsigned bt = task / a.chunks;
+  const int h0 = static_cast<int>(task - bt * a.chunks) * a.chunk;
+  const int h1 = min(h0 + a.chunk, a.heads);
+  const int b = static_cast<int>(bt / a.n);
+  const int t = static_cast<int>(bt - static_cast<unsigned>(b) * a.n);
+  const long long pos = static_cast<long long>(__ldcg(a.rope_base + b)) + a.pos_offset + t;
+  int count = a.n_valid != nullptr ? __ldcg(a.n_valid + b) : a.n;
+  if (count < 0 || count > a.n) {
+    if (lane == 0) flag_status(a.status, VSD_DEV_BAD_LENGTH);
+    count = 0;
+  }
+  // this warp's heads of q, of k and of v, each counted from 0
+  const int q0 = min(h0, a.Hq), q1 = min(h1, a.Hq);
+  const int k0 = max(h0 - a.Hq, 0), k1 = min(h1 - a.Hq, a.Hkv);
+  const int v0 = max(h0 - a.Hq - a.Hkv, 0), v1 = h1 - a.Hq - a.Hkv;
+  uint16_t* q_out = a.q_out + static_cast<size_t>(bt) * a.Hq * D;
+  uint16_t* k_out = a.k_out + static_cast<size_t>(bt) * a.Hkv * D;
+  if (t >= count) {
+    if ((a.zeroed & VSD_ROPE_ZEROED_Q) != 0u) copy_heads<D>(q0, q1, nullptr, 0, q_out, D);
+    if (!kCache && (a.zeroed & VSD_ROPE_ZEROED_K) != 0u) copy_heads<D>(k0, k1, nullptr, 0, k_out, D);
+    return;
+  }
+  const Lanes<D, kPairs> at(lane % (D / 8), a.rot_dim);
+  float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (at.turned) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      cos_sin(static_cast<uint64_t>(pos) * static_cast<uint64_t>(__ldcg(a.turns + at.pair + j)), a.amplitude, &c[j],
+              &s[j]);
+  }
+  if (q0 < q1)
+    turn_heads<D, kPairs, kFull>(a, at, c, s, a.q_weight, q0, q1, a.q.data + b * a.q.batch + t * a.q.row, a.q.head,
+                                 q_out, D);
+  if (k0 >= k1 && (!kCache || v0 >= v1)) return;
+  if (!kCache) {
+    turn_heads<D, kPairs, kFull>(a, at, c, s, a.k_weight, k0, k1, a.k.data + b * a.k.batch + t * a.k.row, a.k.head,
+                                 k_out, D);
+    return;
+  }
+  const long long place = static_cast<long long>(__ldcg(a.pos_base + b)) + a.pos_offset + t;
+  if (place < 0 || place >= static_cast<long long>(a.max_blocks) * kPageQ) {
+    if (lane == 0) flag_status(a.status, VSD_DEV_BAD_LENGTH);
+    return;
+  }
+  const int blk = __ldcg(a.block_table + static_cast<size_t>(b) * a.max_blocks + place / kPageQ);
+  if (blk < 0 || blk >= a.num_blocks) {
+    if (lane == 0) flag_status(a.status, VSD_DEV_BAD_BLOCK);
+    return;
+  }
+  const size_t slot = (static_cast<size_t>(blk) * a.Hkv * kPageQ + place % kPageQ) * D;
+  if (k0 < k1)
+    turn_heads<D, kPairs, kFull>(a, at, c, s, a.k_weight, k0, k1, a.k.data + b * a.k.batch + t * a.k.row, a.k.head,
+                                 a.k_cache + slot, kPageQ * D);
+  if (v0 < v1)
+    copy_heads<D>(v0, v1, a.v.data + b * a.v.batch + t * a.v.row, a.v.head, a.v_cache + slot, kPageQ * D);
+}
+
+template <int D, bool kPairs, bool kFull, bool kCache>
 __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const RopeParams a) {
   ptx::pdl_wait_primary();
   ptx::pdl_launch_dependents();
   const unsigned task = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
-  if (task < a.tasks) token_rows<D, kPairs, kCache>(a, task);
+  if (task < a.tasks) token_rows<D, kPairs, kFull, kCache>(a, task);
 }
 
+// ---------------------------------------------------------------- pages of the 8-bit cache
 // The smallest power of two s >= 2^-126 with amax <= 448 s, from amax's bits (448 = 1.75 * 2^8).
 __device__ __forceinline__ float page_scale_f32(uint32_t amax_bits) {
   const int e = static_cast<int>(amax_bits >> 23) - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   return __uint_as_float(static_cast<uint32_t>(e > 1 ? e : 1) << 23);
 }
 
-// One page and head of K or V: its rows of the call stay in registers, in fp32, between the
-// turn, the maximum and the conversion.
-template <int D, bool kPairs>
-__device__ __forceinline__ void page_rows(const RopeParams& a, unsigned u) {
+// Cosines and sines of a page's positions.
+template <int D>
+struct PageAngles {
+  float c[kPageQ][D / 2], s[kPageQ][D / 2];
+};
+
+// A page of K or V and up to kRopeWarps of its heads, one for each warp: a head's rows of the
+// call stay in registers, in fp32, between the turn, the maximum and the conversion.  The
+// angles, the same for every head, are the block's.
+template <int D, bool kPairs, bool kFull>
+__device__ __forceinline__ void page_rows(const RopeParams& a, unsigned block, PageAngles<D>& angles) {
   constexpr int LPR = D / 8;
   constexpr int RPI = 32 / LPR;
   constexpr int NI = kPageQ / RPI;
   const int lane = threadIdx.x & 31;
   const int sub = lane / LPR, lr = lane % LPR;
-  const PageUnit pu = page_unit(a, u, lane);
+  const unsigned page_of_kv = block / a.head_groups;
+  const int g = static_cast<int>(block - page_of_kv * a.head_groups) * kRopeWarps + static_cast<int>(threadIdx.x >> 5);
+  const unsigned pages = static_cast<unsigned>(a.B) * a.pages;
+  const bool is_v = page_of_kv >= pages;  // (K's first: they take longer)
+  const unsigned page_of = is_v ? page_of_kv - pages : page_of_kv;
+  const PageUnit pu = page_unit(a, (page_of * 2u + (is_v ? 1u : 0u)) * a.Hkv + min(g, a.Hkv - 1), lane);
   const int s0 = pu.s0, s1 = pu.s1;
-  if (s1 <= s0) return;
-  const bool is_v = pu.kv != 0;
-  const int g = static_cast<int>(u % a.Hkv);
+  if (s1 <= s0) return;  // (the block together)
+  const bool mine = g < a.Hkv;
   const Lanes<D, kPairs> at(lr, a.rot_dim);
   const Strided& src = is_v ? a.v : a.k;
   const int t0 = static_cast<int>(pu.lo - pu.rr.p0);  // slot 0 is row t0 of the call
-  const uint16_t* row = src.data + pu.b * src.batch + t0 * src.row + g * src.head;
+  const uint16_t* row = src.data + pu.b * src.batch + t0 * src.row + min(g, a.Hkv - 1) * src.head;
   uint2 x[NI], y[NI];
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int slot = i * RPI + sub;
     x[i] = y[i] = make_uint2(0, 0);
-    if (slot >= s0 && slot < s1) {
+    if (mine && slot >= s0 && slot < s1) {
       x[i] = ldg_stream8(row + slot * src.row + at.a);
       y[i] = ldg_stream8(row + slot * src.row + at.b);
     }
   }
   float* scale = is_v ? a.scale[1] : a.scale[0];
   const float was = s0 > 0 ? __ldcg(scale + pu.ph) : 0.f;
-  float f[NI][8];
-  uint32_t top = 0u;
-  bool finite = true;
-  float w[8];
-  long long p0 = 0;
+  Row w;
   const bool normed = !is_v && a.k_weight != nullptr;
   if (!is_v) {
-    widen(weight_of(a.k_weight, at.a), w);
-    widen(weight_of(a.k_weight, at.b), w + 4);
-    p0 = static_cast<long long>(__ldcg(a.rope_base + pu.b)) + a.pos_offset + t0;
-  }
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    widen(x[i], f[i]);
-    widen(y[i], f[i] + 4);
-    if (!is_v && i * RPI + RPI > s0 && i * RPI < s1) {  // (the warp together)
-      if (normed) {
-        const float s = norm_factor<D>(f[i], a.eps);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[i][j] = f[i][j] * s * w[j];
-      }
-      if (at.turned) turn<kPairs>(f[i], angles_of(a, p0 + i * RPI + sub, at.pair));
+    w = weight_row(a.k_weight, at);
+    constexpr int kPairsOf = D / 2;
+    const int pair = threadIdx.x % kPairsOf;
+    if (2 * pair < a.rot_dim) {
+      const uint64_t turns = static_cast<uint64_t>(__ldcg(a.turns + pair));
+      const long long p0 = static_cast<long long>(__ldcg(a.rope_base + pu.b)) + a.pos_offset + t0;
+      for (int slot = s0 + static_cast<int>(threadIdx.x) / kPairsOf; slot < s1; slot += kRopeThreads / kPairsOf)
+        cos_sin(static_cast<uint64_t>(p0 + slot) * turns, a.amplitude, &angles.c[slot][pair], &angles.s[slot][pair]);
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t bits = __float_as_uint(f[i][j]) & 0x7FFFFFFFu;
-      const bool ok = bits < 0x7F800000u;
-      finite = finite && ok;
-      top = max(top, ok ? bits : 0u);
-    }
+    __syncthreads();
   }
-  top = __reduce_max_sync(0xffffffffu, top);
-  float now = page_scale_f32(top);
-  if (s0 > 0 && was != 0.f && __uint_as_float(top) <= was * kE4M3Max) now = was;
-  uint8_t* page = (is_v ? a.codes[1] : a.codes[0]) + pu.ph * (kPageQ * D);
-  const bool power = (__float_as_uint(now) & 0x007FFFFFu) == 0u && now >= 0x1p-126f;
-  const float inv = power ? reciprocal_of_power(now) : 0.f;
-  const auto code = [&](float v) {  // (a division by a power of two: exact as a product)
-    const float c = power ? v * inv : __fdiv_rn(v, now);
-    return finite || isfinite(v) ? c : NAN;
+  if (!mine) return;
+  Row f[NI];
+  uint32_t top = 0u;  // the largest magnitude's bits (an infinity's or NaN's, where there is one)
+  const auto magnitude = [](F2 v) {
+    const float2 z = parts(v);
+    return max(__float_as_uint(z.x) & 0x7FFFFFFFu, __float_as_uint(z.y) & 0x7FFFFFFFu);
   };
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    const int slot = i * RPI + sub;
-    if (slot >= s0 && slot < s1) {
-      const auto four = [&](const float* v) {
-        return pack_e4m3x2(code(v[0]), code(v[1])) | pack_e4m3x2(code(v[2]), code(v[3])) << 16;
-      };
-      *reinterpret_cast<uint32_t*>(page + slot * D + at.a) = four(f[i]);
-      *reinterpret_cast<uint32_t*>(page + slot * D + at.b) = four(f[i] + 4);
+    f[i] = widen_row(x[i], y[i]);
+    if (!is_v && i * RPI + RPI > s0 && i * RPI < s1) {  // (the warp together)
+      if (normed) norm_row<D>(f[i], a.eps);
+      float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
+      const int slot = i * RPI + sub;
+      if (at.turned && slot >= s0 && slot < s1) {
+        const float4 cc = *reinterpret_cast<const float4*>(&angles.c[slot][at.pair]);
+        const float4 ss = *reinterpret_cast<const float4*>(&angles.s[slot][at.pair]);
+        c[0] = cc.x, c[1] = cc.y, c[2] = cc.z, c[3] = cc.w;
+        s[0] = ss.x, s[1] = ss.y, s[2] = ss.z, s[3] = ss.w;
+      }
+      f[i] = turn_row<kPairs, kFull>(f[i], turn_of<kPairs>(c, s, w), at.turned);
     }
+#pragma unroll
+    for (int p = 0; p < 4; ++p) top = max(top, magnitude(f[i].x[p]));
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (top >= 0x7F800000u) {
+    // rare: a NaN or an infinity somewhere.  They do not set the scale and become NaN.
+    top = 0u;
+    const auto clean = [&top](float v) {
+      const uint32_t bits = __float_as_uint(v) & 0x7FFFFFFFu;
+      const bool ok = bits < 0x7F800000u;
+      top = max(top, ok ? bits : 0u);
+      return ok ? v : NAN;
+    };
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const float2 v = parts(f[i].x[p]);
+        f[i].x[p] = f2(clean(v.x), clean(v.y));
+      }
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+  }
+  float now = page_scale_f32(top);
+  if (s0 > 0 && was != 0.f && __uint_as_float(top) <= was * kE4M3Max) now = was;
+  uint8_t* page = (is_v ? a.codes[1] : a.codes[0]) + pu.ph * (kPageQ * D);
+  // (a division by a power of two is exact as a product; any other scale is a caller's own)
+  const bool power = (__float_as_uint(now) & 0x007FFFFFu) == 0u && now >= 0x1p-126f;
+  const float inv = power ? reciprocal_of_power(now) : 0.f;
+  const auto store = [&](auto&& two) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int slot = i * RPI + sub;
+      if (slot >= s0 && slot < s1) {
+        *reinterpret_cast<uint32_t*>(page + slot * D + at.a) = two(f[i].x[0]) | two(f[i].x[1]) << 16;
+        *reinterpret_cast<uint32_t*>(page + slot * D + at.b) = two(f[i].x[2]) | two(f[i].x[3]) << 16;
+      }
+    }
+  };
+  if (power) {
+    store([inv](F2 v) {
+      const float2 z = parts(mul2(v, f2(inv, inv)));
+      return pack_e4m3x2(z.x, z.y);
+    });
+  } else {
+    store([now](F2 v) {
+      const float2 z = parts(v);
+      return pack_e4m3x2(__fdiv_rn(z.x, now), __fdiv_rn(z.y, now));
+    });
   }
   if (s0 > 0 && now != was) requantise_rows<D>(page + lr * 8, s0, sub, was, now);
   if (lane == 0 && (s0 == 0 || now != was)) scale[pu.ph] = now;
 }
 
-template <int D, bool kPairs>
+template <int D, bool kPairs, bool kFull>
 __global__ void __launch_bounds__(kRopeThreads) norm_rope_quant_kernel(const RopeParams a) {
+  __shared__ __align__(16) PageAngles<D> angles;
   ptx::pdl_wait_primary();
   ptx::pdl_launch_dependents();
-  const unsigned unit_blocks = (a.units + kRopeWarps - 1) / kRopeWarps;
-  const unsigned w = threadIdx.x >> 5;
-  if (blockIdx.x < unit_blocks) {
-    const unsigned u = blockIdx.x * kRopeWarps + w;
-    if (u < a.units) page_rows<D, kPairs>(a, u);
+  if (blockIdx.x < a.page_blocks) {
+    page_rows<D, kPairs, kFull>(a, blockIdx.x, angles);
   } else {
-    const unsigned task = (blockIdx.x - unit_blocks) * kRopeWarps + w;
-    if (task < a.tasks) token_rows<D, kPairs, false>(a, task);
+    const unsigned task = (blockIdx.x - a.page_blocks) * kRopeWarps + (threadIdx.x >> 5);
+    if (task < a.tasks) token_rows<D, kPairs, kFull, false>(a, task);
   }
 }
 
@@ -405,10 +536,19 @@ cudaError_t launch(Kernel kern, const RopeParams& p, unsigned blocks, cudaStream
 
 unsigned blocks_for(unsigned warps) { return warps / kRopeWarps + (warps % kRopeWarps != 0u); }
 
-template <int D, bool kPairs>
+template <int D, bool kPairs, bool kFull>
 cudaError_t launch_rows(const RopeParams& p, cudaStream_t stream) {
-  return p.block_table != nullptr ? launch(norm_rope_kernel<D, kPairs, true>, p, blocks_for(p.tasks), stream)
-                                  : launch(norm_rope_kernel<D, kPairs, false>, p, blocks_for(p.tasks), stream);
+  const unsigned blocks = p.page_blocks + blocks_for(p.tasks);
+  if (p.page_blocks > 0) return launch(norm_rope_quant_kernel<D, kPairs, kFull>, p, blocks, stream);
+  return p.block_table != nullptr ? launch(norm_rope_kernel<D, kPairs, kFull, true>, p, blocks, stream)
+                                  : launch(norm_rope_kernel<D, kPairs, kFull, false>, p, blocks, stream);
+}
+
+template <int D>
+cudaError_t launch_dim(const RopeParams& p, bool pairs, cudaStream_t stream) {
+  const bool full = p.rot_dim == D;
+  if (pairs) return full ? launch_rows<D, true, true>(p, stream) : launch_rows<D, true, false>(p, stream);
+  return full ? launch_rows<D, false, true>(p, stream) : launch_rows<D, false, false>(p, stream);
 }
 
 }  // namespace
@@ -416,21 +556,15 @@ cudaError_t launch_rows(const RopeParams& p, cudaStream_t stream) {
 cudaError_t launch_norm_rope(const RopeArgs& x, cudaStream_t stream) {
   const int with_k = x.k.data != nullptr ? x.Hkv : 0;
   const RopeParams p = rope_params(x, x.Hq + (x.block_table != nullptr ? 2 * x.Hkv : with_k));
-  if (x.d == 128)
-    return x.interleaved ? launch_rows<128, true>(p, stream) : launch_rows<128, false>(p, stream);
-  return x.interleaved ? launch_rows<64, true>(p, stream) : launch_rows<64, false>(p, stream);
+  return x.d == 128 ? launch_dim<128>(p, x.interleaved, stream) : launch_dim<64>(p, x.interleaved, stream);
 }
 
 cudaError_t launch_norm_rope_quant(const RopeArgs& x, cudaStream_t stream) {
   RopeParams p = rope_params(x, x.Hq);
   p.pages = quant_pages(x.n);
-  p.units = 2u * p.B * p.pages * p.Hkv;
-  const unsigned blocks = blocks_for(p.units) + blocks_for(p.tasks);
-  if (x.d == 128)
-    return x.interleaved ? launch(norm_rope_quant_kernel<128, true>, p, blocks, stream)
-                         : launch(norm_rope_quant_kernel<128, false>, p, blocks, stream);
-  return x.interleaved ? launch(norm_rope_quant_kernel<64, true>, p, blocks, stream)
-                       : launch(norm_rope_quant_kernel<64, false>, p, blocks, stream);
+  p.head_groups = (x.Hkv + kRopeWarps - 1) / kRopeWarps;
+  p.page_blocks = 2u * p.B * p.pages * p.head_groups;
+  return x.d == 128 ? launch_dim<128>(p, x.interleaved, stream) : launch_dim<64>(p, x.interleaved, stream);
 }
 
 }  // namespace vsd
