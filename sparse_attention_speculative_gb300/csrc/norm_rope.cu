@@ -329,17 +329,19 @@ __device__ __forceinline__ float page_scale_f32(uint32_t amax_bits) {
   return __uint_as_float(static_cast<uint32_t>(e > 1 ? e : 1) << 23);
 }
 
-// Cosines and sines of a page's positions.
+// A block's shared memory: cosines and sines of a page's positions, and each lane's values of
+// its rows, in fp32 (in registers they would leave an SM half of its warps).
 template <int D>
-struct PageAngles {
+struct PageRows {
   float c[kPageQ][D / 2], s[kPageQ][D / 2];
+  ulonglong2 value[D / 16][2][kRopeThreads];  // of D / 16 rows a lane holds 8 values
 };
 
 // A page of K or V and up to kRopeWarps of its heads, one for each warp: a head's rows of the
-// call stay in registers, in fp32, between the turn, the maximum and the conversion.  The
-// angles, the same for every head, are the block's.
+// call stay here, in fp32, between the turn, the maximum and the conversion.  The angles, the
+// same for every head, are the block's.
 template <int D, bool kPairs, bool kFull>
-__device__ __forceinline__ void page_rows(const RopeParams& a, unsigned block, PageAngles<D>& angles) {
+__device__ __forceinline__ void page_rows(const RopeParams& a, unsigned block, PageRows<D>& own) {
   constexpr int LPR = D / 8;
   constexpr int RPI = 32 / LPR;
   constexpr int NI = kPageQ / RPI;
@@ -380,12 +382,11 @@ __device__ __forceinline__ void page_rows(const RopeParams& a, unsigned block, P
       const uint64_t turns = static_cast<uint64_t>(__ldcg(a.turns + pair));
       const long long p0 = static_cast<long long>(__ldcg(a.rope_base + pu.b)) + a.pos_offset + t0;
       for (int slot = s0 + static_cast<int>(threadIdx.x) / kPairsOf; slot < s1; slot += kRopeThreads / kPairsOf)
-        cos_sin(static_cast<uint64_t>(p0 + slot) * turns, a.amplitude, &angles.c[slot][pair], &angles.s[slot][pair]);
+        cos_sin(static_cast<uint64_t>(p0 + slot) * turns, a.amplitude, &own.c[slot][pair], &own.s[slot][pair]);
     }
     __syncthreads();
   }
   if (!mine) return;
-  Row f[NI];
   uint32_t top = 0u;  // the largest magnitude's bits (an infinity's or NaN's, where there is one)
   const auto magnitude = [](F2 v) {
     const float2 z = parts(v);
@@ -393,39 +394,39 @@ __device__ __forceinline__ void page_rows(const RopeParams& a, unsigned block, P
   };
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    f[i] = widen_row(x[i], y[i]);
+    Row f = widen_row(x[i], y[i]);
     if (!is_v && i * RPI + RPI > s0 && i * RPI < s1) {  // (the warp together)
-      if (normed) norm_row<D>(f[i], a.eps);
+      if (normed) norm_row<D>(f, a.eps);
       float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
       const int slot = i * RPI + sub;
       if (at.turned && slot >= s0 && slot < s1) {
-        const float4 cc = *reinterpret_cast<const float4*>(&angles.c[slot][at.pair]);
-        const float4 ss = *reinterpret_cast<const float4*>(&angles.s[slot][at.pair]);
+        const float4 cc = *reinterpret_cast<const float4*>(&own.c[slot][at.pair]);
+        const float4 ss = *reinterpret_cast<const float4*>(&own.s[slot][at.pair]);
         c[0] = cc.x, c[1] = cc.y, c[2] = cc.z, c[3] = cc.w;
         s[0] = ss.x, s[1] = ss.y, s[2] = ss.z, s[3] = ss.w;
       }
-      f[i] = turn_row<kPairs, kFull>(f[i], turn_of<kPairs>(c, s, w), at.turned);
+      f = turn_row<kPairs, kFull>(f, turn_of<kPairs>(c, s, w), at.turned);
     }
 #pragma unroll
-    for (int p = 0; p < 4; ++p) top = max(top, magnitude(f[i].x[p]));
+    for (int p = 0; p < 4; ++p) top = max(top, magnitude(f.x[p]));
+    own.value[i][0][threadIdx.x] = make_ulonglong2(f.x[0], f.x[1]);
+    own.value[i][1][threadIdx.x] = make_ulonglong2(f.x[2], f.x[3]);
   }
   top = __reduce_max_sync(0xffffffffu, top);
   if (top >= 0x7F800000u) {
     // rare: a NaN or an infinity somewhere.  They do not set the scale and become NaN.
     top = 0u;
-    const auto clean = [&top](float v) {
-      const uint32_t bits = __float_as_uint(v) & 0x7FFFFFFFu;
-      const bool ok = bits < 0x7F800000u;
-      top = max(top, ok ? bits : 0u);
-      return ok ? v : NAN;
+    const auto clean = [&top](F2 x) {
+      const float2 v = parts(x);
+      const uint32_t l = __float_as_uint(v.x) & 0x7FFFFFFFu, h = __float_as_uint(v.y) & 0x7FFFFFFFu;
+      const bool lo_ok = l < 0x7F800000u, hi_ok = h < 0x7F800000u;
+      top = max(top, max(lo_ok ? l : 0u, hi_ok ? h : 0u));
+      return f2(lo_ok ? v.x : NAN, hi_ok ? v.y : NAN);
     };
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const float2 v = parts(f[i].x[p]);
-        f[i].x[p] = f2(clean(v.x), clean(v.y));
-      }
+#pragma unroll 1
+    for (int i = 0; i < 2 * NI; ++i) {
+      ulonglong2& v = own.value[i >> 1][i & 1][threadIdx.x];
+      v = make_ulonglong2(clean(v.x), clean(v.y));
     }
     top = __reduce_max_sync(0xffffffffu, top);
   }
@@ -440,8 +441,9 @@ __device__ __forceinline__ void page_rows(const RopeParams& a, unsigned block, P
     for (int i = 0; i < NI; ++i) {
       const int slot = i * RPI + sub;
       if (slot >= s0 && slot < s1) {
-        *reinterpret_cast<uint32_t*>(page + slot * D + at.a) = two(f[i].x[0]) | two(f[i].x[1]) << 16;
-        *reinterpret_cast<uint32_t*>(page + slot * D + at.b) = two(f[i].x[2]) | two(f[i].x[3]) << 16;
+        const ulonglong2 u = own.value[i][0][threadIdx.x], v = own.value[i][1][threadIdx.x];
+        *reinterpret_cast<uint32_t*>(page + slot * D + at.a) = two(u.x) | two(u.y) << 16;
+        *reinterpret_cast<uint32_t*>(page + slot * D + at.b) = two(v.x) | two(v.y) << 16;
       }
     }
   };
@@ -461,12 +463,12 @@ __device__ __forceinline__ void page_rows(const RopeParams& a, unsigned block, P
 }
 
 template <int D, bool kPairs, bool kFull>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_quant_kernel(const RopeParams a) {
-  __shared__ __align__(16) PageAngles<D> angles;
+__global__ void __launch_bounds__(kRopeThreads, 5) norm_rope_quant_kernel(const RopeParams a) {
+  __shared__ __align__(16) PageRows<D> own;
   ptx::pdl_wait_primary();
   ptx::pdl_launch_dependents();
   if (blockIdx.x < a.page_blocks) {
-    page_rows<D, kPairs, kFull>(a, blockIdx.x, angles);
+    page_rows<D, kPairs, kFull>(a, blockIdx.x, own);
   } else {
     const unsigned task = (blockIdx.x - a.page_blocks) * kRopeWarps + (threadIdx.x >> 5);
     if (task < a.tasks) token_rows<D, kPairs, kFull, false>(a, task);
@@ -509,11 +511,12 @@ RopeParams rope_params(const RopeArgs& x, int heads) {
   p.pos_offset = x.pos_offset;
   p.zeroed = x.zeroed;
   p.heads = heads;
-  // A warp takes as many of a token's heads as leaves about 48 warps for each SM.
+  // A warp takes as many of a token's heads as leaves about 24 warps, what fits, for each SM (4012
+  // tokens of 24 heads: 6.8 us with whole tokens, 8.6 with halves).
   const int rpi = x.d == 128 ? 2 : 4;
   const long long tokens = static_cast<long long>(x.B) * x.n;
   p.chunk = heads;
-  while (p.chunk > rpi && tokens * ((heads + p.chunk - 1) / p.chunk) < 48ll * x.num_sms)
+  while (p.chunk > rpi && tokens * ((heads + p.chunk - 1) / p.chunk) < 24ll * x.num_sms)
     p.chunk = (p.chunk / 2 + rpi - 1) / rpi * rpi;
   p.chunks = (heads + p.chunk - 1) / p.chunk;
   p.tasks = static_cast<unsigned>(tokens * p.chunks);
