@@ -7,8 +7,9 @@
 // in place, and needs no second copy of the cache.
 //
 // How: one cluster for each (sequence, KV head) of K and of V.  In a step each warp of the
-// cluster reads the 16 rows of one destination page into registers; the cluster meets; then
-// every warp writes its page.  8-bit pages take the largest scale of the rows that come in.
+// cluster reads the 16 rows of one destination page into registers, and looks up where its next
+// page's rows lie meanwhile; in place the cluster meets; then every warp writes its page.  8-bit
+// pages take the largest scale of the rows that come in.
 #include <cooperative_groups.h>
 
 #include "launch.h"
@@ -72,44 +73,70 @@ __global__ void __launch_bounds__(kCThreads) compact_kernel(const CompactParams 
   float* w_out = a.weights_out + static_cast<size_t>(pair) * static_cast<size_t>(a.w_out_stride);
   const int pages = (n + kPageC - 1) / kPageC;
   const int step = CS * kCWarps;
-  for (int p0 = 0; p0 < pages; p0 += step) {
-    const int page = p0 + rank * kCWarps + warp;
-    // lanes 0 .. 15: where the page's rows come from
+  // where a page's rows come from (lanes 0 .. 15: a row each) and go to
+  struct Page {
     long long from = -1;  // (block * Hkv + g) * 16 + row
+    int to = -1;          // block
     float w = 0.f, s = 0.f;
-    const int i = page * kPageC + (lane & 15);
-    if (page < pages && i < n && lane < 16) {
+  };
+  const int32_t* sources = a.block_table + static_cast<size_t>(b) * a.max_blocks;
+  const int32_t* places = a.dst_table + static_cast<size_t>(b) * a.dst_blocks;
+  const auto find = [&](int page) {
+    Page r;
+    if (page >= pages) return r;
+    r.to = __ldcg(places + page);
+    const int i = page * kPageC + lane;
+    if (lane < kPageC && i < n) {
       const int j = __ldcg(idx + i);
       if (j < i || j >= P) {
         flag_status(a.status, VSD_DEV_BAD_INDEX);
       } else {
-        const int blk = __ldcg(a.block_table + static_cast<size_t>(b) * a.max_blocks + j / kPageC);
+        const int blk = __ldcg(sources + j / kPageC);
         if (blk < 0 || blk >= a.num_blocks) {
           flag_status(a.status, VSD_DEV_BAD_BLOCK);
         } else {
           const long long ph = static_cast<long long>(blk) * a.Hkv + g;
-          from = ph * kPageC + j % kPageC;
-          if (weighted) w = __ldcg(w_in + j);
-          if (kQuant) s = __ldcg(scale + ph);
+          r.from = ph * kPageC + j % kPageC;
+          if (weighted) r.w = __ldcg(w_in + j);
+          if (kQuant) r.s = __ldcg(scale + ph);
         }
       }
     }
-    const unsigned rows = __ballot_sync(0xffffffffu, from >= 0);
+    if (r.to < 0 || r.to >= a.num_blocks) {
+      if (lane == 0) flag_status(a.status, VSD_DEV_BAD_BLOCK);
+      r.to = -1;
+    }
+    return r;
+  };
+  // Does any page go back to its own place?  (Otherwise no row that is read is ever written, and
+  // the warps need not wait for one another.)  The weights may do so by themselves.
+  bool meet = a.block_table == a.dst_table || (weighted && a.weights == a.weights_out);
+  if (!meet) {
+    bool same = false;
+    for (int p = threadIdx.x; p < min(pages, a.max_blocks); p += kCThreads)
+      same = same || __ldcg(sources + p) == __ldcg(places + p);
+    meet = __syncthreads_or(same);
+  }
+  int page = rank * kCWarps + warp;
+  Page at = find(page);
+  for (int p0 = 0; p0 < pages; p0 += step, page += step) {
+    const unsigned rows = __ballot_sync(0xffffffffu, at.from >= 0);
     uint4 x[NI];
     unsigned there = 0u;
 #pragma unroll
     for (int r = 0; r < NI; ++r) {
-      const long long at = __shfl_sync(0xffffffffu, from, r * RPI + sub);
+      const long long from = __shfl_sync(0xffffffffu, at.from, r * RPI + sub);
       x[r] = make_uint4(0, 0, 0, 0);
-      if (at >= 0) {
+      if (from >= 0) {
         there |= 1u << r;
-        x[r] = ldg_stream16(cache + at * kBytes + lr * 16);
+        x[r] = ldg_stream16(cache + from * kBytes + lr * 16);
       }
     }
+    const Page next = find(page + step);  // (while the rows are on their way)
     float top = 0.f;
     if (kQuant) {
-      top = warp_max_f32(s);
-      const float ratio = s == top ? 1.f : __fdiv_rn(s, top);
+      top = warp_max_f32(at.s);
+      const float ratio = at.s == top ? 1.f : __fdiv_rn(at.s, top);
 #pragma unroll
       for (int r = 0; r < NI; ++r) {
         const float f = __shfl_sync(0xffffffffu, ratio, r * RPI + sub);
@@ -123,15 +150,15 @@ __global__ void __launch_bounds__(kCThreads) compact_kernel(const CompactParams 
         }
       }
     }
-    // every row of the step is in registers before any is written
-    if (CS > 1) cluster.sync(); else __syncthreads();
+    // in place: every row of the step is in registers before any is written
+    if (meet) {
+      if (CS > 1) cluster.sync(); else __syncthreads();
+    }
     if (page < pages) {
-      if (weighted && lane < 16 && i < n) w_out[i] = w;
-      const int blk = __ldcg(a.dst_table + static_cast<size_t>(b) * a.dst_blocks + page);
-      if (blk < 0 || blk >= a.num_blocks) {
-        if (lane == 0) flag_status(a.status, VSD_DEV_BAD_BLOCK);
-      } else {
-        const size_t ph = static_cast<size_t>(blk) * a.Hkv + g;
+      const int i = page * kPageC + lane;
+      if (weighted && lane < kPageC && i < n) w_out[i] = at.w;
+      if (at.to >= 0) {
+        const size_t ph = static_cast<size_t>(at.to) * a.Hkv + g;
         uint8_t* to = cache + ph * (kPageC * kBytes) + lr * 16;
 #pragma unroll
         for (int r = 0; r < NI; ++r)
@@ -139,8 +166,9 @@ __global__ void __launch_bounds__(kCThreads) compact_kernel(const CompactParams 
         if (kQuant && lane == 0 && rows != 0u) scale[ph] = top;
       }
     }
+    at = next;
   }
-  if (weighted) {  // (the last step's meeting is behind: nothing of the old sums is read any more)
+  if (weighted) {  // (in place the last step's meeting is behind: none of the old sums is read any more)
     for (int i = n + rank * kCThreads + static_cast<int>(threadIdx.x); i < a.w_out_stride; i += CS * kCThreads)
       w_out[i] = 0.f;
   }

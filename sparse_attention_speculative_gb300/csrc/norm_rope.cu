@@ -5,14 +5,15 @@
 // pairs of y turned by the angles p f_i.  An angle in turns is p (f_i / 2 pi); its whole part
 // means nothing, so f_i / 2 pi is kept as a 64-bit fraction and the product is taken modulo
 // 2^64: exact where p f_i in fp32 is off by 2^-24 of the angle (at position 131072 that is
-// 0.008 of a radian for the fastest pair).  The upper 32 bits, signed, are the angle in half
-// turns: sincospif's argument.
+// 0.008 of a radian for the fastest pair).  The product's upper 32 bits give the quadrant and
+// the angle in it as they are, without any reduction of an argument.
 //
 // How: a row lies in d / 8 lanes, each with the two halves of four pairs (8 bytes each, or 16
 // next to each other where pairs are interleaved), so that the rotation needs no exchange
 // between lanes, and only the sum of squares does.  A warp takes one token and a range of its
 // heads: the four angles of a lane serve all of them.  Every row is read once, straight from the
 // layer's projections, and written once, to where the attention reads it.
+#include <cstdlib>
 #include "launch.h"
 #include "ptx.cuh"
 #include "quant_rows.cuh"
@@ -26,6 +27,18 @@ constexpr int kRopeWarps = kRopeThreads / 32;
 struct Strided {
   const uint16_t* data;
   long long batch, row, head;
+};
+
+// Division of an unsigned number below 2^31 by a number that the host knows: q = (x + the upper
+// half of x m) >> s, with s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1.
+struct Divisor {
+  uint32_t d = 1, m = 1, s = 0;
+  Divisor() = default;
+  explicit Divisor(uint32_t by) : d(by) {
+    while ((1ull << s) < by) ++s;
+    m = static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - by)) / by + 1);
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t x) const { return (__umulhi(x, m) + x) >> s; }
 };
 
 struct RopeParams {
@@ -49,7 +62,9 @@ struct RopeParams {
   int B, n, Hq, Hkv, max_blocks, num_blocks, pos_offset;
   unsigned zeroed;
   int heads;          // of a token in token_rows: q's alone, with k's, or with k's and v's
-  int chunk, chunks;  // heads of a warp, and warps of a token
+  int chunk;          // heads of a warp
+  Divisor chunks;     // warps of a token
+  Divisor by_n;
   unsigned tasks;     // B * n * chunks
   int pages;          // 8-bit cache: pages that n rows of one sequence can meet
   int head_groups;    // ... heads of a page in blocks of kRopeWarps
@@ -129,27 +144,35 @@ struct Turn {
 };
 
 // Of the cosines and sines of four pairs, in the row's order (s of the pair's first value is
-// negative), times a weight for each value.
+// negative).
 template <bool kPairs>
-__device__ __forceinline__ Turn turn_of(const float (&c)[4], const float (&s)[4], const Row& w) {
+__device__ __forceinline__ Turn turn_of(const float (&c)[4], const float (&s)[4]) {
   Turn t;
   if (kPairs) {
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-      t.c[p] = mul2(f2(c[p], c[p]), w.x[p]);
-      t.s[p] = mul2(f2(-s[p], s[p]), swapped(w.x[p]));
+      t.c[p] = f2(c[p], c[p]);
+      t.s[p] = f2(-s[p], s[p]);
     }
   } else {
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      const F2 cc = f2(c[2 * p], c[2 * p + 1]);
-      t.c[p] = mul2(cc, w.x[p]);
-      t.c[p + 2] = mul2(cc, w.x[p + 2]);
-      t.s[p] = mul2(f2(-s[2 * p], -s[2 * p + 1]), w.x[p + 2]);
-      t.s[p + 2] = mul2(f2(s[2 * p], s[2 * p + 1]), w.x[p]);
+      t.c[p] = t.c[p + 2] = f2(c[2 * p], c[2 * p + 1]);
+      t.s[p] = f2(-s[2 * p], -s[2 * p + 1]);
+      t.s[p + 2] = f2(s[2 * p], s[2 * p + 1]);
     }
   }
   return t;
+}
+
+// The same of weighted rows: a weight for each value, that of s its partner's.
+template <bool kPairs>
+__device__ __forceinline__ void weigh(Turn& t, const Row& w) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    t.c[p] = mul2(t.c[p], w.x[p]);
+    t.s[p] = mul2(t.s[p], kPairs ? swapped(w.x[p]) : w.x[p ^ 2]);
+  }
 }
 
 // (A lane beyond rot_dim has s = 0, and no partner: an infinity times 0 would be NaN.)
@@ -180,17 +203,42 @@ __device__ __forceinline__ void norm_row(Row& r, float eps) {
   for (int p = 0; p < 4; ++p) r.x[p] = mul2(r.x[p], f2(f, f));
 }
 
-// A weight's values at a lane's places (ones without a weight).
+// A weight's values at a lane's places.
 template <int D, bool kPairs>
 __device__ __forceinline__ Row weight_row(const uint16_t* w, const Lanes<D, kPairs>& at) {
-  const uint2 ones = make_uint2(0x3F803F80u, 0x3F803F80u);
-  return w != nullptr ? widen_row(ldg_stream8(w + at.a), ldg_stream8(w + at.b)) : widen_row(ones, ones);
+  return widen_row(ldg_stream8(w + at.a), ldg_stream8(w + at.b));
 }
 
-__device__ __forceinline__ void cos_sin(uint64_t phase, float amplitude, float* c, float* s) {
-  sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 0x1p-31f, s, c);
-  *s *= amplitude;
-  *c *= amplitude;
+// Cosines and sines of two angles, in units of 2^-32 of a turn.  The nearest quarter turn is
+// taken off, and what is left (x, at most pi / 4) goes through polynomials in x^2: minimax fits
+// of (sin x / x - 1) / x^2 and (cos x - 1) / x^2 found by Remez's exchange, off by 4e-9 and 1e-10
+// before they are rounded.  With fp32's roundings sine and cosine are within 1e-7.
+__device__ __forceinline__ void cos_sin2(uint32_t a, uint32_t b, float* c, float* s) {
+  const uint32_t qa = (a + 0x20000000u) >> 30, qb = (b + 0x20000000u) >> 30;
+  const F2 x = mul2(f2(static_cast<float>(static_cast<int>(a - (qa << 30))),
+                       static_cast<float>(static_cast<int>(b - (qb << 30)))),
+                    f2(0x1.921fb6p-30f, 0x1.921fb6p-30f));  // 2 pi / 2^32
+  const auto k = [](float v) { return f2(v, v); };
+  const F2 u = mul2(x, x);
+  F2 p = fma2(u, k(-1.95172994e-4f), k(8.332178e-3f));
+  p = fma2(p, u, k(-0.166666552f));
+  const float2 sn = parts(fma2(mul2(p, u), x, x));
+  F2 q = fma2(u, k(2.43904506e-5f), k(-1.38867635e-3f));
+  q = fma2(q, u, k(0.0416666232f));
+  q = fma2(q, u, k(-0.5f));
+  const float2 cs = parts(fma2(q, u, k(1.f)));
+  const auto put = [](uint32_t quadrant, float cosine, float sine, float* c, float* s) {
+    const bool odd = (quadrant & 1u) != 0u;
+    *c = __uint_as_float(__float_as_uint(odd ? sine : cosine) ^ ((quadrant + 1u) & 2u) << 30);
+    *s = __uint_as_float(__float_as_uint(odd ? cosine : sine) ^ (quadrant & 2u) << 30);
+  };
+  put(qa, cs.x, sn.x, c, s);
+  put(qb, cs.y, sn.y, c + 1, s + 1);
+}
+
+// The angle of position p in those units.
+__device__ __forceinline__ uint32_t angle_of(long long p, long long turns) {
+  return static_cast<uint32_t>((static_cast<uint64_t>(p) * static_cast<uint64_t>(turns)) >> 32);
 }
 
 // ---------------------------------------------------------------- tokens
@@ -215,7 +263,8 @@ __device__ __forceinline__ void turn_heads(const RopeParams& a, const Lanes<D, k
       y[i] = ldg_stream8(p + at.b);
     }
     if (!have) {  // (while the first rows are on their way)
-      t = turn_of<kPairs>(c, s, weight_row(weight, at));
+      t = turn_of<kPairs>(c, s);
+      if (normed) weigh<kPairs>(t, weight_row(weight, at));
       have = true;
     }
 #pragma unroll
@@ -257,10 +306,10 @@ __device__ __forceinline__ void copy_heads(int h0, int h1, const uint16_t* src, 
 template <int D, bool kPairs, bool kFull, bool kCache>
 __device__ __forceinline__ void token_rows(const RopeParams& a, unsigned task) {
   const int lane = threadIdx.x & 31;
-  const unsigned bt = task / a.chunks;
-  const int h0 = static_cast<int>(task - bt * a.chunks) * a.chunk;
+  const unsigned bt = a.chunks(task);
+  const int h0 = static_cast<int>(task - bt * a.chunks.d) * a.chunk;
   const int h1 = min(h0 + a.chunk, a.heads);
-  const int b = static_cast<int>(bt / a.n);
+  const int b = static_cast<int>(a.by_n(bt));
   const int t = static_cast<int>(bt - static_cast<unsigned>(b) * a.n);
   const long long pos = static_cast<long long>(__ldcg(a.rope_base + b)) + a.pos_offset + t;
   int count = a.n_valid != nullptr ? __ldcg(a.n_valid + b) : a.n;
@@ -282,10 +331,18 @@ __device__ __forceinline__ void token_rows(const RopeParams& a, unsigned task) {
   const Lanes<D, kPairs> at(lane % (D / 8), a.rot_dim);
   float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
   if (at.turned) {
+    uint32_t angle[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      cos_sin(static_cast<uint64_t>(pos) * static_cast<uint64_t>(__ldcg(a.turns + at.pair + j)), a.amplitude, &c[j],
-              &s[j]);
+    for (int j = 0; j < 4; ++j) angle[j] = angle_of(pos, __ldcg(a.turns + at.pair + j));
+    cos_sin2(angle[0], angle[1], c, s);
+    cos_sin2(angle[2], angle[3], c + 2, s + 2);
+    if (a.amplitude != 1.f) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        c[j] *= a.amplitude;
+        s[j] *= a.amplitude;
+      }
+    }
   }
   if (q0 < q1)
     turn_heads<D, kPairs, kFull>(a, at, c, s, a.q_weight, q0, q1, a.q.data + b * a.q.batch + t * a.q.row, a.q.head,
@@ -375,14 +432,22 @@ __device__ __forceinline__ void page_rows(const RopeParams& a, unsigned block, P
   Row w;
   const bool normed = !is_v && a.k_weight != nullptr;
   if (!is_v) {
-    w = weight_row(a.k_weight, at);
-    constexpr int kPairsOf = D / 2;
+    if (normed) w = weight_row(a.k_weight, at);
+    constexpr int kPairsOf = D / 2, kApart = kRopeThreads / kPairsOf;
     const int pair = threadIdx.x % kPairsOf;
     if (2 * pair < a.rot_dim) {
-      const uint64_t turns = static_cast<uint64_t>(__ldcg(a.turns + pair));
+      const long long turns = __ldcg(a.turns + pair);
       const long long p0 = static_cast<long long>(__ldcg(a.rope_base + pu.b)) + a.pos_offset + t0;
-      for (int slot = s0 + static_cast<int>(threadIdx.x) / kPairsOf; slot < s1; slot += kRopeThreads / kPairsOf)
-        cos_sin(static_cast<uint64_t>(p0 + slot) * turns, a.amplitude, &own.c[slot][pair], &own.s[slot][pair]);
+      for (int slot = s0 + static_cast<int>(threadIdx.x) / kPairsOf; slot < s1; slot += 2 * kApart) {
+        float c[2], s[2];
+        cos_sin2(angle_of(p0 + slot, turns), angle_of(p0 + slot + kApart, turns), c, s);
+        own.c[slot][pair] = c[0] * a.amplitude;
+        own.s[slot][pair] = s[0] * a.amplitude;
+        if (slot + kApart < s1) {
+          own.c[slot + kApart][pair] = c[1] * a.amplitude;
+          own.s[slot + kApart][pair] = s[1] * a.amplitude;
+        }
+      }
     }
     __syncthreads();
   }
@@ -396,7 +461,11 @@ __device__ __forceinline__ void page_rows(const RopeParams& a, unsigned block, P
   for (int i = 0; i < NI; ++i) {
     Row f = widen_row(x[i], y[i]);
     if (!is_v && i * RPI + RPI > s0 && i * RPI < s1) {  // (the warp together)
-      if (normed) norm_row<D>(f, a.eps);
+      if (normed) {
+        norm_row<D>(f, a.eps);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) f.x[p] = mul2(f.x[p], w.x[p]);
+      }
       float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
       const int slot = i * RPI + sub;
       if (at.turned && slot >= s0 && slot < s1) {
@@ -405,7 +474,7 @@ __device__ __forceinline__ void page_rows(const RopeParams& a, unsigned block, P
         c[0] = cc.x, c[1] = cc.y, c[2] = cc.z, c[3] = cc.w;
         s[0] = ss.x, s[1] = ss.y, s[2] = ss.z, s[3] = ss.w;
       }
-      f = turn_row<kPairs, kFull>(f, turn_of<kPairs>(c, s, w), at.turned);
+      f = turn_row<kPairs, kFull>(f, turn_of<kPairs>(c, s), at.turned);
     }
 #pragma unroll
     for (int p = 0; p < 4; ++p) top = max(top, magnitude(f.x[p]));
@@ -467,10 +536,13 @@ __global__ void __launch_bounds__(kRopeThreads, 5) norm_rope_quant_kernel(const 
   __shared__ __align__(16) PageRows<D> own;
   ptx::pdl_wait_primary();
   ptx::pdl_launch_dependents();
-  if (blockIdx.x < a.page_blocks) {
-    page_rows<D, kPairs, kFull>(a, blockIdx.x, own);
+  // Blocks of pages, evenly among those of queries: the ones compute, the others read and write.
+  const unsigned before = static_cast<unsigned>(static_cast<uint64_t>(blockIdx.x) * a.page_blocks / gridDim.x);
+  const unsigned after = static_cast<unsigned>((static_cast<uint64_t>(blockIdx.x) + 1) * a.page_blocks / gridDim.x);
+  if (after > before) {
+    page_rows<D, kPairs, kFull>(a, before, own);
   } else {
-    const unsigned task = (blockIdx.x - a.page_blocks) * kRopeWarps + (threadIdx.x >> 5);
+    const unsigned task = (blockIdx.x - before) * kRopeWarps + (threadIdx.x >> 5);
     if (task < a.tasks) token_rows<D, kPairs, kFull, false>(a, task);
   }
 }
@@ -516,10 +588,11 @@ RopeParams rope_params(const RopeArgs& x, int heads) {
   const int rpi = x.d == 128 ? 2 : 4;
   const long long tokens = static_cast<long long>(x.B) * x.n;
   p.chunk = heads;
-  while (p.chunk > rpi && tokens * ((heads + p.chunk - 1) / p.chunk) < 24ll * x.num_sms)
+  while (p.chunk > rpi && tokens * ((heads + p.chunk - 1) / p.chunk) < (getenv("VSD_T") ? atoi(getenv("VSD_T")) : 24ll) * x.num_sms)
     p.chunk = (p.chunk / 2 + rpi - 1) / rpi * rpi;
-  p.chunks = (heads + p.chunk - 1) / p.chunk;
-  p.tasks = static_cast<unsigned>(tokens * p.chunks);
+  p.chunks = Divisor(static_cast<uint32_t>((heads + p.chunk - 1) / p.chunk));
+  p.by_n = Divisor(static_cast<uint32_t>(x.n));
+  p.tasks = static_cast<unsigned>(tokens * p.chunks.d);
   return p;
 }
 
