@@ -8,7 +8,7 @@
 //
 // How: one cluster for each (sequence, KV head) of K and of V.  In a step each warp of the
 // cluster reads the 16 rows of one destination page into registers, and looks up where its next
-// page's rows lie meanwhile; in place the cluster meets; then every warp writes its page.  8-bit
+// pages' rows lie meanwhile; in place the cluster meets; then every warp writes its page.  8-bit
 // pages take the largest scale of the rows that come in.
 #include <cooperative_groups.h>
 
@@ -73,41 +73,20 @@ __global__ void __launch_bounds__(kCThreads) compact_kernel(const CompactParams 
   float* w_out = a.weights_out + static_cast<size_t>(pair) * static_cast<size_t>(a.w_out_stride);
   const int pages = (n + kPageC - 1) / kPageC;
   const int step = CS * kCWarps;
-  // where a page's rows come from (lanes 0 .. 15: a row each) and go to
-  struct Page {
-    long long from = -1;  // (block * Hkv + g) * 16 + row
-    int to = -1;          // block
-    float w = 0.f, s = 0.f;
-  };
+  // A page's rows (lanes 0 .. 15: one each) are looked up in steps, each a step of the loop ahead of
+  // the next, so that no load waits for another: the index two ahead, then its block (and the
+  // page's own), then the rows with their scales and weights.
   const int32_t* sources = a.block_table + static_cast<size_t>(b) * a.max_blocks;
   const int32_t* places = a.dst_table + static_cast<size_t>(b) * a.dst_blocks;
-  const auto find = [&](int page) {
-    Page r;
-    if (page >= pages) return r;
-    r.to = __ldcg(places + page);
+  const auto index_of = [&](int page) {
     const int i = page * kPageC + lane;
-    if (lane < kPageC && i < n) {
-      const int j = __ldcg(idx + i);
-      if (j < i || j >= P) {
-        flag_status(a.status, VSD_DEV_BAD_INDEX);
-      } else {
-        const int blk = __ldcg(sources + j / kPageC);
-        if (blk < 0 || blk >= a.num_blocks) {
-          flag_status(a.status, VSD_DEV_BAD_BLOCK);
-        } else {
-          const long long ph = static_cast<long long>(blk) * a.Hkv + g;
-          r.from = ph * kPageC + j % kPageC;
-          if (weighted) r.w = __ldcg(w_in + j);
-          if (kQuant) r.s = __ldcg(scale + ph);
-        }
-      }
-    }
-    if (r.to < 0 || r.to >= a.num_blocks) {
-      if (lane == 0) flag_status(a.status, VSD_DEV_BAD_BLOCK);
-      r.to = -1;
-    }
-    return r;
+    return page < pages && lane < kPageC && i < n ? __ldcg(idx + i) : -1;
   };
+  const auto fits = [&](int j, int page) { return j >= page * kPageC + lane && j < P; };
+  const auto block_of = [&](int j, int page) {
+    return lane < kPageC && fits(j, page) ? __ldcg(sources + j / kPageC) : -1;
+  };
+  const auto place_of = [&](int page) { return page < pages ? __ldcg(places + page) : -1; };
   // Does any page go back to its own place?  (Otherwise no row that is read is ever written, and
   // the warps need not wait for one another.)  The weights may do so by themselves.
   bool meet = a.block_table == a.dst_table || (weighted && a.weights == a.weights_out);
@@ -118,25 +97,43 @@ __global__ void __launch_bounds__(kCThreads) compact_kernel(const CompactParams 
     meet = __syncthreads_or(same);
   }
   int page = rank * kCWarps + warp;
-  Page at = find(page);
+  int j = index_of(page), j1 = index_of(page + step);
+  int blk = block_of(j, page), to = place_of(page);
   for (int p0 = 0; p0 < pages; p0 += step, page += step) {
-    const unsigned rows = __ballot_sync(0xffffffffu, at.from >= 0);
+    const int i = page * kPageC + lane;
+    const bool mine = page < pages && lane < kPageC && i < n;
+    long long from = -1;  // (block * Hkv + g) * 16 + row
+    float w = 0.f, s = 0.f;
+    if (mine) {
+      if (!fits(j, page)) {
+        flag_status(a.status, VSD_DEV_BAD_INDEX);
+      } else if (blk < 0 || blk >= a.num_blocks) {
+        flag_status(a.status, VSD_DEV_BAD_BLOCK);
+      } else {
+        const long long ph = static_cast<long long>(blk) * a.Hkv + g;
+        from = ph * kPageC + j % kPageC;
+        if (weighted) w = __ldcg(w_in + j);
+        if (kQuant) s = __ldcg(scale + ph);
+      }
+    }
+    const unsigned rows = __ballot_sync(0xffffffffu, from >= 0);
     uint4 x[NI];
     unsigned there = 0u;
 #pragma unroll
     for (int r = 0; r < NI; ++r) {
-      const long long from = __shfl_sync(0xffffffffu, at.from, r * RPI + sub);
+      const long long row = __shfl_sync(0xffffffffu, from, r * RPI + sub);
       x[r] = make_uint4(0, 0, 0, 0);
-      if (from >= 0) {
+      if (row >= 0) {
         there |= 1u << r;
-        x[r] = ldg_stream16(cache + from * kBytes + lr * 16);
+        x[r] = ldg_stream16(cache + row * kBytes + lr * 16);
       }
     }
-    const Page next = find(page + step);  // (while the rows are on their way)
+    const int j2 = index_of(page + 2 * step);
+    const int blk1 = block_of(j1, page + step), to1 = place_of(page + step);
     float top = 0.f;
     if (kQuant) {
-      top = warp_max_f32(at.s);
-      const float ratio = at.s == top ? 1.f : __fdiv_rn(at.s, top);
+      top = warp_max_f32(s);
+      const float ratio = s == top ? 1.f : __fdiv_rn(s, top);
 #pragma unroll
       for (int r = 0; r < NI; ++r) {
         const float f = __shfl_sync(0xffffffffu, ratio, r * RPI + sub);
@@ -154,19 +151,23 @@ __global__ void __launch_bounds__(kCThreads) compact_kernel(const CompactParams 
     if (meet) {
       if (CS > 1) cluster.sync(); else __syncthreads();
     }
+    if (mine && weighted) w_out[i] = w;
     if (page < pages) {
-      const int i = page * kPageC + lane;
-      if (weighted && lane < kPageC && i < n) w_out[i] = at.w;
-      if (at.to >= 0) {
-        const size_t ph = static_cast<size_t>(at.to) * a.Hkv + g;
-        uint8_t* to = cache + ph * (kPageC * kBytes) + lr * 16;
+      if (to < 0 || to >= a.num_blocks) {
+        if (lane == 0) flag_status(a.status, VSD_DEV_BAD_BLOCK);
+      } else {
+        const size_t ph = static_cast<size_t>(to) * a.Hkv + g;
+        uint8_t* at = cache + ph * (kPageC * kBytes) + lr * 16;
 #pragma unroll
         for (int r = 0; r < NI; ++r)
-          if (there >> r & 1u) *reinterpret_cast<uint4*>(to + (r * RPI + sub) * kBytes) = x[r];
+          if (there >> r & 1u) *reinterpret_cast<uint4*>(at + (r * RPI + sub) * kBytes) = x[r];
         if (kQuant && lane == 0 && rows != 0u) scale[ph] = top;
       }
     }
-    at = next;
+    j = j1;
+    j1 = j2;
+    blk = blk1;
+    to = to1;
   }
   if (weighted) {  // (in place the last step's meeting is behind: none of the old sums is read any more)
     for (int i = n + rank * kCThreads + static_cast<int>(threadIdx.x); i < a.w_out_stride; i += CS * kCThreads)
