@@ -29,6 +29,7 @@ namespace {
 constexpr int kWMaxCluster = 16;
 constexpr int kWGroup = 8;             // columns at a time
 constexpr int kPageW = 16;
+constexpr float kNone = -3e38f;        // a reference that nothing has set
 
 struct WeightsParams {
   const float* logits;
@@ -45,11 +46,13 @@ struct WeightsParams {
   int8_t slot[kMaxWeightSlots], row[kMaxWeightSlots];
 };
 
+// Exponents are kept to base 2: t = z log2 e, formed in one fma against what is subtracted from
+// it, so that the constant's rounding is the same in every exponential of a row.
 struct Stat {
-  float m, l;  // maximum, and sum of e^(z - m)
+  float m, l;  // a reference (near the largest t), and the sum of 2^(t - m)
 };
 
-__device__ __forceinline__ float exp_of(float x) { return ex2(x * kLog2e); }
+__device__ __forceinline__ float exp_of(float x) { return ex2(x); }
 
 // What exponents are taken against: the maximum, or 0 where there is nothing yet.
 __device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.f : m; }
@@ -100,6 +103,33 @@ __device__ __forceinline__ void load_if(const float* p, bool there, float& z) {
                : "memory");
 }
 
+// How L2 is to hold what a load brings: as usual, or as the first to go.
+__device__ __forceinline__ uint64_t policy_usual() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
+__device__ __forceinline__ uint64_t policy_first_to_go() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
+__device__ __forceinline__ void load_with(const float* p, uint64_t policy, float (&z)[4]) {
+  asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.f32 {%0, %1, %2, %3}, [%4], %5;"
+               : "=f"(z[0]), "=f"(z[1]), "=f"(z[2]), "=f"(z[3])
+               : "l"(p), "l"(policy)
+               : "memory");
+}
+
+__device__ __forceinline__ void load_with(const float* p, uint64_t policy, float& z) {
+  asm volatile("ld.global.L1::no_allocate.L2::cache_hint.f32 %0, [%1], %2;"
+               : "=f"(z)
+               : "l"(p), "l"(policy)
+               : "memory");
+}
+
 // A thread's four values of a step (those at `end` and beyond: minus infinity; a vector that
 // begins before it is read whole, row strides being multiples of four then, and masked).
 template <bool kVec, int kThreads>
@@ -111,6 +141,17 @@ __device__ __forceinline__ void load4(const float* p, int base, int end, float (
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) load_if(p + place<kVec, kThreads>(base, j), place<kVec, kThreads>(base, j) < end, z[j]);
+  }
+}
+
+// The same of a step that lies before the slice's end.
+template <bool kVec, int kThreads>
+__device__ __forceinline__ void load4(const float* p, int base, uint64_t policy, float (&z)[4]) {
+  if (kVec) {
+    load_with(p + place<kVec, kThreads>(base, 0), policy, z);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load_with(p + place<kVec, kThreads>(base, j), policy, z[j]);
   }
 }
 
@@ -128,8 +169,8 @@ constexpr int kRowBytes = 272;  // 128 values and 16 bytes: rows next to each ot
 struct Block {
   uint4 q[kMaxWeightCols][kRowBytes / 16];
   uint4 k[kMaxWeightSlots][kRowBytes / 16];
-  float factor[kMaxWeightSlots];           // scale, times the key's; NaN: no such key
-  float z[kMaxWeightCols][kMaxWeightSlots];  // logits; minus infinity: not seen
+  float factor[kMaxWeightSlots];           // scale log2 e, times the key's; NaN: no such key
+  float z[kMaxWeightCols][kMaxWeightSlots];  // logits log2 e; minus infinity: not seen
 };
 
 // Piece i of those operands: 8 values of a key (the block's first), or of a column's query.
@@ -152,7 +193,7 @@ __device__ __forceinline__ Piece fetch_piece(const WeightsParams& a, int b, int 
                                              int blk) {
   const int pieces = a.d / 8;
   const int u = i / pieces, c = i - u * pieces;
-  Piece r{make_uint4(0, 0, 0, 0), a.scale};
+  Piece r{make_uint4(0, 0, 0, 0), a.scale * kLog2e};
   if (u >= a.R) {
     const int col = rank + (u - a.R) * CS, slot = col / a.G;
     r.v = ldg_stream16(
@@ -343,10 +384,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(c
 #pragma unroll
       for (int c = 0; c < kWGroup; ++c) {
         float(&z)[4] = keep[c0 + c];
-        m[c] = warp_max_f32(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])));
-        const float ref = reference(m[c]);
+        m[c] = warp_max_f32(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]))) * kLog2e;
+        const float ref = -reference(m[c]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) z[j] = exp_of(z[j] - ref);
+        for (int j = 0; j < 4; ++j) z[j] = exp_of(fmaf(z[j], kLog2e, ref));
         l[c] = (z[0] + z[1]) + (z[2] + z[3]);
       }
       const float sum = warp_sum_columns<kWGroup>(l);
@@ -355,39 +396,48 @@ __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(c
         if (lane == c) part[warp][c0 + c] = Stat{m[c], sum};
     }
   } else {
+    const uint64_t policy = policy_usual();
     for (int c0 = 0; c0 < a.cols; c0 += kWGroup) {
       const int nc = min(kWGroup, a.cols - c0);
+      // A thread's reference of a column is its first largest t, raised (with its sum) when one
+      // exceeds it by 2^57: rarely.
       float m[kWGroup], l[kWGroup];
 #pragma unroll
       for (int c = 0; c < kWGroup; ++c) {
-        m[c] = -INFINITY;
+        m[c] = kNone;
         l[c] = 0.f;
       }
-      for (int base = lo; base < hi; base += kStep) {
+      const auto take = [&](const float (&z)[kWGroup][4]) {
+#pragma unroll
+        for (int c = 0; c < kWGroup; ++c) {
+          const float top = fmaxf(fmaxf(z[c][0], z[c][1]), fmaxf(z[c][2], z[c][3]));
+          if (fmaf(top, kLog2e, -m[c]) > 57.f) {
+            const float now = top * kLog2e;
+            l[c] *= exp_of(m[c] - now);
+            m[c] = now;
+          }
+          l[c] += (exp_of(fmaf(z[c][0], kLog2e, -m[c])) + exp_of(fmaf(z[c][1], kLog2e, -m[c]))) +
+                  (exp_of(fmaf(z[c][2], kLog2e, -m[c])) + exp_of(fmaf(z[c][3], kLog2e, -m[c])));
+        }
+      };
+      int base = lo;
+      for (; base + kStep <= hi; base += kStep) {
         float z[kWGroup][4];
 #pragma unroll
-        for (int c = 0; c < kWGroup; ++c) {
-          if (c < nc) {
-            load4<kVec, kThreads>(column[c0 + c], base, hi, z[c]);
-          } else {
-            z[c][0] = z[c][1] = z[c][2] = z[c][3] = -INFINITY;
-          }
-        }
-        if (base + kStep > hi) {
+        for (int c = 0; c < kWGroup; ++c) load4<kVec, kThreads>(column[c < nc ? c0 + c : c0], base, policy, z[c]);
+        take(z);
+      }
+      if (base < hi) {
+        float z[kWGroup][4];
 #pragma unroll
-          for (int c = 0; c < kWGroup; ++c) mask4<kVec, kThreads>(base, hi, z[c]);
-        }
+        for (int c = 0; c < kWGroup; ++c) load4<kVec, kThreads>(column[c < nc ? c0 + c : c0], base, hi, z[c]);
 #pragma unroll
-        for (int c = 0; c < kWGroup; ++c) {
-          const float now = fmaxf(m[c], fmaxf(fmaxf(z[c][0], z[c][1]), fmaxf(z[c][2], z[c][3])));
-          const float ref = reference(now);
-          l[c] *= exp_of(m[c] - ref);
-          l[c] += (exp_of(z[c][0] - ref) + exp_of(z[c][1] - ref)) + (exp_of(z[c][2] - ref) + exp_of(z[c][3] - ref));
-          m[c] = now;
-        }
+        for (int c = 0; c < kWGroup; ++c) mask4<kVec, kThreads>(base, hi, z[c]);
+        take(z);
       }
 #pragma unroll
       for (int c = 0; c < kWGroup; ++c) {
+        if (m[c] == kNone) m[c] = -INFINITY;
         const float wm = warp_max_f32(m[c]);
         l[c] *= exp_of(m[c] - reference(wm));
         m[c] = wm;
@@ -431,21 +481,30 @@ __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(c
     }
     add(lo, p);
   } else {
-    for (int base = lo; base < hi; base += kStep) {
-      load4<kVec, kThreads>(out, base, hi, w);
+    // Backwards: what was read last is still in L2 (and is not needed there afterwards).
+    const uint64_t policy = policy_first_to_go();
+    const int groups = (a.cols + kWGroup - 1) / kWGroup;
+    for (int base = lo + (hi - lo - 1) / kStep * kStep; base >= lo; base -= kStep) {
+      const bool inside = base + kStep <= hi;
+      if (inside) load4<kVec, kThreads>(out, base, policy, w);
+      else load4<kVec, kThreads>(out, base, hi, w);
       float p[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int c0 = 0; c0 < a.cols; c0 += kWGroup) {
-        const int nc = min(kWGroup, a.cols - c0);
+      for (int q = groups - 1; q >= 0; --q) {
+        const int c0 = q * kWGroup, nc = min(kWGroup, a.cols - c0);
         float z[kWGroup][4];
+        if (inside) {
 #pragma unroll
-        for (int c = 0; c < kWGroup; ++c)
-          if (c < nc) load4<kVec, kThreads>(column[c0 + c], base, hi, z[c]);
+          for (int c = 0; c < kWGroup; ++c) load4<kVec, kThreads>(column[c < nc ? c0 + c : c0], base, policy, z[c]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < kWGroup; ++c) load4<kVec, kThreads>(column[c < nc ? c0 + c : c0], base, hi, z[c]);
+        }
 #pragma unroll
         for (int c = 0; c < kWGroup; ++c) {
           if (c < nc) {
             const Stat s = whole[c0 + c];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) p[j] = fmaf(exp_of(z[c][j] - s.m), s.l, p[j]);
+            for (int j = 0; j < 4; ++j) p[j] = fmaf(exp_of(fmaf(z[c][j], kLog2e, -s.m)), s.l, p[j]);
           }
         }
       }
