@@ -117,14 +117,14 @@ __device__ __forceinline__ uint64_t policy_first_to_go() {
 }
 
 __device__ __forceinline__ void load_with(const float* p, uint64_t policy, float (&z)[4]) {
-  asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.f32 {%0, %1, %2, %3}, [%4], %5;"
+  asm volatile("ld.global.cg.L2::cache_hint.v4.f32 {%0, %1, %2, %3}, [%4], %5;"
                : "=f"(z[0]), "=f"(z[1]), "=f"(z[2]), "=f"(z[3])
                : "l"(p), "l"(policy)
                : "memory");
 }
 
 __device__ __forceinline__ void load_with(const float* p, uint64_t policy, float& z) {
-  asm volatile("ld.global.L1::no_allocate.L2::cache_hint.f32 %0, [%1], %2;"
+  asm volatile("ld.global.cg.L2::cache_hint.f32 %0, [%1], %2;"
                : "=f"(z)
                : "l"(p), "l"(policy)
                : "memory");
@@ -543,13 +543,15 @@ cudaError_t launch_vec(const WeightsParams& p, int num_sms, cudaStream_t stream)
   int CS = (p.P_max + 2047) / 2048;
   if (CS <= kWMaxCluster && p.cols <= 16 && pairs * CS <= num_sms)
     return p.cols <= 8 ? launch<kVec, 8, 512, 2>(p, CS, stream) : launch<kVec, 16, 512, 1>(p, CS, stream);
-  // read again: slices of at least a step of 1024 positions.  Where clusters of 8 fill the GPU
-  // (three CTAs an SM), wider ones wait for one another more than they win: 16 x 32K with 8
-  // heads of 8 queries 93 us with 8 CTAs, 111 with 16, 99 with 6.
+  // Read again: slices of at least a step of 1024 positions, four CTAs an SM (three where values
+  // come one by one: their registers do not fit otherwise).  Where clusters of 8 fill the GPU,
+  // wider ones wait for one another more than they win: 16 x 32K with 8 heads of 8 queries 75 us
+  // with 8 CTAs a cluster, 84 with 4, 86 with 12, 95 with 16.  (Rounds of 8 columns, whose
+  // second reading finds more in L2, took 79: the sums go round the cluster twice.)
   CS = (p.P_max + 1023) / 1024;
   const int widest = pairs * 8 >= 3ll * num_sms ? 8 : kWMaxCluster;
   if (CS > widest) CS = widest;
-  return launch<kVec, 0, 256, 3>(p, CS, stream);
+  return launch<kVec, 0, 256, kVec ? 4 : 3>(p, CS, stream);
 }
 
 }  // namespace
