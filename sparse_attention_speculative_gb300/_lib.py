@@ -300,6 +300,10 @@ def vsd_select_topk(partial, prefix_len, *, k: int, n_sink: int, n_recent: int, 
                     n_sel=None, scores_out=None, want_scores: bool = False,
                     stream=None) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
     """Protected top-k over the aggregated score.  partial: fp32 [n_rows, Hkv, P_max]."""
+    module = _binding or _bound_or_none()
+    if module is not None:
+        return module.select(partial, prefix_len, int(k), int(n_sink), int(n_recent), idx, n_sel,
+                             scores_out, want_scores, _handle(stream))
     lib = load()
     _need(partial, torch.float32, "partial")
     _need(prefix_len, torch.int32, "prefix_len")
@@ -691,9 +695,24 @@ def _bound():
     module.attach_more(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.vsd_norm_rope, lib.vsd_norm_rope_append_kv, lib.vsd_norm_rope_append_kv_quant,
         lib.vsd_accumulate_weights, lib.vsd_accumulate_weights_quant, lib.vsd_compact_kv,
-        lib.vsd_compact_kv_quant)))
+        lib.vsd_compact_kv_quant, lib.vsd_select_topk)))
     _binding = module
     return module
+
+
+_no_binding = False
+
+
+def _bound_or_none():
+    """The extension module, or None where it cannot be used: for a call that has another way."""
+    global _no_binding
+    if not _no_binding:
+        load()
+        try:
+            return _bound()
+        except RuntimeError:
+            _no_binding = True
+    return None
 
 
 def _handle(stream):

@@ -36,6 +36,7 @@ struct Calls {
   decltype(&vsd_accumulate_weights_quant) weights_quant = nullptr;
   decltype(&vsd_compact_kv) compact = nullptr;
   decltype(&vsd_compact_kv_quant) compact_quant = nullptr;
+  decltype(&vsd_select_topk) select = nullptr;
   PyObject* error = nullptr;  // VsdError(status, name)
 };
 Calls g_calls;
@@ -648,6 +649,41 @@ PyObject* py_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// select(partial, prefix_len, k, n_sink, n_recent, idx, n_sel, scores_out, want_scores, stream)
+//   -> (idx, n_sel, scores_out).  (Buffers that are given are taken as they are.)
+PyObject* py_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 10, [&]() -> PyObject* {
+    const at::Tensor &partial = as_tensor(a[0], "partial"), &pl = as_tensor(a[1], "prefix_len");
+    need(partial, at::kFloat, 3, "partial");
+    need(pl, at::kInt, pl.dim(), "prefix_len");
+    const Place p(partial, a[9]);
+    const int rows = dim_of(partial.size(0), "n_rows"), Hkv = dim_of(partial.size(1), "Hkv");
+    const int P_max = dim_of(partial.size(2), "P_max"), k = as_int(a[2], "k");
+    const int n_sink = as_int(a[3], "n_sink"), n_recent = as_int(a[4], "n_recent");
+    const auto output = [&](PyObject* given, at::ScalarType type, at::IntArrayRef shape, const char* name) {
+      Output o;
+      if (given != Py_None) {
+        o.object = given;
+        o.at = pointer(as_tensor(given, name));
+      } else {
+        o.take(Py_None, p, type, shape, name);
+      }
+      return o;
+    };
+    const Output idx = output(a[5], at::kInt, {rows, k}, "idx"), ns = output(a[6], at::kInt, {rows}, "n_sel");
+    Output scores;
+    if (as_bool(a[8]) || a[7] != Py_None) scores = output(a[7], at::kFloat, {rows, P_max}, "scores_out");
+    check(without_gil([&] {
+            return g_calls.select(rows, Hkv, static_cast<const float*>(pointer(partial)),
+                                  static_cast<const int32_t*>(pointer(pl)), P_max, k, n_sink, n_recent,
+                                  static_cast<int32_t*>(idx.at), static_cast<int32_t*>(ns.at),
+                                  static_cast<float*>(scores.at), nullptr, 0, p.stream);
+          }),
+          "vsd_select_topk");
+    return Py_BuildValue("(NNN)", idx.result(), ns.result(), scores.result());
+  });
+}
+
 // attach(error class, addresses of the six library calls)
 PyObject* py_attach(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 7) {
@@ -670,14 +706,14 @@ PyObject* py_attach(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
-// attach_more(addresses of the seven library calls of rows, weights and eviction)
+// attach_more(addresses of the library calls of rows, weights and eviction, and of the selection)
 PyObject* py_attach_more(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 7) {
-    PyErr_SetString(PyExc_TypeError, "attach_more takes seven addresses");
+  if (n != 8) {
+    PyErr_SetString(PyExc_TypeError, "attach_more takes eight addresses");
     return nullptr;
   }
-  void* at[7];
-  for (int i = 0; i < 7; ++i) {
+  void* at[8];
+  for (int i = 0; i < 8; ++i) {
     at[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) return nullptr;
   }
@@ -688,6 +724,7 @@ PyObject* py_attach_more(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_calls.weights_quant = reinterpret_cast<decltype(g_calls.weights_quant)>(at[4]);
   g_calls.compact = reinterpret_cast<decltype(g_calls.compact)>(at[5]);
   g_calls.compact_quant = reinterpret_cast<decltype(g_calls.compact_quant)>(at[6]);
+  g_calls.select = reinterpret_cast<decltype(g_calls.select)>(at[7]);
   Py_RETURN_NONE;
 }
 
@@ -697,7 +734,7 @@ PyMethodDef g_methods[] = {VSD_METHOD("attach", py_attach), VSD_METHOD("append",
                            VSD_METHOD("read", py_read),     VSD_METHOD("verify", py_verify),
                            VSD_METHOD("sparse", py_sparse), VSD_METHOD("attach_more", py_attach_more),
                            VSD_METHOD("rope", py_rope),     VSD_METHOD("weights", py_weights),
-                           VSD_METHOD("compact", py_compact), {nullptr, nullptr, 0, nullptr}};
+                           VSD_METHOD("compact", py_compact), VSD_METHOD("select", py_select), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};
 
