@@ -588,7 +588,7 @@ RopeParams rope_params(const RopeArgs& x, int heads) {
   const int rpi = x.d == 128 ? 2 : 4;
   const long long tokens = static_cast<long long>(x.B) * x.n;
   p.chunk = heads;
-  while (p.chunk > rpi && tokens * ((heads + p.chunk - 1) / p.chunk) < (getenv("VSD_T") ? atoi(getenv("VSD_T")) : 24ll) * x.num_sms)
+  while (p.chunk > rpi && tokens * ((heads + p.chunk - 1) / p.chunk) < 24ll * x.num_sms)
     p.chunk = (p.chunk / 2 + rpi - 1) / rpi * rpi;
   p.chunks = Divisor(static_cast<uint32_t>((heads + p.chunk - 1) / p.chunk));
   p.by_n = Divisor(static_cast<uint32_t>(x.n));
