@@ -43,6 +43,8 @@ struct WeightsParams {
   int B, Hq, Hkv, G, R, C, d, max_blocks, num_blocks, P_max, weights_stride;
   float scale;
   int cols;  // counted rows * G
+  int shift_g, shift_c;  // log2 of G, and of a row's 16-byte pieces
+  int by_cluster;        // 2^16 / CTAs of a cluster, rounded up: col * by_cluster >> 16 divides
   int8_t slot[kMaxWeightSlots], row[kMaxWeightSlots];
 };
 
@@ -179,23 +181,27 @@ struct Piece {
   float f;
 };
 
+// Columns of a CTA: rank, rank + CS, ...
+__device__ __forceinline__ int own_columns(const WeightsParams& a, int rank, int CS) {
+  return (a.cols - rank + CS - 1) * a.by_cluster >> 16;
+}
+
 __device__ __forceinline__ int block_pieces(const WeightsParams& a, int rank, int CS) {
-  return (a.R + (a.cols - rank + CS - 1) / CS) * (a.d / 8);
+  return (a.R + own_columns(a, rank, CS)) << a.shift_c;
 }
 
 // The block-table entry of a key's piece (-1: none, or a query's).
 __device__ __forceinline__ int piece_page(const WeightsParams& a, int b, int P, int i) {
-  const int u = i / (a.d / 8);
+  const int u = i >> a.shift_c;
   return u < a.R ? __ldcg(a.block_table + static_cast<size_t>(b) * a.max_blocks + (P + u) / kPageW) : -1;
 }
 
 __device__ __forceinline__ Piece fetch_piece(const WeightsParams& a, int b, int g, int P, int rank, int CS, int i,
                                              int blk) {
-  const int pieces = a.d / 8;
-  const int u = i / pieces, c = i - u * pieces;
+  const int u = i >> a.shift_c, c = i - (u << a.shift_c);
   Piece r{make_uint4(0, 0, 0, 0), a.scale * kLog2e};
   if (u >= a.R) {
-    const int col = rank + (u - a.R) * CS, slot = col / a.G;
+    const int col = rank + (u - a.R) * CS, slot = col >> a.shift_g;
     r.v = ldg_stream16(
         a.q + ((static_cast<size_t>(b) * a.R + a.row[slot]) * a.Hq + g * a.G + (col - slot * a.G)) * a.d + c * 8);
     return r;
@@ -219,8 +225,7 @@ __device__ __forceinline__ Piece fetch_piece(const WeightsParams& a, int b, int 
 }
 
 __device__ __forceinline__ void put_piece(const WeightsParams& a, int i, const Piece& r, Block& s) {
-  const int pieces = a.d / 8;
-  const int u = i / pieces, c = i - u * pieces;
+  const int u = i >> a.shift_c, c = i - (u << a.shift_c);
   if (u >= a.R) {
     s.q[u - a.R][c] = r.v;
     return;
@@ -240,32 +245,30 @@ __device__ __forceinline__ void put_piece(const WeightsParams& a, int i, const P
 // Eight lanes form one product.
 template <int kThreads>
 __device__ __forceinline__ void block_logits(const WeightsParams& a, int rank, int CS, Block& s) {
-  const int mine = (a.cols - rank + CS - 1) / CS;  // columns of this CTA
-  const int l8 = threadIdx.x & 7;
-  for (int i0 = static_cast<int>(threadIdx.x >> 5) * 4; i0 < mine * a.R; i0 += kThreads / 8) {  // (the warp together)
-    const int i = i0 + static_cast<int>((threadIdx.x >> 3) & 3u);
-    const int at = i / a.R, u = i - at * a.R;
-    const bool real = at < mine;
-    float dot[2] = {0.f, 0.f};
-    if (real) {
-      for (int c = l8; c < a.d / 8; c += 8) {
-        const uint4 x = s.q[at][c], y = s.k[u][c];
-        dot[0] = fmaf(bf16_lo(x.x), bf16_lo(y.x), dot[0]);
-        dot[1] = fmaf(bf16_hi(x.x), bf16_hi(y.x), dot[1]);
-        dot[0] = fmaf(bf16_lo(x.y), bf16_lo(y.y), dot[0]);
-        dot[1] = fmaf(bf16_hi(x.y), bf16_hi(y.y), dot[1]);
-        dot[0] = fmaf(bf16_lo(x.z), bf16_lo(y.z), dot[0]);
-        dot[1] = fmaf(bf16_hi(x.z), bf16_hi(y.z), dot[1]);
-        dot[0] = fmaf(bf16_lo(x.w), bf16_lo(y.w), dot[0]);
-        dot[1] = fmaf(bf16_hi(x.w), bf16_hi(y.w), dot[1]);
+  const int mine = own_columns(a, rank, CS);
+  const int l8 = threadIdx.x & 7, oct = static_cast<int>((threadIdx.x >> 3) & 3u);
+  for (int at = threadIdx.x >> 5; at < mine; at += kThreads / 32) {  // a column for each warp, four keys at a time
+    const int row = a.row[(rank + at * CS) >> a.shift_g];
+    for (int u0 = 0; u0 < a.R; u0 += 4) {
+      const int u = u0 + oct;
+      float dot[2] = {0.f, 0.f};
+      if (u <= row) {
+        for (int c = l8; c < a.d / 8; c += 8) {
+          const uint4 x = s.q[at][c], y = s.k[u][c];
+          dot[0] = fmaf(bf16_lo(x.x), bf16_lo(y.x), dot[0]);
+          dot[1] = fmaf(bf16_hi(x.x), bf16_hi(y.x), dot[1]);
+          dot[0] = fmaf(bf16_lo(x.y), bf16_lo(y.y), dot[0]);
+          dot[1] = fmaf(bf16_hi(x.y), bf16_hi(y.y), dot[1]);
+          dot[0] = fmaf(bf16_lo(x.z), bf16_lo(y.z), dot[0]);
+          dot[1] = fmaf(bf16_hi(x.z), bf16_hi(y.z), dot[1]);
+          dot[0] = fmaf(bf16_lo(x.w), bf16_lo(y.w), dot[0]);
+          dot[1] = fmaf(bf16_hi(x.w), bf16_hi(y.w), dot[1]);
+        }
       }
-    }
-    float z = dot[0] + dot[1];
+      float z = dot[0] + dot[1];
 #pragma unroll
-    for (int m = 4; m >= 1; m >>= 1) z += __shfl_xor_sync(0xffffffffu, z, m);
-    if (real && l8 == 0) {
-      const bool seen = u <= a.row[(rank + at * CS) / a.G] && !isnan(s.factor[u]);
-      s.z[at][u] = seen ? z * s.factor[u] : -INFINITY;
+      for (int m = 4; m >= 1; m >>= 1) z += __shfl_xor_sync(0xffffffffu, z, m);
+      if (l8 == 0 && u < a.R) s.z[at][u] = u <= row && !isnan(s.factor[u]) ? z * s.factor[u] : -INFINITY;
     }
   }
 }
@@ -291,8 +294,9 @@ __device__ __forceinline__ void share_sums(const WeightsParams& a, int rank, int
     Stat s{-INFINITY, 0.f};
     if (col < a.cols) {
       if (l16 < kWarps) s = part[l16][col];
-      if (col % CS == rank) {
-        const float z = l16 < a.R ? block.z[col / CS][l16] : -INFINITY, m = fmaxf(s.m, z);
+      const int at = col * a.by_cluster >> 16;
+      if (col - at * CS == rank) {
+        const float z = l16 < a.R ? block.z[at][l16] : -INFINITY, m = fmaxf(s.m, z);
         s = Stat{m, s.l * exp_of(s.m - reference(m)) + exp_of(z - reference(m))};
       }
     }
@@ -337,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(c
   const int b = pair / a.Hkv, g = pair - b * a.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (static_cast<int>(threadIdx.x) < a.cols) {
-    const int s = static_cast<int>(threadIdx.x) / a.G;
+    const int s = static_cast<int>(threadIdx.x) >> a.shift_g;
     column[threadIdx.x] = a.logits + ((static_cast<size_t>(b) * a.C + a.slot[s]) * a.Hq + g * a.G +
                                       (static_cast<int>(threadIdx.x) - s * a.G)) * static_cast<size_t>(a.P_max);
   }
@@ -514,7 +518,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(c
 }
 
 template <bool kVec, int kHold, int kThreads, int kBlocks>
-cudaError_t launch(const WeightsParams& p, int CS, cudaStream_t stream) {
+cudaError_t launch(WeightsParams p, int CS, cudaStream_t stream) {
+  p.by_cluster = (65536 + CS - 1) / CS;
   auto* kern = accumulate_weights_kernel<kVec, kHold, kThreads, kBlocks>;
   if (CS > 8) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -579,6 +584,8 @@ cudaError_t launch_accumulate_weights(const WeightsArgs& x, cudaStream_t stream)
   p.weights_stride = x.weights_stride;
   p.scale = x.scale;
   p.cols = x.used * x.G;
+  while (1 << p.shift_g < x.G) ++p.shift_g;
+  p.shift_c = x.d == 128 ? 4 : 3;
   for (int i = 0; i < x.used; ++i) {
     p.slot[i] = x.slot[i];
     p.row[i] = x.row[i];
