@@ -210,23 +210,30 @@ __device__ __forceinline__ Row weight_row(const uint16_t* w, const Lanes<D, kPai
 }
 
 // Cosines and sines of two angles, in units of 2^-32 of a turn.  The nearest quarter turn is
-// taken off, and what is left (x, at most pi / 4) goes through polynomials in x^2: minimax fits
-// of (sin x / x - 1) / x^2 and (cos x - 1) / x^2 found by Remez's exchange, off by 4e-9 and 1e-10
-// before they are rounded.  With fp32's roundings sine and cosine are within 1e-7.
+// taken off; what is left is x + dx, |x| at most pi / 4 and dx its rounding.  Polynomials in
+// u = x^2: minimax fits of (sin x / x - 1) / u and (cos x - 1 + u / 2) / u^2 found by Remez's
+// exchange, whose errors are below 4e-9 of the result, with dx to first order and 1 - u / 2 with
+// its rounding: both are within 5e-8, mostly the nearest float (8-bit codes show the rest).
 __device__ __forceinline__ void cos_sin2(uint32_t a, uint32_t b, float* c, float* s) {
   const uint32_t qa = (a + 0x20000000u) >> 30, qb = (b + 0x20000000u) >> 30;
-  const F2 x = mul2(f2(static_cast<float>(static_cast<int>(a - (qa << 30))),
-                       static_cast<float>(static_cast<int>(b - (qb << 30)))),
-                    f2(0x1.921fb6p-30f, 0x1.921fb6p-30f));  // 2 pi / 2^32
+  const int ra = static_cast<int>(a - (qa << 30)), rb = static_cast<int>(b - (qb << 30));
+  const float fa = static_cast<float>(ra), fb = static_cast<float>(rb);
+  const F2 high = f2(fa, fb);
+  const F2 low = f2(static_cast<float>(ra - static_cast<int>(fa)), static_cast<float>(rb - static_cast<int>(fb)));
   const auto k = [](float v) { return f2(v, v); };
+  const F2 x = mul2(high, k(0x1.921fb6p-30f));  // 2 pi / 2^32, and what its rounding leaves
+  const F2 less = fma2(high, k(0x1.777a5cp-55f), fma2(low, k(-0x1.921fb6p-30f), fma2(high, k(-0x1.921fb6p-30f), x)));
+  const F2 dx = mul2(less, k(-1.f));
   const F2 u = mul2(x, x);
   F2 p = fma2(u, k(-1.95172994e-4f), k(8.332178e-3f));
-  p = fma2(p, u, k(-0.166666552f));
-  const float2 sn = parts(fma2(mul2(p, u), x, x));
+  p = mul2(fma2(p, u, k(-0.166666552f)), u);
   F2 q = fma2(u, k(2.43904506e-5f), k(-1.38867635e-3f));
   q = fma2(q, u, k(0.0416666232f));
-  q = fma2(q, u, k(-0.5f));
-  const float2 cs = parts(fma2(q, u, k(1.f)));
+  const F2 w = fma2(u, k(-0.5f), k(1.f));
+  F2 rest = fma2(u, k(-0.5f), fma2(w, k(-1.f), k(1.f)));
+  rest = fma2(less, fma2(p, x, x), fma2(mul2(u, q), u, rest));
+  const F2 cosine = fma2(w, k(1.f), rest);
+  const float2 cs = parts(cosine), sn = parts(fma2(fma2(p, x, mul2(dx, cosine)), k(1.f), x));
   const auto put = [](uint32_t quadrant, float cosine, float sine, float* c, float* s) {
     const bool odd = (quadrant & 1u) != 0u;
     *c = __uint_as_float(__float_as_uint(odd ? sine : cosine) ^ ((quadrant + 1u) & 2u) << 30);
