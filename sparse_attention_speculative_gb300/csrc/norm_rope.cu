@@ -466,8 +466,9 @@ __device__ __forceinline__ void page_rows(const RopeParams& a, unsigned block, P
   };
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
+    if (i * RPI + RPI <= s0 || i * RPI >= s1) continue;  // (the warp together)
     Row f = widen_row(x[i], y[i]);
-    if (!is_v && i * RPI + RPI > s0 && i * RPI < s1) {  // (the warp together)
+    if (!is_v) {
       if (normed) {
         norm_row<D>(f, a.eps);
 #pragma unroll
@@ -500,7 +501,7 @@ __device__ __forceinline__ void page_rows(const RopeParams& a, unsigned block, P
       return f2(lo_ok ? v.x : NAN, hi_ok ? v.y : NAN);
     };
 #pragma unroll 1
-    for (int i = 0; i < 2 * NI; ++i) {
+    for (int i = s0 / RPI * 2; i < (s1 + RPI - 1) / RPI * 2; ++i) {
       ulonglong2& v = own.value[i >> 1][i & 1][threadIdx.x];
       v = make_ulonglong2(clean(v.x), clean(v.y));
     }
@@ -590,12 +591,14 @@ RopeParams rope_params(const RopeArgs& x, int heads) {
   p.pos_offset = x.pos_offset;
   p.zeroed = x.zeroed;
   p.heads = heads;
-  // A warp takes as many of a token's heads as leaves about 24 warps, what fits, for each SM (4012
-  // tokens of 24 heads: 6.8 us with whole tokens, 8.6 with halves).
+  // A warp takes as many of a token's heads as leaves an SM about as many warps as it holds: 24
+  // (4012 tokens of 24 heads 6.7 us with whole tokens, 8.6 with halves), 10 beside the pages of an
+  // 8-bit cache (96 tokens of 64 heads 5.8 us with 4 heads a warp, 7.1 with 2).
+  const long long warps = (x.k_scale != nullptr ? 10ll : 24ll) * x.num_sms;
   const int rpi = x.d == 128 ? 2 : 4;
   const long long tokens = static_cast<long long>(x.B) * x.n;
   p.chunk = heads;
-  while (p.chunk > rpi && tokens * ((heads + p.chunk - 1) / p.chunk) < 24ll * x.num_sms)
+  while (p.chunk > rpi && tokens * ((heads + p.chunk - 1) / p.chunk) < warps)
     p.chunk = (p.chunk / 2 + rpi - 1) / rpi * rpi;
   p.chunks = Divisor(static_cast<uint32_t>((heads + p.chunk - 1) / p.chunk));
   p.by_n = Divisor(static_cast<uint32_t>(x.n));
