@@ -705,8 +705,8 @@ vsd_status vsd_sparse_decode_attn_quant(const vsd_geom* geom, const void* q,
  *   in between).  A sequence whose range is refused stores nothing; its q_out is written.
  *
  * Supported: head_dim 64 or 128, rot_dim a multiple of 8 up to head_dim (0: no rotation, turns
- * may be NULL), B * n * ceil((Hq + 2 Hkv) / 2) below 2^31.  All are programmatic dependents of
- * the preceding kernel on the stream.
+ * may be NULL), B * n * (Hq + 2 Hkv + 2) / 2 below 2^31 and, into an 8-bit cache, B * Hkv *
+ * (n / 16 + 2) below 2^29.  All are programmatic dependents of the preceding kernel on the stream.
  * ------------------------------------------------------------------------------ */
 typedef struct vsd_rows {
   const void* data;
@@ -767,9 +767,9 @@ vsd_status vsd_norm_rope_append_kv_quant(const vsd_geom* geom, int n, const vsd_
  * The keys are those of the cache; with an 8-bit cache its key codes and their scales.  A key
  * of the verify block whose block-table entry is outside the cache is left out and flagged
  * VSD_DEV_BAD_BLOCK; a prefix outside [0, P_max], or whose verify block leaves the table, is
- * flagged VSD_DEV_BAD_LENGTH and that sequence's weights stay.  A row with a NaN or an
- * infinite logit adds NaN, one whose logits are all minus infinity adds nothing.  Sums are
- * formed in a fixed order (two runs are bit-identical).
+ * flagged VSD_DEV_BAD_LENGTH and that sequence's weights stay.  A row with a NaN or plus infinity
+ * among its logits (one beyond 2^127 counts as that) adds NaN; minus infinity weighs nothing.
+ * Sums are formed in a fixed order (two runs are bit-identical).
  * Supported: as vsd_verify_attn_collect with C <= 16, C * G <= 64, P_max up to 2^30 and B * Hkv
  * below 2^26.
  * ------------------------------------------------------------------------------ */

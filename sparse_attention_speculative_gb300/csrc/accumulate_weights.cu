@@ -322,8 +322,8 @@ __device__ __forceinline__ int slice_of(const WeightsParams& a, int P, int CS) {
   return (((kHold > 0 ? a.P_max : P) + CS - 1) / CS + 31) / 32 * 32;
 }
 
-// kHold: columns whose exponentials stay in registers between the passes (the slice is one step then); 0: the slice
-// is read again.
+// kHold: columns whose exponentials stay in registers between the passes (the slice is one step
+// then); 0: the slice is read again.
 template <bool kVec, int kHold, int kThreads, int kBlocks>
 __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(const WeightsParams a) {
   constexpr int kWarps = kThreads / 32;
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(c
   __shared__ const float* column[kMaxWeightCols];
   __shared__ Stat part[kWarps][kMaxWeightCols];       // of each warp
   __shared__ Stat slices[kWMaxCluster][kMaxWeightCols];  // of each CTA of the cluster
-  __shared__ Stat whole[kMaxWeightCols];              // of the row: maximum and 1 / sum
+  __shared__ Stat whole[kMaxWeightCols];              // of the row: reference and 1 / sum
   __shared__ float factor[kHold > 0 ? kWarps : 1][kHold > 0 ? kHold : 1];
   __shared__ Block block;
   cg::cluster_group cluster = cg::this_cluster();

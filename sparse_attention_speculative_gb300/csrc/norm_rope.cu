@@ -13,7 +13,6 @@
 // between lanes, and only the sum of squares does.  A warp takes one token and a range of its
 // heads: the four angles of a lane serve all of them.  Every row is read once, straight from the
 // layer's projections, and written once, to where the attention reads it.
-#include <cstdlib>
 #include "launch.h"
 #include "ptx.cuh"
 #include "quant_rows.cuh"
@@ -282,7 +281,7 @@ __device__ __forceinline__ void turn_heads(const RopeParams& a, const Lanes<D, k
       if (normed) norm_row<D>(r, a.eps);
       r = turn_row<kPairs, kFull>(r, t, at.turned);
       if (hh < h1) {
-        uint16_t* p = dst + hh * to;
+        uint16_t* p = dst + static_cast<long long>(hh) * to;
         *reinterpret_cast<uint2*>(p + at.a) = make_uint2(narrow2(r.x[0]), narrow2(r.x[1]));
         *reinterpret_cast<uint2*>(p + at.b) = make_uint2(narrow2(r.x[2]), narrow2(r.x[3]));
       }
@@ -305,7 +304,7 @@ __device__ __forceinline__ void copy_heads(int h0, int h1, const uint16_t* src, 
     }
 #pragma unroll
     for (int i = 0; i < U; ++i)
-      if (h + i * RPI < h1) *reinterpret_cast<uint4*>(dst + (h + i * RPI) * to + at) = x[i];
+      if (h + i * RPI < h1) *reinterpret_cast<uint4*>(dst + static_cast<long long>(h + i * RPI) * to + at) = x[i];
   }
 }
 

@@ -1267,8 +1267,10 @@ vsd_status rope_checks(const vsd_geom* geom, int n, const vsd_rows* q, const vsd
   if (!std::isfinite(rope->amplitude) || !std::isfinite(rope->eps) || rope->eps < 0.f)
     return VSD_ERR_INVALID_ARG;
   if (geom->B == 0 || n == 0) return VSD_OK;
+  // (32 bits count the heads of a token, and the warps and blocks of a launch)
   const double heads = geom->Hq + 2.0 * geom->Hkv;
-  if (static_cast<double>(geom->B) * n * (heads / 2 + 1) > 2147483647.0) return VSD_ERR_UNSUPPORTED;
+  if (heads > 2147483647.0 || static_cast<double>(geom->B) * n * (heads / 2 + 1) > 2147483647.0)
+    return VSD_ERR_UNSUPPORTED;
   if (!rows_ok(q) || !pos_base || !q_out || (k != nullptr && !rows_ok(k)))
     return VSD_ERR_INVALID_ARG;
   if (!aligned(q_out, 16) || !aligned(pos_base, 4) || !aligned(rope_base, 4) ||
@@ -1370,7 +1372,7 @@ vsd_status vsd_norm_rope_append_kv_quant(const vsd_geom* geom, int n, const vsd_
   vsd_status st = rope_checks(geom, n, q, k, rope, pos_base, rope_base, n_valid, q_out, zeroed,
                               &run);
   if (st != VSD_OK || !run) return st;
-  if (2.0 * geom->B * vsd::quant_pages(n) * geom->Hkv > 2147483647.0) return VSD_ERR_UNSUPPORTED;
+  if (2.0 * geom->B * vsd::quant_pages(n) * geom->Hkv > 1073741823.0) return VSD_ERR_UNSUPPORTED;
   if (!k || !rows_ok(v) || !block_table || !aligned(block_table, 4) ||
       !quant_cache_ok(k_cache, v_cache, k_scale, v_scale))
     return VSD_ERR_INVALID_ARG;

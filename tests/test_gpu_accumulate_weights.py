@@ -181,6 +181,20 @@ def test_logits_that_are_not_finite(vsd, P_max):
 
 
 @pytest.mark.parametrize("P_max", [700, 40000])
+def test_the_largest_logits(vsd, P_max):
+    """Up to 2^127 in magnitude a logit is one like others; beyond, it counts as infinite."""
+    c = Case([P_max], P_max, R=1, C=1, G=1, Hkv=4, d=64, quant=False, seed=6)
+    c.logits[0, 0, 0, 7] = 2.0 ** 127
+    c.logits[0, 0, 1, :] = -(2.0 ** 127)
+    c.logits[0, 0, 2, :] = -3.4028234663852886e38
+    c.logits[0, 0, 3, 7] = 3.4028234663852886e38
+    got = c.call(vsd).cpu()[0] - c.weights[0]
+    assert abs(float(got[0, 7]) - 1) <= 2.0 ** -20 and float(got[0].sum()) <= 1 + 2.0 ** -18
+    assert torch.all(got[1:3] == 0)          # the block's own key has it all
+    assert torch.all(torch.isnan(got[3]))
+
+
+@pytest.mark.parametrize("P_max", [700, 40000])
 def test_every_value_nan(vsd, P_max):
     c = Case([P_max], P_max, R=1, C=1, G=1, Hkv=1, d=64, quant=False, seed=6)
     c.logits.fill_(math.nan)
