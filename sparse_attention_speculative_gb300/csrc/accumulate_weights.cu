@@ -18,6 +18,7 @@
 #include <cooperative_groups.h>
 
 #include "launch.h"
+#include "pairs.cuh"
 #include "ptx.cuh"
 #include "quant.cuh"
 
@@ -278,7 +279,7 @@ __device__ __forceinline__ void block_logits(const WeightsParams& a, int rank, i
 template <int kThreads>
 __device__ __forceinline__ void share_sums(const WeightsParams& a, int rank, int CS,
                                            const Stat (*part)[kMaxWeightCols], Block& block,
-                                           Stat (*slices)[kMaxWeightCols], Stat* whole, bool first) {
+                                           Stat (*slices)[kMaxWeightCols], float4* whole, bool first) {
   constexpr int kWarps = kThreads / 32;
   cg::cluster_group cluster = cg::this_cluster();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -310,7 +311,13 @@ __device__ __forceinline__ void share_sums(const WeightsParams& a, int rank, int
     if (col < a.cols && l16 < CS) s = slices[l16][col];
     s = join_lanes<16>(s);
     // (nothing in sight: l is 0, or NaN)
-    if (col < a.cols && l16 == 0) whole[col] = Stat{reference(s.m), s.m == -INFINITY ? s.l : 1.f / s.l};
+    const float l = s.m == -INFINITY ? s.l : 1.f / s.l, m = -reference(s.m);
+    if (col < a.cols && l16 == 0) {
+      whole[col] = make_float4(m, m, l, l);
+      if (col == 0) {  // the last group's missing columns: column 0 once more, without weight
+        for (int c = a.cols; c % kWGroup != 0; ++c) whole[c] = make_float4(m, m, 0.f, 0.f);
+      }
+    }
   }
   __syncthreads();
 }
@@ -328,10 +335,11 @@ template <bool kVec, int kHold, int kThreads, int kBlocks>
 __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(const WeightsParams a) {
   constexpr int kWarps = kThreads / 32;
   constexpr int kStep = kThreads * 4;
-  __shared__ const float* column[kMaxWeightCols];
+  // (volatile: kept in registers over the steps, eight of these would push out what is counted)
+  __shared__ const float* volatile column[kMaxWeightCols];
   __shared__ Stat part[kWarps][kMaxWeightCols];       // of each warp
   __shared__ Stat slices[kWMaxCluster][kMaxWeightCols];  // of each CTA of the cluster
-  __shared__ Stat whole[kMaxWeightCols];              // of the row: reference and 1 / sum
+  __shared__ float4 whole[kMaxWeightCols];            // of the row: -reference and 1 / sum, twice each
   __shared__ float factor[kHold > 0 ? kWarps : 1][kHold > 0 ? kHold : 1];
   __shared__ Block block;
   cg::cluster_group cluster = cg::this_cluster();
@@ -340,10 +348,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(c
   const int pair = static_cast<int>(blockIdx.x) / CS;
   const int b = pair / a.Hkv, g = pair - b * a.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (static_cast<int>(threadIdx.x) < a.cols) {
-    const int s = static_cast<int>(threadIdx.x) >> a.shift_g;
+  if (static_cast<int>(threadIdx.x) < kMaxWeightCols) {  // (those that are missing: column 0)
+    const int col = static_cast<int>(threadIdx.x) < a.cols ? static_cast<int>(threadIdx.x) : 0;
+    const int s = col >> a.shift_g;
     column[threadIdx.x] = a.logits + ((static_cast<size_t>(b) * a.C + a.slot[s]) * a.Hq + g * a.G +
-                                      (static_cast<int>(threadIdx.x) - s * a.G)) * static_cast<size_t>(a.P_max);
+                                      (col - (s << a.shift_g))) * static_cast<size_t>(a.P_max);
   }
   __syncthreads();
   ptx::pdl_wait_primary();
@@ -376,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(c
   // ---- pass 1: maximum and sum of every column over the slice
   const int pieces = block_pieces(a, rank, CS);
   Piece piece;
-  if (static_cast<int>(threadIdx.x) < pieces)
+  if (kHold > 0 && static_cast<int>(threadIdx.x) < pieces)
     piece = fetch_piece(a, b, g, P, rank, CS, threadIdx.x, piece_page(a, b, P, threadIdx.x));
   if (kHold > 0) {
     load4<kVec, kThreads>(out, lo, hi, w);
@@ -412,29 +421,36 @@ __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(c
         l[c] = 0.f;
       }
       const auto take = [&](const float (&z)[kWGroup][4]) {
+        const auto top = [&](int c) { return fmaxf(fmaxf(z[c][0], z[c][1]), fmaxf(z[c][2], z[c][3])); };
+        bool up = false;
 #pragma unroll
-        for (int c = 0; c < kWGroup; ++c) {
-          const float top = fmaxf(fmaxf(z[c][0], z[c][1]), fmaxf(z[c][2], z[c][3]));
-          if (fmaf(top, kLog2e, -m[c]) > 57.f) {
-            const float now = top * kLog2e;
+        for (int c = 0; c < kWGroup; ++c) up |= fmaf(top(c), kLog2e, -m[c]) > 57.f;
+        if (up) {
+#pragma unroll
+          for (int c = 0; c < kWGroup; ++c) {
+            const float now = fmaf(top(c), kLog2e, -m[c]) > 57.f ? top(c) * kLog2e : m[c];
             l[c] *= exp_of(m[c] - now);
             m[c] = now;
           }
-          l[c] += (exp_of(fmaf(z[c][0], kLog2e, -m[c])) + exp_of(fmaf(z[c][1], kLog2e, -m[c]))) +
-                  (exp_of(fmaf(z[c][2], kLog2e, -m[c])) + exp_of(fmaf(z[c][3], kLog2e, -m[c])));
+        }
+#pragma unroll
+        for (int c = 0; c < kWGroup; ++c) {
+          const auto e = [&](int j) { return exp_of(fmaf(z[c][j], kLog2e, -m[c])); };
+          const float2 s = parts(add2(f2(e(0), e(1)), f2(e(2), e(3))));
+          l[c] += s.x + s.y;
         }
       };
       int base = lo;
       for (; base + kStep <= hi; base += kStep) {
         float z[kWGroup][4];
 #pragma unroll
-        for (int c = 0; c < kWGroup; ++c) load4<kVec, kThreads>(column[c < nc ? c0 + c : c0], base, policy, z[c]);
+        for (int c = 0; c < kWGroup; ++c) load4<kVec, kThreads>(column[c0 + c], base, policy, z[c]);
         take(z);
       }
       if (base < hi) {
         float z[kWGroup][4];
 #pragma unroll
-        for (int c = 0; c < kWGroup; ++c) load4<kVec, kThreads>(column[c < nc ? c0 + c : c0], base, hi, z[c]);
+        for (int c = 0; c < kWGroup; ++c) load4<kVec, kThreads>(column[c0 + c], base, hi, z[c]);
 #pragma unroll
         for (int c = 0; c < kWGroup; ++c) mask4<kVec, kThreads>(base, hi, z[c]);
         take(z);
@@ -453,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(c
     }
   }
   for (int i = threadIdx.x; i < pieces; i += kThreads) {
-    if (i >= kThreads) piece = fetch_piece(a, b, g, P, rank, CS, i, piece_page(a, b, P, i));
+    if (kHold == 0 || i >= kThreads) piece = fetch_piece(a, b, g, P, rank, CS, i, piece_page(a, b, P, i));
     put_piece(a, i, piece, block);
   }
   share_sums<kThreads>(a, rank, CS, part, block, slices, whole, true);
@@ -472,8 +488,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(c
   if (kHold > 0) {
     // e^(z - M) / L = e^(z - m) (e^(m - M) / L), m the warp's maximum
     if (lane < kHold) {
-      const Stat s = whole[lane < a.cols ? lane : 0];
-      factor[warp][lane] = lane < a.cols ? exp_of(part[warp][lane].m - s.m) * s.l : 0.f;
+      const float4 s = whole[lane < a.cols ? lane : 0];
+      factor[warp][lane] = lane < a.cols ? exp_of(part[warp][lane].m + s.x) * s.z : 0.f;
     }
     __syncwarp();
     float p[4] = {0.f, 0.f, 0.f, 0.f};
@@ -492,27 +508,30 @@ __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(c
       const bool inside = base + kStep <= hi;
       if (inside) load4<kVec, kThreads>(out, base, policy, w);
       else load4<kVec, kThreads>(out, base, hi, w);
-      float p[4] = {0.f, 0.f, 0.f, 0.f};
+      F2 p[2] = {0ull, 0ull};
       for (int q = groups - 1; q >= 0; --q) {
-        const int c0 = q * kWGroup, nc = min(kWGroup, a.cols - c0);
+        const int c0 = q * kWGroup;
         float z[kWGroup][4];
         if (inside) {
 #pragma unroll
-          for (int c = 0; c < kWGroup; ++c) load4<kVec, kThreads>(column[c < nc ? c0 + c : c0], base, policy, z[c]);
+          for (int c = 0; c < kWGroup; ++c) load4<kVec, kThreads>(column[c0 + c], base, policy, z[c]);
         } else {
 #pragma unroll
-          for (int c = 0; c < kWGroup; ++c) load4<kVec, kThreads>(column[c < nc ? c0 + c : c0], base, hi, z[c]);
+          for (int c = 0; c < kWGroup; ++c) load4<kVec, kThreads>(column[c0 + c], base, hi, z[c]);
         }
 #pragma unroll
         for (int c = 0; c < kWGroup; ++c) {
-          if (c < nc) {
-            const Stat s = whole[c0 + c];
+          const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(&whole[c0 + c]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) p[j] = fmaf(exp_of(fmaf(z[c][j], kLog2e, -s.m)), s.l, p[j]);
+          for (int j = 0; j < 2; ++j) {
+            const float2 t = parts(fma2(f2(z[c][2 * j], z[c][2 * j + 1]), f2(kLog2e, kLog2e), s.x));
+            p[j] = fma2(f2(exp_of(t.x), exp_of(t.y)), s.y, p[j]);
           }
         }
       }
-      add(base, p);
+      const float2 p0 = parts(p[0]), p1 = parts(p[1]);
+      const float sums[4] = {p0.x, p0.y, p1.x, p1.y};
+      add(base, sums);
     }
   }
 }

@@ -14,6 +14,7 @@
 // heads: the four angles of a lane serve all of them.  Every row is read once, straight from the
 // layer's projections, and written once, to where the attention reads it.
 #include "launch.h"
+#include "pairs.cuh"
 #include "ptx.cuh"
 #include "quant_rows.cuh"
 
@@ -71,33 +72,6 @@ struct RopeParams {
 };
 
 // ---------------------------------------------------------------- pairs of floats
-// (one instruction for two; the row arithmetic is what bounds these kernels beside the reading)
-using F2 = unsigned long long;
-
-__device__ __forceinline__ F2 f2(float lo, float hi) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-
-__device__ __forceinline__ float2 parts(F2 x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 __device__ __forceinline__ F2 widen2(uint32_t w) { return f2(bf16_lo(w), bf16_hi(w)); }
 
 __device__ __forceinline__ uint32_t narrow2(F2 x) {
