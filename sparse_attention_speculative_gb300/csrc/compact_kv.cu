@@ -132,18 +132,34 @@ __global__ void __launch_bounds__(kCThreads) compact_kernel(const CompactParams 
     const int blk1 = block_of(j1, page + step), to1 = place_of(page + step);
     float top = 0.f;
     if (kQuant) {
+      // Codes times s / top.  By a power of two from 2^-15 on that is exact in halves, two codes at a
+      // time, before the one rounding back; anything else goes through fp32.
       top = warp_max_f32(s);
-      const float ratio = s == top ? 1.f : __fdiv_rn(s, top);
+      const float ratio = s == top || from < 0 ? 1.f : __fdiv_rn(s, top);
+      const bool power = (__float_as_uint(ratio) & 0x007FFFFFu) == 0u && ratio >= 0x1p-15f;
+      if (__all_sync(0xffffffffu, power)) {
+        if (__any_sync(0xffffffffu, ratio != 1.f)) {
 #pragma unroll
-      for (int r = 0; r < NI; ++r) {
-        const float f = __shfl_sync(0xffffffffu, ratio, r * RPI + sub);
-        if (f != 1.f) {
+          for (int r = 0; r < NI; ++r) {
+            const __half2 f = __float2half2_rn(__shfl_sync(0xffffffffu, ratio, r * RPI + sub));
+            const auto two = [f](uint32_t c) {
+              const uint32_t h = e4m3x2_to_f16x2(c);
+              return pack_e4m3x2_h(__hmul2(*reinterpret_cast<const __half2*>(&h), f));
+            };
+            const auto four = [&](uint32_t c) { return two(c & 0xFFFFu) | two(c >> 16) << 16; };
+            x[r] = make_uint4(four(x[r].x), four(x[r].y), four(x[r].z), four(x[r].w));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < NI; ++r) {
+          const float f = __shfl_sync(0xffffffffu, ratio, r * RPI + sub);
           const auto two = [f](uint32_t c) {
             const float2 v = e4m3x2_to_float2(c);
             return pack_e4m3x2(__fmul_rn(v.x, f), __fmul_rn(v.y, f));
           };
           const auto four = [&](uint32_t c) { return two(c & 0xFFFFu) | two(c >> 16) << 16; };
-          x[r] = make_uint4(four(x[r].x), four(x[r].y), four(x[r].z), four(x[r].w));
+          if (f != 1.f) x[r] = make_uint4(four(x[r].x), four(x[r].y), four(x[r].z), four(x[r].w));
         }
       }
     }
