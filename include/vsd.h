@@ -705,8 +705,9 @@ vsd_status vsd_sparse_decode_attn_quant(const vsd_geom* geom, const void* q,
  *   in between).  A sequence whose range is refused stores nothing; its q_out is written.
  *
  * Supported: head_dim 64 or 128, rot_dim a multiple of 8 up to head_dim (0: no rotation, turns
- * may be NULL), B * n * (Hq + 2 Hkv + 2) / 2 below 2^31 and, into an 8-bit cache, B * Hkv *
- * (n / 16 + 2) below 2^29.  All are programmatic dependents of the preceding kernel on the stream.
+ * may be NULL), Hq + 2 Hkv up to 2^19, B * n * (Hq + 2 Hkv + 2) / 2 below 2^31 and, into an
+ * 8-bit cache, B * Hkv * (n / 16 + 2) below 2^29.  All are programmatic dependents of the
+ * preceding kernel on the stream.
  * ------------------------------------------------------------------------------ */
 typedef struct vsd_rows {
   const void* data;

@@ -222,7 +222,8 @@ __device__ __forceinline__ uint32_t angle_of(long long p, long long turns) {
 }
 
 // ---------------------------------------------------------------- tokens
-// Rows of one kind: heads [h0, h1) of a token, from src + head * from to dst + head * to.
+// Rows of one kind: heads [h0, h1) of a token, from src + head * from to dst + head * to (within 32
+// bits: a token has at most 2^19 heads).
 template <int D, bool kPairs, bool kFull>
 __device__ __forceinline__ void turn_heads(const RopeParams& a, const Lanes<D, kPairs>& at, const float (&c)[4],
                                            const float (&s)[4], const uint16_t* weight, int h0, int h1,
@@ -255,7 +256,7 @@ __device__ __forceinline__ void turn_heads(const RopeParams& a, const Lanes<D, k
       if (normed) norm_row<D>(r, a.eps);
       r = turn_row<kPairs, kFull>(r, t, at.turned);
       if (hh < h1) {
-        uint16_t* p = dst + static_cast<long long>(hh) * to;
+        uint16_t* p = dst + hh * to;
         *reinterpret_cast<uint2*>(p + at.a) = make_uint2(narrow2(r.x[0]), narrow2(r.x[1]));
         *reinterpret_cast<uint2*>(p + at.b) = make_uint2(narrow2(r.x[2]), narrow2(r.x[3]));
       }
@@ -278,7 +279,7 @@ __device__ __forceinline__ void copy_heads(int h0, int h1, const uint16_t* src, 
     }
 #pragma unroll
     for (int i = 0; i < U; ++i)
-      if (h + i * RPI < h1) *reinterpret_cast<uint4*>(dst + static_cast<long long>(h + i * RPI) * to + at) = x[i];
+      if (h + i * RPI < h1) *reinterpret_cast<uint4*>(dst + (h + i * RPI) * to + at) = x[i];
   }
 }
 

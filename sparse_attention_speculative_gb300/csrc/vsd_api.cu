@@ -1267,9 +1267,9 @@ vsd_status rope_checks(const vsd_geom* geom, int n, const vsd_rows* q, const vsd
   if (!std::isfinite(rope->amplitude) || !std::isfinite(rope->eps) || rope->eps < 0.f)
     return VSD_ERR_INVALID_ARG;
   if (geom->B == 0 || n == 0) return VSD_OK;
-  // (32 bits count the heads of a token, and the warps and blocks of a launch)
+  // (32 bits count the values of a token in a cache's block, and the warps and blocks of a launch)
   const double heads = geom->Hq + 2.0 * geom->Hkv;
-  if (heads > 2147483647.0 || static_cast<double>(geom->B) * n * (heads / 2 + 1) > 2147483647.0)
+  if (heads > 524288.0 || static_cast<double>(geom->B) * n * (heads / 2 + 1) > 2147483647.0)
     return VSD_ERR_UNSUPPORTED;
   if (!rows_ok(q) || !pos_base || !q_out || (k != nullptr && !rows_ok(k)))
     return VSD_ERR_INVALID_ARG;

@@ -112,6 +112,7 @@ def test_row_calls(lib, p, call):  # noqa: F811
     assert call(lib, geom(), p, z=4) == -1
     assert call(lib, geom(), p, n=-1) == -1
     assert call(lib, geom(B=2 ** 16), p, n=2 ** 16) == -2      # more warps than 32 bits count
+    assert call(lib, geom(Hq=2 ** 19), p, n=1) == -2            # more heads than a token may have
     assert call(lib, geom(), p, n=0, q=None) == 0              # nothing to do: no device needed
     assert call(lib, geom(B=0), p, q=None) == 0
 
