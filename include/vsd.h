@@ -694,7 +694,8 @@ vsd_status vsd_sparse_decode_attn_quant(const vsd_geom* geom, const void* q,
  *           VSD_DEV_BAD_LENGTH and counts as 0.  Rows behind it are not read; those of q_out
  *           (k_out) are left as they were, or become zeros with VSD_ROPE_ZEROED_Q (_K)
  *   q_out, k_out  bf16 [B][n][Hq or Hkv][head_dim].  q_out may be q's own memory where q is
- *           contiguous (k_out k's)
+ *           contiguous (k_out k's); memory that overlaps the rows in any other way is refused
+ *           (VSD_ERR_INVALID_ARG)
  *
  * vsd_norm_rope: q and, unless it is NULL, k.  geom's page_size, max_blocks_per_seq and
  *   num_blocks are not used.
@@ -802,7 +803,8 @@ vsd_status vsd_accumulate_weights_quant(const vsd_geom* geom, int R, int C, cons
  *              block_table itself) or a page that no sequence of the call reads; no page is
  *              written for two sequences.  Rows at n and beyond stay as they were
  *   weights, weights_out  fp32 [B][Hkv][stride] each, both or neither NULL; weights_out may be
- *              weights (with one stride); weights_out_stride >= k_max
+ *              weights (with one stride), and does not overlap it otherwise
+ *              (VSD_ERR_INVALID_ARG); weights_out_stride >= k_max
  *   8-bit cache  a destination page takes the largest scale of the rows that come into it, and
  *              codes of a smaller one become e4m3(code * (scale / largest)) (exact down to
  *              e4m3's subnormals where scales are powers of two)
@@ -811,6 +813,8 @@ vsd_status vsd_accumulate_weights_quant(const vsd_geom* geom, int R, int C, cons
  * VSD_DEV_BAD_LENGTH and that list moves nothing (its weights_out stays too); a source or
  * destination entry outside the cache is flagged VSD_DEV_BAD_BLOCK and its rows are not
  * written.  weights_out of a row whose index or source is refused becomes 0.
+ * A call that follows directly must not fetch rows before it waits (VSD_VERIFY_EARLY_PREFETCH,
+ * VSD_STEP_EARLY_GATHER, VSD_SPARSE_VERIFY_EARLY_GATHER): this one writes the rows below its prefix.
  * Supported: head_dim 64 or 128, B * Hkv below 2^26.  Programmatic dependents of the preceding
  * kernel.
  * ------------------------------------------------------------------------------ */

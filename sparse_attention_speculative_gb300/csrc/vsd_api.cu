@@ -1249,6 +1249,39 @@ bool rows_ok(const vsd_rows* r) {
          r->row_stride % 8 == 0 && r->head_stride % 8 == 0;
 }
 
+// The memory [first, last) that rows (or an output of them) lie in.
+struct Extent {
+  const char* first = nullptr;
+  const char* last = nullptr;
+  bool meets(const Extent& o) const { return first < o.last && o.first < last; }
+};
+
+Extent rows_extent(const vsd_rows* r, int B, int n, int heads, int d) {
+  Extent e;
+  if (r == nullptr) return e;
+  long long lo = 0, hi = d;
+  const long long steps[3] = {(B - 1ll) * r->batch_stride, (n - 1ll) * r->row_stride, (heads - 1ll) * r->head_stride};
+  for (long long s : steps) (s < 0 ? lo : hi) += s;
+  e.first = static_cast<const char*>(r->data) + 2 * lo;
+  e.last = static_cast<const char*>(r->data) + 2 * hi;
+  return e;
+}
+
+Extent output_extent(const void* out, int B, int n, int heads, int d) {
+  Extent e;
+  e.first = static_cast<const char*>(out);
+  if (out != nullptr) e.last = e.first + 2ull * B * n * heads * d;
+  return e;
+}
+
+// May an output be written where its rows are read: in no part, or each row in its own place.
+bool own_place_or_none(const vsd_rows* r, const Extent& rows, const void* out, const Extent& at, int B, int n,
+                       int heads, int d) {
+  if (!rows.meets(at)) return true;
+  return r->data == out && (heads == 1 || r->head_stride == d) && (n == 1 || r->row_stride == 1ll * heads * d) &&
+         (B == 1 || r->batch_stride == 1ll * n * heads * d);
+}
+
 vsd::StridedRows rows_of(const vsd_rows* r) {
   return vsd::StridedRows{r->data, r->batch_stride, r->row_stride, r->head_stride};
 }
@@ -1277,6 +1310,11 @@ vsd_status rope_checks(const vsd_geom* geom, int n, const vsd_rows* q, const vsd
       !aligned(n_valid, 4) || !aligned(rope->q_weight, 16) || !aligned(rope->k_weight, 16))
     return VSD_ERR_INVALID_ARG;
   if (rope->rot_dim > 0 && (!rope->turns || !aligned(rope->turns, 8))) return VSD_ERR_INVALID_ARG;
+  const int B = geom->B, d = geom->head_dim;
+  const Extent at = output_extent(q_out, B, n, geom->Hq, d), keys = rows_extent(k, B, n, geom->Hkv, d);
+  if (keys.meets(at) ||
+      !own_place_or_none(q, rows_extent(q, B, n, geom->Hq, d), q_out, at, B, n, geom->Hq, d))
+    return VSD_ERR_INVALID_ARG;
   *run = true;
   return VSD_OK;
 }
@@ -1327,7 +1365,14 @@ vsd_status vsd_norm_rope(const vsd_geom* geom, int n, const vsd_rows* q, const v
   bool run = false;
   vsd_status st = rope_checks(&g, n, q, k, rope, pos_base, nullptr, n_valid, q_out, zeroed, &run);
   if (st != VSD_OK || !run) return st;
-  if (k != nullptr && (!k_out || !aligned(k_out, 16))) return VSD_ERR_INVALID_ARG;
+  if (k != nullptr) {
+    if (!k_out || !aligned(k_out, 16)) return VSD_ERR_INVALID_ARG;
+    const Extent at = output_extent(k_out, g.B, n, g.Hkv, g.head_dim);
+    if (at.meets(output_extent(q_out, g.B, n, g.Hq, g.head_dim)) ||
+        at.meets(rows_extent(q, g.B, n, g.Hq, g.head_dim)) ||
+        !own_place_or_none(k, rows_extent(k, g.B, n, g.Hkv, g.head_dim), k_out, at, g.B, n, g.Hkv, g.head_dim))
+      return VSD_ERR_INVALID_ARG;
+  }
   vsd::RopeArgs a;
   st = rope_args(&g, n, q, k, rope, pos_base, pos_offset, nullptr, n_valid, q_out, zeroed, &a);
   if (st != VSD_OK) return st;
@@ -1348,6 +1393,9 @@ vsd_status vsd_norm_rope_append_kv(const vsd_geom* geom, int n, const vsd_rows* 
   if (st != VSD_OK || !run) return st;
   if (!k || !rows_ok(v) || !block_table || !k_cache || !v_cache || !aligned(block_table, 4) ||
       !aligned(k_cache, 16) || !aligned(v_cache, 16))
+    return VSD_ERR_INVALID_ARG;
+  if (rows_extent(v, geom->B, n, geom->Hkv, geom->head_dim)
+          .meets(output_extent(q_out, geom->B, n, geom->Hq, geom->head_dim)))
     return VSD_ERR_INVALID_ARG;
   vsd::RopeArgs a;
   st = rope_args(geom, n, q, k, rope, pos_base, pos_offset, rope_base, n_valid, q_out, zeroed, &a);
@@ -1375,6 +1423,9 @@ vsd_status vsd_norm_rope_append_kv_quant(const vsd_geom* geom, int n, const vsd_
   if (2.0 * geom->B * vsd::quant_pages(n) * geom->Hkv > 1073741823.0) return VSD_ERR_UNSUPPORTED;
   if (!k || !rows_ok(v) || !block_table || !aligned(block_table, 4) ||
       !quant_cache_ok(k_cache, v_cache, k_scale, v_scale))
+    return VSD_ERR_INVALID_ARG;
+  if (rows_extent(v, geom->B, n, geom->Hkv, geom->head_dim)
+          .meets(output_extent(q_out, geom->B, n, geom->Hq, geom->head_dim)))
     return VSD_ERR_INVALID_ARG;
   vsd::RopeArgs a;
   st = rope_args(geom, n, q, k, rope, pos_base, pos_offset, rope_base, n_valid, q_out, zeroed, &a);
@@ -1462,6 +1513,12 @@ vsd_status compact_call(const vsd_geom* geom, const int32_t* block_table,
   if (static_cast<long long>(geom->B) * geom->Hkv >= kMaxPairs || k_max > kMaxPositions)
     return VSD_ERR_UNSUPPORTED;
   if (geom->B == 0) return VSD_OK;
+  if (weights != weights_out) {  // (in place, or apart)
+    const double lists = static_cast<double>(geom->B) * geom->Hkv;
+    const uintptr_t in = reinterpret_cast<uintptr_t>(weights), out = reinterpret_cast<uintptr_t>(weights_out);
+    if (in < out ? out - in < lists * weights_stride * 4 : in - out < lists * weights_out_stride * 4)
+      return VSD_ERR_INVALID_ARG;
+  }
   if (!block_table || !dst_table || !prefix_len || !n_sel || !k_cache || !v_cache ||
       (k_max > 0 && !idx))
     return VSD_ERR_INVALID_ARG;

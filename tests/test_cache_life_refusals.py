@@ -19,8 +19,11 @@ class Rope(ctypes.Structure):
                 ("eps", ctypes.c_float)]
 
 
-def rows(p, batch=4096, row=4096, head=128):  # noqa: F811
-    return Rows(p.value if p is not None else None, batch, row, head)
+FAR = 1 << 30   # (addresses that nothing reads: the checks come before any use)
+
+
+def rows(p, batch=16384, row=4096, head=128):  # noqa: F811
+    return Rows(p.value + FAR if p is not None else None, batch, row, head)
 
 
 def rope(p, **kw):  # noqa: F811
@@ -34,21 +37,21 @@ def ref_of(x):
 
 
 def norm(lib, g, p, n=4, **kw):  # noqa: F811
-    a = dict(q=rows(p), k=rows(p), r=rope(p), pos=p, nv=None, qo=p, ko=p, z=0)
+    a = dict(q=rows(p), k=rows(off(p, 1 << 20)), r=rope(p), pos=p, nv=None, qo=p, ko=off(p, 1 << 20), z=0)
     a.update(kw)
     return lib.vsd_norm_rope(g, n, ref_of(a["q"]), ref_of(a["k"]), ref_of(a["r"]), a["pos"], 0, a["nv"], a["qo"],
                              a["ko"], a["z"], None)
 
 
 def store(lib, g, p, n=4, **kw):  # noqa: F811
-    a = dict(q=rows(p), k=rows(p), v=rows(p), r=rope(p), bt=p, pos=p, rb=None, nv=None, qo=p, z=0, kc=p, vc=p)
+    a = dict(q=rows(p), k=rows(off(p, 1 << 20)), v=rows(off(p, 2 << 20)), r=rope(p), bt=p, pos=p, rb=None, nv=None, qo=p, z=0, kc=p, vc=p)
     a.update(kw)
     return lib.vsd_norm_rope_append_kv(g, n, ref_of(a["q"]), ref_of(a["k"]), ref_of(a["v"]), ref_of(a["r"]), a["bt"],
                                        a["pos"], 0, a["rb"], a["nv"], a["qo"], a["z"], a["kc"], a["vc"], None)
 
 
 def store_quant(lib, g, p, n=4, **kw):  # noqa: F811
-    a = dict(q=rows(p), k=rows(p), v=rows(p), r=rope(p), bt=p, pos=p, rb=None, nv=None, qo=p, z=0, kc=p, vc=p, ks=p,
+    a = dict(q=rows(p), k=rows(off(p, 1 << 20)), v=rows(off(p, 2 << 20)), r=rope(p), bt=p, pos=p, rb=None, nv=None, qo=p, z=0, kc=p, vc=p, ks=p,
              vs=p)
     a.update(kw)
     return lib.vsd_norm_rope_append_kv_quant(g, n, ref_of(a["q"]), ref_of(a["k"]), ref_of(a["v"]), ref_of(a["r"]),
@@ -66,7 +69,7 @@ def weights(lib, g, p, R=4, which=(0, 3), P_max=512, scale=0.1, stride=512, quan
 
 
 def compact(lib, g, p, dst=16, heads=1, k=64, ws=512, wos=512, quant=False, **kw):  # noqa: F811
-    a = dict(bt=p, dt=p, pl=p, idx=p, ns=p, kc=p, vc=p, ks=p, vs=p, w=p, wo=off(p, 1024))
+    a = dict(bt=p, dt=p, pl=p, idx=p, ns=p, kc=p, vc=p, ks=p, vs=p, w=p, wo=off(p, 1 << 20))
     a.update(kw)
     head = (g, a["bt"], a["dt"], dst, a["pl"], a["idx"], a["ns"], heads, k, a["kc"], a["vc"])
     tail = (a["w"], ws, a["wo"], wos, None)
@@ -117,6 +120,25 @@ def test_row_calls(lib, p, call):  # noqa: F811
     assert call(lib, geom(B=0), p, q=None) == 0
 
 
+def test_outputs_that_overlap_rows(lib, p):  # noqa: F811
+    """Refused, but for each row's own place.  (Zero rows of a bad count show what passed: the next check.)"""
+    def call(**kw):
+        return norm(lib, geom(Hq=32, Hkv=8), p, n=4, **kw)
+    at = p.value + FAR
+    for qo in (at - 16, at + 16, at + 4 * 4096 * 2 - 16, at - 4 * 4096 * 2 + 16):
+        assert call(qo=ctypes.c_void_p(qo)) == -1
+    # its own place: passes (and fails where there is no GPU, or is not run there: a null k_out is next)
+    assert call(qo=ctypes.c_void_p(at), ko=None) == -1
+    for bad in (rows(p, row=6144), rows(p, head=0), rows(p, head=256, row=8192)):
+        assert call(q=bad, qo=ctypes.c_void_p(at)) == -1
+    kat = at + (1 << 20)
+    for ko in (kat + 16, kat - 16, at, p.value, p.value + 16):
+        assert call(k=rows(off(p, 1 << 20), row=1024), ko=ctypes.c_void_p(ko)) == -1
+    assert call(qo=ctypes.c_void_p(kat)) == -1                       # the queries over the keys
+    assert store(lib, geom(), p, qo=ctypes.c_void_p(at + (2 << 20))) == -1      # over the values
+    assert store_quant(lib, geom(), p, qo=ctypes.c_void_p(at + (2 << 20) + 64)) == -1
+
+
 def test_norm_rope_needs_no_cache(lib, p):  # noqa: F811
     assert norm(lib, geom(page_size=0, num_blocks=0, max_blocks_per_seq=0, B=0), p) == 0
     assert norm(lib, geom(head_dim=96), p) == -2
@@ -162,6 +184,8 @@ def test_compact_call(lib, p, quant):  # noqa: F811
     assert call(w=None) == -1 and call(wo=None) == -1
     assert call(wos=63) == -1 and call(ws=-1) == -1
     assert call(wo=p, ws=512, wos=256) == -1                    # in place with two strides
+    for d in (4, 8 * 512 * 4 - 4):
+        assert call(wo=off(p, d)) == -1 and call(w=off(p, d), wo=p) == -1      # partly over each other
     assert call(heads=2) == -1 and call(heads=0) == -1
     assert call(k=-1) == -1 and call(dst=-1) == -1
     assert call(k=2 ** 30 + 1, wos=2 ** 31 - 1) == -2

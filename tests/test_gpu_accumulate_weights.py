@@ -130,6 +130,20 @@ def test_long_slices(vsd, P_max, prefix):
     c.check(c.call(vsd), (0, 1))
 
 
+@pytest.mark.parametrize("P_max,stride", [(32, 35), (700, 701), (40000, 40001)])
+def test_strides_and_addresses_that_vectors_do_not_fit(vsd, P_max, stride):
+    """Row strides or bases off 16 bytes: values one by one, the same sums."""
+    c = Case([P_max - 1, 5], P_max, R=2, C=2, G=2, Hkv=2, d=64, quant=False, seed=2, stride=stride)
+    c.check(c.call(vsd), (0, 1))
+    c = Case([P_max - 1, 5], P_max, R=2, C=2, G=2, Hkv=2, d=64, quant=False, seed=2, stride=P_max)
+    c.check(c.call(vsd), (0, 1))
+    for off in (1, 2, 3):
+        lg = torch.empty(c.logits.numel() + 4, device="cuda")[off:off + c.logits.numel()].view(c.logits.shape).copy_(c.logits)
+        w = torch.empty(c.weights.numel() + 4, device="cuda")[off:off + c.weights.numel()].view(c.weights.shape).copy_(c.weights)
+        c.check(c.call(vsd, logits=lg), (0, 1))
+        c.check(c.call(vsd, weights=w), (0, 1))
+
+
 def test_chosen_rows(vsd):
     c = Case([300, 40], 300, R=5, C=2, G=4, Hkv=2, d=64, quant=False, seed=3)
     for rows in ((0, 4), (3, 1), (-1, 2), (4, -1), (2, 2)):

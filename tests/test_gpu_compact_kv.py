@@ -269,5 +269,8 @@ def test_mismatched_tensors(vsd):
     for kw in (dict(kc=kc.float()), dict(idx=idx.long()), dict(weights=w.double()), dict(dst=None)):
         with pytest.raises(TypeError):
             call(**kw)
+    apart = torch.zeros(200, device="cuda")
+    with pytest.raises(vsd.VsdError):                 # partly over each other
+        call(weights=apart[:60].view(1, 2, 30), weights_out=apart[50:110].view(1, 2, 30))
     with pytest.raises(vsd.VsdError):                 # one buffer, two strides
         call(weights=w, weights_out=w.view(-1)[:2 * 16].view(1, 2, 16))

@@ -127,6 +127,19 @@ def test_queries_alone_and_in_place(vsd):
     assert torch.equal(both[0], alone)
     q, k = vsd.vsd_norm_rope(gpu[0], gpu[1], turns, int32([3, 4]), q_out=gpu[0], k_out=gpu[1])
     assert q.data_ptr() == gpu[0].data_ptr() and torch.equal(q, both[0]) and torch.equal(k, both[1])
+    # one token's projection: its parts are contiguous, and may be turned where they are
+    x = torch.randn((1, 1, 12, 64), generator=g).to(torch.bfloat16)
+    y = x.cuda()
+    want = vsd.vsd_norm_rope(y[:, :, :8], y[:, :, 8:10], turns, int32([9]))
+    vsd.vsd_norm_rope(y[:, :, :8], y[:, :, 8:10], turns, int32([9]), q_out=y[:, :, :8], k_out=y[:, :, 8:10])
+    assert torch.equal(y[:, :, :8], want[0]) and torch.equal(y[:, :, 8:10], want[1]) and torch.equal(y[:, :, 10:].cpu(), x[:, :, 10:])
+    # other memory of the rows is refused
+    y = torch.zeros((2, 4, 12, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(vsd.VsdError):
+        vsd.vsd_norm_rope(y[:, :, :8], None, turns, int32([3, 4]), q_out=y.view(-1)[:2 * 4 * 8 * 64].view(2, 4, 8, 64))
+    with pytest.raises(vsd.VsdError):
+        vsd.vsd_norm_rope(y.view(-1)[:2 * 4 * 4 * 64].view(2, 4, 4, 64), None, turns, int32([3, 4]),
+                          q_out=y.view(-1)[64:2 * 4 * 4 * 64 + 64].view(2, 4, 4, 64))
     # one row for all: strides of 0
     one = cpu[0][:1, :1].cuda().expand(2, 4, 8, 64)
     many = vsd.vsd_norm_rope(one, None, turns, int32([3, 4]))[0]
