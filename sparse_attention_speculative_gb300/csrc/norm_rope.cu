@@ -10,18 +10,19 @@
 //
 // How: a row lies in d / 8 lanes, each with the two halves of four pairs (8 bytes each, or 16
 // next to each other where pairs are interleaved), so that the rotation needs no exchange
-// between lanes, and only the sum of squares does.  A warp takes one token and a range of its
-// heads: the four angles of a lane serve all of them.  Every row is read once, straight from the
+// between lanes, and only the sum of squares does.  A warp takes a token's heads, or a part of
+// them; the token's angles are found once, by one of its warps, in the time of the first rows'
+// way, and reach the others through shared memory.  Every row is read once, straight from the
 // layer's projections, and written once, to where the attention reads it.
 //   An 8-bit page needs the maximum of its rows before the first code, so there a warp takes a page
 // and a head, its turned rows in shared memory in between.
 //
-// What bounds it: HBM, for a prompt (32768 tokens of 32 + 8 + 8 heads of 128: 805 MB in 128.6 us,
-// 0.92 of the copy rate; 196 us before two values went through one instruction and weights and
-// angles were joined).  4096 tokens into an 8-bit cache take 26 us (92 MB, 0.52): 2.7 waves of
-// blocks whose loads wait in turn.  One token of 16 sequences is a launch, 2.8 us.  Rows loaded
-// a step ahead made the prompt slower (138 us: fewer warps an SM), and so did loads before the
-// angles (143).
+// What bounds it: HBM, for a prompt (32768 tokens of 32 + 8 + 8 heads of 128: 805 MB in 123 us,
+// 0.96 of the copy rate; 129 us with every lane finding its four angles before its first rows,
+// 196 us before two values went through one instruction and weights and angles were joined).
+// 4096 tokens into an 8-bit cache take 25 us (92 MB, 0.54; 26): the queries alone 14.5 (21.7), the
+// pages, whose blocks leave an SM 20 warps, the rest.  One token of 16 sequences is a launch,
+// 2.6 us (2.85).  Rows loaded a step ahead made the prompt slower (138 us: fewer warps an SM).
 #include "launch.h"
 #include "pairs.cuh"
 #include "ptx.cuh"
@@ -72,9 +73,12 @@ struct RopeParams {
   unsigned zeroed;
   int heads;          // of a token in token_rows: q's alone, with k's, or with k's and v's
   int chunk;          // heads of a warp
-  Divisor chunks;     // warps of a token
+  int token_warps;    // warps of a token in a block
+  int block_tokens;   // tokens of a block
+  Divisor parts;      // blocks of a token (or of block_tokens of them)
   Divisor by_n;
-  unsigned tasks;     // B * n * chunks
+  unsigned tokens;    // B * n
+  unsigned token_blocks;
   int pages;          // 8-bit cache: pages that n rows of one sequence can meet
   int head_groups;    // ... heads of a page in blocks of kRopeWarps
   unsigned page_blocks;  // ... and blocks of pages, 2 * B * pages * head_groups
@@ -231,20 +235,26 @@ __device__ __forceinline__ uint32_t angle_of(long long p, long long turns) {
 }
 
 // ---------------------------------------------------------------- tokens
+// Cosines and sines of a block's tokens.
+constexpr uint32_t kAnglesBar = 1;
+template <int D>
+struct TokenAngles {
+  float c[kRopeWarps][D / 2], s[kRopeWarps][D / 2];
+};
+
 // Rows of one kind: heads [h0, h1) of a token, from src + head * from to dst + head * to (within 32
-// bits: a token has at most 2^19 heads).
-template <int D, bool kPairs, bool kFull>
-__device__ __forceinline__ void turn_heads(const RopeParams& a, const Lanes<D, kPairs>& at, const float (&c)[4],
-                                           const float (&s)[4], const uint16_t* weight, int h0, int h1,
-                                           const uint16_t* src, long long from, uint16_t* dst, int to) {
+// bits: a token has at most 2^19 heads).  angles(c, s): the token's, asked for once the first rows
+// are on their way.
+template <int D, bool kPairs, bool kFull, typename F>
+__device__ __forceinline__ void turn_heads(const RopeParams& a, const Lanes<D, kPairs>& at, F&& angles,
+                                           const uint16_t* weight, int h0, int h1, const uint16_t* src,
+                                           long long from, uint16_t* dst, int to) {
   constexpr int RPI = 32 / (D / 8);  // rows of a warp instruction
   constexpr int U = 4;               // instructions in flight
   const int sub = (threadIdx.x & 31) / (D / 8);
   const bool normed = weight != nullptr;
-  Turn t;
-  bool have = false;
-  for (int h = h0; h < h1; h += U * RPI) {
-    uint2 x[U], y[U];
+  uint2 x[U], y[U];
+  const auto load = [&](int h) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int hh = h + i * RPI + sub;
@@ -252,11 +262,16 @@ __device__ __forceinline__ void turn_heads(const RopeParams& a, const Lanes<D, k
       x[i] = ldg_stream8(p + at.a);
       y[i] = ldg_stream8(p + at.b);
     }
-    if (!have) {  // (while the first rows are on their way)
-      t = turn_of<kPairs>(c, s);
-      if (normed) weigh<kPairs>(t, weight_row(weight, at));
-      have = true;
-    }
+  };
+  load(h0);
+  Turn t;
+  {
+    float c[4], s[4];
+    angles(c, s);
+    t = turn_of<kPairs>(c, s);
+    if (normed) weigh<kPairs>(t, weight_row(weight, at));
+  }
+  for (int h = h0;;) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       if (h + i * RPI >= h1) break;  // (the warp together)
@@ -270,6 +285,9 @@ __device__ __forceinline__ void turn_heads(const RopeParams& a, const Lanes<D, k
         *reinterpret_cast<uint2*>(p + at.b) = make_uint2(narrow2(r.x[2]), narrow2(r.x[3]));
       }
     }
+    h += U * RPI;
+    if (h >= h1) break;
+    load(h);
   }
 }
 
@@ -292,81 +310,106 @@ __device__ __forceinline__ void copy_heads(int h0, int h1, const uint16_t* src, 
   }
 }
 
-// One warp's rows: a range of the heads of one token.  kCache: k and v go to the bf16 cache.
+// A block's rows: of a few tokens, or of a part of one's heads; a warp has a range of the heads of
+// one.  The angles of a token are found once, by its first warp in the block, while the rows are on
+// their way.  kCache: k and v go to the bf16 cache.
 template <int D, bool kPairs, bool kFull, bool kCache>
-__device__ __forceinline__ void token_rows(const RopeParams& a, unsigned task) {
-  const int lane = threadIdx.x & 31;
-  const unsigned bt = a.chunks(task);
-  const int h0 = static_cast<int>(task - bt * a.chunks.d) * a.chunk;
-  const int h1 = min(h0 + a.chunk, a.heads);
-  const int b = static_cast<int>(a.by_n(bt));
-  const int t = static_cast<int>(bt - static_cast<unsigned>(b) * a.n);
-  const long long pos = static_cast<long long>(__ldcg(a.rope_base + b)) + a.pos_offset + t;
-  int count = a.n_valid != nullptr ? __ldcg(a.n_valid + b) : a.n;
-  if (count < 0 || count > a.n) {
-    if (lane == 0) flag_status(a.status, VSD_DEV_BAD_LENGTH);
-    count = 0;
+__device__ __forceinline__ void token_rows(const RopeParams& a, unsigned block, TokenAngles<D>& own) {
+  const int lane = threadIdx.x & 31, warp = static_cast<int>(threadIdx.x >> 5);
+  const unsigned group = a.parts(block);
+  int mine = 0, part = warp;  // token of the block, and part of its heads
+  while (part >= a.token_warps) {
+    part -= a.token_warps;
+    ++mine;
   }
+  const bool leads = part == 0;
+  part += static_cast<int>(block - group * a.parts.d) * kRopeWarps;
+  const unsigned bt = group * a.block_tokens + mine;
+  const int h0 = min(part * a.chunk, a.heads), h1 = min(h0 + a.chunk, a.heads);
+  bool there = mine < a.block_tokens && bt < a.tokens;
+  const int b = there ? static_cast<int>(a.by_n(bt)) : 0;
+  const int t = static_cast<int>(bt - static_cast<unsigned>(b) * a.n);
+  long long pos = 0;
   // this warp's heads of q, of k and of v, each counted from 0
   const int q0 = min(h0, a.Hq), q1 = min(h1, a.Hq);
   const int k0 = max(h0 - a.Hq, 0), k1 = min(h1 - a.Hq, a.Hkv);
   const int v0 = max(h0 - a.Hq - a.Hkv, 0), v1 = h1 - a.Hq - a.Hkv;
   uint16_t* q_out = a.q_out + static_cast<size_t>(bt) * a.Hq * D;
   uint16_t* k_out = a.k_out + static_cast<size_t>(bt) * a.Hkv * D;
-  if (t >= count) {
-    if ((a.zeroed & VSD_ROPE_ZEROED_Q) != 0u) copy_heads<D>(q0, q1, nullptr, 0, q_out, D);
-    if (!kCache && (a.zeroed & VSD_ROPE_ZEROED_K) != 0u) copy_heads<D>(k0, k1, nullptr, 0, k_out, D);
-    return;
-  }
-  const Lanes<D, kPairs> at(lane % (D / 8), a.rot_dim);
-  float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
-  if (at.turned) {
-    uint32_t angle[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) angle[j] = angle_of(pos, __ldcg(a.turns + at.pair + j));
-    cos_sin2(angle[0], angle[1], c, s);
-    cos_sin2(angle[2], angle[3], c + 2, s + 2);
-    if (a.amplitude != 1.f) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        c[j] *= a.amplitude;
-        s[j] *= a.amplitude;
-      }
+  if (there) {
+    pos = static_cast<long long>(__ldcg(a.rope_base + b)) + a.pos_offset + t;
+    int count = a.n_valid != nullptr ? __ldcg(a.n_valid + b) : a.n;
+    if (count < 0 || count > a.n) {
+      if (lane == 0) flag_status(a.status, VSD_DEV_BAD_LENGTH);
+      count = 0;
+    }
+    if (t >= count) {
+      there = false;
+      if ((a.zeroed & VSD_ROPE_ZEROED_Q) != 0u) copy_heads<D>(q0, q1, nullptr, 0, q_out, D);
+      if (!kCache && (a.zeroed & VSD_ROPE_ZEROED_K) != 0u) copy_heads<D>(k0, k1, nullptr, 0, k_out, D);
     }
   }
-  if (q0 < q1)
-    turn_heads<D, kPairs, kFull>(a, at, c, s, a.q_weight, q0, q1, a.q.data + b * a.q.batch + t * a.q.row, a.q.head,
+  const Lanes<D, kPairs> at(lane % (D / 8), a.rot_dim);
+  bool met = false;
+  // every warp of the block comes here once, from where it is: the leaders with their tokens' angles
+  const auto meet = [&] {
+    if (met) return;
+    met = true;
+    if (there && leads && 4 * lane < a.rot_dim) {  // two pairs a lane
+      float c[2], s[2];
+      cos_sin2(angle_of(pos, __ldcg(a.turns + 2 * lane)), angle_of(pos, __ldcg(a.turns + 2 * lane + 1)), c, s);
+      *reinterpret_cast<float2*>(&own.c[mine][2 * lane]) = make_float2(c[0] * a.amplitude, c[1] * a.amplitude);
+      *reinterpret_cast<float2*>(&own.s[mine][2 * lane]) = make_float2(s[0] * a.amplitude, s[1] * a.amplitude);
+    }
+    ptx::named_barrier_sync(kAnglesBar, kRopeThreads);
+  };
+  const auto angles = [&](float (&c)[4], float (&s)[4]) {
+    meet();
+    c[0] = c[1] = c[2] = c[3] = 1.f;
+    s[0] = s[1] = s[2] = s[3] = 0.f;
+    if (!at.turned) return;
+    const float4 cc = *reinterpret_cast<const float4*>(&own.c[mine][at.pair]);
+    const float4 ss = *reinterpret_cast<const float4*>(&own.s[mine][at.pair]);
+    c[0] = cc.x, c[1] = cc.y, c[2] = cc.z, c[3] = cc.w;
+    s[0] = ss.x, s[1] = ss.y, s[2] = ss.z, s[3] = ss.w;
+  };
+  if (there && q0 < q1)
+    turn_heads<D, kPairs, kFull>(a, at, angles, a.q_weight, q0, q1, a.q.data + b * a.q.batch + t * a.q.row, a.q.head,
                                  q_out, D);
-  if (k0 >= k1 && (!kCache || v0 >= v1)) return;
   if (!kCache) {
-    turn_heads<D, kPairs, kFull>(a, at, c, s, a.k_weight, k0, k1, a.k.data + b * a.k.batch + t * a.k.row, a.k.head,
-                                 k_out, D);
-    return;
+    if (there && k0 < k1)
+      turn_heads<D, kPairs, kFull>(a, at, angles, a.k_weight, k0, k1, a.k.data + b * a.k.batch + t * a.k.row,
+                                   a.k.head, k_out, D);
+  } else if (there && (k0 < k1 || v0 < v1)) {
+    const long long place = static_cast<long long>(__ldcg(a.pos_base + b)) + a.pos_offset + t;
+    int blk = -1;
+    if (place < 0 || place >= static_cast<long long>(a.max_blocks) * kPageQ) {
+      if (lane == 0) flag_status(a.status, VSD_DEV_BAD_LENGTH);
+    } else {
+      blk = __ldcg(a.block_table + static_cast<size_t>(b) * a.max_blocks + place / kPageQ);
+      if (blk < 0 || blk >= a.num_blocks) {
+        if (lane == 0) flag_status(a.status, VSD_DEV_BAD_BLOCK);
+        blk = -1;
+      }
+    }
+    if (blk >= 0) {
+      const size_t slot = (static_cast<size_t>(blk) * a.Hkv * kPageQ + place % kPageQ) * D;
+      if (k0 < k1)
+        turn_heads<D, kPairs, kFull>(a, at, angles, a.k_weight, k0, k1, a.k.data + b * a.k.batch + t * a.k.row,
+                                     a.k.head, a.k_cache + slot, kPageQ * D);
+      if (v0 < v1)
+        copy_heads<D>(v0, v1, a.v.data + b * a.v.batch + t * a.v.row, a.v.head, a.v_cache + slot, kPageQ * D);
+    }
   }
-  const long long place = static_cast<long long>(__ldcg(a.pos_base + b)) + a.pos_offset + t;
-  if (place < 0 || place >= static_cast<long long>(a.max_blocks) * kPageQ) {
-    if (lane == 0) flag_status(a.status, VSD_DEV_BAD_LENGTH);
-    return;
-  }
-  const int blk = __ldcg(a.block_table + static_cast<size_t>(b) * a.max_blocks + place / kPageQ);
-  if (blk < 0 || blk >= a.num_blocks) {
-    if (lane == 0) flag_status(a.status, VSD_DEV_BAD_BLOCK);
-    return;
-  }
-  const size_t slot = (static_cast<size_t>(blk) * a.Hkv * kPageQ + place % kPageQ) * D;
-  if (k0 < k1)
-    turn_heads<D, kPairs, kFull>(a, at, c, s, a.k_weight, k0, k1, a.k.data + b * a.k.batch + t * a.k.row, a.k.head,
-                                 a.k_cache + slot, kPageQ * D);
-  if (v0 < v1)
-    copy_heads<D>(v0, v1, a.v.data + b * a.v.batch + t * a.v.row, a.v.head, a.v_cache + slot, kPageQ * D);
+  meet();
 }
 
 template <int D, bool kPairs, bool kFull, bool kCache>
 __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const RopeParams a) {
+  __shared__ __align__(16) TokenAngles<D> own;
   ptx::pdl_wait_primary();
   ptx::pdl_launch_dependents();
-  const unsigned task = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
-  if (task < a.tasks) token_rows<D, kPairs, kFull, kCache>(a, task);
+  token_rows<D, kPairs, kFull, kCache>(a, blockIdx.x, own);
 }
 
 // ---------------------------------------------------------------- pages of the 8-bit cache
@@ -524,17 +567,17 @@ __device__ __forceinline__ void page_rows(const RopeParams& a, unsigned block, P
 
 template <int D, bool kPairs, bool kFull>
 __global__ void __launch_bounds__(kRopeThreads, 5) norm_rope_quant_kernel(const RopeParams a) {
-  __shared__ __align__(16) PageRows<D> own;
+  static_assert(sizeof(PageRows<D>) >= sizeof(TokenAngles<D>));
+  __shared__ __align__(16) unsigned char shared[sizeof(PageRows<D>)];
   ptx::pdl_wait_primary();
   ptx::pdl_launch_dependents();
   // Blocks of pages, evenly among those of queries: the ones compute, the others read and write.
   const unsigned before = static_cast<unsigned>(static_cast<uint64_t>(blockIdx.x) * a.page_blocks / gridDim.x);
   const unsigned after = static_cast<unsigned>((static_cast<uint64_t>(blockIdx.x) + 1) * a.page_blocks / gridDim.x);
   if (after > before) {
-    page_rows<D, kPairs, kFull>(a, before, own);
+    page_rows<D, kPairs, kFull>(a, before, *reinterpret_cast<PageRows<D>*>(shared));
   } else {
-    const unsigned task = (blockIdx.x - before) * kRopeWarps + (threadIdx.x >> 5);
-    if (task < a.tasks) token_rows<D, kPairs, kFull, false>(a, task);
+    token_rows<D, kPairs, kFull, false>(a, blockIdx.x - before, *reinterpret_cast<TokenAngles<D>*>(shared));
   }
 }
 
@@ -574,18 +617,23 @@ RopeParams rope_params(const RopeArgs& x, int heads) {
   p.pos_offset = x.pos_offset;
   p.zeroed = x.zeroed;
   p.heads = heads;
-  // A warp takes as many of a token's heads as leaves an SM about as many warps as it holds: 24
-  // (4012 tokens of 24 heads 6.7 us with whole tokens, 8.6 with halves), 10 beside the pages of an
-  // 8-bit cache (96 tokens of 64 heads 5.8 us with 4 heads a warp, 7.1 with 2).
-  const long long warps = (x.k_scale != nullptr ? 10ll : 24ll) * x.num_sms;
+  // A warp takes a token's heads, or such a part of them (whole instructions of two or four rows)
+  // that an SM has ten warps: the fixed part of a warp costs more than the longest token's rows in
+  // turn.  (32768 tokens of 48 heads 123 us with whole tokens, 143 with thirds; 96 tokens of 64
+  // heads beside 8-bit pages 4.2 us with 10 warps an SM, 4.6 with 20.)
   const int rpi = x.d == 128 ? 2 : 4;
   const long long tokens = static_cast<long long>(x.B) * x.n;
-  p.chunk = heads;
-  while (p.chunk > rpi && tokens * ((heads + p.chunk - 1) / p.chunk) < warps)
-    p.chunk = (p.chunk / 2 + rpi - 1) / rpi * rpi;
-  p.chunks = Divisor(static_cast<uint32_t>((heads + p.chunk - 1) / p.chunk));
+  const int its = (heads + rpi - 1) / rpi;
+  int of_token = 1;
+  while (of_token < its && tokens * of_token < 10ll * x.num_sms) of_token *= 2;
+  p.chunk = (its + of_token - 1) / of_token * rpi;
+  of_token = (heads + p.chunk - 1) / p.chunk;
+  p.token_warps = of_token < kRopeWarps ? of_token : kRopeWarps;
+  p.block_tokens = of_token < kRopeWarps ? kRopeWarps / of_token : 1;
+  p.parts = Divisor(static_cast<uint32_t>((of_token + kRopeWarps - 1) / kRopeWarps));
   p.by_n = Divisor(static_cast<uint32_t>(x.n));
-  p.tasks = static_cast<unsigned>(tokens * p.chunks.d);
+  p.tokens = static_cast<unsigned>(tokens);
+  p.token_blocks = static_cast<unsigned>((tokens + p.block_tokens - 1) / p.block_tokens * p.parts.d);
   return p;
 }
 
@@ -603,14 +651,12 @@ cudaError_t launch(Kernel kern, const RopeParams& p, unsigned blocks, cudaStream
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-unsigned blocks_for(unsigned warps) { return warps / kRopeWarps + (warps % kRopeWarps != 0u); }
-
 template <int D, bool kPairs, bool kFull>
 cudaError_t launch_rows(const RopeParams& p, cudaStream_t stream) {
-  const unsigned blocks = p.page_blocks + blocks_for(p.tasks);
-  if (p.page_blocks > 0) return launch(norm_rope_quant_kernel<D, kPairs, kFull>, p, blocks, stream);
-  return p.block_table != nullptr ? launch(norm_rope_kernel<D, kPairs, kFull, true>, p, blocks, stream)
-                                  : launch(norm_rope_kernel<D, kPairs, kFull, false>, p, blocks, stream);
+  if (p.page_blocks > 0)
+    return launch(norm_rope_quant_kernel<D, kPairs, kFull>, p, p.page_blocks + p.token_blocks, stream);
+  return p.block_table != nullptr ? launch(norm_rope_kernel<D, kPairs, kFull, true>, p, p.token_blocks, stream)
+                                  : launch(norm_rope_kernel<D, kPairs, kFull, false>, p, p.token_blocks, stream);
 }
 
 template <int D>
