@@ -234,6 +234,11 @@ __device__ void find_bin_low(const uint32_t* cnt, int n, int r, SelShared& sh) {
   __syncthreads();
 }
 
+// A list of candidates to where it begins in the row of n.
+__device__ __forceinline__ void write_list(const int32_t* list, int32_t* dst, int at, int count, int n) {
+  for (int i = threadIdx.x; i < count && at + i < n; i += kSelThreads) dst[at + i] = list[i];
+}
+
 // Set this thread's selected positions (bit q of `sel` = position my0 + q) in the
 // bitmap `bm`, one atomic per word.
 __device__ __forceinline__ void mark_bits(uint32_t* bm, int my0, uint64_t sel) {
@@ -321,6 +326,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_topk_kernel(const SelPa
     for (int i = t; i < kBins0 + 2 * kBinsL; i += kSelThreads) L.ghist[i] = 0u;
   if (t == 0) sh.gcount = 0u;
   for (int i = t; i < kBins0; i += kSelThreads) L.hist[i] = 0u;
+  for (int i = t; i < chunk / 32; i += kSelThreads) L.loc[i] = 0u;
   __syncthreads();
   cluster_arrive();  // this CTA's shared memory is ready; waited on before remote use
   ptx::pdl_wait_primary();  // the partial scores come from the preceding kernels
@@ -590,8 +596,6 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_topk_kernel(const SelPa
     }
     // this CTA's words of the position bitmap (short rows: also stored to rank 0); its
     // count goes to every CTA
-    for (int i = t; i < nw_cta; i += kSelThreads) lbm[i] = 0u;
-    __syncthreads();
     mark_bits(lbm, t * KPT, sure);
     uint32_t n_sure;
     (void)block_excl_scan(static_cast<uint32_t>(__popcll(sure)), sh.scan, &n_sure);
@@ -634,6 +638,11 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_topk_kernel(const SelPa
   const int CS = static_cast<int>(cluster.num_blocks());
   int32_t* dst = a.idx + static_cast<size_t>(row) * a.k;
   const int n_recent_kept = P - rb;
+  // The chosen candidates go to global memory by way of a list in shared memory: stores of a few
+  // positions from each of a warp's lanes took longer than all the rest here.  The list lies on
+  // the buffer of boundary keys and what follows it, 32768 words before the row's bitmap, all of
+  // which are done with by then.
+  int32_t* list = reinterpret_cast<int32_t*>(L.gbuf);
 
   if (short_row) {
     // ---- E/F (short rows). Rank 0 alone: resolve the boundary bin, mark the winners
@@ -676,9 +685,10 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_topk_kernel(const SelPa
       for (int w = t; w < CS * nw_cta && w < a.bm_words; w += kSelThreads)
         a.out_bitmap[static_cast<size_t>(row) * a.bm_words + w] = L.bitmap[w];
     uint32_t total;
-    uint32_t o = sink_end + block_excl_scan(static_cast<uint32_t>(__popcll(bits)), sh.scan, &total);
-    for (; bits; bits &= bits - 1, ++o)
-      if (o < static_cast<uint32_t>(n)) dst[o] = t * per + __ffsll(static_cast<long long>(bits)) - 1;
+    uint32_t o = block_excl_scan(static_cast<uint32_t>(__popcll(bits)), sh.scan, &total);
+    for (; bits; bits &= bits - 1) list[o++] = t * per + __ffsll(static_cast<long long>(bits)) - 1;
+    __syncthreads();
+    write_list(list, dst, sink_end, static_cast<int>(total), n);
     if (a.out_count != nullptr && t == 0) a.out_count[row] = static_cast<int>(total);
     for (int i = t; i < sink_end; i += kSelThreads) dst[i] = i;
     for (int i = t; i < n_recent_kept; i += kSelThreads) dst[n - n_recent_kept + i] = rb + i;
@@ -739,27 +749,20 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_topk_kernel(const SelPa
   }
 
   // ---- F. every CTA writes its candidates in position order from its bitmap words
-  //      (one word per thread per round, a block scan of the words' counts); rank 0
+  //      (a word per thread, a block scan of the words' counts); rank 0
   //      writes the sinks, the recent window and the padding
-  uint32_t o_base = static_cast<uint32_t>(out_base);
-  for (int w0 = 0; w0 < nw_cta; w0 += kSelThreads) {
-    const int w = w0 + t;
-    uint32_t bits = w < nw_cta ? lbm[w] : 0u;
-    if (a.out_bitmap != nullptr && w < nw_cta) {
-      // this pass's chosen candidates, for the next pass of the hybrid budget
-      const int gw = rank * nw_cta + w;
-      if (gw < a.bm_words) a.out_bitmap[static_cast<size_t>(row) * a.bm_words + gw] = bits;
-    }
-    uint32_t r_tot;
-    uint32_t o = o_base + block_excl_scan(static_cast<uint32_t>(__popc(bits)), sh.scan, &r_tot);
-    while (bits) {
-      const int bit = __ffs(bits) - 1;
-      bits &= bits - 1;
-      if (o < static_cast<uint32_t>(n)) dst[o] = rank * chunk + w * 32 + bit;
-      ++o;
-    }
-    o_base += r_tot;
+  static_assert(kMaxChunk / 32 <= kSelThreads && kMaxChunk <= 2 * kGatherCap);
+  uint32_t bits = t < nw_cta ? lbm[t] : 0u;
+  if (a.out_bitmap != nullptr && t < nw_cta) {
+    // this pass's chosen candidates, for the next pass of the hybrid budget
+    const int gw = rank * nw_cta + t;
+    if (gw < a.bm_words) a.out_bitmap[static_cast<size_t>(row) * a.bm_words + gw] = bits;
   }
+  uint32_t mine;
+  uint32_t o = block_excl_scan(static_cast<uint32_t>(__popc(bits)), sh.scan, &mine);
+  for (; bits; bits &= bits - 1) list[o++] = rank * chunk + t * 32 + __ffs(bits) - 1;
+  __syncthreads();
+  write_list(list, dst, out_base, static_cast<int>(mine), n);
   if (rank != 0) return;
   if (a.out_count != nullptr && t == 0) a.out_count[row] = static_cast<int>(total);
   for (int i = t; i < sink_end; i += kSelThreads) dst[i] = i;
