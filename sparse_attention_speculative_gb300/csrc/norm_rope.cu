@@ -79,8 +79,8 @@ struct RopeParams {
   Divisor by_n;
   unsigned tokens;    // B * n
   unsigned token_blocks;
-  int pages;          // 8-bit cache: pages that n rows of one sequence can meet
-  int head_groups;    // ... heads of a page in blocks of kRopeWarps
+  Divisor pages;        // 8-bit cache: pages that n rows of one sequence can meet
+  Divisor head_groups;  // ... heads of a page in blocks of kRopeWarps
   unsigned page_blocks;  // ... and blocks of pages, 2 * B * pages * head_groups
 };
 
@@ -437,20 +437,26 @@ __device__ __forceinline__ void page_rows(const RopeParams& a, unsigned block, P
   constexpr int NI = kPageQ / RPI;
   const int lane = threadIdx.x & 31;
   const int sub = lane / LPR, lr = lane % LPR;
-  const unsigned page_of_kv = block / a.head_groups;
-  const int g = static_cast<int>(block - page_of_kv * a.head_groups) * kRopeWarps + static_cast<int>(threadIdx.x >> 5);
-  const unsigned pages = static_cast<unsigned>(a.B) * a.pages;
+  const int warp = static_cast<int>(threadIdx.x >> 5);
+  const unsigned page_of_kv = a.head_groups(block);
+  const int g0 = static_cast<int>(block - page_of_kv * a.head_groups.d) * kRopeWarps, g = g0 + warp;
+  const unsigned pages = static_cast<unsigned>(a.B) * a.pages.d;
   const bool is_v = page_of_kv >= pages;  // (K's first: they take longer)
   const unsigned page_of = is_v ? page_of_kv - pages : page_of_kv;
-  const PageUnit pu = page_unit(a, (page_of * 2u + (is_v ? 1u : 0u)) * a.Hkv + min(g, a.Hkv - 1), lane);
-  const int s0 = pu.s0, s1 = pu.s1;
-  if (s1 <= s0) return;  // (the block together)
+  const int b = static_cast<int>(a.pages(page_of)), pg = static_cast<int>(page_of - b * a.pages.d);
+  const RowRange rr = row_range(a, b, lane == 0 && warp == 0 && g0 == 0 && pg == 0 && !is_v);
+  const long long first = rr.p0 / kPageQ + pg, lo = first * kPageQ;  // the page, and its first position
+  const long long left = rr.p0 + rr.count - lo;
+  const int s0 = rr.p0 > lo ? static_cast<int>(rr.p0 - lo) : 0;  // slots [s0, s1) are the call's
+  const int s1 = left < kPageQ ? static_cast<int>(left) : kPageQ;
+  if (rr.count <= 0 || s1 <= s0) return;  // (the block together)
+  const int blk = __ldcg(a.block_table + static_cast<size_t>(b) * a.max_blocks + first);
   const bool mine = g < a.Hkv;
   const Lanes<D, kPairs> at(lr, a.rot_dim);
   const Strided& src = is_v ? a.v : a.k;
-  const int t0 = static_cast<int>(pu.lo - pu.rr.p0);  // slot 0 is row t0 of the call
-  const uint16_t* row = src.data + pu.b * src.batch + t0 * src.row + min(g, a.Hkv - 1) * src.head;
-  uint2 x[NI], y[NI];
+  const int t0 = static_cast<int>(lo - rr.p0);  // slot 0 is row t0 of the call
+  const uint16_t* row = src.data + b * src.batch + t0 * src.row + min(g, a.Hkv - 1) * src.head;
+  uint2 x[NI], y[NI];  // (on their way before the page is known)
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int slot = i * RPI + sub;
@@ -461,7 +467,6 @@ __device__ __forceinline__ void page_rows(const RopeParams& a, unsigned block, P
     }
   }
   float* scale = is_v ? a.scale[1] : a.scale[0];
-  const float was = s0 > 0 ? __ldcg(scale + pu.ph) : 0.f;
   Row w;
   const bool normed = !is_v && a.k_weight != nullptr;
   if (!is_v) {
@@ -470,7 +475,7 @@ __device__ __forceinline__ void page_rows(const RopeParams& a, unsigned block, P
     const int pair = threadIdx.x % kPairsOf;
     if (2 * pair < a.rot_dim) {
       const long long turns = __ldcg(a.turns + pair);
-      const long long p0 = static_cast<long long>(__ldcg(a.rope_base + pu.b)) + a.pos_offset + t0;
+      const long long p0 = static_cast<long long>(__ldcg(a.rope_base + b)) + a.pos_offset + t0;
       for (int slot = s0 + static_cast<int>(threadIdx.x) / kPairsOf; slot < s1; slot += 2 * kApart) {
         float c[2], s[2];
         cos_sin2(angle_of(p0 + slot, turns), angle_of(p0 + slot + kApart, turns), c, s);
@@ -485,6 +490,12 @@ __device__ __forceinline__ void page_rows(const RopeParams& a, unsigned block, P
     __syncthreads();
   }
   if (!mine) return;
+  if (blk < 0 || blk >= a.num_blocks) {
+    if (lane == 0) flag_status(a.status, VSD_DEV_BAD_BLOCK);
+    return;
+  }
+  const size_t ph = static_cast<size_t>(blk) * a.Hkv + g;  // (physical page, head)
+  const float was = s0 > 0 ? __ldcg(scale + ph) : 0.f;
   uint32_t top = 0u;  // the largest magnitude's bits (an infinity's or NaN's, where there is one)
   const auto magnitude = [](F2 v) {
     const float2 z = parts(v);
@@ -535,7 +546,7 @@ __device__ __forceinline__ void page_rows(const RopeParams& a, unsigned block, P
   }
   float now = page_scale_f32(top);
   if (s0 > 0 && was != 0.f && __uint_as_float(top) <= was * kE4M3Max) now = was;
-  uint8_t* page = (is_v ? a.codes[1] : a.codes[0]) + pu.ph * (kPageQ * D);
+  uint8_t* page = (is_v ? a.codes[1] : a.codes[0]) + ph * (kPageQ * D);
   // (a division by a power of two is exact as a product; any other scale is a caller's own)
   const bool power = (__float_as_uint(now) & 0x007FFFFFu) == 0u && now >= 0x1p-126f;
   const float inv = power ? reciprocal_of_power(now) : 0.f;
@@ -562,7 +573,7 @@ __device__ __forceinline__ void page_rows(const RopeParams& a, unsigned block, P
     });
   }
   if (s0 > 0 && now != was) requantise_rows<D>(page + lr * 8, s0, sub, was, now);
-  if (lane == 0 && (s0 == 0 || now != was)) scale[pu.ph] = now;
+  if (lane == 0 && (s0 == 0 || now != was)) scale[ph] = now;
 }
 
 template <int D, bool kPairs, bool kFull>
@@ -676,9 +687,9 @@ cudaError_t launch_norm_rope(const RopeArgs& x, cudaStream_t stream) {
 
 cudaError_t launch_norm_rope_quant(const RopeArgs& x, cudaStream_t stream) {
   RopeParams p = rope_params(x, x.Hq);
-  p.pages = quant_pages(x.n);
-  p.head_groups = (x.Hkv + kRopeWarps - 1) / kRopeWarps;
-  p.page_blocks = 2u * p.B * p.pages * p.head_groups;
+  p.pages = Divisor(static_cast<uint32_t>(quant_pages(x.n)));
+  p.head_groups = Divisor(static_cast<uint32_t>((x.Hkv + kRopeWarps - 1) / kRopeWarps));
+  p.page_blocks = 2u * p.B * p.pages.d * p.head_groups.d;
   return x.d == 128 ? launch_dim<128>(p, x.interleaved, stream) : launch_dim<64>(p, x.interleaved, stream);
 }
 
