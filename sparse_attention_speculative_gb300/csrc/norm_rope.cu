@@ -496,11 +496,7 @@ __device__ __forceinline__ void page_rows(const RopeParams& a, unsigned block, P
   }
   const size_t ph = static_cast<size_t>(blk) * a.Hkv + g;  // (physical page, head)
   const float was = s0 > 0 ? __ldcg(scale + ph) : 0.f;
-  uint32_t top = 0u;  // the largest magnitude's bits (an infinity's or NaN's, where there is one)
-  const auto magnitude = [](F2 v) {
-    const float2 z = parts(v);
-    return max(__float_as_uint(z.x) & 0x7FFFFFFFu, __float_as_uint(z.y) & 0x7FFFFFFFu);
-  };
+  float largest = 0.f;  // magnitude (an infinity, or NaN, where there is one)
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     if (i * RPI + RPI <= s0 || i * RPI >= s1) continue;  // (the warp together)
@@ -522,11 +518,14 @@ __device__ __forceinline__ void page_rows(const RopeParams& a, unsigned block, P
       f = turn_row<kPairs, kFull>(f, turn_of<kPairs>(c, s), at.turned);
     }
 #pragma unroll
-    for (int p = 0; p < 4; ++p) top = max(top, magnitude(f.x[p]));
+    for (int p = 0; p < 4; ++p) {
+      const float2 z = parts(f.x[p]);
+      asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(largest) : "f"(z.x), "f"(z.y));
+    }
     own.value[i][0][threadIdx.x] = make_ulonglong2(f.x[0], f.x[1]);
     own.value[i][1][threadIdx.x] = make_ulonglong2(f.x[2], f.x[3]);
   }
-  top = __reduce_max_sync(0xffffffffu, top);
+  uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(largest) & 0x7FFFFFFFu);
   if (top >= 0x7F800000u) {
     // rare: a NaN or an infinity somewhere.  They do not set the scale and become NaN.
     top = 0u;
