@@ -581,9 +581,13 @@ __global__ void __launch_bounds__(kRopeThreads, 5) norm_rope_quant_kernel(const 
   __shared__ __align__(16) unsigned char shared[sizeof(PageRows<D>)];
   ptx::pdl_wait_primary();
   ptx::pdl_launch_dependents();
-  // Blocks of pages, evenly among those of queries: the ones compute, the others read and write.
-  const unsigned before = static_cast<unsigned>(static_cast<uint64_t>(blockIdx.x) * a.page_blocks / gridDim.x);
-  const unsigned after = static_cast<unsigned>((static_cast<uint64_t>(blockIdx.x) + 1) * a.page_blocks / gridDim.x);
+  // Blocks of pages, evenly among the first half of those of queries: the ones compute, the others
+  // read and write, and the last blocks are to be short.
+  const unsigned span = a.page_blocks + a.token_blocks / 2;
+  const auto pages_before = [&](unsigned i) {
+    return min(a.page_blocks, static_cast<unsigned>(static_cast<uint64_t>(i) * a.page_blocks / span));
+  };
+  const unsigned before = pages_before(blockIdx.x), after = pages_before(blockIdx.x + 1);
   if (after > before) {
     page_rows<D, kPairs, kFull>(a, before, *reinterpret_cast<PageRows<D>*>(shared));
   } else {
