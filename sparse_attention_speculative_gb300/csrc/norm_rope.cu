@@ -20,9 +20,12 @@
 // What bounds it: HBM, for a prompt (32768 tokens of 32 + 8 + 8 heads of 128: 805 MB in 123 us,
 // 0.96 of the copy rate; 129 us with every lane finding its four angles before its first rows,
 // 196 us before two values went through one instruction and weights and angles were joined).
-// 4096 tokens into an 8-bit cache take 25 us (92 MB, 0.54; 26): the queries alone 14.5 (21.7), the
-// pages, whose blocks leave an SM 20 warps, the rest.  One token of 16 sequences is a launch,
-// 2.6 us (2.85).  Rows loaded a step ahead made the prompt slower (138 us: fewer warps an SM).
+// 4096 tokens into an 8-bit cache take 23.6 us (92 MB, 0.58; 26 before that): the queries alone 14.5 (21.7),
+// the pages, whose blocks leave an SM 20 warps, the rest.  (Two warps a page and head, its rows in
+// registers and 24 warps an SM: 24.7, with a fifth more instructions.)  A verify block of 16
+// sequences takes 3.8 us (5.6 with the page looked up before its rows).  One token of 16
+// sequences is a launch, 2.6 us.  Rows loaded a step ahead made the prompt slower (138 us:
+// fewer warps an SM).
 #include "launch.h"
 #include "pairs.cuh"
 #include "ptx.cuh"
@@ -582,7 +585,7 @@ __global__ void __launch_bounds__(kRopeThreads, 5) norm_rope_quant_kernel(const 
   ptx::pdl_wait_primary();
   ptx::pdl_launch_dependents();
   // Blocks of pages, evenly among the first half of those of queries: the ones compute, the others
-  // read and write, and the last blocks are to be short.
+  // read and write, and the last blocks are to be short (a 4K chunk 23.6 us, 24.5 among all).
   const unsigned span = a.page_blocks + a.token_blocks / 2;
   const auto pages_before = [&](unsigned i) {
     return min(a.page_blocks, static_cast<unsigned>(static_cast<uint64_t>(i) * a.page_blocks / span));
@@ -634,7 +637,7 @@ RopeParams rope_params(const RopeArgs& x, int heads) {
   // A warp takes a token's heads, or such a part of them (whole instructions of two or four rows)
   // that an SM has ten warps: the fixed part of a warp costs more than the longest token's rows in
   // turn.  (32768 tokens of 48 heads 123 us with whole tokens, 143 with thirds; 96 tokens of 64
-  // heads beside 8-bit pages 4.2 us with 10 warps an SM, 4.6 with 20.)
+  // heads beside 8-bit pages 4.25 us with 10 warps an SM, 4.6 with 16 or more.)
   const int rpi = x.d == 128 ? 2 : 4;
   const long long tokens = static_cast<long long>(x.B) * x.n;
   const int its = (heads + rpi - 1) / rpi;
