@@ -467,3 +467,50 @@ def test_mismatched_tensors(vsd):
         vsd.vsd_norm_rope_append_kv(q, None, k, c, c.clone(), bt, pos, turns)
     with pytest.raises(TypeError):
         vsd.vsd_norm_rope_append_kv(q, k, k, c.float(), c.float(), bt, pos, turns)
+
+
+@pytest.mark.parametrize("d,inter", [(128, False), (64, True)])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 3), (4, 1), (10, 5), (28, 7), (96, 12)])
+@pytest.mark.parametrize("B,n", [(1, 1), (3, 2), (5, 97), (1, 1531), (2, 1700)])
+def test_numbers_of_heads_and_tokens(vsd, B, n, Hq, Hkv, d, inter):
+    """Parts of a token, tokens and several tokens a block, the last block not full, counts that end
+    inside a block: the rows of the formula, and the same bits by each of the calls."""
+    g = torch.Generator().manual_seed(B * n + Hq)
+    cpu, gpu = projection(g, B, n, Hq, Hkv, d, True)
+    wq, wk = weights_of(g, d, True)
+    freq = life.inv_freq(d)
+    turns = vsd.vsd_rope_turns(freq)
+    valid = [max(0, n - 1 - 5 * b) if n > 1 else n for b in range(B)]
+    base = [1 + 40 * b for b in range(B)]
+    how = dict(n_valid=int32(valid), q_weight=cuda(wq), k_weight=cuda(wk), interleaved=inter)
+    q, k = vsd.vsd_norm_rope(gpu[0], gpu[1], turns, int32(base), **how)
+    for b in range(B):
+        t = valid[b]
+        pos = [base[b] + j for j in range(t)]
+        check_rows(q[b, :t].cpu(), cpu[0][b, :t], wq, pos, freq, inter)
+        check_rows(k[b, :t].cpu(), cpu[1][b, :t], wk, pos, freq, inter)
+        assert torch.all(q[b, t:] == 0) and torch.all(k[b, t:] == 0)
+    pages = (max(base) + n + PAGE - 1) // PAGE
+    table = torch.arange(B * pages, dtype=torch.int32).reshape(B, pages).cuda()
+    cache = [torch.zeros((B * pages, Hkv, PAGE, d), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    assert torch.equal(vsd.vsd_norm_rope_append_kv(*gpu, *cache, table, int32(base), turns, **how), q)
+    for b in range(B):
+        at = slice(base[b], base[b] + valid[b])
+        for c, x in zip(cache, (k, gpu[2])):
+            rows = c[b * pages:(b + 1) * pages].transpose(1, 2).reshape(pages * PAGE, Hkv, d)
+            assert torch.equal(rows[at], x[b, :valid[b]])
+            rows = rows.clone()
+            rows[at] = 0
+            assert torch.all(rows == 0)
+    codes = [torch.zeros_like(c).to(torch.float8_e4m3fn) for c in cache]
+    scales = [torch.zeros((B * pages, Hkv), device="cuda") for _ in range(2)]
+    assert torch.equal(vsd.vsd_norm_rope_append_kv_quant(*gpu, *codes, *scales, table, int32(base), turns, **how), q)
+    for b in range(B):
+        rows = codes[0][b * pages:(b + 1) * pages].float() * scales[0][b * pages:(b + 1) * pages, :, None, None]
+        rows = rows.transpose(1, 2).reshape(pages * PAGE, Hkv, d)[base[b]:base[b] + valid[b]]
+        have, want = rows, k[b, :valid[b]].float()
+        # half a step of e4m3 and one of bf16; below its normals 2^-10 of the page's scale, the largest of the page's
+        # values (at most the largest of all) over 448 and less than twice that
+        top = float(want.abs().max()) if valid[b] else 0.0
+        assert torch.all((have - want).abs() <= (2.0 ** -4 + 2.0 ** -7) * want.abs() + 2.0 ** -9 * top / 224)
+    assert vsd.vsd_read_device_status() == 0
