@@ -625,7 +625,9 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_topk_kernel(const SelPa
       while (inbin) {
         const int q = __ffsll(static_cast<long long>(inbin)) - 1;
         inbin &= inbin - 1;
-        gb0[o++] = make_uint2(L.keys[t * KPT + q], static_cast<uint32_t>(my0 + q));
+        // (more than the bin's count said: a histogram that is not these scores')
+        if (o < kGatherCap) gb0[o] = make_uint2(L.keys[t * KPT + q], static_cast<uint32_t>(my0 + q));
+        ++o;
       }
     }
   }
@@ -649,7 +651,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_topk_kernel(const SelPa
     //      in its row bitmap, write the row from the bitmap
     if (rank != 0) return;
     if (mode == kModeGather) {
-      const int n_in = static_cast<int>(sh.gcount);
+      const int n_in = min(static_cast<int>(sh.gcount), kGatherCap);
       if (n_in <= kFewIn) {
         // few: how many stand before each, counted by a few threads of a warp
         const int i = t / kThreadsOfOne, part = t % kThreadsOfOne;
@@ -704,7 +706,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_topk_kernel(const SelPa
   uint32_t total = 0;  // candidates chosen in the row (rank 0)
   if (mode == kModeGather) {
     if (rank == 0) {
-      const int n_in = static_cast<int>(sh.gcount);
+      const int n_in = min(static_cast<int>(sh.gcount), kGatherCap);
       int cut;
       resolve_boundary(L.gbuf, n_in, L.hist, sh, prefix, mask, r_rem, cut);
       if (t < CS) sh.taken[t] = 0u;

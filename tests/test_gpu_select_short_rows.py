@@ -56,3 +56,21 @@ def test_one_value(vsd, P):
                                     n_recent=10)
     assert idx[0].tolist() == list(range(290)) + list(range(P - 10, P))
     assert idx[1].tolist() == list(range(290)) + list(range(P - 11, P - 1))
+
+
+@pytest.mark.parametrize("P", [1500, 20000, 60000])
+@pytest.mark.parametrize("count", [101, 5000])
+def test_histogram_of_other_scores(vsd, P, count):
+    """A histogram that names fewer keys than the boundary bin has: positions of the row, in order,
+    and nothing outside the buffers."""
+    score = torch.ones((2, P), device="cuda")
+    key = (0x80000000 | 0x3F800000) >> 20          # (of 1.0: the order-preserving key's upper 12 bits)
+    hist = torch.zeros((2, 4096), dtype=torch.int32, device="cuda")
+    hist[:, key] = count
+    idx, n = vsd.vsd_select_topk_scored(score, hist, torch.full((2,), P, dtype=torch.int32).cuda(), k=100, n_sink=0,
+                                        n_recent=0)
+    torch.cuda.synchronize()
+    vsd.vsd_read_device_status()
+    assert n.tolist() == [100, 100]
+    for row in idx.tolist():
+        assert all(0 <= a < b < P for a, b in zip(row, row[1:]))
