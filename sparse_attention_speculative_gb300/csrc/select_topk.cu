@@ -38,8 +38,8 @@
 //      in position order from its own bitmap words; rank 0 adds the sinks, the recent
 //      window and the padding.
 // A row of one CTA searches its own histogram and exchanges nothing: 20 rows of 1000
-// positions 7.7 us (10.9 with the exchanges of a cluster); one of 32768 summed over 8
-// heads 10.3.
+// positions 7.5 us (10.9 with the exchanges of a cluster); one of 32768 summed over 8
+// heads 9.7.
 // Scored input (the fused verification has already summed the groups and counted the
 // level-0 histogram of every prefix position): A reads one score per position, and
 // every CTA copies the row's histogram, takes the sinks and the recent window out of
