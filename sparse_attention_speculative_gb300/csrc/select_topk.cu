@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_topk_kernel(const SelPa
   const int row = blockIdx.y;
   const int t = threadIdx.x;
   const int chunk = a.chunk;
-  const int KPT = chunk / kSelThreads;  // 4, 8, 16 or 32 positions per thread
+  const int KPT = chunk / kSelThreads;  // positions per thread: a multiple of 4 up to 32
   const SelLayout L = sel_layout(sel_smem, chunk);
   const bool single = cluster.num_blocks() == 1;  // (a row of one CTA exchanges nothing)
 
@@ -399,14 +399,16 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_topk_kernel(const SelPa
     prot_key = order_key(__ldcg(base + j));
   }
   // candidates chosen beforehand (first pass of the hybrid budget) are always taken
-  // and not ranked; this thread's KPT positions sit in one word of that bitmap
+  // and not ranked; this thread's KPT positions sit in one or two words of that bitmap
   uint32_t pre_bits = 0u;
   int n_pre = 0;
   if (a.pre_bitmap != nullptr) {
     const int wi = my0 >> 5;
     if (wi < a.bm_words) {
-      const uint32_t wv = __ldcg(a.pre_bitmap + static_cast<size_t>(row) * a.bm_words + wi);
-      pre_bits = (wv >> (my0 & 31)) & (KPT >= 32 ? 0xFFFFFFFFu : ((1u << KPT) - 1u));
+      const uint32_t* words = a.pre_bitmap + static_cast<size_t>(row) * a.bm_words + wi;
+      const bool two = (my0 & 31) + KPT > 32 && wi + 1 < a.bm_words;
+      pre_bits = __funnelshift_r(__ldcg(words), two ? __ldcg(words + 1) : 0u, my0 & 31) &
+                 (KPT >= 32 ? 0xFFFFFFFFu : ((1u << KPT) - 1u));
     }
     n_pre = __ldcg(a.pre_count + row);
   }
