@@ -808,7 +808,8 @@ vsd_status vsd_accumulate_weights_quant(const vsd_geom* geom, int R, int C, cons
  *   8-bit cache  a destination page takes the largest scale of the rows that come into it, and
  *              codes of a smaller one become e4m3(code * (scale / largest)) (exact down to
  *              e4m3's subnormals where scales are powers of two)
- * An index outside [i, prefix_len[b]) is flagged VSD_DEV_BAD_INDEX and its row is not written;
+ * An index outside [i, prefix_len[b]), or with weights at weights_stride or beyond (a kept row
+ * has its sum), is flagged VSD_DEV_BAD_INDEX and its row is not written;
  * a count outside [0, k_max] or beyond dst_table's pages, or a bad prefix length, is flagged
  * VSD_DEV_BAD_LENGTH and that list moves nothing (its weights_out stays too); a source or
  * destination entry outside the cache is flagged VSD_DEV_BAD_BLOCK and its rows are not

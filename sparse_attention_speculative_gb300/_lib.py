@@ -879,8 +879,8 @@ def vsd_compact_kv(k_cache, v_cache, block_table, dst_table, prefix_len, idx, n_
     """Eviction from a bf16 cache: the rows idx (int32 [B, k], or [B, Hkv, k] with a list for
     each KV head; ascending, as vsd_select_topk gives them) of each sequence move to rows 0 ..
     n_sel - 1 of dst_table's pages (int32 [B, pages]: block_table itself, its leading columns'
-    copy, or pages that nothing else uses), and so do their weights (fp32 [B, Hkv, .]), with
-    zeros behind them.  n_sel is the new length.  Returns weights_out."""
+    copy, or pages that nothing else uses), and so do their weights (fp32 [B, Hkv, .], a sum for
+    every index), with zeros behind them.  n_sel is the new length.  Returns weights_out."""
     return (_binding or _bound()).compact(k_cache, v_cache, None, None, block_table, dst_table,
                                           prefix_len, idx, n_sel, weights, weights_out,
                                           _handle(stream))

@@ -74,6 +74,8 @@ __global__ void __launch_bounds__(kCThreads) compact_kernel(const CompactParams 
   uint8_t* cache = kv ? a.cache[1] : a.cache[0];
   float* scale = kv ? a.scale[1] : a.scale[0];
   const bool weighted = kv == 0 && a.weights != nullptr;
+  // (a kept row has a sum: K's and V's clusters refuse the same indices)
+  const int last = a.weights != nullptr ? min(P, a.w_stride) : P;
   const float* w_in = a.weights + static_cast<size_t>(pair) * static_cast<size_t>(a.w_stride);
   float* w_out = a.weights_out + static_cast<size_t>(pair) * static_cast<size_t>(a.w_out_stride);
   const int pages = (n + kPageC - 1) / kPageC;
@@ -87,7 +89,7 @@ __global__ void __launch_bounds__(kCThreads) compact_kernel(const CompactParams 
     const int i = page * kPageC + lane;
     return page < pages && lane < kPageC && i < n ? __ldcg(idx + i) : -1;
   };
-  const auto fits = [&](int j, int page) { return j >= page * kPageC + lane && j < P; };
+  const auto fits = [&](int j, int page) { return j >= page * kPageC + lane && j < last; };
   const auto block_of = [&](int j, int page) {
     return lane < kPageC && fits(j, page) ? __ldcg(sources + j / kPageC) : -1;
   };
@@ -191,7 +193,8 @@ __global__ void __launch_bounds__(kCThreads) compact_kernel(const CompactParams 
     to = to1;
   }
   if (weighted) {  // (in place the last step's meeting is behind: none of the old sums is read any more)
-    for (int i = n + rank * kCThreads + static_cast<int>(threadIdx.x); i < a.w_out_stride; i += CS * kCThreads)
+    // (unsigned: the step past the end of the longest stride)
+    for (unsigned i = n + rank * kCThreads + threadIdx.x; i < static_cast<unsigned>(a.w_out_stride); i += CS * kCThreads)
       w_out[i] = 0.f;
   }
 }
