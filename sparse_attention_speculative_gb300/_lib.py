@@ -164,6 +164,15 @@ def _need(t: torch.Tensor, dtype, name: str) -> None:
         raise ValueError("%s must be contiguous" % name)
 
 
+def _shaped(t: torch.Tensor, dtype, shape, device, name: str) -> torch.Tensor:
+    _need(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.device != device:
+        raise ValueError("%s is on another device" % name)
+    return t
+
+
 def geom_for(B: int, Hq: int, k_cache: torch.Tensor, block_table: torch.Tensor) -> Geom:
     NB, Hkv, page, d = k_cache.shape
     return Geom(B, Hq, Hkv, d, page, int(block_table.shape[1]), NB)
@@ -299,22 +308,31 @@ def vsd_verify_attn_collect_noalloc(q, k_cache, v_cache, block_table, prefix_len
 def vsd_select_topk(partial, prefix_len, *, k: int, n_sink: int, n_recent: int, idx=None,
                     n_sel=None, scores_out=None, want_scores: bool = False,
                     stream=None) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
-    """Protected top-k over the aggregated score.  partial: fp32 [n_rows, Hkv, P_max]."""
+    """Protected top-k over the aggregated score.  partial: fp32 [n_rows, Hkv, P_max];
+    prefix_len: int32, one for each row.  Outputs that are given have the shapes of those
+    returned: (idx [n_rows, k], n_sel [n_rows], scores_out [n_rows, P_max])."""
     module = _binding or _bound_or_none()
     if module is not None:
         return module.select(partial, prefix_len, int(k), int(n_sink), int(n_recent), idx, n_sel,
                              scores_out, want_scores, _handle(stream))
     lib = load()
     _need(partial, torch.float32, "partial")
-    _need(prefix_len, torch.int32, "prefix_len")
+    if partial.dim() != 3:
+        raise ValueError("partial must have 3 dimensions, got shape %s" % (tuple(partial.shape),))
     n_rows, Hkv, P_max = partial.shape
-    dev = partial.device
-    if idx is None:
-        idx = torch.empty((n_rows, k), dtype=torch.int32, device=dev)
-    if n_sel is None:
-        n_sel = torch.empty((n_rows,), dtype=torch.int32, device=dev)
-    if want_scores and scores_out is None:
-        scores_out = torch.empty((n_rows, P_max), dtype=torch.float32, device=dev)
+    _shaped(prefix_len, torch.int32, prefix_len.shape, partial.device, "prefix_len")
+    if prefix_len.numel() != n_rows:
+        raise ValueError("prefix_len must have a length for each of %d rows, got shape %s"
+                         % (n_rows, tuple(prefix_len.shape)))
+
+    def output(given, dtype, shape, name):
+        if given is None:
+            return torch.empty(shape, dtype=dtype, device=partial.device)
+        return _shaped(given, dtype, shape, partial.device, name)
+    idx = output(idx, torch.int32, (n_rows, int(k)), "idx")
+    n_sel = output(n_sel, torch.int32, (n_rows,), "n_sel")
+    if want_scores or scores_out is not None:
+        scores_out = output(scores_out, torch.float32, (n_rows, P_max), "scores_out")
     rc = lib.vsd_select_topk(n_rows, Hkv, _ptr(partial), _ptr(prefix_len), P_max, int(k),
                              int(n_sink), int(n_recent), _ptr(idx), _ptr(n_sel),
                              _ptr(scores_out), None, 0, _stream(stream))

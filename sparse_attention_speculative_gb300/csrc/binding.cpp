@@ -650,29 +650,24 @@ PyObject* py_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // select(partial, prefix_len, k, n_sink, n_recent, idx, n_sel, scores_out, want_scores, stream)
-//   -> (idx, n_sel, scores_out).  (Buffers that are given are taken as they are.)
+//   -> (idx, n_sel, scores_out)
 PyObject* py_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call(n, 10, [&]() -> PyObject* {
     const at::Tensor &partial = as_tensor(a[0], "partial"), &pl = as_tensor(a[1], "prefix_len");
     need(partial, at::kFloat, 3, "partial");
-    need(pl, at::kInt, pl.dim(), "prefix_len");
     const Place p(partial, a[9]);
     const int rows = dim_of(partial.size(0), "n_rows"), Hkv = dim_of(partial.size(1), "Hkv");
     const int P_max = dim_of(partial.size(2), "P_max"), k = as_int(a[2], "k");
     const int n_sink = as_int(a[3], "n_sink"), n_recent = as_int(a[4], "n_recent");
-    const auto output = [&](PyObject* given, at::ScalarType type, at::IntArrayRef shape, const char* name) {
-      Output o;
-      if (given != Py_None) {
-        o.object = given;
-        o.at = pointer(as_tensor(given, name));
-      } else {
-        o.take(Py_None, p, type, shape, name);
-      }
-      return o;
-    };
-    const Output idx = output(a[5], at::kInt, {rows, k}, "idx"), ns = output(a[6], at::kInt, {rows}, "n_sel");
-    Output scores;
-    if (as_bool(a[8]) || a[7] != Py_None) scores = output(a[7], at::kFloat, {rows, P_max}, "scores_out");
+    // (a length for each row, in any shape: [layers, sequences] too)
+    need(pl, at::kInt, pl.sizes(), p.dev, "prefix_len");
+    if (pl.numel() != rows)
+      refuse(PyExc_ValueError, "prefix_len must have a length for each of " + std::to_string(rows) +
+                                   " rows, got shape " + text(pl.sizes()));
+    Output idx, ns, scores;
+    idx.take(a[5], p, at::kInt, {rows, k}, "idx");
+    ns.take(a[6], p, at::kInt, {rows}, "n_sel");
+    if (as_bool(a[8]) || a[7] != Py_None) scores.take(a[7], p, at::kFloat, {rows, P_max}, "scores_out");
     check(without_gil([&] {
             return g_calls.select(rows, Hkv, static_cast<const float*>(pointer(partial)),
                                   static_cast<const int32_t*>(pointer(pl)), P_max, k, n_sink, n_recent,
