@@ -770,7 +770,8 @@ vsd_status vsd_norm_rope_append_kv_quant(const vsd_geom* geom, int n, const vsd_
  * of the verify block whose block-table entry is outside the cache is left out and flagged
  * VSD_DEV_BAD_BLOCK; a prefix outside [0, P_max], or whose verify block leaves the table, is
  * flagged VSD_DEV_BAD_LENGTH and that sequence's weights stay.  A row with a NaN or plus infinity
- * among its logits (one beyond 2^127 counts as that) adds NaN; minus infinity weighs nothing.
+ * among its logits (one beyond 2^127 counts as that), or a NaN in a key of the verify block that
+ * it sees or in that key's scale, adds NaN; minus infinity weighs nothing.
  * Sums are formed in a fixed order (two runs are bit-identical).
  * Supported: as vsd_verify_attn_collect with C <= 16, C * G <= 64, P_max up to 2^30 and B * Hkv
  * below 2^26.

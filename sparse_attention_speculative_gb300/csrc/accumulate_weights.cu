@@ -181,7 +181,8 @@ constexpr int kRowBytes = 272;  // 128 values and 16 bytes: rows next to each ot
 struct Block {
   uint4 q[kMaxWeightCols][kRowBytes / 16];
   uint4 k[kMaxWeightSlots][kRowBytes / 16];
-  float factor[kMaxWeightSlots];           // scale log2 e, times the key's; NaN: no such key
+  float factor[kMaxWeightSlots];           // scale log2 e, times the key's
+  bool there[kMaxWeightSlots];             // is the key's page in the cache (a factor may be NaN)
   float z[kMaxWeightCols][kMaxWeightSlots];  // logits log2 e; minus infinity: not seen
 };
 
@@ -207,7 +208,7 @@ __device__ __forceinline__ int piece_page(const WeightsParams& a, int b, int P, 
 }
 
 __device__ __forceinline__ Piece fetch_piece(const WeightsParams& a, int b, int g, int P, int rank, int CS, int i,
-                                             int blk) {
+                                             int blk, Block& s) {
   const int u = i >> a.shift_c, c = i - (u << a.shift_c);
   Piece r{make_uint4(0, 0, 0, 0), a.scale * kLog2e};
   if (u >= a.R) {
@@ -216,9 +217,10 @@ __device__ __forceinline__ Piece fetch_piece(const WeightsParams& a, int b, int 
         a.q + ((static_cast<size_t>(b) * a.R + a.row[slot]) * a.Hq + g * a.G + (col - slot * a.G)) * a.d + c * 8);
     return r;
   }
-  if (blk < 0 || blk >= a.num_blocks) {
+  const bool there = blk >= 0 && blk < a.num_blocks;
+  if (c == 0) s.there[u] = there;
+  if (!there) {
     if (g == 0 && rank == 0 && c == 0) flag_status(a.status, VSD_DEV_BAD_BLOCK);
-    r.f = NAN;
     return r;
   }
   const size_t ph = static_cast<size_t>(blk) * a.Hkv + g;
@@ -278,7 +280,7 @@ __device__ __forceinline__ void block_logits(const WeightsParams& a, int rank, i
       float z = dot[0] + dot[1];
 #pragma unroll
       for (int m = 4; m >= 1; m >>= 1) z += __shfl_xor_sync(0xffffffffu, z, m);
-      if (l8 == 0 && u < a.R) s.z[at][u] = u <= row && !isnan(s.factor[u]) ? z * s.factor[u] : -INFINITY;
+      if (l8 == 0 && u < a.R) s.z[at][u] = u <= row && s.there[u] ? z * s.factor[u] : -INFINITY;
     }
   }
 }
@@ -395,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(c
   const int pieces = block_pieces(a, rank, CS);
   Piece piece;
   if (kHold > 0 && static_cast<int>(threadIdx.x) < pieces)
-    piece = fetch_piece(a, b, g, P, rank, CS, threadIdx.x, piece_page(a, b, P, threadIdx.x));
+    piece = fetch_piece(a, b, g, P, rank, CS, threadIdx.x, piece_page(a, b, P, threadIdx.x), block);
   if (kHold > 0) {
     load4<kVec, kThreads>(out, lo, hi, w);
 #pragma unroll
@@ -478,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) accumulate_weights_kernel(c
     }
   }
   for (int i = threadIdx.x; i < pieces; i += kThreads) {
-    if (kHold == 0 || i >= kThreads) piece = fetch_piece(a, b, g, P, rank, CS, i, piece_page(a, b, P, i));
+    if (kHold == 0 || i >= kThreads) piece = fetch_piece(a, b, g, P, rank, CS, i, piece_page(a, b, P, i), block);
     put_piece(a, i, piece, block);
   }
   share_sums<kThreads>(a, rank, CS, part, block, slices, whole, true);
