@@ -631,13 +631,14 @@ PyObject* py_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
         wo.take(Py_None, p, at::kFloat, {B, g.Hkv, wos}, "weights_out");
         wo.made.zero_();  // (a list that is refused leaves its row)
       }
+      if (wos == 0) w = nullptr;  // (lists of no index: a tensor without elements has no address)
     } else if (a[10] != Py_None) {
       refuse(PyExc_ValueError, "weights_out needs weights");
     }
     check(without_gil([&] {
             const int32_t* idx = static_cast<const int32_t*>(pointer(it));
             const int32_t* ns = static_cast<const int32_t*>(pointer(nt));
-            float* to = static_cast<float*>(wo.at);
+            float* to = wos > 0 ? static_cast<float*>(wo.at) : nullptr;
             const int lists = heads ? g.Hkv : 1, dst = other.max_blocks_per_seq;
             if (c.ks != nullptr)
               return g_calls.compact_quant(&g, bt, dt, dst, pl, idx, ns, lists, k, c.k, c.v, c.ks, c.vs, w, ws, to,

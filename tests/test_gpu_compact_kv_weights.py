@@ -68,3 +68,23 @@ def test_the_longest_stride(vsd):  # noqa: F811
     assert int(torch.count_nonzero(out[0, 0, n:])) == 0
     del out
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("heads", [False, True])
+def test_lists_of_no_index(vsd, quant, heads):  # noqa: F811
+    """k = 0: nothing moves, and the sums that are returned have no elements."""
+    c = Case([40, 0], 0, 2, 64, quant, heads, seed=3)
+    for weights, shape in (("new", (2, 2, 0)), ("none", None), ("place", c.weights.shape)):
+        got = c.run(vsd, weights=weights)
+        assert all(torch.equal(a, b) for a, b in zip(got[0] + got[1], c.caches + c.scales))
+        assert got[2] is None if shape is None else got[2].shape == shape and not got[2].any()
+    assert vsd.vsd_read_device_status() == 0
+
+
+def test_sums_of_no_position(vsd):  # noqa: F811
+    """Rows of sums without elements beside lists that have some: refused, not ignored."""
+    c = Case([40], 16, 2, 64, False, False, seed=4)
+    c.weights = c.weights[..., :0]
+    with pytest.raises(vsd.VsdError):
+        c.run(vsd)
