@@ -816,8 +816,11 @@ def vsd_sparse_decode_attn_quant(q, k_cache, v_cache, k_scale, v_scale, block_ta
 def vsd_rope_turns(inv_freq, device=None):
     """The rotation's table for the calls below, made once for a model: int64 [rot_dim / 2],
     each inv_freq / (2 pi) in units of 2^-64, modulo 1.  inv_freq: radians per position, a
-    tensor or sequence (taken in 64 bits)."""
+    tensor or sequence (taken in 64 bits) of finite numbers (checked where they are on the
+    host; a table of others means nothing)."""
     f = torch.as_tensor(inv_freq, dtype=torch.float64)
+    if not f.is_cuda and not bool(torch.isfinite(f).all()):
+        raise ValueError("inv_freq must be finite")
     if device is None:
         device = f.device if f.is_cuda else "cuda"
     t = f.to(device) / (2.0 * math.pi)
