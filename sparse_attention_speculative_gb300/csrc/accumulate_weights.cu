@@ -178,18 +178,25 @@ __device__ __forceinline__ void mask4(int base, int end, float (&z)[4]) {
 // then a thread forms one product.
 constexpr int kRowBytes = 272;  // 128 values and 16 bytes: rows next to each other in other banks
 
+// What a key's products are multiplied by, scale log2 e times the key's scale, in two parts: a
+// power of two up to 1 that the query's values take beforehand (exact; bf16's largest values times
+// codes would leave fp32 on the way to a logit of order one), and the rest.
+struct __align__(16) KeyScale {
+  float down, rest;
+  bool there;  // is the key's page in the cache (the parts of a scale may be NaN)
+};
+
 struct Block {
   uint4 q[kMaxWeightCols][kRowBytes / 16];
   uint4 k[kMaxWeightSlots][kRowBytes / 16];
-  float factor[kMaxWeightSlots];           // scale log2 e, times the key's
-  bool there[kMaxWeightSlots];             // is the key's page in the cache (a factor may be NaN)
+  KeyScale key[kMaxWeightSlots];
   float z[kMaxWeightCols][kMaxWeightSlots];  // logits log2 e; minus infinity: not seen
 };
 
 // Piece i of those operands: 8 values of a key (the block's first), or of a column's query.
 struct Piece {
   uint4 v;
-  float f;
+  float f;  // the key's scale
 };
 
 // Columns of a CTA: rank, rank + CS, ...
@@ -210,7 +217,7 @@ __device__ __forceinline__ int piece_page(const WeightsParams& a, int b, int P, 
 __device__ __forceinline__ Piece fetch_piece(const WeightsParams& a, int b, int g, int P, int rank, int CS, int i,
                                              int blk, Block& s) {
   const int u = i >> a.shift_c, c = i - (u << a.shift_c);
-  Piece r{make_uint4(0, 0, 0, 0), a.scale * kLog2e};
+  Piece r{make_uint4(0, 0, 0, 0), 1.f};
   if (u >= a.R) {
     const int col = rank + (u - a.R) * CS, slot = col >> a.shift_g;
     r.v = ldg_stream16(
@@ -218,7 +225,7 @@ __device__ __forceinline__ Piece fetch_piece(const WeightsParams& a, int b, int 
     return r;
   }
   const bool there = blk >= 0 && blk < a.num_blocks;
-  if (c == 0) s.there[u] = there;
+  if (c == 0) s.key[u].there = there;
   if (!there) {
     if (g == 0 && rank == 0 && c == 0) flag_status(a.status, VSD_DEV_BAD_BLOCK);
     return r;
@@ -231,7 +238,7 @@ __device__ __forceinline__ Piece fetch_piece(const WeightsParams& a, int b, int 
     const uint2 x = ldg_stream8(static_cast<const uint8_t*>(a.k_cache) + at);
     r.v.x = x.x;
     r.v.y = x.y;
-    if (c == 0) r.f *= __ldcg(a.k_scale + ph);
+    if (c == 0) r.f = __ldcg(a.k_scale + ph);
   }
   return r;
 }
@@ -242,7 +249,11 @@ __device__ __forceinline__ void put_piece(const WeightsParams& a, int i, const P
     s.q[u - a.R][c] = r.v;
     return;
   }
-  if (c == 0) s.factor[u] = r.f;
+  if (c == 0) {
+    const uint32_t e = min(max(__float_as_uint(r.f) >> 23 & 0xFFu, 1u), 127u);
+    s.key[u].down = __uint_as_float(e << 23);
+    s.key[u].rest = a.scale * kLog2e * (r.f * __uint_as_float((254u - e) << 23));
+  }
   if (a.k_scale == nullptr) {
     s.k[u][c] = r.v;
   } else {
@@ -264,23 +275,24 @@ __device__ __forceinline__ void block_logits(const WeightsParams& a, int rank, i
     for (int u0 = 0; u0 < a.R; u0 += 4) {
       const int u = u0 + oct;
       float dot[2] = {0.f, 0.f};
+      const KeyScale key = s.key[u];  // (u below kMaxWeightSlots, a multiple of four)
       if (u <= row) {
         for (int c = l8; c < a.d / 8; c += 8) {
           const uint4 x = s.q[at][c], y = s.k[u][c];
-          dot[0] = fmaf(bf16_lo(x.x), bf16_lo(y.x), dot[0]);
-          dot[1] = fmaf(bf16_hi(x.x), bf16_hi(y.x), dot[1]);
-          dot[0] = fmaf(bf16_lo(x.y), bf16_lo(y.y), dot[0]);
-          dot[1] = fmaf(bf16_hi(x.y), bf16_hi(y.y), dot[1]);
-          dot[0] = fmaf(bf16_lo(x.z), bf16_lo(y.z), dot[0]);
-          dot[1] = fmaf(bf16_hi(x.z), bf16_hi(y.z), dot[1]);
-          dot[0] = fmaf(bf16_lo(x.w), bf16_lo(y.w), dot[0]);
-          dot[1] = fmaf(bf16_hi(x.w), bf16_hi(y.w), dot[1]);
+          dot[0] = fmaf(bf16_lo(x.x) * key.down, bf16_lo(y.x), dot[0]);
+          dot[1] = fmaf(bf16_hi(x.x) * key.down, bf16_hi(y.x), dot[1]);
+          dot[0] = fmaf(bf16_lo(x.y) * key.down, bf16_lo(y.y), dot[0]);
+          dot[1] = fmaf(bf16_hi(x.y) * key.down, bf16_hi(y.y), dot[1]);
+          dot[0] = fmaf(bf16_lo(x.z) * key.down, bf16_lo(y.z), dot[0]);
+          dot[1] = fmaf(bf16_hi(x.z) * key.down, bf16_hi(y.z), dot[1]);
+          dot[0] = fmaf(bf16_lo(x.w) * key.down, bf16_lo(y.w), dot[0]);
+          dot[1] = fmaf(bf16_hi(x.w) * key.down, bf16_hi(y.w), dot[1]);
         }
       }
       float z = dot[0] + dot[1];
 #pragma unroll
       for (int m = 4; m >= 1; m >>= 1) z += __shfl_xor_sync(0xffffffffu, z, m);
-      if (l8 == 0 && u < a.R) s.z[at][u] = u <= row && s.there[u] ? z * s.factor[u] : -INFINITY;
+      if (l8 == 0 && u < a.R) s.z[at][u] = u <= row && key.there ? z * key.rest : -INFINITY;
     }
   }
 }
