@@ -683,7 +683,10 @@ vsd_status vsd_sparse_decode_attn_quant(const vsd_geom* geom, const void* q,
  *   dimensions from rot_dim on stay y.
  * p = the row's position, rope_base[b] + pos_offset + t (pos_base where rope_base is NULL:
  * after an eviction a sequence holds fewer rows than it has positions).  All in fp32, rounded
- * once to what is written; a row whose sum of squares leaves fp32's range becomes zeros.
+ * once to what is written, cosine and sine within 5e-8 of the angle's.  A row whose sum of
+ * squares overflows fp32 becomes zeros (its infinities NaN).  With eps = 0 a row's squares have
+ * to be numbers that fp32 holds: a row of zeros becomes NaN, and one whose squares underflow to
+ * zero infinities or NaN.
  *   turns   int64 [rot_dim / 2] (device): f_i / (2 pi) in units of 2^-64, modulo 1.  The
  *           product with p wraps at whole turns, so that every position's angle is exact to
  *           2^-24 of half a turn
@@ -763,16 +766,19 @@ vsd_status vsd_norm_rope_append_kv_quant(const vsd_geom* geom, int n, const vsd_
  * caller put there (zeros).
  *   logits     fp32 [B][C][Hq][P_max]
  *   rows       C host integers in [-1, R): -1 leaves a slot out (with R = 1 a collecting
- *              verification writes its one row twice: rows = {0, -1} counts it once)
+ *              verification writes its one row twice: rows = {0, -1} counts it once).  One
+ *              list for all sequences: the rows of drafts that a sequence then rejects count
+ *              like its others, where they are named
  *   q          bf16 [B][R][Hq][head_dim], scale: the verification's
- *   weights    fp32 [B][Hkv][weights_stride], weights_stride >= P_max
+ *   weights    fp32 [B][Hkv][weights_stride], weights_stride >= P_max; apart from what is read
  * The keys are those of the cache; with an 8-bit cache its key codes and their scales.  A key
  * of the verify block whose block-table entry is outside the cache is left out and flagged
  * VSD_DEV_BAD_BLOCK; a prefix outside [0, P_max], or whose verify block leaves the table, is
  * flagged VSD_DEV_BAD_LENGTH and that sequence's weights stay.  A row with a NaN or plus infinity
  * among its logits (one beyond 2^127 counts as that), or a NaN in a key of the verify block that
  * it sees or in that key's scale, adds NaN; minus infinity weighs nothing.
- * Sums are formed in a fixed order (two runs are bit-identical).
+ * Sums are formed in a fixed order (two runs are bit-identical), in fp32: a weight of p, whose
+ * logit is z below the row's largest, to p (2^-19 + 2^-22 z).
  * Supported: as vsd_verify_attn_collect with C <= 16, C * G <= 64, P_max up to 2^30 and B * Hkv
  * below 2^26.
  * ------------------------------------------------------------------------------ */
@@ -797,12 +803,15 @@ vsd_status vsd_accumulate_weights_quant(const vsd_geom* geom, int R, int C, cons
  *   weights_out[b][g][i] <- weights[b][g][j];  weights_out[b][g][n ..] <- 0
  * idx is ascending, as vsd_select_topk gives it from the accumulated weights (one set for all
  * heads with its partial_scores = weights; one for each head with n_rows = B * Hkv rows of one
- * group), and n_sel is the new length.  Keys keep the rotation of their old positions, and new
+ * group, each with its sequence's length, and P_max within that call's limit for so many rows),
+ * and n_sel is the new length.  Keys keep the rotation of their old positions, and new
  * rows follow at n with rope_base still counting every position (vsd_norm_rope_append_kv).
  *   dst_table  int32 [B][dst_blocks].  The page that the rows 16 i .. 16 i + 15 go to is either
  *              block_table's page i of that sequence (moved in place: dst_table may be
- *              block_table itself) or a page that no sequence of the call reads; no page is
- *              written for two sequences.  Rows at n and beyond stay as they were
+ *              block_table itself) or a page that the sequence does not read.  Either way no
+ *              other sequence of the call reads it (a prefix that sequences share moves into
+ *              pages of each one's own), and no page is written for two sequences.  Rows at n
+ *              and beyond stay as they were
  *   weights, weights_out  fp32 [B][Hkv][stride] each, both or neither NULL; weights_out may be
  *              weights (with one stride), and does not overlap it otherwise
  *              (VSD_ERR_INVALID_ARG); weights_out_stride >= k_max

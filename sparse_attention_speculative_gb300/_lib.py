@@ -881,7 +881,7 @@ def vsd_accumulate_weights(logits, q, k_cache, block_table, prefix_len, weights,
     to weights (fp32 [B, Hkv, at least P_max]), for each prefix position and KV head.  q, the
     cache and scale are the verification's.  rows: the verify row of each of the C slots, -1 to
     leave one out; None: all of them where C = R, else the two collected rows 0 and R - 1 (one,
-    for R = 1).  Returns weights."""
+    for R = 1).  They count for every sequence, whatever it accepts of them.  Returns weights."""
     return (_binding or _bound()).weights(logits, q, k_cache, None, block_table, prefix_len,
                                           weights, scale, rows, _handle(stream))
 
@@ -899,8 +899,8 @@ def vsd_compact_kv(k_cache, v_cache, block_table, dst_table, prefix_len, idx, n_
                    weights=None, weights_out=None, stream=None):
     """Eviction from a bf16 cache: the rows idx (int32 [B, k], or [B, Hkv, k] with a list for
     each KV head; ascending, as vsd_select_topk gives them) of each sequence move to rows 0 ..
-    n_sel - 1 of dst_table's pages (int32 [B, pages]: block_table itself, its leading columns'
-    copy, or pages that nothing else uses), and so do their weights (fp32 [B, Hkv, .], a sum for
+    n_sel - 1 of dst_table's pages (int32 [B, pages]: block_table itself or its leading columns'
+    copy, where no other sequence reads those pages, or pages that nothing else uses), and so do their weights (fp32 [B, Hkv, .], a sum for
     every index), with zeros behind them.  n_sel is the new length.  Returns weights_out."""
     return (_binding or _bound()).compact(k_cache, v_cache, None, None, block_table, dst_table,
                                           prefix_len, idx, n_sel, weights, weights_out,

@@ -18,8 +18,9 @@
 //
 // What it takes: two rows of 8 x 4 heads over 512 positions 4.9 us, over 32768 7.3 us (a chain of
 // load, exponentials, two joins and the cluster's barrier of 5 us, and a launch); 16 sequences of
-// 32768 with 8 x 8 heads 71 us (301 MB that it needs, 390 MB that DRAM moves since L2 keeps a
-// quarter of the second reading; 0.62 of the copy rate).  Other forms of the large case:
+// 32768 with 8 x 8 heads 71 us (301 MB that it needs, 390 MB that DRAM moves: L2 has two thirds
+// of the second reading; 0.62 of the copy rate for what it needs, 0.8 for what is moved).  Other
+// forms of the large case, when this one took 75:
 // exponentials kept in shared memory and registers by two CTAs an SM in clusters of 16 (150 us:
 // seven such clusters fit the GPU, and their CTAs wait for one another), clusters that take pair
 // after pair with the next one's logits on their way into shared memory (173), half of the
@@ -592,9 +593,9 @@ cudaError_t launch_vec(const WeightsParams& p, int num_sms, cudaStream_t stream)
     return p.cols <= 8 ? launch<kVec, 8, 512, 2>(p, CS, stream) : launch<kVec, 16, 512, 1>(p, CS, stream);
   // Read again: slices of at least a step of 1024 positions, four CTAs an SM (three where values
   // come one by one: their registers do not fit otherwise).  Where clusters of 8 fill the GPU,
-  // wider ones wait for one another more than they win: 16 x 32K with 8 heads of 8 queries 75 us
-  // with 8 CTAs a cluster, 84 with 4, 86 with 12, 95 with 16.  (Rounds of 8 columns, whose
-  // second reading finds more in L2, took 79: the sums go round the cluster twice.)
+  // wider ones wait for one another more than they win: 16 x 32K with 8 heads of 8 queries 71 us
+  // with 8 CTAs a cluster, 81 with 4, 79 with 12, 82 with 16.  (Rounds of 8 columns, whose
+  // second reading finds more in L2, took 79 for 75: the sums go round the cluster twice.)
   CS = (p.P_max + 1023) / 1024;
   const int widest = pairs * 8 >= 3ll * num_sms ? 8 : kWMaxCluster;
   if (CS > widest) CS = widest;

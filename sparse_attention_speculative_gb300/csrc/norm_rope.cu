@@ -21,7 +21,7 @@
 // 0.96 of the copy rate; 129 us with every lane finding its four angles before its first rows,
 // 196 us before two values went through one instruction and weights and angles were joined).
 // 4096 tokens into an 8-bit cache take 23.6 us (92 MB, 0.58; 26 before that): the queries alone 14.5 (21.7),
-// the pages, whose blocks leave an SM 20 warps, the rest.  (Two warps a page and head, its rows in
+// the pages, whose blocks leave an SM room for 20 warps (17 on average), the rest.  (Two warps a page and head, its rows in
 // registers and 24 warps an SM: 24.7, with a fifth more instructions.)  A verify block of 16
 // sequences takes 3.8 us (5.6 with the page looked up before its rows).  One token of 16
 // sequences is a launch, 2.6 us.  Rows loaded a step ahead made the prompt slower (138 us:
@@ -42,8 +42,9 @@ struct Strided {
   long long batch, row, head;
 };
 
-// Division of an unsigned number below 2^31 by a number that the host knows: q = (x + the upper
-// half of x m) >> s, with s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1.
+// Division of an unsigned number below 2^31 by a number that the host knows, by a multiplication
+// (T. Granlund and P. Montgomery, "Division by Invariant Integers using Multiplication", 1994):
+// q = (x + the upper half of x m) >> s, with s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1.
 struct Divisor {
   uint32_t d = 1, m = 1, s = 0;
   Divisor() = default;

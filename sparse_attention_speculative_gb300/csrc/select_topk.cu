@@ -68,7 +68,7 @@ constexpr int kBins0 = 4096;                     // level 0: top 12 bits
 constexpr int kBinsL = 1024;                     // levels 1, 2: 10 bits each
 constexpr int kGatherCap = 8192;                 // boundary-bin keys rank 0 can hold
 // Rows of up to this many bitmap words (32768 positions) are written by rank 0 alone,
-// two rounds of its threads; longer rows by every CTA in parallel, which costs one more
+// up to 64 positions a thread; longer rows by every CTA in parallel, which costs one more
 // cluster barrier.
 constexpr int kShortRowWords = 2 * kSelThreads;
 // Boundary keys of a short row that are ranked against each other at once, several threads
