@@ -811,7 +811,7 @@ vsd_status vsd_accumulate_weights_quant(const vsd_geom* geom, int R, int C, cons
  *              block_table itself) or a page that the sequence does not read.  Either way no
  *              other sequence of the call reads it (a prefix that sequences share moves into
  *              pages of each one's own), and no page is written for two sequences.  Rows at n
- *              and beyond stay as they were
+ *              and beyond stay as they were (8 bit: their codes, under the page's new scale)
  *   weights, weights_out  fp32 [B][Hkv][stride] each, both or neither NULL; weights_out may be
  *              weights (with one stride), and does not overlap it otherwise
  *              (VSD_ERR_INVALID_ARG); weights_out_stride >= k_max

@@ -8,7 +8,7 @@ from tests.test_gpu_accumulate_weights import Case, clean_status, vsd  # noqa: F
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("P_max", [4097, 9000, 12000, 12001, 16384, 20000, 25001, 30720, 32768])
+@pytest.mark.parametrize("P_max", [4097, 9000, 12000, 12001, 16384, 20000, 25001, 30000, 32768])
 @pytest.mark.parametrize("G,C", [(4, 2), (8, 2), (4, 3), (1, 16)])    # 8, 16, 12 and 16 columns
 def test_held_sums_of_clusters(vsd, P_max, G, C):  # noqa: F811
     R = max(C, 4)
