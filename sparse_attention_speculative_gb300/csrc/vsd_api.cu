@@ -509,11 +509,17 @@ vsd_status vsd_sparse_verify_attn(const vsd_geom* geom, int R, const void* q,
   return VSD_OK;
 }
 
+namespace {
+// (a launch has a row of clusters for each row: its grid's second dimension ends at 65535)
+bool select_fits(int n_rows, int P_max) {
+  return n_rows <= 65535 && vsd::select_chunk(P_max, vsd::select_cluster_size(P_max, n_rows)) >= 0;
+}
+}  // namespace
+
 vsd_status vsd_select_workspace_size(int n_rows, int Hkv, int P_max, int k, size_t* bytes) {
   if (bytes == nullptr || n_rows < 0 || Hkv < 1 || P_max < 0 || k < 1)
     return VSD_ERR_INVALID_ARG;
-  if (vsd::select_chunk(P_max, vsd::select_cluster_size(P_max, n_rows)) < 0)
-    return VSD_ERR_UNSUPPORTED;
+  if (!select_fits(n_rows, P_max)) return VSD_ERR_UNSUPPORTED;
   *bytes = 0;
   return VSD_OK;
 }
@@ -527,8 +533,7 @@ vsd_status vsd_select_topk(int n_rows, int Hkv, const float* partial_scores,
   if (n_rows < 0 || Hkv < 1 || P_max < 0 || k < 1 || n_sink < 0 || n_recent < 0)
     return VSD_ERR_INVALID_ARG;
   if (static_cast<long long>(n_sink) + n_recent > k) return VSD_ERR_INVALID_ARG;
-  if (vsd::select_chunk(P_max, vsd::select_cluster_size(P_max, n_rows)) < 0)
-    return VSD_ERR_UNSUPPORTED;
+  if (!select_fits(n_rows, P_max)) return VSD_ERR_UNSUPPORTED;
   if (n_rows == 0) return VSD_OK;
   if (!partial_scores || !prefix_len || !idx || !n_sel) return VSD_ERR_INVALID_ARG;
   if (!aligned(partial_scores, 16) || !aligned(idx, 4) || !aligned(n_sel, 4) ||
@@ -597,8 +602,7 @@ size_t hybrid_bitmap_bytes(int n_rows, int P_max) {
 
 vsd_status vsd_select_hybrid_workspace_size(int n_rows, int P_max, size_t* bytes) {
   if (bytes == nullptr || n_rows < 0 || P_max < 0) return VSD_ERR_INVALID_ARG;
-  if (vsd::select_chunk(P_max, vsd::select_cluster_size(P_max, n_rows)) < 0)
-    return VSD_ERR_UNSUPPORTED;
+  if (!select_fits(n_rows, P_max)) return VSD_ERR_UNSUPPORTED;
   *bytes = hybrid_bitmap_bytes(n_rows, P_max) + (static_cast<size_t>(n_rows) * 4 + 255) / 256 * 256;
   return VSD_OK;
 }
@@ -612,8 +616,7 @@ vsd_status vsd_select_topk_hybrid(int n_rows, int Hkv_target, const float* parti
       n_sink < 0 || n_recent < 0)
     return VSD_ERR_INVALID_ARG;
   if (static_cast<long long>(n_sink) + n_recent > k) return VSD_ERR_INVALID_ARG;
-  if (vsd::select_chunk(P_max, vsd::select_cluster_size(P_max, n_rows)) < 0)
-    return VSD_ERR_UNSUPPORTED;
+  if (!select_fits(n_rows, P_max)) return VSD_ERR_UNSUPPORTED;
   if (n_rows == 0) return VSD_OK;
   if (!partial_target || !partial_draft || !prefix_len || !idx || !n_sel)
     return VSD_ERR_INVALID_ARG;
